@@ -331,6 +331,142 @@ int w12_verify_tree_fused(const uint16_t* H, const w12_weights* head, const int3
                           int32_t* accept_len, int32_t* bonus, int32_t* argmax_out, void* ws,
                           size_t ws_bytes, int32_t* dev_status, void* stream);
 
+/* --- Page tables of a paged cache ----------------------------------------- */
+/* A paged cache keeps a request's tokens in pages of page_size tokens (16, 32,
+ * 64 or 128): token position i of request b is row i % page_size of page
+ * table[b, i / page_size], and its slot is page * page_size + i % page_size
+ * (slots are int32: n_pages * page_size < 2^31). The pages have no counterpart
+ * to this part; it gives the verify path a cache that requests of different
+ * lengths share.
+ *
+ * w12_pages_update brings every request to ceil((start[b] + add[b]) / page_size)
+ * pages, taking pages from or giving pages back to a free stack, and writes
+ * the slots of the new tokens: slots[b, i] for position start[b] + i, i <
+ * add[b], and -1 in the rest of the row. A verify step reserves with start =
+ * committed length, add = draft tokens; after acceptance it trims with start =
+ * new length, T = 0 (add and slots may then be NULL: add = 0); start = 0 with
+ * T = 0 releases a request. State, all device int32, updated in place:
+ *   table [B, max_pages]  page ids (entries at or past used[b] are not read)
+ *   used [B]              pages each request holds
+ *   free_pages [n_pages]  stack of free page ids, free_pages[0 .. n_free)
+ *   n_free [1]
+ * Pages are taken in (request, page) order, the k-th from
+ * free_pages[n_free - 1 - k]; pages given back land so that a reserve followed
+ * by the matching trim restores the stack; pages given back in a call serve
+ * the next call, not this one. Table entries given back become -1. Requests are served in order until one does not fit: it and the later
+ * ones that need pages keep what they hold, get slots of -1, and set
+ * W12_ERR_WORKSPACE in dev_status. A request whose lengths or counts are out of
+ * range (start or add < 0, add > T, more than max_pages pages, used outside
+ * [0, max_pages]) is left as it is with slots of -1 and sets W12_ERR_ARG, as
+ * does a free count outside [0, n_pages]. B <= 8192. Errors: W12_ERR_ARG,
+ * W12_ERR_SHAPE, W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
+int w12_pages_update(int32_t* table, int32_t* used, int32_t* free_pages, int32_t* n_free, int B, int max_pages,
+                     int page_size, int64_t n_pages, const int32_t* start, const int32_t* add, int T,
+                     int32_t* slots, int32_t* dev_status, void* stream);
+
+/* --- Paged key/value cache held in 4 bits ("KV4") ------------------------- */
+/* One layer's keys and values: a pool of n_pages pages for Hkv kv heads of
+ * head_dim 64 or 128. A row (token, head) of K or of V is held as 4-bit codes
+ * q with a bf16 scale s and a bf16 centre z, value = z + s (q - 8):
+ *   s = bf16(max/15 - min/15), z = bf16(min + 8 s),
+ *   q = clamp(round((x - z) / s) + 8, 0, 15),
+ * in fp32, over the row's head_dim values; a scale below 2^-100 is stored as 0
+ * (the row reads as z). A row that holds a value that is not finite gets s = z
+ * = NaN and reads as NaN. Layout, pool 16-byte aligned: one block per (page,
+ * kv head), page-major, of page_size * (head_dim + 8) bytes: K codes
+ * [page_size, head_dim/2], V codes, K parameters [page_size] (s in the low, z
+ * in the high half of a 32-bit word), V parameters. 32-bit word w of a row's
+ * codes holds dims 8w .. 8w+7: nibble j < 4 is dim 8w + 2j, nibble j + 4 is
+ * dim 8w + 2j + 1; at head_dim 128 the two 32-byte halves of a row are swapped
+ * in rows whose index in the page has bit 1 set. */
+typedef struct w12_kv4 {
+  uint8_t* pool;
+  int64_t n_pages;
+  int Hkv, head_dim, page_size;
+} w12_kv4;
+
+/* Element types of the operators below that take more than one. */
+enum { W12_F32 = 0, W12_BF16 = 1, W12_F16 = 2 };
+
+/* Bytes of one page (all heads), 0 for a layout the library does not have. */
+int64_t w12_kv4_page_bytes(int Hkv, int head_dim, int page_size);
+
+/* Quantise n tokens into the cache: row i goes to slot slots[i] (-1: skipped;
+ * any other slot outside the pool sets W12_ERR_ARG in dev_status and is
+ * skipped; slots of one call are distinct). K and V: dtype W12_F32, W12_BF16 or
+ * W12_F16, element (i, h, c) at i * token_stride + h * head_stride + c (strides
+ * in elements, of any sign), so they may be views into a wider product. Rows
+ * whose base and strides are multiples of 16 bytes are read in wide loads.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
+int w12_kv4_append(const w12_kv4* cache, const void* K, const void* V, int dtype, int64_t n,
+                   int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                   const int32_t* slots, int32_t* dev_status, void* stream);
+
+/* Rows back as bf16: K_out and V_out [n, Hkv, head_dim], contiguous, 16-byte
+ * aligned (slot -1: zeros; another slot outside the pool: zeros and
+ * W12_ERR_ARG). Errors as for w12_kv4_append. */
+int w12_kv4_read(const w12_kv4* cache, const int32_t* slots, int64_t n, uint16_t* K_out, uint16_t* V_out,
+                 int32_t* dev_status, void* stream);
+
+/* w12_kv_commit for paged caches: in every cache of the HOST array `caches`
+ * (one per layer, all of one layout and page numbering) the rows of positions
+ * prefix_len[b] + path[b, k] move to positions prefix_len[b] + k, k <
+ * path_len[b], through table [B, max_pages]; new_len (nullable, another array
+ * than prefix_len) as there. A request whose path is invalid (empty, longer
+ * than path_stride, not increasing, or on a page outside the pool) is left
+ * unchanged and sets W12_ERR_BAD_TREE. The pages of these positions belong to
+ * the request alone. Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED,
+ * W12_ERR_CUDA. */
+int w12_kv4_commit(const w12_kv4* caches, int n_caches, int B, const int32_t* table, int max_pages,
+                   const int32_t* prefix_len, const int32_t* path, int path_stride, const int32_t* path_len,
+                   int32_t* new_len, int32_t* dev_status, void* stream);
+
+/* Attention of new tokens over the 4-bit cache:
+ *   O[b, t, h, :] = sum_j softmax_j(scale * Q[b, t, h, :] . K_j) * V_j
+ * over the cached rows j of kv head h / (Hq / Hkv) that token t sees, Q bf16
+ * with element strides (multiples of 8; base 16-byte aligned), O bf16
+ * [B, T, Hq, head_dim] contiguous. Request b has prefix_len[b] cached tokens and
+ * q_len[b] <= T new ones (NULL: T), whose rows are already in the cache at
+ * positions prefix_len[b] + t. With parents = NULL new token t sees positions
+ * up to its own (a decode step T = 1, a drafted block, a prompt chunk of any
+ * length); with parents [B, T] (T <= 128; parents[b, 0] = -1, 0 <= parents[b, i]
+ * < i) it sees the prefix and its root-to-node path. Rows t >= q_len[b] of O
+ * are zero. Positions that no token sees may hold anything, values that are
+ * not finite among them. max_kv_len (host) bounds prefix_len[b] + q_len[b] and
+ * is at most max_pages * page_size; table [B, max_pages] int32. Scores,
+ * softmax and sums are fp32. Device-side errors: W12_ERR_ARG (lengths out of
+ * range: taken clamped; a page outside the pool: outputs unspecified),
+ * W12_ERR_BAD_TREE (that request's outputs are unspecified), W12_ERR_TIMEOUT. The
+ * workspace follows the rules at the top. Returns W12_ERR_ARG,
+ * W12_ERR_SHAPE, W12_ERR_WORKSPACE, W12_ERR_UNSUPPORTED or W12_ERR_CUDA. */
+size_t w12_kv4_attention_ws_bytes(int B, int T, int Hq, int Hkv, int head_dim, int page_size, int64_t max_kv_len);
+
+int w12_kv4_attention(const uint16_t* Q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
+                      const w12_kv4* cache, const int32_t* table, int max_pages, int B, int T, int Hq,
+                      int64_t max_kv_len, const int32_t* prefix_len, const int32_t* q_len, const int32_t* parents,
+                      float scale, uint16_t* O, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
+/* --- Log probabilities of tokens ------------------------------------------ */
+/* For logits [M, V] (dtype W12_F32, W12_BF16 or W12_F16; rows row_stride >= V
+ * elements apart), x = scale * logit in fp32:
+ *   lse[m] = log sum_v e^x, logprob[m, j] = x[tokens[m, j]] - lse,
+ *   entropy[m] = lse - sum_v p x, p = e^(x - lse),
+ *   top_logprob / top_id [m, k]: the k <= 32 largest, in order, the lowest
+ *   token first among equal values.
+ * tokens [M, n] int32 (n may be 0): -1 gives 0, another token outside [0, V)
+ * gives NaN and W12_ERR_ARG in dev_status. Logits of -inf are masked tokens: they
+ * add nothing and are never listed; places of the list without a token get id
+ * -1 and -inf. A row of nothing but -inf has lse -inf, entropy 0 and every
+ * logprob -inf. A NaN or +inf in a row makes its lse, entropy and logprobs NaN.
+ * 1 <= M <= 65535, V < 2^30, scale > 0. The workspace follows the rules at the
+ * top. Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_WORKSPACE,
+ * W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
+size_t w12_logprobs_ws_bytes(int64_t M, int64_t V, int k);
+
+int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t row_stride, float scale,
+                 const int32_t* tokens, int n, int k, float* logprob, float* entropy, float* lse,
+                 float* top_logprob, int32_t* top_id, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /* --- Diagnostics -------------------------------------------------------- */
 
 /* Launch a kernel that waits on a barrier nothing arrives at, with a bound of

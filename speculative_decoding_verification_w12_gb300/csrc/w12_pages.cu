@@ -1,0 +1,190 @@
+// Page tables of a paged cache: pages handed out and taken back on the GPU.
+//
+// Request b holds used[b] pages, table[b][0 .. used[b]). A call brings every
+// request to want = ceil((start + add) / P) pages. Requests that grow pop from
+// the top of the free stack, in (request, page) order: the k-th page taken is
+// free[n_free - 1 - k]. Requests that shrink push theirs so that the k-th page
+// given back (in the same order) lands at free[n_free' + R - 1 - k], n_free'
+// the count after the pops and R the pages given back: growing and then
+// shrinking by the same amounts restores the stack.
+//
+// One thread-block cluster runs the call. Each CTA scans all B lengths itself
+// (B loads from L2 and one block scan are cheaper than exchanging partial sums),
+// then the cluster's threads share the pages to pop; a cluster barrier orders
+// the pops before the pushes that reuse their stack entries and before the
+// slots, which read entries that other CTAs wrote. Latency-bound: a call is
+// a few dependent L2 round trips.
+#include <cooperative_groups.h>
+
+#include "w12_dev.cuh"
+#include "w12_host.h"
+#include "w12_kv4.cuh"
+
+namespace w12 {
+namespace pages_impl {
+
+constexpr int kThreads = 512;
+constexpr int kCluster = 8;
+constexpr int kMaxB = 8192;  // requests per call (two prefix sums of B ints in shared memory)
+
+struct PagesParams {
+  int32_t *table, *used, *free_pages, *n_free;
+  const int32_t *start, *add;
+  int32_t* slots;
+  int32_t* status;
+  int B, max_pages, P, n_pages, T;
+};
+
+struct Need {
+  int have, want;
+  bool ok;  // lengths and counts in range
+};
+
+__device__ __forceinline__ Need need_of(const PagesParams& p, int b) {
+  const int start = p.start[b], add = p.add ? p.add[b] : 0, have = p.used[b];
+  Need n;
+  const int64_t total = int64_t(start) + add;
+  n.ok = start >= 0 && add >= 0 && add <= p.T && have >= 0 && have <= p.max_pages &&
+         total <= int64_t(p.max_pages) * p.P;
+  n.have = n.ok ? have : 0;
+  n.want = n.ok ? int((total + p.P - 1) / p.P) : 0;
+  return n;
+}
+
+// Last index b in [0, n) with pre[b] <= k (pre ascending, pre[0] <= k).
+__device__ __forceinline__ int last_le(const int* pre, int n, int k) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= k) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_constant__ PagesParams p) {
+  extern __shared__ int smem[];
+  int* gpre = smem;         // pages taken by the requests before b
+  int* spre = smem + p.B;   // pages given back by the requests before b
+  __shared__ long long warp_sum[kThreads / 32];
+  __shared__ int granted;   // pages taken by all requests that get theirs
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto cluster = cooperative_groups::this_cluster();
+  const int rank = int(blockIdx.x), all = int(gridDim.x) * kThreads, me = rank * kThreads + tid;
+
+  grid_dep_wait();
+  grid_dep_launch();
+  if (tid == 0) granted = 0;
+  const int n_free = min(max(*p.n_free, 0), p.n_pages);
+  if (n_free != *p.n_free) set_status(p.status, W12_ERR_ARG);
+  // Prefix sums, kThreads requests at a time; (grow, shrink) packed in one 64-bit sum.
+  long long carry = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + tid;
+    long long v = 0;
+    if (b < p.B) {
+      const Need n = need_of(p, b);
+      v = (static_cast<long long>(max(0, n.want - n.have)) << 32) | static_cast<long long>(max(0, n.have - n.want));
+    }
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    long long before = carry, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const long long s = warp_sum[w];
+      if (w < warp) before += s;
+      total += s;
+    }
+    inc += before;
+    if (b < p.B) {
+      gpre[b] = int((inc - v) >> 32);
+      spre[b] = int((inc - v) & 0xFFFFFFFFll);
+      // Growing requests whose pages all lie within the free stack get them.
+      const int upto = int(inc >> 32);
+      if ((v >> 32) > 0 && upto <= n_free) atomicMax(&granted, upto);
+    }
+    carry += total;
+    __syncthreads();
+  }
+  const int G = granted, R = int(carry & 0xFFFFFFFFll);
+  // Pops.
+  for (int k = me; k < G; k += all) {
+    const int b = last_le(gpre, p.B, k);
+    p.table[int64_t(b) * p.max_pages + p.used[b] + (k - gpre[b])] = p.free_pages[n_free - 1 - k];
+  }
+  cluster.sync();
+  // Pushes.
+  for (int k = me; k < R; k += all) {
+    const int b = last_le(spre, p.B, k);
+    const Need n = need_of(p, b);
+    int32_t* e = p.table + int64_t(b) * p.max_pages + n.want + (k - spre[b]);
+    const int at = n_free - G + R - 1 - k;
+    if (at < p.n_pages) p.free_pages[at] = *e;
+    else set_status(p.status, W12_ERR_ARG);  // more pages than the pool has: counts that do not match
+    *e = -1;
+  }
+  // Slots of the new tokens.
+  const uint32_t cells = uint32_t(p.B) * uint32_t(p.T);  // < 2^31
+  for (uint32_t c = me; c < cells; c += all) {
+    const int b = int(c / uint32_t(p.T)), i = int(c - uint32_t(b) * uint32_t(p.T));
+    const Need n = need_of(p, b);
+    const int grow = n.want - n.have;
+    int slot = -1;
+    if (n.ok && i < p.add[b] && (grow <= 0 || gpre[b] + grow <= n_free)) {
+      const int pos = p.start[b] + i;
+      slot = p.table[int64_t(b) * p.max_pages + pos / p.P] * p.P + pos % p.P;
+    }
+    p.slots[c] = slot;
+  }
+  cluster.sync();
+  for (int b = me; b < p.B; b += all) {
+    const Need n = need_of(p, b);
+    const int grow = n.want - n.have;
+    if (!n.ok) set_status(p.status, W12_ERR_ARG);
+    else if (grow > 0 && gpre[b] + grow > n_free) set_status(p.status, W12_ERR_WORKSPACE);
+    else p.used[b] = n.want;
+  }
+  if (me == 0) *p.n_free = min(n_free - G + R, p.n_pages);
+}
+
+}  // namespace pages_impl
+}  // namespace w12
+
+using namespace w12;
+using namespace w12::pages_impl;
+
+extern "C" int w12_pages_update(int32_t* table, int32_t* used, int32_t* free_pages, int32_t* n_free, int B,
+                                int max_pages, int page_size, int64_t n_pages, const int32_t* start,
+                                const int32_t* add, int T, int32_t* slots, int32_t* dev_status, void* stream) {
+  if (!table || !used || !free_pages || !n_free || !start || T < 0 || (T > 0 && (!add || !slots))) return W12_ERR_ARG;
+  if (B < 1 || B > kMaxB || max_pages < 1 || !kv4::page_ok(page_size) || n_pages < 1 ||
+      n_pages > int64_t(0x7FFFFFFF) / page_size || int64_t(B) * max_pages > 0x7FFFFFFF ||
+      int64_t(B) * T > 0x7FFFFFFF)
+    return W12_ERR_SHAPE;
+  if (!device_supported()) return W12_ERR_UNSUPPORTED;
+  PagesParams p{table, used, free_pages, n_free, start, add, slots, dev_status, B, max_pages, page_size, int(n_pages), T};
+  const size_t smem = size_t(B) * 2 * sizeof(int);
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxB * 8) != cudaSuccess)
+    return W12_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap_enabled() ? 2 : 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, pages_update_kernel, p));
+}

@@ -26,7 +26,9 @@ EXPORTS = [
     "w12_verify_greedy_fused", "w12_verify_tree", "w12_verify_tree_fused", "w12_selftest_timeout",
     "w12_set_wait_limit_us", "w12_set_overlap", "w12_gemm_noalloc", "w12_gemm_grouped_ws_bytes",
     "w12_gemm_grouped", "w12_gemm_grouped_bf16_ref", "w12_kv_commit", "w12_state_select",
-    "w12_tree_attention_ws_bytes", "w12_tree_attention", "w12_copy",
+    "w12_tree_attention_ws_bytes", "w12_tree_attention", "w12_copy", "w12_pages_update", "w12_kv4_page_bytes",
+    "w12_kv4_append", "w12_kv4_read", "w12_kv4_commit", "w12_kv4_attention_ws_bytes", "w12_kv4_attention",
+    "w12_logprobs_ws_bytes", "w12_logprobs",
 ]
 
 
@@ -54,6 +56,11 @@ class _Swiglu(ctypes.Structure):
 class _Sizes(ctypes.Structure):
     _fields_ = [("plane_bytes", ctypes.c_int64), ("ebase_bytes", ctypes.c_int64),
                 ("exc_off_count", ctypes.c_int64), ("n_exc", ctypes.c_int64), ("total_bytes", ctypes.c_int64)]
+
+
+class _KV4(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("Hkv", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int)]
 
 
 _lib = None
@@ -99,6 +106,17 @@ def lib() -> ctypes.CDLL:
             "w12_tree_attention_ws_bytes": (sz, [i32, i32, i32, i32, i64]),
             "w12_tree_attention": (i32, [vp, vp, vp, i32, i32, i32, i32, i32, i64, i64, vp, vp, ctypes.c_float, vp,
                                          vp, sz, vp, vp]),
+            "w12_pages_update": (i32, [vp, vp, vp, vp, i32, i32, i32, i64, vp, vp, i32, vp, vp, vp]),
+            "w12_kv4_page_bytes": (i64, [i32, i32, i32]),
+            "w12_kv4_append": (i32, [ctypes.POINTER(_KV4), vp, vp, i32, i64, i64, i64, i64, i64, vp, vp, vp]),
+            "w12_kv4_read": (i32, [ctypes.POINTER(_KV4), vp, i64, vp, vp, vp, vp]),
+            "w12_kv4_commit": (i32, [ctypes.POINTER(_KV4), i32, i32, vp, i32, vp, vp, i32, vp, vp, vp, vp]),
+            "w12_kv4_attention_ws_bytes": (sz, [i32, i32, i32, i32, i32, i32, i64]),
+            "w12_kv4_attention": (i32, [vp, i64, i64, i64, ctypes.POINTER(_KV4), vp, i32, i32, i32, i32, i64, vp, vp,
+                                        vp, ctypes.c_float, vp, vp, sz, vp, vp]),
+            "w12_logprobs_ws_bytes": (sz, [i64, i64, i32]),
+            "w12_logprobs": (i32, [vp, i32, i64, i64, i64, ctypes.c_float, vp, i32, i32, vp, vp, vp, vp, vp, vp, sz,
+                                   vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -489,6 +507,259 @@ def verify_tree_fused(H: torch.Tensor, head: W12Weights, parents: torch.Tensor, 
                                        bonus.data_ptr(), am.data_ptr(), ws.data_ptr(), ws.numel(), _ptr(status),
                                        _stream(stream)), "w12_verify_tree_fused")
     return path, plen, acc, bonus, am
+
+
+# ---------------------------------------------------------------------------
+# Paged 4-bit cache, its attention, and token log probabilities
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}   # W12_F32, W12_BF16, W12_F16
+
+
+def _want(t: torch.Tensor, what: str, dtype, shape=None) -> torch.Tensor:
+    """t, checked: a contiguous CUDA tensor of the given type (and shape)."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} CUDA tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t
+
+
+def _empty(shape, dtype, device, stream):
+    """Uninitialised output of a call on `stream` (None: the current one): the
+    memory belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _kept_workspace(nbytes: int, device) -> torch.Tensor:
+    """A workspace that is ready on every stream (the zero fill has finished),
+    unless a graph is being captured, which then holds the fill."""
+    ws = workspace(nbytes, device)
+    if not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream(ws.device).synchronize()
+    return ws
+
+
+class PageTable:
+    """Page tables of a paged cache (w12_pages_update), updated on the GPU.
+
+    table int32 [B, max_pages], used int32 [B], free int32 [n_pages] (a stack,
+    its first n_free[0] entries are free page ids), n_free int32 [1]; all are
+    updated in place. create() makes an empty table with every page free.
+    """
+
+    def __init__(self, table: torch.Tensor, used: torch.Tensor, free: torch.Tensor, n_free: torch.Tensor,
+                 page_size: int):
+        self.B, self.max_pages = table.shape
+        self.n_pages, self.page_size = free.numel(), int(page_size)
+        self.table = _want(table, "table", torch.int32)
+        self.used = _want(used, "used", torch.int32, (self.B,))
+        self.free = _want(free, "free", torch.int32, (self.n_pages,))
+        self.n_free = _want(n_free, "n_free", torch.int32, (1,))
+        self._state = (table.data_ptr(), used.data_ptr(), free.data_ptr(), n_free.data_ptr(), self.B, self.max_pages,
+                       self.page_size, self.n_pages)
+
+    @classmethod
+    def create(cls, B: int, max_pages: int, n_pages: int, page_size: int, device="cuda") -> "PageTable":
+        """B requests without pages; the first page taken is page 0, then 1, ..."""
+        return cls(torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(B, dtype=torch.int32, device=device),
+                   torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   torch.full((1,), n_pages, dtype=torch.int32, device=device), page_size)
+
+    def reserve(self, start: torch.Tensor, new: torch.Tensor, T: int, slots: torch.Tensor | None = None,
+                status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Pages for new[b] <= T tokens from position start[b] on; returns their slots int32 [B, T] (-1 padded)."""
+        _want(start, "start", torch.int32, (self.B,))
+        _want(new, "new", torch.int32, (self.B,))
+        if slots is None:
+            slots = _empty((self.B, T), torch.int32, start.device, stream)
+        else:
+            _want(slots, "slots", torch.int32, (self.B, T))
+        _check(lib().w12_pages_update(*self._state, start.data_ptr(), new.data_ptr(), T, slots.data_ptr(),
+                                      _ptr(status), _stream(stream)), "w12_pages_update")
+        return slots
+
+    def trim(self, length: torch.Tensor, status: torch.Tensor | None = None, stream=None):
+        """Give back the pages past length[b] tokens (0 releases request b)."""
+        _want(length, "length", torch.int32, (self.B,))
+        _check(lib().w12_pages_update(*self._state, length.data_ptr(), None, 0, None, _ptr(status),
+                                      _stream(stream)), "w12_pages_update")
+
+
+class KV4Cache:
+    """One layer's paged key/value cache in 4 bits: pool uint8
+    [n_pages, Hkv, page_size * (head_dim + 8)] (layout in include/w12.h)."""
+
+    def __init__(self, pool: torch.Tensor, page_size: int, head_dim: int):
+        self.n_pages, self.Hkv, _ = pool.shape
+        self.page_size, self.head_dim = int(page_size), int(head_dim)
+        if lib().w12_kv4_page_bytes(self.Hkv, self.head_dim, self.page_size) != pool[0].numel():
+            raise ValueError("pool must be [n_pages, Hkv, page_size * (head_dim + 8)] with a page size of 16, 32, 64 or "
+                             "128 and a head dimension of 64 or 128")
+        self.pool = _want(pool, "pool", torch.uint8)
+        self._struct = _KV4(pool.data_ptr(), self.n_pages, self.Hkv, self.head_dim, self.page_size)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def create(cls, n_pages: int, Hkv: int, head_dim: int, page_size: int, device="cuda") -> "KV4Cache":
+        return cls(torch.zeros((n_pages, Hkv, page_size * (head_dim + 8)), dtype=torch.uint8, device=device),
+                   page_size, head_dim)
+
+    def append(self, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, status: torch.Tensor | None = None,
+               stream=None):
+        """Quantise rows K, V [n, Hkv, head_dim] (fp32, bf16 or fp16; views with a
+        contiguous last dimension) into the given slots (int32, n of them, -1 skips)."""
+        n = K.shape[0]
+        if K.shape != V.shape or tuple(K.shape) != (n, self.Hkv, self.head_dim):
+            raise ValueError("K and V must be [n, Hkv, head_dim]")
+        dt = _DTYPES.get(K.dtype)
+        if dt is None or V.dtype != K.dtype:
+            raise TypeError("K and V must both be float32, bfloat16 or float16")
+        ks, vs = K.stride(), V.stride()
+        if ks[2] != 1 or vs[2] != 1 or not (K.is_cuda and V.is_cuda):
+            raise ValueError("K and V must be CUDA tensors with a contiguous last dimension")
+        if slots.numel() != n:
+            raise ValueError("one slot for each row of K")
+        _want(slots, "slots", torch.int32)
+        if n:
+            _check(lib().w12_kv4_append(self._ref, K.data_ptr(), V.data_ptr(), dt, n, ks[0], ks[1], vs[0], vs[1],
+                                        slots.data_ptr(), _ptr(status), _stream(stream)), "w12_kv4_append")
+
+    def read(self, slots: torch.Tensor, out=None, status: torch.Tensor | None = None, stream=None):
+        """(K, V) bf16 [n, Hkv, head_dim] of the given slots (int32; -1 reads as zeros)."""
+        _want(slots, "slots", torch.int32)
+        n = slots.numel()
+        shape = (n, self.Hkv, self.head_dim)
+        if out is None:
+            out = tuple(_empty(shape, torch.bfloat16, slots.device, stream) for _ in range(2))
+        K, V = (_want(t, "out", torch.bfloat16, shape) for t in out)
+        if n:
+            _check(lib().w12_kv4_read(self._ref, slots.data_ptr(), n, K.data_ptr(), V.data_ptr(), _ptr(status),
+                                      _stream(stream)), "w12_kv4_read")
+        return K, V
+
+
+def kv4_commit(caches, table: torch.Tensor, prefix_len: torch.Tensor, path: torch.Tensor, path_len: torch.Tensor,
+               new_len: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """kv_commit over paged 4-bit caches (KV4Cache objects of one layout and page
+    numbering, one per layer). Returns new_len int32 [B] = prefix_len + path_len
+    (prefix_len for invalid paths)."""
+    caches = list(caches)
+    B, max_pages = table.shape
+    _want(table, "table", torch.int32)
+    _want(prefix_len, "prefix_len", torch.int32, (B,))
+    _want(path, "path", torch.int32)
+    _want(path_len, "path_len", torch.int32, (B,))
+    if path.dim() != 2 or path.shape[0] != B:
+        raise ValueError("path must be [B, stride]")
+    if new_len is None:
+        new_len = _empty((B,), torch.int32, table.device, stream)
+    elif new_len.data_ptr() == prefix_len.data_ptr():
+        raise ValueError("new_len must be another tensor than prefix_len")
+    arr = caches[0]._ref if len(caches) == 1 else (_KV4 * len(caches))(*[c._struct for c in caches])
+    _check(lib().w12_kv4_commit(arr, len(caches), B, table.data_ptr(), max_pages, prefix_len.data_ptr(),
+                                path.data_ptr(), path.shape[1], path_len.data_ptr(), new_len.data_ptr(),
+                                _ptr(status), _stream(stream)), "w12_kv4_commit")
+    return new_len
+
+
+class KV4Attention:
+    """Attention of new tokens over a KV4Cache, planned once: B requests of up to
+    T new tokens each (1: decode; a drafted block or tree; a prompt chunk),
+    ``max_kv_len`` bounds prefix_len[b] + q_len[b] over the requests."""
+
+    def __init__(self, B: int, T: int, Hq: int, Hkv: int, head_dim: int, page_size: int, max_kv_len: int,
+                 device="cuda"):
+        self.B, self.T, self.Hq, self.Hkv, self.head_dim = B, T, Hq, Hkv, head_dim
+        self.page_size, self.max_kv_len = page_size, int(max_kv_len)
+        nbytes = lib().w12_kv4_attention_ws_bytes(B, T, Hq, Hkv, head_dim, page_size, self.max_kv_len)
+        if nbytes == 0:
+            raise W12Error(2, "w12_kv4_attention_ws_bytes")
+        self.ws = _kept_workspace(nbytes, device)
+
+    def reset(self):
+        """Zero the workspace again (needed after a call that ended with an error status)."""
+        self.ws.zero_()
+
+    def run(self, Q: torch.Tensor, cache: KV4Cache, table: torch.Tensor, prefix_len: torch.Tensor,
+            parents: torch.Tensor | None = None, q_len: torch.Tensor | None = None, scale: float | None = None,
+            out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """O bf16 [B, T, Hq, head_dim] for Q bf16 of that shape (a view with a
+        contiguous last dimension and strides that are multiples of 8 will do).
+        q_len int32 [B] (default: T of every request); parents int32 [B, T] for a
+        draft tree (default: each token sees the ones before it)."""
+        shape = (self.B, self.T, self.Hq, self.head_dim)
+        if tuple(Q.shape) != shape or Q.dtype != torch.bfloat16 or not Q.is_cuda:
+            raise ValueError(f"Q must be a bfloat16 CUDA tensor of shape {shape}")
+        qs = Q.stride()
+        if qs[3] != 1:
+            raise ValueError("Q must have a contiguous last dimension")
+        if (cache.Hkv, cache.head_dim, cache.page_size) != (self.Hkv, self.head_dim, self.page_size):
+            raise ValueError("the cache's heads and page size must match the planned ones")
+        _want(table, "table", torch.int32)
+        if table.dim() != 2 or table.shape[0] != self.B:
+            raise ValueError("table must be [B, max_pages]")
+        _want(prefix_len, "prefix_len", torch.int32, (self.B,))
+        if q_len is not None:
+            _want(q_len, "q_len", torch.int32, (self.B,))
+        if parents is not None:
+            _want(parents, "parents", torch.int32, (self.B, self.T))
+        if out is None:
+            out = _empty(shape, torch.bfloat16, Q.device, stream)
+        else:
+            _want(out, "out", torch.bfloat16, shape)
+        scale = self.head_dim ** -0.5 if scale is None else float(scale)
+        _check(lib().w12_kv4_attention(Q.data_ptr(), qs[0], qs[1], qs[2], cache._ref, table.data_ptr(),
+                                       table.shape[1], self.B, self.T, self.Hq, self.max_kv_len,
+                                       prefix_len.data_ptr(), _ptr(q_len), _ptr(parents), scale, out.data_ptr(),
+                                       self.ws.data_ptr(), self.ws.numel(), _ptr(status), _stream(stream)),
+               "w12_kv4_attention")
+        return out
+
+
+class TokenLogprobs:
+    """Log probabilities of given tokens, entropy and the k most likely tokens of
+    M logits rows over V tokens (w12_logprobs), with its workspace."""
+
+    def __init__(self, M: int, V: int, k: int = 0, device="cuda"):
+        self.M, self.V, self.k = M, V, k
+        nbytes = lib().w12_logprobs_ws_bytes(M, V, k)
+        if nbytes == 0:
+            raise W12Error(2, "w12_logprobs_ws_bytes")
+        self.ws = _kept_workspace(nbytes, device)
+
+    def run(self, logits: torch.Tensor, tokens: torch.Tensor | None = None, scale: float = 1.0,
+            status: torch.Tensor | None = None, stream=None):
+        """(logprob [M, n], entropy [M], lse [M], top_logprob [M, k], top_id int32
+        [M, k]) of scale * logits; logits [M, V] fp32, bf16 or fp16 (rows may be
+        padded), tokens int32 [M, n] (-1: no token, 0)."""
+        dt = _DTYPES.get(logits.dtype)
+        if dt is None:
+            raise TypeError("logits must be float32, bfloat16 or float16")
+        if tuple(logits.shape) != (self.M, self.V) or logits.stride(1) != 1 or not logits.is_cuda:
+            raise ValueError(f"logits must be a CUDA tensor [{self.M}, {self.V}] with a contiguous last dimension")
+        n = 0 if tokens is None else tokens.shape[1]
+        if tokens is not None:
+            _want(tokens, "tokens", torch.int32, (self.M, n))
+        M, k, dev = self.M, self.k, logits.device
+        # One buffer: the outputs are small, and an allocation costs more than the views.
+        out = _empty(M * (n + 2 + 2 * k), torch.float32, dev, stream)
+        lp, entropy, lse, top_lp, top_id = out.split([M * n, M, M, M * k, M * k])
+        _check(lib().w12_logprobs(logits.data_ptr(), dt, M, self.V, logits.stride(0) if M > 1 else self.V,
+                                  float(scale), _ptr(tokens), n, k, lp.data_ptr(), entropy.data_ptr(),
+                                  lse.data_ptr(), top_lp.data_ptr(), top_id.data_ptr(), self.ws.data_ptr(),
+                                  self.ws.numel(), _ptr(status), _stream(stream)), "w12_logprobs")
+        return lp.view(M, n), entropy, lse, top_lp.view(M, k), top_id.view(torch.int32).view(M, k)
+
+
+def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0, scale: float = 1.0,
+             status: torch.Tensor | None = None, stream=None):
+    """One call of TokenLogprobs on logits [M, V]."""
+    return TokenLogprobs(logits.shape[0], logits.shape[1], k, logits.device).run(logits, tokens, scale, status, stream)
 
 
 def selftest_timeout(limit_us: int, status: torch.Tensor, stream=None):
