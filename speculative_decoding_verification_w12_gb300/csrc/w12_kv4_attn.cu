@@ -1,25 +1,12 @@
 // Attention over the paged 4-bit cache: simple form, one warp per query row.
-#include "w12_kv4.cuh"
+#include <algorithm>
+
+#include "w12_kv4_rows.cuh"
 
 namespace w12 {
 namespace kv4_attn {
 
-using namespace kv4;
-
 constexpr int kWarps = 4;
-constexpr int kMaxTree = 128;
-
-struct Params {
-  const uint16_t* Q;
-  int64_t q_b, q_t, q_h;  // strides in elements
-  uint16_t* O;            // [B, T, Hq, d]
-  const uint8_t* pool;
-  int64_t n_pages, block;
-  const int32_t *table, *prefix_len, *q_len, *parents;
-  int32_t* status;
-  int B, T, Hq, Hkv, G, P, p_shift, max_pages, max_len;
-  float scale;
-};
 
 template <int kD>
 __global__ void __launch_bounds__(kWarps * 32) kv4_attn_simple_kernel(const __grid_constant__ Params p) {
@@ -87,13 +74,13 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_simple_kernel(const __gr
           dot = fmaf(v.y, qs[warp][8 * w + 2 * i + 1], dot);
         }
       }
-      x = dot * p.scale;
+      x = dot * p.c;
     }
     float mx = x;
     for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, s));
     const float mn = fmaxf(m, mx);
-    const float f = m == -INFINITY ? 0.f : expf(m - mn);
-    const float e = see ? expf(x - (mn == -INFINITY ? 0.f : mn)) : 0.f;
+    const float f = m == -INFINITY ? 0.f : ex2(m - mn);
+    const float e = see ? ex2(x - (mn == -INFINITY ? 0.f : mn)) : 0.f;
     m = mn;
     float es = e;
     for (int s = 16; s > 0; s >>= 1) es += __shfl_xor_sync(0xFFFFFFFFu, es, s);
@@ -120,6 +107,60 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attn_simple_kernel(const __gr
     *reinterpret_cast<uint32_t*>(o + lane * kPer + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
 }
 
+// How a call is run: by the rows a kv head has, T G.
+struct Plan {
+  int kind;   // 1, 2: few rows (one or two 8-row tiles); 0: a warp a row
+  int ntile, rows;
+  int64_t grid, items;
+  size_t cnt, ml, o, total;  // workspace: counts, then partial (m, l), then partial O
+};
+
+static int sms_or_default() {
+  const int sms = device_sm_count();
+  return sms > 0 ? sms : 152;
+}
+
+static Plan plan_of(int B, int T, int Hq, int Hkv, int d, int64_t max_len) {
+  Plan q{};
+  const int64_t R = int64_t(T) * (Hq / Hkv);
+  q.kind = R <= 8 ? 1 : R <= 16 ? 2 : 0;
+  q.ntile = 1;
+  q.rows = q.kind == 1 ? 8 : q.kind == 2 ? 16 : 0;
+  q.items = int64_t(B) * Hkv * q.ntile;
+  const int64_t units = q.items * ((max_len + kKeys - 1) / kKeys);
+  q.grid = std::min<int64_t>(units, int64_t(sms_or_default()) * (q.kind == 1 ? RowsCfg<128, 1>::kCtas : 1));
+  q.cnt = size_t(round_up(q.items * 4, 256));
+  q.ml = size_t(round_up(q.grid * 2 * q.rows * 8, 256));
+  q.o = size_t(q.grid) * 2 * q.rows * d * 4;
+  q.total = q.cnt + q.ml + q.o + 256;
+  return q;
+}
+
+template <int kD, int kNT>
+static cudaError_t launch_rows(const Params& p, int64_t grid, cudaStream_t stream) {
+  using C = RowsCfg<kD, kNT>;
+  static bool ready[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(kv4_attn_rows_kernel<kD, kNT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kv4_attn_rows_kernel<kD, kNT>, p);
+}
+
 static bool shape_ok(int B, int T, int Hq, int Hkv, int head_dim, int page_size, int64_t max_len) {
   return B >= 1 && B <= 65535 && T >= 1 && T <= (1 << 20) && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hq <= 1024 &&
          (head_dim == 64 || head_dim == 128) && page_ok(page_size) && max_len >= 1 && max_len < (int64_t(1) << 31) - 256;
@@ -134,7 +175,9 @@ using namespace w12::kv4;
 extern "C" {
 
 size_t w12_kv4_attention_ws_bytes(int B, int T, int Hq, int Hkv, int head_dim, int page_size, int64_t max_kv_len) {
-  return kv4_attn::shape_ok(B, T, Hq, Hkv, head_dim, page_size, max_kv_len) ? 256 : 0;
+  return kv4_attn::shape_ok(B, T, Hq, Hkv, head_dim, page_size, max_kv_len)
+             ? kv4_attn::plan_of(B, T, Hq, Hkv, head_dim, max_kv_len).total
+             : 0;
 }
 
 int w12_kv4_attention(const uint16_t* Q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
@@ -176,11 +219,25 @@ int w12_kv4_attention(const uint16_t* Q, int64_t q_batch_stride, int64_t q_token
   p.p_shift = __builtin_ctz(unsigned(cache->page_size));
   p.max_pages = max_pages;
   p.max_len = int(max_kv_len);
-  p.scale = scale;
+  p.c = float(double(scale) * 1.4426950408889634);
+  p.limit_ns = wait_limit_ns();
+  const kv4_attn::Plan pl = kv4_attn::plan_of(B, T, Hq, cache->Hkv, cache->head_dim, max_kv_len);
+  p.ntile = pl.ntile;
+  p.rows_per_tile = pl.rows;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.cnt = reinterpret_cast<int32_t*>(w);
+  p.part_ml = reinterpret_cast<float2*>(w + pl.cnt);
+  p.part_o = reinterpret_cast<float*>(w + pl.cnt + pl.ml);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pl.kind == 1)
+    return cuda_status(cache->head_dim == 128 ? kv4_attn::launch_rows<128, 1>(p, pl.grid, s)
+                                              : kv4_attn::launch_rows<64, 1>(p, pl.grid, s));
+  if (pl.kind == 2)
+    return cuda_status(cache->head_dim == 128 ? kv4_attn::launch_rows<128, 2>(p, pl.grid, s)
+                                              : kv4_attn::launch_rows<64, 2>(p, pl.grid, s));
   const int64_t rows = int64_t(B) * T * Hq;
   const int64_t grid = (rows + kv4_attn::kWarps - 1) / kv4_attn::kWarps;
   if (grid > 0x7FFFFFFF) return W12_ERR_SHAPE;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cache->head_dim == 128)
     kv4_attn::kv4_attn_simple_kernel<128><<<unsigned(grid), kv4_attn::kWarps * 32, 0, s>>>(p);
   else

@@ -1,0 +1,478 @@
+// Attention over the 4-bit cache for few query rows a kv head (single tokens,
+// short blocks): streams the codes and multiplies them in registers.
+//
+// Bound by HBM: d + 8 bytes a (key, kv head) against at most 16 rows of work.
+// A copy warp brings 128 keys at a time (their pages' blocks, one bulk copy
+// each) into a ring in shared memory; each of the other warps takes groups of
+// 16 keys. With few rows, a tensor-memory tile of 128 rows would be nearly
+// empty and the restored operands would have to pass through shared memory;
+// here a code word is restored straight into the registers of an
+// mma.m16n8k16 operand, keys (or dims) on the 16-wide side and the rows on the
+// 8-wide side:
+//   S^T[16 keys, rows]  = K Q^T:  A = K codes, B = Q
+//   O^T[16 dims, rows] += V^T P^T: A = V codes, B = P
+// Codes are never scaled: a code q becomes the bf16 number u = 1 + q/16 (its
+// bits placed in the mantissa, exact), so with z + s (q - 8) = 16 s u + (z - 24 s)
+//   score = 16 c s (q.u) + c (z - 24 s) sum(q),     c = scale log2(e)
+//   o     = 16 sum p~ u - 24 sum p~ + sum p z,      p~ = bf16(p s)
+// with both products exact up to fp32 accumulation: the one rounding is P to
+// bf16, the same rounded p~ stands in both of its sums. sum p~ comes from one
+// more product with a matrix of ones.
+//
+// Layout of the 16-key group: lane (g, t) = (lane / 4, lane % 4). K: key phi(g)
+// (and 8 + phi(g)), dims (d/4) t ..: one 16-byte load per key gives all its A
+// fragments. V: keys phi(2t), phi(2t+1) (and + 8), dims (d/8) g ..: the two
+// keys' nibbles are paired by byte permutes. phi is the permutation
+// 0 5 2 7 1 4 3 6, chosen with the layout's swapped halves so that both kinds of
+// loads are free of bank conflicts.
+//
+// A warp's running maximum moves only when a score exceeds it by more than 8
+// (log2 units; one vote per group), so rescaling is rare and p <= 256.
+#pragma once
+
+#include "w12_kv4_sched.cuh"
+
+namespace w12 {
+namespace kv4_attn {
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit elements spread over the warp (lane
+// (g, t) holds row g, columns 2t and 2t + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Nibble j of both 16-bit halves of w as bf16 numbers 1 + q/16.
+template <int kJ>
+__device__ __forceinline__ uint32_t unit_pair(uint32_t w) {
+  const uint32_t x = kJ == 0 ? w << 3 : w >> (4 * kJ - 3);
+  return (x & 0x00780078u) | 0x3F803F80u;
+}
+
+template <int kD, int kNT>
+struct RowsCfg {
+  static constexpr int kWarps = kNT == 1 ? 7 : 11;      // warps that compute (a multiple of 4 with the copy warp)
+  static constexpr int kCtas = kNT == 1 ? 2 : 1;        // CTAs an SM
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kRows = 8 * kNT;
+  static constexpr int kStage = kKeys * (kD + 8);
+  static constexpr int kStages = kNT == 1 ? 4 : 6;
+  static constexpr int kPitch = kD + 8;                 // floats of an output row in shared memory
+  static constexpr int kOOff = kStages * kStage;
+  static constexpr int kMlOff = kOOff + kWarps * kRows * kPitch * 4;
+  static constexpr int kBarOff = kMlOff + kWarps * kRows * 8;
+  static constexpr int kRunOff = kBarOff + 128;
+  static constexpr int kSmem = kRunOff + 512;
+};
+
+template <int kD, int kNT>
+__global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::kCtas)
+    kv4_attn_rows_kernel(const __grid_constant__ Params p) {
+  using C = RowsCfg<kD, kNT>;
+  constexpr int kComp = C::kWarps * 32;   // computing threads
+  constexpr int kKW = kD / 32;            // code words of a key a lane reads (K)
+  constexpr int kVW = kD / 64;            // and (V)
+  constexpr int kMT = kD / 16;            // 16-dim tiles
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
+  uint64_t* empty = full + C::kStages;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(empty + C::kStages);
+  volatile int* merge_here = abort_flag + 1;
+  RunSmem& rs = *reinterpret_cast<RunSmem*>(smem + C::kRunOff);
+  static_assert(sizeof(RunSmem) <= 512 && C::kStages * 16 + 8 <= 128, "shared memory carve-up");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 8);  // one arrival per 16-key group
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  grid_dep_wait();
+  const Run run = plan_run<C::kThreads>(p, rs);  // its barriers publish the mbarriers too
+  zero_idle_rows<kD, C::kThreads>(p);
+  if (run.begin >= run.end) return;
+  const uint64_t lim = p.limit_ns;
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 0; i < 0x80000000u; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if ((i & 63u) == 63u) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > lim) break;
+      }
+    }
+    set_status(p.status, W12_ERR_TIMEOUT);
+    *abort_flag = 1;
+    return false;
+  };
+
+  if (warp == C::kWarps) {
+    // ------------------------------------------------------------- copies
+    // Lane i brings the i-th page of a block; page ids are read one block ahead.
+    const int per = kKeys >> p.p_shift;               // pages of a block (1 to 8)
+    const uint32_t bytes = uint32_t(p.block);
+    const uint64_t page_stride = uint64_t(p.Hkv) * uint64_t(p.block);
+    int issued = 0;
+    bool ok = true;
+    Walk walk(run);
+    Seg s;
+    while (ok && walk.next(p, run, s)) {
+      const int32_t* tab = p.table + int64_t(s.b) * p.max_pages;
+      const uint8_t* pool = p.pool + uint64_t(s.h) * uint64_t(p.block);
+      auto page_of = [&](int j) -> int {
+        const int i = j * per + lane;
+        return lane < per && (int64_t(i) << p.p_shift) < s.keys ? tab[i] : -2;
+      };
+      int next = page_of(s.j0);
+      for (int j = s.j0; j < s.j1; ++j) {
+        int page = next;
+        if (j + 1 < s.j1) next = page_of(j + 1);
+        const bool need = page != -2;
+        if (need && (page < 0 || page >= p.n_pages)) {
+          set_status(p.status, W12_ERR_ARG);
+          page = 0;
+        }
+        const int st = issued % C::kStages;
+        if (issued >= C::kStages &&
+            !__all_sync(0xFFFFFFFFu, wait(&empty[st], uint32_t(issued / C::kStages - 1) & 1u))) {
+          ok = false;
+          break;
+        }
+        const int pages = __popc(__ballot_sync(0xFFFFFFFFu, need));
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], uint32_t(pages) * bytes);
+        __syncwarp();
+        if (need) bulk_load(smem + st * C::kStage + lane * bytes, pool + uint64_t(page) * page_stride, bytes, &full[st]);
+        ++issued;
+      }
+    }
+    grid_dep_launch();
+    if (*abort_flag)
+      for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+        mbar_wait(&full[i % C::kStages], uint32_t(i / C::kStages) & 1u, drain_limit_ns(lim));
+    return;
+  }
+
+  // ---------------------------------------------------------------- compute
+  const int g = lane >> 2, t = lane & 3;
+  float* osm = reinterpret_cast<float*>(smem + C::kOOff);
+  float2* mlsm = reinterpret_cast<float2*>(smem + C::kMlOff);
+  const int phi_g = ((g >> 2) & 1) | (((g >> 1) & 1) << 1), row_k = phi_g ^ ((g & 1) ? 5 : 0);
+  const int row_v = ((t >> 1) & 1) | ((t & 1) << 1);  // phi(2t); phi(2t + 1) = row_v ^ 5
+  const int P = p.P;
+  int group = 0;  // 16-key groups of the run before this segment
+  Walk walk(run);
+  Seg s;
+  bool ok = true;
+  while (walk.next(p, run, s)) {
+    const int R = s.n * p.G;  // rows of the item
+    // Q fragments: row 8 nt + g, dims (d/4) t .. + d/4 - 1.
+    uint32_t q[kNT][kD / 8];
+    float sq[kNT][2];           // sums of the rows 8 nt + 2t, + 1
+    uint32_t see[kNT][2];       // draft tokens those rows see (bit i: token i)
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      const int r = 8 * nt + g;
+#pragma unroll
+      for (int i = 0; i < kD / 8; ++i) q[nt][i] = 0u;
+      if (r < R) {
+        const int tok = r / p.G;
+        const uint4* src = reinterpret_cast<const uint4*>(p.Q + s.b * p.q_b + tok * p.q_t +
+                                                          (int64_t(s.h) * p.G + (r - tok * p.G)) * p.q_h + t * (kD / 4));
+#pragma unroll
+        for (int i = 0; i < kD / 32; ++i) *reinterpret_cast<uint4*>(&q[nt][4 * i]) = __ldg(src + i);
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kD / 8; ++i) sum += bf16_lo(q[nt][i]) + bf16_hi(q[nt][i]);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+      sq[nt][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t);
+      sq[nt][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rr = 8 * nt + 2 * t + e;
+        uint32_t m = 0;
+        if (rr < R) {
+          const int tok = rr / p.G;
+          if (!p.parents) {
+            m = (2u << tok) - 1u;
+          } else {
+            const int32_t* par = p.parents + int64_t(s.b) * p.T;
+            bool bad = false;
+            for (int i = 0; i < p.T; ++i) bad |= i == 0 ? par[0] != -1 : (par[i] < 0 || par[i] >= i);
+            if (bad) set_status(p.status, W12_ERR_BAD_TREE);
+            for (int i = tok; i >= 0; i = bad ? -1 : par[i]) m |= 1u << i;
+          }
+        }
+        see[nt][e] = m;
+      }
+    }
+    float o[kNT][kMT][4], m[kNT][2], l[kNT][2], zs[kNT][2], sp[kNT][4];
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < kMT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = zs[nt][e] = 0.f;
+      sp[nt][0] = sp[nt][1] = sp[nt][2] = sp[nt][3] = 0.f;
+    }
+    const int group_end = group + (s.j1 - s.j0) * 8;
+    // This warp's groups: those whose number is its own modulo kWarps.
+    int gi = group + (C::kWarps + warp - group % C::kWarps) % C::kWarps;
+    for (; gi < group_end; gi += C::kWarps) {
+      const int blk = gi >> 3;
+      const int st = blk % C::kStages;
+      if (!__all_sync(0xFFFFFFFFu, wait(&full[st], uint32_t(blk / C::kStages) & 1u))) {
+        ok = false;
+        break;
+      }
+      const int sub = gi & 7;                                         // 16-key group of the block
+      const int key0 = (s.j0 + blk - (group >> 3)) * kKeys + sub * 16;  // its first position
+      if (key0 < s.keys) {
+        const int r0 = (sub * 16) & (P - 1);
+        const uint8_t* pg = smem + st * C::kStage + ((sub * 16) >> p.p_shift) * int(p.block);
+        const uint8_t* kc = pg + (r0 + row_k) * (kD / 2);
+        const uint32_t* par = reinterpret_cast<const uint32_t*>(pg + P * kD) + r0 + row_k;
+        uint32_t ka[kKW], kb[kKW];
+        if constexpr (kD == 128) {
+          const int off = (t ^ (row_k & 2)) * 16;
+          *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(kc + off);
+          *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(kc + 8 * (kD / 2) + off);
+        } else {
+          *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(kc + t * 8);
+          *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(kc + 8 * (kD / 2) + t * 8);
+        }
+        const uint32_t kpa = par[0], kpb = par[8], vpa = par[P], vpb = par[P + 8];
+        float x[kNT][4];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kKW; ++i) {
+          const uint32_t a0 = unit_pair<0>(ka[i]), a1 = unit_pair<1>(ka[i]), a2 = unit_pair<2>(ka[i]), a3 = unit_pair<3>(ka[i]);
+          const uint32_t b0 = unit_pair<0>(kb[i]), b1 = unit_pair<1>(kb[i]), b2 = unit_pair<2>(kb[i]), b3 = unit_pair<3>(kb[i]);
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            mma16816(x[nt], a0, b0, a1, b1, q[nt][4 * i], q[nt][4 * i + 1]);
+            mma16816(x[nt], a2, b2, a3, b3, q[nt][4 * i + 2], q[nt][4 * i + 3]);
+          }
+        }
+        const float ksa = p.c * bf16_lo(kpa), ksb = p.c * bf16_lo(kpb);
+        const float kza = fmaf(-24.f, ksa, p.c * bf16_hi(kpa)), kzb = fmaf(-24.f, ksb, p.c * bf16_hi(kpb));
+        const bool edge = key0 + 16 > s.prefix;
+        uint32_t hidden = 0;  // bit 4 nt + i: element i is masked
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          x[nt][0] = fmaf(x[nt][0], 16.f * ksa, sq[nt][0] * kza);
+          x[nt][1] = fmaf(x[nt][1], 16.f * ksa, sq[nt][1] * kza);
+          x[nt][2] = fmaf(x[nt][2], 16.f * ksb, sq[nt][0] * kzb);
+          x[nt][3] = fmaf(x[nt][3], 16.f * ksb, sq[nt][1] * kzb);
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int rel = key0 + row_k + (i >= 2 ? 8 : 0) - s.prefix;  // draft token of the key
+              const bool vis = rel < 0 ? see[nt][i & 1] != 0 : rel < 32 && ((see[nt][i & 1] >> rel) & 1u);
+              if (!vis) {
+                x[nt][i] = -INFINITY;
+                hidden |= 1u << (4 * nt + i);
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) over |= x[nt][i] > m[nt][i & 1] + 8.f;
+        }
+        if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float mx = fmaxf(x[nt][e], x[nt][2 + e]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+              mx = fmaxf(mx, m[nt][e]);
+              const float f = m[nt][e] == mx ? 1.f : ex2(m[nt][e] - mx);  // 0 while m = -inf
+              m[nt][e] = mx;
+              l[nt][e] *= f;
+              zs[nt][e] *= f;
+              sp[nt][e] *= f;
+#pragma unroll
+              for (int i = 0; i < kMT; ++i) {
+                o[nt][i][e] *= f;
+                o[nt][i][2 + e] *= f;
+              }
+            }
+        }
+        const float vsa = bf16_lo(vpa), vsb = bf16_lo(vpb), vza = bf16_hi(vpa), vzb = bf16_hi(vpb);
+        uint32_t pb[kNT][2];
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          const float e0 = ex2(x[nt][0] - m0), e1 = ex2(x[nt][1] - m1), e2 = ex2(x[nt][2] - m0), e3 = ex2(x[nt][3] - m1);
+          l[nt][0] += e0 + e2;
+          l[nt][1] += e1 + e3;
+          float w0 = e0 * vsa, w1 = e1 * vsa, w2 = e2 * vsb, w3 = e3 * vsb;
+          float z0 = e0 * vza, z1 = e1 * vza, z2 = e2 * vzb, z3 = e3 * vzb;
+          if (edge) {  // parameters in masked places may be anything
+            const uint32_t hd = hidden >> (4 * nt);
+            if (hd & 1u) w0 = z0 = 0.f;
+            if (hd & 2u) w1 = z1 = 0.f;
+            if (hd & 4u) w2 = z2 = 0.f;
+            if (hd & 8u) w3 = z3 = 0.f;
+          }
+          zs[nt][0] += z0 + z2;
+          zs[nt][1] += z1 + z3;
+          pb[nt][0] = transpose8x8(pack_bf16x2(w0, w1));
+          pb[nt][1] = transpose8x8(pack_bf16x2(w2, w3));
+          mma16816(sp[nt], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, pb[nt][0], pb[nt][1]);
+        }
+        // V: keys phi(2t), phi(2t + 1) and 8 further, dims (d/8) g ..
+        const uint8_t* vc = pg + P * (kD / 2) + r0 * (kD / 2);
+        uint32_t v[4][kVW];  // keys: 2t, 2t + 1, 2t + 8, 2t + 9 of the group's order
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = ((k & 1) ? row_v ^ 5 : row_v) + ((k & 2) ? 8 : 0);
+          if constexpr (kD == 128)
+            *reinterpret_cast<uint2*>(v[k]) =
+                *reinterpret_cast<const uint2*>(vc + r * (kD / 2) + ((g * 8) ^ ((r & 2) << 4)));
+          else
+            v[k][0] = *reinterpret_cast<const uint32_t*>(vc + r * (kD / 2) + g * 4);
+        }
+#pragma unroll
+        for (int e = 0; e < kVW; ++e) {
+          const uint32_t lo0 = __byte_perm(v[0][e], v[1][e], 0x5410), hi0 = __byte_perm(v[0][e], v[1][e], 0x7632);
+          const uint32_t lo1 = __byte_perm(v[2][e], v[3][e], 0x5410), hi1 = __byte_perm(v[2][e], v[3][e], 0x7632);
+          const uint32_t a0[4] = {unit_pair<0>(lo0), unit_pair<1>(lo0), unit_pair<2>(lo0), unit_pair<3>(lo0)};
+          const uint32_t a1[4] = {unit_pair<0>(hi0), unit_pair<1>(hi0), unit_pair<2>(hi0), unit_pair<3>(hi0)};
+          const uint32_t a2[4] = {unit_pair<0>(lo1), unit_pair<1>(lo1), unit_pair<2>(lo1), unit_pair<3>(lo1)};
+          const uint32_t a3[4] = {unit_pair<0>(hi1), unit_pair<1>(hi1), unit_pair<2>(hi1), unit_pair<3>(hi1)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+              mma16816(o[nt][4 * e + j], a0[j], a1[j], a2[j], a3[j], pb[nt][0], pb[nt][1]);
+        }
+      }
+      fence_proxy_async_smem();  // these reads come before the copy that refills the stage
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    }
+    group = group_end;
+    // ------------------------------------------------------------ epilogue
+    // The warps' results meet in shared memory: o (dims 2j of word e at
+    // ((4 e + j) 8 + g) 2), then every row's sum over the warps.
+    if (named_bar_any(1, kComp, !ok)) break;
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float ls = l[nt][e], z = zs[nt][e];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          ls += __shfl_xor_sync(0xFFFFFFFFu, ls, x);
+          z += __shfl_xor_sync(0xFFFFFFFFu, z, x);
+        }
+        const int r = 8 * nt + 2 * t + e;
+        const float shift = fmaf(-24.f, sp[nt][e], z);
+        if (g == 0) mlsm[warp * C::kRows + r] = make_float2(m[nt][e], ls);
+        float* dst = osm + (warp * C::kRows + r) * C::kPitch + g * 2;
+#pragma unroll
+        for (int i = 0; i < kMT; ++i)
+          *reinterpret_cast<float2*>(dst + i * 16) =
+              make_float2(fmaf(16.f, o[nt][i][e], shift), fmaf(16.f, o[nt][i][2 + e], shift));
+      }
+    named_bar_sync(1, kComp);
+    const bool whole = s.whole();
+    float* po = p.part_o + (int64_t(blockIdx.x) * 2 + s.slot) * C::kRows * kD;
+    float2* pml = p.part_ml + (int64_t(blockIdx.x) * 2 + s.slot) * C::kRows;
+    // Output pairs of dims: pair pd is dims 2 pd, 2 pd + 1.
+    auto out_row = [&](int r) -> uint32_t* {
+      const int tok = r / p.G;
+      return reinterpret_cast<uint32_t*>(p.O + ((int64_t(s.b) * p.T + tok) * p.Hq + int64_t(s.h) * p.G + (r - tok * p.G)) * kD);
+    };
+    for (int i = tid; i < R * (kD / 2); i += kComp) {
+      const int r = i / (kD / 2), pd = i - r * (kD / 2);
+      const int at = kD == 128 ? ((((pd >> 2) & 1) * 4 + (pd & 3)) * 8 + (pd >> 3)) * 2 : ((pd & 3) * 8 + (pd >> 2)) * 2;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w) M = fmaxf(M, mlsm[w * C::kRows + r].x);
+      float L = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+      for (int w = 0; w < C::kWarps; ++w) {
+        const float2 ml = mlsm[w * C::kRows + r];
+        const float f = ml.x == M ? 1.f : ex2(ml.x - M);
+        const float2 v = *reinterpret_cast<const float2*>(osm + (w * C::kRows + r) * C::kPitch + at);
+        L = fmaf(f, ml.y, L);
+        a = fmaf(f, v.x, a);
+        b = fmaf(f, v.y, b);
+      }
+      if (whole) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        out_row(r)[pd] = pack_bf16x2(a * inv, b * inv);
+      } else {
+        *reinterpret_cast<float2*>(po + r * kD + 2 * pd) = make_float2(a, b);
+        if (pd == 0) pml[r] = make_float2(M, L);
+      }
+    }
+    if (!whole) {
+      const int item = s.b * p.Hkv + s.h;
+      fence_acq_rel_gpu();
+      named_bar_sync(1, kComp);
+      if (tid == 0) {
+        const int add = s.j1 - s.j0;
+        *merge_here = atomic_add_acq_rel_gpu(p.cnt + item, add) + add == s.nkb;
+        if (*merge_here) p.cnt[item] = 0;
+      }
+      named_bar_sync(1, kComp);
+      if (*merge_here) {
+        fence_acq_rel_gpu();
+        // Only the first of the item's CTAs can have begun its run before the item.
+        const int c0 = run_of(run, s.x0), c1 = run_of(run, s.x0 + s.nkb - 1);
+        const int first = run_start(run, c0) >= s.x0 ? 0 : 1;
+        for (int i = tid; i < R * (kD / 2); i += kComp) {
+          const int r = i / (kD / 2), pd = i - r * (kD / 2);
+          float M = -INFINITY, L = 0.f, a = 0.f, b = 0.f;
+#pragma unroll 4
+          for (int c = c0; c <= c1; ++c) {
+            const int64_t slot = int64_t(c) * 2 + (c == c0 ? first : 0);
+            const float2 ml = __ldcg(p.part_ml + slot * C::kRows + r);
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_o + (slot * C::kRows + r) * kD) + pd);
+            const float mn = fmaxf(M, ml.x);
+            const float fa = M == mn ? 1.f : ex2(M - mn), fb = ml.x == mn ? 1.f : ex2(ml.x - mn);
+            L = L * fa + fb * ml.y;
+            a = a * fa + fb * v.x;
+            b = b * fa + fb * v.y;
+            M = mn;
+          }
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          out_row(r)[pd] = pack_bf16x2(a * inv, b * inv);
+        }
+      }
+    }
+    named_bar_sync(1, kComp);  // shared memory is free for the next segment
+  }
+}
+
+}  // namespace kv4_attn
+}  // namespace w12
