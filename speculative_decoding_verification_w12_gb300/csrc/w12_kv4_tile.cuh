@@ -4,24 +4,32 @@
 // Work unit: 128 query rows of one (request, kv head), token-major, against one
 // block of 128 keys (the split is w12_kv4_sched.cuh's). Per block:
 //   raw pages -> shared memory   one bulk copy a page (warp 0)
-//   codes -> bf16 K and V tiles  four warps; thread i restores row i of the block:
-//                                z + s (q - 8), one rounding to bf16
+//   codes -> fp16 K and V tiles  eight warps, four for each; a thread restores one row
 //   S = Q K^T                    tcgen05.mma, D in TMEM, two buffers (warp 1)
-//   P = exp2(c S - m)            two warpgroups, one a 64-key half of the block; P
-//                                over its half's first 32 S columns as bf16 pairs
+//   P = exp2(S - M)              two warpgroups, one a 64-key half of the block; P
+//                                over its half's first 32 S columns as fp16 pairs
 //   O_h += P_h V_h               tcgen05.mma, A = P from TMEM, V MN-major (warp 2)
-// Here the scale is applied when the codes are restored: with 128 rows a tile,
-// one more packed operation on a restored pair costs less than scales and
-// centres in the softmax of 128 scores a key. The restored values are rounded
-// to bf16 (2^-8 relative), as the rows of a bf16 cache would be.
+//
+// Operands are fp16 (2^-11 relative) rather than bf16 (2^-8): restored values
+// z + s (q - 8) and P then add nothing that shows next to the output's own
+// rounding to bf16. Their range is kept by powers of two, which are exact: every
+// 32 keys (one restore warp) have an exponent e for K and f for V, the tile holds
+// value / 2^e, and a row of Q is held over its own power of two 2^a. With
+//   y_ij = c 2^(a_i + e_j) S_ij + f_j,       c = scale log2(e)
+// the weight that meets the scaled V is P = 2^(y - M), M a running maximum of y,
+// so what rounds to zero in P is below 2^-24 of what counts in the output; the
+// denominator sum of 2^(y - M) / 2^f_j is kept in fp32. Values that are more than
+// 2^14 below the largest of their 32 keys become fp16 subnormals, an absolute
+// error of at most 2^-25 of that largest value.
+//
+// The softmax takes 32 scores at a time and does not wait for a block's maximum:
+// it uses the running one, notes the block's, and does the block again in the rare
+// case that a score exceeds M by more than 8 (S is still in TMEM). The two
+// warpgroups keep separate maxima, sums and O accumulators, joined in the epilogue.
 //
 // A key whose V parameters are not finite gets V = 0 and K = NaN: its score is
 // NaN for the rows that see it and masked for the others, which P = 0 times NaN
-// would not leave alone. Rows of the block past the keys get V = 0.
-//
-// The softmax warpgroups keep separate maxima, sums and O accumulators for the
-// two key halves, joined in the epilogue; a maximum moves only when exceeded by
-// more than 8 (log2 units).
+// would not leave alone. Rows of the block past the keys get K = V = 0.
 #pragma once
 
 #include "w12_attn_dev.cuh"
@@ -31,17 +39,18 @@ namespace w12 {
 namespace kv4_attn {
 
 using attn_impl::block_max;
-using attn_impl::exp_pack;
+using attn_impl::add2;
+using attn_impl::fma2;
+using attn_impl::pack_f16x2;
 using attn_impl::fast_exp2;
 using attn_impl::mask_block;
 using attn_impl::rescale_row;
 using attn_impl::sdesc_mn_sw128;
-using attn_impl::tmem_ld_wait64;
 
 template <int kD>
 struct TileCfg {
-  static constexpr int kThreads = 512;     // warps 0-3 copy and issue, 4-11 softmax, 12-15 restore
-  static constexpr uint32_t kHalf = 128u * 128u;       // 128 rows x 64 bf16, 128-byte swizzle
+  static constexpr int kThreads = 640;     // warps 0-3 copy and issue, 4-11 softmax, 12-19 restore
+  static constexpr uint32_t kHalf = 128u * 128u;       // 128 rows x 64 fp16, 128-byte swizzle
   static constexpr uint32_t kTile = kHalf * (kD / 64);
   static constexpr uint32_t kRaw = uint32_t(kKeys) * (kD + 8);
   static constexpr int kRawStages = kD == 128 ? 3 : 6;
@@ -51,47 +60,61 @@ struct TileCfg {
   static constexpr uint32_t kVOff = kKOff + kStages * kTile;
   static constexpr uint32_t kRawOff = kVOff + kStages * kTile;
   static constexpr uint32_t kXchOff = kRawOff + kRawStages * kRaw;  // (m, l) of the two halves
-  static constexpr uint32_t kBarOff = kXchOff + 2 * 128 * 8;
+  static constexpr uint32_t kQxOff = kXchOff + 2 * 128 * 8;         // largest |Q| of the two half rows
+  // Exponents of the restored tiles, by block modulo 4 and 32 keys: (c 2^e, f, 2^-f, -).
+  // Four deep: K of block j + 2 may be restored while the softmax of block j still reads.
+  static constexpr uint32_t kExpOff = kQxOff + 2 * 128 * 4;
+  static constexpr uint32_t kBarOff = kExpOff + 16 * 16;
   static constexpr uint32_t kRunOff = kBarOff + 320;
   static constexpr uint32_t kSmem = kRunOff + 512 + 1024;           // 1024: alignment slack
   // TMEM columns: S of even and odd blocks, O of the two key halves.
   static constexpr uint32_t kS0 = 0, kS1 = 128, kOA = 256, kOB = 256 + kD, kCols = 512;
 };
 
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
 
-// Eight dims of a code word as bf16 values z + s (q - 8): 128 + q in bf16 bits,
-// less 136 (exact), then one rounding. s2 and z2 hold s and z in both halves.
+// Eight dims of a code word as fp16 values z + s (q - 8), s2 and z2 holding s and
+// z in both halves. A nibble in the lowest bits of fp16 1024 is 1024 + q, in the
+// next four 1024 + 16 q; both become q - 8 exactly, then one rounding.
 __device__ __forceinline__ uint4 restore_word(uint32_t w, uint32_t s2, uint32_t z2) {
+  constexpr uint32_t k1024 = 0x64006400u, kM1032 = 0xE408E408u, kSixteenth = 0x2C002C00u, kM72 = 0xD480D480u;
+  const uint32_t v = w >> 8;
   uint4 o;
-  const uint32_t k136 = 0x43084308u;
-  o.x = hfma2(hsub2((w & 0x000F000Fu) | 0x43004300u, k136), s2, z2);
-  o.y = hfma2(hsub2(((w >> 4) & 0x000F000Fu) | 0x43004300u, k136), s2, z2);
-  o.z = hfma2(hsub2(((w >> 8) & 0x000F000Fu) | 0x43004300u, k136), s2, z2);
-  o.w = hfma2(hsub2(((w >> 12) & 0x000F000Fu) | 0x43004300u, k136), s2, z2);
+  o.x = hfma2(hadd2((w & 0x000F000Fu) | k1024, kM1032), s2, z2);
+  o.y = hfma2(hfma2((w & 0x00F000F0u) | k1024, kSixteenth, kM72), s2, z2);
+  o.z = hfma2(hadd2((v & 0x000F000Fu) | k1024, kM1032), s2, z2);
+  o.w = hfma2(hfma2((v & 0x00F000F0u) | k1024, kSixteenth, kM72), s2, z2);
   return o;
 }
+
+// Exponent of a power of two that no value of a row passes: |z| + 8 s < 2^e,
+// -100 for rows of zeros and of values that are not finite; at most 120 (fp16
+// has room for the 2^8 that the largest rows then keep).
+__device__ __forceinline__ int row_exponent(uint32_t par) {
+  const float b = fmaf(8.f, bf16_lo(par), fabsf(bf16_hi(par)));
+  const int e = int((__float_as_uint(b) >> 23) & 255u) - 126;
+  return e > 128 ? -100 : min(max(e, -100), 120);  // 129: inf or NaN
+}
+
+// 2^e for -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
 // Thread i's row of the block: its codes (kD / 2 bytes at `src`, row r of its
 // page) into row i of a 128-byte-swizzled tile. The 16-byte pieces are taken in
 // an order that differs from row to row, so that the eight rows of a
 // shared-memory phase read and write different banks.
 template <int kD>
-__device__ __forceinline__ void restore_row(uint8_t* tile, const uint8_t* src, int i, uint32_t par, bool zero,
-                                            uint32_t poison) {
+__device__ __forceinline__ void restore_row(uint8_t* tile, const uint8_t* src, int i, uint32_t s2, uint32_t z2) {
   constexpr int kPieces = kD / 32;
-  uint32_t s2 = __byte_perm(par, par, 0x1010), z2 = __byte_perm(par, par, 0x3232);
-  if (zero) s2 = z2 = 0u;
-  z2 |= poison;
   const uint32_t flip = kD == 128 ? uint32_t(i) & 2u : 0u;  // halves swapped in rows with bit 1 set
 #pragma unroll
   for (int k = 0; k < kPieces; ++k) {
@@ -109,6 +132,41 @@ __device__ __forceinline__ void restore_row(uint8_t* tile, const uint8_t* src, i
 
 __device__ __forceinline__ bool not_finite(uint32_t par) {
   return (par & 0x7F80u) == 0x7F80u || (par & 0x7F800000u) == 0x7F800000u;
+}
+
+// Each thread of the warp reads 32 consecutive 32-bit columns of its own lane;
+// valid after tmem_ld_wait32, which ties the values to the wait.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : W12_TIE8(v, 0), W12_TIE8(v, 8), W12_TIE8(v, 16), W12_TIE8(v, 24)
+               :
+               : "memory");
+}
+
+// 2^(c v + b) of 32 scores: fp16 pairs into out[0 .. 16), returns the fp32 sum.
+__device__ __forceinline__ float exp_pack_f16(const uint32_t (&v)[32], float c, float b, uint32_t* out) {
+  float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  const float2 c2 = make_float2(c, c), b2 = make_float2(b, b);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 y = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, b2);
+    const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+    sum[k & 3] = add2(sum[k & 3], e);
+    out[k] = pack_f16x2(e.x, e.y);
+  }
+  const float2 s = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+  return s.x + s.y;
 }
 
 template <int kD>
@@ -132,13 +190,14 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* merge_here = abort_flag + 1;
   RunSmem& rs = *reinterpret_cast<RunSmem*>(smem + C::kRunOff);
+  float4* exps = reinterpret_cast<float4*>(smem + C::kExpOff);
   static_assert((2 * C::kRawStages + 4 * C::kStages + 12) * 8 + 16 <= 320 && sizeof(RunSmem) <= 512, "carve-up");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < C::kRawStages; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], 4);
+      mbar_init(&raw_empty[s], 8);
     }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&k_full[s], 4);
@@ -232,32 +291,35 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         mbar_wait(&raw_full[i % C::kRawStages], uint32_t(i / C::kRawStages) & 1u, drain_limit_ns(lim));
   } else if (warp == 1 || warp == 2) {
     // ---------------------------------------------------------------- MMA
-    if (lane == 0) {
-      const uint32_t sbase = smem_u32(smem);
-      const bool is_s = warp == 1;
-      const uint64_t qd = sdesc_k_sw128(sbase + C::kQOff);
-      const uint64_t kd0 = sdesc_k_sw128(sbase + C::kKOff);
-      const uint64_t vd0 = sdesc_mn_sw128(sbase + C::kVOff, C::kHalf);
-      const uint32_t idesc_s = idesc_bf16(128, 128);
-      const uint32_t idesc_o = idesc_bf16(128, kD) | (1u << 16);  // B (V) MN-major
-      int base = 0, si = 0;
-      bool ok = true;
-      while (ok && walk.next(p, run, s)) {
-        const int n = s.j1 - s.j0;
-        if (!wait(q_ready, uint32_t(si) & 1u)) break;
-        for (int j = 0; j < n; ++j) {
-          const int gj = base + j;
-          const int st = gj % C::kStages;
-          const uint32_t sb = tmem + ((gj & 1) ? C::kS1 : C::kS0);
-          if (is_s) {
-            // P of block j - 2 sits in the buffer that S overwrites.
-            if (!wait(&k_full[st], uint32_t(gj / C::kStages) & 1u) ||
-                (gj >= 2 && !wait(&o_done[gj & 1], uint32_t((gj - 2) >> 1) & 1u))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t kd = kd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
+    // The whole warp waits; one elected lane issues. (With the loop under one
+    // lane, descriptors pass from vector to uniform registers product by product.)
+    const uint32_t sbase = smem_u32(smem);
+    const bool is_s = warp == 1;
+    const uint64_t qd = sdesc_k_sw128(sbase + C::kQOff);
+    const uint64_t kd0 = sdesc_k_sw128(sbase + C::kKOff);
+    const uint64_t vd0 = sdesc_mn_sw128(sbase + C::kVOff, C::kHalf);
+    constexpr uint32_t idesc_s = idesc_f16(128, 128);
+    constexpr uint32_t idesc_o = idesc_f16(128, kD) | (1u << 16);  // B (V) MN-major
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+    int base = 0, si = 0;
+    bool ok = true;
+    while (ok && walk.next(p, run, s)) {
+      const int n = s.j1 - s.j0;
+      if (!wait_all(q_ready, uint32_t(si) & 1u)) break;
+      for (int j = 0; j < n; ++j) {
+        const int gj = base + j;
+        const int st = gj % C::kStages;
+        const uint32_t sb = tmem + ((gj & 1) ? C::kS1 : C::kS0);
+        if (is_s) {
+          // P of block j - 2 sits in the buffer that S overwrites.
+          if (!wait_all(&k_full[st], uint32_t(gj / C::kStages) & 1u) ||
+              (gj >= 2 && !wait_all(&o_done[gj & 1], uint32_t((gj - 2) >> 1) & 1u))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t kd = kd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < kD / 16; ++ks) {
               const uint64_t off = uint64_t((uint32_t(ks >> 2) * C::kHalf + uint32_t(ks & 3) * 32u) >> 4);
@@ -265,71 +327,88 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
             }
             tc_commit(&s_full[gj & 1]);
             tc_commit(&k_empty[st]);
-          } else {
-            if (!wait(&v_full[st], uint32_t(gj / C::kStages) & 1u)) {
+          }
+          __syncwarp();
+        } else {
+          if (!wait_all(&v_full[st], uint32_t(gj / C::kStages) & 1u)) {
+            ok = false;
+            break;
+          }
+          const uint64_t vd = vd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
+          for (int h = 0; h < 2; ++h) {
+            if (!wait_all(&p_full[(gj & 1) * 2 + h], uint32_t(gj >> 1) & 1u)) {
               ok = false;
               break;
             }
-            const uint64_t vd = vd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
-            for (int h = 0; h < 2; ++h) {
-              if (!wait(&p_full[(gj & 1) * 2 + h], uint32_t(gj >> 1) & 1u)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
               for (int ks = 0; ks < 4; ++ks) {
                 const uint64_t off = uint64_t((uint32_t(h) * 8192u + uint32_t(ks) * 2048u) >> 4);
                 mma_bf16_ts(tmem + (h ? C::kOB : C::kOA), sb + uint32_t(64 * h + 8 * ks), vd + off, idesc_o,
                             (j > 0 || ks > 0) ? 1u : 0u);
               }
+              if (h == 1) {
+                tc_commit(&o_done[gj & 1]);
+                tc_commit(&v_empty[st]);
+              }
             }
-            if (!ok) break;
-            tc_commit(&o_done[gj & 1]);
-            tc_commit(&v_empty[st]);
+            __syncwarp();
           }
+          if (!ok) break;
         }
-        if (!ok) break;
-        tc_commit(o_final);
-        base += n;
-        ++si;
       }
-      tc_commit(&drained[is_s ? 0 : 1]);
-      mbar_wait(&drained[is_s ? 0 : 1], 0, drain_limit_ns(lim));
+      if (!ok) break;
+      if (elect_one()) tc_commit(o_final);
+      __syncwarp();
+      base += n;
+      ++si;
     }
+    if (elect_one()) tc_commit(&drained[is_s ? 0 : 1]);
+    __syncwarp();
+    mbar_wait(&drained[is_s ? 0 : 1], 0, drain_limit_ns(lim));
   } else if (warp >= 12) {
     // ------------------------------------------------------------ restore
-    const int i = tid - 384;  // row of the block
+    // Warps 12-15 restore K, 16-19 V; thread i of each four has row i of the block.
+    const bool is_k = warp < 16;
+    const int i = (tid - 384) & 127;
+    uint64_t* fullb = is_k ? k_full : v_full;
+    uint64_t* emptyb = is_k ? k_empty : v_empty;
+    uint8_t* tiles = smem + (is_k ? C::kKOff : C::kVOff);
     int gj = 0;
     bool ok = true;
     while (ok && walk.next(p, run, s)) {
       for (int j = s.j0; j < s.j1; ++j, ++gj) {
         const int rst = gj % C::kRawStages, st = gj % C::kStages;
-        const uint32_t use = uint32_t(gj / C::kStages);
         if (!__all_sync(0xFFFFFFFFu, wait(&raw_full[rst], uint32_t(gj / C::kRawStages) & 1u)) ||
-            (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&k_empty[st], (use - 1u) & 1u)))) {
+            (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&emptyb[st], uint32_t(gj / C::kStages - 1) & 1u)))) {
           ok = false;
           break;
         }
         const uint8_t* pg = smem + C::kRawOff + rst * C::kRaw + (i >> p.p_shift) * int(p.block);
         const int r = i & (p.P - 1);
         const uint32_t* par = reinterpret_cast<const uint32_t*>(pg + p.P * kD) + r;
-        const uint32_t kp = par[0], vp = par[p.P];
+        const uint32_t vp = par[p.P], mine = is_k ? par[0] : vp;
         const bool past = j * kKeys + i >= s.keys;
-        const bool odd = !past && not_finite(vp);
-        restore_row<kD>(smem + C::kKOff + st * C::kTile, pg + r * (kD / 2), i, kp, past, odd ? 0x7FC07FC0u : 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&k_full[st]);
-        if (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&v_empty[st], (use - 1u) & 1u))) {
-          ok = false;
-          break;
+        const bool odd = not_finite(vp);
+        const int e = __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(mine));
+        const float down = pow2(-e);
+        uint32_t s2 = 0u, z2 = 0u;
+        if (!past && (is_k || !odd)) {
+          s2 = pack_f16x2(bf16_lo(mine) * down, bf16_lo(mine) * down);
+          z2 = pack_f16x2(bf16_hi(mine) * down, bf16_hi(mine) * down);
+          if (is_k && odd) z2 = 0x7E007E00u;
         }
-        restore_row<kD>(smem + C::kVOff + st * C::kTile, pg + (p.P + r) * (kD / 2), i, vp, past || odd, 0u);
+        if (is_k) {
+          // The K warps publish both exponents: the softmax then waits for K alone.
+          const int f = __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(vp));
+          if (lane == 0) exps[(gj & 3) * 4 + (i >> 5)] = make_float4(p.c * pow2(e), float(f), pow2(-f), 0.f);
+        }
+        restore_row<kD>(tiles + st * C::kTile, pg + (is_k ? r : p.P + r) * (kD / 2), i, s2, z2);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&v_full[st]);
+          mbar_arrive(&fullb[st]);
           mbar_arrive(&raw_empty[rst]);
         }
       }
@@ -350,34 +429,54 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       const bool valid = rr < R;
       const bool warp_live = __any_sync(0xFFFFFFFFu, valid);
       const int tok = valid ? rr / p.G : 0, hh = valid ? rr - tok * p.G : 0;
-      // Q rows into the swizzled Q tile: thread (h, r) takes half the row's pieces.
+      // Q rows into the swizzled Q tile, over a power of two that no value of the
+      // row passes: thread (h, r) takes half the row's pieces.
+      float up = 1.f;  // that power
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.Q + s.b * p.q_b + tok * p.q_t +
                                                           (int64_t(s.h) * p.G + hh) * p.q_h) + h * (kD / 16);
         uint4 v[kD / 16];
+        uint32_t big = 0u;
 #pragma unroll
-        for (int k = 0; k < kD / 16; ++k) v[k] = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < kD / 16; ++k) {
+          v[k] = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) big = max(big, max((w[x] << 16) & 0x7FFFFFFFu, w[x] & 0x7FFF0000u));
+        }
+        uint32_t* qx = reinterpret_cast<uint32_t*>(smem + C::kQxOff);
+        qx[h * 128 + r] = big;
+        named_bar_sync(1, 256);
+        big = max(big, qx[(1 - h) * 128 + r]);
+        const int a = min(max(int(big >> 23) - 126, -100), 120);  // a row with NaN or infinities stays one
+        up = pow2(a);
+        const float down = pow2(-a);
 #pragma unroll
         for (int k = 0; k < kD / 16; ++k) {
           const uint32_t piece = uint32_t(h * (kD / 16) + k);  // 8 dims
+          uint4 w;
+          w.x = pack_f16x2(bf16_lo(v[k].x) * down, bf16_hi(v[k].x) * down);
+          w.y = pack_f16x2(bf16_lo(v[k].y) * down, bf16_hi(v[k].y) * down);
+          w.z = pack_f16x2(bf16_lo(v[k].z) * down, bf16_hi(v[k].z) * down);
+          w.w = pack_f16x2(bf16_lo(v[k].w) * down, bf16_hi(v[k].w) * down);
           *reinterpret_cast<uint4*>(smem + C::kQOff + (piece >> 3) * C::kHalf + uint32_t(r) * 128u +
-                                    (((piece & 7u) ^ (uint32_t(r) & 7u)) << 4)) = v[k];
+                                    (((piece & 7u) ^ (uint32_t(r) & 7u)) << 4)) = w;
         }
       }
       uint32_t anc[4] = {0u, 0u, 0u, 0u};
-      int limit = 0;  // keys before it are seen
+      int limit = 0x7FFFFFFF;  // keys before it are seen (idle rows mask nothing: their results are not stored)
       if (p.parents) {
         int pr[4];
         attn_impl::parent_row(p.parents + int64_t(s.b) * p.T, p.T, pr);
         attn_impl::tree_ancestors(pr, tok, p.T, valid, anc, p.status);
-        limit = s.prefix;
-      } else {
+        if (valid) limit = s.prefix;
+      } else if (valid) {
         limit = s.prefix + tok + 1;
       }
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive(q_ready);
-      float m_ref = -INFINITY, l = 0.f;
+      float M = -INFINITY, l = 0.f;
       bool ok = true;
       const int n = s.j1 - s.j0;
       for (int i = 0; i < n; ++i) {
@@ -390,30 +489,43 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         tc_fence_after();
         if (warp_live) {
           const uint32_t sc = tmem + lane_off + ((gi & 1) ? C::kS1 : C::kS0) + uint32_t(64 * h);
-          uint32_t v[64];
+          const bool edge = limit - kb < 64;
+          uint32_t pk[32];
+          float psum, mx;
+          for (;;) {
+            const float ref = M == -INFINITY ? 0.f : M;
+            psum = 0.f;
+            mx = -INFINITY;
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) tmem_ld16(sc + uint32_t(ch * 16), *reinterpret_cast<uint32_t(*)[16]>(&v[ch * 16]));
-          tmem_ld_wait64(v);
-          if (kb + 64 > limit || !valid) mask_block<64>(v, kb, limit, anc, valid);
-          const float mx = block_max<64>(v) * p.c;
-          float factor = 1.f;
-          if (mx > m_ref + 8.f) {
-            factor = fast_exp2(m_ref - mx);  // 0 while m_ref = -inf
-            m_ref = mx;
-          }
-          const float psum = exp_pack<64>(v, p.c, m_ref == -INFINITY ? 0.f : -m_ref);
-          const bool resc = i > 0 && factor < 1.f && l > 0.f;
-          if (__any_sync(0xFFFFFFFFu, resc)) {
-            if (!__all_sync(0xFFFFFFFFu, wait(&o_done[(gi - 1) & 1], uint32_t((gi - 1) >> 1) & 1u))) {
-              ok = false;
-              break;
+            for (int ch = 0; ch < 2; ++ch) {
+              uint32_t v[32];
+              tmem_ld32(sc + uint32_t(ch * 32), v);
+              const float4 ex = exps[(gi & 3) * 4 + 2 * h + ch];
+              const float cc = fmaxf(ex.x * up, 1.2e-38f);
+              tmem_ld_wait32(v);
+              if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
+              mx = fmaxf(mx, fmaf(block_max<32>(v), cc, ex.y));
+              psum = fmaf(exp_pack_f16(v, cc, ex.y - ref, pk + 16 * ch), ex.z, psum);
             }
-            tc_fence_after();
-            rescale_row<kD>(o_own, resc ? factor : 1.f);
+            const bool over = mx > M + 8.f;
+            if (!__any_sync(0xFFFFFFFFu, over)) break;
+            // The running maximum moves: O and the sum follow, the block is done again.
+            const float factor = over ? fast_exp2(M - mx) : 1.f;  // 0 while M = -inf
+            if (over) M = mx;
+            l *= factor;
+            if (i > 0) {
+              if (!__all_sync(0xFFFFFFFFu, wait(&o_done[(gi - 1) & 1], uint32_t((gi - 1) >> 1) & 1u))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              rescale_row<kD>(o_own, factor);
+            }
           }
-          l = l * factor + psum;
-          tmem_st16(sc, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
-          tmem_st16(sc + 16u, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+          if (!ok) break;
+          l += psum;
+          tmem_st16(sc, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
+          tmem_st16(sc + 16u, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
           tmem_st_wait();
         }
         tc_fence_before();
@@ -423,12 +535,12 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       const bool fin = __all_sync(0xFFFFFFFFu, ok && wait(o_final, uint32_t(si) & 1u));
       if (named_bar_any(1, 256, !fin)) break;
       tc_fence_after();
-      xch[h * 128 + r] = make_float2(m_ref, l);
+      xch[h * 128 + r] = make_float2(M, l);
       named_bar_sync(1, 256);
       const float2 other = xch[(1 - h) * 128 + r];
-      const float ma = h ? other.x : m_ref, la = h ? other.y : l;
-      const float mb = h ? m_ref : other.x, lb = h ? l : other.y;
-      const float M = fmaxf(ma, mb);
+      const float ma = h ? other.x : M, la = h ? other.y : l;
+      const float mb = h ? M : other.x, lb = h ? l : other.y;
+      M = fmaxf(ma, mb);
       const float wa = ma == M ? 1.f : fast_exp2(ma - M), wb = mb == M ? 1.f : fast_exp2(mb - M);
       const float den = wa * la + wb * lb;
       const bool whole = s.whole();
