@@ -22,9 +22,11 @@
 // 2^14 below the largest of their 32 keys become fp16 subnormals, an absolute
 // error of at most 2^-25 of that largest value.
 //
-// The softmax takes 32 scores at a time and does not wait for a block's maximum:
-// it uses the running one, notes the block's, and does the block again in the rare
-// case that a score exceeds M by more than 8 (S is still in TMEM). The two
+// The softmax takes 32 scores at a time and does not look for a block's maximum: it
+// uses the running M, and only if the 32 weights sum to more than 2^12 (the first
+// block, or scores that grow along the keys) does it find the maximum and do the
+// block again (S is still in TMEM). Weights then stay below 2^12, inside fp16, and
+// the largest was at least 1 when M was set. The two
 // warpgroups keep separate maxima, sums and O accumulators, joined in the epilogue.
 //
 // A key whose V parameters are not finite gets V = 0 and K = NaN: its score is
@@ -46,6 +48,9 @@ using attn_impl::fast_exp2;
 using attn_impl::mask_block;
 using attn_impl::rescale_row;
 using attn_impl::sdesc_mn_sw128;
+
+constexpr float kMost = 4096.f;          // sum of 32 weights above which the running maximum moves
+constexpr uint32_t kWaitHintNs = 10000;  // asleep on a barrier between looks at the abort flag and the clock
 
 template <int kD>
 struct TileCfg {
@@ -108,27 +113,28 @@ __device__ __forceinline__ int row_exponent(uint32_t par) {
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
-// Thread i's row of the block: its codes (kD / 2 bytes at `src`, row r of its
-// page) into row i of a 128-byte-swizzled tile. The 16-byte pieces are taken in
-// an order that differs from row to row, so that the eight rows of a
-// shared-memory phase read and write different banks.
+// Where thread i of a block restores its row: the 16-byte pieces of its codes are
+// taken in an order that differs from row to row, so that the eight rows of a
+// shared-memory phase read and write different banks. Piece k is at byte 16 at(k)
+// of the row's codes and holds dims 32 c .. 32 c + 31; its word m goes to
+// dst(k) + word(m) of the row's 128-byte-swizzled tile.
 template <int kD>
-__device__ __forceinline__ void restore_row(uint8_t* tile, const uint8_t* src, int i, uint32_t s2, uint32_t z2) {
-  constexpr int kPieces = kD / 32;
-  const uint32_t flip = kD == 128 ? uint32_t(i) & 2u : 0u;  // halves swapped in rows with bit 1 set
+struct RowPlace {
+  static constexpr int kPieces = kD / 32;
+  uint32_t at[kPieces], dst[kPieces], word[4];
+  __device__ __forceinline__ explicit RowPlace(int i) {
+    const uint32_t x = uint32_t(i) & 7u;
 #pragma unroll
-  for (int k = 0; k < kPieces; ++k) {
-    const uint32_t at = (kD == 128 ? (uint32_t(i) >> 1) + k : (uint32_t(i) >> 2) + k) & (kPieces - 1);
-    const uint4 w = *reinterpret_cast<const uint4*>(src + at * 16);
-    const uint32_t c = at ^ flip;  // dims 32 c .. 32 c + 31
-    uint8_t* row = tile + (c >> 1) * 16384u + uint32_t(i) * 128u;
-    const uint32_t c8 = (c & 1u) * 4u, x = uint32_t(i) & 7u;
-    *reinterpret_cast<uint4*>(row + (((c8 + 0) ^ x) << 4)) = restore_word(w.x, s2, z2);
-    *reinterpret_cast<uint4*>(row + (((c8 + 1) ^ x) << 4)) = restore_word(w.y, s2, z2);
-    *reinterpret_cast<uint4*>(row + (((c8 + 2) ^ x) << 4)) = restore_word(w.z, s2, z2);
-    *reinterpret_cast<uint4*>(row + (((c8 + 3) ^ x) << 4)) = restore_word(w.w, s2, z2);
+    for (int k = 0; k < kPieces; ++k) {
+      const uint32_t a = (kD == 128 ? (uint32_t(i) >> 1) + k : (uint32_t(i) >> 2) + k) & (kPieces - 1);
+      const uint32_t c = a ^ (kD == 128 ? uint32_t(i) & 2u : 0u);  // halves swapped in rows with bit 1 set
+      at[k] = a * 16u;
+      dst[k] = (c >> 1) * 16384u + uint32_t(i) * 128u + ((((c & 1u) * 4u) ^ (x & 4u)) << 4);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) word[m] = (uint32_t(m) ^ (x & 3u)) << 4;
   }
-}
+};
 
 __device__ __forceinline__ bool not_finite(uint32_t par) {
   return (par & 0x7F80u) == 0x7F80u || (par & 0x7F800000u) == 0x7F800000u;
@@ -231,14 +237,12 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   const uint64_t lim = p.limit_ns;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 0; i < 0x80000000u; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if ((i & 63u) == 63u) {
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > lim) break;
-      }
+      if (mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > lim) break;
     }
     set_status(p.status, W12_ERR_TIMEOUT);
     *abort_flag = 1;
@@ -375,20 +379,24 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     uint64_t* fullb = is_k ? k_full : v_full;
     uint64_t* emptyb = is_k ? k_empty : v_empty;
     uint8_t* tiles = smem + (is_k ? C::kKOff : C::kVOff);
+    const RowPlace<kD> place(i);
     int gj = 0;
     bool ok = true;
     while (ok && walk.next(p, run, s)) {
       for (int j = s.j0; j < s.j1; ++j, ++gj) {
         const int rst = gj % C::kRawStages, st = gj % C::kStages;
-        if (!__all_sync(0xFFFFFFFFu, wait(&raw_full[rst], uint32_t(gj / C::kRawStages) & 1u)) ||
-            (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&emptyb[st], uint32_t(gj / C::kStages - 1) & 1u)))) {
+        if (!__all_sync(0xFFFFFFFFu, wait(&raw_full[rst], uint32_t(gj / C::kRawStages) & 1u))) {
           ok = false;
           break;
         }
         const uint8_t* pg = smem + C::kRawOff + rst * C::kRaw + (i >> p.p_shift) * int(p.block);
         const int r = i & (p.P - 1);
         const uint32_t* par = reinterpret_cast<const uint32_t*>(pg + p.P * kD) + r;
+        const uint8_t* src = pg + (is_k ? r : p.P + r) * (kD / 2);
         const uint32_t vp = par[p.P], mine = is_k ? par[0] : vp;
+        uint4 w[kD / 32];
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k) w[k] = *reinterpret_cast<const uint4*>(src + place.at[k]);
         const bool past = j * kKeys + i >= s.keys;
         const bool odd = not_finite(vp);
         const int e = __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(mine));
@@ -399,13 +407,25 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           z2 = pack_f16x2(bf16_hi(mine) * down, bf16_hi(mine) * down);
           if (is_k && odd) z2 = 0x7E007E00u;
         }
+        if (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&emptyb[st], uint32_t(gj / C::kStages - 1) & 1u))) {
+          ok = false;
+          break;
+        }
         if (is_k) {
           // The K warps publish both exponents: the softmax then waits for K alone.
           const int f = __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(vp));
           if (lane == 0) exps[(gj & 3) * 4 + (i >> 5)] = make_float4(p.c * pow2(e), float(f), pow2(-f), 0.f);
         }
-        restore_row<kD>(tiles + st * C::kTile, pg + (is_k ? r : p.P + r) * (kD / 2), i, s2, z2);
-        fence_proxy_async_smem();
+        uint8_t* tile = tiles + st * C::kTile;
+#pragma unroll
+        for (int k = 0; k < kD / 32; ++k) {
+          uint8_t* dst = tile + place.dst[k];
+          *reinterpret_cast<uint4*>(dst + place.word[0]) = restore_word(w[k].x, s2, z2);
+          *reinterpret_cast<uint4*>(dst + place.word[1]) = restore_word(w[k].y, s2, z2);
+          *reinterpret_cast<uint4*>(dst + place.word[2]) = restore_word(w[k].z, s2, z2);
+          *reinterpret_cast<uint4*>(dst + place.word[3]) = restore_word(w[k].w, s2, z2);
+        }
+        fence_proxy_async_smem();  // the tile before the MMAs read it, the raw stage before it is refilled
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&fullb[st]);
@@ -491,36 +511,50 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           const uint32_t sc = tmem + lane_off + ((gi & 1) ? C::kS1 : C::kS0) + uint32_t(64 * h);
           const bool edge = limit - kb < 64;
           uint32_t pk[32];
-          float psum, mx;
+          float psum;
+          // Rows that have seen nothing yet have no maximum to go by.
+          bool look = __any_sync(0xFFFFFFFFu, M == -INFINITY);
           for (;;) {
+            if (look) {
+              // The maximum moves to this block's where that is larger; O and the sum follow.
+              float mx = -INFINITY;
+#pragma unroll
+              for (int ch = 0; ch < 2; ++ch) {
+                uint32_t v[32];
+                tmem_ld32(sc + uint32_t(ch * 32), v);
+                tmem_ld_wait32(v);
+                const float4 ex = exps[(gi & 3) * 4 + 2 * h + ch];
+                if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
+                mx = fmaxf(mx, fmaf(block_max<32>(v), fmaxf(ex.x * up, 1.2e-38f), ex.y));
+              }
+              const float factor = mx > M ? fast_exp2(M - mx) : 1.f;  // 0 while M = -inf
+              M = fmaxf(M, mx);
+              l *= factor;
+              if (i > 0) {
+                if (!__all_sync(0xFFFFFFFFu, wait(&o_done[(gi - 1) & 1], uint32_t((gi - 1) >> 1) & 1u))) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                rescale_row<kD>(o_own, factor);
+              }
+            }
             const float ref = M == -INFINITY ? 0.f : M;
+            bool over = false;
             psum = 0.f;
-            mx = -INFINITY;
 #pragma unroll
             for (int ch = 0; ch < 2; ++ch) {
               uint32_t v[32];
               tmem_ld32(sc + uint32_t(ch * 32), v);
               const float4 ex = exps[(gi & 3) * 4 + 2 * h + ch];
-              const float cc = fmaxf(ex.x * up, 1.2e-38f);
               tmem_ld_wait32(v);
               if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
-              mx = fmaxf(mx, fmaf(block_max<32>(v), cc, ex.y));
-              psum = fmaf(exp_pack_f16(v, cc, ex.y - ref, pk + 16 * ch), ex.z, psum);
+              const float sum = exp_pack_f16(v, fmaxf(ex.x * up, 1.2e-38f), ex.y - ref, pk + 16 * ch);
+              over |= sum > kMost;
+              psum = fmaf(sum, ex.z, psum);
             }
-            const bool over = mx > M + 8.f;
-            if (!__any_sync(0xFFFFFFFFu, over)) break;
-            // The running maximum moves: O and the sum follow, the block is done again.
-            const float factor = over ? fast_exp2(M - mx) : 1.f;  // 0 while M = -inf
-            if (over) M = mx;
-            l *= factor;
-            if (i > 0) {
-              if (!__all_sync(0xFFFFFFFFu, wait(&o_done[(gi - 1) & 1], uint32_t((gi - 1) >> 1) & 1u))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              rescale_row<kD>(o_own, factor);
-            }
+            if (look || !__any_sync(0xFFFFFFFFu, over)) break;
+            look = true;
           }
           if (!ok) break;
           l += psum;
