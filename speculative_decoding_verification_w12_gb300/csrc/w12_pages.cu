@@ -23,8 +23,9 @@
 namespace w12 {
 namespace pages_impl {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kCluster = 8;
+constexpr int kSpan = 512;   // slots of one request that a warp writes at a time
 constexpr int kMaxB = 8192;  // requests per call (two prefix sums of B ints in shared memory)
 
 struct PagesParams {
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     const int b = last_le(gpre, p.B, k);
     p.table[int64_t(b) * p.max_pages + p.used[b] + (k - gpre[b])] = p.free_pages[n_free - 1 - k];
   }
-  cluster.sync();
+  if (G > 0) cluster.sync();  // the same in every CTA
   // Pushes.
   for (int k = me; k < R; k += all) {
     const int b = last_le(spre, p.B, k);
@@ -129,18 +130,25 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
     else set_status(p.status, W12_ERR_ARG);  // more pages than the pool has: counts that do not match
     *e = -1;
   }
-  // Slots of the new tokens.
-  const uint32_t cells = uint32_t(p.B) * uint32_t(p.T);  // < 2^31
-  for (uint32_t c = me; c < cells; c += all) {
-    const int b = int(c / uint32_t(p.T)), i = int(c - uint32_t(b) * uint32_t(p.T));
-    const Need n = need_of(p, b);
-    const int grow = n.want - n.have;
-    int slot = -1;
-    if (n.ok && i < p.add[b] && (grow <= 0 || gpre[b] + grow <= n_free)) {
-      const int pos = p.start[b] + i;
-      slot = p.table[int64_t(b) * p.max_pages + pos / p.P] * p.P + pos % p.P;
+  // Slots of the new tokens: a warp takes kSpan slots of one request at a time.
+  if (p.T > 0) {
+    const int spans = (p.T + kSpan - 1) / kSpan, units = p.B * spans;
+    const int p_shift = __ffs(p.P) - 1;
+    for (int u = me >> 5; u < units; u += all >> 5) {
+      const int b = u / spans, i0 = (u - b * spans) * kSpan;
+      const Need n = need_of(p, b);
+      const int grow = n.want - n.have;
+      const int start = p.start[b];
+      const int live = n.ok && (grow <= 0 || gpre[b] + grow <= n_free) ? p.add[b] : 0;
+      const int32_t* tab = p.table + int64_t(b) * p.max_pages;
+      int32_t* out = p.slots + int64_t(b) * p.T;
+      const int end = min(p.T, i0 + kSpan);
+#pragma unroll 4
+      for (int i = i0 + lane; i < end; i += 32) {
+        const int pos = start + i;
+        out[i] = i < live ? (tab[pos >> p_shift] << p_shift) + (pos & (p.P - 1)) : -1;
+      }
     }
-    p.slots[c] = slot;
   }
   cluster.sync();
   for (int b = me; b < p.B; b += all) {
@@ -173,14 +181,17 @@ extern "C" int w12_pages_update(int32_t* table, int32_t* used, int32_t* free_pag
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxB * 8) != cudaSuccess)
     return W12_ERR_CUDA;
+  // One CTA has a thread for every slot and request of a small call; more would
+  // only add the cluster's launch and barrier.
+  const int ctas = int64_t(B) * T <= 2 * kThreads && B <= kThreads ? 1 : kCluster;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCluster;
+  attr[0].val.clusterDim.x = unsigned(ctas);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(unsigned(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
