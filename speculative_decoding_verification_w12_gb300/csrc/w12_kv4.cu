@@ -12,7 +12,9 @@
 // All three are bound by HBM: append reads the input rows and writes d + 8
 // bytes a (token, head), read the reverse. One code word (8 dims) per lane:
 // d/8 lanes form a row, so inputs come in 16-byte (bf16) or 32-byte (fp32)
-// pieces and a row's codes leave as one 32- or 64-byte segment.
+// pieces and a row's codes leave as one 32- or 64-byte segment. A group of lanes
+// takes K and V of one (token, head), two loads in flight and one set of
+// indices (32-bit: a 64-bit division a row costs more than the quantiser).
 #include "w12_kv4.cuh"
 
 namespace w12 {
@@ -22,8 +24,8 @@ constexpr int kRowThreads = 256;
 
 struct RowParams {
   uint8_t* pool;
-  int64_t n_pages, block;  // bytes of a (page, kv head) block
-  int Hkv, P, p_shift;
+  int64_t block;  // bytes of a (page, kv head) block
+  int n_pages, Hkv, P, p_shift;
   const void *K, *V;
   int64_t k_tok, k_head, v_tok, v_head;  // strides in elements
   uint16_t *Ko, *Vo;
@@ -32,84 +34,89 @@ struct RowParams {
   int32_t* status;
 };
 
-template <typename E>
-__device__ __forceinline__ float to_f32(E v);
-template <>
-__device__ __forceinline__ float to_f32<float>(float v) {
-  return v;
-}
-struct Bf16 {
-  uint16_t b;
+// Input elements by type: 8 of them as loaded, their least and largest value over
+// a row's lanes (NaN passes), and their values.
+struct F32 {
+  static constexpr int kSize = 4;
+  uint32_t w[8];
+  __device__ __forceinline__ float value(int i) const { return __uint_as_float(w[i]); }
+  template <int kLanes>
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    lo = hi = value(0);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(value(i)));
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(value(i)));
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(__shfl_xor_sync(0xFFFFFFFFu, lo, o)));
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(__shfl_xor_sync(0xFFFFFFFFu, hi, o)));
+    }
+  }
 };
-struct F16 {
-  uint16_t b;
+
+// 16-bit types: pairs, and (largest, -least) as one pair on its way through the lanes.
+template <bool kBf16>
+struct Half {
+  static constexpr int kSize = 2;
+  uint32_t w[4];
+  static __device__ __forceinline__ float2 pair(uint32_t v) {
+    if constexpr (kBf16) return make_float2(bf16_lo(v), bf16_hi(v));
+    float2 f;
+    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(v));
+    return f;
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (kBf16) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ __forceinline__ float value(int i) const {
+    const float2 f = pair(w[i >> 1]);
+    return (i & 1) ? f.y : f.x;
+  }
+  template <int kLanes>
+  __device__ __forceinline__ void range(float& lo, float& hi) const {
+    constexpr uint32_t kSign = 0x80008000u;
+    uint32_t up = max2(max2(w[0], w[1]), max2(w[2], w[3]));
+    uint32_t down = max2(max2(w[0] ^ kSign, w[1] ^ kSign), max2(w[2] ^ kSign, w[3] ^ kSign));
+    // (largest of the even elements, least negated) and the same of the odd ones.
+    uint32_t v = max2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = max2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    const float2 f = pair(v);
+    hi = f.x;
+    lo = -f.y;
+  }
 };
-template <>
-__device__ __forceinline__ float to_f32<Bf16>(Bf16 v) {
-  return __uint_as_float(uint32_t(v.b) << 16);
-}
-template <>
-__device__ __forceinline__ float to_f32<F16>(F16 v) {
-  float f;
-  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(v.b));
-  return f;
-}
 
 template <typename E, bool kVec>
-__device__ __forceinline__ void load8(const E* p, float (&x)[8]) {
-  E e[8];
+__device__ __forceinline__ E load8(const uint8_t* p) {
+  E e;
   if constexpr (kVec) {
-    constexpr int kN = int(sizeof(e) / 16);
-    uint4* w = reinterpret_cast<uint4*>(e);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < int(sizeof(E) / 16); ++i)
+      reinterpret_cast<uint4*>(e.w)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  } else if constexpr (E::kSize == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e.w[i] = reinterpret_cast<const uint32_t*>(p)[i];
   } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = p[i];
+    for (int i = 0; i < 4; ++i) e.w[i] = uint32_t(h[2 * i]) | (uint32_t(h[2 * i + 1]) << 16);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = to_f32<E>(e[i]);
+  return e;
 }
 
-// Row unit u = (token, kv head, K or V); d/8 lanes per row.
-template <int kD, typename E, bool kVec>
-__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const __grid_constant__ RowParams p) {
-  constexpr int kLanes = kD / 8;
-  grid_dep_wait();
-  grid_dep_launch();
-  const int64_t unit = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) / kLanes;
-  const int w = threadIdx.x % kLanes;
-  const int per = 2 * p.Hkv;
-  const int64_t tok = unit / per;
-  const int rest = int(unit - tok * per);
-  const int which = rest & 1, h = rest >> 1;
-  const bool live = tok < p.n;
-  const int slot = live ? p.slots[tok] : -1;
-  const int64_t page = slot >> p.p_shift;
-  const bool in = slot >= 0 && page < p.n_pages;
-  if (live && !in && slot != -1) set_status(p.status, W12_ERR_ARG);
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = 0.f;
-  if (in) {
-    const E* src = static_cast<const E*>(which ? p.V : p.K) +
-                   (which ? tok * p.v_tok + h * p.v_head : tok * p.k_tok + h * p.k_head) + w * 8;
-    load8<E, kVec>(src, x);
-  }
-  float lo = x[0], hi = x[0], odd = 0.f;  // odd: NaN when any value is not finite
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    odd = fmaf(x[i], 0.f, odd);
-  }
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-    odd += __shfl_xor_sync(0xFFFFFFFFu, odd, o);
-  }
-  if (!in) return;
+// A row's code word of this lane and its parameter word.
+template <int kLanes, typename E>
+__device__ __forceinline__ uint2 quantise8(const E& e) {
+  float lo, hi;
+  e.template range<kLanes>(lo, hi);
   constexpr float kR = 1.0f / 15.0f;
   uint32_t sb = f32_to_bf16_rne(__fsub_rn(__fmul_rn(hi, kR), __fmul_rn(lo, kR)));
   float s = __uint_as_float(sb << 16);
@@ -117,21 +124,45 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const __grid_co
     sb = 0;
     s = 0.f;
   }
-  uint32_t zb = f32_to_bf16_rne(fmaf(8.f, s, lo));
+  const uint32_t zb = f32_to_bf16_rne(fmaf(8.f, s, lo));
   const float z = __uint_as_float(zb << 16);
-  if (odd != 0.f) sb = zb = 0x7FC0u;  // true for NaN
   const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
   uint32_t word = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(x[i], z), inv)) + 8.f, 0.f), 15.f);
+    const float q = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(e.value(i), z), inv)) + 8.f, 0.f), 15.f);
     word |= uint32_t(int(q)) << (4 * ((i >> 1) + 4 * (i & 1)));
   }
-  if (odd != 0.f) word = 0x88888888u;
+  const bool finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;  // false for NaN
+  return finite ? make_uint2(word, sb | (zb << 16)) : make_uint2(0x88888888u, 0x7FC07FC0u);
+}
+
+template <int kD, typename E, bool kVec>
+__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const __grid_constant__ RowParams p) {
+  constexpr int kLanes = kD / 8;
+  grid_dep_wait();
+  grid_dep_launch();
+  const uint32_t unit = blockIdx.x * uint32_t(kRowThreads / kLanes) + threadIdx.x / kLanes;  // < 2^31 + a CTA's
+  const int w = threadIdx.x % kLanes;
+  const uint32_t tok = unit / uint32_t(p.Hkv), h = unit - tok * uint32_t(p.Hkv);
+  const bool live = tok < uint32_t(p.n);
+  const int slot = live ? p.slots[tok] : -1;
+  const int page = slot >> p.p_shift;
+  const bool in = slot >= 0 && page < p.n_pages;
+  if (live && !in && slot != -1) set_status(p.status, W12_ERR_ARG);
+  E k{}, v{};
+  if (in) {
+    k = load8<E, kVec>(static_cast<const uint8_t*>(p.K) + (int64_t(tok) * p.k_tok + int64_t(h) * p.k_head + w * 8) * E::kSize);
+    v = load8<E, kVec>(static_cast<const uint8_t*>(p.V) + (int64_t(tok) * p.v_tok + int64_t(h) * p.v_head + w * 8) * E::kSize);
+  }
+  const uint2 kq = quantise8<kLanes>(k), vq = quantise8<kLanes>(v);
+  if (!in) return;
   const int r = slot & (p.P - 1);
-  uint8_t* blk = p.pool + (page * p.Hkv + h) * p.block;
-  *reinterpret_cast<uint32_t*>(blk + (which * p.P + r) * (kD / 2) + word_off(kD, r, w)) = word;
-  if (w == 0) *reinterpret_cast<uint32_t*>(blk + p.P * kD + (which * p.P + r) * 4) = sb | (zb << 16);
+  uint8_t* blk = p.pool + (int64_t(page) * p.Hkv + h) * p.block;
+  uint8_t* codes = blk + r * (kD / 2) + word_off(kD, r, w);
+  *reinterpret_cast<uint32_t*>(codes) = kq.x;
+  *reinterpret_cast<uint32_t*>(codes + p.P * (kD / 2)) = vq.x;
+  if (w < 2) *reinterpret_cast<uint32_t*>(blk + p.P * kD + (w * p.P + r) * 4) = w ? vq.y : kq.y;
 }
 
 template <int kD>
@@ -139,34 +170,34 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(const __grid_cons
   constexpr int kLanes = kD / 8;
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t unit = (int64_t(blockIdx.x) * kRowThreads + threadIdx.x) / kLanes;
+  const uint32_t unit = blockIdx.x * uint32_t(kRowThreads / kLanes) + threadIdx.x / kLanes;
   const int w = threadIdx.x % kLanes;
-  // K rows of all (token, head) first, then V's: a warp's stores are contiguous.
-  const int64_t rows = p.n * p.Hkv;
-  if (unit >= 2 * rows) return;
-  const int which = unit >= rows;
-  const int64_t row = unit - which * rows;
-  const int64_t tok = row / p.Hkv;
-  const int h = int(row - tok * p.Hkv);
+  const uint32_t tok = unit / uint32_t(p.Hkv), h = unit - tok * uint32_t(p.Hkv);
+  if (tok >= uint32_t(p.n)) return;
   const int slot = p.slots[tok];
-  const int64_t page = slot >> p.p_shift;
-  uint4 out = make_uint4(0, 0, 0, 0);
+  const int page = slot >> p.p_shift;
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
   if (slot >= 0 && page < p.n_pages) {
     const int r = slot & (p.P - 1);
-    const uint8_t* blk = p.pool + (page * p.Hkv + h) * p.block;
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(blk + (which * p.P + r) * (kD / 2) + word_off(kD, r, w));
-    const uint32_t par = *reinterpret_cast<const uint32_t*>(blk + p.P * kD + (which * p.P + r) * 4);
-    const float s = bf16_lo(par), z = bf16_hi(par);
-    uint32_t* o = &out.x;
+    const uint8_t* blk = p.pool + (int64_t(page) * p.Hkv + h) * p.block;
+    const uint8_t* codes = blk + r * (kD / 2) + word_off(kD, r, w);
+    const uint32_t* par = reinterpret_cast<const uint32_t*>(blk + p.P * kD) + r;
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(codes);
+    const uint32_t vw = *reinterpret_cast<const uint32_t*>(codes + p.P * (kD / 2));
+    const uint32_t kp = par[0], vp = par[p.P];
+    uint32_t *ko = &k.x, *vo = &v.x;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 v = value_pair(word, j, s, z);
-      o[j] = pack_bf16x2(v.x, v.y);
+      const float2 a = value_pair(kw, j, bf16_lo(kp), bf16_hi(kp)), b = value_pair(vw, j, bf16_lo(vp), bf16_hi(vp));
+      ko[j] = pack_bf16x2(a.x, a.y);
+      vo[j] = pack_bf16x2(b.x, b.y);
     }
   } else if (slot != -1) {
     set_status(p.status, W12_ERR_ARG);
   }
-  *reinterpret_cast<uint4*>((which ? p.Vo : p.Ko) + row * kD + w * 8) = out;
+  const int64_t at = int64_t(unit) * kD + w * 8;
+  *reinterpret_cast<uint4*>(p.Ko + at) = k;
+  *reinterpret_cast<uint4*>(p.Vo + at) = v;
 }
 
 // ------------------------------------------------------------------- commit
@@ -271,16 +302,16 @@ static cudaError_t launch_append(const cudaLaunchConfig_t& cfg, const RowParams&
 
 template <int kD>
 static cudaError_t launch_append(const cudaLaunchConfig_t& cfg, const RowParams& p, int dtype, bool vec) {
-  return dtype == W12_F32    ? launch_append<kD, float>(cfg, p, vec)
-         : dtype == W12_BF16 ? launch_append<kD, Bf16>(cfg, p, vec)
-                             : launch_append<kD, F16>(cfg, p, vec);
+  return dtype == W12_F32    ? launch_append<kD, F32>(cfg, p, vec)
+         : dtype == W12_BF16 ? launch_append<kD, Half<true>>(cfg, p, vec)
+                             : launch_append<kD, Half<false>>(cfg, p, vec);
 }
 
 static int row_params(const w12_kv4* c, const int32_t* slots, int64_t n, int32_t* status, RowParams* p) {
   if (!c || !c->pool || !slots || n < 0 || !aligned(c->pool, 16)) return W12_ERR_ARG;
-  if (!cache_ok(c) || n > (int64_t(1) << 31) / c->Hkv) return W12_ERR_SHAPE;
+  if (!cache_ok(c) || n > int64_t(0x7FFFFFFF) / c->Hkv) return W12_ERR_SHAPE;
   p->pool = c->pool;
-  p->n_pages = c->n_pages;
+  p->n_pages = int(c->n_pages);
   p->block = block_bytes(c->page_size, c->head_dim);
   p->Hkv = c->Hkv;
   p->P = c->page_size;
@@ -323,7 +354,7 @@ int w12_kv4_append(const w12_kv4* cache, const void* K, const void* V, int dtype
   p.v_head = v_head_stride;
   const int64_t all = (k_token_stride | k_head_stride | v_token_stride | v_head_stride) * esize;
   const bool vec = aligned(K, 16) && aligned(V, 16) && all % 16 == 0;
-  const int64_t threads = n * 2 * p.Hkv * (cache->head_dim / 8);
+  const int64_t threads = n * p.Hkv * (cache->head_dim / 8);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = config(dim3(unsigned((threads + kRowThreads - 1) / kRowThreads)), kRowThreads,
                                         static_cast<cudaStream_t>(stream), attr);
@@ -341,7 +372,7 @@ int w12_kv4_read(const w12_kv4* cache, const int32_t* slots, int64_t n, uint16_t
   if (n == 0) return W12_OK;
   p.Ko = K_out;
   p.Vo = V_out;
-  const int64_t threads = n * 2 * p.Hkv * (cache->head_dim / 8);
+  const int64_t threads = n * p.Hkv * (cache->head_dim / 8);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = config(dim3(unsigned((threads + kRowThreads - 1) / kRowThreads)), kRowThreads,
                                         static_cast<cudaStream_t>(stream), attr);

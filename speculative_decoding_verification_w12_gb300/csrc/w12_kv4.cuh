@@ -51,10 +51,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
-// Dim pair (2j, 2j + 1) of a code word as two fp32 values z + s (q - 8).
+// Dim pair (2j, 2j + 1) of a code word as two fp32 values z + s (q - 8). The
+// nibble becomes the mantissa of 2^23 + q, from which 2^23 + 8 leaves q - 8.
 __device__ __forceinline__ float2 value_pair(uint32_t w, int j, float s, float z) {
-  const uint32_t n = w >> (4 * j);
-  const float a = float(int(n & 15u) - 8), b = float(int((n >> 16) & 15u) - 8);
+  const float a = __uint_as_float(((w >> (4 * j)) & 15u) | 0x4B000000u) - 8388616.f;
+  const float b = __uint_as_float(((w >> (4 * j + 16)) & 15u) | 0x4B000000u) - 8388616.f;
   return make_float2(fmaf(s, a, z), fmaf(s, b, z));
 }
 

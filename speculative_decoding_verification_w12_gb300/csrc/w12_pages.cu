@@ -23,9 +23,10 @@
 namespace w12 {
 namespace pages_impl {
 
-constexpr int kThreads = 1024;
+constexpr int kSmall = 256;   // threads of a small call's only CTA
+constexpr int kLarge = 1024;  // threads of each CTA of a large call's cluster
 constexpr int kCluster = 8;
-constexpr int kSpan = 512;   // slots of one request that a warp writes at a time
+constexpr int kSpan = 256;    // slots of one request that a warp writes at a time
 constexpr int kMaxB = 8192;  // requests per call (two prefix sums of B ints in shared memory)
 
 struct PagesParams {
@@ -33,7 +34,7 @@ struct PagesParams {
   const int32_t *start, *add;
   int32_t* slots;
   int32_t* status;
-  int B, max_pages, P, n_pages, T;
+  int B, max_pages, p_shift, n_pages, T;
 };
 
 struct Need {
@@ -44,11 +45,10 @@ struct Need {
 __device__ __forceinline__ Need need_of(const PagesParams& p, int b) {
   const int start = p.start[b], add = p.add ? p.add[b] : 0, have = p.used[b];
   Need n;
-  const int64_t total = int64_t(start) + add;
-  n.ok = start >= 0 && add >= 0 && add <= p.T && have >= 0 && have <= p.max_pages &&
-         total <= int64_t(p.max_pages) * p.P;
+  const int64_t want = (int64_t(start) + add + (1 << p.p_shift) - 1) >> p.p_shift;
+  n.ok = start >= 0 && add >= 0 && add <= p.T && have >= 0 && have <= p.max_pages && want <= p.max_pages;
   n.have = n.ok ? have : 0;
-  n.want = n.ok ? int((total + p.P - 1) / p.P) : 0;
+  n.want = n.ok ? int(want) : 0;
   return n;
 }
 
@@ -63,6 +63,7 @@ __device__ __forceinline__ int last_le(const int* pre, int n, int k) {
   return lo;
 }
 
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_constant__ PagesParams p) {
   extern __shared__ int smem[];
   int* gpre = smem;         // pages taken by the requests before b
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
   }
   if (G > 0) cluster.sync();  // the same in every CTA
   // Pushes.
+#pragma unroll 2
   for (int k = me; k < R; k += all) {
     const int b = last_le(spre, p.B, k);
     const Need n = need_of(p, b);
@@ -133,7 +135,6 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
   // Slots of the new tokens: a warp takes kSpan slots of one request at a time.
   if (p.T > 0) {
     const int spans = (p.T + kSpan - 1) / kSpan, units = p.B * spans;
-    const int p_shift = __ffs(p.P) - 1;
     for (int u = me >> 5; u < units; u += all >> 5) {
       const int b = u / spans, i0 = (u - b * spans) * kSpan;
       const Need n = need_of(p, b);
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
 #pragma unroll 4
       for (int i = i0 + lane; i < end; i += 32) {
         const int pos = start + i;
-        out[i] = i < live ? (tab[pos >> p_shift] << p_shift) + (pos & (p.P - 1)) : -1;
+        out[i] = i < live ? (tab[pos >> p.p_shift] << p.p_shift) + (pos & ((1 << p.p_shift) - 1)) : -1;
       }
     }
   }
@@ -176,26 +177,34 @@ extern "C" int w12_pages_update(int32_t* table, int32_t* used, int32_t* free_pag
       int64_t(B) * T > 0x7FFFFFFF)
     return W12_ERR_SHAPE;
   if (!device_supported()) return W12_ERR_UNSUPPORTED;
-  PagesParams p{table, used, free_pages, n_free, start, add, slots, dev_status, B, max_pages, page_size, int(n_pages), T};
+  PagesParams p{table, used, free_pages, n_free, start, add, slots, dev_status, B, max_pages,
+                __builtin_ctz(unsigned(page_size)), int(n_pages), T};
   const size_t smem = size_t(B) * 2 * sizeof(int);
-  if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(pages_update_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxB * 8) != cudaSuccess)
-    return W12_ERR_CUDA;
-  // One CTA has a thread for every slot and request of a small call; more would
-  // only add the cluster's launch and barrier.
-  const int ctas = int64_t(B) * T <= 2 * kThreads && B <= kThreads ? 1 : kCluster;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = unsigned(ctas);
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = attr;
+  cfg.attrs = overlap_enabled() ? attr : attr + 1;
+  // A small call (a verify step's blocks) is one CTA: a cluster's launch and
+  // barriers cost more than its threads bring (16 requests: 2.4 us a trim
+  // instead of 5). A trim is small by the pages it may give back.
+  const int64_t most = T > 0 ? int64_t(B) * T : int64_t(B) * max_pages / 2;
+  if (most <= 4096 && B <= kSmall) {
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kSmall);
+    cfg.numAttrs = overlap_enabled() ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, pages_update_kernel<kSmall>, p));
+  }
+  if (smem > 40 * 1024 && cudaFuncSetAttribute(pages_update_kernel<kLarge>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMaxB * 8) != cudaSuccess)
+    return W12_ERR_CUDA;
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kLarge);
   cfg.numAttrs = overlap_enabled() ? 2 : 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, pages_update_kernel, p));
+  return cuda_status(cudaLaunchKernelEx(&cfg, pages_update_kernel<kLarge>, p));
 }
