@@ -127,12 +127,20 @@ __device__ __forceinline__ uint2 quantise8(const E& e) {
   const uint32_t zb = f32_to_bf16_rne(fmaf(8.f, s, lo));
   const float z = __uint_as_float(zb << 16);
   const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-  uint32_t word = 0;
+  // q = clamp(round(t), -8, 7) + 8 as the low bits of 1.5 2^23 + 8 + t (adding it
+  // rounds t to the nearest integer, ties to even, like rint); the eight sums of
+  // the constant's own bits come off at the end.
+  constexpr float kMagic = 12582920.f;
+  constexpr uint32_t kBits = 0x4B400000u;
+  uint32_t word = 0, base = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(e.value(i), z), inv)) + 8.f, 0.f), 15.f);
-    word |= uint32_t(int(q)) << (4 * ((i >> 1) + 4 * (i & 1)));
+    const int at = 4 * ((i >> 1) + 4 * (i & 1));
+    const float t = __fmul_rn(__fsub_rn(e.value(i), z), inv);
+    word += __float_as_uint(__fadd_rn(fminf(fmaxf(t, -8.f), 7.f), kMagic)) << at;
+    base += kBits << at;
   }
+  word -= base;
   const bool finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;  // false for NaN
   return finite ? make_uint2(word, sb | (zb << 16)) : make_uint2(0x88888888u, 0x7FC07FC0u);
 }
@@ -146,15 +154,17 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const __grid_co
   const int w = threadIdx.x % kLanes;
   const uint32_t tok = unit / uint32_t(p.Hkv), h = unit - tok * uint32_t(p.Hkv);
   const bool live = tok < uint32_t(p.n);
-  const int slot = live ? p.slots[tok] : -1;
-  const int page = slot >> p.p_shift;
-  const bool in = slot >= 0 && page < p.n_pages;
-  if (live && !in && slot != -1) set_status(p.status, W12_ERR_ARG);
+  // The inputs do not wait for the slot: all three loads are in flight together.
   E k{}, v{};
-  if (in) {
+  int slot = -1;
+  if (live) {
     k = load8<E, kVec>(static_cast<const uint8_t*>(p.K) + (int64_t(tok) * p.k_tok + int64_t(h) * p.k_head + w * 8) * E::kSize);
     v = load8<E, kVec>(static_cast<const uint8_t*>(p.V) + (int64_t(tok) * p.v_tok + int64_t(h) * p.v_head + w * 8) * E::kSize);
+    slot = p.slots[tok];
   }
+  const int page = slot >> p.p_shift;
+  const bool in = slot >= 0 && page < p.n_pages;
+  if (!in && slot != -1) set_status(p.status, W12_ERR_ARG);
   const uint2 kq = quantise8<kLanes>(k), vq = quantise8<kLanes>(v);
   if (!in) return;
   const int r = slot & (p.P - 1);
