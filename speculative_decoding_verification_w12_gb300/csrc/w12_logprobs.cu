@@ -2,24 +2,29 @@
 //
 // With x = scale * logit: lse = log sum e^x, logprob(t) = x_t - lse,
 // entropy = lse - sum p x, and the k largest logprobs with their tokens (ties:
-// lowest token first). One pass: a CTA holds a chunk of one row in registers (as
-// it came: 16-byte pieces), finds its maximum m, the sums s0 = sum 2^y and
-// s1 = sum 2^y y over y = (x - m) log2(e), and its k largest elements; the row's
-// last CTA to finish joins the chunks:
-//   M = max m_i, d_i = (m_i - M) log2(e), S0 = sum 2^d_i s0_i,
-//   S1 = sum 2^d_i (s1_i + d_i s0_i), lse = M + log S0, entropy = log S0 - ln 2 S1 / S0.
-// Sums are fp32, over at most 64 elements a thread and then trees. Bound by the
-// read of the logits for many rows, by launch and join latency for few.
+// lowest token first). One pass over chunks of 16 KB of a row. Persistent CTAs take
+// runs of consecutive chunks (a run ends with its row); a copy warp streams the
+// chunks into a ring in shared memory. A thread keeps, over a run, a reference r
+// (its first maximum; it moves only when a value exceeds it by more than 40) and
+//   s0 = sum 2^y, s1 = sum 2^y y,  y = (x - r) log2(e),
+// so the warps go through the run without a barrier. At its end they are joined:
+//   M = max r_i, d_i = (r_i - M) log2(e), S0 = sum 2^d_i s0_i,
+//   S1 = sum 2^d_i (s1_i + d_i s0_i), lse = M + log S0, entropy = log S0 - ln 2 S1 / S0,
+// and likewise a row's runs by the one that finishes last. Sums are fp32: at most
+// a run's share of a thread, then trees. Bound by the read of the logits and the
+// issue of about 7 instructions an element for many rows, by launch and join
+// latency for few.
 //
-// Top k of a set held by the CTA's threads: an element's key is its value as an
-// ordered 32-bit integer over the complement of its index, so keys are unique
-// and their order is the output's. Each warp finds the r = ceil(k / warps)
-// largest of its lanes' own maxima; the least of the warps' r-th is a value that
-// at least k elements reach, so only elements from it on are candidates (a few
-// dozen; a thread looks only into pieces whose maximum reaches it). They go to a
-// list in shared memory, and a candidate's rank is the number of larger ones. A
-// list that would overflow (equal values, or values sorted along the row) takes
-// the k maxima one by one instead.
+// Top k of a run: an element's key is its value as an ordered 32-bit integer over
+// the complement of its index, so keys are unique and their order is the
+// output's. In the first chunk each warp finds the r = ceil(k / warps) largest of
+// its lanes' own maxima; the least of the warps' r-th is a value that at least k
+// elements reach, so only elements from it on are candidates (a few dozen). They
+// go to a list in shared memory; a candidate's rank is the number of larger ones,
+// and the k-th is the bound for the run's other chunks, where a thread looks only
+// into pieces whose maximum reaches it. A list that would overflow (equal values,
+// or values that rise along the row) is not used: the k maxima are then taken one
+// by one from the logits.
 //
 // Elements of -inf (masked tokens) are no candidates: slots of the top list
 // that no element fills get token -1 and logprob -inf. A row of nothing else
@@ -33,10 +38,15 @@
 namespace w12 {
 namespace logprobs_impl {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // and a copy warp
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxK = 32;
 constexpr int kCap = 1024;  // candidates listed in shared memory
+constexpr int kPieces = 4;     // 16-byte pieces of a chunk that a thread holds
+constexpr int kChunkBytes = kThreads * kPieces * 16;
+constexpr int kStages = 2;
+constexpr int kCtas = 4;       // CTAs an SM
+constexpr float kFar = 40.f;   // a value this far above its thread's reference moves it
 constexpr int kStaged = 1280;   // chunk candidates the join holds in shared memory
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -47,9 +57,11 @@ struct Params {
   float scale;
   const int32_t* tokens;
   int n, k, nch;
+  int64_t chunks;   // M nch
+  uint64_t limit_ns;
   float *logprob, *entropy, *lse, *top_lp;
   int32_t* top_id;
-  float4* part;     // [M, nch]: (m, s0, s1, -)
+  float4* part;     // [M, nch], by run of the row: (m, s0, s1, -)
   uint64_t* cand;   // [M, nch, k]: keys, largest first (0 = none)
   int32_t* done;    // [M]: chunks finished (zero between calls)
   int32_t* status;
@@ -83,28 +95,46 @@ __device__ __forceinline__ float warp_fmax(float v) {
   return v;
 }
 
-struct TopSmem {
+struct Smem {
+  alignas(128) uint8_t ring[kStages][kChunkBytes];
   uint64_t list[kCap];
+  uint64_t staged[kStaged];
+  uint64_t best[kMaxK];
   uint64_t warp_key[kWarps];
-  int count;
+  uint64_t full[kStages], empty[kStages];
+  float red[3][kWarps];
+  uint32_t wtop[kWarps];  // each warp's r-th largest lane maximum
+  int count;              // candidates of the run
+  int last;               // whether the run completed its row
+  int failed;
 };
 
-// The k largest of the listed candidates, largest first, in out[0 .. k) (0 where
-// there are fewer); n is their number. With n > kCap the list does not hold them
-// all: each(f) calls f(key) for all keys of the thread (0 = none).
-template <typename Each>
-__device__ __forceinline__ void rank_candidates(TopSmem& sm, int n, int k, uint64_t* out, Each&& each) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (n <= kCap) {
-    for (int i = tid; i < n; i += kThreads) {
-      const uint64_t key = sm.list[i];
-      int rank = 0;
-      for (int j = 0; j < n; ++j) rank += sm.list[j] > key;
-      if (rank < k) out[rank] = key;
-    }
-    for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
-    return;
+// Barrier of the computing threads.
+__device__ __forceinline__ void sync() { named_bar_sync(1, kThreads); }
+
+// The k largest of the n <= kCap listed candidates, largest first, in out[0 .. k)
+// (0 where there are fewer); four lanes count a candidate's larger ones.
+__device__ __forceinline__ void rank_list(const uint64_t* list, int n, int k, uint64_t* out) {
+  const int tid = threadIdx.x, warp = tid >> 5;
+  for (int i0 = 0; i0 < n; i0 += kThreads / 4) {
+    const int i = i0 + (tid >> 2);
+    if (i0 + (warp << 3) >= n) break;  // no candidate in this warp
+    const uint64_t key = i < n ? list[i] : ~uint64_t(0);
+    int rank = 0;
+#pragma unroll 4
+    for (int j = tid & 3; j < n; j += 4) rank += list[j] > key;
+    rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 1);
+    rank += __shfl_xor_sync(0xFFFFFFFFu, rank, 2);
+    if (i < n && (tid & 3) == 0 && rank < k) out[rank] = key;
   }
+  for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
+}
+
+// The same one maximum at a time: each(f) calls f(key) for all keys of the thread
+// (0 = none). Every computing thread calls it.
+template <typename Each>
+__device__ __forceinline__ void rank_all(Smem& s, int k, uint64_t* out, Each&& each) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint64_t below = ~uint64_t(0);
   for (int i = 0; i < k; ++i) {
     uint64_t m = 0;
@@ -112,20 +142,20 @@ __device__ __forceinline__ void rank_candidates(TopSmem& sm, int n, int k, uint6
       if (key < below && key > m) m = key;
     });
     m = warp_max(m);
-    __syncthreads();
-    if (lane == 0) sm.warp_key[warp] = m;
-    __syncthreads();
-    m = sm.warp_key[0];
+    sync();
+    if (lane == 0) s.warp_key[warp] = m;
+    sync();
+    m = s.warp_key[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = max(m, sm.warp_key[w]);
+    for (int w = 1; w < kWarps; ++w) m = max(m, s.warp_key[w]);
     if (tid == 0) out[i] = m;
     below = m;
   }
 }
 
-__device__ __forceinline__ void list_candidate(TopSmem& sm, uint64_t key) {
-  const int at = atomicAdd(&sm.count, 1);
-  if (at < kCap) sm.list[at] = key;
+__device__ __forceinline__ void list_candidate(Smem& s, uint64_t key) {
+  const int at = atomicAdd(&s.count, 1);
+  if (at < kCap) s.list[at] = key;
 }
 
 // Warps whose lanes all hold elements where the first `threads` threads do (at
@@ -200,243 +230,112 @@ __device__ __forceinline__ float ex2(float x) {
 
 // Keeps the pieces as loaded between passes: without it the compiler holds their
 // converted values (twice the registers) from one pass to the next.
-template <int kPieces>
 __device__ __forceinline__ void as_loaded(uint4 (&raw)[kPieces]) {
 #pragma unroll
   for (int i = 0; i < kPieces; ++i)
     asm volatile("" : "+r"(raw[i].x), "+r"(raw[i].y), "+r"(raw[i].z), "+r"(raw[i].w));
 }
 
-// kPieces 16-byte pieces a thread: piece i of thread t is the chunk's elements
-// (i * kThreads + t) * kN .. + kN - 1 (kVec: one 16-byte load).
-template <int kType, int kPieces, bool kVec>
-__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ Params p) {
-  using Pc = Piece<kType>;
-  constexpr int kN = Pc::kN;
-  __shared__ TopSmem sm;
-  __shared__ float red[2][kWarps];
-  __shared__ uint32_t wtop[2][kWarps];  // each warp's largest and r-th largest lane maximum
-  __shared__ int last;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunk = blockIdx.x;
-  const int64_t row = blockIdx.y;
-  constexpr int64_t kEsize = kType == kF32 ? 4 : 2;
-  const uint8_t* base = static_cast<const uint8_t*>(p.logits) + row * p.pitch * kEsize;
-  const int64_t c0 = int64_t(chunk) * (kThreads * kPieces * kN);
+// (r, s0, s1) of a set with the reference moved to `to` (>= r); an empty set adds nothing.
+__device__ __forceinline__ void moved(float r, float to, float& s0, float& s1) {
+  if (r == to || (r == -INFINITY && s0 == 0.f)) return;  // (NaN sums stay in)
+  const float d = max_nan((r - to) * kLog2e, -200.f), f = ex2(d);
+  s1 = f * fmaf(d, s0, s1);
+  s0 *= f;
+}
 
-  grid_dep_wait();
-  grid_dep_launch();
-  uint4 raw[kPieces];
+// Joins (r, s0, s1) of all computing threads; every one gets the result.
+__device__ __forceinline__ void join_sums(Smem& s, float& r, float& s0, float& s1) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float wm = warp_fmax(r);
+  if (lane == 0) s.red[0][warp] = wm;
+  sync();
+  float M = s.red[0][0];
 #pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    const int64_t e0 = c0 + (i * kThreads + tid) * kN;
-    if (kVec && e0 + kN <= p.V) {
-      raw[i] = __ldg(reinterpret_cast<const uint4*>(base + e0 * kEsize));
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = Pc::kMinusInf;
-        if constexpr (kType == kF32) {
-          if (e0 + j < p.V) w[j] = reinterpret_cast<const uint32_t*>(base)[e0 + j];
-        } else {
-          const uint16_t* h = reinterpret_cast<const uint16_t*>(base);
-          if (e0 + 2 * j < p.V) w[j] = (w[j] & 0xFFFF0000u) | h[e0 + 2 * j];
-          if (e0 + 2 * j + 1 < p.V) w[j] = (w[j] & 0x0000FFFFu) | (uint32_t(h[e0 + 2 * j + 1]) << 16);
-        }
-      }
-      raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  }
-  // x = scale * logit + 0: monotonic in the logit, and a zero of either sign is one value.
-  float top[kPieces], mine = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i) {
-    top[i] = fmaf(Pc::largest(raw[i]), p.scale, 0.f);
-    mine = fmaxf(mine, top[i]);
-  }
-  const int live = live_warps((p.V - c0) / kN);
-  {
-    // Lanes of equal value leave together: the r-th taken is then lower, a weaker bound.
-    const int r = max(1, (p.k + live - 1) / live);
-    uint32_t o = mine > -INFINITY ? order_of(mine) : 0u, cut = 0u;
-    for (int i = 0; i < r; ++i) {
-      cut = __reduce_max_sync(0xFFFFFFFFu, o);
-      if (i == 0 && lane == 0) wtop[0][warp] = cut;
-      if (o == cut) o = 0u;
-    }
-    if (lane == 0) wtop[1][warp] = cut;
-    if (tid == 0) sm.count = 0;
-  }
-  __syncthreads();
-  uint32_t mo = wtop[0][0], cut = wtop[1][0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) {
-    mo = max(mo, wtop[0][w]);
-    if (w < live) cut = min(cut, wtop[1][w]);
-  }
-  const float m = mo ? value_of(mo) : -INFINITY;
-  const uint32_t i0 = uint32_t(c0) + tid * kN;
-  as_loaded(raw);
-  if (p.k > 0) {
-    // cut = 0 (a warp without r maxima): every element is a candidate.
-    const float least = cut ? value_of(cut) : -INFINITY;
-    if (mine >= least) {
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i)
-        if (top[i] >= least) {
-          float x[kN];
-          Pc::values(raw[i], x);
-#pragma unroll
-          for (int j = 0; j < kN; ++j) {
-            x[j] = fmaf(x[j], p.scale, 0.f);
-            if (x[j] >= least && x[j] > -INFINITY) list_candidate(sm, key_of(x[j], i0 + i * (kThreads * kN) + j));
-          }
-        }
-    }
-  }
-  float s0, s1;
-  as_loaded(raw);
-  {
-    // Masked elements: y = -inf is held at -200, whose power is 0. NaN passes.
-    // (x - m first: m log2(e) alone may pass the fp32 range.)
-    const float bb = m == -INFINITY ? 0.f : -m;
-    float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-    const float2 c2 = make_float2(p.scale, p.scale), b2 = make_float2(bb, bb);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      float x[kN];
-      Pc::values(raw[i], x);
-#pragma unroll
-      for (int j = 0; j < kN; j += 2) {
-        float2 y = attn_impl::fma2(make_float2(x[j], x[j + 1]), c2, b2);
-        y.x = max_nan(y.x * kLog2e, -200.f);
-        y.y = max_nan(y.y * kLog2e, -200.f);
-        const float2 e = make_float2(ex2(y.x), ex2(y.y));
-        a0 = attn_impl::add2(a0, e);
-        a1 = attn_impl::fma2(e, y, a1);
-      }
-    }
-    s0 = warp_sum(a0.x + a0.y);
-    s1 = warp_sum(a1.x + a1.y);
-  }
-  as_loaded(raw);
+  for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s.red[0][w]);
+  moved(r, M, s0, s1);
+  s0 = warp_sum(s0);
+  s1 = warp_sum(s1);
   if (lane == 0) {
-    red[0][warp] = s0;
-    red[1][warp] = s1;
+    s.red[1][warp] = s0;
+    s.red[2][warp] = s1;
   }
-  __syncthreads();
-  const int64_t slot = row * p.nch + chunk;
-  if (tid == 0) {
-    float a = 0.f, b = 0.f;
+  sync();
+  s0 = s1 = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      a += red[0][w];
-      b += red[1][w];
-    }
-    p.part[slot] = make_float4(m, a, b, 0.f);
+  for (int w = 0; w < kWarps; ++w) {
+    s0 += s.red[1][w];
+    s1 += s.red[2][w];
   }
-  if (p.k > 0)
-    rank_candidates(sm, sm.count, p.k, p.cand + slot * p.k, [&](auto&& f) {
-      as_loaded(raw);
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        float x[kN];
-        Pc::values(raw[i], x);
-#pragma unroll
-        for (int j = 0; j < kN; ++j) {
-          x[j] = fmaf(x[j], p.scale, 0.f);
-          f(x[j] > -INFINITY ? key_of(x[j], i0 + i * (kThreads * kN) + j) : uint64_t(0));
-        }
-      }
-    });
-  // The row's last chunk joins them all.
-  __syncthreads();
-  if (tid == 0) {
-    fence_acq_rel_gpu();
-    const int before = atomic_add_acq_rel_gpu(p.done + row, 1);
-    last = before == p.nch - 1;
-    if (last) p.done[row] = 0;
-  }
-  __syncthreads();
-  if (!last) return;
+  r = M;
+}
+
+// Joins the np runs of a finished row and writes its outputs. Every computing
+// thread calls it.
+template <int kType>
+__device__ __noinline__ void join_row(const Params& p, int64_t row, int np, Smem& s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint8_t* base = static_cast<const uint8_t*>(p.logits) + row * p.pitch * (kType == kF32 ? 4 : 2);
   fence_acq_rel_gpu();
   // Loads of both kinds are in flight together.
   const float4* part = p.part + row * p.nch;
   const uint64_t* cand = p.cand + row * p.nch * p.k;
-  const int total = p.nch * p.k;
-  __shared__ uint64_t staged[kStaged];
+  const int total = np * p.k;
   const bool in_smem = total <= kStaged;
-  float4 first = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-  if (tid < p.nch) first = __ldcg(part + tid);
+  float4 v = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  if (tid < np) v = __ldcg(part + tid);
   uint64_t best = 0;
   for (int i = tid; i < total; i += kThreads) {
     const uint64_t key = __ldcg(cand + i);
     best = max(best, key);
-    if (in_smem) staged[i] = key;
+    if (in_smem) s.staged[i] = key;
   }
-  float M = first.x;
-  for (int i = tid + kThreads; i < p.nch; i += kThreads) M = fmaxf(M, __ldcg(part + i).x);
-  M = warp_fmax(M);
-  if (lane == 0) red[0][warp] = M;
-  const int live2 = live_warps(total);
-  {
-    const int r = max(1, (p.k + live2 - 1) / live2);
-    uint64_t mine2 = best, cut2 = 0;
-    for (int i = 0; i < r; ++i) {
-      cut2 = warp_max(mine2);
-      if (mine2 == cut2) mine2 = 0;
-    }
-    if (lane == 0) sm.warp_key[warp] = cut2;
-    if (tid == 0) sm.count = 0;
+  float r = v.x, s0 = v.y, s1 = v.z;
+  for (int i = tid + kThreads; i < np; i += kThreads) {
+    float4 u = __ldcg(part + i);
+    const float to = fmaxf(r, u.x);
+    moved(r, to, s0, s1);
+    moved(u.x, to, u.y, u.z);
+    r = to;
+    s0 += u.y;
+    s1 += u.z;
   }
-  __syncthreads();
-  M = red[0][0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) M = fmaxf(M, red[0][w]);
+  const int live = live_warps(total);
   if (p.k > 0) {
-    uint64_t cut2 = sm.warp_key[0];
-    for (int w = 1; w < live2; ++w) cut2 = min(cut2, sm.warp_key[w]);
-    cut2 = max(cut2, uint64_t(1));  // key 0 is no element
-    if (best >= cut2)
+    const int n = (p.k + live - 1) / live;
+    uint64_t mine = best, cut = 0;
+    for (int i = 0; i < n; ++i) {
+      cut = warp_max(mine);
+      if (mine == cut) mine = 0;
+    }
+    if (lane == 0) s.warp_key[warp] = cut;
+  }
+  if (tid == 0) s.count = 0;
+  join_sums(s, r, s0, s1);
+  if (p.k > 0) {
+    uint64_t cut = s.warp_key[0];
+    for (int w = 1; w < live; ++w) cut = min(cut, s.warp_key[w]);
+    cut = max(cut, uint64_t(1));  // key 0 is no element
+    if (best >= cut)
       for (int i = tid; i < total; i += kThreads) {
-        const uint64_t key = in_smem ? staged[i] : __ldcg(cand + i);
-        if (key >= cut2) list_candidate(sm, key);
+        const uint64_t key = in_smem ? s.staged[i] : __ldcg(cand + i);
+        if (key >= cut) list_candidate(s, key);
       }
+    sync();
+    if (s.count <= kCap)
+      rank_list(s.list, s.count, p.k, s.best);
+    else
+      rank_all(s, p.k, s.best, [&](auto&& f) {
+        for (int i = tid; i < total; i += kThreads) f(in_smem ? s.staged[i] : __ldcg(cand + i));
+      });
+    sync();
   }
-  float S0 = 0.f, S1 = 0.f;
-  for (int i = tid; i < p.nch; i += kThreads) {
-    const float4 v = i < kThreads ? first : __ldcg(part + i);
-    if (v.x == -INFINITY && v.y == 0.f) continue;  // a chunk of masked tokens (NaN sums stay in)
-    const float d = v.x == M ? 0.f : max_nan((v.x - M) * kLog2e, -200.f), w = ex2(d);
-    S0 = fmaf(w, v.y, S0);
-    S1 += w * fmaf(d, v.y, v.z);
-  }
-  S0 = warp_sum(S0);
-  S1 = warp_sum(S1);
-  __syncthreads();
-  if (lane == 0) {
-    red[0][warp] = S0;
-    red[1][warp] = S1;
-  }
-  __shared__ uint64_t best_keys[kMaxK];
-  if (p.k > 0)
-    rank_candidates(sm, sm.count, p.k, best_keys, [&](auto&& f) {
-      for (int i = tid; i < total; i += kThreads) f(in_smem ? staged[i] : __ldcg(cand + i));
-    });
-  __syncthreads();
-  S0 = S1 = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    S0 += red[0][w];
-    S1 += red[1][w];
-  }
-  const bool nothing = M == -INFINITY && S0 == 0.f;
-  const float logS = logf(S0);
-  const float lse = nothing ? -INFINITY : M + logS;
+  const bool nothing = r == -INFINITY && s0 == 0.f;
+  const float logS = logf(s0);
+  const float lse = nothing ? -INFINITY : r + logS;
   if (tid == 0) {
     p.lse[row] = lse;
-    p.entropy[row] = nothing ? 0.f : logS - kLn2 * (S1 / S0);
+    p.entropy[row] = nothing ? 0.f : logS - kLn2 * (s1 / s0);
   }
   for (int j = tid; j < p.n; j += kThreads) {
     const int t = p.tokens[row * p.n + j];
@@ -450,44 +349,272 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     p.logprob[row * p.n + j] = lp;
   }
   if (tid < p.k) {
-    const uint64_t key = best_keys[tid];
+    const uint64_t key = s.best[tid];
     p.top_id[row * p.k + tid] = key ? int32_t(~uint32_t(key)) : -1;
     p.top_lp[row * p.k + tid] = key ? value_of(uint32_t(key >> 32)) - lse : -INFINITY;
   }
 }
 
-// 16-byte pieces a thread: 8 where the rows then still give every SM a few chunks,
-// 4 below that (short calls are latency-bound: more, smaller chunks).
-static int pieces_of(int64_t M, int64_t V, int esize) {
-  const int64_t c = int64_t(kThreads) * 8 * (16 / esize);
-  return M * ((V + c - 1) / c) >= 600 ? 8 : 4;
+// Chunk c is elements (c % nch) * kPer .. of row c / nch; piece i of thread t is
+// the chunk's elements (i * kThreads + t) * kN .. + kN - 1. kVec: rows start on
+// 16-byte boundaries and come by bulk copies, but for a last part of a piece.
+template <int kType, bool kVec>
+__global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const __grid_constant__ Params p) {
+  using Pc = Piece<kType>;
+  constexpr int kN = Pc::kN;
+  constexpr int kEsize = kType == kF32 ? 4 : 2;
+  constexpr int kPer = kChunkBytes / kEsize;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+  volatile int* failed = &s.failed;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t c_begin = int64_t(blockIdx.x) * p.chunks / gridDim.x;
+  const int64_t c_end = int64_t(blockIdx.x + 1) * p.chunks / gridDim.x;
+  const int total = int(c_end - c_begin);
+  const uint8_t* logits = static_cast<const uint8_t*>(p.logits);
+  int64_t row = c_begin / p.nch;
+  int chunk = int(c_begin - row * p.nch);
+
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kWarps);
+    }
+    s.count = 0;
+    s.failed = 0;
+    fence_barrier_init();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  __syncthreads();
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------- copies
+    if (!kVec || lane != 0) return;
+    int c = 0;
+    for (; c < total; ++c) {
+      const int st = c % kStages;
+      if (c >= kStages && !mbar_wait(&s.empty[st], uint32_t(c / kStages - 1) & 1u, p.limit_ns)) {
+        set_status(p.status, W12_ERR_TIMEOUT);
+        *failed = 1;
+        break;
+      }
+      const int64_t left = (p.V - int64_t(chunk) * kPer) * kEsize;
+      const uint32_t bytes = uint32_t(left < kChunkBytes ? left : int64_t(kChunkBytes)) & ~15u;
+      mbar_arrive_expect_tx(&s.full[st], bytes);
+      if (bytes) bulk_load(s.ring[st], logits + (row * p.pitch + int64_t(chunk) * kPer) * kEsize, bytes, &s.full[st]);
+      if (++chunk == p.nch) {
+        chunk = 0;
+        ++row;
+      }
+    }
+    // The CTA ends only with every copy landed.
+    for (int i = c > kStages ? c - kStages : 0; i < c; ++i)
+      mbar_wait(&s.full[i % kStages], uint32_t(i / kStages) & 1u, drain_limit_ns(p.limit_ns));
+    return;
+  }
+
+  // ---------------------------------------------------------------- compute
+  const float2 c2 = make_float2(p.scale, p.scale);
+  int done = 0;                              // chunks of the run
+  float ref = -INFINITY, s0 = 0.f, s1 = 0.f;
+  float least = -INFINITY;                   // candidates reach it
+  for (int c = 0; c < total; ++c) {
+    const int64_t e0 = int64_t(chunk) * kPer;
+    const uint8_t* base = logits + row * p.pitch * kEsize;
+    uint4 raw[kPieces];
+    if constexpr (kVec) {
+      const int st = c % kStages;
+      if (!*failed && !mbar_wait(&s.full[st], uint32_t(c / kStages) & 1u, p.limit_ns)) {
+        set_status(p.status, W12_ERR_TIMEOUT);
+        *failed = 1;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) raw[i] = *reinterpret_cast<const uint4*>(&s.ring[st][(i * kThreads + tid) * 16]);
+      fence_proxy_async_smem();  // before the copy that refills the stage
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.empty[st]);
+    }
+    if (!kVec || e0 + kPer > p.V) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int64_t at = e0 + (i * kThreads + tid) * kN;
+        if (kVec && at + kN <= p.V) continue;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = Pc::kMinusInf;
+          if constexpr (kType == kF32) {
+            if (at + j < p.V) w[j] = reinterpret_cast<const uint32_t*>(base)[at + j];
+          } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(base);
+            if (at + 2 * j < p.V) w[j] = (w[j] & 0xFFFF0000u) | h[at + 2 * j];
+            if (at + 2 * j + 1 < p.V) w[j] = (w[j] & 0x0000FFFFu) | (uint32_t(h[at + 2 * j + 1]) << 16);
+          }
+        }
+        raw[i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    // x = scale * logit + 0: monotonic in the logit, and a zero of either sign is one value.
+    float top[kPieces], mine = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      top[i] = fmaf(Pc::largest(raw[i]), p.scale, 0.f);
+      mine = fmaxf(mine, top[i]);
+    }
+    if (mine > ref + kFar) {
+      moved(ref, mine, s0, s1);
+      ref = mine;
+    }
+    if (p.k > 0 && done == 0) {
+      // A run's first chunk: a value that k of its elements reach (0: not known).
+      // Lanes of equal value leave together: the r-th taken is then lower.
+      const int live = live_warps((p.V - e0) / kN), r = (p.k + live - 1) / live;
+      uint32_t o = mine > -INFINITY ? order_of(mine) : 0u, cut = 0u;
+      for (int i = 0; i < r; ++i) {
+        cut = __reduce_max_sync(0xFFFFFFFFu, o);
+        if (o == cut) o = 0u;
+      }
+      if (lane == 0) s.wtop[warp] = cut;
+      sync();
+      cut = s.wtop[0];
+      for (int w = 1; w < live; ++w) cut = min(cut, s.wtop[w]);
+      least = cut ? value_of(cut) : -INFINITY;
+    }
+    const uint32_t i0 = uint32_t(e0) + tid * kN;
+    as_loaded(raw);
+    if (p.k > 0 && mine >= least && mine > -INFINITY) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (top[i] >= least) {
+          float x[kN];
+          Pc::values(raw[i], x);
+#pragma unroll
+          for (int j = 0; j < kN; ++j) {
+            x[j] = fmaf(x[j], p.scale, 0.f);
+            if (x[j] >= least && x[j] > -INFINITY) list_candidate(s, key_of(x[j], i0 + i * (kThreads * kN) + j));
+          }
+        }
+    }
+    as_loaded(raw);
+    {
+      // Masked elements: y = -inf is held at -200, whose power is 0. NaN passes.
+      // (x - r first: r log2(e) alone may pass the fp32 range.)
+      const float b = ref == -INFINITY ? 0.f : -ref;
+      const float2 b2 = make_float2(b, b);
+      float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        float x[kN];
+        Pc::values(raw[i], x);
+#pragma unroll
+        for (int j = 0; j < kN; j += 2) {
+          float2 y = attn_impl::fma2(make_float2(x[j], x[j + 1]), c2, b2);
+          y.x = max_nan(y.x * kLog2e, -200.f);
+          y.y = max_nan(y.y * kLog2e, -200.f);
+          const float2 e = make_float2(ex2(y.x), ex2(y.y));
+          a0 = attn_impl::add2(a0, e);
+          a1 = attn_impl::fma2(e, y, a1);
+        }
+      }
+      s0 += a0.x + a0.y;
+      s1 += a1.x + a1.y;
+    }
+    ++done;
+    const bool ends = chunk == p.nch - 1 || c + 1 == total;
+    if (p.k > 0 && done == 1 && !ends) {
+      // The bound for the rest of the run: the k-th of the first chunk.
+      sync();
+      const int n = s.count;
+      if (n <= kCap) {
+        rank_list(s.list, n, p.k, s.best);
+        sync();
+        const uint64_t kth = s.best[p.k - 1];
+        if (kth) least = value_of(uint32_t(kth >> 32));
+        if (tid < p.k) s.list[tid] = s.best[tid];
+        if (tid == 0) s.count = n < p.k ? n : p.k;
+      }
+      sync();
+    }
+    if (ends) {
+      // The run's results: slot by the run's place among those of its row.
+      const int64_t g = gridDim.x;
+      const int64_t x0 = row * p.nch;
+      const int first = int(((x0 + 1) * g - 1) / p.chunks);  // the CTA that holds the row's first chunk
+      const int64_t slot = x0 + (int64_t(blockIdx.x) - first);
+      join_sums(s, ref, s0, s1);
+      if (tid == 0) p.part[slot] = make_float4(ref, s0, s1, 0.f);
+      if (p.k > 0) {
+        uint64_t* out = p.cand + slot * p.k;
+        if (s.count <= kCap) {  // (join_sums' barriers: the list is whole)
+          rank_list(s.list, s.count, p.k, out);
+        } else {
+          const int64_t r0 = e0 + kPer - int64_t(done) * kPer, r1 = min(p.V, e0 + kPer);
+          rank_all(s, p.k, out, [&](auto&& f) {
+            for (int64_t e = r0 + tid; e < r1; e += kThreads) {
+              const float x = fmaf(element<kType>(base, e), p.scale, 0.f);
+              f(x > -INFINITY ? key_of(x, uint32_t(e)) : uint64_t(0));
+            }
+          });
+        }
+      }
+      sync();
+      if (tid == 0) {
+        fence_acq_rel_gpu();
+        const bool last = atomic_add_acq_rel_gpu(p.done + row, done) + done == p.nch;
+        if (last) p.done[row] = 0;
+        s.last = last;
+        s.count = 0;
+      }
+      sync();
+      if (s.last) {
+        const int end = int(((x0 + p.nch) * g - 1) / p.chunks);  // the CTA of the row's last chunk
+        join_row<kType>(p, row, end - first + 1, s);
+        sync();
+        if (tid == 0) s.count = 0;
+      }
+      done = 0;
+      ref = -INFINITY;
+      s0 = s1 = 0.f;
+      least = -INFINITY;
+    }
+    if (++chunk == p.nch) {
+      chunk = 0;
+      ++row;
+    }
+  }
 }
 
-static int chunks_of(int64_t M, int64_t V, int esize) {
-  const int64_t c = int64_t(kThreads) * pieces_of(M, V, esize) * (16 / esize);
-  return int((V + c - 1) / c);
-}
+static int esize_of(int dtype) { return dtype == W12_F32 ? 4 : 2; }
+
+static int64_t chunks_of(int64_t V, int esize) { return (V * esize + kChunkBytes - 1) / kChunkBytes; }
 
 static bool shape_ok(int64_t M, int64_t V, int k) {
   return M >= 1 && M <= 65535 && V >= 1 && V < (int64_t(1) << 30) && k >= 0 && k <= kMaxK;
 }
 
-// For either element size (fp32 has the more chunks of a given size, but may
-// take the larger pieces earlier).
+// For any element type (fp32 has the most chunks).
 static size_t ws_bytes_of(int64_t M, int64_t V, int k) {
-  const int64_t a = chunks_of(M, V, 4), b = chunks_of(M, V, 2), nch = a > b ? a : b;
+  const int64_t nch = chunks_of(V, 4);
   return size_t(round_up(M * 4, 256) + M * nch * 16 + M * nch * k * 8);
 }
 
-template <int kType, int kPieces>
-static cudaError_t launch(const cudaLaunchConfig_t& cfg, const Params& p, bool vec) {
-  return vec ? cudaLaunchKernelEx(&cfg, logprobs_kernel<kType, kPieces, true>, p)
-             : cudaLaunchKernelEx(&cfg, logprobs_kernel<kType, kPieces, false>, p);
-}
-
 template <int kType>
-static cudaError_t launch(const cudaLaunchConfig_t& cfg, const Params& p, int pieces, bool vec) {
-  return pieces == 8 ? launch<kType, 8>(cfg, p, vec) : launch<kType, 4>(cfg, p, vec);
+static cudaError_t launch(cudaLaunchConfig_t cfg, const Params& p, bool vec) {
+  static bool ready[64] = {false};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev]) {
+    e = cudaFuncSetAttribute(logprobs_kernel<kType, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Smem)));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(logprobs_kernel<kType, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(Smem)));
+    if (e != cudaSuccess) return e;
+    ready[dev] = true;
+  }
+  return vec ? cudaLaunchKernelEx(&cfg, logprobs_kernel<kType, true>, p)
+             : cudaLaunchKernelEx(&cfg, logprobs_kernel<kType, false>, p);
 }
 
 }  // namespace logprobs_impl
@@ -503,7 +630,7 @@ size_t w12_logprobs_ws_bytes(int64_t M, int64_t V, int k) { return shape_ok(M, V
 int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t row_stride, float scale,
                  const int32_t* tokens, int n, int k, float* logprob, float* entropy, float* lse, float* top_logprob,
                  int32_t* top_id, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream) {
-  const int esize = dtype == W12_F32 ? 4 : 2;
+  const int esize = esize_of(dtype);
   if (!logits || dtype < W12_F32 || dtype > W12_F16 || !aligned(logits, esize) || !(scale > 0.f) || scale > 1e30f ||
       n < 0 || (n > 0 && (!tokens || !logprob)) || !entropy || !lse || (k > 0 && (!top_logprob || !top_id)))
     return W12_ERR_ARG;
@@ -518,7 +645,9 @@ int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ro
   p.tokens = tokens;
   p.n = n;
   p.k = k;
-  p.nch = chunks_of(M, V, esize);
+  p.nch = int(chunks_of(V, esize));
+  p.chunks = M * p.nch;
+  p.limit_ns = wait_limit_ns();
   p.logprob = logprob;
   p.entropy = entropy;
   p.lse = lse;
@@ -533,16 +662,17 @@ int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ro
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.nch), unsigned(M));
-  cfg.blockDim = dim3(kThreads);
+  const int64_t room = int64_t(device_sm_count()) * kCtas;
+  cfg.gridDim = dim3(unsigned(p.chunks < room ? p.chunks : room));
+  cfg.dynamicSmemBytes = sizeof(Smem);
+  cfg.blockDim = dim3(kThreads + 32);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = overlap_enabled() ? 1 : 0;
-  const int pieces = pieces_of(M, V, esize);
   const bool vec = aligned(logits, 16) && (row_stride * esize) % 16 == 0;
-  return cuda_status(dtype == W12_F32    ? launch<kF32>(cfg, p, pieces, vec)
-                     : dtype == W12_BF16 ? launch<kBf16>(cfg, p, pieces, vec)
-                                         : launch<kF16>(cfg, p, pieces, vec));
+  return cuda_status(dtype == W12_F32    ? launch<kF32>(cfg, p, vec)
+                     : dtype == W12_BF16 ? launch<kBf16>(cfg, p, vec)
+                                         : launch<kF16>(cfg, p, vec));
 }
 
 }  // extern "C"
