@@ -44,6 +44,14 @@ __host__ __device__ constexpr int word_off(int d, int r, int w) {
 __device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
+// (a & mask) | bits in one instruction (left to itself the compiler takes two, with
+// an immediate each).
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(mask), "r"(bits));
+  return r;
+}
+
 // Two fp32 values -> one word of bf16 (round to nearest even): lo in bits 0..15.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
@@ -54,8 +62,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // Dim pair (2j, 2j + 1) of a code word as two fp32 values z + s (q - 8). The
 // nibble becomes the mantissa of 2^23 + q, from which 2^23 + 8 leaves q - 8.
 __device__ __forceinline__ float2 value_pair(uint32_t w, int j, float s, float z) {
-  const float a = __uint_as_float(((w >> (4 * j)) & 15u) | 0x4B000000u) - 8388616.f;
-  const float b = __uint_as_float(((w >> (4 * j + 16)) & 15u) | 0x4B000000u) - 8388616.f;
+  const float a = __uint_as_float(and_or(w >> (4 * j), 15u, 0x4B000000u)) - 8388616.f;
+  const float b = __uint_as_float(and_or(w >> (4 * j + 16), 15u, 0x4B000000u)) - 8388616.f;
   return make_float2(fmaf(s, a, z), fmaf(s, b, z));
 }
 

@@ -62,7 +62,7 @@ __device__ __forceinline__ float ex2(float x) {
 template <int kJ>
 __device__ __forceinline__ uint32_t unit_pair(uint32_t w) {
   const uint32_t x = kJ == 0 ? w << 3 : w >> (4 * kJ - 3);
-  return (x & 0x00780078u) | 0x3F803F80u;
+  return and_or(x, 0x00780078u, 0x3F803F80u);
 }
 
 template <int kD, int kNT>

@@ -94,10 +94,10 @@ __device__ __forceinline__ uint4 restore_word(uint32_t w, uint32_t s2, uint32_t 
   constexpr uint32_t k1024 = 0x64006400u, kM1032 = 0xE408E408u, kSixteenth = 0x2C002C00u, kM72 = 0xD480D480u;
   const uint32_t v = w >> 8;
   uint4 o;
-  o.x = hfma2(hadd2((w & 0x000F000Fu) | k1024, kM1032), s2, z2);
-  o.y = hfma2(hfma2((w & 0x00F000F0u) | k1024, kSixteenth, kM72), s2, z2);
-  o.z = hfma2(hadd2((v & 0x000F000Fu) | k1024, kM1032), s2, z2);
-  o.w = hfma2(hfma2((v & 0x00F000F0u) | k1024, kSixteenth, kM72), s2, z2);
+  o.x = hfma2(hadd2(and_or(w, 0x000F000Fu, k1024), kM1032), s2, z2);
+  o.y = hfma2(hfma2(and_or(w, 0x00F000F0u, k1024), kSixteenth, kM72), s2, z2);
+  o.z = hfma2(hadd2(and_or(v, 0x000F000Fu, k1024), kM1032), s2, z2);
+  o.w = hfma2(hfma2(and_or(v, 0x00F000F0u, k1024), kSixteenth, kM72), s2, z2);
   return o;
 }
 
