@@ -264,9 +264,12 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
           *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(kc + 8 * (kD / 2) + t * 8);
         }
         const uint32_t kpa = par[0], kpb = par[8], vpa = par[P], vpb = par[P + 8];
-        float x[kNT][4];
+        float x[kNT][4], x2[kNT][4];
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+        for (int nt = 0; nt < kNT; ++nt) {
+          x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+          x2[nt][0] = x2[nt][1] = x2[nt][2] = x2[nt][3] = 0.f;
+        }
 #pragma unroll
         for (int i = 0; i < kKW; ++i) {
           const uint32_t a0 = unit_pair<0>(ka[i]), a1 = unit_pair<1>(ka[i]), a2 = unit_pair<2>(ka[i]), a3 = unit_pair<3>(ka[i]);
@@ -274,9 +277,13 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt) {
             mma16816(x[nt], a0, b0, a1, b1, q[nt][4 * i], q[nt][4 * i + 1]);
-            mma16816(x[nt], a2, b2, a3, b3, q[nt][4 * i + 2], q[nt][4 * i + 3]);
+            mma16816(x2[nt], a2, b2, a3, b3, q[nt][4 * i + 2], q[nt][4 * i + 3]);
           }
         }
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[nt][i] += x2[nt][i];
         const float ksa = p.c * bf16_lo(kpa), ksb = p.c * bf16_lo(kpb);
         const float kza = fmaf(-24.f, ksa, p.c * bf16_hi(kpa)), kzb = fmaf(-24.f, ksb, p.c * bf16_hi(kpb));
         const bool edge = key0 + 16 > s.prefix;

@@ -88,7 +88,7 @@ struct RunSmem {
 // thread i sums entries [i C, (i + 1) C); the thread whose entries hold the
 // run's first unit walks to it.
 template <int kN>
-__device__ __forceinline__ Run plan_run(const Params& p, RunSmem& sm) {
+__device__ __forceinline__ const Run& plan_run(const Params& p, RunSmem& sm) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.B * p.ntile, C = (E + kN - 1) / kN;
   const int e0 = min(E, tid * C), e1 = min(E, e0 + C);
@@ -149,6 +149,7 @@ struct Walk {
   int64_t pos, base;  // next unit; first unit of `entry`
   int entry;
 
+  Walk() = default;
   __device__ __forceinline__ explicit Walk(const Run& r) : pos(r.begin), base(r.entry_base), entry(r.entry) {}
 
   __device__ __forceinline__ bool next(const Params& p, const Run& r, Seg& s) {

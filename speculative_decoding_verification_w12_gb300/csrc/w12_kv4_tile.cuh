@@ -71,7 +71,8 @@ struct TileCfg {
   static constexpr uint32_t kExpOff = kQxOff + 2 * 128 * 4;
   static constexpr uint32_t kBarOff = kExpOff + 16 * 16;
   static constexpr uint32_t kRunOff = kBarOff + 320;
-  static constexpr uint32_t kSmem = kRunOff + 512 + 1024;           // 1024: alignment slack
+  static constexpr uint32_t kSegOff = kRunOff + 512;
+  static constexpr uint32_t kSmem = kSegOff + 256 + 1024;           // 1024: alignment slack
   // TMEM columns: S of even and odd blocks, O of the two key halves.
   static constexpr uint32_t kS0 = 0, kS1 = 128, kOA = 256, kOB = 256 + kD, kCols = 512;
 };
@@ -175,6 +176,14 @@ __device__ __forceinline__ float exp_pack_f16(const uint32_t (&v)[32], float c, 
   return s.x + s.y;
 }
 
+// What the softmax warps keep of their place in the run.
+struct SoftmaxSeg {
+  Walk walk;
+  Seg seg;
+  bool more;
+};
+static_assert(sizeof(SoftmaxSeg) <= 256, "shared memory carve-up");
+
 template <int kD>
 __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel(const __grid_constant__ Params p) {
   using C = TileCfg<kD>;
@@ -223,7 +232,8 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     fence_barrier_init();
   }
   grid_dep_wait();
-  const Run run = plan_run<C::kThreads>(p, rs);  // its barriers publish the mbarriers too
+  plan_run<C::kThreads>(p, rs);  // its barriers publish the mbarriers too
+  const Run& run = rs.run;       // read where it is used: registers are short
   zero_idle_rows<kD, C::kThreads>(p);
   if (run.begin >= run.end) return;
   if (warp == 1) {
@@ -249,10 +259,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     return false;
   };
 
-  Walk walk(run);
-  Seg s;
   if (warp == 0) {
     // ------------------------------------------------------------- copies
+    Walk walk(run);
+    Seg s;
     const int per = kKeys >> p.p_shift;
     const uint32_t bytes = uint32_t(p.block);
     const uint64_t page_stride = uint64_t(p.Hkv) * uint64_t(p.block);
@@ -305,6 +315,8 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     constexpr uint32_t idesc_s = idesc_f16(128, 128);
     constexpr uint32_t idesc_o = idesc_f16(128, kD) | (1u << 16);  // B (V) MN-major
     auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+    Walk walk(run);
+    Seg s;
     int base = 0, si = 0;
     bool ok = true;
     while (ok && walk.next(p, run, s)) {
@@ -380,12 +392,15 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     uint64_t* emptyb = is_k ? k_empty : v_empty;
     uint8_t* tiles = smem + (is_k ? C::kKOff : C::kVOff);
     const RowPlace<kD> place(i);
-    int gj = 0;
+    Walk walk(run);
+    Seg s;
+    int rst = 0, gj = 0;
+    uint32_t rph = 0u;
     bool ok = true;
     while (ok && walk.next(p, run, s)) {
       for (int j = s.j0; j < s.j1; ++j, ++gj) {
-        const int rst = gj % C::kRawStages, st = gj % C::kStages;
-        if (!__all_sync(0xFFFFFFFFu, wait(&raw_full[rst], uint32_t(gj / C::kRawStages) & 1u))) {
+        const int st = gj & 1;
+        if (!__all_sync(0xFFFFFFFFu, wait(&raw_full[rst], rph))) {
           ok = false;
           break;
         }
@@ -400,6 +415,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         const bool past = j * kKeys + i >= s.keys;
         const bool odd = not_finite(vp);
         const int e = __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(mine));
+        const int f = is_k ? __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(vp)) : 0;
         const float down = pow2(-e);
         uint32_t s2 = 0u, z2 = 0u;
         if (!past && (is_k || !odd)) {
@@ -407,15 +423,12 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           z2 = pack_f16x2(bf16_hi(mine) * down, bf16_hi(mine) * down);
           if (is_k && odd) z2 = 0x7E007E00u;
         }
-        if (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&emptyb[st], uint32_t(gj / C::kStages - 1) & 1u))) {
+        if (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&emptyb[st], uint32_t((gj >> 1) - 1) & 1u))) {
           ok = false;
           break;
         }
-        if (is_k) {
-          // The K warps publish both exponents: the softmax then waits for K alone.
-          const int f = __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(vp));
-          if (lane == 0) exps[(gj & 3) * 4 + (i >> 5)] = make_float4(p.c * pow2(e), float(f), pow2(-f), 0.f);
-        }
+        // The K warps publish both exponents: the softmax then waits for K alone.
+        if (is_k && lane == 0) exps[(gj & 3) * 4 + (i >> 5)] = make_float4(p.c * pow2(e), float(f), pow2(-f), 0.f);
         uint8_t* tile = tiles + st * C::kTile;
 #pragma unroll
         for (int k = 0; k < kD / 32; ++k) {
@@ -431,6 +444,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           mbar_arrive(&fullb[st]);
           mbar_arrive(&raw_empty[rst]);
         }
+        if (++rst == C::kRawStages) {
+          rst = 0;
+          rph ^= 1u;
+        }
       }
     }
   } else if (warp >= 4) {
@@ -442,8 +459,15 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     const uint32_t o_own = tmem + lane_off + (h ? C::kOB : C::kOA);
     float2* xch = reinterpret_cast<float2*>(smem + C::kXchOff);
     int base = 0, si = 0;
-    bool more = walk.next(p, run, s);
-    while (more) {
+    // The segment and the walk are kept in shared memory: registers are short.
+    SoftmaxSeg& sh = *reinterpret_cast<SoftmaxSeg*>(smem + C::kSegOff);
+    const Seg& s = sh.seg;
+    if (tid == 128) sh.walk = Walk(run);
+    for (;;) {
+      named_bar_sync(1, 256);
+      if (tid == 128) sh.more = sh.walk.next(p, run, sh.seg);
+      named_bar_sync(1, 256);
+      if (!sh.more) break;
       const int R = s.n * p.G;
       const int rr = s.tile * 128 + r;
       const bool valid = rr < R;
@@ -498,10 +522,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       mbar_arrive(q_ready);
       float M = -INFINITY, l = 0.f;
       bool ok = true;
-      const int n = s.j1 - s.j0;
+      const int n = s.j1 - s.j0, key0 = s.j0 * kKeys + 64 * h;
       for (int i = 0; i < n; ++i) {
         const int gi = base + i;
-        const int kb = (s.j0 + i) * kKeys + 64 * h;
+        const int kb = key0 + i * kKeys;
         if (!__all_sync(0xFFFFFFFFu, wait(&s_full[gi & 1], uint32_t(gi >> 1) & 1u))) {
           ok = false;
           break;
@@ -518,7 +542,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
             if (look) {
               // The maximum moves to this block's where that is larger; O and the sum follow.
               float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
               for (int ch = 0; ch < 2; ++ch) {
                 uint32_t v[32];
                 tmem_ld32(sc + uint32_t(ch * 32), v);
@@ -659,7 +683,6 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       }
       base += n;
       ++si;
-      more = walk.next(p, run, s);
     }
   }
 
