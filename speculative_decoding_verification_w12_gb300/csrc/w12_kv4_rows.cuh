@@ -11,13 +11,13 @@
 // 8-wide side:
 //   S^T[16 keys, rows]  = K Q^T:  A = K codes, B = Q
 //   O^T[16 dims, rows] += V^T P^T: A = V codes, B = P
-// Codes are never scaled: a code q becomes the bf16 number u = 1 + q/16 (its
-// bits placed in the mantissa, exact), so with z + s (q - 8) = 16 s u + (z - 24 s)
-//   score = 16 c s (q.u) + c (z - 24 s) sum(q),     c = scale log2(e)
-//   o     = 16 sum p~ u - 24 sum p~ + sum p z,      p~ = bf16(p s)
-// with both products exact up to fp32 accumulation: the one rounding is P to
-// bf16, the same rounded p~ stands in both of its sums. sum p~ comes from one
-// more product with a matrix of ones.
+// Codes are never scaled: a code becomes the fp16 number q - 8 (exact), so with
+// z + s (q - 8)
+//   score = c 2^a (s (q^.(q - 8)) + z sum(q^)),     c = scale log2(e)
+//   o     = sum p~ (q - 8) + sum p z,               p~ = fp16(p s)
+// with both products exact up to fp32 accumulation: the one rounding is p~ (2^-11
+// relative). A row of Q is held as q^ = q / 2^a, a power of two that keeps it in
+// the fp16 range.
 //
 // Layout of the 16-key group: lane (g, t) = (lane / 4, lane % 4). K: key phi(g)
 // (and 8 + phi(g)), dims (d/4) t ..: one 16-byte load per key gives all its A
@@ -26,19 +26,25 @@
 // 0 5 2 7 1 4 3 6, chosen with the layout's swapped halves so that both kinds of
 // loads are free of bank conflicts.
 //
-// A warp's running maximum moves only when a score exceeds it by more than 8
-// (log2 units; one vote per group), so rescaling is rare and p <= 256.
+// Weights are p = 2^(score - M). M follows the maximum of score + f, 2^f a power of
+// two that bounds the key's V row, so that p~ stays inside fp16 and what it rounds
+// to zero is below 2^-24 of what counts in o. It moves only when a p~ passes 2^10
+// (or p itself 2^100, which V rows of zeros allow): one vote a group, rescaling
+// is rare.
 #pragma once
 
+#include "w12_attn_dev.cuh"
 #include "w12_kv4_sched.cuh"
 
 namespace w12 {
 namespace kv4_attn {
 
+using attn_impl::pack_f16x2;
+
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -58,11 +64,25 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Nibble j of both 16-bit halves of w as bf16 numbers 1 + q/16.
-template <int kJ>
-__device__ __forceinline__ uint32_t unit_pair(uint32_t w) {
-  const uint32_t x = kJ == 0 ? w << 3 : w >> (4 * kJ - 3);
-  return and_or(x, 0x00780078u, 0x3F803F80u);
+// The four nibbles of both 16-bit halves of w as fp16 pairs q - 8. Masked into
+// place, a nibble is 1024 + q or 1024 + 16 q: one shift a word on the logic pipe,
+// the rest on the multiply pipe (a shift for every nibble keeps the logic pipe, at
+// half the rate, the busier one).
+__device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&o)[4]) {
+  constexpr uint32_t k1024 = 0x64006400u, kM1032 = 0xE408E408u, kSixteenth = 0x2C002C00u, kM72 = 0xD480D480u;
+  const uint32_t v = w >> 8;
+  o[0] = hadd2(and_or(w, 0x000F000Fu, k1024), kM1032);
+  o[1] = hfma2(and_or(w, 0x00F000F0u, k1024), kSixteenth, kM72);
+  o[2] = hadd2(and_or(v, 0x000F000Fu, k1024), kM1032);
+  o[3] = hfma2(and_or(v, 0x00F000F0u, k1024), kSixteenth, kM72);
+}
+
+// f of a row of V with the given parameters: |z| + 8 s < 2^f, at least -100 (rows
+// of zeros; values that are not finite, whose weights are NaN all the same).
+__device__ __forceinline__ float row_bound(uint32_t par) {
+  const float b = fmaf(8.f, bf16_lo(par), fabsf(bf16_hi(par)));
+  const int e = int((__float_as_uint(b) >> 23) & 255u) - 126;
+  return float(e > 128 ? -100 : max(e, -100));
 }
 
 template <int kD, int kNT>
@@ -186,9 +206,10 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
   bool ok = true;
   while (walk.next(p, run, s)) {
     const int R = s.n * p.G;  // rows of the item
-    // Q fragments: row 8 nt + g, dims (d/4) t .. + d/4 - 1.
+    // Q fragments: row 8 nt + g, dims (d/4) t .. + d/4 - 1, over 2^a.
     uint32_t q[kNT][kD / 8];
     float sq[kNT][2];           // sums of the rows 8 nt + 2t, + 1
+    float cr[kNT][2];           // c 2^a of those rows
     uint32_t see[kNT][2];       // draft tokens those rows see (bit i: token i)
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
@@ -202,13 +223,27 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
 #pragma unroll
         for (int i = 0; i < kD / 32; ++i) *reinterpret_cast<uint4*>(&q[nt][4 * i]) = __ldg(src + i);
       }
+      uint32_t big = 0u;
+#pragma unroll
+      for (int i = 0; i < kD / 8; ++i) big = max(big, max((q[nt][i] << 16) & 0x7FFFFFFFu, q[nt][i] & 0x7FFF0000u));
+      big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+      big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+      const int a = min(max(int(big >> 23) - 126, -100), 120);  // a row with NaN or infinities stays one
+      const float down = __uint_as_float(uint32_t(127 - a) << 23);
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kD / 8; ++i) sum += bf16_lo(q[nt][i]) + bf16_hi(q[nt][i]);
+      for (int i = 0; i < kD / 8; ++i) {
+        const float lo = bf16_lo(q[nt][i]) * down, hi = bf16_hi(q[nt][i]) * down;
+        sum += lo + hi;
+        q[nt][i] = pack_f16x2(lo, hi);
+      }
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
       sq[nt][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t);
       sq[nt][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4);
+      const float cs = fmaxf(p.c * __uint_as_float(uint32_t(127 + a) << 23), 1.2e-38f);
+      cr[nt][0] = __shfl_sync(0xFFFFFFFFu, cs, 8 * t);
+      cr[nt][1] = __shfl_sync(0xFFFFFFFFu, cs, 8 * t + 4);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rr = 8 * nt + 2 * t + e;
@@ -228,14 +263,15 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
         see[nt][e] = m;
       }
     }
-    float o[kNT][kMT][4], m[kNT][2], l[kNT][2], zs[kNT][2], sp[kNT][4];
+    float o[kNT][kMT][4], m[kNT][2], l[kNT][2], zs[kNT][2];
+    float neg[kNT][2];  // -M, 0 while there is none
+    bool fresh = true;  // some row has no M yet (the same in the whole warp)
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
       for (int i = 0; i < kMT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = zs[nt][e] = 0.f;
-      sp[nt][0] = sp[nt][1] = sp[nt][2] = sp[nt][3] = 0.f;
+      for (int e = 0; e < 2; ++e) m[nt][e] = -INFINITY, l[nt][e] = zs[nt][e] = neg[nt][e] = 0.f;
     }
     const int group_end = group + (s.j1 - s.j0) * 8;
     // This warp's groups: those whose number is its own modulo kWarps.
@@ -264,7 +300,7 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
           *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(kc + 8 * (kD / 2) + t * 8);
         }
         const uint32_t kpa = par[0], kpb = par[8], vpa = par[P], vpb = par[P + 8];
-        float x[kNT][4], x2[kNT][4];
+        float x[kNT][4], x2[kNT][4];  // two accumulators: half the chain of dependent products
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
           x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
@@ -272,29 +308,26 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
         }
 #pragma unroll
         for (int i = 0; i < kKW; ++i) {
-          const uint32_t a0 = unit_pair<0>(ka[i]), a1 = unit_pair<1>(ka[i]), a2 = unit_pair<2>(ka[i]), a3 = unit_pair<3>(ka[i]);
-          const uint32_t b0 = unit_pair<0>(kb[i]), b1 = unit_pair<1>(kb[i]), b2 = unit_pair<2>(kb[i]), b3 = unit_pair<3>(kb[i]);
+          uint32_t a[4], b[4];
+          codes_of(ka[i], a);
+          codes_of(kb[i], b);
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt) {
-            mma16816(x[nt], a0, b0, a1, b1, q[nt][4 * i], q[nt][4 * i + 1]);
-            mma16816(x2[nt], a2, b2, a3, b3, q[nt][4 * i + 2], q[nt][4 * i + 3]);
+            mma16816(x[nt], a[0], b[0], a[1], b[1], q[nt][4 * i], q[nt][4 * i + 1]);
+            mma16816(x2[nt], a[2], b[2], a[3], b[3], q[nt][4 * i + 2], q[nt][4 * i + 3]);
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[nt][i] += x2[nt][i];
-        const float ksa = p.c * bf16_lo(kpa), ksb = p.c * bf16_lo(kpb);
-        const float kza = fmaf(-24.f, ksa, p.c * bf16_hi(kpa)), kzb = fmaf(-24.f, ksb, p.c * bf16_hi(kpb));
+        // x: scores without c 2^a, -inf where masked.
+        const float ksa = bf16_lo(kpa), ksb = bf16_lo(kpb), kza = bf16_hi(kpa), kzb = bf16_hi(kpb);
+        const float vsa = bf16_lo(vpa), vsb = bf16_lo(vpb), vza = bf16_hi(vpa), vzb = bf16_hi(vpb);
         const bool edge = key0 + 16 > s.prefix;
         uint32_t hidden = 0;  // bit 4 nt + i: element i is masked
-        bool over = false;
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          x[nt][0] = fmaf(x[nt][0], 16.f * ksa, sq[nt][0] * kza);
-          x[nt][1] = fmaf(x[nt][1], 16.f * ksa, sq[nt][1] * kza);
-          x[nt][2] = fmaf(x[nt][2], 16.f * ksb, sq[nt][0] * kzb);
-          x[nt][3] = fmaf(x[nt][3], 16.f * ksb, sq[nt][1] * kzb);
+          x[nt][0] = fmaf(x[nt][0] + x2[nt][0], ksa, sq[nt][0] * kza);
+          x[nt][1] = fmaf(x[nt][1] + x2[nt][1], ksa, sq[nt][1] * kza);
+          x[nt][2] = fmaf(x[nt][2] + x2[nt][2], ksb, sq[nt][0] * kzb);
+          x[nt][3] = fmaf(x[nt][3] + x2[nt][3], ksb, sq[nt][1] * kzb);
           if (edge) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -306,53 +339,74 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
               }
             }
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) over |= x[nt][i] > m[nt][i & 1] + 8.f;
         }
-        if (__any_sync(0xFFFFFFFFu, over)) {
+        float e[kNT][4], w[kNT][4], l2[kNT][2];
+        bool move = fresh;
+#pragma unroll 1
+        for (;;) {
+          if (move) {
+            const float fa = row_bound(vpa), fb = row_bound(vpb);
 #pragma unroll
-          for (int nt = 0; nt < kNT; ++nt)
+            for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = fmaxf(x[nt][e], x[nt][2 + e]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-              mx = fmaxf(mx, m[nt][e]);
-              const float f = m[nt][e] == mx ? 1.f : ex2(m[nt][e] - mx);  // 0 while m = -inf
-              m[nt][e] = mx;
-              l[nt][e] *= f;
-              zs[nt][e] *= f;
-              sp[nt][e] *= f;
+              for (int r = 0; r < 2; ++r) {
+                float mx = fmaxf(fmaf(x[nt][r], cr[nt][r], fa), fmaf(x[nt][2 + r], cr[nt][r], fb));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+                mx = fmaxf(mx, m[nt][r]);
+                const float f = m[nt][r] == mx ? 1.f : ex2(m[nt][r] - mx);  // 0 while m = -inf
+                m[nt][r] = mx;
+                l[nt][r] *= f;
+                zs[nt][r] *= f;
 #pragma unroll
-              for (int i = 0; i < kMT; ++i) {
-                o[nt][i][e] *= f;
-                o[nt][i][2 + e] *= f;
+                for (int i = 0; i < kMT; ++i) {
+                  o[nt][i][r] *= f;
+                  o[nt][i][2 + r] *= f;
+                }
+                neg[nt][r] = mx == -INFINITY ? 0.f : -mx;
               }
-            }
+            bool none = false;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) none |= m[nt][0] == -INFINITY || m[nt][1] == -INFINITY;
+            fresh = __any_sync(0xFFFFFFFFu, none);
+          }
+          float most = 0.f, sum = 0.f;
+#pragma unroll
+          for (int nt = 0; nt < kNT; ++nt) {
+            e[nt][0] = ex2(fmaf(x[nt][0], cr[nt][0], neg[nt][0]));
+            e[nt][1] = ex2(fmaf(x[nt][1], cr[nt][1], neg[nt][1]));
+            e[nt][2] = ex2(fmaf(x[nt][2], cr[nt][0], neg[nt][0]));
+            e[nt][3] = ex2(fmaf(x[nt][3], cr[nt][1], neg[nt][1]));
+            w[nt][0] = e[nt][0] * vsa;
+            w[nt][1] = e[nt][1] * vsa;
+            w[nt][2] = e[nt][2] * vsb;
+            w[nt][3] = e[nt][3] * vsb;
+            most = fmaxf(most, fmaxf(fmaxf(w[nt][0], w[nt][1]), fmaxf(w[nt][2], w[nt][3])));
+            l2[nt][0] = e[nt][0] + e[nt][2];
+            l2[nt][1] = e[nt][1] + e[nt][3];
+            sum += l2[nt][0] + l2[nt][1];
+          }
+          if (move || !__any_sync(0xFFFFFFFFu, most > 1024.f || sum > 1.2676506e30f)) break;
+          move = true;
         }
-        const float vsa = bf16_lo(vpa), vsb = bf16_lo(vpb), vza = bf16_hi(vpa), vzb = bf16_hi(vpb);
         uint32_t pb[kNT][2];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-          const float e0 = ex2(x[nt][0] - m0), e1 = ex2(x[nt][1] - m1), e2 = ex2(x[nt][2] - m0), e3 = ex2(x[nt][3] - m1);
-          l[nt][0] += e0 + e2;
-          l[nt][1] += e1 + e3;
-          float w0 = e0 * vsa, w1 = e1 * vsa, w2 = e2 * vsb, w3 = e3 * vsb;
-          float z0 = e0 * vza, z1 = e1 * vza, z2 = e2 * vzb, z3 = e3 * vzb;
+          float z0 = e[nt][0] * vza, z1 = e[nt][1] * vza, z2 = e[nt][2] * vzb, z3 = e[nt][3] * vzb;
           if (edge) {  // parameters in masked places may be anything
             const uint32_t hd = hidden >> (4 * nt);
-            if (hd & 1u) w0 = z0 = 0.f;
-            if (hd & 2u) w1 = z1 = 0.f;
-            if (hd & 4u) w2 = z2 = 0.f;
-            if (hd & 8u) w3 = z3 = 0.f;
+            if (hd & 1u) w[nt][0] = z0 = 0.f;
+            if (hd & 2u) w[nt][1] = z1 = 0.f;
+            if (hd & 4u) w[nt][2] = z2 = 0.f;
+            if (hd & 8u) w[nt][3] = z3 = 0.f;
           }
+          l[nt][0] += l2[nt][0];
+          l[nt][1] += l2[nt][1];
           zs[nt][0] += z0 + z2;
           zs[nt][1] += z1 + z3;
-          pb[nt][0] = transpose8x8(pack_bf16x2(w0, w1));
-          pb[nt][1] = transpose8x8(pack_bf16x2(w2, w3));
-          mma16816(sp[nt], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, pb[nt][0], pb[nt][1]);
+          pb[nt][0] = transpose8x8(pack_f16x2(w[nt][0], w[nt][1]));
+          pb[nt][1] = transpose8x8(pack_f16x2(w[nt][2], w[nt][3]));
         }
         // V: keys phi(2t), phi(2t + 1) and 8 further, dims (d/8) g ..
         const uint8_t* vc = pg + P * (kD / 2) + r0 * (kD / 2);
@@ -370,10 +424,11 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
         for (int e = 0; e < kVW; ++e) {
           const uint32_t lo0 = __byte_perm(v[0][e], v[1][e], 0x5410), hi0 = __byte_perm(v[0][e], v[1][e], 0x7632);
           const uint32_t lo1 = __byte_perm(v[2][e], v[3][e], 0x5410), hi1 = __byte_perm(v[2][e], v[3][e], 0x7632);
-          const uint32_t a0[4] = {unit_pair<0>(lo0), unit_pair<1>(lo0), unit_pair<2>(lo0), unit_pair<3>(lo0)};
-          const uint32_t a1[4] = {unit_pair<0>(hi0), unit_pair<1>(hi0), unit_pair<2>(hi0), unit_pair<3>(hi0)};
-          const uint32_t a2[4] = {unit_pair<0>(lo1), unit_pair<1>(lo1), unit_pair<2>(lo1), unit_pair<3>(lo1)};
-          const uint32_t a3[4] = {unit_pair<0>(hi1), unit_pair<1>(hi1), unit_pair<2>(hi1), unit_pair<3>(hi1)};
+          uint32_t a0[4], a1[4], a2[4], a3[4];
+          codes_of(lo0, a0);
+          codes_of(hi0, a1);
+          codes_of(lo1, a2);
+          codes_of(hi1, a3);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -401,13 +456,12 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
           z += __shfl_xor_sync(0xFFFFFFFFu, z, x);
         }
         const int r = 8 * nt + 2 * t + e;
-        const float shift = fmaf(-24.f, sp[nt][e], z);
         if (g == 0) mlsm[warp * C::kRows + r] = make_float2(m[nt][e], ls);
         float* dst = osm + (warp * C::kRows + r) * C::kPitch + g * 2;
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
           *reinterpret_cast<float2*>(dst + i * 16) =
-              make_float2(fmaf(16.f, o[nt][i][e], shift), fmaf(16.f, o[nt][i][2 + e], shift));
+              make_float2(o[nt][i][e] + z, o[nt][i][2 + e] + z);
       }
     named_bar_sync(1, kComp);
     const bool whole = s.whole();

@@ -77,17 +77,6 @@ struct TileCfg {
   static constexpr uint32_t kS0 = 0, kS1 = 128, kOA = 256, kOB = 256 + kD, kCols = 512;
 };
 
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t r;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-  return r;
-}
-
 // Eight dims of a code word as fp16 values z + s (q - 8), s2 and z2 holding s and
 // z in both halves. A nibble in the lowest bits of fp16 1024 is 1024 + q, in the
 // next four 1024 + 16 q; both become q - 8 exactly, then one rounding.
