@@ -17,6 +17,10 @@ kernel, not a copy-engine transfer, so that the step's first GEMM starts
 requesting its weights while the inputs arrive) and the step, whose accept
 kernel writes the results straight into the pinned host buffer (the device
 addresses page-locked memory in place).
+
+PagedVerifyStep is one layer's step over a paged 4-bit key/value cache: pages for
+the draft tree, the layer's products and attention, acceptance, log probabilities
+of what is answered, commit of the accepted path and the pages given back.
 """
 from __future__ import annotations
 
@@ -151,3 +155,81 @@ class VerifyStep:
 
     def d2h_bytes(self) -> int:
         return self._out_host.numel() * 4
+
+
+class PagedVerifyStep:
+    """A tree-verify step of one target layer over a paged 4-bit cache.
+
+    B requests of T draft nodes (B * T <= 256 rows). qkv, out and head are packed
+    weights: hidden -> (Hq + 2 Hkv) * head_dim, Hq * head_dim -> hidden, hidden ->
+    vocabulary. Position encodings, norms and the MLP are the caller's: the step
+    takes the rows that enter the layer. length int32 [B] holds each request's
+    committed tokens and is advanced by every step.
+    """
+
+    def __init__(self, qkv: w12.W12Weights, out: w12.W12Weights, head: w12.W12Weights, B: int, T: int, Hq: int,
+                 Hkv: int, head_dim: int, n_pages: int, page_size: int = 64, max_len: int = 8192, top_k: int = 8,
+                 device=None):
+        dev = torch.device(device or "cuda")
+        if qkv.N != (Hq + 2 * Hkv) * head_dim or out.K != Hq * head_dim or head.K != out.N:
+            raise ValueError("qkv, out and head do not fit the heads")
+        self.B, self.T, self.M, self.Hq, self.Hkv, self.head_dim = B, T, B * T, Hq, Hkv, head_dim
+        self.qkv, self.out, self.head, self.top_k = qkv, out, head, top_k
+        self.cache = w12.KV4Cache.create(n_pages, Hkv, head_dim, page_size, dev)
+        self.pages = w12.PageTable.create(B, -(-max_len // page_size), n_pages, page_size, dev)
+        self.length = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.nodes = torch.full((B,), T, dtype=torch.int32, device=dev)
+        self.attention = w12.KV4Attention(B, T, Hq, Hkv, head_dim, page_size, max_len, dev)
+        self.logprobs = w12.TokenLogprobs(self.M, head.N, top_k, dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._ws = [w12.workspace(w12.gemm_ws_bytes(self.M, w.N, w.K), dev) for w in (qkv, out, head)]
+        self._vws = w12.workspace(w12.verify_ws_bytes(self.M, head.N), dev)
+
+    def prefill(self, K: torch.Tensor, V: torch.Tensor, length: torch.Tensor):
+        """Cache the first length[b] rows of K, V [B, n, Hkv, head_dim] (one prompt a request)."""
+        n = K.shape[1]
+        slots = self.pages.reserve(torch.zeros_like(length), length, n, status=self.status)
+        self.cache.append(K.flatten(0, 1), V.flatten(0, 1), slots, status=self.status)
+        self.length.copy_(length)
+
+    def run(self, X: torch.Tensor, parents: torch.Tensor, draft: torch.Tensor) -> dict:
+        """One step on X bf16 [B * T, hidden], the draft trees parents, draft int32 [B, T].
+
+        Returns path [B, T], path_len, accept_len, bonus (as verify_tree); tokens
+        [B, T], the answered tokens in order (the accepted drafts, then the bonus
+        token, -1 after it), and at the same places logprob, entropy, top_logprob
+        and top_id of the rows that predicted them.
+        """
+        B, T, M, d = self.B, self.T, self.M, self.head_dim
+        st = self.status
+        slots = self.pages.reserve(self.length, self.nodes, T, status=st)
+        Y = w12.gemm(X, self.qkv, ws=self._ws[0], status=st)
+        q, k, v = Y.split([self.Hq * d, self.Hkv * d, self.Hkv * d], 1)
+        # Keys and values are quantised straight from the fp32 product (views of it).
+        self.cache.append(k.unflatten(1, (self.Hkv, d)), v.unflatten(1, (self.Hkv, d)), slots, status=st)
+        O = self.attention.run(q.to(torch.bfloat16).view(B, T, self.Hq, d), self.cache, self.pages.table, self.length,
+                               parents=parents, q_len=self.nodes, status=st)
+        H = w12.gemm(O.view(M, self.Hq * d), self.out, ws=self._ws[1], status=st).to(torch.bfloat16)
+        logits = w12.gemm(H, self.head, ws=self._ws[2], status=st)
+        path, path_len, accept_len, bonus, _ = w12.verify_tree(logits, parents, draft, ws=self._vws, status=st)
+        # Row path[i] predicted the draft of path[i + 1], the last row of the path the bonus token.
+        step = torch.arange(T, device=X.device)[None]
+        nxt = torch.cat([path[:, 1:], path[:, :1]], 1).clamp(min=0).long()
+        tokens = torch.where(step < accept_len[:, None], draft.gather(1, nxt), bonus[:, None])
+        tokens = torch.where(step <= accept_len[:, None], tokens, -1).to(torch.int32)
+        # The token asked of each row: the answered one on the path, none (-1) elsewhere.
+        asked = torch.full((B, T + 1), -1, dtype=torch.int32, device=X.device)
+        asked.scatter_(1, torch.where(path >= 0, path, T).long(), tokens)
+        asked = asked[:, :T].contiguous()
+        rows = path.clamp(min=0).long()
+        lp, entropy, _, top_lp, top_id = self.logprobs.run(logits, asked.view(M, 1), status=st)
+        new_len = w12.kv4_commit([self.cache], self.pages.table, self.length, path, path_len, status=st)
+        self.pages.trim(new_len, status=st)
+        self.length.copy_(new_len)
+
+        def answered(t):  # rows of the path, in its order
+            t = t.view(B, T, -1)
+            return t.gather(1, rows[:, :, None].expand(B, T, t.shape[2]))
+        return dict(path=path, path_len=path_len, accept_len=accept_len, bonus=bonus, tokens=tokens,
+                    logprob=answered(lp)[..., 0], entropy=answered(entropy)[..., 0], top_logprob=answered(top_lp),
+                    top_id=answered(top_id))

@@ -304,3 +304,83 @@ def test_binding_refusals():
     assert e.value.code == 2
     with pytest.raises(w12.W12Error):
         w12.KV4Attention(1, 8, 4, 3, 64, 16, 48)
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_pages_past_4_gigabytes(T):
+    """Byte offsets of pages pass 32 bits."""
+    c = Case([300, 500], [T, T], T, 40, 8, 128, 128, seed=13, extra_pages=(9 << 29) // (8 * 128 * 136))
+    assert c.cache.pool.numel() > 1 << 32 and int(c.table.max()) * 8 * 128 * 136 > 1 << 32
+    c.check(c.run(), heads=(0, 7))
+
+
+@pytest.mark.parametrize("scale", [1e-20, 1e20])
+@pytest.mark.parametrize("T", [1, 16])
+def test_queries_far_from_one(T, scale):
+    """Queries of 1e20 with a small scale, and the reverse: rows keep powers of two of their own."""
+    c = Case([200], [T], T, 8, 2, 64, 32, seed=14)
+    c.Q = (c.Q.float() * scale).bfloat16()
+    c.check(c.run(scale=0.125 / scale), scale=float(np.float32(0.125 / scale)))
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_values_of_very_different_size(T):
+    """Keys whose value rows are 1e-12, 1 and 1e12 large, in runs and alternating."""
+    c = Case([400], [T], T, 8, 2, 128, 64, seed=15)
+    g = np.random.default_rng(16)
+    L = 400 + T
+    size = np.ones(L, dtype=np.float32)
+    size[:128], size[128:260], size[300:] = 1e-12, 1e12, 1e-12
+    size[301::2] = 1.0
+    kv = g.standard_normal((2, L, 2, 128)).astype(np.float32)
+    kv[1] *= size[:, None, None]
+    c.cache.append(torch.from_numpy(kv[0]).cuda(), torch.from_numpy(kv[1]).cuda(), to_dev_i32(c.slots[0]))
+    c.K, c.V = [O.values(*O.quantise(kv[0]))], [O.values(*O.quantise(kv[1]))]
+    c.check(c.run())
+    # Rows that see the tiny values alone keep them: a tree whose prefix is tiny throughout.
+    kv[1] = g.standard_normal(kv[1].shape).astype(np.float32) * np.float32(1e-12)
+    c.cache.append(torch.from_numpy(kv[0]).cuda(), torch.from_numpy(kv[1]).cuda(), to_dev_i32(c.slots[0]))
+    c.V = [O.values(*O.quantise(kv[1]))]
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_values_that_are_zero_or_constant(T):
+    """Rows with scale 0 (all of one value) and rows of zeros, and keys to match."""
+    c = Case([300], [T], T, 8, 2, 128, 64, seed=17)
+    g = np.random.default_rng(18)
+    L = 300 + T
+    kv = g.standard_normal((2, L, 2, 128)).astype(np.float32)
+    kv[1, :150] = 0.0
+    kv[1, 150:200] = 2.5
+    kv[0, 40:60] = 0.0
+    kv[0, 250:] = -1.5
+    c.cache.append(torch.from_numpy(kv[0]).cuda(), torch.from_numpy(kv[1]).cuda(), to_dev_i32(c.slots[0]))
+    c.K, c.V = [O.values(*O.quantise(kv[0]))], [O.values(*O.quantise(kv[1]))]
+    c.check(c.run())
+    kv[1] = 0.0
+    c.cache.append(torch.from_numpy(kv[0]).cuda(), torch.from_numpy(kv[1]).cuda(), to_dev_i32(c.slots[0]))
+    assert (c.run() == 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 16, 40])
+def test_an_expired_wait_is_reported_and_the_next_call_is_right(T):
+    """With a 1 us bound a wait may give up (W12_ERR_TIMEOUT); the call ends, and after
+    the bound and the workspace are set back the next one matches the oracle."""
+    c = Case([3000, 50], [T, T], T, 10, 2, 128, 64, seed=19)
+    att = w12.KV4Attention(2, T, 10, 2, 128, 64, 3000 + T)
+    torch.cuda.synchronize()
+    w12.set_wait_limit_us(1)
+    try:
+        st = new_status()
+        out = c.run(att=att, status=st)
+        code = status_value(st)
+    finally:
+        w12.set_wait_limit_us(2000000)
+    assert code in (0, 6)
+    if code == 0:
+        c.check(out)
+    att.reset()
+    st = new_status()
+    c.check(c.run(att=att, status=st))
+    assert status_value(st) == 0

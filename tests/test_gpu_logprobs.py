@@ -169,3 +169,36 @@ def test_binding_refusals():
     with pytest.raises(w12.W12Error) as e:
         w12.TokenLogprobs(4, 100, 33)
     assert e.value.code == 2
+
+
+def test_an_expired_wait_is_reported_and_the_next_call_is_right():
+    a = w12.TokenLogprobs(40, 60000, 5)
+    x = torch.randn((40, 60000), device="cuda")
+    tokens = np.arange(40)[:, None]
+    torch.cuda.synchronize()
+    w12.set_wait_limit_us(1)
+    try:
+        st = new_status()
+        out = a.run(x, to_dev_i32(tokens), status=st)
+        code = status_value(st)
+    finally:
+        w12.set_wait_limit_us(2000000)
+    assert code in (0, 6)
+    if code == 0:
+        _check(x, 1.0, tokens, 5, out)
+    a.ws.zero_()
+    st = new_status()
+    out = a.run(x, to_dev_i32(tokens), status=st)
+    assert status_value(st) == 0
+    _check(x, 1.0, tokens, 5, out)
+
+
+@pytest.mark.parametrize("kind", ["rising", "jump"])
+def test_values_that_climb_along_a_run(kind):
+    """A thread's reference moves, and the first chunk's bound is far below the rest."""
+    x = torch.randn((3, 120001), device="cuda")
+    i = torch.arange(120001, device="cuda")
+    x += (i / 200.0 if kind == "rising" else torch.where(i > 90000, 500.0, 0.0))
+    tokens = np.array([[0], [120000], [60000]])
+    _check(x, 1.0, tokens, 20, _run(x, tokens, 20))
+    _check(x.bfloat16(), 1.0, tokens, 20, _run(x.bfloat16(), tokens, 20))
