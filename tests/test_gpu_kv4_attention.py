@@ -30,13 +30,15 @@ U = 2.0 ** -8
 class Case:
     """A cache filled for requests of the given lengths, and the oracle's view of it."""
 
-    def __init__(self, prefix, new, T, Hq, Hkv, d, P, seed=0, std=1.0, grow=None, extra_pages=2):
+    def __init__(self, prefix, new, T, Hq, Hkv, d, P, seed=0, std=1.0, grow=None, extra_pages=2, high=False):
         g = np.random.default_rng(seed)
         self.prefix, self.new, self.T, self.Hq, self.Hkv, self.d, self.P = list(prefix), list(new), T, Hq, Hkv, d, P
         B = self.B = len(prefix)
         lens = [a + n for a, n in zip(prefix, new)]
         need = [-(-L // P) for L in lens]
         ids = g.permutation(sum(need) + extra_pages)
+        if high:                               # the requests hold the pool's last pages
+            ids = np.sort(ids)[::-1]
         width = max(max(need), 1) + 8
         self.table = np.full((B, width), -1)
         at = 0
@@ -309,8 +311,9 @@ def test_binding_refusals():
 @pytest.mark.parametrize("T", [1, 16])
 def test_pages_past_4_gigabytes(T):
     """Byte offsets of pages pass 32 bits."""
-    c = Case([300, 500], [T, T], T, 40, 8, 128, 128, seed=13, extra_pages=(9 << 29) // (8 * 128 * 136))
-    assert c.cache.pool.numel() > 1 << 32 and int(c.table.max()) * 8 * 128 * 136 > 1 << 32
+    c = Case([300, 500], [T, T], T, 40, 8, 128, 128, seed=13, extra_pages=(9 << 29) // (8 * 128 * 136),
+             high=True)
+    assert c.cache.pool.numel() > 1 << 32 and int(c.table[c.table >= 0].min()) * 8 * 128 * 136 > 1 << 32
     c.check(c.run(), heads=(0, 7))
 
 
