@@ -177,7 +177,8 @@ template <int kD>
 __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel(const __grid_constant__ Params p) {
   using C = TileCfg<kD>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (An offset, not a rounded pointer: the compiler then still knows that it is shared memory.)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // pages of a block landed
   uint64_t* raw_empty = raw_full + C::kRawStages;                       // and restored (one arrival a warp)
   uint64_t* k_full = raw_empty + C::kRawStages;                         // K tile restored
