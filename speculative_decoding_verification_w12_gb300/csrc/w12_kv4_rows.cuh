@@ -11,13 +11,16 @@
 // 8-wide side:
 //   S^T[16 keys, rows]  = K Q^T:  A = K codes, B = Q
 //   O^T[16 dims, rows] += V^T P^T: A = V codes, B = P
-// Codes are never scaled: a code becomes the fp16 number q - 8 (exact), so with
-// z + s (q - 8)
-//   score = c 2^a (s (q^.(q - 8)) + z sum(q^)),     c = scale log2(e)
-//   o     = sum p~ (q - 8) + sum p z,               p~ = fp16(p s)
+// Codes are never scaled: masked into place, a nibble q is the fp16 subnormal
+// q 2^-24 (or q 2^-20, the nibble above it), exact and at full rate as an operand.
+// With z + s (q - 8) = (z - 8 s) + s q
+//   score = c 2^a (s (q^.q) + (z - 8 s) sum(q^)),   c = scale log2(e)
+//   o     = sum p~ q + sum (p z - 8 p~),            p~ = fp16(p s)
 // with both products exact up to fp32 accumulation: the one rounding is p~ (2^-11
-// relative). A row of Q is held as q^ = q / 2^a, a power of two that keeps it in
-// the fp16 range.
+// relative, and times q - 8 only, because -8 p~ takes the rounded p~). The powers of
+// two of the nibbles' places are made up for in Q (even pairs of dims times 16) and
+// in the epilogue. A row of Q is held as q^ = q / 2^a, a power of two that keeps it
+// in the fp16 range.
 //
 // Layout of the 16-key group: lane (g, t) = (lane / 4, lane % 4). K: key phi(g)
 // (and 8 + phi(g)), dims (d/4) t ..: one 16-byte load per key gives all its A
@@ -64,25 +67,30 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The four nibbles of both 16-bit halves of w as fp16 pairs q - 8. Masked into
-// place, a nibble is 1024 + q or 1024 + 16 q: one shift a word on the logic pipe,
-// the rest on the multiply pipe (a shift for every nibble keeps the logic pipe, at
-// half the rate, the busier one).
+// The four nibbles of both 16-bit halves of w as fp16 pairs: q 2^-24 in o[0] and
+// o[2], q 2^-20 in o[1] and o[3]. Five operations a word (with q - 8 restored
+// exactly it was nine, and the kernel 101 us where it now takes 94, 64 requests of
+// 8192 tokens).
 __device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&o)[4]) {
-  constexpr uint32_t k1024 = 0x64006400u, kM1032 = 0xE408E408u, kSixteenth = 0x2C002C00u, kM72 = 0xD480D480u;
   const uint32_t v = w >> 8;
-  o[0] = hadd2(and_or(w, 0x000F000Fu, k1024), kM1032);
-  o[1] = hfma2(and_or(w, 0x00F000F0u, k1024), kSixteenth, kM72);
-  o[2] = hadd2(and_or(v, 0x000F000Fu, k1024), kM1032);
-  o[3] = hfma2(and_or(v, 0x00F000F0u, k1024), kSixteenth, kM72);
+  o[0] = w & 0x000F000Fu;
+  o[1] = w & 0x00F000F0u;
+  o[2] = v & 0x000F000Fu;
+  o[3] = v & 0x00F000F0u;
+}
+
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
+  float2 r;
+  asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(r.x), "=f"(r.y) : "r"(v));
+  return r;
 }
 
 // f of a row of V with the given parameters: |z| + 8 s < 2^f, at least -100 (rows
 // of zeros; values that are not finite, whose weights are NaN all the same).
 __device__ __forceinline__ float row_bound(uint32_t par) {
-  const float b = fmaf(8.f, bf16_lo(par), fabsf(bf16_hi(par)));
-  const int e = int((__float_as_uint(b) >> 23) & 255u) - 126;
-  return float(e > 128 ? -100 : max(e, -100));
+  const float half = fmaf(4.f, bf16_lo(par), 0.5f * fabsf(bf16_hi(par)));  // (the whole may pass the fp32 range)
+  const int e = int((__float_as_uint(half) >> 23) & 255u) - 125;
+  return float(e > 129 ? -100 : max(e, -100));
 }
 
 template <int kD, int kNT>
@@ -211,6 +219,10 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
     float sq[kNT][2];           // sums of the rows 8 nt + 2t, + 1
     float cr[kNT][2];           // c 2^a of those rows
     uint32_t see[kNT][2];       // draft tokens those rows see (bit i: token i)
+    // Scores come in units of 2^9 c 2^a, so that no product with a key passes the fp32
+    // range, or of c 2^a where a row of Q is so large that 2^9 c 2^a might.
+    float unit = 1.f;
+    int ra[kNT];                // |q| < 2^ra in row 8 nt + g
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
       const int r = 8 * nt + g;
@@ -228,20 +240,26 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
       for (int i = 0; i < kD / 8; ++i) big = max(big, max((q[nt][i] << 16) & 0x7FFFFFFFu, q[nt][i] & 0x7FFF0000u));
       big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
       big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-      const int a = min(max(int(big >> 23) - 126, -100), 120);  // a row with NaN or infinities stays one
-      const float down = __uint_as_float(uint32_t(127 - a) << 23);
+      ra[nt] = min(max(int(big >> 23) - 126, -100), 127);  // (a row with NaN or infinities stays one)
+      if (__any_sync(0xFFFFFFFFu, ra[nt] > 100)) unit = 512.f;
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNT; ++nt) {
+      // q^ = q 2^(11 - a), 16 times that where the codes are 2^-24 units: just inside fp16.
+      const float down = __uint_as_float(uint32_t(127 + 11 - ra[nt]) << 23);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < kD / 8; ++i) {
         const float lo = bf16_lo(q[nt][i]) * down, hi = bf16_hi(q[nt][i]) * down;
         sum += lo + hi;
-        q[nt][i] = pack_f16x2(lo, hi);
+        q[nt][i] = (i & 1) ? pack_f16x2(lo, hi) : pack_f16x2(lo * 16.f, hi * 16.f);
       }
+      sum *= 0x1p-20f * unit;
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
       sq[nt][0] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t);
       sq[nt][1] = __shfl_sync(0xFFFFFFFFu, sum, 8 * t + 4);
-      const float cs = fmaxf(p.c * __uint_as_float(uint32_t(127 + a) << 23), 1.2e-38f);
+      const float cs = fmaxf(p.c * __uint_as_float(uint32_t(127 + ra[nt] + (unit == 1.f ? 9 : 0)) << 23), 1.2e-38f);
       cr[nt][0] = __shfl_sync(0xFFFFFFFFu, cs, 8 * t);
       cr[nt][1] = __shfl_sync(0xFFFFFFFFu, cs, 8 * t + 4);
 #pragma unroll
@@ -266,6 +284,9 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
     float o[kNT][kMT][4], m[kNT][2], l[kNT][2], zs[kNT][2];
     float neg[kNT][2];  // -M, 0 while there is none
     bool fresh = true;  // some row has no M yet (the same in the whole warp)
+    // Weights are held as 2^(score - M + lift), parameters of V over 2^lift: 0, or 40
+    // once M has met value rows so large that 2^(score - M) might leave the fp32 range.
+    float lift = 0.f, low = 1.f;  // low: 2^-lift
 #pragma unroll
     for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
@@ -318,16 +339,17 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
           }
         }
         // x: scores without c 2^a, -inf where masked.
-        const float ksa = bf16_lo(kpa), ksb = bf16_lo(kpb), kza = bf16_hi(kpa), kzb = bf16_hi(kpb);
-        const float vsa = bf16_lo(vpa), vsb = bf16_lo(vpb), vza = bf16_hi(vpa), vzb = bf16_hi(vpb);
+        const float ksa = bf16_lo(kpa), ksb = bf16_lo(kpb);
+        const float kza = fmaf(-8.f, ksa, bf16_hi(kpa)), kzb = fmaf(-8.f, ksb, bf16_hi(kpb));
+        const float kua = ksa * unit, kub = ksb * unit;
         const bool edge = key0 + 16 > s.prefix;
         uint32_t hidden = 0;  // bit 4 nt + i: element i is masked
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          x[nt][0] = fmaf(x[nt][0] + x2[nt][0], ksa, sq[nt][0] * kza);
-          x[nt][1] = fmaf(x[nt][1] + x2[nt][1], ksa, sq[nt][1] * kza);
-          x[nt][2] = fmaf(x[nt][2] + x2[nt][2], ksb, sq[nt][0] * kzb);
-          x[nt][3] = fmaf(x[nt][3] + x2[nt][3], ksb, sq[nt][1] * kzb);
+          x[nt][0] = fmaf(x[nt][0] + x2[nt][0], kua, sq[nt][0] * kza);
+          x[nt][1] = fmaf(x[nt][1] + x2[nt][1], kua, sq[nt][1] * kza);
+          x[nt][2] = fmaf(x[nt][2] + x2[nt][2], kub, sq[nt][0] * kzb);
+          x[nt][3] = fmaf(x[nt][3] + x2[nt][3], kub, sq[nt][1] * kzb);
           if (edge) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -340,12 +362,20 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
             }
           }
         }
-        float e[kNT][4], w[kNT][4], l2[kNT][2];
+        float e[kNT][4], w[kNT][4], l2[kNT][2], vsa, vsb;
         bool move = fresh;
 #pragma unroll 1
         for (;;) {
           if (move) {
-            const float fa = row_bound(vpa), fb = row_bound(vpb);
+            float fa = row_bound(vpa), fb = row_bound(vpb);
+            float up = 1.f;
+            if (lift == 0.f && __any_sync(0xFFFFFFFFu, fmaxf(fa, fb) > 86.f)) {
+              lift = 40.f;
+              up = 0x1p40f;
+              low = 0x1p-40f;
+            }
+            fa = fmaxf(fa, lift - 100.f);
+            fb = fmaxf(fb, lift - 100.f);
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -357,20 +387,21 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
                 mx = fmaxf(mx, m[nt][r]);
                 const float f = m[nt][r] == mx ? 1.f : ex2(m[nt][r] - mx);  // 0 while m = -inf
                 m[nt][r] = mx;
-                l[nt][r] *= f;
+                l[nt][r] *= f * up;
                 zs[nt][r] *= f;
 #pragma unroll
                 for (int i = 0; i < kMT; ++i) {
                   o[nt][i][r] *= f;
                   o[nt][i][2 + r] *= f;
                 }
-                neg[nt][r] = mx == -INFINITY ? 0.f : -mx;
+                neg[nt][r] = mx == -INFINITY ? 0.f : lift - mx;
               }
             bool none = false;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) none |= m[nt][0] == -INFINITY || m[nt][1] == -INFINITY;
             fresh = __any_sync(0xFFFFFFFFu, none);
           }
+          vsa = bf16_lo(vpa) * low, vsb = bf16_lo(vpb) * low;
           float most = 0.f, sum = 0.f;
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt) {
@@ -390,6 +421,7 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
           if (move || !__any_sync(0xFFFFFFFFu, most > 1024.f || sum > 1.2676506e30f)) break;
           move = true;
         }
+        const float vza = bf16_hi(vpa) * low, vzb = bf16_hi(vpb) * low;
         uint32_t pb[kNT][2];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
@@ -405,8 +437,12 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
           l[nt][1] += l2[nt][1];
           zs[nt][0] += z0 + z2;
           zs[nt][1] += z1 + z3;
-          pb[nt][0] = transpose8x8(pack_f16x2(w[nt][0], w[nt][1]));
-          pb[nt][1] = transpose8x8(pack_f16x2(w[nt][2], w[nt][3]));
+          const uint32_t ra = pack_f16x2(w[nt][0], w[nt][1]), rb = pack_f16x2(w[nt][2], w[nt][3]);
+          pb[nt][0] = transpose8x8(ra);
+          pb[nt][1] = transpose8x8(rb);
+          const float2 fa = unpack_f16x2(ra), fb = unpack_f16x2(rb);  // the weights as they are multiplied
+          zs[nt][0] = fmaf(-8.f, fa.x + fb.x, zs[nt][0]);
+          zs[nt][1] = fmaf(-8.f, fa.y + fb.y, zs[nt][1]);
         }
         // V: keys phi(2t), phi(2t + 1) and 8 further, dims (d/8) g ..
         const uint8_t* vc = pg + P * (kD / 2) + r0 * (kD / 2);
@@ -456,12 +492,12 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
           z += __shfl_xor_sync(0xFFFFFFFFu, z, x);
         }
         const int r = 8 * nt + 2 * t + e;
-        if (g == 0) mlsm[warp * C::kRows + r] = make_float2(m[nt][e], ls);
+        if (g == 0) mlsm[warp * C::kRows + r] = make_float2(m[nt][e], ls * low);
         float* dst = osm + (warp * C::kRows + r) * C::kPitch + g * 2;
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
           *reinterpret_cast<float2*>(dst + i * 16) =
-              make_float2(o[nt][i][e] + z, o[nt][i][2 + e] + z);
+              make_float2(fmaf(o[nt][i][e], i & 1 ? 0x1p20f : 0x1p24f, z), fmaf(o[nt][i][2 + e], i & 1 ? 0x1p20f : 0x1p24f, z));
       }
     named_bar_sync(1, kComp);
     const bool whole = s.whole();
@@ -489,8 +525,7 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
         b = fmaf(f, v.y, b);
       }
       if (whole) {
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        out_row(r)[pd] = pack_bf16x2(a * inv, b * inv);
+        out_row(r)[pd] = L == 0.f ? 0u : pack_bf16x2(a / L, b / L);  // (1 / L may pass the fp32 range)
       } else {
         *reinterpret_cast<float2*>(po + r * kD + 2 * pd) = make_float2(a, b);
         if (pd == 0) pml[r] = make_float2(M, L);
@@ -526,8 +561,7 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
             b = b * fa + fb * v.y;
             M = mn;
           }
-          const float inv = L == 0.f ? 0.f : 1.f / L;
-          out_row(r)[pd] = pack_bf16x2(a * inv, b * inv);
+          out_row(r)[pd] = L == 0.f ? 0u : pack_bf16x2(a / L, b / L);
         }
       }
     }
