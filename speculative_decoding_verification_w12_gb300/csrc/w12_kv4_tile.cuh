@@ -11,16 +11,17 @@
 //   O_h += P_h V_h               tcgen05.mma, A = P from TMEM, V MN-major (warp 2)
 //
 // Operands are fp16 (2^-11 relative) rather than bf16 (2^-8): restored values
-// z + s (q - 8) and P then add nothing that shows next to the output's own
+// (z - 8 s) + s q and P then add little that shows next to the output's own
 // rounding to bf16. Their range is kept by powers of two, which are exact: every
-// 32 keys (one restore warp) have an exponent e for K and f for V, the tile holds
-// value / 2^e, and a row of Q is held over its own power of two 2^a. With
+// 32 keys (one restore warp) have an exponent e for K and f for V;
+// the tile holds K / 2^e and V / 2^(f + 8), and a row of Q is held over its own power
+// of two 2^a. With
 //   y_ij = c 2^(a_i + e_j) S_ij + f_j,       c = scale log2(e)
 // the weight that meets the scaled V is P = 2^(y - M), M a running maximum of y,
-// so what rounds to zero in P is below 2^-24 of what counts in the output; the
-// denominator sum of 2^(y - M) / 2^f_j is kept in fp32. Values that are more than
-// 2^14 below the largest of their 32 keys become fp16 subnormals, an absolute
-// error of at most 2^-25 of that largest value.
+// so what rounds to zero in P is below 2^-20 of what counts in the output; the
+// denominator sum of 2^(y - M) / 2^f_j is kept in fp32, and the output is 2^8 times
+// their quotient. Values far below the largest of their 32 keys become fp16
+// subnormals, an absolute error of at most 2^-20 of that largest value.
 //
 // The softmax takes 32 scores at a time and does not look for a block's maximum: it
 // uses the running M, and only if the 32 weights sum to more than 2^12 (the first
@@ -66,10 +67,11 @@ struct TileCfg {
   static constexpr uint32_t kRawOff = kVOff + kStages * kTile;
   static constexpr uint32_t kXchOff = kRawOff + kRawStages * kRaw;  // (m, l) of the two halves
   static constexpr uint32_t kQxOff = kXchOff + 2 * 128 * 8;         // largest |Q| of the two half rows
-  // Exponents of the restored tiles, by block modulo 4 and 32 keys: (c 2^e, f, 2^-f, -).
+  // Exponents of the restored tiles, by block modulo 4 and 32 keys: (c 2^(e - 8), f, 2^-f, -).
   // Four deep: K of block j + 2 may be restored while the softmax of block j still reads.
+  static constexpr int kExpRing = 4;
   static constexpr uint32_t kExpOff = kQxOff + 2 * 128 * 4;
-  static constexpr uint32_t kBarOff = kExpOff + 16 * 16;
+  static constexpr uint32_t kBarOff = kExpOff + kExpRing * 4 * 16;
   static constexpr uint32_t kRunOff = kBarOff + 320;
   static constexpr uint32_t kSegOff = kRunOff + 512;
   static constexpr uint32_t kSmem = kSegOff + 256 + 1024;           // 1024: alignment slack
@@ -77,27 +79,30 @@ struct TileCfg {
   static constexpr uint32_t kS0 = 0, kS1 = 128, kOA = 256, kOB = 256 + kD, kCols = 512;
 };
 
-// Eight dims of a code word as fp16 values z + s (q - 8), s2 and z2 holding s and
-// z in both halves. A nibble in the lowest bits of fp16 1024 is 1024 + q, in the
-// next four 1024 + 16 q; both become q - 8 exactly, then one rounding.
-__device__ __forceinline__ uint4 restore_word(uint32_t w, uint32_t s2, uint32_t z2) {
-  constexpr uint32_t k1024 = 0x64006400u, kM1032 = 0xE408E408u, kSixteenth = 0x2C002C00u, kM72 = 0xD480D480u;
+// Eight dims of a code word as fp16 values c + s q, c = z - 8 s. A nibble masked
+// into place is the fp16 subnormal q 2^-24, or q 2^-20 for the next four bits: slo,
+// shi hold s 2^24 and s 2^20, c2 holds c, in both halves. One operation to mask and
+// one to scale (q - 8 made exact first took one more and a masked-in exponent: trees
+// 214 us, blocks 87; so 203 and 84). c is a rounded fp16 number, 2^-12 relative at
+// most: next to the same rounding of the value itself that is a shift of the whole
+// row by less than its step / 2^8 unless z is beyond 16 steps.
+__device__ __forceinline__ uint4 restore_word(uint32_t w, uint32_t slo, uint32_t shi, uint32_t c2) {
   const uint32_t v = w >> 8;
   uint4 o;
-  o.x = hfma2(hadd2(and_or(w, 0x000F000Fu, k1024), kM1032), s2, z2);
-  o.y = hfma2(hfma2(and_or(w, 0x00F000F0u, k1024), kSixteenth, kM72), s2, z2);
-  o.z = hfma2(hadd2(and_or(v, 0x000F000Fu, k1024), kM1032), s2, z2);
-  o.w = hfma2(hfma2(and_or(v, 0x00F000F0u, k1024), kSixteenth, kM72), s2, z2);
+  o.x = hfma2(w & 0x000F000Fu, slo, c2);
+  o.y = hfma2(w & 0x00F000F0u, shi, c2);
+  o.z = hfma2(v & 0x000F000Fu, slo, c2);
+  o.w = hfma2(v & 0x00F000F0u, shi, c2);
   return o;
 }
 
-// Exponent of a power of two that no value of a row passes: |z| + 8 s < 2^e,
-// -100 for rows of zeros and of values that are not finite; at most 120 (fp16
-// has room for the 2^8 that the largest rows then keep).
+// Exponent of a power of two that no value of a row passes and that leaves s 2^24
+// inside fp16: |z| + 8 s < 2^e and s < 2^(e - 8). At least -92; that, too, for rows of
+// zeros and of values that are not finite. At most 134 (s < 2^126).
 __device__ __forceinline__ int row_exponent(uint32_t par) {
-  const float b = fmaf(8.f, bf16_lo(par), fabsf(bf16_hi(par)));
-  const int e = int((__float_as_uint(b) >> 23) & 255u) - 126;
-  return e > 128 ? -100 : min(max(e, -100), 120);  // 129: inf or NaN
+  const float half = fmaf(4.f, bf16_lo(par), 0.5f * fabsf(bf16_hi(par)));  // (the whole may pass the fp32 range)
+  const int e = int((__float_as_uint(half) >> 23) & 255u) - 125, es = int((par >> 7) & 255u) - 126 + 8;
+  return e > 129 ? -92 : max(max(e, es), -92);  // 130: inf or NaN
 }
 
 // 2^e for -126 <= e <= 127.
@@ -404,29 +409,31 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         for (int k = 0; k < kD / 32; ++k) w[k] = *reinterpret_cast<const uint4*>(src + place.at[k]);
         const bool past = j * kKeys + i >= s.keys;
         const bool odd = not_finite(vp);
-        const int e = __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(mine));
-        const int f = is_k ? __reduce_max_sync(0xFFFFFFFFu, past ? -100 : row_exponent(vp)) : 0;
-        const float down = pow2(-e);
-        uint32_t s2 = 0u, z2 = 0u;
+        const int e = __reduce_max_sync(0xFFFFFFFFu, past ? -92 : row_exponent(mine));
+        const int f = is_k ? __reduce_max_sync(0xFFFFFFFFu, past ? -92 : row_exponent(vp)) - 8 : 0;
+        const float down = pow2(8 - e) * 0x1p-8f;
+        uint32_t slo = 0u, shi = 0u, c2 = 0u;
         if (!past && (is_k || !odd)) {
-          s2 = pack_f16x2(bf16_lo(mine) * down, bf16_lo(mine) * down);
-          z2 = pack_f16x2(bf16_hi(mine) * down, bf16_hi(mine) * down);
-          if (is_k && odd) z2 = 0x7E007E00u;
+          const float sd = bf16_lo(mine) * down, cd = fmaf(-8.f, sd, bf16_hi(mine) * down);
+          slo = pack_f16x2(sd * 0x1p24f, sd * 0x1p24f);
+          shi = pack_f16x2(sd * 0x1p20f, sd * 0x1p20f);
+          c2 = is_k && odd ? 0x7E007E00u : pack_f16x2(cd, cd);
         }
         if (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&emptyb[st], uint32_t((gj >> 1) - 1) & 1u))) {
           ok = false;
           break;
         }
         // The K warps publish both exponents: the softmax then waits for K alone.
-        if (is_k && lane == 0) exps[(gj & 3) * 4 + (i >> 5)] = make_float4(p.c * pow2(e), float(f), pow2(-f), 0.f);
+        if (is_k && lane == 0)
+          exps[(gj % C::kExpRing) * 4 + (i >> 5)] = make_float4(p.c * pow2(e - 8), float(f), pow2(-f), 0.f);
         uint8_t* tile = tiles + st * C::kTile;
 #pragma unroll
         for (int k = 0; k < kD / 32; ++k) {
           uint8_t* dst = tile + place.dst[k];
-          *reinterpret_cast<uint4*>(dst + place.word[0]) = restore_word(w[k].x, s2, z2);
-          *reinterpret_cast<uint4*>(dst + place.word[1]) = restore_word(w[k].y, s2, z2);
-          *reinterpret_cast<uint4*>(dst + place.word[2]) = restore_word(w[k].z, s2, z2);
-          *reinterpret_cast<uint4*>(dst + place.word[3]) = restore_word(w[k].w, s2, z2);
+          *reinterpret_cast<uint4*>(dst + place.word[0]) = restore_word(w[k].x, slo, shi, c2);
+          *reinterpret_cast<uint4*>(dst + place.word[1]) = restore_word(w[k].y, slo, shi, c2);
+          *reinterpret_cast<uint4*>(dst + place.word[2]) = restore_word(w[k].z, slo, shi, c2);
+          *reinterpret_cast<uint4*>(dst + place.word[3]) = restore_word(w[k].w, slo, shi, c2);
         }
         fence_proxy_async_smem();  // the tile before the MMAs read it, the raw stage before it is refilled
         __syncwarp();
@@ -465,7 +472,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       const int tok = valid ? rr / p.G : 0, hh = valid ? rr - tok * p.G : 0;
       // Q rows into the swizzled Q tile, over a power of two that no value of the
       // row passes: thread (h, r) takes half the row's pieces.
-      float up = 1.f;  // that power
+      float up = 1.f;  // that power, times 2^8
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.Q + s.b * p.q_b + tok * p.q_t +
                                                           (int64_t(s.h) * p.G + hh) * p.q_h) + h * (kD / 16);
@@ -482,8 +489,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         qx[h * 128 + r] = big;
         named_bar_sync(1, 256);
         big = max(big, qx[(1 - h) * 128 + r]);
-        const int a = min(max(int(big >> 23) - 126, -100), 120);  // a row with NaN or infinities stays one
-        up = pow2(a);
+        // Held below 2^10, so that c 2^(e - 8) and 2^(a + 8) have room up to the largest
+        // values; a row with NaN or infinities stays one.
+        const int a = min(max(int(big >> 23) - 126, -100), 128) - 10;
+        up = pow2(a + 8);
         const float down = pow2(-a);
 #pragma unroll
         for (int k = 0; k < kD / 16; ++k) {
@@ -537,7 +546,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
                 uint32_t v[32];
                 tmem_ld32(sc + uint32_t(ch * 32), v);
                 tmem_ld_wait32(v);
-                const float4 ex = exps[(gi & 3) * 4 + 2 * h + ch];
+                const float4 ex = exps[(gi % C::kExpRing) * 4 + 2 * h + ch];
                 if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
                 mx = fmaxf(mx, fmaf(block_max<32>(v), fmaxf(ex.x * up, 1.2e-38f), ex.y));
               }
@@ -560,7 +569,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
             for (int ch = 0; ch < 2; ++ch) {
               uint32_t v[32];
               tmem_ld32(sc + uint32_t(ch * 32), v);
-              const float4 ex = exps[(gi & 3) * 4 + 2 * h + ch];
+              const float4 ex = exps[(gi % C::kExpRing) * 4 + 2 * h + ch];
               tmem_ld_wait32(v);
               if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
               const float sum = exp_pack_f16(v, fmaxf(ex.x * up, 1.2e-38f), ex.y - ref, pk + 16 * ch);
@@ -589,8 +598,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       const float ma = h ? other.x : M, la = h ? other.y : l;
       const float mb = h ? M : other.x, lb = h ? l : other.y;
       M = fmaxf(ma, mb);
-      const float wa = ma == M ? 1.f : fast_exp2(ma - M), wb = mb == M ? 1.f : fast_exp2(mb - M);
+      float wa = ma == M ? 1.f : fast_exp2(ma - M), wb = mb == M ? 1.f : fast_exp2(mb - M);
       const float den = wa * la + wb * lb;
+      wa *= 256.f;  // V is held over 2^(f + 8)
+      wb *= 256.f;
       const bool whole = s.whole();
       const float inv = !whole ? 1.f : den == 0.f ? 0.f : 1.f / den;
       uint32_t* out = reinterpret_cast<uint32_t*>(

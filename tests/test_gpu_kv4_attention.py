@@ -366,6 +366,26 @@ def test_values_that_are_zero_or_constant(T):
     assert (c.run() == 0).all()
 
 
+@pytest.mark.parametrize("T", [1, 3, 16])
+def test_rows_at_the_ends_of_the_range(T):
+    """Keys and values of up to 3.3e38, whose |z| + 8 s passes the fp32 range, with
+    queries that bring the scores back to ordinary size; then the smallest scales."""
+    c = Case([300], [T], T, 10, 2, 128, 64, seed=19)
+    g = np.random.default_rng(20)
+    L = 300 + T
+    kv = g.uniform(-1, 1, (2, L, 2, 128)).astype(np.float32)
+    kv[1, 100:] += np.sign(kv[1, 100:, :, :1])   # rows with a centre of half the range
+    kv[1] *= np.float32(0.5)
+    for size in (3.3e38, 2.0 ** -96):
+        x = kv * np.float32(size)
+        c.cache.append(torch.from_numpy(x[0]).cuda(), torch.from_numpy(x[1]).cuda(), to_dev_i32(c.slots[0]))
+        c.K, c.V = [O.values(*O.quantise(x[0]))], [O.values(*O.quantise(x[1]))]
+        q = np.float32(2.0 ** -100 if size > 1 else 2.0 ** 80)
+        c.Q = torch.from_numpy(g.standard_normal((1, T, 10, 128)).astype(np.float32) * q).cuda().bfloat16()
+        scale = float(np.float32(1 / size / q / 8))
+        c.check(c.run(scale=scale, max_len=L), scale=scale)
+
+
 @pytest.mark.parametrize("T", [1, 16, 40])
 def test_an_expired_wait_is_reported_and_the_next_call_is_right(T):
     """With a 1 us bound a wait may give up (W12_ERR_TIMEOUT); the call ends, and after
