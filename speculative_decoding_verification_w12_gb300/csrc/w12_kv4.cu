@@ -112,37 +112,71 @@ __device__ __forceinline__ E load8(const uint8_t* p) {
   return e;
 }
 
-// A row's code word of this lane and its parameter word.
+// Scale, centre and 1 / s of a row.
+struct RowScale {
+  uint32_t par;
+  float z, inv;
+  bool finite, inside;  // inside: no code of the row needs its clamp
+};
+
 template <int kLanes, typename E>
-__device__ __forceinline__ uint2 quantise8(const E& e) {
+__device__ __forceinline__ RowScale row_scale(const E& e) {
   float lo, hi;
   e.template range<kLanes>(lo, hi);
   constexpr float kR = 1.0f / 15.0f;
-  uint32_t sb = f32_to_bf16_rne(__fsub_rn(__fmul_rn(hi, kR), __fmul_rn(lo, kR)));
+  uint32_t sb = pack_bf16x2(__fsub_rn(__fmul_rn(hi, kR), __fmul_rn(lo, kR)), 0.f);
   float s = __uint_as_float(sb << 16);
   if (s < kTiny) {
     sb = 0;
     s = 0.f;
   }
-  const uint32_t zb = f32_to_bf16_rne(fmaf(8.f, s, lo));
-  const float z = __uint_as_float(zb << 16);
-  const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;
-  // q = clamp(round(t), -8, 7) + 8 as the low bits of 1.5 2^23 + 8 + t (adding it
-  // rounds t to the nearest integer, ties to even, like rint); the eight sums of
-  // the constant's own bits come off at the end.
+  const uint32_t zb = pack_bf16x2(0.f, fmaf(8.f, s, lo));  // in bits 16..31
+  RowScale r;
+  r.z = __uint_as_float(zb);
+  r.inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  r.par = sb | zb;
+  r.finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;  // false for NaN
+  // (x - z) inv grows with x, so the row's ends bound it.
+  r.inside = __fmul_rn(__fsub_rn(lo, r.z), r.inv) >= -8.5f && __fmul_rn(__fsub_rn(hi, r.z), r.inv) < 7.5f;
+  return r;
+}
+
+// A lane's code word. q = clamp(round(t), -8, 7) + 8 as the low bits of 1.5 2^23 +
+// 8 + t (adding it rounds t to the nearest integer, ties to even, like rint); the
+// eight sums of the constant's own bits come off at the end.
+template <bool kClamp, typename E>
+__device__ __forceinline__ uint32_t code_word(const E& e, const RowScale& r) {
   constexpr float kMagic = 12582920.f;
   constexpr uint32_t kBits = 0x4B400000u;
   uint32_t word = 0, base = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int at = 4 * ((i >> 1) + 4 * (i & 1));
-    const float t = __fmul_rn(__fsub_rn(e.value(i), z), inv);
-    word += __float_as_uint(__fadd_rn(fminf(fmaxf(t, -8.f), 7.f), kMagic)) << at;
+    float t = __fmul_rn(__fsub_rn(e.value(i), r.z), r.inv);
+    if constexpr (kClamp) t = fminf(fmaxf(t, -8.f), 7.f);
+    word += __float_as_uint(__fadd_rn(t, kMagic)) << at;
     base += kBits << at;
   }
-  word -= base;
-  const bool finite = fabsf(lo) < INFINITY && fabsf(hi) < INFINITY;  // false for NaN
-  return finite ? make_uint2(word, sb | (zb << 16)) : make_uint2(0x88888888u, 0x7FC07FC0u);
+  return word - base;
+}
+
+// Code words of this lane and parameter words of its two rows. Most rows have no code
+// outside -8 .. 7 (their centre's rounding is far below a step), and a warp of such
+// rows saves the clamps, a third of its work an element.
+template <int kLanes, typename E>
+__device__ __forceinline__ void quantise8(const E& k, const E& v, uint2& kq, uint2& vq) {
+  const RowScale a = row_scale<kLanes>(k), b = row_scale<kLanes>(v);
+  if (__all_sync(0xFFFFFFFFu, a.inside && b.inside)) {
+    kq.x = code_word<false>(k, a);
+    vq.x = code_word<false>(v, b);
+  } else {
+    kq.x = code_word<true>(k, a);
+    vq.x = code_word<true>(v, b);
+  }
+  kq.y = a.par;
+  vq.y = b.par;
+  if (!a.finite) kq = make_uint2(0x88888888u, 0x7FC07FC0u);
+  if (!b.finite) vq = make_uint2(0x88888888u, 0x7FC07FC0u);
 }
 
 template <int kD, typename E, bool kVec>
@@ -165,7 +199,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const __grid_co
   const int page = slot >> p.p_shift;
   const bool in = slot >= 0 && page < p.n_pages;
   if (!in && slot != -1) set_status(p.status, W12_ERR_ARG);
-  const uint2 kq = quantise8<kLanes>(k), vq = quantise8<kLanes>(v);
+  uint2 kq, vq;
+  quantise8<kLanes>(k, v, kq, vq);
   if (!in) return;
   const int r = slot & (p.P - 1);
   uint8_t* blk = p.pool + (int64_t(page) * p.Hkv + h) * p.block;
