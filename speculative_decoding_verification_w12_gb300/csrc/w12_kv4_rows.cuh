@@ -136,8 +136,10 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
   }
   grid_dep_wait();
   const Run run = plan_run<C::kThreads>(p, rs);  // its barriers publish the mbarriers too
-  zero_idle_rows<kD, C::kThreads>(p);
-  if (run.begin >= run.end) return;
+  if (run.begin >= run.end) {
+    if (warp == 0) zero_idle_rows<kD>(p);
+    return;
+  }
   const uint64_t lim = p.limit_ns;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
       }
     }
     grid_dep_launch();
+    zero_idle_rows<kD>(p);
     if (*abort_flag)
       for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
         mbar_wait(&full[i % C::kStages], uint32_t(i / C::kStages) & 1u, drain_limit_ns(lim));
@@ -549,17 +552,27 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
         for (int i = tid; i < R * (kD / 2); i += kComp) {
           const int r = i / (kD / 2), pd = i - r * (kD / 2);
           float M = -INFINITY, L = 0.f, a = 0.f, b = 0.f;
-#pragma unroll 4
-          for (int c = c0; c <= c1; ++c) {
-            const int64_t slot = int64_t(c) * 2 + (c == c0 ? first : 0);
-            const float2 ml = __ldcg(p.part_ml + slot * C::kRows + r);
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_o + (slot * C::kRows + r) * kD) + pd);
-            const float mn = fmaxf(M, ml.x);
-            const float fa = M == mn ? 1.f : ex2(M - mn), fb = ml.x == mn ? 1.f : ex2(ml.x - mn);
-            L = L * fa + fb * ml.y;
-            a = a * fa + fb * v.x;
-            b = b * fa + fb * v.y;
-            M = mn;
+          for (int c = c0; c <= c1; c += 4) {  // four partials' loads in flight
+            float2 ml[4], v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int64_t slot = int64_t(c + u) * 2 + (c + u == c0 ? first : 0);
+              ml[u] = make_float2(-INFINITY, 0.f);
+              v[u] = make_float2(0.f, 0.f);
+              if (c + u <= c1) {
+                ml[u] = __ldcg(p.part_ml + slot * C::kRows + r);
+                v[u] = __ldcg(reinterpret_cast<const float2*>(p.part_o + (slot * C::kRows + r) * kD) + pd);
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float mn = fmaxf(M, ml[u].x);
+              const float fa = M == mn ? 1.f : ex2(M - mn), fb = ml[u].x == mn ? 1.f : ex2(ml[u].x - mn);
+              L = L * fa + fb * ml[u].y;
+              a = a * fa + fb * v[u].x;
+              b = b * fa + fb * v[u].y;
+              M = mn;
+            }
           }
           out_row(r)[pd] = L == 0.f ? 0u : pack_bf16x2(a / L, b / L);
         }

@@ -178,16 +178,26 @@ struct Walk {
   }
 };
 
-// Rows t >= q_len[b] of the output are zero: shared out over all CTAs.
-template <int kD, int kN>
+// Rows t >= q_len[b] of the output are zero: shared out over all CTAs, in each of
+// which one warp (all its lanes call it) looks at 32 (request, token) pairs at a
+// time. Off the other warps' way: done by the whole CTA before its run, pair by pair,
+// it held up a prompt chunk of 2 x 2048 tokens by 8 us.
+template <int kD>
 __device__ __forceinline__ void zero_idle_rows(const Params& p) {
-  const int64_t pairs = int64_t(p.B) * p.T;
+  const int lane = threadIdx.x & 31;
+  const int64_t pairs = int64_t(p.B) * p.T, step = gridDim.x;
   const int words = p.Hq * kD / 8;
-  for (int64_t i = blockIdx.x; i < pairs; i += gridDim.x) {
-    const int b = int(i / p.T), t = int(i - int64_t(b) * p.T);
-    if (t < lens_of(p, b).n) continue;
-    uint4* o = reinterpret_cast<uint4*>(p.O + i * p.Hq * kD);
-    for (int w = threadIdx.x; w < words; w += kN) o[w] = make_uint4(0, 0, 0, 0);
+  for (int64_t first = blockIdx.x; first < pairs; first += 32 * step) {
+    const int64_t i = first + lane * step;
+    bool idle = false;
+    if (i < pairs) {
+      const int b = int(i / p.T);
+      idle = int(i - int64_t(b) * p.T) >= lens_of(p, b).n;
+    }
+    for (uint32_t m = __ballot_sync(0xFFFFFFFFu, idle); m; m &= m - 1) {
+      uint4* o = reinterpret_cast<uint4*>(p.O + (first + (__ffs(m) - 1) * step) * p.Hq * kD);
+      for (int w = lane; w < words; w += 32) o[w] = make_uint4(0, 0, 0, 0);
+    }
   }
 }
 

@@ -74,7 +74,9 @@ struct TileCfg {
   static constexpr uint32_t kBarOff = kExpOff + kExpRing * 4 * 16;
   static constexpr uint32_t kRunOff = kBarOff + 320;
   static constexpr uint32_t kSegOff = kRunOff + 512;
-  static constexpr uint32_t kSmem = kSegOff + 256 + 1024;           // 1024: alignment slack
+  static constexpr uint32_t kAncOff = kSegOff + 256;                // [2][128] sets, then 128 words
+  static constexpr uint32_t kSmem = kAncOff + 2 * 128 * 16 + 512 + 1024;  // 1024: alignment slack
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
   // TMEM columns: S of even and odd blocks, O of the two key halves.
   static constexpr uint32_t kS0 = 0, kS1 = 128, kOA = 256, kOB = 256 + kD, kCols = 512;
 };
@@ -170,13 +172,60 @@ __device__ __forceinline__ float exp_pack_f16(const uint32_t (&v)[32], float c, 
   return s.x + s.y;
 }
 
-// What the softmax warps keep of their place in the run.
-struct SoftmaxSeg {
-  Walk walk;
+// A segment as warp 3 hands it to the softmax warps, two ahead at most.
+struct SegSlot {
   Seg seg;
-  bool more;
+  int more;  // 0: the run is over
 };
-static_assert(sizeof(SoftmaxSeg) <= 256, "shared memory carve-up");
+static_assert(sizeof(SegSlot) <= 128, "shared memory carve-up");
+
+// Ancestors of a draft tree's nodes, themselves included, as 128-bit sets in anc[0 .. T),
+// by one warp, four nodes a lane: each round a node joins the set of the node that its
+// pointer has reached and moves on to that node's pointer, so paths double in length.
+// at: 128 words of shared memory. A malformed tree is flagged and every node then sees
+// itself alone.
+__device__ __forceinline__ void ancestors_of(const int32_t* parents, int T, uint4* anc, int* at, int32_t* status) {
+  const int lane = threadIdx.x & 31;
+  int to[4];
+  uint4 a[4];
+  attn_impl::parent_row(parents, T, to);
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = lane + 32 * k;
+    if (i < T) bad |= i == 0 ? to[k] != -1 : (to[k] < 0 || to[k] >= i);
+  }
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if (bad && lane == 0) set_status(status, W12_ERR_BAD_TREE);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t own = 1u << lane;
+    a[k] = make_uint4(k == 0 ? own : 0u, k == 1 ? own : 0u, k == 2 ? own : 0u, k == 3 ? own : 0u);
+    if (bad) to[k] = -1;
+    anc[lane + 32 * k] = a[k];
+    at[lane + 32 * k] = to[k];
+  }
+  __syncwarp();
+  for (int round = 0; round < 7; ++round) {
+    bool on = false;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (to[k] >= 0) {
+        const uint4 x = anc[to[k]];
+        a[k] = make_uint4(a[k].x | x.x, a[k].y | x.y, a[k].z | x.z, a[k].w | x.w);
+        to[k] = at[to[k]];
+        on = true;
+      }
+    if (!__any_sync(0xFFFFFFFFu, on)) break;  // (the vote also keeps these reads before the writes)
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      anc[lane + 32 * k] = a[k];
+      at[lane + 32 * k] = to[k];
+    }
+    __syncwarp();
+  }
+}
 
 template <int kD>
 __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel(const __grid_constant__ Params p) {
@@ -196,12 +245,17 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   uint64_t* o_final = o_done + 2;                                       // every MMA of the segment done
   uint64_t* q_ready = o_final + 1;                                      // the segment's Q stored, O free
   uint64_t* drained = q_ready + 1;                                      // [2]
-  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(drained + 2);
+  uint64_t* seg_full = drained + 2;                                     // [2] segment i found, in slot i % 2
+  uint64_t* seg_empty = seg_full + 2;                                   // [2] and done with (one arrival a warp)
+  uint64_t* anc_full = seg_empty + 2;                                   // [2] its tree's ancestors found
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(anc_full + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* merge_here = abort_flag + 1;
   RunSmem& rs = *reinterpret_cast<RunSmem*>(smem + C::kRunOff);
   float4* exps = reinterpret_cast<float4*>(smem + C::kExpOff);
-  static_assert((2 * C::kRawStages + 4 * C::kStages + 12) * 8 + 16 <= 320 && sizeof(RunSmem) <= 512, "carve-up");
+  SegSlot* segs = reinterpret_cast<SegSlot*>(smem + C::kSegOff);
+  uint4* ancs = reinterpret_cast<uint4*>(smem + C::kAncOff);
+  static_assert((2 * C::kRawStages + 4 * C::kStages + 18) * 8 + 16 <= 320 && sizeof(RunSmem) <= 512, "carve-up");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -219,6 +273,9 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       mbar_init(&s_full[k], 1);
       mbar_init(&o_done[k], 1);
       mbar_init(&drained[k], 1);
+      mbar_init(&seg_full[k], 1);
+      mbar_init(&seg_empty[k], 8);
+      mbar_init(&anc_full[k], 1);
     }
     for (int k = 0; k < 4; ++k) mbar_init(&p_full[k], 128);
     mbar_init(o_final, 2);
@@ -229,8 +286,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   grid_dep_wait();
   plan_run<C::kThreads>(p, rs);  // its barriers publish the mbarriers too
   const Run& run = rs.run;       // read where it is used: registers are short
-  zero_idle_rows<kD, C::kThreads>(p);
-  if (run.begin >= run.end) return;
+  if (run.begin >= run.end) {
+    if (warp == 0) zero_idle_rows<kD>(p);
+    return;
+  }
   if (warp == 1) {
     tmem_alloc(const_cast<uint32_t*>(tmem_slot), C::kCols);
     tmem_relinquish();
@@ -378,6 +437,41 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     if (elect_one()) tc_commit(&drained[is_s ? 0 : 1]);
     __syncwarp();
     mbar_wait(&drained[is_s ? 0 : 1], 0, drain_limit_ns(lim));
+  } else if (warp == 3) {
+    // ----------------------------------------------------------- segments
+    // Finds the run's segments for the softmax warps, up to two ahead, with the
+    // ancestors of their trees (7000 cycles a segment when every softmax warp walked
+    // the paths of its rows), and brings their Q rows to the L2 cache.
+    Walk walk(run);
+    for (int si = 0;; ++si) {
+      const int sl = si & 1;
+      if (si >= 2 && !__all_sync(0xFFFFFFFFu, wait(&seg_empty[sl], uint32_t((si >> 1) - 1) & 1u))) break;
+      Seg s;
+      const bool more = walk.next(p, run, s);
+      if (lane == 0) {
+        if (more) segs[sl].seg = s;
+        segs[sl].more = more;
+        mbar_arrive(&seg_full[sl]);
+      }
+      if (more) {
+        for (int x = lane; x < 128; x += 32) {
+          const int rr = s.tile * 128 + x;
+          if (rr < s.n * p.G) {
+            const int tok = rr / p.G;
+            const uint16_t* row = p.Q + s.b * p.q_b + tok * p.q_t + (int64_t(s.h) * p.G + rr - tok * p.G) * p.q_h;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+            if (kD == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64));
+          }
+        }
+        if (p.parents) {
+          ancestors_of(p.parents + int64_t(s.b) * p.T, p.T, ancs + sl * 128, reinterpret_cast<int*>(ancs + 256), p.status);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&anc_full[sl]);
+        }
+      }
+      if (si == 0) zero_idle_rows<kD>(p);
+      if (!more) break;
+    }
   } else if (warp >= 12) {
     // ------------------------------------------------------------ restore
     // Warps 12-15 restore K, 16-19 V; thread i of each four has row i of the block.
@@ -456,15 +550,12 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     const uint32_t o_own = tmem + lane_off + (h ? C::kOB : C::kOA);
     float2* xch = reinterpret_cast<float2*>(smem + C::kXchOff);
     int base = 0, si = 0;
-    // The segment and the walk are kept in shared memory: registers are short.
-    SoftmaxSeg& sh = *reinterpret_cast<SoftmaxSeg*>(smem + C::kSegOff);
-    const Seg& s = sh.seg;
-    if (tid == 128) sh.walk = Walk(run);
     for (;;) {
-      named_bar_sync(1, 256);
-      if (tid == 128) sh.more = sh.walk.next(p, run, sh.seg);
-      named_bar_sync(1, 256);
-      if (!sh.more) break;
+      const int sl = si & 1;
+      const Seg& s = segs[sl].seg;  // read where it is used: registers are short
+      const bool got = wait(&seg_full[sl], uint32_t(si >> 1) & 1u);
+      if (named_bar_any(1, 256, !got)) break;
+      if (!segs[sl].more) break;
       const int R = s.n * p.G;
       const int rr = s.tile * 128 + r;
       const bool valid = rr < R;
@@ -506,23 +597,23 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
                                     (((piece & 7u) ^ (uint32_t(r) & 7u)) << 4)) = w;
         }
       }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(q_ready);
       uint32_t anc[4] = {0u, 0u, 0u, 0u};
       int limit = 0x7FFFFFFF;  // keys before it are seen (idle rows mask nothing: their results are not stored)
+      bool ok = true;
       if (p.parents) {
-        int pr[4];
-        attn_impl::parent_row(p.parents + int64_t(s.b) * p.T, p.T, pr);
-        attn_impl::tree_ancestors(pr, tok, p.T, valid, anc, p.status);
+        ok = __all_sync(0xFFFFFFFFu, wait(&anc_full[sl], uint32_t(si >> 1) & 1u));
+        const uint4 x = ancs[sl * 128 + tok];
+        anc[0] = x.x, anc[1] = x.y, anc[2] = x.z, anc[3] = x.w;
         if (valid) limit = s.prefix;
       } else if (valid) {
         limit = s.prefix + tok + 1;
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(q_ready);
       float M = -INFINITY, l = 0.f;
-      bool ok = true;
       const int n = s.j1 - s.j0, key0 = s.j0 * kKeys + 64 * h;
-      for (int i = 0; i < n; ++i) {
+      for (int i = 0; i < n && ok; ++i) {
         const int gi = base + i;
         const int kb = key0 + i * kKeys;
         if (!__all_sync(0xFFFFFFFFu, wait(&s_full[gi & 1], uint32_t(gi >> 1) & 1u))) {
@@ -651,30 +742,49 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           fence_acq_rel_gpu();
           const int c0 = run_of(run, s.x0), c1 = run_of(run, s.x0 + s.nkb - 1);
           const int first = run_start(run, c0) >= s.x0 ? 0 : 1;
+          // Three partials' loads are in flight at a time (an item has two or three as
+          // a rule; one after the other they took 15000 cycles, 80 rows of 128 dims).
+          auto slot_of = [&](int c) { return int64_t(c) * 2 + (c == c0 ? first : 0); };
           float Mx = -INFINITY, L = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float2 ml = __ldcg(p.part_ml + (int64_t(c) * 2 + (c == c0 ? first : 0)) * 128 + r);
-            const float mn = fmaxf(Mx, ml.x);
-            L = L * (Mx == mn ? 1.f : fast_exp2(Mx - mn)) + ml.y * (ml.x == mn ? 1.f : fast_exp2(ml.x - mn));
-            Mx = mn;
+          for (int c = c0; c <= c1; c += 3) {
+            float2 ml[3];
+#pragma unroll
+            for (int u = 0; u < 3; ++u)
+              ml[u] = c + u <= c1 ? __ldcg(p.part_ml + slot_of(c + u) * 128 + r) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int u = 0; u < 3; ++u) {
+              const float mn = fmaxf(Mx, ml[u].x);
+              L = L * (Mx == mn ? 1.f : fast_exp2(Mx - mn)) + ml[u].y * (ml[u].x == mn ? 1.f : fast_exp2(ml[u].x - mn));
+              Mx = mn;
+            }
           }
           const float scale = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 1
           for (int ch = 0; ch < kD / 32; ++ch) {  // 16 dims at a time
             float o[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) o[k] = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-              const int64_t slot = int64_t(c) * 2 + (c == c0 ? first : 0);
-              const float mx = __ldcg(p.part_ml + slot * 128 + r).x;
-              const float f = mx == Mx ? 1.f : fast_exp2(mx - Mx);
-              const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * (kD / 4) + h * (kD / 8) + ch * 4) * 128 + r;
+            for (int c = c0; c <= c1; c += 3) {
+              float4 v[3][4];
+              float mx[3];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float4 v = __ldcg(src + k * 128);
-                o[4 * k] = fmaf(f, v.x, o[4 * k]);
-                o[4 * k + 1] = fmaf(f, v.y, o[4 * k + 1]);
-                o[4 * k + 2] = fmaf(f, v.z, o[4 * k + 2]);
-                o[4 * k + 3] = fmaf(f, v.w, o[4 * k + 3]);
+              for (int u = 0; u < 3; ++u) {
+                const int64_t slot = slot_of(c + u);
+                const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * (kD / 4) + h * (kD / 8) + ch * 4) * 128 + r;
+                mx[u] = c + u <= c1 ? __ldcg(p.part_ml + slot * 128 + r).x : -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[u][k] = c + u <= c1 ? __ldcg(src + k * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+#pragma unroll
+              for (int u = 0; u < 3; ++u) {
+                const float f = mx[u] == Mx ? 1.f : fast_exp2(mx[u] - Mx);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  o[4 * k] = fmaf(f, v[u][k].x, o[4 * k]);
+                  o[4 * k + 1] = fmaf(f, v[u][k].y, o[4 * k + 1]);
+                  o[4 * k + 2] = fmaf(f, v[u][k].z, o[4 * k + 2]);
+                  o[4 * k + 3] = fmaf(f, v[u][k].w, o[4 * k + 3]);
+                }
               }
             }
 #pragma unroll
@@ -682,6 +792,8 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&seg_empty[sl]);
       base += n;
       ++si;
     }
