@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
     }
     if (!whole) {
       const int item = s.b * p.Hkv + s.h;
-      fence_acq_rel_gpu();
+      // (The barrier orders the CTA's stores before the one release, and its acquire before all loads.)
       named_bar_sync(1, kComp);
       if (tid == 0) {
         const int add = s.j1 - s.j0;
@@ -545,7 +545,6 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
       }
       named_bar_sync(1, kComp);
       if (*merge_here) {
-        fence_acq_rel_gpu();
         // Only the first of the item's CTAs can have begun its run before the item.
         const int c0 = run_of(run, s.x0), c1 = run_of(run, s.x0 + s.nkb - 1);
         const int first = run_start(run, c0) >= s.x0 ? 0 : 1;

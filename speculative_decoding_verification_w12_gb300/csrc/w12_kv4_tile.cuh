@@ -66,13 +66,13 @@ struct TileCfg {
   static constexpr uint32_t kVOff = kKOff + kStages * kTile;
   static constexpr uint32_t kRawOff = kVOff + kStages * kTile;
   static constexpr uint32_t kXchOff = kRawOff + kRawStages * kRaw;  // (m, l) of the two halves
-  static constexpr uint32_t kQxOff = kXchOff + 2 * 128 * 8;         // largest |Q| of the two half rows
+  static constexpr uint32_t kQxOff = kXchOff + 2 * 128 * 8;         // [2][128] powers of two of Q rows
   // Exponents of the restored tiles, by block modulo 4 and 32 keys: (c 2^(e - 8), f, 2^-f, -).
   // Four deep: K of block j + 2 may be restored while the softmax of block j still reads.
   static constexpr int kExpRing = 4;
   static constexpr uint32_t kExpOff = kQxOff + 2 * 128 * 4;
   static constexpr uint32_t kBarOff = kExpOff + kExpRing * 4 * 16;
-  static constexpr uint32_t kRunOff = kBarOff + 320;
+  static constexpr uint32_t kRunOff = kBarOff + 336;
   static constexpr uint32_t kSegOff = kRunOff + 512;
   static constexpr uint32_t kAncOff = kSegOff + 256;                // [2][128] sets, then 128 words
   static constexpr uint32_t kSmem = kAncOff + 2 * 128 * 16 + 512 + 1024;  // 1024: alignment slack
@@ -227,6 +227,44 @@ __device__ __forceinline__ void ancestors_of(const int32_t* parents, int T, uint
   }
 }
 
+// Sixteen rows of a segment's Q (part of eight) into the swizzled fp16 Q tile, by one
+// warp: each over a power of two 2^ra[row] that brings it below 2^10, so that
+// c 2^(e - 8) and 2^(ra + 8) have room up to the largest values. A row with NaN or
+// infinities stays one.
+template <int kD>
+__device__ __forceinline__ void load_q(const Params& p, const Seg& s, int part, uint8_t* tile, int* ra) {
+  constexpr int kLanes = kD / 8, kStep = 32 / kLanes, kN = 16 / kStep;  // lanes a row, rows a load, loads
+  const int lane = threadIdx.x & 31, c = lane % kLanes, r0 = part * 16 + lane / kLanes;
+  const int R = s.n * p.G;
+  const uint16_t* q = p.Q + s.b * p.q_b + int64_t(s.h) * p.G * p.q_h + c * 8;
+  int rr = s.tile * 128 + r0, tok = rr / p.G, hh = rr - tok * p.G;
+  uint4 v[kN];
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    v[k] = rr < R ? __ldg(reinterpret_cast<const uint4*>(q + tok * p.q_t + hh * p.q_h)) : make_uint4(0, 0, 0, 0);
+    rr += kStep;
+    for (hh += kStep; hh >= p.G; hh -= p.G) ++tok;
+  }
+#pragma unroll
+  for (int k = 0; k < kN; ++k) {
+    const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+    uint32_t big = 0u;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) big = max(big, max((w[x] << 16) & 0x7FFFFFFFu, w[x] & 0x7FFF0000u));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+    const int a = min(max(int(big >> 23) - 126, -100), 128) - 10, r = r0 + k * kStep;
+    const float down = pow2(-a);
+    uint4 o;
+    o.x = pack_f16x2(bf16_lo(w[0]) * down, bf16_hi(w[0]) * down);
+    o.y = pack_f16x2(bf16_lo(w[1]) * down, bf16_hi(w[1]) * down);
+    o.z = pack_f16x2(bf16_lo(w[2]) * down, bf16_hi(w[2]) * down);
+    o.w = pack_f16x2(bf16_lo(w[3]) * down, bf16_hi(w[3]) * down);
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * TileCfg<kD>::kHalf + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = o;
+    if (c == 0) ra[r] = a;
+  }
+}
+
 template <int kD>
 __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel(const __grid_constant__ Params p) {
   using C = TileCfg<kD>;
@@ -242,9 +280,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   uint64_t* s_full = v_empty + C::kStages;                              // [2] S of block i in buffer i % 2
   uint64_t* p_full = s_full + 2;                                        // [2][2] P of block i, key half h
   uint64_t* o_done = p_full + 4;                                        // [2] P V of block i (both halves) done
-  uint64_t* o_final = o_done + 2;                                       // every MMA of the segment done
-  uint64_t* q_ready = o_final + 1;                                      // the segment's Q stored, O free
-  uint64_t* drained = q_ready + 1;                                      // [2]
+  uint64_t* o_final = o_done + 2;                                       // P V of the segment's last block done
+  uint64_t* o_free = o_final + 1;                                       // O of the segment read (one arrival a warp)
+  uint64_t* q_full = o_free + 1;                                        // its Q stored (one arrival a warp)
+  uint64_t* drained = q_full + 1;                                      // [2]
   uint64_t* seg_full = drained + 2;                                     // [2] segment i found, in slot i % 2
   uint64_t* seg_empty = seg_full + 2;                                   // [2] and done with (one arrival a warp)
   uint64_t* anc_full = seg_empty + 2;                                   // [2] its tree's ancestors found
@@ -255,7 +294,8 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   float4* exps = reinterpret_cast<float4*>(smem + C::kExpOff);
   SegSlot* segs = reinterpret_cast<SegSlot*>(smem + C::kSegOff);
   uint4* ancs = reinterpret_cast<uint4*>(smem + C::kAncOff);
-  static_assert((2 * C::kRawStages + 4 * C::kStages + 18) * 8 + 16 <= 320 && sizeof(RunSmem) <= 512, "carve-up");
+  int* qx = reinterpret_cast<int*>(smem + C::kQxOff);
+  static_assert((2 * C::kRawStages + 4 * C::kStages + 19) * 8 + 16 <= 336 && sizeof(RunSmem) <= 512, "carve-up");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -278,8 +318,9 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       mbar_init(&anc_full[k], 1);
     }
     for (int k = 0; k < 4; ++k) mbar_init(&p_full[k], 128);
-    mbar_init(o_final, 2);
-    mbar_init(q_ready, 256);
+    mbar_init(o_final, 1);
+    mbar_init(o_free, 8);
+    mbar_init(q_full, 8);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -375,7 +416,11 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     bool ok = true;
     while (ok && walk.next(p, run, s)) {
       const int n = s.j1 - s.j0;
-      if (!wait_all(q_ready, uint32_t(si) & 1u)) break;
+      if (is_s) {
+        if (!wait_all(q_full, uint32_t(si) & 1u)) break;
+      } else if (si >= 1 && !wait_all(o_free, uint32_t(si - 1) & 1u)) {
+        break;
+      }
       for (int j = 0; j < n; ++j) {
         const int gj = base + j;
         const int st = gj % C::kStages;
@@ -429,7 +474,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         }
       }
       if (!ok) break;
-      if (elect_one()) tc_commit(o_final);
+      if (!is_s && elect_one()) tc_commit(o_final);
       __syncwarp();
       base += n;
       ++si;
@@ -550,6 +595,12 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     const uint32_t o_own = tmem + lane_off + (h ? C::kOB : C::kOA);
     float2* xch = reinterpret_cast<float2*>(smem + C::kXchOff);
     int base = 0, si = 0;
+    auto store_q = [&](int slot) {
+      load_q<kD>(p, segs[slot].seg, warp - 4, smem + C::kQOff, qx + slot * 128);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
     for (;;) {
       const int sl = si & 1;
       const Seg& s = segs[sl].seg;  // read where it is used: registers are short
@@ -561,50 +612,13 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       const bool valid = rr < R;
       const bool warp_live = __any_sync(0xFFFFFFFFu, valid);
       const int tok = valid ? rr / p.G : 0, hh = valid ? rr - tok * p.G : 0;
-      // Q rows into the swizzled Q tile, over a power of two that no value of the
-      // row passes: thread (h, r) takes half the row's pieces.
-      float up = 1.f;  // that power, times 2^8
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(p.Q + s.b * p.q_b + tok * p.q_t +
-                                                          (int64_t(s.h) * p.G + hh) * p.q_h) + h * (kD / 16);
-        uint4 v[kD / 16];
-        uint32_t big = 0u;
-#pragma unroll
-        for (int k = 0; k < kD / 16; ++k) {
-          v[k] = valid ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) big = max(big, max((w[x] << 16) & 0x7FFFFFFFu, w[x] & 0x7FFF0000u));
-        }
-        uint32_t* qx = reinterpret_cast<uint32_t*>(smem + C::kQxOff);
-        qx[h * 128 + r] = big;
-        named_bar_sync(1, 256);
-        big = max(big, qx[(1 - h) * 128 + r]);
-        // Held below 2^10, so that c 2^(e - 8) and 2^(a + 8) have room up to the largest
-        // values; a row with NaN or infinities stays one.
-        const int a = min(max(int(big >> 23) - 126, -100), 128) - 10;
-        up = pow2(a + 8);
-        const float down = pow2(-a);
-#pragma unroll
-        for (int k = 0; k < kD / 16; ++k) {
-          const uint32_t piece = uint32_t(h * (kD / 16) + k);  // 8 dims
-          uint4 w;
-          w.x = pack_f16x2(bf16_lo(v[k].x) * down, bf16_hi(v[k].x) * down);
-          w.y = pack_f16x2(bf16_lo(v[k].y) * down, bf16_hi(v[k].y) * down);
-          w.z = pack_f16x2(bf16_lo(v[k].z) * down, bf16_hi(v[k].z) * down);
-          w.w = pack_f16x2(bf16_lo(v[k].w) * down, bf16_hi(v[k].w) * down);
-          *reinterpret_cast<uint4*>(smem + C::kQOff + (piece >> 3) * C::kHalf + uint32_t(r) * 128u +
-                                    (((piece & 7u) ^ (uint32_t(r) & 7u)) << 4)) = w;
-        }
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(q_ready);
+      if (si == 0) store_q(0);
+      bool ok = __all_sync(0xFFFFFFFFu, wait(q_full, uint32_t(si) & 1u));
+      const float up = pow2(qx[sl * 128 + r] + 8);  // the row's power of two, times 2^8
       uint32_t anc[4] = {0u, 0u, 0u, 0u};
       int limit = 0x7FFFFFFF;  // keys before it are seen (idle rows mask nothing: their results are not stored)
-      bool ok = true;
       if (p.parents) {
-        ok = __all_sync(0xFFFFFFFFu, wait(&anc_full[sl], uint32_t(si >> 1) & 1u));
+        ok &= __all_sync(0xFFFFFFFFu, wait(&anc_full[sl], uint32_t(si >> 1) & 1u));
         const uint4 x = ancs[sl * 128 + tok];
         anc[0] = x.x, anc[1] = x.y, anc[2] = x.z, anc[3] = x.w;
         if (valid) limit = s.prefix;
@@ -679,6 +693,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         tc_fence_before();
         mbar_arrive(&p_full[(gi & 1) * 2 + h]);
       }
+      // The last S of the segment is done, so Q makes room for the next segment's: its S
+      // goes on under this epilogue.
+      if (ok && __all_sync(0xFFFFFFFFu, wait(&seg_full[sl ^ 1], uint32_t((si + 1) >> 1) & 1u)) && segs[sl ^ 1].more)
+        store_q(sl ^ 1);
       // Epilogue: thread (h, r) joins the halves for dims (kD / 2) h .. of its row.
       const bool fin = __all_sync(0xFFFFFFFFu, ok && wait(o_final, uint32_t(si) & 1u));
       if (named_bar_any(1, 256, !fin)) break;
@@ -727,10 +745,12 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         }
       }
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
       if (!whole) {
         if (h == 0 && valid) p.part_ml[(int64_t(blockIdx.x) * 2 + s.slot) * 128 + r] = make_float2(M, den);
         const int item = s.entry * p.Hkv + s.h;
-        fence_acq_rel_gpu();
+        // (The barrier orders the CTA's stores before the one release, and its acquire before all loads.)
         named_bar_sync(1, 256);
         if (tid == 128) {
           const int add = s.j1 - s.j0;
@@ -739,7 +759,6 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         }
         named_bar_sync(1, 256);
         if (*merge_here && valid) {
-          fence_acq_rel_gpu();
           const int c0 = run_of(run, s.x0), c1 = run_of(run, s.x0 + s.nkb - 1);
           const int first = run_start(run, c0) >= s.x0 ? 0 : 1;
           // Three partials' loads are in flight at a time (an item has two or three as
@@ -788,7 +807,14 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
               }
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) out[ch * 8 + k] = kv4::pack_bf16x2(o[2 * k] * scale, o[2 * k + 1] * scale);
+            for (int k = 0; k < 2; ++k) {
+              uint4 w;
+              w.x = kv4::pack_bf16x2(o[8 * k] * scale, o[8 * k + 1] * scale);
+              w.y = kv4::pack_bf16x2(o[8 * k + 2] * scale, o[8 * k + 3] * scale);
+              w.z = kv4::pack_bf16x2(o[8 * k + 4] * scale, o[8 * k + 5] * scale);
+              w.w = kv4::pack_bf16x2(o[8 * k + 6] * scale, o[8 * k + 7] * scale);
+              reinterpret_cast<uint4*>(out)[ch * 2 + k] = w;
+            }
           }
         }
       }
