@@ -62,20 +62,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// The same with a time hint: the hardware may keep the thread asleep for about
-// that long, so that a long wait does not spend issue slots on polling.
-__device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
-
 // Wait until the phase with the given parity has completed. Bounded: gives up
 // after `limit_ns` of wall time (and after 2^31 polls) and returns false.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
@@ -206,11 +192,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N) {
          | ((M >> 4) << 24);  // M / 16
 }
 
-// The same with fp16 A and B.
-__host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N) {
-  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
 // Shared-memory matrix descriptor for a K-major operand stored with the
 // 128-byte swizzle (rows of 128 bytes, 8-row groups 1024 bytes apart).
 __device__ __forceinline__ uint64_t sdesc_k_sw128(uint32_t saddr) {
@@ -258,13 +239,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
                  "+r"(v[15])
                :
                : "memory");
-}
-
-// True for one lane of the (converged) warp, the same one at every call.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
 }
 
 // Programmatic dependent launch: wait until the grids this launch depends on

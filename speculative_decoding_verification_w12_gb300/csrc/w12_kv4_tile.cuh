@@ -58,6 +58,32 @@ using attn_impl::mask_block;
 using attn_impl::rescale_row;
 using attn_impl::sdesc_mn_sw128;
 
+// mbar_try_wait with a time hint: the hardware may keep the thread asleep for about
+// that long, so that a long wait does not spend issue slots on polling.
+__device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
+// True for one lane of the (converged) warp, the same one at every call.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// idesc_bf16 with fp16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+
 constexpr float kMost = 4096.f;          // sum of 32 weights above which the running maximum moves
 constexpr uint32_t kWaitHintNs = 10000;  // asleep on a barrier between looks at the abort flag and the clock
 
