@@ -10,16 +10,18 @@
 // s = z = NaN: all of it reads as NaN. A scale below 2^-100 stores z alone.
 //
 // All three are bound by HBM: append reads the input rows and writes d + 8
-// bytes a (token, head), read the reverse. One code word (8 dims) per lane:
-// d/8 lanes form a row, so inputs come in 16-byte (bf16) or 32-byte (fp32)
-// pieces and a row's codes leave as one 32- or 64-byte segment. A group of lanes
-// takes K and V of one (token, head), two loads in flight and one set of
-// indices (32-bit: a 64-bit division a row costs more than the quantiser).
+// bytes a (token, head), read the reverse. In append a group of d/8 lanes takes one
+// (token, head), half of it K and half V, and a lane two code words (8 dims each) of
+// its row, one in each half of the row: loads and stores are contiguous over the
+// lanes, and a row's scale is worked out by d/16 lanes only (by d/8, each with a word of
+// K and one of V as in read, 40.5 us where it is 36.7). Indices are 32-bit: a 64-bit
+// division a row costs more than the quantiser.
 //
-// 28,305 tokens of 8 heads x 128 in bf16 (4 requests): append 40.5 us, 3.6 TB/s of
-// the 147 MB it has to move, 53 % of a copy's rate, held back by the issue of about
-// 200 instructions a pair of words; read 32.4 us, 4.5 TB/s. A tree's 256 tokens take
-// 1.9 us (append), 3.3 us (commit) and 1.7 us (read), which is launch latency.
+// 28,305 tokens of 8 heads x 128 in bf16 (4 requests): append 36.7 us, 4.0 TB/s of
+// the 147 MB it has to move, 59 % of a copy's rate, held back by the issue of about
+// 260 instructions a lane; read 32.4 us, 4.5 TB/s, most of it writes (halving its
+// arithmetic changed nothing). A tree's 256 tokens take 1.8 us (append), 3.3 us (commit)
+// and 1.6 us (read), which is launch latency.
 #include "w12_kv4.cuh"
 
 namespace w12 {
@@ -46,12 +48,13 @@ struct F32 {
   uint32_t w[8];
   __device__ __forceinline__ float value(int i) const { return __uint_as_float(w[i]); }
   template <int kLanes>
-  __device__ __forceinline__ void range(float& lo, float& hi) const {
-    lo = hi = value(0);
+  static __device__ __forceinline__ void range(const F32& a, const F32& b, float& lo, float& hi) {
+    lo = hi = a.value(0);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(value(i)));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(value(i)));
+    for (int i = 1; i < 16; ++i) {
+      const float x = i < 8 ? a.value(i) : b.value(i - 8);
+      asm("min.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(x));
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(x));
     }
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) {
@@ -85,10 +88,15 @@ struct Half {
     return (i & 1) ? f.y : f.x;
   }
   template <int kLanes>
-  __device__ __forceinline__ void range(float& lo, float& hi) const {
+  static __device__ __forceinline__ void range(const Half& a, const Half& b, float& lo, float& hi) {
     constexpr uint32_t kSign = 0x80008000u;
-    uint32_t up = max2(max2(w[0], w[1]), max2(w[2], w[3]));
-    uint32_t down = max2(max2(w[0] ^ kSign, w[1] ^ kSign), max2(w[2] ^ kSign, w[3] ^ kSign));
+    uint32_t up = a.w[0], down = a.w[0] ^ kSign;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      const uint32_t x = i < 4 ? a.w[i] : b.w[i - 4];
+      up = max2(up, x);
+      down = max2(down, x ^ kSign);
+    }
     // (largest of the even elements, least negated) and the same of the odd ones.
     uint32_t v = max2(__byte_perm(up, down, 0x5410), __byte_perm(up, down, 0x7632));
 #pragma unroll
@@ -124,10 +132,11 @@ struct RowScale {
   bool finite, inside;  // inside: no code of the row needs its clamp
 };
 
+// Of the row that kLanes lanes hold, two pieces each.
 template <int kLanes, typename E>
-__device__ __forceinline__ RowScale row_scale(const E& e) {
+__device__ __forceinline__ RowScale row_scale(const E& a, const E& b) {
   float lo, hi;
-  e.template range<kLanes>(lo, hi);
+  E::template range<kLanes>(a, b, lo, hi);
   constexpr float kR = 1.0f / 15.0f;
   uint32_t sb = pack_bf16x2(__fsub_rn(__fmul_rn(hi, kR), __fmul_rn(lo, kR)), 0.f);
   float s = __uint_as_float(sb << 16);
@@ -165,23 +174,22 @@ __device__ __forceinline__ uint32_t code_word(const E& e, const RowScale& r) {
   return word - base;
 }
 
-// Code words of this lane and parameter words of its two rows. Most rows have no code
+// The lane's two code words and its row's parameter word (z). Most rows have no code
 // outside -8 .. 7 (their centre's rounding is far below a step), and a warp of such
 // rows saves the clamps, a third of its work an element.
 template <int kLanes, typename E>
-__device__ __forceinline__ void quantise8(const E& k, const E& v, uint2& kq, uint2& vq) {
-  const RowScale a = row_scale<kLanes>(k), b = row_scale<kLanes>(v);
-  if (__all_sync(0xFFFFFFFFu, a.inside && b.inside)) {
-    kq.x = code_word<false>(k, a);
-    vq.x = code_word<false>(v, b);
+__device__ __forceinline__ uint3 quantise16(const E& a, const E& b) {
+  const RowScale r = row_scale<kLanes>(a, b);
+  uint3 q;
+  if (__all_sync(0xFFFFFFFFu, r.inside)) {
+    q.x = code_word<false>(a, r);
+    q.y = code_word<false>(b, r);
   } else {
-    kq.x = code_word<true>(k, a);
-    vq.x = code_word<true>(v, b);
+    q.x = code_word<true>(a, r);
+    q.y = code_word<true>(b, r);
   }
-  kq.y = a.par;
-  vq.y = b.par;
-  if (!a.finite) kq = make_uint2(0x88888888u, 0x7FC07FC0u);
-  if (!b.finite) vq = make_uint2(0x88888888u, 0x7FC07FC0u);
+  q.z = r.par;
+  return r.finite ? q : make_uint3(0x88888888u, 0x88888888u, 0x7FC07FC0u);
 }
 
 template <int kD, typename E, bool kVec>
@@ -190,29 +198,32 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const __grid_co
   grid_dep_wait();
   grid_dep_launch();
   const uint32_t unit = blockIdx.x * uint32_t(kRowThreads / kLanes) + threadIdx.x / kLanes;  // < 2^31 + a CTA's
-  const int w = threadIdx.x % kLanes;
+  constexpr int kRow = kLanes / 2;  // lanes of a row
+  const int w = threadIdx.x % kRow;
+  const bool is_v = threadIdx.x & kRow;
   const uint32_t tok = unit / uint32_t(p.Hkv), h = unit - tok * uint32_t(p.Hkv);
   const bool live = tok < uint32_t(p.n);
-  // The inputs do not wait for the slot: all three loads are in flight together.
-  E k{}, v{};
+  // The inputs do not wait for the slot: all loads are in flight together.
+  E a{}, b{};
   int slot = -1;
   if (live) {
-    k = load8<E, kVec>(static_cast<const uint8_t*>(p.K) + (int64_t(tok) * p.k_tok + int64_t(h) * p.k_head + w * 8) * E::kSize);
-    v = load8<E, kVec>(static_cast<const uint8_t*>(p.V) + (int64_t(tok) * p.v_tok + int64_t(h) * p.v_head + w * 8) * E::kSize);
+    const int64_t at = int64_t(tok) * (is_v ? p.v_tok : p.k_tok) + int64_t(h) * (is_v ? p.v_head : p.k_head) + w * 8;
+    const uint8_t* x = static_cast<const uint8_t*>(is_v ? p.V : p.K) + at * E::kSize;
+    a = load8<E, kVec>(x);
+    b = load8<E, kVec>(x + kRow * 8 * E::kSize);
     slot = p.slots[tok];
   }
   const int page = slot >> p.p_shift;
   const bool in = slot >= 0 && page < p.n_pages;
   if (!in && slot != -1) set_status(p.status, W12_ERR_ARG);
-  uint2 kq, vq;
-  quantise8<kLanes>(k, v, kq, vq);
+  const uint3 q = quantise16<kRow>(a, b);
   if (!in) return;
   const int r = slot & (p.P - 1);
   uint8_t* blk = p.pool + (int64_t(page) * p.Hkv + h) * p.block;
-  uint8_t* codes = blk + r * (kD / 2) + word_off(kD, r, w);
-  *reinterpret_cast<uint32_t*>(codes) = kq.x;
-  *reinterpret_cast<uint32_t*>(codes + p.P * (kD / 2)) = vq.x;
-  if (w < 2) *reinterpret_cast<uint32_t*>(blk + p.P * kD + (w * p.P + r) * 4) = w ? vq.y : kq.y;
+  uint8_t* codes = blk + (is_v ? p.P + r : r) * (kD / 2);
+  *reinterpret_cast<uint32_t*>(codes + word_off(kD, r, w)) = q.x;
+  *reinterpret_cast<uint32_t*>(codes + word_off(kD, r, w + kRow)) = q.y;
+  if (w == 0) *reinterpret_cast<uint32_t*>(blk + p.P * kD + (is_v ? p.P + r : r) * 4) = q.z;
 }
 
 template <int kD>
