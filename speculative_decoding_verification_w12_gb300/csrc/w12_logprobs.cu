@@ -12,8 +12,8 @@
 //   S1 = sum 2^d_i (s1_i + d_i s0_i), lse = M + log S0, entropy = log S0 - ln 2 S1 / S0,
 // and likewise a row's runs by the one that finishes last. Sums are fp32: at most
 // a run's share of a thread, then trees. 256 rows of
-// 151,936 bf16 logits: 22.8 us without a list (3.4 TB/s, half a copy's rate), 34 us
-// with the 8 largest (2.3 TB/s); 16 fp32 rows 7.0 us and, with the 20 largest, 12.9.
+// 151,936 bf16 logits: 21.8 us without a list (3.6 TB/s, half a copy's rate), 33.7 us
+// with the 8 largest (2.3 TB/s); 16 fp32 rows 6.3 us and, with the 20 largest, 12.1.
 // Bound by issue (58 % of the slots) and the barriers of the lists for many rows, by
 // launch and join latency for few.
 //
@@ -86,15 +86,9 @@ __device__ __forceinline__ uint64_t warp_max(uint64_t v) {
   return (uint64_t(hi) << 32) | lo;
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
-}
+// (NaN is below every number.)
 __device__ __forceinline__ float warp_fmax(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
+  return value_of(__reduce_max_sync(0xFFFFFFFFu, v == v ? order_of(v) : 0x007FFFFFu));
 }
 
 struct Smem {
@@ -104,7 +98,8 @@ struct Smem {
   uint64_t best[kMaxK];
   uint64_t warp_key[kWarps];
   uint64_t full[kStages], empty[kStages];
-  float red[3][kWarps];
+  float red[kWarps];
+  float2 sums[kWarps];
   uint32_t wtop[kWarps];  // each warp's r-th largest lane maximum
   int count;              // candidates of the run
   int last;               // whether the run completed its row
@@ -246,30 +241,30 @@ __device__ __forceinline__ void moved(float r, float to, float& s0, float& s1) {
   s0 *= f;
 }
 
-// Joins (r, s0, s1) of all computing threads; every one gets the result.
-__device__ __forceinline__ void join_sums(Smem& s, float& r, float& s0, float& s1) {
+// Joins (r, s0, s1) of all computing threads; every one gets the result. Loops stay
+// loops: what runs once a run is mostly not in the instruction cache, where its length
+// counts for more than its steps.
+__device__ __forceinline__ float3 join_sums(Smem& s, float r, float s0, float s1) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float wm = warp_fmax(r);
-  if (lane == 0) s.red[0][warp] = wm;
+  if (lane == 0) s.red[warp] = wm;
   sync();
-  float M = s.red[0][0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s.red[0][w]);
+  const float M = warp_fmax(s.red[lane % kWarps]);
   moved(r, M, s0, s1);
-  s0 = warp_sum(s0);
-  s1 = warp_sum(s1);
-  if (lane == 0) {
-    s.red[1][warp] = s0;
-    s.red[2][warp] = s1;
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1) {
+    s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
+    s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
   }
+  if (lane == 0) s.sums[warp] = make_float2(s0, s1);
   sync();
-  s0 = s1 = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    s0 += s.red[1][w];
-    s1 += s.red[2][w];
+  float2 v = s.sums[lane % kWarps];
+#pragma unroll 1
+  for (int o = kWarps / 2; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, o);
+    v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, o);
   }
-  r = M;
+  return make_float3(M, v.x, v.y);
 }
 
 // Joins the np runs of a finished row and writes its outputs. Every computing
@@ -278,7 +273,6 @@ template <int kType>
 __device__ __noinline__ void join_row(const Params& p, int64_t row, int np, Smem& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint8_t* base = static_cast<const uint8_t*>(p.logits) + row * p.pitch * (kType == kF32 ? 4 : 2);
-  fence_acq_rel_gpu();
   // Loads of both kinds are in flight together.
   const float4* part = p.part + row * p.nch;
   const uint64_t* cand = p.cand + row * p.nch * p.k;
@@ -313,7 +307,8 @@ __device__ __noinline__ void join_row(const Params& p, int64_t row, int np, Smem
     if (lane == 0) s.warp_key[warp] = cut;
   }
   if (tid == 0) s.count = 0;
-  join_sums(s, r, s0, s1);
+  const float3 all = join_sums(s, r, s0, s1);
+  r = all.x, s0 = all.y, s1 = all.z;
   if (p.k > 0) {
     uint64_t cut = s.warp_key[0];
     for (int w = 1; w < live; ++w) cut = min(cut, s.warp_key[w]);
@@ -545,8 +540,8 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const __
       const int64_t x0 = row * p.nch;
       const int first = int(((x0 + 1) * g - 1) / p.chunks);  // the CTA that holds the row's first chunk
       const int64_t slot = x0 + (int64_t(blockIdx.x) - first);
-      join_sums(s, ref, s0, s1);
-      if (tid == 0) p.part[slot] = make_float4(ref, s0, s1, 0.f);
+      const float3 all = join_sums(s, ref, s0, s1);
+      if (tid == 0) p.part[slot] = make_float4(all.x, all.y, all.z, 0.f);
       if (p.k > 0) {
         uint64_t* out = p.cand + slot * p.k;
         if (s.count <= kCap) {  // (join_sums' barriers: the list is whole)
@@ -563,7 +558,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const __
       }
       sync();
       if (tid == 0) {
-        fence_acq_rel_gpu();
+        // (The barriers around order all threads' stores before it and their loads after.)
         const bool last = atomic_add_acq_rel_gpu(p.done + row, done) + done == p.nch;
         if (last) p.done[row] = 0;
         s.last = last;
