@@ -9,12 +9,13 @@
 // shrinking by the same amounts restores the stack.
 //
 // One thread-block cluster runs the call. Each CTA scans all B lengths itself
-// (B loads from L2 and one block scan are cheaper than exchanging partial sums),
-// then the cluster's threads share the pages to pop; a cluster barrier orders
-// the pops before the pushes that reuse their stack entries and before the
-// slots, which read entries that other CTAs wrote. Latency-bound: a call is
+// (B loads from L2 and one block scan are cheaper than exchanging partial sums) and
+// keeps them in shared memory; then the cluster's threads share the pages to pop and
+// the slots to write. A slot on a page that the call takes is read from the free stack,
+// not from the table entry that another CTA may be writing, so nothing waits for the
+// pops but the pushes that reuse their stack entries. Latency-bound: a call is
 // a few dependent L2 round trips (16 requests of 16 tokens: reserve and trim take
-// 6.3 us on the device; 256 prompts of 1024 tokens, 1.2 MB of slots and pages: 19 us).
+// 6.3 us on the device; 256 prompts of 1024 tokens, 1.2 MB of slots and pages: 16.6 us).
 #include <cooperative_groups.h>
 
 #include "w12_dev.cuh"
@@ -28,7 +29,8 @@ constexpr int kSmall = 256;   // threads of a small call's only CTA
 constexpr int kLarge = 1024;  // threads of each CTA of a large call's cluster
 constexpr int kCluster = 8;
 constexpr int kSpan = 256;    // slots of one request that a warp writes at a time
-constexpr int kMaxB = 8192;  // requests per call (two prefix sums of B ints in shared memory)
+constexpr int kMaxB = 8192;  // requests per call
+constexpr int kPerRequest = 5 * 4;  // bytes of shared memory a request
 
 struct PagesParams {
   int32_t *table, *used, *free_pages, *n_free;
@@ -68,7 +70,10 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_constant__ PagesParams p) {
   extern __shared__ int smem[];
   int* gpre = smem;         // pages taken by the requests before b
-  int* spre = smem + p.B;   // pages given back by the requests before b
+  int* spre = gpre + p.B;   // pages given back by the requests before b
+  int* base = spre + p.B;   // pages that request b holds before and after the call
+  int* from = base + p.B;   // its start
+  int* live = from + p.B;   // its new tokens, 0 where it is not served
   __shared__ long long warp_sum[kThreads / 32];
   __shared__ int granted;   // pages taken by all requests that get theirs
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -85,8 +90,9 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + tid;
     long long v = 0;
+    Need n{};
     if (b < p.B) {
-      const Need n = need_of(p, b);
+      n = need_of(p, b);
       v = (static_cast<long long>(max(0, n.want - n.have)) << 32) | static_cast<long long>(max(0, n.have - n.want));
     }
     long long inc = v;
@@ -110,49 +116,59 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
       spre[b] = int((inc - v) & 0xFFFFFFFFll);
       // Growing requests whose pages all lie within the free stack get them.
       const int upto = int(inc >> 32);
-      if ((v >> 32) > 0 && upto <= n_free) atomicMax(&granted, upto);
+      const bool grows = (v >> 32) > 0, served = n.ok && (!grows || upto <= n_free);
+      if (grows && served) atomicMax(&granted, upto);
+      base[b] = min(n.have, n.want);
+      from[b] = p.start[b];
+      live[b] = served && p.add ? p.add[b] : 0;
     }
     carry += total;
     __syncthreads();
   }
   const int G = granted, R = int(carry & 0xFFFFFFFFll);
+  cluster.barrier_arrive();  // this CTA has read the lengths and counts
   // Pops.
   for (int k = me; k < G; k += all) {
     const int b = last_le(gpre, p.B, k);
-    p.table[int64_t(b) * p.max_pages + p.used[b] + (k - gpre[b])] = p.free_pages[n_free - 1 - k];
-  }
-  if (G > 0) cluster.sync();  // the same in every CTA
-  // Pushes.
-#pragma unroll 2
-  for (int k = me; k < R; k += all) {
-    const int b = last_le(spre, p.B, k);
-    const Need n = need_of(p, b);
-    int32_t* e = p.table + int64_t(b) * p.max_pages + n.want + (k - spre[b]);
-    const int at = n_free - G + R - 1 - k;
-    if (at < p.n_pages) p.free_pages[at] = *e;
-    else set_status(p.status, W12_ERR_ARG);  // more pages than the pool has: counts that do not match
-    *e = -1;
+    p.table[int64_t(b) * p.max_pages + base[b] + (k - gpre[b])] = p.free_pages[n_free - 1 - k];
   }
   // Slots of the new tokens: a warp takes kSpan slots of one request at a time.
   if (p.T > 0) {
     const int spans = (p.T + kSpan - 1) / kSpan, units = p.B * spans;
     for (int u = me >> 5; u < units; u += all >> 5) {
       const int b = u / spans, i0 = (u - b * spans) * kSpan;
-      const Need n = need_of(p, b);
-      const int grow = n.want - n.have;
-      const int start = p.start[b];
-      const int live = n.ok && (grow <= 0 || gpre[b] + grow <= n_free) ? p.add[b] : 0;
+      const int start = from[b], n = live[b], held = base[b];
       const int32_t* tab = p.table + int64_t(b) * p.max_pages;
+      const int32_t* taken = p.free_pages + (n_free - 1 - gpre[b]);
       int32_t* out = p.slots + int64_t(b) * p.T;
-      const int end = min(p.T, i0 + kSpan);
-#pragma unroll 4
-      for (int i = i0 + lane; i < end; i += 32) {
-        const int pos = start + i;
-        out[i] = i < live ? (tab[pos >> p.p_shift] << p.p_shift) + (pos & ((1 << p.p_shift) - 1)) : -1;
+      // All loads of the span are in flight before the first store.
+      int page[kSpan / 32];
+#pragma unroll
+      for (int x = 0; x < kSpan / 32; ++x) {
+        const int i = i0 + 32 * x + lane, q = (start + i) >> p.p_shift;
+        const int32_t* at = q < held ? tab + q : taken + (held - q);
+        page[x] = 0;
+        if (i < n) page[x] = *at;
+      }
+#pragma unroll
+      for (int x = 0; x < kSpan / 32; ++x) {
+        const int i = i0 + 32 * x + lane;
+        if (i < p.T) out[i] = i < n ? (page[x] << p.p_shift) + ((start + i) & ((1 << p.p_shift) - 1)) : -1;
       }
     }
   }
-  cluster.sync();
+  cluster.barrier_wait();
+  if (G > 0 && R > 0) cluster.sync();  // (the same in every CTA) pushes reuse the entries of pops
+  // Pushes.
+#pragma unroll 2
+  for (int k = me; k < R; k += all) {
+    const int b = last_le(spre, p.B, k);
+    int32_t* e = p.table + int64_t(b) * p.max_pages + base[b] + (k - spre[b]);
+    const int at = n_free - G + R - 1 - k;
+    if (at < p.n_pages) p.free_pages[at] = *e;
+    else set_status(p.status, W12_ERR_ARG);  // more pages than the pool has: counts that do not match
+    *e = -1;
+  }
   for (int b = me; b < p.B; b += all) {
     const Need n = need_of(p, b);
     const int grow = n.want - n.have;
@@ -180,7 +196,7 @@ extern "C" int w12_pages_update(int32_t* table, int32_t* used, int32_t* free_pag
   if (!device_supported()) return W12_ERR_UNSUPPORTED;
   PagesParams p{table, used, free_pages, n_free, start, add, slots, dev_status, B, max_pages,
                 __builtin_ctz(unsigned(page_size)), int(n_pages), T};
-  const size_t smem = size_t(B) * 2 * sizeof(int);
+  const size_t smem = size_t(B) * kPerRequest;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -202,7 +218,7 @@ extern "C" int w12_pages_update(int32_t* table, int32_t* used, int32_t* free_pag
     return cuda_status(cudaLaunchKernelEx(&cfg, pages_update_kernel<kSmall>, p));
   }
   if (smem > 40 * 1024 && cudaFuncSetAttribute(pages_update_kernel<kLarge>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kMaxB * 8) != cudaSuccess)
+                                               kMaxB * kPerRequest) != cudaSuccess)
     return W12_ERR_CUDA;
   cfg.gridDim = dim3(kCluster);
   cfg.blockDim = dim3(kLarge);
