@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
       int page[kSpan / 32];
 #pragma unroll
       for (int x = 0; x < kSpan / 32; ++x) {
-        const int i = i0 + 32 * x + lane, q = (start + i) >> p.p_shift;
+        const int i = i0 + 32 * x + lane, q = int((uint32_t(start) + uint32_t(i)) >> p.p_shift);  // (up to 2^31 + T)
         const int32_t* at = q < held ? tab + q : taken + (held - q);
         page[x] = 0;
         if (i < n) page[x] = *at;
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) pages_update_kernel(const __grid_con
 #pragma unroll
       for (int x = 0; x < kSpan / 32; ++x) {
         const int i = i0 + 32 * x + lane;
-        if (i < p.T) out[i] = i < n ? (page[x] << p.p_shift) + ((start + i) & ((1 << p.p_shift) - 1)) : -1;
+        if (i < p.T) out[i] = i < n ? (page[x] << p.p_shift) + int((uint32_t(start) + uint32_t(i)) & ((1u << p.p_shift) - 1u)) : -1;
       }
     }
   }

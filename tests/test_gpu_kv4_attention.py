@@ -386,6 +386,28 @@ def test_rows_at_the_ends_of_the_range(T):
         c.check(c.run(scale=scale, max_len=L), scale=scale)
 
 
+@pytest.mark.parametrize("power", [-90, 101, 118])
+@pytest.mark.parametrize("T", [1, 3, 16])
+def test_queries_at_the_ends_of_the_range(T, power):
+    """Queries of 2^-90 and of 2^101 and 2^118 (products with the keys stay finite), the scale making up for it."""
+    c = Case([260], [T], T, 10, 2, 128, 64, seed=21)
+    f = float(2.0 ** power)
+    c.Q = (c.Q.float() * f).bfloat16()
+    scale = float(np.float32(128 ** -0.5 / f))
+    c.check(c.run(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("T,new", [(2, [0, 1, 2, 0]), (200, [0, 3, 200, 1])])
+def test_rows_past_short_requests_where_most_of_the_gpu_is_idle(T, new):
+    """A plan for long requests, a call with short ones: CTAs without work share in writing the zero rows."""
+    c = Case([0, 5, 40, 130], new, T, 10, 2, 64, 16, seed=22)
+    att = w12.KV4Attention(4, T, 10, 2, 64, 16, (len(c.table[0])) * 16)
+    out = torch.full((4, T, 10, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+    st = new_status()
+    c.check(c.run(att=att, out=out, status=st))
+    assert status_value(st) == 0
+
+
 @pytest.mark.parametrize("T", [1, 16, 40])
 def test_an_expired_wait_is_reported_and_the_next_call_is_right(T):
     """With a 1 us bound a wait may give up (W12_ERR_TIMEOUT); the call ends, and after

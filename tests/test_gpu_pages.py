@@ -150,3 +150,15 @@ def test_binding_refusals():
     with pytest.raises(w12.W12Error) as e:
         bad.reserve(i, i, 4)
     assert e.value.code == 2
+
+
+def test_positions_past_2_to_the_31():
+    """A request that grows over position 2^31: slots of its last held page, then of the page it takes."""
+    held, P = 1 << 24, 128
+    table = torch.zeros((1, held + 2), dtype=torch.int32, device="cuda")
+    pages = w12.PageTable(table, to_dev_i32([held]), to_dev_i32([1, 0]), to_dev_i32([1]), P)
+    st = new_status()
+    slots = pages.reserve(to_dev_i32([2 ** 31 - 4]), to_dev_i32([8]), 9, status=st)
+    assert status_value(st) == 0
+    assert slots.tolist() == [[124, 125, 126, 127, 128, 129, 130, 131, -1]]
+    assert pages.used.item() == held + 1 and pages.n_free.item() == 0 and table[0, held].item() == 1
