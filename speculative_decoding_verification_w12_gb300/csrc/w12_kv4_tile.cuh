@@ -2,8 +2,8 @@
 // trees, prompt chunks): 128-row tiles on the tensor memory.
 //
 // The floor is the tensor pipe (1024 cycles a tile and block at d = 128), or HBM for a
-// single tile of rows. 4 trees of 64 nodes over 32768 tokens: 191 us, 0.90 PFLOP/s of
-// the 320 rows, 46 % of the measured bf16 rate; 16 blocks of 16 over 8192: 78.6 us, 28 % of
+// single tile of rows. 4 trees of 64 nodes over 32768 tokens: 189 us, 0.91 PFLOP/s of
+// the 320 rows, 46 % of the measured bf16 rate; 16 blocks of 16 over 8192: 77.3 us, 28 % of
 // either bound; prompt chunk 2 x 2048 (d 64): 134 us. A block takes 2150 cycles of a
 // CTA: the softmax and restore warps (two of each a scheduler) issue 49 % of the slots
 // and wait on one another's and on tensor-memory latencies for the rest.
@@ -14,8 +14,8 @@
 //   raw pages -> shared memory   one bulk copy a page (warp 0)
 //   codes -> fp16 K and V tiles  eight warps, four for each; a thread restores one row
 //   S = Q K^T                    tcgen05.mma, D in TMEM, two buffers (warp 1)
-//   P = exp2(S - M)              two warpgroups, one a 64-key half of the block; P
-//                                over its half's first 32 S columns as fp16 pairs
+//   P = exp2(S - M)              two warpgroups, one a 64-key part of the block; P
+//                                over its part's first 32 S columns as fp16 pairs
 //   O_h += P_h V_h               tcgen05.mma, A = P from TMEM, V MN-major (warp 2)
 //
 // Operands are fp16 (2^-11 relative) rather than bf16 (2^-8): restored values
@@ -89,7 +89,13 @@ constexpr uint32_t kWaitHintNs = 10000;  // asleep on a barrier between looks at
 
 template <int kD>
 struct TileCfg {
-  static constexpr int kThreads = 640;     // warps 0-3 copy and issue, 4-11 softmax, 12-19 restore
+  // Parts of a block's keys with softmax warps, a maximum and an O of their own. (Four at
+  // d = 64, where O has room: 16 softmax warps at 72 registers, prompt chunk 146 us for 134.)
+  static constexpr int kParts = 2;
+  static constexpr int kPart = 128 / kParts;              // keys of a part
+  static constexpr int kSoft = 4 * kParts;                // softmax warps, from warp 4 on
+  static constexpr int kRest = 4 + kSoft;                 // eight restore warps from here; 0-3 copy, issue, plan
+  static constexpr int kThreads = (kRest + 8) * 32;
   static constexpr uint32_t kHalf = 128u * 128u;       // 128 rows x 64 fp16, 128-byte swizzle
   static constexpr uint32_t kTile = kHalf * (kD / 64);
   static constexpr uint32_t kRaw = uint32_t(kKeys) * (kD + 8);
@@ -99,20 +105,21 @@ struct TileCfg {
   static constexpr uint32_t kKOff = kTile;
   static constexpr uint32_t kVOff = kKOff + kStages * kTile;
   static constexpr uint32_t kRawOff = kVOff + kStages * kTile;
-  static constexpr uint32_t kXchOff = kRawOff + kRawStages * kRaw;  // (m, l) of the two halves
-  static constexpr uint32_t kQxOff = kXchOff + 2 * 128 * 8;         // [2][128] powers of two of Q rows
+  static constexpr uint32_t kXchOff = kRawOff + kRawStages * kRaw;  // (m, l) of the parts
+  static constexpr uint32_t kQxOff = kXchOff + kParts * 128 * 8;         // [2][128] powers of two of Q rows
   // Exponents of the restored tiles, by block modulo 4 and 32 keys: (c 2^(e - 8), f, 2^-f, -).
   // Four deep: K of block j + 2 may be restored while the softmax of block j still reads.
   static constexpr int kExpRing = 4;
   static constexpr uint32_t kExpOff = kQxOff + 2 * 128 * 4;
   static constexpr uint32_t kBarOff = kExpOff + kExpRing * 4 * 16;
-  static constexpr uint32_t kRunOff = kBarOff + 336;
+  static constexpr uint32_t kRunOff = kBarOff + 384;
   static constexpr uint32_t kSegOff = kRunOff + 512;
   static constexpr uint32_t kAncOff = kSegOff + 256;                // [2][128] sets, then 128 words
   static constexpr uint32_t kSmem = kAncOff + 2 * 128 * 16 + 512 + 1024;  // 1024: alignment slack
   static_assert(kSmem <= 232448, "shared memory of a CTA");
-  // TMEM columns: S of even and odd blocks, O of the two key halves.
-  static constexpr uint32_t kS0 = 0, kS1 = 128, kOA = 256, kOB = 256 + kD, kCols = 512;
+  // TMEM columns: S of even and odd blocks, O of the parts (kD columns each).
+  static constexpr uint32_t kS0 = 0, kS1 = 128, kO = 256, kCols = 512;
+  static_assert(kO + kParts * kD <= kCols, "tensor memory");
 };
 
 // Eight dims of a code word as fp16 values c + s q, c = z - 8 s. A nibble masked
@@ -261,14 +268,14 @@ __device__ __forceinline__ void ancestors_of(const int32_t* parents, int T, uint
   }
 }
 
-// Sixteen rows of a segment's Q (part of eight) into the swizzled fp16 Q tile, by one
-// warp: each over a power of two 2^ra[row] that brings it below 2^10, so that
+// A softmax warp's share of a segment's Q rows into the swizzled fp16 Q tile: each over a power of two 2^ra[row] that brings it below 2^10, so that
 // c 2^(e - 8) and 2^(ra + 8) have room up to the largest values. A row with NaN or
 // infinities stays one.
 template <int kD>
-__device__ __forceinline__ void load_q(const Params& p, const Seg& s, int part, uint8_t* tile, int* ra) {
-  constexpr int kLanes = kD / 8, kStep = 32 / kLanes, kN = 16 / kStep;  // lanes a row, rows a load, loads
-  const int lane = threadIdx.x & 31, c = lane % kLanes, r0 = part * 16 + lane / kLanes;
+__device__ __forceinline__ void load_q(const Params& p, const Seg& s, int share, uint8_t* tile, int* ra) {
+  constexpr int kRows = 128 / TileCfg<kD>::kSoft;
+  constexpr int kLanes = kD / 8, kStep = 32 / kLanes, kN = kRows / kStep;  // lanes a row, rows a load, loads
+  const int lane = threadIdx.x & 31, c = lane % kLanes, r0 = share * kRows + lane / kLanes;
   const int R = s.n * p.G;
   const uint16_t* q = p.Q + s.b * p.q_b + int64_t(s.h) * p.G * p.q_h + c * 8;
   int rr = s.tile * 128 + r0, tok = rr / p.G, hh = rr - tok * p.G;
@@ -312,8 +319,8 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   uint64_t* v_full = k_empty + C::kStages;
   uint64_t* v_empty = v_full + C::kStages;                              // P V of its block done
   uint64_t* s_full = v_empty + C::kStages;                              // [2] S of block i in buffer i % 2
-  uint64_t* p_full = s_full + 2;                                        // [2][2] P of block i, key half h
-  uint64_t* o_done = p_full + 4;                                        // [2] P V of block i (both halves) done
+  uint64_t* p_full = s_full + 2;                                        // [2][parts] P of block i, part h
+  uint64_t* o_done = p_full + 2 * C::kParts;                            // [2] P V of block i (all parts) done
   uint64_t* o_final = o_done + 2;                                       // P V of the segment's last block done
   uint64_t* o_free = o_final + 1;                                       // O of the segment read (one arrival a warp)
   uint64_t* q_full = o_free + 1;                                        // its Q stored (one arrival a warp)
@@ -329,7 +336,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   SegSlot* segs = reinterpret_cast<SegSlot*>(smem + C::kSegOff);
   uint4* ancs = reinterpret_cast<uint4*>(smem + C::kAncOff);
   int* qx = reinterpret_cast<int*>(smem + C::kQxOff);
-  static_assert((2 * C::kRawStages + 4 * C::kStages + 19) * 8 + 16 <= 336 && sizeof(RunSmem) <= 512, "carve-up");
+  static_assert((2 * C::kRawStages + 4 * C::kStages + 15 + 2 * C::kParts) * 8 + 16 <= 384 && sizeof(RunSmem) <= 512, "carve-up");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -348,13 +355,13 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       mbar_init(&o_done[k], 1);
       mbar_init(&drained[k], 1);
       mbar_init(&seg_full[k], 1);
-      mbar_init(&seg_empty[k], 8);
+      mbar_init(&seg_empty[k], C::kSoft);
       mbar_init(&anc_full[k], 1);
     }
-    for (int k = 0; k < 4; ++k) mbar_init(&p_full[k], 128);
+    for (int k = 0; k < 2 * C::kParts; ++k) mbar_init(&p_full[k], 128);
     mbar_init(o_final, 1);
-    mbar_init(o_free, 8);
-    mbar_init(q_full, 8);
+    mbar_init(o_free, C::kSoft);
+    mbar_init(q_full, C::kSoft);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -484,20 +491,20 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
             break;
           }
           const uint64_t vd = vd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
-          for (int h = 0; h < 2; ++h) {
-            if (!wait_all(&p_full[(gj & 1) * 2 + h], uint32_t(gj >> 1) & 1u)) {
+          for (int h = 0; h < C::kParts; ++h) {
+            if (!wait_all(&p_full[(gj & 1) * C::kParts + h], uint32_t(gj >> 1) & 1u)) {
               ok = false;
               break;
             }
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks) {
-                const uint64_t off = uint64_t((uint32_t(h) * 8192u + uint32_t(ks) * 2048u) >> 4);
-                mma_bf16_ts(tmem + (h ? C::kOB : C::kOA), sb + uint32_t(64 * h + 8 * ks), vd + off, idesc_o,
+              for (int ks = 0; ks < C::kPart / 16; ++ks) {
+                const uint64_t off = uint64_t((uint32_t(h * C::kPart) * 128u + uint32_t(ks) * 2048u) >> 4);
+                mma_bf16_ts(tmem + C::kO + uint32_t(h * kD), sb + uint32_t(C::kPart * h + 8 * ks), vd + off, idesc_o,
                             (j > 0 || ks > 0) ? 1u : 0u);
               }
-              if (h == 1) {
+              if (h == C::kParts - 1) {
                 tc_commit(&o_done[gj & 1]);
                 tc_commit(&v_empty[st]);
               }
@@ -551,11 +558,11 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       if (si == 0) zero_idle_rows<kD>(p);
       if (!more) break;
     }
-  } else if (warp >= 12) {
+  } else if (warp >= C::kRest) {
     // ------------------------------------------------------------ restore
-    // Warps 12-15 restore K, 16-19 V; thread i of each four has row i of the block.
-    const bool is_k = warp < 16;
-    const int i = (tid - 384) & 127;
+    // Four warps restore K, four V; thread i of each four has row i of the block.
+    const bool is_k = warp < C::kRest + 4;
+    const int i = tid & 127;
     uint64_t* fullb = is_k ? k_full : v_full;
     uint64_t* emptyb = is_k ? k_empty : v_empty;
     uint8_t* tiles = smem + (is_k ? C::kKOff : C::kVOff);
@@ -622,11 +629,12 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax
-    // Warps 4-7 take keys 0-63 of every block, warps 8-11 keys 64-127; thread
-    // (warp w, lane) owns row 32 (w % 4) + lane.
+    // Each four warps take a part of every block's keys; thread (warp w, lane) owns
+    // row 32 (w % 4) + lane.
     const int q = warp & 3, h = (warp - 4) >> 2, r = q * 32 + lane;
     const uint32_t lane_off = uint32_t(q * 32) << 16;
-    const uint32_t o_own = tmem + lane_off + (h ? C::kOB : C::kOA);
+    const uint32_t o_own = tmem + lane_off + C::kO + uint32_t(h * kD);
+    constexpr int kSoftThreads = C::kSoft * 32;
     float2* xch = reinterpret_cast<float2*>(smem + C::kXchOff);
     int base = 0, si = 0;
     auto store_q = [&](int slot) {
@@ -639,7 +647,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       const int sl = si & 1;
       const Seg& s = segs[sl].seg;  // read where it is used: registers are short
       const bool got = wait(&seg_full[sl], uint32_t(si >> 1) & 1u);
-      if (named_bar_any(1, 256, !got)) break;
+      if (named_bar_any(1, kSoftThreads, !got)) break;
       if (!segs[sl].more) break;
       const int R = s.n * p.G;
       const int rr = s.tile * 128 + r;
@@ -660,7 +668,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         limit = s.prefix + tok + 1;
       }
       float M = -INFINITY, l = 0.f;
-      const int n = s.j1 - s.j0, key0 = s.j0 * kKeys + 64 * h;
+      const int n = s.j1 - s.j0, key0 = s.j0 * kKeys + C::kPart * h;
       for (int i = 0; i < n && ok; ++i) {
         const int gi = base + i;
         const int kb = key0 + i * kKeys;
@@ -670,9 +678,9 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         }
         tc_fence_after();
         if (warp_live) {
-          const uint32_t sc = tmem + lane_off + ((gi & 1) ? C::kS1 : C::kS0) + uint32_t(64 * h);
-          const bool edge = limit - kb < 64;
-          uint32_t pk[32];
+          const uint32_t sc = tmem + lane_off + ((gi & 1) ? C::kS1 : C::kS0) + uint32_t(C::kPart * h);
+          const bool edge = limit - kb < C::kPart;
+          uint32_t pk[C::kPart / 2];
           float psum;
           // Rows that have seen nothing yet have no maximum to go by.
           bool look = __any_sync(0xFFFFFFFFu, M == -INFINITY);
@@ -681,11 +689,11 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
               // The maximum moves to this block's where that is larger; O and the sum follow.
               float mx = -INFINITY;
 #pragma unroll 1
-              for (int ch = 0; ch < 2; ++ch) {
+              for (int ch = 0; ch < C::kPart / 32; ++ch) {
                 uint32_t v[32];
                 tmem_ld32(sc + uint32_t(ch * 32), v);
                 tmem_ld_wait32(v);
-                const float4 ex = exps[(gi % C::kExpRing) * 4 + 2 * h + ch];
+                const float4 ex = exps[(gi % C::kExpRing) * 4 + C::kPart / 32 * h + ch];
                 if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
                 mx = fmaxf(mx, fmaf(block_max<32>(v), fmaxf(ex.x * up, 1.2e-38f), ex.y));
               }
@@ -705,10 +713,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
             bool over = false;
             psum = 0.f;
 #pragma unroll
-            for (int ch = 0; ch < 2; ++ch) {
+            for (int ch = 0; ch < C::kPart / 32; ++ch) {
               uint32_t v[32];
               tmem_ld32(sc + uint32_t(ch * 32), v);
-              const float4 ex = exps[(gi % C::kExpRing) * 4 + 2 * h + ch];
+              const float4 ex = exps[(gi % C::kExpRing) * 4 + C::kPart / 32 * h + ch];
               tmem_ld_wait32(v);
               if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
               const float sum = exp_pack_f16(v, fmaxf(ex.x * up, 1.2e-38f), ex.y - ref, pk + 16 * ch);
@@ -720,47 +728,57 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           }
           if (!ok) break;
           l += psum;
-          tmem_st16(sc, *reinterpret_cast<uint32_t(*)[16]>(&pk[0]));
-          tmem_st16(sc + 16u, *reinterpret_cast<uint32_t(*)[16]>(&pk[16]));
+#pragma unroll
+          for (int ch = 0; ch < C::kPart / 32; ++ch)
+            tmem_st16(sc + uint32_t(16 * ch), *reinterpret_cast<uint32_t(*)[16]>(&pk[16 * ch]));
           tmem_st_wait();
         }
         tc_fence_before();
-        mbar_arrive(&p_full[(gi & 1) * 2 + h]);
+        mbar_arrive(&p_full[(gi & 1) * C::kParts + h]);
       }
       // The last S of the segment is done, so Q makes room for the next segment's: its S
       // goes on under this epilogue.
       if (ok && __all_sync(0xFFFFFFFFu, wait(&seg_full[sl ^ 1], uint32_t((si + 1) >> 1) & 1u)) && segs[sl ^ 1].more)
         store_q(sl ^ 1);
-      // Epilogue: thread (h, r) joins the halves for dims (kD / 2) h .. of its row.
+      // Epilogue: thread (h, r) joins the parts for its share of its row's dims.
       const bool fin = __all_sync(0xFFFFFFFFu, ok && wait(o_final, uint32_t(si) & 1u));
-      if (named_bar_any(1, 256, !fin)) break;
+      if (named_bar_any(1, kSoftThreads, !fin)) break;
       tc_fence_after();
       xch[h * 128 + r] = make_float2(M, l);
-      named_bar_sync(1, 256);
-      const float2 other = xch[(1 - h) * 128 + r];
-      const float ma = h ? other.x : M, la = h ? other.y : l;
-      const float mb = h ? M : other.x, lb = h ? l : other.y;
-      M = fmaxf(ma, mb);
-      float wa = ma == M ? 1.f : fast_exp2(ma - M), wb = mb == M ? 1.f : fast_exp2(mb - M);
-      const float den = wa * la + wb * lb;
-      wa *= 256.f;  // V is held over 2^(f + 8)
-      wb *= 256.f;
+      named_bar_sync(1, kSoftThreads);
+      M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < C::kParts; ++k) M = fmaxf(M, xch[k * 128 + r].x);
+      float den = 0.f, wt[C::kParts];
+#pragma unroll
+      for (int k = 0; k < C::kParts; ++k) {
+        const float2 ml = xch[k * 128 + r];
+        const float f = ml.x == M ? 1.f : fast_exp2(ml.x - M);
+        den = fmaf(f, ml.y, den);
+        wt[k] = 256.f * f;  // V is held over 2^(f + 8)
+      }
+      constexpr int kDims = kD / C::kParts;
       const bool whole = s.whole();
       const float inv = !whole ? 1.f : den == 0.f ? 0.f : 1.f / den;
       uint32_t* out = reinterpret_cast<uint32_t*>(
-          p.O + ((int64_t(s.b) * p.T + tok) * p.Hq + int64_t(s.h) * p.G + hh) * kD + h * (kD / 2));
+          p.O + ((int64_t(s.b) * p.T + tok) * p.Hq + int64_t(s.h) * p.G + hh) * kD + h * kDims);
       float4* po = reinterpret_cast<float4*>(p.part_o) + (int64_t(blockIdx.x) * 2 + s.slot) * (kD / 4) * 128 + r;
       if (warp_live) {
 #pragma unroll
-        for (int ch = 0; ch < kD / 32; ++ch) {
-          uint32_t a[16], b[16];
-          tmem_ld16(tmem + lane_off + C::kOA + uint32_t(h * (kD / 2) + ch * 16), a);
-          tmem_ld16(tmem + lane_off + C::kOB + uint32_t(h * (kD / 2) + ch * 16), b);
-          tmem_ld_wait(a);
-          tmem_ld_wait(b);
+        for (int ch = 0; ch < kDims / 16; ++ch) {
           float o[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = (wa * __uint_as_float(a[k]) + wb * __uint_as_float(b[k])) * inv;
+          for (int k = 0; k < 16; ++k) o[k] = 0.f;
+#pragma unroll
+          for (int part = 0; part < C::kParts; ++part) {
+            uint32_t a[16];
+            tmem_ld16(tmem + lane_off + C::kO + uint32_t(part * kD + h * kDims + ch * 16), a);
+            tmem_ld_wait(a);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = fmaf(wt[part], __uint_as_float(a[k]), o[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] *= inv;
           if (valid && whole) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -774,7 +792,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           } else if (valid) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              po[(h * (kD / 8) + ch * 4 + k) * 128] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              po[(h * (kDims / 4) + ch * 4 + k) * 128] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
         }
       }
@@ -785,13 +803,13 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         if (h == 0 && valid) p.part_ml[(int64_t(blockIdx.x) * 2 + s.slot) * 128 + r] = make_float2(M, den);
         const int item = s.entry * p.Hkv + s.h;
         // (The barrier orders the CTA's stores before the one release, and its acquire before all loads.)
-        named_bar_sync(1, 256);
+        named_bar_sync(1, kSoftThreads);
         if (tid == 128) {
           const int add = s.j1 - s.j0;
           *merge_here = atomic_add_acq_rel_gpu(p.cnt + item, add) + add == s.nkb;
           if (*merge_here) p.cnt[item] = 0;
         }
-        named_bar_sync(1, 256);
+        named_bar_sync(1, kSoftThreads);
         if (*merge_here && valid) {
           const int c0 = run_of(run, s.x0), c1 = run_of(run, s.x0 + s.nkb - 1);
           const int first = run_start(run, c0) >= s.x0 ? 0 : 1;
@@ -813,7 +831,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           }
           const float scale = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll 1
-          for (int ch = 0; ch < kD / 32; ++ch) {  // 16 dims at a time
+          for (int ch = 0; ch < kDims / 16; ++ch) {  // 16 dims at a time
             float o[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) o[k] = 0.f;
@@ -823,7 +841,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
 #pragma unroll
               for (int u = 0; u < 3; ++u) {
                 const int64_t slot = slot_of(c + u);
-                const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * (kD / 4) + h * (kD / 8) + ch * 4) * 128 + r;
+                const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * (kD / 4) + h * (kDims / 4) + ch * 4) * 128 + r;
                 mx[u] = c + u <= c1 ? __ldcg(p.part_ml + slot * 128 + r).x : -INFINITY;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[u][k] = c + u <= c1 ? __ldcg(src + k * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
