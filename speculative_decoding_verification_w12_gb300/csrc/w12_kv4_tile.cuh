@@ -2,9 +2,9 @@
 // trees, prompt chunks): 128-row tiles on the tensor memory.
 //
 // The floor is the tensor pipe (1024 cycles a tile and block at d = 128), or HBM for a
-// single tile of rows. 4 trees of 64 nodes over 32768 tokens: 189 us, 0.91 PFLOP/s of
-// the 320 rows, 46 % of the measured bf16 rate; 16 blocks of 16 over 8192: 77.3 us, 28 % of
-// either bound; prompt chunk 2 x 2048 (d 64): 134 us. A block takes 2150 cycles of a
+// single tile of rows. 4 trees of 64 nodes over 32768 tokens: 204 us, 0.84 PFLOP/s of
+// the 320 rows, 43 % of the measured bf16 rate; 16 blocks of 16 over 8192: 82 us, 27 % of
+// either bound; prompt chunk 2 x 2048 (d 64): 140 us. A block takes 2300 cycles of a
 // CTA: the softmax and restore warps (two of each a scheduler) issue 49 % of the slots
 // and wait on one another's and on tensor-memory latencies for the rest.
 //
@@ -19,17 +19,17 @@
 //   O_h += P_h V_h               tcgen05.mma, A = P from TMEM, V MN-major (warp 2)
 //
 // Operands are fp16 (2^-11 relative) rather than bf16 (2^-8): restored values
-// (z - 8 s) + s q and P then add little that shows next to the output's own
+// z + s (q - 8) and P then add little that shows next to the output's own
 // rounding to bf16. Their range is kept by powers of two, which are exact: every
-// 32 keys (one restore warp) have an exponent e for K and f for V;
+// 32 keys (one restore warp) have an exponent e for K and f + 8 for V;
 // the tile holds K / 2^e and V / 2^(f + 8), and a row of Q is held over its own power
 // of two 2^a. With
 //   y_ij = c 2^(a_i + e_j) S_ij + f_j,       c = scale log2(e)
 // the weight that meets the scaled V is P = 2^(y - M), M a running maximum of y,
-// so what rounds to zero in P is below 2^-20 of what counts in the output; the
+// so what rounds to zero in P is below 2^-24 of what counts in the output; the
 // denominator sum of 2^(y - M) / 2^f_j is kept in fp32, and the output is 2^8 times
-// their quotient. Values far below the largest of their 32 keys become fp16
-// subnormals, an absolute error of at most 2^-20 of that largest value.
+// their quotient. Values that are more than 2^14 below the largest of their 32 keys
+// become fp16 subnormals, an absolute error of at most 2^-25 of that.
 //
 // The softmax takes 32 scores at a time and does not look for a block's maximum: it
 // uses the running M, and only if the 32 weights sum to more than 2^12 (the first
@@ -122,30 +122,30 @@ struct TileCfg {
   static_assert(kO + kParts * kD <= kCols, "tensor memory");
 };
 
-// Eight dims of a code word as fp16 values c + s q, c = z - 8 s. A nibble masked
-// into place is the fp16 subnormal q 2^-24, or q 2^-20 for the next four bits: slo,
-// shi hold s 2^24 and s 2^20, c2 holds c, in both halves. One operation to mask and
-// one to scale (q - 8 made exact first took one more and a masked-in exponent: trees
-// 214 us, blocks 87; so 203 and 84). c is a rounded fp16 number, 2^-12 relative at
-// most: next to the same rounding of the value itself that is a shift of the whole
-// row by less than its step / 2^8 unless z is beyond 16 steps.
-__device__ __forceinline__ uint4 restore_word(uint32_t w, uint32_t slo, uint32_t shi, uint32_t c2) {
+// Eight dims of a code word as fp16 values z + s (q - 8), s2 and z2 holding s and
+// z in both halves. A nibble in the lowest bits of fp16 1024 is 1024 + q, in the
+// next four 1024 + 16 q; both become q - 8 exactly, then one rounding. Two operations
+// instead of three would give (z - 8 s) + s q with z - 8 s rounded first (trees 189 us
+// for 204, blocks 77 for 82), but that shifts a whole row by up to 2^-11 of its largest
+// value: where one key has most of the weight, outputs near 0 came out 2 % off. For K
+// alone, as code of its own beside V's, it gains nothing (200, 88).
+__device__ __forceinline__ uint4 restore_word(uint32_t w, uint32_t s2, uint32_t z2) {
+  constexpr uint32_t k1024 = 0x64006400u, kM1032 = 0xE408E408u, kSixteenth = 0x2C002C00u, kM72 = 0xD480D480u;
   const uint32_t v = w >> 8;
   uint4 o;
-  o.x = hfma2(w & 0x000F000Fu, slo, c2);
-  o.y = hfma2(w & 0x00F000F0u, shi, c2);
-  o.z = hfma2(v & 0x000F000Fu, slo, c2);
-  o.w = hfma2(v & 0x00F000F0u, shi, c2);
+  o.x = hfma2(hadd2(and_or(w, 0x000F000Fu, k1024), kM1032), s2, z2);
+  o.y = hfma2(hfma2(and_or(w, 0x00F000F0u, k1024), kSixteenth, kM72), s2, z2);
+  o.z = hfma2(hadd2(and_or(v, 0x000F000Fu, k1024), kM1032), s2, z2);
+  o.w = hfma2(hfma2(and_or(v, 0x00F000F0u, k1024), kSixteenth, kM72), s2, z2);
   return o;
 }
 
-// Exponent of a power of two that no value of a row passes and that leaves s 2^24
-// inside fp16: |z| + 8 s < 2^e and s < 2^(e - 8). At least -92; that, too, for rows of
-// zeros and of values that are not finite. At most 134 (s < 2^126).
+// Exponent of a power of two that no value of a row passes: |z| + 8 s < 2^e, at
+// least -92; that, too, for rows of zeros and of values that are not finite. At most 129.
 __device__ __forceinline__ int row_exponent(uint32_t par) {
   const float half = fmaf(4.f, bf16_lo(par), 0.5f * fabsf(bf16_hi(par)));  // (the whole may pass the fp32 range)
-  const int e = int((__float_as_uint(half) >> 23) & 255u) - 125, es = int((par >> 7) & 255u) - 126 + 8;
-  return e > 129 ? -92 : max(max(e, es), -92);  // 130: inf or NaN
+  const int e = int((__float_as_uint(half) >> 23) & 255u) - 125;
+  return e > 129 ? -92 : max(e, -92);  // 130: inf or NaN
 }
 
 // 2^e for -126 <= e <= 127.
@@ -592,12 +592,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         const int e = __reduce_max_sync(0xFFFFFFFFu, past ? -92 : row_exponent(mine));
         const int f = is_k ? __reduce_max_sync(0xFFFFFFFFu, past ? -92 : row_exponent(vp)) - 8 : 0;
         const float down = pow2(8 - e) * 0x1p-8f;
-        uint32_t slo = 0u, shi = 0u, c2 = 0u;
+        uint32_t s2 = 0u, z2 = 0u;
         if (!past && (is_k || !odd)) {
-          const float sd = bf16_lo(mine) * down, cd = fmaf(-8.f, sd, bf16_hi(mine) * down);
-          slo = pack_f16x2(sd * 0x1p24f, sd * 0x1p24f);
-          shi = pack_f16x2(sd * 0x1p20f, sd * 0x1p20f);
-          c2 = is_k && odd ? 0x7E007E00u : pack_f16x2(cd, cd);
+          s2 = pack_f16x2(bf16_lo(mine) * down, bf16_lo(mine) * down);
+          z2 = is_k && odd ? 0x7E007E00u : pack_f16x2(bf16_hi(mine) * down, bf16_hi(mine) * down);
         }
         if (gj >= C::kStages && !__all_sync(0xFFFFFFFFu, wait(&emptyb[st], uint32_t((gj >> 1) - 1) & 1u))) {
           ok = false;
@@ -610,10 +608,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
 #pragma unroll
         for (int k = 0; k < kD / 32; ++k) {
           uint8_t* dst = tile + place.dst[k];
-          *reinterpret_cast<uint4*>(dst + place.word[0]) = restore_word(w[k].x, slo, shi, c2);
-          *reinterpret_cast<uint4*>(dst + place.word[1]) = restore_word(w[k].y, slo, shi, c2);
-          *reinterpret_cast<uint4*>(dst + place.word[2]) = restore_word(w[k].z, slo, shi, c2);
-          *reinterpret_cast<uint4*>(dst + place.word[3]) = restore_word(w[k].w, slo, shi, c2);
+          *reinterpret_cast<uint4*>(dst + place.word[0]) = restore_word(w[k].x, s2, z2);
+          *reinterpret_cast<uint4*>(dst + place.word[1]) = restore_word(w[k].y, s2, z2);
+          *reinterpret_cast<uint4*>(dst + place.word[2]) = restore_word(w[k].z, s2, z2);
+          *reinterpret_cast<uint4*>(dst + place.word[3]) = restore_word(w[k].w, s2, z2);
         }
         fence_proxy_async_smem();  // the tile before the MMAs read it, the raw stage before it is refilled
         __syncwarp();

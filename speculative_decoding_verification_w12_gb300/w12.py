@@ -629,7 +629,7 @@ class KV4Cache:
         if dt is None or V.dtype != K.dtype:
             raise TypeError("K and V must both be float32, bfloat16 or float16")
         ks, vs = K.stride(), V.stride()
-        if ks[2] != 1 or vs[2] != 1 or not (K.is_cuda and V.is_cuda):
+        if n and (ks[2] != 1 or vs[2] != 1) or not (K.is_cuda and V.is_cuda):
             raise ValueError("K and V must be CUDA tensors with a contiguous last dimension")
         if slots.numel() != n:
             raise ValueError("one slot for each row of K")

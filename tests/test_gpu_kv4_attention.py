@@ -408,6 +408,27 @@ def test_rows_past_short_requests_where_most_of_the_gpu_is_idle(T, new):
     assert status_value(st) == 0
 
 
+@pytest.mark.parametrize("T,d", [(1, 128), (17, 128), (17, 64)])
+def test_rows_that_see_one_key_return_its_values(T, d):
+    """The first token of an empty cache sees itself alone: every value of its key, those
+    near 0 beside large ones among them, comes back to the roundings of that value."""
+    c = Case([0] * 24, [T] * 24, T, 8, 2, d, 64, seed=23, std=3.0)
+    out = c.run()
+    c.check(out)
+    out = out[:, 0].float().cpu().numpy().astype(np.float64).reshape(24, 2, 4, d)
+    V = np.stack([v[0] for v in c.V])[:, :, None]
+    assert (np.abs(out - V) <= np.abs(V) * (3 * U + 2.0 ** -12)).all()
+
+
+def test_append_of_no_rows():
+    c = Case([3], [1], 1, 2, 1, 64, 16, seed=24)
+    before = c.cache.pool.clone()
+    none = torch.from_numpy(np.zeros((0, 1, 64), dtype=np.float32)).cuda()
+    for rows in (none, none.transpose(1, 2).contiguous().transpose(1, 2)):
+        c.cache.append(rows, rows, torch.empty(0, dtype=torch.int32, device="cuda"))
+    assert torch.equal(c.cache.pool, before)
+
+
 @pytest.mark.parametrize("T", [1, 16, 40])
 def test_an_expired_wait_is_reported_and_the_next_call_is_right(T):
     """With a 1 us bound a wait may give up (W12_ERR_TIMEOUT); the call ends, and after
