@@ -2,8 +2,8 @@
 // short blocks): streams the codes and multiplies them in registers.
 //
 // The floor is HBM: d + 8 bytes a (key, kv head) against at most 16 rows of work.
-// 64 requests of 2048 to 8192 tokens (40 q / 8 kv heads x 128, 332 MB): 92.6 us, 3.6
-// TB/s, 53 % of a copy's rate. What bounds it is the issue of about 340 instructions a
+// 64 requests of 2048 to 8192 tokens (40 q / 8 kv heads x 128, 332 MB): 96.4 us, 3.4
+// TB/s, 51 % of a copy's rate. What bounds it is the issue of about 350 instructions a
 // 16-key group by seven warps a CTA, two CTAs an SM (57 % of the issue slots, the logic
 // pipe 54 % busy): registers (127 a thread) allow no more warps, and nine a CTA at 96
 // registers spill and take 106 us.
@@ -16,16 +16,16 @@
 // 8-wide side:
 //   S^T[16 keys, rows]  = K Q^T:  A = K codes, B = Q
 //   O^T[16 dims, rows] += V^T P^T: A = V codes, B = P
-// Codes are never scaled: masked into place, a nibble q is the fp16 subnormal
-// q 2^-24 (or q 2^-20, the nibble above it), exact and at full rate as an operand.
-// With z + s (q - 8) = (z - 8 s) + s q
+// Codes are never scaled. A nibble of K, masked into place, is the fp16 subnormal q 2^-24
+// (or q 2^-20, the nibble above it) as it stands; one of V is made q - 8. With
+// z + s (q - 8) = (z - 8 s) + s q
 //   score = c 2^a (s (q^.q) + (z - 8 s) sum(q^)),   c = scale log2(e)
-//   o     = sum p~ q + sum (p z - 8 p~),            p~ = fp16(p s)
-// with both products exact up to fp32 accumulation: the one rounding is p~ (2^-11
-// relative, and times q - 8 only, because -8 p~ takes the rounded p~). The powers of
-// two of the nibbles' places are made up for in Q (even pairs of dims times 16) and
-// in the epilogue. A row of Q is held as q^ = q / 2^a, a power of two that keeps it
-// in the fp16 range.
+//   o     = sum p~ (q - 8) + sum p~ z/s,            p~ = fp16(p s)
+// with products exact: the one rounding is p~, which stands for the weight p~/s of the
+// whole value (2^-11 relative; with p z in place of p~ z/s the rounding would show where
+// the two cancel). The powers of two of the K nibbles' places are made up for in Q (even
+// pairs of dims times 16). A row of Q is held as q^ = q / 2^a, a power of two that keeps
+// it in the fp16 range.
 //
 // Layout of the 16-key group: lane (g, t) = (lane / 4, lane % 4). K: key phi(g)
 // (and 8 + phi(g)), dims (d/4) t ..: one 16-byte load per key gives all its A
@@ -34,11 +34,11 @@
 // 0 5 2 7 1 4 3 6, chosen with the layout's swapped halves so that both kinds of
 // loads are free of bank conflicts.
 //
-// Weights are p = 2^(score - M). M follows the maximum of score + f, 2^f a power of
-// two that bounds the key's V row, so that p~ stays inside fp16 and what it rounds
-// to zero is below 2^-24 of what counts in o. It moves only when a p~ passes 2^10
-// (or p itself 2^100, which V rows of zeros allow): one vote a group, rescaling
-// is rare.
+// Weights are p = 2^(score - M). M follows the maximum of score + f - 8, 2^f a power of
+// two that bounds the key's V row, so that p~ stays inside fp16 (2^5 where it is
+// largest) and what it rounds to zero is below 2^-28 of what counts in o. It moves only
+// when a p~ passes 2^14 (or p itself 2^112, which V rows of zeros allow): one vote a
+// group, rescaling is rare.
 #pragma once
 
 #include "w12_attn_dev.cuh"
@@ -72,16 +72,34 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The four nibbles of both 16-bit halves of w as fp16 pairs: q 2^-24 in o[0] and
-// o[2], q 2^-20 in o[1] and o[3]. Five operations a word (with q - 8 restored
-// exactly it was nine, and the kernel 101 us where it now takes 94, 64 requests of
-// 8192 tokens).
-__device__ __forceinline__ void codes_of(uint32_t w, uint32_t (&o)[4]) {
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The four nibbles of both 16-bit halves of a K word as fp16 pairs: q 2^-24 in o[0]
+// and o[2], q 2^-20 in o[1] and o[3]. Five operations a word. (The products of
+// subnormal operands are summed with up to 10 bits less than others: 2^-13 of a step of
+// the row's scale, far inside what a score's operands are rounded by.)
+__device__ __forceinline__ void key_codes(uint32_t w, uint32_t (&o)[4]) {
   const uint32_t v = w >> 8;
   o[0] = w & 0x000F000Fu;
   o[1] = w & 0x00F000F0u;
   o[2] = v & 0x000F000Fu;
   o[3] = v & 0x00F000F0u;
+}
+
+// Those of a V word as q - 8, exactly: masked into place, a nibble is 1024 + q or
+// 1024 + 16 q. Nine operations a word; as subnormals the values of V came out up to
+// 2^-13 of a step off, which shows in an output that is 0 where one key has the weight.
+__device__ __forceinline__ void value_codes(uint32_t w, uint32_t (&o)[4]) {
+  constexpr uint32_t k1024 = 0x64006400u, kM1032 = 0xE408E408u, kSixteenth = 0x2C002C00u, kM72 = 0xD480D480u;
+  const uint32_t v = w >> 8;
+  o[0] = hadd2(and_or(w, 0x000F000Fu, k1024), kM1032);
+  o[1] = hfma2(and_or(w, 0x00F000F0u, k1024), kSixteenth, kM72);
+  o[2] = hadd2(and_or(v, 0x000F000Fu, k1024), kM1032);
+  o[3] = hfma2(and_or(v, 0x00F000F0u, k1024), kSixteenth, kM72);
 }
 
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
@@ -338,8 +356,8 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
 #pragma unroll
         for (int i = 0; i < kKW; ++i) {
           uint32_t a[4], b[4];
-          codes_of(ka[i], a);
-          codes_of(kb[i], b);
+          key_codes(ka[i], a);
+          key_codes(kb[i], b);
 #pragma unroll
           for (int nt = 0; nt < kNT; ++nt) {
             mma16816(x[nt], a[0], b[0], a[1], b[1], q[nt][4 * i], q[nt][4 * i + 1]);
@@ -382,8 +400,8 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
               up = 0x1p40f;
               low = 0x1p-40f;
             }
-            fa = fmaxf(fa, lift - 100.f);
-            fb = fmaxf(fb, lift - 100.f);
+            fa = fmaxf(fa, lift - 100.f) - 8.f;
+            fb = fmaxf(fb, lift - 100.f) - 8.f;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -426,31 +444,38 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
             l2[nt][1] = e[nt][1] + e[nt][3];
             sum += l2[nt][0] + l2[nt][1];
           }
-          if (move || !__any_sync(0xFFFFFFFFu, most > 1024.f || sum > 1.2676506e30f)) break;
+          if (move || !__any_sync(0xFFFFFFFFu, most > 16384.f || sum > 0x1p112f)) break;
           move = true;
         }
-        const float vza = bf16_hi(vpa) * low, vzb = bf16_hi(vpb) * low;
+        // A key adds p~ z/s, or p z where |z| >= 16 s (z/s may not be there).
+        const float ta = bf16_hi(vpa) * rcp(bf16_lo(vpa)), tb = bf16_hi(vpb) * rcp(bf16_lo(vpb));
+        const bool ina = fabsf(ta) < 16.f, inb = fabsf(tb) < 16.f;
+        const float k1a = ina ? ta : 0.f, k2a = ina ? 0.f : bf16_hi(vpa) * low;
+        const float k1b = inb ? tb : 0.f, k2b = inb ? 0.f : bf16_hi(vpb) * low;
         uint32_t pb[kNT][2];
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-          float z0 = e[nt][0] * vza, z1 = e[nt][1] * vza, z2 = e[nt][2] * vzb, z3 = e[nt][3] * vzb;
+          const uint32_t hd = edge ? hidden >> (4 * nt) : 0u;
           if (edge) {  // parameters in masked places may be anything
-            const uint32_t hd = hidden >> (4 * nt);
-            if (hd & 1u) w[nt][0] = z0 = 0.f;
-            if (hd & 2u) w[nt][1] = z1 = 0.f;
-            if (hd & 4u) w[nt][2] = z2 = 0.f;
-            if (hd & 8u) w[nt][3] = z3 = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((hd >> i) & 1u) w[nt][i] = 0.f;
           }
           l[nt][0] += l2[nt][0];
           l[nt][1] += l2[nt][1];
-          zs[nt][0] += z0 + z2;
-          zs[nt][1] += z1 + z3;
           const uint32_t ra = pack_f16x2(w[nt][0], w[nt][1]), rb = pack_f16x2(w[nt][2], w[nt][3]);
           pb[nt][0] = transpose8x8(ra);
           pb[nt][1] = transpose8x8(rb);
           const float2 fa = unpack_f16x2(ra), fb = unpack_f16x2(rb);  // the weights as they are multiplied
-          zs[nt][0] = fmaf(-8.f, fa.x + fb.x, zs[nt][0]);
-          zs[nt][1] = fmaf(-8.f, fa.y + fb.y, zs[nt][1]);
+          float z[4] = {fmaf(fa.x, k1a, e[nt][0] * k2a), fmaf(fa.y, k1a, e[nt][1] * k2a),
+                        fmaf(fb.x, k1b, e[nt][2] * k2b), fmaf(fb.y, k1b, e[nt][3] * k2b)};
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((hd >> i) & 1u) z[i] = 0.f;
+          }
+          zs[nt][0] += z[0] + z[2];
+          zs[nt][1] += z[1] + z[3];
         }
         // V: keys phi(2t), phi(2t + 1) and 8 further, dims (d/8) g ..
         const uint8_t* vc = pg + P * (kD / 2) + r0 * (kD / 2);
@@ -469,10 +494,10 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
           const uint32_t lo0 = __byte_perm(v[0][e], v[1][e], 0x5410), hi0 = __byte_perm(v[0][e], v[1][e], 0x7632);
           const uint32_t lo1 = __byte_perm(v[2][e], v[3][e], 0x5410), hi1 = __byte_perm(v[2][e], v[3][e], 0x7632);
           uint32_t a0[4], a1[4], a2[4], a3[4];
-          codes_of(lo0, a0);
-          codes_of(hi0, a1);
-          codes_of(lo1, a2);
-          codes_of(hi1, a3);
+          value_codes(lo0, a0);
+          value_codes(hi0, a1);
+          value_codes(lo1, a2);
+          value_codes(hi1, a3);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -505,7 +530,7 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
 #pragma unroll
         for (int i = 0; i < kMT; ++i)
           *reinterpret_cast<float2*>(dst + i * 16) =
-              make_float2(fmaf(o[nt][i][e], i & 1 ? 0x1p20f : 0x1p24f, z), fmaf(o[nt][i][2 + e], i & 1 ? 0x1p20f : 0x1p24f, z));
+              make_float2(o[nt][i][e] + z, o[nt][i][2 + e] + z);
       }
     named_bar_sync(1, kComp);
     const bool whole = s.whole();

@@ -420,6 +420,23 @@ def test_rows_that_see_one_key_return_its_values(T, d):
     assert (np.abs(out - V) <= np.abs(V) * (3 * U + 2.0 ** -12)).all()
 
 
+@pytest.mark.parametrize("T,d", [(1, 128), (1, 64), (3, 128), (17, 128)])
+@pytest.mark.parametrize("centre", [0.0, 1.0, 40.0])
+def test_few_keys_of_large_spread(T, d, centre):
+    """Two or three keys a request, scores far apart: outputs are small where the values of
+    the key with the weight are, whatever the row's scale and centre."""
+    c = Case([1, 2] * 40, [T] * 80, T, 8, 2, d, 16, seed=25)
+    g = np.random.default_rng(26)
+    for b in range(80):
+        kv = (g.standard_normal((2, 1 + b % 2 + T, 2, d)) * 3).astype(np.float32)
+        kv[1] += np.float32(centre * 3)
+        c.cache.append(torch.from_numpy(kv[0]).cuda(), torch.from_numpy(kv[1]).cuda(), to_dev_i32(c.slots[b]))
+        c.K[b], c.V[b] = O.values(*O.quantise(kv[0])), O.values(*O.quantise(kv[1]))
+    # Weights of less than 2^-14 round with 2^-25 of the largest: left out of the comparison
+    # by scores that are no further apart than that.
+    c.check(c.run(scale=0.01), scale=float(np.float32(0.01)))
+
+
 def test_append_of_no_rows():
     c = Case([3], [1], 1, 2, 1, 64, 16, seed=24)
     before = c.cache.pool.clone()
