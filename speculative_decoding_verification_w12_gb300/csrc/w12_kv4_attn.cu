@@ -15,9 +15,9 @@ static bool shape_ok(int B, int T, int Hq, int Hkv, int head_dim, int page_size,
 
 // How a call is run: by T G, the rows a kv head has. Up to 8 rows go to the rows kernel
 // in one 8-row tile, up to 16 in two, more to 128-row tiles. 64 requests of up to 8192
-// tokens, us, rows kernel against tiles: 1 row 89 / 171, 5 rows 92 / 169, 8 rows 96 /
-// 169; 10 rows 233 / 261 (no short requests among them), 16 rows 181 / 170. One request
-// of 777 tokens, 10 rows: 13.7 / 19.9, so two 8-row tiles are kept up to 16.
+// tokens, us, rows kernel against tiles: 1 row 97 / 181, 5 rows 100 / 182, 8 rows 103 /
+// 180; 10 rows 255 / 278 (no short requests among them), 16 rows 190 / 181. One request
+// of 777 tokens, 10 rows: 13.7 / 20.0, so two 8-row tiles are kept up to 16.
 struct Plan {
   int kind;   // few rows: their 8-row tiles (1 or 2); 0: 128-row tiles
   int ntile, rows;

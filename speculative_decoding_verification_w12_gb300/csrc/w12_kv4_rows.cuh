@@ -2,10 +2,10 @@
 // short blocks): streams the codes and multiplies them in registers.
 //
 // The floor is HBM: d + 8 bytes a (key, kv head) against at most 16 rows of work.
-// 64 requests of 2048 to 8192 tokens (40 q / 8 kv heads x 128, 332 MB): 96.4 us, 3.4
-// TB/s, 51 % of a copy's rate. What bounds it is the issue of about 350 instructions a
-// 16-key group by seven warps a CTA, two CTAs an SM (57 % of the issue slots, the logic
-// pipe 54 % busy): registers (127 a thread) allow no more warps, and nine a CTA at 96
+// 64 requests of 2048 to 8192 tokens (40 q / 8 kv heads x 128, 332 MB): 100 us, 3.3
+// TB/s, 49 % of a copy's rate. What bounds it is the issue of about 380 instructions a
+// 16-key group by seven warps a CTA, two CTAs an SM (59 % of the issue slots, the logic
+// pipe 51 % busy): registers (128 a thread) allow no more warps, and nine a CTA at 96
 // registers spill and take 106 us.
 // A copy warp brings 128 keys at a time (their pages' blocks, one bulk copy
 // each) into a ring in shared memory; each of the other warps takes groups of

@@ -5,7 +5,7 @@
 // single tile of rows. 4 trees of 64 nodes over 32768 tokens: 204 us, 0.84 PFLOP/s of
 // the 320 rows, 43 % of the measured bf16 rate; 16 blocks of 16 over 8192: 82 us, 27 % of
 // either bound; prompt chunk 2 x 2048 (d 64): 140 us. A block takes 2300 cycles of a
-// CTA: the softmax and restore warps (two of each a scheduler) issue 49 % of the slots
+// CTA: the softmax and restore warps (two of each a scheduler) issue 51 % of the slots
 // and wait on one another's and on tensor-memory latencies for the rest.
 //
 // Work unit: 128 query rows of one (request, kv head), token-major, against one
