@@ -221,9 +221,10 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
     }
     grid_dep_launch();
     zero_idle_rows<kD>(p);
-    if (*abort_flag)
-      for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
-        mbar_wait(&full[i % C::kStages], uint32_t(i / C::kStages) & 1u, drain_limit_ns(lim));
+    // The CTA ends only with every copy landed, whatever the computing warps do: one of their
+    // waits may still expire. (They need all copies, so this costs a call nothing.)
+    for (int i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+      mbar_wait(&full[i % C::kStages], uint32_t(i / C::kStages) & 1u, drain_limit_ns(lim));
     return;
   }
 

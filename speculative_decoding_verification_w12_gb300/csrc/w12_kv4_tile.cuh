@@ -436,9 +436,10 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       }
     }
     if (lane == 0) grid_dep_launch();
-    if (*abort_flag)
-      for (int i = issued > C::kRawStages ? issued - C::kRawStages : 0; i < issued; ++i)
-        mbar_wait(&raw_full[i % C::kRawStages], uint32_t(i / C::kRawStages) & 1u, drain_limit_ns(lim));
+    // The CTA ends only with every copy landed, whatever the other warps do: one of their waits
+    // may still expire. (They need all copies, so this costs a call nothing.)
+    for (int i = issued > C::kRawStages ? issued - C::kRawStages : 0; i < issued; ++i)
+      mbar_wait(&raw_full[i % C::kRawStages], uint32_t(i / C::kRawStages) & 1u, drain_limit_ns(lim));
   } else if (warp == 1 || warp == 2) {
     // ---------------------------------------------------------------- MMA
     // The whole warp waits; one elected lane issues. (With the loop under one

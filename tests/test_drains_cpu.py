@@ -1,0 +1,43 @@
+"""A thread block may not end while a copy that it has requested can still land in its
+shared memory: the memory may be another block's by then. A wait of another warp can
+expire after the copying warp has issued its last copy, so the wait for the copies in
+flight has to stand on every path to that warp's end. Read from the sources: no run
+could show it without the race itself.
+"""
+import os
+import re
+
+import pytest
+
+from speculative_decoding_verification_w12_gb300 import build as B
+
+# The kernels that request copies: source, and the barriers that their copies complete on.
+COPIES = {"w12_kv4_rows.cuh": ["full"], "w12_kv4_tile.cuh": ["raw_full"], "w12_logprobs.cu": ["s.full"]}
+
+
+def enclosing(src, at):
+    """Heads of the blocks and single statements that hold position `at`, innermost first."""
+    heads, depth = [], 0
+    lines = src[:at].split("\n")
+    indent = len(lines[-1]) - len(lines[-1].lstrip())
+    for line in reversed(lines[:-1]):
+        text = line.strip()
+        if not text or text.startswith(("//", "#")):
+            continue
+        own = len(line) - len(line.lstrip())
+        if own < indent:
+            heads.append(text)
+            indent = own
+            depth += 1
+    return heads
+
+
+@pytest.mark.parametrize("source", sorted(COPIES))
+def test_copies_in_flight_are_waited_for_on_every_path(source):
+    src = open(os.path.join(B.CSRC, source)).read()
+    for bar in COPIES[source]:
+        drains = list(re.finditer(r"mbar_wait\(&" + re.escape(bar) + r"\[[^;]*drain_limit_ns", src))
+        assert drains, f"{source}: no wait for the copies of {bar}"
+        for m in drains:
+            heads = enclosing(src, m.start())
+            assert not [h for h in heads if "abort" in h or "failed" in h], heads
