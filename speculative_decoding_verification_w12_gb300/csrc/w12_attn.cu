@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile uint32_t* tmem_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile int* merge_here = reinterpret_cast<volatile int*>(misc + 2);  // this CTA merges the segment's item
+  volatile int* copied = reinterpret_cast<volatile int*>(misc + 3);      // [2]: K and V blocks requested
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = int(blockIdx.x) / P.ntile;
@@ -444,10 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (isK) grid_dep_launch();
-      if (*abort_flag) {
-        for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-          mbar_wait(&fullb[i % kStages], uint32_t(i / kStages) & 1u, drain_limit_ns(lim));
-      }
+      copied[isK ? 0 : 1] = issued;
     }
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------------ MMA
@@ -721,6 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   cta_sync();
+  // Only now is no wait left that could expire: after one, copies may be in flight still.
+  if (*abort_flag && lane == 0 && (warp == 0 || warp == 2)) {
+    uint64_t* fullb = warp == 0 ? kfull : vfull;
+    const int issued = copied[warp == 0 ? 0 : 1];
+    for (int i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
+      mbar_wait(&fullb[i % kStages], uint32_t(i / kStages) & 1u, drain_limit_ns(lim));
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(Cfg<kW12>::kThreads, 1)
   volatile uint32_t* ent_end = misc + 5;
   volatile int* pref_flag = reinterpret_cast<volatile int*>(misc + 6);
   volatile int* fast_flag = reinterpret_cast<volatile int*>(misc + 7);
+  volatile int* copied = reinterpret_cast<volatile int*>(misc + 8);  // units whose copies were requested
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -283,11 +284,7 @@ __global__ void __launch_bounds__(Cfg<kW12>::kThreads, 1)
         }
       }
       grid_dep_launch();
-      if (*abort_flag) {
-        // Let the copies already issued land before the CTA can exit.
-        for (int i = issued > S ? issued - S : 0; i < issued; ++i)
-          mbar_wait(&B.full[i % S], uint32_t(i / S) & 1u, drain_limit_ns(lim));
-      }
+      *copied = issued;
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------------ MMA
@@ -678,6 +675,10 @@ __global__ void __launch_bounds__(Cfg<kW12>::kThreads, 1)
   }
 
   cta_sync();
+  // Only now is no wait left that could expire: after one, copies may be in flight still.
+  if (*abort_flag && threadIdx.x == 0)
+    for (int i = *copied > S ? *copied - S : 0; i < *copied; ++i)
+      mbar_wait(&B.full[i % S], uint32_t(i / S) & 1u, drain_limit_ns(lim));
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::kTmemCols);

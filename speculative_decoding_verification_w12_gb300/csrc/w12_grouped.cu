@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(Cfg<kW12>::kThreads, 1)
   volatile int* pref_flag = reinterpret_cast<volatile int*>(misc + 6);
   volatile int* fast_flag = reinterpret_cast<volatile int*>(misc + 7);
   volatile int* glu_flag = reinterpret_cast<volatile int*>(misc + 8);
+  volatile int* copied = reinterpret_cast<volatile int*>(misc + 11);  // units whose copies were requested
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -442,15 +443,7 @@ __global__ void __launch_bounds__(Cfg<kW12>::kThreads, 1)
         }
       }
       grid_dep_launch();
-      if (*abort_flag) {
-        // Let the copies already issued land before the CTA can exit. The
-        // loop only stops at a stage boundary with every stage before it
-        // fully issued (weights and X).
-        for (int i = issued > S ? issued - S : 0; i < issued; ++i) {
-          mbar_wait(&B.full[i % S], uint32_t(i / S) & 1u, drain_limit_ns(lim));
-          mbar_wait(&B.full_x[i % S], uint32_t(i / S) & 1u, drain_limit_ns(lim));
-        }
-      }
+      *copied = issued;
     }
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------------ MMA
@@ -1025,6 +1018,14 @@ __global__ void __launch_bounds__(Cfg<kW12>::kThreads, 1)
   }
 
   cta_sync();
+  // Only now is no wait left that could expire: after one, copies may be in flight still.
+  // (The loop over the units stops at a stage boundary with every stage before it fully
+  // issued, weights and X.)
+  if (*abort_flag && threadIdx.x == 0)
+    for (int i = *copied > S ? *copied - S : 0; i < *copied; ++i) {
+      mbar_wait(&B.full[i % S], uint32_t(i / S) & 1u, drain_limit_ns(lim));
+      mbar_wait(&B.full_x[i % S], uint32_t(i / S) & 1u, drain_limit_ns(lim));
+    }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::kTmemCols);
