@@ -46,16 +46,21 @@ static Plan plan_of(int B, int T, int Hq, int Hkv, int d, int64_t max_len) {
   return q;
 }
 
-// Launch of one kernel with its shared memory (granted once a device).
+// Launch of one kernel with its shared memory (granted once a device). regs: registers a
+// thread that it counts on being launched with.
 template <typename Kernel>
 static cudaError_t launch(Kernel* kernel, bool (&ready)[64], int threads, int smem, const Params& p, int64_t grid,
-                          cudaStream_t stream) {
+                          cudaStream_t stream, int regs = 0) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev]) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes has;
+    e = cudaFuncGetAttributes(&has, kernel);
+    if (e != cudaSuccess) return e;
+    if (has.numRegs < regs) return cudaErrorInvalidConfiguration;  // (warps would wait for registers for good)
     ready[dev] = true;
   }
   cudaLaunchAttribute attr[1];
@@ -78,7 +83,8 @@ static cudaError_t launch_kind(int kind, const Params& p, int64_t grid, cudaStre
     return launch(kv4_attn_rows_kernel<kD, 1>, ready[1], RowsCfg<kD, 1>::kThreads, RowsCfg<kD, 1>::kSmem, p, grid, stream);
   if (kind == 2)
     return launch(kv4_attn_rows_kernel<kD, 2>, ready[2], RowsCfg<kD, 2>::kThreads, RowsCfg<kD, 2>::kSmem, p, grid, stream);
-  return launch(kv4_attn_tile_kernel<kD>, ready[0], TileCfg<kD>::kThreads, int(TileCfg<kD>::kSmem), p, grid, stream);
+  return launch(kv4_attn_tile_kernel<kD>, ready[0], TileCfg<kD>::kThreads, int(TileCfg<kD>::kSmem), p, grid, stream,
+                TileCfg<kD>::kLaunchRegs);
 }
 
 }  // namespace kv4_attn

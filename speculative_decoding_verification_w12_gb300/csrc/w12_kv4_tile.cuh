@@ -21,15 +21,20 @@
 // Operands are fp16 (2^-11 relative) rather than bf16 (2^-8): restored values
 // z + s (q - 8) and P then add little that shows next to the output's own
 // rounding to bf16. Their range is kept by powers of two, which are exact: every
-// 32 keys (one restore warp) have an exponent e for K and f + 8 for V;
-// the tile holds K / 2^e and V / 2^(f + 8), and a row of Q is held over its own power
+// 32 keys (one restore warp) have an exponent e for K and f + 8 for V, the largest
+// of their rows', as long as no row's own is more than 8 below it (of K: no row but
+// zeros); otherwise each of the 32 keys has its own. So a row keeps its values to 2^-11
+// relative or 2^-16 of its own bound, whatever stands beside it: a key of another
+// size, seen or masked, does not coarsen it. (Exponents a key for all would cost the
+// softmax two loads and three operations more for each pair of scores. As it is, finding
+// out takes trees 210.5 us where one exponent for any 32 rows takes 205, blocks 85 for 82.)
+// The tile holds K / 2^e and V / 2^(f + 8), and a row of Q is held over its own power
 // of two 2^a. With
 //   y_ij = c 2^(a_i + e_j) S_ij + f_j,       c = scale log2(e)
 // the weight that meets the scaled V is P = 2^(y - M), M a running maximum of y,
 // so what rounds to zero in P is below 2^-24 of what counts in the output; the
 // denominator sum of 2^(y - M) / 2^f_j is kept in fp32, and the output is 2^8 times
-// their quotient. Values that are more than 2^14 below the largest of their 32 keys
-// become fp16 subnormals, an absolute error of at most 2^-25 of that.
+// their quotient.
 //
 // The softmax takes 32 scores at a time and does not look for a block's maximum: it
 // uses the running M, and only if the 32 weights sum to more than 2^12 (the first
@@ -79,11 +84,22 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// Registers of the calling warp's threads, from here on; all warps of its warpgroup call it.
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // idesc_bf16 with fp16 A and B.
 __host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+constexpr int kSpread = 8;               // rows of a 32-key group may be this much smaller, as powers of two
 constexpr float kMost = 4096.f;          // sum of 32 weights above which the running maximum moves
 constexpr uint32_t kWaitHintNs = 10000;  // asleep on a barrier between looks at the abort flag and the clock
 
@@ -96,6 +112,12 @@ struct TileCfg {
   static constexpr int kSoft = 4 * kParts;                // softmax warps, from warp 4 on
   static constexpr int kRest = 4 + kSoft;                 // eight restore warps from here; 0-3 copy, issue, plan
   static constexpr int kThreads = (kRest + 8) * 32;
+  // Registers a thread from the role's start on, of the 96 that the launch has for each
+  // (checked there): the softmax, with code of its own for keys that have exponents of
+  // their own, spills at 96 (blocks 89 us for 85, prompt chunk 144.5 for 142). A
+  // warpgroup's warps change theirs together.
+  static constexpr int kLaunchRegs = 96, kPlainRegs = 88, kSoftRegs = 120, kRestRegs = 72;
+  static_assert(kPlainRegs * 4 + kSoftRegs * kSoft + kRestRegs * 8 <= kLaunchRegs * (kThreads / 32), "the launch's registers");
   static constexpr uint32_t kHalf = 128u * 128u;       // 128 rows x 64 fp16, 128-byte swizzle
   static constexpr uint32_t kTile = kHalf * (kD / 64);
   static constexpr uint32_t kRaw = uint32_t(kKeys) * (kD + 8);
@@ -107,11 +129,13 @@ struct TileCfg {
   static constexpr uint32_t kRawOff = kVOff + kStages * kTile;
   static constexpr uint32_t kXchOff = kRawOff + kRawStages * kRaw;  // (m, l) of the parts
   static constexpr uint32_t kQxOff = kXchOff + kParts * 128 * 8;         // [2][128] powers of two of Q rows
-  // Exponents of the restored tiles, by block modulo 4 and 32 keys: (c 2^(e - 8), f, 2^-f, -).
+  // Exponents of the restored tiles, by block modulo 4 and 32 keys: (c 2^(e - 8), f, 2^-f,
+  // whether the keys have their own), and those of the keys, (c 2^(e - 8), f), where they do.
   // Four deep: K of block j + 2 may be restored while the softmax of block j still reads.
   static constexpr int kExpRing = 4;
   static constexpr uint32_t kExpOff = kQxOff + 2 * 128 * 4;
-  static constexpr uint32_t kBarOff = kExpOff + kExpRing * 4 * 16;
+  static constexpr uint32_t kKeyOff = kExpOff + kExpRing * 4 * 16;
+  static constexpr uint32_t kBarOff = kKeyOff + kExpRing * 128 * 8;
   static constexpr uint32_t kRunOff = kBarOff + 384;
   static constexpr uint32_t kSegOff = kRunOff + 512;
   static constexpr uint32_t kAncOff = kSegOff + 256;                // [2][128] sets, then 128 words
@@ -211,6 +235,22 @@ __device__ __forceinline__ float exp_pack_f16(const uint32_t (&v)[32], float c, 
   }
   const float2 s = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
   return s.x + s.y;
+}
+
+// Scores of 32 keys with exponents of their own, (c 2^(e - 8), f) each in key: v becomes
+// y = score + f. Returns the sum of the keys' 2^(score - ref).
+__device__ __forceinline__ float key_scores(uint32_t (&v)[32], const float2* key, float up, float ref) {
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float4 x = reinterpret_cast<const float4*>(key)[k];
+    const float s0 = __uint_as_float(v[2 * k]) * fmaxf(x.x * up, 1.2e-38f);
+    const float s1 = __uint_as_float(v[2 * k + 1]) * fmaxf(x.z * up, 1.2e-38f);
+    sum += fast_exp2(s0 - ref) + fast_exp2(s1 - ref);
+    v[2 * k] = __float_as_uint(s0 + x.y);
+    v[2 * k + 1] = __float_as_uint(s1 + x.w);
+  }
+  return sum;
 }
 
 // A segment as warp 3 hands it to the softmax warps, two ahead at most.
@@ -333,6 +373,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   volatile int* merge_here = abort_flag + 1;
   RunSmem& rs = *reinterpret_cast<RunSmem*>(smem + C::kRunOff);
   float4* exps = reinterpret_cast<float4*>(smem + C::kExpOff);
+  float2* key_exps = reinterpret_cast<float2*>(smem + C::kKeyOff);
   SegSlot* segs = reinterpret_cast<SegSlot*>(smem + C::kSegOff);
   uint4* ancs = reinterpret_cast<uint4*>(smem + C::kAncOff);
   int* qx = reinterpret_cast<int*>(smem + C::kQxOff);
@@ -397,6 +438,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
 
   if (warp == 0) {
     // ------------------------------------------------------------- copies
+    fewer_registers<C::kPlainRegs>();
     Walk walk(run);
     Seg s;
     const int per = kKeys >> p.p_shift;
@@ -441,6 +483,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     for (int i = issued > C::kRawStages ? issued - C::kRawStages : 0; i < issued; ++i)
       mbar_wait(&raw_full[i % C::kRawStages], uint32_t(i / C::kRawStages) & 1u, drain_limit_ns(lim));
   } else if (warp == 1 || warp == 2) {
+    fewer_registers<C::kPlainRegs>();
     // ---------------------------------------------------------------- MMA
     // The whole warp waits; one elected lane issues. (With the loop under one
     // lane, descriptors pass from vector to uniform registers product by product.)
@@ -525,6 +568,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     __syncwarp();
     mbar_wait(&drained[is_s ? 0 : 1], 0, drain_limit_ns(lim));
   } else if (warp == 3) {
+    fewer_registers<C::kPlainRegs>();
     // ----------------------------------------------------------- segments
     // Finds the run's segments for the softmax warps, up to two ahead, with the
     // ancestors of their trees (7000 cycles a segment when every softmax warp walked
@@ -560,6 +604,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       if (!more) break;
     }
   } else if (warp >= C::kRest) {
+    fewer_registers<C::kRestRegs>();
     // ------------------------------------------------------------ restore
     // Four warps restore K, four V; thread i of each four has row i of the block.
     const bool is_k = warp < C::kRest + 4;
@@ -590,8 +635,21 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         for (int k = 0; k < kD / 32; ++k) w[k] = *reinterpret_cast<const uint4*>(src + place.at[k]);
         const bool past = j * kKeys + i >= s.keys;
         const bool odd = not_finite(vp);
-        const int e = __reduce_max_sync(0xFFFFFFFFu, past ? -92 : row_exponent(mine));
-        const int f = is_k ? __reduce_max_sync(0xFFFFFFFFu, past ? -92 : row_exponent(vp)) - 8 : 0;
+        // Exponents of this thread's row: its warp's, or its own where the warp's rows differ.
+        // (A row that does not count has none: past the keys, not finite, zeros of K.)
+        int e = row_exponent(mine), f = is_k ? row_exponent(vp) : e;
+        const int top = __reduce_max_sync(0xFFFFFFFFu, past ? -92 : e);
+        const bool apart =
+            __any_sync(0xFFFFFFFFu, !past && e < top - kSpread && !not_finite(mine) && (!is_k || (mine & 0x7FFF7FFFu)));
+        bool key_apart = apart;  // in K or in V (K warps)
+        if (!apart) e = top;
+        if (is_k) {
+          const int top_v = __reduce_max_sync(0xFFFFFFFFu, past ? -92 : f);
+          const bool apart_v = __any_sync(0xFFFFFFFFu, !past && f < top_v - kSpread && !odd);
+          if (!apart_v) f = top_v;
+          key_apart |= apart_v;
+        }
+        f -= 8;
         const float down = pow2(8 - e) * 0x1p-8f;
         uint32_t s2 = 0u, z2 = 0u;
         if (!past && (is_k || !odd)) {
@@ -604,7 +662,8 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         }
         // The K warps publish both exponents: the softmax then waits for K alone.
         if (is_k && lane == 0)
-          exps[(gj % C::kExpRing) * 4 + (i >> 5)] = make_float4(p.c * pow2(e - 8), float(f), pow2(-f), 0.f);
+          exps[(gj % C::kExpRing) * 4 + (i >> 5)] = make_float4(p.c * pow2(e - 8), float(f), pow2(-f), key_apart ? 1.f : 0.f);
+        if (is_k && key_apart) key_exps[(gj % C::kExpRing) * 128 + i] = make_float2(p.c * pow2(e - 8), float(f));
         uint8_t* tile = tiles + st * C::kTile;
 #pragma unroll
         for (int k = 0; k < kD / 32; ++k) {
@@ -627,6 +686,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       }
     }
   } else if (warp >= 4) {
+    more_registers<C::kSoftRegs>();
     // ------------------------------------------------------------ softmax
     // Each four warps take a part of every block's keys; thread (warp w, lane) owns
     // row 32 (w % 4) + lane.
@@ -681,51 +741,70 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
           const bool edge = limit - kb < C::kPart;
           uint32_t pk[C::kPart / 2];
           float psum;
+          const float4* own = exps + (gi % C::kExpRing) * 4 + C::kPart / 32 * h;
           // Rows that have seen nothing yet have no maximum to go by.
           bool look = __any_sync(0xFFFFFFFFu, M == -INFINITY);
-          for (;;) {
-            if (look) {
-              // The maximum moves to this block's where that is larger; O and the sum follow.
-              float mx = -INFINITY;
-#pragma unroll 1
-              for (int ch = 0; ch < C::kPart / 32; ++ch) {
-                uint32_t v[32];
-                tmem_ld32(sc + uint32_t(ch * 32), v);
-                tmem_ld_wait32(v);
-                const float4 ex = exps[(gi % C::kExpRing) * 4 + C::kPart / 32 * h + ch];
-                if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
-                mx = fmaxf(mx, fmaf(block_max<32>(v), fmaxf(ex.x * up, 1.2e-38f), ex.y));
-              }
-              const float factor = mx > M ? fast_exp2(M - mx) : 1.f;  // 0 while M = -inf
-              M = fmaxf(M, mx);
-              l *= factor;
-              if (i > 0) {
-                if (!__all_sync(0xFFFFFFFFu, wait(&o_done[(gi - 1) & 1], uint32_t((gi - 1) >> 1) & 1u))) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                rescale_row<kD>(o_own, factor);
-              }
-            }
-            const float ref = M == -INFINITY ? 0.f : M;
-            bool over = false;
+          if (!look) {
             psum = 0.f;
 #pragma unroll
             for (int ch = 0; ch < C::kPart / 32; ++ch) {
               uint32_t v[32];
               tmem_ld32(sc + uint32_t(ch * 32), v);
-              const float4 ex = exps[(gi % C::kExpRing) * 4 + C::kPart / 32 * h + ch];
+              const float4 ex = own[ch];
               tmem_ld_wait32(v);
               if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
-              const float sum = exp_pack_f16(v, fmaxf(ex.x * up, 1.2e-38f), ex.y - ref, pk + 16 * ch);
-              over |= sum > kMost;
+              const float sum = exp_pack_f16(v, fmaxf(ex.x * up, 1.2e-38f), ex.y - M, pk + 16 * ch);
+              look |= sum > kMost || ex.w != 0.f;
               psum = fmaf(sum, ex.z, psum);
             }
-            if (look || !__any_sync(0xFFFFFFFFu, over)) break;
-            look = true;
+            look = __any_sync(0xFFFFFFFFu, look);
           }
-          if (!ok) break;
+          if (look) {
+            const float2* key = key_exps + (gi % C::kExpRing) * 128 + C::kPart * h;
+            // The maximum moves to this block's where that is larger; O and the sum follow.
+            float mx = -INFINITY;
+#pragma unroll 1
+            for (int ch = 0; ch < C::kPart / 32; ++ch) {
+              uint32_t v[32];
+              tmem_ld32(sc + uint32_t(ch * 32), v);
+              tmem_ld_wait32(v);
+              const float4 ex = own[ch];
+              if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
+              float c = fmaxf(ex.x * up, 1.2e-38f), f = ex.y;
+              if (ex.w != 0.f) {
+                key_scores(v, key + 32 * ch, up, 0.f);
+                c = 1.f, f = 0.f;
+              }
+              mx = fmaxf(mx, fmaf(block_max<32>(v), c, f));
+            }
+            const float factor = mx > M ? fast_exp2(M - mx) : 1.f;  // 0 while M = -inf
+            M = fmaxf(M, mx);
+            l *= factor;
+            if (i > 0) {
+              if (!__all_sync(0xFFFFFFFFu, wait(&o_done[(gi - 1) & 1], uint32_t((gi - 1) >> 1) & 1u))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              rescale_row<kD>(o_own, factor);
+            }
+            const float ref = M == -INFINITY ? 0.f : M;
+            psum = 0.f;
+#pragma unroll
+            for (int ch = 0; ch < C::kPart / 32; ++ch) {
+              uint32_t v[32];
+              tmem_ld32(sc + uint32_t(ch * 32), v);
+              const float4 ex = own[ch];
+              tmem_ld_wait32(v);
+              if (edge) mask_block<32>(v, kb + 32 * ch, limit, anc, true);
+              float c = fmaxf(ex.x * up, 1.2e-38f), f = ex.y, w = ex.z;
+              if (ex.w != 0.f) {
+                psum += key_scores(v, key + 32 * ch, up, ref);
+                c = 1.f, f = w = 0.f;
+              }
+              psum = fmaf(exp_pack_f16(v, c, f - ref, pk + 16 * ch), w, psum);
+            }
+          }
           l += psum;
 #pragma unroll
           for (int ch = 0; ch < C::kPart / 32; ++ch)
