@@ -31,16 +31,17 @@
 // The tile holds K / 2^e and V / 2^(f + 8), and a row of Q is held over its own power
 // of two 2^a. With
 //   y_ij = c 2^(a_i + e_j) S_ij + f_j,       c = scale log2(e)
-// the weight that meets the scaled V is P = 2^(y - M), M a running maximum of y,
-// so what rounds to zero in P is below 2^-24 of what counts in the output; the
-// denominator sum of 2^(y - M) / 2^f_j is kept in fp32, and the output is 2^8 times
-// their quotient.
+// the weight that meets the scaled V is P = 2^(y - M), M a running maximum of y less
+// kTop: the largest weight was 2^8 when M was set, so weights are rounded to 2^-11
+// relative down to 2^-22 of it, and below that to 2^-33 of it (a key with nearly all of
+// the weight may add little, as the first of a long cache often does: the others keep
+// theirs). The denominator sum of 2^(y - M) / 2^f_j is kept in fp32, and the output is
+// 2^8 times their quotient.
 //
 // The softmax takes 32 scores at a time and does not look for a block's maximum: it
-// uses the running M, and only if the 32 weights sum to more than 2^12 (the first
+// uses the running M, and only if the 32 weights sum to more than kMost (the first
 // block, or scores that grow along the keys) does it find the maximum and do the
-// block again (S is still in TMEM). Weights then stay below 2^12, inside fp16, and
-// the largest was at least 1 when M was set. The two
+// block again (S is still in TMEM). Weights then stay inside fp16. The two
 // warpgroups keep separate maxima, sums and O accumulators, joined in the epilogue.
 //
 // A key whose V parameters are not finite gets V = 0 and K = NaN: its score is
@@ -100,7 +101,11 @@ __host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N) {
 }
 
 constexpr int kSpread = 8;               // rows of a 32-key group may be this much smaller, as powers of two
-constexpr float kMost = 4096.f;          // sum of 32 weights above which the running maximum moves
+// Least exponents of rows: the smallest ones still keep 2^-16 of their bound (2^-97 with
+// the smallest scale), and 2^24 keys of value rows of zeros their sum of weights 2^(8 - f).
+constexpr int kLeastK = -92, kLeastV = -88;
+constexpr float kTop = 8.f;              // the largest weight when the running maximum was set, as a power of two
+constexpr float kMost = 61440.f;         // sum of 32 weights above which it moves (fp16 ends at 65504)
 constexpr uint32_t kWaitHintNs = 10000;  // asleep on a barrier between looks at the abort flag and the clock
 
 template <int kD>
@@ -164,12 +169,12 @@ __device__ __forceinline__ uint4 restore_word(uint32_t w, uint32_t s2, uint32_t 
   return o;
 }
 
-// Exponent of a power of two that no value of a row passes: |z| + 8 s < 2^e, at
-// least -92; that, too, for rows of zeros and of values that are not finite. At most 129.
-__device__ __forceinline__ int row_exponent(uint32_t par) {
+// Exponent of a power of two that no value of a row passes: |z| + 8 s < 2^e, at least
+// `least`; that, too, for rows of zeros and of values that are not finite. At most 129.
+__device__ __forceinline__ int row_exponent(uint32_t par, int least) {
   const float half = fmaf(4.f, bf16_lo(par), 0.5f * fabsf(bf16_hi(par)));  // (the whole may pass the fp32 range)
   const int e = int((__float_as_uint(half) >> 23) & 255u) - 125;
-  return e > 129 ? -92 : max(e, -92);  // 130: inf or NaN
+  return e > 129 ? least : max(e, least);  // 130: inf or NaN
 }
 
 // 2^e for -126 <= e <= 127.
@@ -637,14 +642,14 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         const bool odd = not_finite(vp);
         // Exponents of this thread's row: its warp's, or its own where the warp's rows differ.
         // (A row that does not count has none: past the keys, not finite, zeros of K.)
-        int e = row_exponent(mine), f = is_k ? row_exponent(vp) : e;
-        const int top = __reduce_max_sync(0xFFFFFFFFu, past ? -92 : e);
+        int e = row_exponent(mine, is_k ? kLeastK : kLeastV), f = is_k ? row_exponent(vp, kLeastV) : e;
+        const int top = __reduce_max_sync(0xFFFFFFFFu, past ? kLeastK : e);
         const bool apart =
             __any_sync(0xFFFFFFFFu, !past && e < top - kSpread && !not_finite(mine) && (!is_k || (mine & 0x7FFF7FFFu)));
         bool key_apart = apart;  // in K or in V (K warps)
         if (!apart) e = top;
         if (is_k) {
-          const int top_v = __reduce_max_sync(0xFFFFFFFFu, past ? -92 : f);
+          const int top_v = __reduce_max_sync(0xFFFFFFFFu, past ? kLeastV : f);
           const bool apart_v = __any_sync(0xFFFFFFFFu, !past && f < top_v - kSpread && !odd);
           if (!apart_v) f = top_v;
           key_apart |= apart_v;
@@ -777,6 +782,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
               }
               mx = fmaxf(mx, fmaf(block_max<32>(v), c, f));
             }
+            mx -= kTop;
             const float factor = mx > M ? fast_exp2(M - mx) : 1.f;  // 0 while M = -inf
             M = fmaxf(M, mx);
             l *= factor;

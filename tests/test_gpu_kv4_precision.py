@@ -145,3 +145,34 @@ def test_a_dominant_key_with_a_small_value_row(T, Hq, Hkv, gap, value, apart):
     kv[1, at] *= np.float32(value)
     fill(c, 0, kv)
     check(c, c.run())
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 8, 2), (4, 8, 2), (5, 8, 2), (40, 8, 2)])
+@pytest.mark.parametrize("gap", [12, 16])
+def test_a_dominant_key_whose_values_are_zero_in_some_dims(T, Hq, Hkv, gap):
+    """Where the value row of a key `gap` nats above the others is zero, the output is the
+    others' alone; elsewhere it is that key's."""
+    d, L = 128, 3000
+    c = Case([L], [T], T, Hq, Hkv, d, 64, seed=37)
+    g = np.random.default_rng(38)
+    c.Q = torch.from_numpy((1 + 0.02 * g.standard_normal((1, T, Hq, d))).astype(np.float32)).cuda().bfloat16()
+    kv = g.standard_normal((2, L + T, Hkv, d)).astype(np.float32)
+    kv[0] *= 0.05
+    kv[0, 5] = np.float32(gap / d ** 0.5)
+    kv[1, 5] = np.float32(15 / 64) * (np.arange(d) % 2)
+    fill(c, 0, kv)
+    assert (c.V[0][5, :, ::2] == 0).all() and (c.V[0][5, :, 1::2] == 15 / 64).all()
+    check(c, c.run())
+    if T * Hq // Hkv <= 16:
+        return  # there p s (q - 8) and p z are summed apart in fp32: 2^-24 of the key's 8 s is 1e-3 of these
+    # The dims of the others alone, over all rows together.
+    K, V, q = c.K[0][:, 0], c.V[0][:, 0, ::2], c.Q[0, :, 0].float().cpu().numpy().astype(np.float64)
+    out = c.run()[0, :, 0, ::2].float().cpu().numpy().astype(np.float64)
+    err2 = ref2 = 0.0
+    for t in range(T):
+        s = d ** -0.5 * (K[:L + t + 1] @ q[t])
+        p = np.exp(s - s.max())
+        ref = p @ V[:L + t + 1] / p.sum()
+        err2 += ((out[t] - ref) ** 2).sum()
+        ref2 += (ref ** 2).sum()
+    assert (err2 / ref2) ** 0.5 <= NORM
