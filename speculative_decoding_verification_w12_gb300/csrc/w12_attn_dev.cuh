@@ -51,6 +51,13 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// l 2^d for d <= 0, where l may be as large as 2^d is small: in two factors, as 2^d alone
+// may be below the fp32 range.
+__device__ __forceinline__ float scaled_down(float l, float d) {
+  const float half = fast_exp2(0.5f * d);
+  return l * half * half;
+}
+
 // Two fp32 values -> one word of bf16 (round to nearest even): lo in bits 0..15.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

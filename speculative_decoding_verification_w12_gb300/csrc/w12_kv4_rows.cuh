@@ -48,6 +48,7 @@ namespace w12 {
 namespace kv4_attn {
 
 using attn_impl::pack_f16x2;
+using attn_impl::scaled_down;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -412,9 +413,9 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
                 mx = fmaxf(mx, m[nt][r]);
-                const float f = m[nt][r] == mx ? 1.f : ex2(m[nt][r] - mx);  // 0 while m = -inf
+                const float m_old = m[nt][r], f = m_old == mx ? 1.f : ex2(m_old - mx);  // 0 while m = -inf
                 m[nt][r] = mx;
-                l[nt][r] *= f * up;
+                l[nt][r] = scaled_down(l[nt][r], m_old == mx ? 0.f : m_old - mx) * up;
                 zs[nt][r] *= f;
 #pragma unroll
                 for (int i = 0; i < kMT; ++i) {
@@ -552,9 +553,9 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
 #pragma unroll
       for (int w = 0; w < C::kWarps; ++w) {
         const float2 ml = mlsm[w * C::kRows + r];
-        const float f = ml.x == M ? 1.f : ex2(ml.x - M);
+        const float d = ml.x == M ? 0.f : ml.x - M, f = ex2(d);
         const float2 v = *reinterpret_cast<const float2*>(osm + (w * C::kRows + r) * C::kPitch + at);
-        L = fmaf(f, ml.y, L);
+        L += scaled_down(ml.y, d);
         a = fmaf(f, v.x, a);
         b = fmaf(f, v.y, b);
       }
@@ -597,8 +598,9 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const float mn = fmaxf(M, ml[u].x);
-              const float fa = M == mn ? 1.f : ex2(M - mn), fb = ml[u].x == mn ? 1.f : ex2(ml[u].x - mn);
-              L = L * fa + fb * ml[u].y;
+              const float da = M == mn ? 0.f : M - mn, db = ml[u].x == mn ? 0.f : ml[u].x - mn;
+              const float fa = ex2(da), fb = ex2(db);
+              L = scaled_down(L, da) + scaled_down(ml[u].y, db);
               a = a * fa + fb * v[u].x;
               b = b * fa + fb * v[u].y;
               M = mn;

@@ -62,6 +62,7 @@ using attn_impl::pack_f16x2;
 using attn_impl::fast_exp2;
 using attn_impl::mask_block;
 using attn_impl::rescale_row;
+using attn_impl::scaled_down;
 using attn_impl::sdesc_mn_sw128;
 
 // mbar_try_wait with a time hint: the hardware may keep the thread asleep for about
@@ -104,6 +105,9 @@ constexpr int kSpread = 8;               // rows of a 32-key group may be this m
 // Least exponents of rows: the smallest ones still keep 2^-16 of their bound (2^-97 with
 // the smallest scale), and 2^24 keys of value rows of zeros their sum of weights 2^(8 - f).
 constexpr int kLeastK = -92, kLeastV = -88;
+// Exponent of a row of V below which keys have their own: 2^(score + f - M) may then be below
+// the fp32 range where 2^(score - M) is not (M may be of rows 2^134 larger).
+constexpr int kSmallV = -44;
 constexpr float kTop = 8.f;              // the largest weight when the running maximum was set, as a power of two
 constexpr float kMost = 61440.f;         // sum of 32 weights above which it moves (fp16 ends at 65504)
 constexpr uint32_t kWaitHintNs = 10000;  // asleep on a barrier between looks at the abort flag and the clock
@@ -121,7 +125,7 @@ struct TileCfg {
   // (checked there): the softmax, with code of its own for keys that have exponents of
   // their own, spills at 96 (blocks 89 us for 85, prompt chunk 144.5 for 142). A
   // warpgroup's warps change theirs together.
-  static constexpr int kLaunchRegs = 96, kPlainRegs = 88, kSoftRegs = 120, kRestRegs = 72;
+  static constexpr int kLaunchRegs = 96, kPlainRegs = 88, kSoftRegs = 112, kRestRegs = 80;
   static_assert(kPlainRegs * 4 + kSoftRegs * kSoft + kRestRegs * 8 <= kLaunchRegs * (kThreads / 32), "the launch's registers");
   static constexpr uint32_t kHalf = 128u * 128u;       // 128 rows x 64 fp16, 128-byte swizzle
   static constexpr uint32_t kTile = kHalf * (kD / 64);
@@ -644,13 +648,13 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         // (A row that does not count has none: past the keys, not finite, zeros of K.)
         int e = row_exponent(mine, is_k ? kLeastK : kLeastV), f = is_k ? row_exponent(vp, kLeastV) : e;
         const int top = __reduce_max_sync(0xFFFFFFFFu, past ? kLeastK : e);
-        const bool apart =
-            __any_sync(0xFFFFFFFFu, !past && e < top - kSpread && !not_finite(mine) && (!is_k || (mine & 0x7FFF7FFFu)));
+        const bool apart = __any_sync(0xFFFFFFFFu, !past && e < (is_k ? top - kSpread : max(top - kSpread, kSmallV)) &&
+                                                       !not_finite(mine) && (!is_k || (mine & 0x7FFF7FFFu)));
         bool key_apart = apart;  // in K or in V (K warps)
         if (!apart) e = top;
         if (is_k) {
           const int top_v = __reduce_max_sync(0xFFFFFFFFu, past ? kLeastV : f);
-          const bool apart_v = __any_sync(0xFFFFFFFFu, !past && f < top_v - kSpread && !odd);
+          const bool apart_v = __any_sync(0xFFFFFFFFu, !past && f < max(top_v - kSpread, kSmallV) && !odd);
           if (!apart_v) f = top_v;
           key_apart |= apart_v;
         }
@@ -783,9 +787,9 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
               mx = fmaxf(mx, fmaf(block_max<32>(v), c, f));
             }
             mx -= kTop;
-            const float factor = mx > M ? fast_exp2(M - mx) : 1.f;  // 0 while M = -inf
+            const float down = mx > M ? M - mx : 0.f, factor = fast_exp2(down);  // 0 while M = -inf
             M = fmaxf(M, mx);
-            l *= factor;
+            l = scaled_down(l, down);
             if (i > 0) {
               if (!__all_sync(0xFFFFFFFFu, wait(&o_done[(gi - 1) & 1], uint32_t((gi - 1) >> 1) & 1u))) {
                 ok = false;
@@ -837,9 +841,9 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
 #pragma unroll
       for (int k = 0; k < C::kParts; ++k) {
         const float2 ml = xch[k * 128 + r];
-        const float f = ml.x == M ? 1.f : fast_exp2(ml.x - M);
-        den = fmaf(f, ml.y, den);
-        wt[k] = 256.f * f;  // V is held over 2^(f + 8)
+        const float d = ml.x == M ? 0.f : ml.x - M;
+        den += scaled_down(ml.y, d);
+        wt[k] = 256.f * fast_exp2(d);  // V is held over 2^(f + 8)
       }
       constexpr int kDims = kD / C::kParts;
       const bool whole = s.whole();
@@ -909,7 +913,7 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
 #pragma unroll
             for (int u = 0; u < 3; ++u) {
               const float mn = fmaxf(Mx, ml[u].x);
-              L = L * (Mx == mn ? 1.f : fast_exp2(Mx - mn)) + ml[u].y * (ml[u].x == mn ? 1.f : fast_exp2(ml[u].x - mn));
+              L = scaled_down(L, Mx == mn ? 0.f : Mx - mn) + scaled_down(ml[u].y, ml[u].x == mn ? 0.f : ml[u].x - mn);
               Mx = mn;
             }
           }

@@ -176,3 +176,33 @@ def test_a_dominant_key_whose_values_are_zero_in_some_dims(T, Hq, Hkv, gap):
         err2 += ((out[t] - ref) ** 2).sum()
         ref2 += (ref ** 2).sum()
     assert (err2 / ref2) ** 0.5 <= NORM
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 8, 2), (5, 8, 2), (40, 8, 2)])
+@pytest.mark.parametrize("power", [40, 60, 80])
+def test_blocks_of_zero_values_beside_very_large_ones(T, Hq, Hkv, power):
+    """Runs of keys with most of the weight and value rows of zeros, beside value rows of
+    2^power: their weight stays in the denominator."""
+    d, L = 128, 500
+    c = Case([L], [T], T, Hq, Hkv, d, 64, seed=39)
+    g = np.random.default_rng(40)
+    c.Q = torch.from_numpy((1 + 0.1 * g.standard_normal((1, T, Hq, d))).astype(np.float32)).cuda().bfloat16()
+    kv = g.standard_normal((2, L + T, Hkv, d)).astype(np.float32)
+    kv[0] *= 0.1
+    kv[0, 128:256] += np.float32(6 / d ** 0.5)
+    kv[1] *= np.float32(2.0 ** power)
+    kv[1, 128:256] = 0.0
+    fill(c, 0, kv)
+    check(c, c.run())
+
+
+@pytest.mark.parametrize("T,Hq,Hkv", [(1, 8, 2), (5, 8, 2), (40, 8, 2)])
+@pytest.mark.parametrize("power", [-60, -50, -44, -40])
+def test_small_values_of_varied_size(T, Hq, Hkv, power):
+    """Value rows of 2^power to 2^(power + 6), all of them small."""
+    c = Case([300], [T], T, Hq, Hkv, 128, 64, seed=41)
+    g = np.random.default_rng(42)
+    kv = g.standard_normal((2, 300 + T, Hkv, 128)).astype(np.float32)
+    kv[1] *= np.float32(2.0 ** power) * (np.float32(2.0) ** g.integers(0, 7, (300 + T, 1, 1))).astype(np.float32)
+    fill(c, 0, kv)
+    check(c, c.run())
