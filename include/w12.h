@@ -43,9 +43,13 @@
  *     The word is never cleared by the library.
  *   - `ws` / `ws_bytes`: caller-owned device workspace of at least the size
  *     the matching *_ws_bytes function returns, ZERO-FILLED before its first
- *     use; the library leaves it zeroed after every successful call, so it can
- *     be reused. After an error status, zero it again. Calls that share one
- *     workspace must not overlap in time (same stream, or synchronised).
+ *     use. A successful call leaves zeroed what the next one needs zeroed, so
+ *     calls of the same function, sizes and layout reuse it as it is (the rest
+ *     holds partial results). For another function or other sizes, and after an
+ *     error status, zero it again; w12_kv4_attention and w12_logprobs need that
+ *     after an error status only: calls of both, of any sizes, may take turns on
+ *     a workspace that is large enough for each. Calls that share one workspace
+ *     must not overlap in time (same stream, or synchronised).
  *   - Shapes: N % 128 == 0, K % 128 == 0, 1 <= M <= 256 rows.
  */
 #ifndef W12_H

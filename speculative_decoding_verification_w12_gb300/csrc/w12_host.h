@@ -48,6 +48,13 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 inline int64_t round_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
+// The workspaces of the paged attention and of the log probabilities begin with one int32
+// counter a CTA, zero between calls: of the item (row of logits) that begins in the CTA's
+// run and ends in another's, of which there is one at most. Their place does not depend on
+// the call, and partial results come after them, so calls of any shape of both may take
+// turns on one workspace.
+constexpr int kRunCounters = 1024;
+
 // Stream-K schedule shared by the GEMM launcher and its workspace sizing.
 struct GemmShape {
   int M, Mpad, N, K, KB, tiles, grid;

@@ -21,8 +21,8 @@ static bool shape_ok(int B, int T, int Hq, int Hkv, int head_dim, int page_size,
 struct Plan {
   int kind;   // few rows: their 8-row tiles (1 or 2); 0: 128-row tiles
   int ntile, rows;
-  int64_t grid, items;
-  size_t cnt, ml, o, total;  // workspace: counts, then partial (m, l), then partial O
+  int64_t grid;
+  size_t ml, o, total;  // workspace: kRunCounters counts, then partial (m, l), then partial O
 };
 
 static int sms_or_default() {
@@ -36,13 +36,12 @@ static Plan plan_of(int B, int T, int Hq, int Hkv, int d, int64_t max_len) {
   q.kind = R <= 8 ? 1 : R <= 16 ? 2 : 0;
   q.rows = q.kind ? 8 * q.kind : 128;
   q.ntile = int((R + q.rows - 1) / q.rows);
-  q.items = int64_t(B) * Hkv * q.ntile;
-  const int64_t units = q.items * ((max_len + kKeys - 1) / kKeys);
+  const int64_t units = int64_t(B) * Hkv * q.ntile * ((max_len + kKeys - 1) / kKeys);
   q.grid = std::min<int64_t>(units, int64_t(sms_or_default()) * (q.kind == 1 ? RowsCfg<128, 1>::kCtas : 1));
-  q.cnt = size_t(round_up(q.items * 4, 256));
+  q.grid = std::min<int64_t>(q.grid, kRunCounters);
   q.ml = size_t(round_up(q.grid * 2 * q.rows * 8, 256));
   q.o = size_t(q.grid) * 2 * q.rows * d * 4;
-  q.total = q.cnt + q.ml + q.o;
+  q.total = kRunCounters * 4 + q.ml + q.o;
   return q;
 }
 
@@ -145,8 +144,8 @@ int w12_kv4_attention(const uint16_t* Q, int64_t q_batch_stride, int64_t q_token
   p.rows_per_tile = pl.rows;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.cnt = reinterpret_cast<int32_t*>(w);
-  p.part_ml = reinterpret_cast<float2*>(w + pl.cnt);
-  p.part_o = reinterpret_cast<float*>(w + pl.cnt + pl.ml);
+  p.part_ml = reinterpret_cast<float2*>(w + kRunCounters * 4);
+  p.part_o = reinterpret_cast<float*>(w + kRunCounters * 4 + pl.ml);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(cache->head_dim == 128 ? kv4_attn::launch_kind<128>(pl.kind, p, pl.grid, s)
                                             : kv4_attn::launch_kind<64>(pl.kind, p, pl.grid, s));

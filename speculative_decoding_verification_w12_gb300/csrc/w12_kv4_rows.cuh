@@ -567,13 +567,13 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
       }
     }
     if (!whole) {
-      const int item = s.b * p.Hkv + s.h;
       // (The barrier orders the CTA's stores before the one release, and its acquire before all loads.)
       named_bar_sync(1, kComp);
       if (tid == 0) {
         const int add = s.j1 - s.j0;
-        *merge_here = atomic_add_acq_rel_gpu(p.cnt + item, add) + add == s.nkb;
-        if (*merge_here) p.cnt[item] = 0;
+        int32_t* cnt = p.cnt + run_of(run, s.x0);
+        *merge_here = atomic_add_acq_rel_gpu(cnt, add) + add == s.nkb;
+        if (*merge_here) *cnt = 0;
       }
       named_bar_sync(1, kComp);
       if (*merge_here) {

@@ -34,7 +34,7 @@ struct Params {
   int32_t* status;
   float* part_o;   // [grid][2 slots][rows][d]
   float2* part_ml; // [grid][2 slots][rows]
-  int32_t* cnt;    // [items]: units of the item done (zero between calls)
+  int32_t* cnt;    // [grid]: units done of the item that begins in the CTA's run and ends in another's (zero between calls)
   int B, T, Hq, Hkv, G, P, p_shift, max_pages, max_len, ntile, rows_per_tile;
   float c;         // scale * log2(e)
   uint64_t limit_ns;
@@ -135,7 +135,7 @@ __device__ __forceinline__ int run_of(const Run& r, int64_t x) { return int(((x 
 // One segment of a run.
 struct Seg {
   int64_t x0;         // first unit of the item
-  int entry, b, tile, h;
+  int b, tile, h;
   int nkb;            // blocks of the item
   int j0, j1;         // blocks of the segment
   int prefix, n;      // the request's tokens
@@ -167,7 +167,6 @@ struct Walk {
       base += units;
       ++entry;
     }
-    s.entry = entry;
     s.h = int((pos - base) / s.nkb);
     s.x0 = base + int64_t(s.h) * s.nkb;
     s.j0 = int(pos - s.x0);

@@ -889,13 +889,13 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
       if (lane == 0) mbar_arrive(o_free);
       if (!whole) {
         if (h == 0 && valid) p.part_ml[(int64_t(blockIdx.x) * 2 + s.slot) * 128 + r] = make_float2(M, den);
-        const int item = s.entry * p.Hkv + s.h;
         // (The barrier orders the CTA's stores before the one release, and its acquire before all loads.)
         named_bar_sync(1, kSoftThreads);
         if (tid == 128) {
           const int add = s.j1 - s.j0;
-          *merge_here = atomic_add_acq_rel_gpu(p.cnt + item, add) + add == s.nkb;
-          if (*merge_here) p.cnt[item] = 0;
+          int32_t* cnt = p.cnt + run_of(run, s.x0);
+          *merge_here = atomic_add_acq_rel_gpu(cnt, add) + add == s.nkb;
+          if (*merge_here) *cnt = 0;
         }
         named_bar_sync(1, kSoftThreads);
         if (*merge_here && valid) {

@@ -65,7 +65,7 @@ struct Params {
   int32_t* top_id;
   float4* part;     // [M, nch], by run of the row: (m, s0, s1, -)
   uint64_t* cand;   // [M, nch, k]: keys, largest first (0 = none)
-  int32_t* done;    // [M]: chunks finished (zero between calls)
+  int32_t* done;    // [grid]: chunks done of the row that begins in the CTA's run and ends in another's (zero between calls)
   int32_t* status;
 };
 
@@ -559,8 +559,11 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const __
       sync();
       if (tid == 0) {
         // (The barriers around order all threads' stores before it and their loads after.)
-        const bool last = atomic_add_acq_rel_gpu(p.done + row, done) + done == p.nch;
-        if (last) p.done[row] = 0;
+        bool last = done == p.nch;  // the whole row
+        if (!last) {
+          last = atomic_add_acq_rel_gpu(p.done + first, done) + done == p.nch;
+          if (last) p.done[first] = 0;
+        }
         s.last = last;
         s.count = 0;
       }
@@ -594,7 +597,7 @@ static bool shape_ok(int64_t M, int64_t V, int k) {
 // For any element type (fp32 has the most chunks).
 static size_t ws_bytes_of(int64_t M, int64_t V, int k) {
   const int64_t nch = chunks_of(V, 4);
-  return size_t(round_up(M * 4, 256) + M * nch * 16 + M * nch * k * 8);
+  return size_t(kRunCounters * 4 + M * nch * 16 + M * nch * k * 8);
 }
 
 template <int kType>
@@ -652,14 +655,15 @@ int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ro
   p.top_id = top_id;
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.done = reinterpret_cast<int32_t*>(w);
-  p.part = reinterpret_cast<float4*>(w + round_up(M * 4, 256));
-  p.cand = reinterpret_cast<uint64_t*>(w + round_up(M * 4, 256) + M * p.nch * 16);
+  p.part = reinterpret_cast<float4*>(w + kRunCounters * 4);
+  p.cand = reinterpret_cast<uint64_t*>(w + kRunCounters * 4 + M * p.nch * 16);
   p.status = dev_status;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  const int64_t room = int64_t(device_sm_count()) * kCtas;
+  int64_t room = int64_t(device_sm_count()) * kCtas;
+  if (room > kRunCounters) room = kRunCounters;
   cfg.gridDim = dim3(unsigned(p.chunks < room ? p.chunks : room));
   cfg.dynamicSmemBytes = sizeof(Smem);
   cfg.blockDim = dim3(kThreads + 32);

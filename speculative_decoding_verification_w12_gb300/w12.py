@@ -162,7 +162,7 @@ def _bits16(t: torch.Tensor) -> torch.Tensor:
 
 
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:
-    """Zero-filled device workspace (the library leaves it zeroed after each call)."""
+    """Zero-filled device workspace, for calls of one function and size (see include/w12.h)."""
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
