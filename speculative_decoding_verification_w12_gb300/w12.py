@@ -772,7 +772,8 @@ class TokenLogprobs:
 def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0, scale: float = 1.0,
              status: torch.Tensor | None = None, stream=None):
     """One call of TokenLogprobs on logits [M, V]."""
-    return TokenLogprobs(logits.shape[0], logits.shape[1], k, logits.device).run(logits, tokens, scale, status, stream)
+    with torch.cuda.stream(stream):  # (None: the current one) the workspace belongs to the stream that uses it
+        return TokenLogprobs(logits.shape[0], logits.shape[1], k, logits.device).run(logits, tokens, scale, status, stream)
 
 
 def selftest_timeout(limit_us: int, status: torch.Tensor, stream=None):
