@@ -161,9 +161,20 @@ def _bits16(t: torch.Tensor) -> torch.Tensor:
     return t
 
 
-def workspace(nbytes: int, device="cuda") -> torch.Tensor:
-    """Zero-filled device workspace, for calls of one function and size (see include/w12.h)."""
-    return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+def _empty(shape, dtype, device, stream, make=None):
+    """Uninitialised output of a call on `stream` (None: the current one): the
+    memory belongs to the stream that writes it."""
+    make = make or torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
+def workspace(nbytes: int, device="cuda", stream=None) -> torch.Tensor:
+    """Zero-filled device workspace, for calls of one function and size (see include/w12.h).
+    One for a single call on `stream` (None: the current one) is made, and filled, on it."""
+    return _empty(max(int(nbytes), 256), torch.uint8, device, stream, torch.zeros)
 
 
 @dataclass
@@ -203,7 +214,7 @@ def pack(W: torch.Tensor, stream=None) -> W12Weights:
     W = _bits16(W)
     N, K = W.shape
     dev = W.device
-    ws = torch.zeros(max(int(lib().w12_pack_ws_bytes(N, K)), 4), dtype=torch.uint8, device=dev)
+    ws = workspace(lib().w12_pack_ws_bytes(N, K), dev, stream)
     sizes = _Sizes()
     _check(lib().w12_pack_query(W.data_ptr(), N, K, ctypes.byref(sizes), ws.data_ptr(), ws.numel(),
                                 _stream(stream)), "w12_pack_query")
@@ -211,12 +222,12 @@ def pack(W: torch.Tensor, stream=None) -> W12Weights:
     U = (N // 128) * (K // 128)
     out = W12Weights(
         N=N, K=K,
-        p0=torch.empty((N, K // 2), dtype=torch.uint8, device=dev),
-        p1=torch.empty((N, K // 2), dtype=torch.uint8, device=dev),
-        p2=torch.empty((N, K // 2), dtype=torch.uint8, device=dev),
-        ebase=torch.empty((K // 128, N), dtype=torch.uint8, device=dev),
-        exc_off=torch.empty(U + 1, dtype=torch.int32, device=dev),
-        exc_ent=torch.empty(max(n_exc, 1), dtype=torch.int32, device=dev),
+        p0=_empty((N, K // 2), torch.uint8, dev, stream),
+        p1=_empty((N, K // 2), torch.uint8, dev, stream),
+        p2=_empty((N, K // 2), torch.uint8, dev, stream),
+        ebase=_empty((K // 128, N), torch.uint8, dev, stream),
+        exc_off=_empty(U + 1, torch.int32, dev, stream),
+        exc_ent=_empty(max(n_exc, 1), torch.int32, dev, stream),
         n_exc=n_exc)
     _check(lib().w12_pack(W.data_ptr(), N, K, ctypes.byref(out.struct()), _stream(stream)), "w12_pack")
     return out
@@ -224,7 +235,7 @@ def pack(W: torch.Tensor, stream=None) -> W12Weights:
 
 def unpack(w: W12Weights, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """bf16 [N, K] restored bit-exactly from a packed matrix."""
-    out = torch.empty((w.N, w.K), dtype=torch.bfloat16, device=w.p0.device)
+    out = _empty((w.N, w.K), torch.bfloat16, w.p0.device, stream)
     _check(lib().w12_unpack(ctypes.byref(w.struct()), out.data_ptr(), _ptr(status), _stream(stream)), "w12_unpack")
     return out
 
@@ -243,9 +254,9 @@ def gemm(X: torch.Tensor, w: W12Weights, Y: torch.Tensor | None = None, ws: torc
     X = _bits16(X)
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, w.N), dtype=torch.float32, device=X.device)
+        Y = _empty((M, w.N), torch.float32, X.device, stream)
     if ws is None:
-        ws = workspace(gemm_ws_bytes(M, w.N, w.K), X.device)
+        ws = workspace(gemm_ws_bytes(M, w.N, w.K), X.device, stream)
     _check(lib().w12_gemm(X.data_ptr(), M, ctypes.byref(w.struct()), Y.data_ptr(), ws.data_ptr(), ws.numel(),
                           _ptr(status), _stream(stream)), "w12_gemm")
     return Y
@@ -344,7 +355,7 @@ def kv_commit(caches, prefix_len: torch.Tensor, path: torch.Tensor, path_len: to
         if not c.is_contiguous() or tuple(c.shape[:2]) != (B, S_max) or c[0, 0].numel() * c.element_size() != row_bytes:
             raise ValueError("caches must be contiguous [B, S_max, ...] tensors with equal row sizes")
     if new_len is None:
-        new_len = torch.empty(B, dtype=torch.int32, device=caches[0].device)
+        new_len = _empty(B, torch.int32, caches[0].device, stream)
     ptrs = (ctypes.c_void_p * len(caches))(*[c.data_ptr() for c in caches])
     _check(lib().w12_kv_commit(ptrs, len(caches), B, S_max, row_bytes, prefix_len.data_ptr(), path.data_ptr(),
                                path.shape[1], path_len.data_ptr(), new_len.data_ptr(), _ptr(status),
@@ -382,7 +393,7 @@ def state_select(states: torch.Tensor, path: torch.Tensor, path_len: torch.Tenso
     B, T = states.shape[:2]
     row_bytes = states[0, 0].numel() * states.element_size()
     if out is None:
-        out = torch.empty((B,) + tuple(states.shape[2:]), dtype=states.dtype, device=states.device)
+        out = _empty((B,) + tuple(states.shape[2:]), states.dtype, states.device, stream)
     _check(lib().w12_state_select(states.data_ptr(), B, T, row_bytes, path.data_ptr(), path.shape[1],
                                   path_len.data_ptr(), out.data_ptr(), _ptr(status), _stream(stream)),
            "w12_state_select")
@@ -399,7 +410,7 @@ class TreeAttention:
     """
 
     def __init__(self, B: int, T: int, Hq: int, Hkv: int, S_max: int, max_kv_len: int | None = None,
-                 device="cuda"):
+                 device="cuda", stream=None):
         self.B, self.T, self.Hq, self.Hkv, self.S_max = B, T, Hq, Hkv, S_max
         self.max_kv_len = S_max if max_kv_len is None else int(max_kv_len)
         nbytes = lib().w12_tree_attention_ws_bytes(B, T, Hq, Hkv, self.max_kv_len)
@@ -407,7 +418,7 @@ class TreeAttention:
             raise W12Error(2, "w12_tree_attention_ws_bytes")
         # Zero-filled once: the kernel's per-item arrival counts start at zero
         # and a W12_OK call leaves them there.
-        self.ws = torch.zeros(int(nbytes), dtype=torch.uint8, device=device)
+        self.ws = workspace(nbytes, device, stream)
 
     def reset(self):
         """Zero the workspace again (needed after a call that ended with an error status)."""
@@ -422,7 +433,7 @@ class TreeAttention:
                 or K_cache.shape != V_cache.shape:
             raise ValueError("Q [B, T, Hq, d] and caches [B, S_max, Hkv, d] must match the planned shape")
         if out is None:
-            out = torch.empty_like(Q)
+            out = _empty(Q.shape, Q.dtype, Q.device, stream)
         scale = d ** -0.5 if scale is None else float(scale)
         _check(lib().w12_tree_attention(Q.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), B, T, Hq, self.Hkv,
                                         d, self.S_max, self.max_kv_len, prefix_len.data_ptr(), parents.data_ptr(),
@@ -436,7 +447,7 @@ def tree_attention(Q: torch.Tensor, K_cache: torch.Tensor, V_cache: torch.Tensor
                    out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """One call of the tree-masked verify attention (see TreeAttention)."""
     B, T, Hq, _ = Q.shape
-    a = TreeAttention(B, T, Hq, K_cache.shape[2], K_cache.shape[1], max_kv_len, device=Q.device)
+    a = TreeAttention(B, T, Hq, K_cache.shape[2], K_cache.shape[1], max_kv_len, Q.device, stream)
     return a.run(Q, K_cache, V_cache, prefix_len, parents, scale, out, status, stream)
 
 
@@ -447,16 +458,16 @@ def gemm_bf16_ref(X: torch.Tensor, W: torch.Tensor, Y: torch.Tensor | None = Non
     M = X.shape[0]
     N, K = W.shape
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=X.device)
+        Y = _empty((M, N), torch.float32, X.device, stream)
     if ws is None:
-        ws = workspace(gemm_ws_bytes(M, N, K), X.device)
+        ws = workspace(gemm_ws_bytes(M, N, K), X.device, stream)
     _check(lib().w12_gemm_bf16_ref(X.data_ptr(), M, W.data_ptr(), N, K, Y.data_ptr(), ws.data_ptr(), ws.numel(),
                                    _ptr(status), _stream(stream)), "w12_gemm_bf16_ref")
     return Y
 
 
-def _i32(n, device):
-    return torch.empty(n, dtype=torch.int32, device=device)
+def _i32(device, stream, *shapes):
+    return tuple(_empty(n, torch.int32, device, stream) for n in shapes)
 
 
 def verify_greedy(logits: torch.Tensor, draft: torch.Tensor, T_rows: int, ws=None, status=None, stream=None):
@@ -464,9 +475,9 @@ def verify_greedy(logits: torch.Tensor, draft: torch.Tensor, T_rows: int, ws=Non
     B, T = draft.shape
     V = logits.shape[1]
     dev = logits.device
-    acc, bonus, am = _i32(B, dev), _i32(B, dev), _i32(B * T_rows, dev)
+    acc, bonus, am = _i32(dev, stream, B, B, B * T_rows)
     if ws is None:
-        ws = workspace(verify_ws_bytes(B * T_rows, V), dev)
+        ws = workspace(verify_ws_bytes(B * T_rows, V), dev, stream)
     _check(lib().w12_verify_greedy(logits.data_ptr(), V, draft.data_ptr(), B, T, T_rows, acc.data_ptr(),
                                    bonus.data_ptr(), am.data_ptr(), ws.data_ptr(), ws.numel(), _ptr(status),
                                    _stream(stream)), "w12_verify_greedy")
@@ -479,9 +490,9 @@ def verify_greedy_fused(H: torch.Tensor, head: W12Weights, draft: torch.Tensor, 
     H = _bits16(H)
     B, T = draft.shape
     dev = H.device
-    acc, bonus, am = out if out is not None else (_i32(B, dev), _i32(B, dev), _i32(B * T_rows, dev))
+    acc, bonus, am = out if out is not None else _i32(dev, stream, B, B, B * T_rows)
     if ws is None:
-        ws = workspace(verify_ws_bytes(B * T_rows, head.N), dev)
+        ws = workspace(verify_ws_bytes(B * T_rows, head.N), dev, stream)
     _check(lib().w12_verify_greedy_fused(H.data_ptr(), ctypes.byref(head.struct()), draft.data_ptr(), B, T, T_rows,
                                          acc.data_ptr(), bonus.data_ptr(), _ptr(am), ws.data_ptr(), ws.numel(),
                                          _ptr(status), _stream(stream)), "w12_verify_greedy_fused")
@@ -493,9 +504,9 @@ def verify_tree(logits: torch.Tensor, parents: torch.Tensor, draft: torch.Tensor
     B, T = parents.shape
     V = logits.shape[1]
     dev = logits.device
-    path, plen, acc, bonus, am = _i32((B, T), dev), _i32(B, dev), _i32(B, dev), _i32(B, dev), _i32(B * T, dev)
+    path, plen, acc, bonus, am = _i32(dev, stream, (B, T), B, B, B, B * T)
     if ws is None:
-        ws = workspace(verify_ws_bytes(B * T, V), dev)
+        ws = workspace(verify_ws_bytes(B * T, V), dev, stream)
     _check(lib().w12_verify_tree(logits.data_ptr(), V, parents.data_ptr(), draft.data_ptr(), B, T, path.data_ptr(),
                                  plen.data_ptr(), acc.data_ptr(), bonus.data_ptr(), am.data_ptr(), ws.data_ptr(),
                                  ws.numel(), _ptr(status), _stream(stream)), "w12_verify_tree")
@@ -508,9 +519,9 @@ def verify_tree_fused(H: torch.Tensor, head: W12Weights, parents: torch.Tensor, 
     H = _bits16(H)
     B, T = parents.shape
     dev = H.device
-    path, plen, acc, bonus, am = _i32((B, T), dev), _i32(B, dev), _i32(B, dev), _i32(B, dev), _i32(B * T, dev)
+    path, plen, acc, bonus, am = _i32(dev, stream, (B, T), B, B, B, B * T)
     if ws is None:
-        ws = workspace(verify_ws_bytes(B * T, head.N), dev)
+        ws = workspace(verify_ws_bytes(B * T, head.N), dev, stream)
     _check(lib().w12_verify_tree_fused(H.data_ptr(), ctypes.byref(head.struct()), parents.data_ptr(),
                                        draft.data_ptr(), B, T, path.data_ptr(), plen.data_ptr(), acc.data_ptr(),
                                        bonus.data_ptr(), am.data_ptr(), ws.data_ptr(), ws.numel(), _ptr(status),
@@ -532,15 +543,6 @@ def _want(t: torch.Tensor, what: str, dtype, shape=None) -> torch.Tensor:
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
     return t
-
-
-def _empty(shape, dtype, device, stream):
-    """Uninitialised output of a call on `stream` (None: the current one): the
-    memory belongs to the stream that writes it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _kept_workspace(nbytes: int, device) -> torch.Tensor:

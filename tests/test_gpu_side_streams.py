@@ -35,3 +35,21 @@ def test_log_probabilities_in_one_call():
     for got in beside(lambda s: w12.logprobs(x, tokens, k, status=st, stream=s), [size, M * k * 4, M * 4]):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert status_value(st) == 0
+
+
+def test_gemm_and_tree_attention_in_one_call():
+    g = torch.Generator(device="cuda").manual_seed(0)
+    W = w12.pack(torch.randn((1024, 512), generator=g, device="cuda").bfloat16())
+    X = torch.randn((16, 512), generator=g, device="cuda").bfloat16()
+    ws = w12.workspace(w12.gemm_ws_bytes(16, 1024, 512))
+    want = w12.gemm(X, W, ws=ws)
+    for got in beside(lambda s: w12.gemm(X, W, stream=s), [ws.numel(), want.numel() * 4]):
+        assert torch.equal(got, want)
+    B, T, Hq, Hkv, S = 2, 16, 10, 2, 600
+    Q, K, V = (torch.randn(shape, generator=g, device="cuda").bfloat16()
+               for shape in ((B, T, Hq, 128), (B, S, Hkv, 128), (B, S, Hkv, 128)))
+    prefix, parents = to_dev_i32([500, 37]), to_dev_i32([list(range(-1, T - 1))] * B)
+    att = w12.TreeAttention(B, T, Hq, Hkv, S)
+    want = att.run(Q, K, V, prefix, parents)
+    for got in beside(lambda s: w12.tree_attention(Q, K, V, prefix, parents, stream=s), [att.ws.numel(), want.numel() * 2]):
+        assert torch.equal(got, want)
