@@ -671,7 +671,7 @@ def kv4_commit(caches, table: torch.Tensor, prefix_len: torch.Tensor, path: torc
         raise ValueError("path must be [B, stride]")
     if new_len is None:
         new_len = _empty((B,), torch.int32, table.device, stream)
-    elif new_len.data_ptr() == prefix_len.data_ptr():
+    elif _want(new_len, "new_len", torch.int32, (B,)).data_ptr() == prefix_len.data_ptr():
         raise ValueError("new_len must be another tensor than prefix_len")
     arr = caches[0]._ref if len(caches) == 1 else (_KV4 * len(caches))(*[c._struct for c in caches])
     _check(lib().w12_kv4_commit(arr, len(caches), B, table.data_ptr(), max_pages, prefix_len.data_ptr(),
