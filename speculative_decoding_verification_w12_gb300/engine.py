@@ -174,6 +174,7 @@ class PagedVerifyStep:
         if qkv.N != (Hq + 2 * Hkv) * head_dim or out.K != Hq * head_dim or head.K != out.N:
             raise ValueError("qkv, out and head do not fit the heads")
         self.B, self.T, self.M, self.Hq, self.Hkv, self.head_dim = B, T, B * T, Hq, Hkv, head_dim
+        self.max_len = max_len
         self.qkv, self.out, self.head, self.top_k = qkv, out, head, top_k
         self.cache = w12.KV4Cache.create(n_pages, Hkv, head_dim, page_size, dev)
         self.pages = w12.PageTable.create(B, -(-max_len // page_size), n_pages, page_size, dev)
@@ -186,11 +187,21 @@ class PagedVerifyStep:
         self._vws = w12.workspace(w12.verify_ws_bytes(self.M, head.N), dev)
 
     def prefill(self, K: torch.Tensor, V: torch.Tensor, length: torch.Tensor):
-        """Cache the first length[b] rows of K, V [B, n, Hkv, head_dim] (one prompt a request)."""
+        """Cache the first length[b] rows of K, V [B, n, Hkv, head_dim] (one prompt a request).
+
+        length int32 [B]: a request with -1 stays as it is, 0 ends one and frees its
+        pages. A prompt that there are no pages for, or that is longer than n or
+        max_len, leaves its request as it was and sets the status word.
+        """
         n = K.shape[1]
-        slots = self.pages.reserve(torch.zeros_like(length), length, n, status=self.status)
+        keep = length < 0
+        # (A kept request asks for no more than it has; a count of -1 is refused.)
+        start = torch.where(keep, self.length, 0)
+        new = torch.where(keep, 0, torch.where(length <= self.max_len, length, -1))
+        slots = self.pages.reserve(start, new, n, status=self.status)
         self.cache.append(K.flatten(0, 1), V.flatten(0, 1), slots, status=self.status)
-        self.length.copy_(length)
+        given = (new == 0) | (slots[:, :1] >= 0).any(1)
+        self.length.copy_(torch.where(given & ~keep, length, self.length))
 
     def run(self, X: torch.Tensor, parents: torch.Tensor, draft: torch.Tensor) -> dict:
         """One step on X bf16 [B * T, hidden], the draft trees parents, draft int32 [B, T].
