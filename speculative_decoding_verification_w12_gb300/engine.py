@@ -165,6 +165,11 @@ class PagedVerifyStep:
     vocabulary. Position encodings, norms and the MLP are the caller's: the step
     takes the rows that enter the layer. length int32 [B] holds each request's
     committed tokens and is advanced by every step.
+
+    A request that there are no pages for, or whose tokens would pass max_len, is
+    not served by a step: its length, pages and cached rows stay as they are, and
+    the status word (int32 [1], set once, cleared by the caller) says
+    W12_ERR_WORKSPACE or W12_ERR_ARG. The other requests are served as ever.
     """
 
     def __init__(self, qkv: w12.W12Weights, out: w12.W12Weights, head: w12.W12Weights, B: int, T: int, Hq: int,
@@ -209,20 +214,26 @@ class PagedVerifyStep:
         Returns path [B, T], path_len, accept_len, bonus (as verify_tree); tokens
         [B, T], the answered tokens in order (the accepted drafts, then the bonus
         token, -1 after it), and at the same places logprob, entropy, top_logprob
-        and top_id of the rows that predicted them.
+        and top_id of the rows that predicted them. A request that is not served
+        has path, bonus and tokens of -1 and path_len and accept_len 0.
         """
         B, T, M, d = self.B, self.T, self.M, self.head_dim
         st = self.status
-        slots = self.pages.reserve(self.length, self.nodes, T, status=st)
+        # (A negative count is refused: the request keeps its pages and gets slots of -1.)
+        nodes = torch.where(self.length <= self.max_len - T, self.nodes, -1)
+        slots = self.pages.reserve(self.length, nodes, T, status=st)
+        served = slots[:, 0] >= 0
         Y = w12.gemm(X, self.qkv, ws=self._ws[0], status=st)
         q, k, v = Y.split([self.Hq * d, self.Hkv * d, self.Hkv * d], 1)
         # Keys and values are quantised straight from the fp32 product (views of it).
         self.cache.append(k.unflatten(1, (self.Hkv, d)), v.unflatten(1, (self.Hkv, d)), slots, status=st)
         O = self.attention.run(q.to(torch.bfloat16).view(B, T, self.Hq, d), self.cache, self.pages.table, self.length,
-                               parents=parents, q_len=self.nodes, status=st)
+                               parents=parents, q_len=torch.where(served, nodes, 0), status=st)
         H = w12.gemm(O.view(M, self.Hq * d), self.out, ws=self._ws[1], status=st).to(torch.bfloat16)
         logits = w12.gemm(H, self.head, ws=self._ws[2], status=st)
         path, path_len, accept_len, bonus, _ = w12.verify_tree(logits, parents, draft, ws=self._vws, status=st)
+        path, bonus = torch.where(served[:, None], path, -1), torch.where(served, bonus, -1)
+        path_len, accept_len = path_len * served, accept_len * served
         # Row path[i] predicted the draft of path[i + 1], the last row of the path the bonus token.
         step = torch.arange(T, device=X.device)[None]
         nxt = torch.cat([path[:, 1:], path[:, :1]], 1).clamp(min=0).long()

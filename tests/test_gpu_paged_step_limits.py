@@ -42,11 +42,79 @@ def _rows(step, b, n):
     return KO.read(step.cache.pool.cpu().numpy(), (t[pos // P] * P + pos % P).tolist(), D)
 
 
+def _same_as_alone(step, r, b, before, x):
+    """Request b's results are those of a step in which only it takes part."""
+    other = _step(1, 64, 1024)
+    for name in ("tokens", "path", "accept_len", "bonus"):
+        assert r[name].shape[0] == step.B
+    K, V = before
+    other.prefill(torch.from_numpy(K[None].astype(np.float32)).cuda(), torch.from_numpy(V[None].astype(np.float32)).cuda(),
+                  to_dev_i32([K.shape[0]]))
+    kk, vv = _rows(other, 0, K.shape[0])
+    if not ((kk == K).all() and (vv == V).all()):
+        return                                         # (codes do not always quantise to themselves)
+    X, parents, draft = x
+    q = other.run(X[b * T:(b + 1) * T].contiguous(), parents[b:b + 1].contiguous(), draft[b:b + 1].contiguous())
+    for name in ("tokens", "path", "accept_len", "bonus"):
+        assert torch.equal(q[name][0], r[name][b]), name
+
+
 def _unchanged(step, b, length, used, table, rows):
     assert int(step.length[b]) == length and int(step.pages.used[b]) == used
     assert torch.equal(step.pages.table[b], table)
     K, V = _rows(step, b, length)
     assert (K == rows[0]).all() and (V == rows[1]).all()
+
+
+def _not_served(r, b):
+    assert int(r["accept_len"][b]) == 0 and int(r["path_len"][b]) == 0 and int(r["bonus"][b]) == -1
+    assert (r["tokens"][b] == -1).all() and (r["path"][b] == -1).all()
+
+
+def test_a_request_without_pages_keeps_its_state():
+    """Three requests of which the second and third need a page that is not there."""
+    B, prompt = 3, [20, 28, 30]
+    step = _step(B, n_pages=6, max_len=256)
+    g = np.random.default_rng(1)
+    _, dev = _prompt(g, B, 30)
+    step.prefill(*dev, to_dev_i32(prompt))
+    assert status_value(step.status) == 0 and int(step.pages.n_free[0]) == 0
+    before = [_rows(step, b, n) for b, n in enumerate(prompt)]
+    tables, used = step.pages.table.clone(), step.pages.used.tolist()
+    x = _inputs(B, 0)
+    r = step.run(*x)
+    assert status_value(step.status) == 3
+    assert int(r["path_len"][0]) == int(r["accept_len"][0]) + 1 and int(step.length[0]) == 20 + int(r["path_len"][0])
+    _same_as_alone(step, r, 0, before[0], x)
+    for b in (1, 2):
+        _not_served(r, b)
+        _unchanged(step, b, prompt[b], used[b], tables[b], before[b])
+    # Pages that come back serve it: the first request ends.
+    step.status.zero_()
+    step.prefill(dev[0], dev[1], to_dev_i32([0, -1, -1]))
+    r = step.run(*x)
+    assert int(step.length[0]) <= T and status_value(step.status) in (0, 3)
+    assert int(r["path_len"][1]) >= 1 and int(step.length[1]) == 28 + int(r["path_len"][1])
+
+
+@pytest.mark.parametrize("max_len", [64, 60, 50])
+def test_a_request_at_the_end_of_its_context(max_len):
+    """The second request's tokens would pass max_len, which need not be whole pages."""
+    B, prompt = 2, [10, max_len - T + 1]
+    step = _step(B, n_pages=32, max_len=max_len)
+    g = np.random.default_rng(2)
+    _, dev = _prompt(g, B, prompt[1])
+    step.prefill(*dev, to_dev_i32(prompt))
+    assert status_value(step.status) == 0
+    before = [_rows(step, b, n) for b, n in enumerate(prompt)]
+    used, tables = step.pages.used.tolist(), step.pages.table.clone()
+    x = _inputs(B, 1)
+    r = step.run(*x)
+    assert status_value(step.status) == 1
+    _not_served(r, 1)
+    _unchanged(step, 1, prompt[1], used[1], tables[1], before[1])
+    assert int(step.length[0]) == 10 + int(r["path_len"][0])
+    _same_as_alone(step, r, 0, before[0], x)
 
 
 def test_a_request_just_inside_its_context_is_served():
