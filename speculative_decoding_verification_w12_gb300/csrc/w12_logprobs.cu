@@ -422,16 +422,20 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const __
     uint4 raw[kPieces];
     if constexpr (kVec) {
       const int st = c % kStages;
-      if (!*failed && !mbar_wait(&s.full[st], uint32_t(c / kStages) & 1u, p.limit_ns)) {
+      // A warp frees a stage only if it has seen the copy land. After an expired wait it goes on
+      // to the CTA's barriers, but the copying warp must not find a stage free that a copy is
+      // still on its way to: that would request a second one on an open phase of its barrier.
+      const bool go = !*failed, mine = go && mbar_wait(&s.full[st], uint32_t(c / kStages) & 1u, p.limit_ns);
+      if (go && !mine) {
         set_status(p.status, W12_ERR_TIMEOUT);
         *failed = 1;
       }
-      __syncwarp();
+      const bool landed = __all_sync(0xFFFFFFFFu, mine);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) raw[i] = *reinterpret_cast<const uint4*>(&s.ring[st][(i * kThreads + tid) * 16]);
       fence_proxy_async_smem();  // before the copy that refills the stage
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.empty[st]);
+      if (landed && lane == 0) mbar_arrive(&s.empty[st]);
     }
     if (!kVec || e0 + kPer > p.V) {
 #pragma unroll

@@ -1,4 +1,6 @@
-"""A thread block may not end while a copy that it has requested can still land in its
+"""Copies into shared memory and the waits for them, where one may expire.
+
+A thread block may not end while a copy that it has requested can still land in its
 shared memory: the memory may be another block's by then. A wait of another warp can
 expire after the copying warp has issued its last copy, so the wait for the copies in
 flight has to stand on every path to that warp's end. Read from the sources: no run
@@ -47,3 +49,14 @@ def test_copies_in_flight_are_waited_for_on_every_path(source):
                 continue
             heads = enclosing(src, m.start())
             assert not [h for h in heads if "abort" in h or "failed" in h], heads
+
+
+def test_log_probabilities_free_no_stage_whose_copy_they_have_not_seen():
+    """After an expired wait the computing warps go on to the block's barriers. A stage that
+    they freed all the same would be filled again while its first copy is in flight, two
+    requests on one phase of its barrier, which faults."""
+    src = open(os.path.join(B.CSRC, "w12_logprobs.cu")).read()
+    arrivals = re.findall(r"^(.*)mbar_arrive\(&s\.empty", src, re.M)
+    assert arrivals and all("landed" in a for a in arrivals)
+    assert re.search(r"mine = go && \w*(::)?mbar_wait\w*\(&s\.full\[st\]", src)
+    assert re.search(r"landed = __all_sync\(0xFFFFFFFFu, mine\)", src)
