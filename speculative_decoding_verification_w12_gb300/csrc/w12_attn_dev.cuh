@@ -45,6 +45,37 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo)
   return d;
 }
 
+// Longest sleep of a waiting thread between looks at the flag that ends its wait and at the
+// clock (a long one does not spend issue slots on polling); never longer than the wait's bound.
+constexpr uint64_t kSleepNs = 10000;
+inline uint32_t sleep_ns(uint64_t limit_ns) { return uint32_t(limit_ns < kSleepNs ? limit_ns : kSleepNs); }
+
+// mbar_try_wait with the time that the hardware may keep the thread asleep.
+__device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
+// Wait for the barrier's phase, `sleep` at a time, up to `limit` or until `stop` is set: whether it
+// has come. (mbar_wait sleeps for as long as the hardware likes: a bound of microseconds does not hold.)
+__device__ __forceinline__ bool mbar_wait_asleep(uint64_t* bar, uint32_t parity, uint64_t limit, uint32_t sleep,
+                                                 const volatile int* stop) {
+  if (mbar_try_wait_hint(bar, parity, sleep)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 0; i < 0x80000000u; ++i) {
+    if (mbar_try_wait_hint(bar, parity, sleep)) return true;
+    if (*stop || globaltimer_ns() - t0 > limit) break;
+  }
+  return false;
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

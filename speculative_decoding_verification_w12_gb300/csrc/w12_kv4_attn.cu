@@ -140,6 +140,7 @@ int w12_kv4_attention(const uint16_t* Q, int64_t q_batch_stride, int64_t q_token
   p.max_len = int(max_kv_len);
   p.c = float(double(scale) * 1.4426950408889634);
   p.limit_ns = wait_limit_ns();
+  p.sleep_ns = attn_impl::sleep_ns(p.limit_ns);
   p.ntile = pl.ntile;
   p.rows_per_tile = pl.rows;
   uint8_t* w = static_cast<uint8_t*>(ws);

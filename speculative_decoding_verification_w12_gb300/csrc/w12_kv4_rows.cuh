@@ -49,6 +49,7 @@ namespace kv4_attn {
 
 using attn_impl::pack_f16x2;
 using attn_impl::scaled_down;
+using attn_impl::mbar_wait_asleep;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -167,15 +168,8 @@ __global__ void __launch_bounds__(RowsCfg<kD, kNT>::kThreads, RowsCfg<kD, kNT>::
   const uint64_t lim = p.limit_ns;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 0; i < 0x80000000u; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if ((i & 63u) == 63u) {
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > lim) break;
-      }
-    }
+    if (mbar_wait_asleep(bar, parity, lim, p.sleep_ns, abort_flag)) return true;
+    if (*abort_flag) return false;
     set_status(p.status, W12_ERR_TIMEOUT);
     *abort_flag = 1;
     return false;

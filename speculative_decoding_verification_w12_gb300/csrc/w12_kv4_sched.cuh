@@ -38,6 +38,7 @@ struct Params {
   int B, T, Hq, Hkv, G, P, p_shift, max_pages, max_len, ntile, rows_per_tile;
   float c;         // scale * log2(e)
   uint64_t limit_ns;
+  uint32_t sleep_ns;
 };
 
 // Request b's cached and new tokens, clamped into range when they are not.

@@ -63,21 +63,8 @@ using attn_impl::fast_exp2;
 using attn_impl::mask_block;
 using attn_impl::rescale_row;
 using attn_impl::scaled_down;
+using attn_impl::mbar_wait_asleep;
 using attn_impl::sdesc_mn_sw128;
-
-// mbar_try_wait with a time hint: the hardware may keep the thread asleep for about
-// that long, so that a long wait does not spend issue slots on polling.
-__device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
-      : "memory");
-  return ok != 0;
-}
 
 // True for one lane of the (converged) warp, the same one at every call.
 __device__ __forceinline__ bool elect_one() {
@@ -110,7 +97,6 @@ constexpr int kLeastK = -92, kLeastV = -88;
 constexpr int kSmallV = -44;
 constexpr float kTop = 8.f;              // the largest weight when the running maximum was set, as a power of two
 constexpr float kMost = 61440.f;         // sum of 32 weights above which it moves (fp16 ends at 65504)
-constexpr uint32_t kWaitHintNs = 10000;  // asleep on a barrier between looks at the abort flag and the clock
 
 template <int kD>
 struct TileCfg {
@@ -433,13 +419,8 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
   const uint64_t lim = p.limit_ns;
 
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t i = 0; i < 0x80000000u; ++i) {
-      if (mbar_try_wait_hint(bar, parity, kWaitHintNs)) return true;
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > lim) break;
-    }
+    if (mbar_wait_asleep(bar, parity, lim, p.sleep_ns, abort_flag)) return true;
+    if (*abort_flag) return false;
     set_status(p.status, W12_ERR_TIMEOUT);
     *abort_flag = 1;
     return false;

@@ -61,6 +61,7 @@ struct Params {
   int n, k, nch;
   int64_t chunks;   // M nch
   uint64_t limit_ns;
+  uint32_t sleep_ns;
   float *logprob, *entropy, *lse, *top_lp;
   int32_t* top_id;
   float4* part;     // [M, nch], by run of the row: (m, s0, s1, -)
@@ -160,6 +161,8 @@ __device__ __forceinline__ void list_candidate(Smem& s, uint64_t key) {
 __device__ __forceinline__ int live_warps(int64_t threads) {
   return int(max(int64_t(1), min(int64_t(kWarps), threads / 32)));
 }
+
+using attn_impl::mbar_wait_asleep;
 
 enum { kF32 = 0, kBf16 = 1, kF16 = 2 };
 
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const __
     int c = 0;
     for (; c < total; ++c) {
       const int st = c % kStages;
-      if (c >= kStages && !mbar_wait(&s.empty[st], uint32_t(c / kStages - 1) & 1u, p.limit_ns)) {
+      if (c >= kStages && !mbar_wait_asleep(&s.empty[st], uint32_t(c / kStages - 1) & 1u, p.limit_ns, p.sleep_ns, failed)) {
         set_status(p.status, W12_ERR_TIMEOUT);
         *failed = 1;
         break;
@@ -425,7 +428,8 @@ __global__ void __launch_bounds__(kThreads + 32, kCtas) logprobs_kernel(const __
       // A warp frees a stage only if it has seen the copy land. After an expired wait it goes on
       // to the CTA's barriers, but the copying warp must not find a stage free that a copy is
       // still on its way to: that would request a second one on an open phase of its barrier.
-      const bool go = !*failed, mine = go && mbar_wait(&s.full[st], uint32_t(c / kStages) & 1u, p.limit_ns);
+      const bool go = !*failed;
+      const bool mine = go && mbar_wait_asleep(&s.full[st], uint32_t(c / kStages) & 1u, p.limit_ns, p.sleep_ns, failed);
       if (go && !mine) {
         set_status(p.status, W12_ERR_TIMEOUT);
         *failed = 1;
@@ -652,6 +656,7 @@ int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ro
   p.nch = int(chunks_of(V, esize));
   p.chunks = M * p.nch;
   p.limit_ns = wait_limit_ns();
+  p.sleep_ns = attn_impl::sleep_ns(p.limit_ns);
   p.logprob = logprob;
   p.entropy = entropy;
   p.lse = lse;
