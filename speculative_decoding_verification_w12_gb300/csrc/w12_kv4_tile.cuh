@@ -109,10 +109,11 @@ struct TileCfg {
   static constexpr int kThreads = (kRest + 8) * 32;
   // Registers a thread from the role's start on, of the 96 that the launch has for each
   // (checked there): the softmax, with code of its own for keys that have exponents of
-  // their own, spills at 96 (blocks 89 us for 85, prompt chunk 144.5 for 142). A
-  // warpgroup's warps change theirs together.
+  // their own, spills at 96 (blocks 89 us for 86, prompt chunk 146 for 143.5). A warpgroup
+  // changes its registers by one instruction that all its warps meet.
   static constexpr int kLaunchRegs = 96, kPlainRegs = 88, kSoftRegs = 112, kRestRegs = 80;
-  static_assert(kPlainRegs * 4 + kSoftRegs * kSoft + kRestRegs * 8 <= kLaunchRegs * (kThreads / 32), "the launch's registers");
+  static_assert(kPlainRegs * 4 + kSoftRegs * kSoft + kRestRegs * 8 <= kLaunchRegs * (kThreads / 32),
+                "the launch's registers");
   static constexpr uint32_t kHalf = 128u * 128u;       // 128 rows x 64 fp16, 128-byte swizzle
   static constexpr uint32_t kTile = kHalf * (kD / 64);
   static constexpr uint32_t kRaw = uint32_t(kKeys) * (kD + 8);
@@ -426,172 +427,172 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
     return false;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------- copies
+  if (warp < 4) {
     fewer_registers<C::kPlainRegs>();
-    Walk walk(run);
-    Seg s;
-    const int per = kKeys >> p.p_shift;
-    const uint32_t bytes = uint32_t(p.block);
-    const uint64_t page_stride = uint64_t(p.Hkv) * uint64_t(p.block);
-    int issued = 0;
-    bool ok = true;
-    while (ok && walk.next(p, run, s)) {
-      const int32_t* tab = p.table + int64_t(s.b) * p.max_pages;
-      const uint8_t* pool = p.pool + uint64_t(s.h) * uint64_t(p.block);
-      auto page_of = [&](int j) -> int {
-        const int i = j * per + lane;
-        return lane < per && (int64_t(i) << p.p_shift) < s.keys ? tab[i] : -2;
-      };
-      int next = page_of(s.j0);
-      for (int j = s.j0; j < s.j1; ++j) {
-        int page = next;
-        if (j + 1 < s.j1) next = page_of(j + 1);
-        const bool need = page != -2;
-        if (need && (page < 0 || page >= p.n_pages)) {
-          set_status(p.status, W12_ERR_ARG);
-          page = 0;
+    if (warp == 0) {
+      // ------------------------------------------------------------- copies
+      Walk walk(run);
+      Seg s;
+      const int per = kKeys >> p.p_shift;
+      const uint32_t bytes = uint32_t(p.block);
+      const uint64_t page_stride = uint64_t(p.Hkv) * uint64_t(p.block);
+      int issued = 0;
+      bool ok = true;
+      while (ok && walk.next(p, run, s)) {
+        const int32_t* tab = p.table + int64_t(s.b) * p.max_pages;
+        const uint8_t* pool = p.pool + uint64_t(s.h) * uint64_t(p.block);
+        auto page_of = [&](int j) -> int {
+          const int i = j * per + lane;
+          return lane < per && (int64_t(i) << p.p_shift) < s.keys ? tab[i] : -2;
+        };
+        int next = page_of(s.j0);
+        for (int j = s.j0; j < s.j1; ++j) {
+          int page = next;
+          if (j + 1 < s.j1) next = page_of(j + 1);
+          const bool need = page != -2;
+          if (need && (page < 0 || page >= p.n_pages)) {
+            set_status(p.status, W12_ERR_ARG);
+            page = 0;
+          }
+          const int st = issued % C::kRawStages;
+          if (issued >= C::kRawStages &&
+              !__all_sync(0xFFFFFFFFu, wait(&raw_empty[st], uint32_t(issued / C::kRawStages - 1) & 1u))) {
+            ok = false;
+            break;
+          }
+          const int pages = __popc(__ballot_sync(0xFFFFFFFFu, need));
+          if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], uint32_t(pages) * bytes);
+          __syncwarp();
+          if (need)
+            bulk_load(smem + C::kRawOff + st * C::kRaw + lane * bytes, pool + uint64_t(page) * page_stride, bytes,
+                      &raw_full[st]);
+          ++issued;
         }
-        const int st = issued % C::kRawStages;
-        if (issued >= C::kRawStages &&
-            !__all_sync(0xFFFFFFFFu, wait(&raw_empty[st], uint32_t(issued / C::kRawStages - 1) & 1u))) {
-          ok = false;
+      }
+      if (lane == 0) grid_dep_launch();
+      // The CTA ends only with every copy landed, whatever the other warps do: one of their waits
+      // may still expire. (They need all copies, so this costs a call nothing.)
+      for (int i = issued > C::kRawStages ? issued - C::kRawStages : 0; i < issued; ++i)
+        mbar_wait(&raw_full[i % C::kRawStages], uint32_t(i / C::kRawStages) & 1u, drain_limit_ns(lim));
+    } else if (warp == 1 || warp == 2) {
+      // ---------------------------------------------------------------- MMA
+      // The whole warp waits; one elected lane issues. (With the loop under one
+      // lane, descriptors pass from vector to uniform registers product by product.)
+      const uint32_t sbase = smem_u32(smem);
+      const bool is_s = warp == 1;
+      const uint64_t qd = sdesc_k_sw128(sbase + C::kQOff);
+      const uint64_t kd0 = sdesc_k_sw128(sbase + C::kKOff);
+      const uint64_t vd0 = sdesc_mn_sw128(sbase + C::kVOff, C::kHalf);
+      constexpr uint32_t idesc_s = idesc_f16(128, 128);
+      constexpr uint32_t idesc_o = idesc_f16(128, kD) | (1u << 16);  // B (V) MN-major
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+      Walk walk(run);
+      Seg s;
+      int base = 0, si = 0;
+      bool ok = true;
+      while (ok && walk.next(p, run, s)) {
+        const int n = s.j1 - s.j0;
+        if (is_s) {
+          if (!wait_all(q_full, uint32_t(si) & 1u)) break;
+        } else if (si >= 1 && !wait_all(o_free, uint32_t(si - 1) & 1u)) {
           break;
         }
-        const int pages = __popc(__ballot_sync(0xFFFFFFFFu, need));
-        if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], uint32_t(pages) * bytes);
-        __syncwarp();
-        if (need)
-          bulk_load(smem + C::kRawOff + st * C::kRaw + lane * bytes, pool + uint64_t(page) * page_stride, bytes,
-                    &raw_full[st]);
-        ++issued;
-      }
-    }
-    if (lane == 0) grid_dep_launch();
-    // The CTA ends only with every copy landed, whatever the other warps do: one of their waits
-    // may still expire. (They need all copies, so this costs a call nothing.)
-    for (int i = issued > C::kRawStages ? issued - C::kRawStages : 0; i < issued; ++i)
-      mbar_wait(&raw_full[i % C::kRawStages], uint32_t(i / C::kRawStages) & 1u, drain_limit_ns(lim));
-  } else if (warp == 1 || warp == 2) {
-    fewer_registers<C::kPlainRegs>();
-    // ---------------------------------------------------------------- MMA
-    // The whole warp waits; one elected lane issues. (With the loop under one
-    // lane, descriptors pass from vector to uniform registers product by product.)
-    const uint32_t sbase = smem_u32(smem);
-    const bool is_s = warp == 1;
-    const uint64_t qd = sdesc_k_sw128(sbase + C::kQOff);
-    const uint64_t kd0 = sdesc_k_sw128(sbase + C::kKOff);
-    const uint64_t vd0 = sdesc_mn_sw128(sbase + C::kVOff, C::kHalf);
-    constexpr uint32_t idesc_s = idesc_f16(128, 128);
-    constexpr uint32_t idesc_o = idesc_f16(128, kD) | (1u << 16);  // B (V) MN-major
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
-    Walk walk(run);
-    Seg s;
-    int base = 0, si = 0;
-    bool ok = true;
-    while (ok && walk.next(p, run, s)) {
-      const int n = s.j1 - s.j0;
-      if (is_s) {
-        if (!wait_all(q_full, uint32_t(si) & 1u)) break;
-      } else if (si >= 1 && !wait_all(o_free, uint32_t(si - 1) & 1u)) {
-        break;
-      }
-      for (int j = 0; j < n; ++j) {
-        const int gj = base + j;
-        const int st = gj % C::kStages;
-        const uint32_t sb = tmem + ((gj & 1) ? C::kS1 : C::kS0);
-        if (is_s) {
-          // P of block j - 2 sits in the buffer that S overwrites.
-          if (!wait_all(&k_full[st], uint32_t(gj / C::kStages) & 1u) ||
-              (gj >= 2 && !wait_all(&o_done[gj & 1], uint32_t((gj - 2) >> 1) & 1u))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t kd = kd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < kD / 16; ++ks) {
-              const uint64_t off = uint64_t((uint32_t(ks >> 2) * C::kHalf + uint32_t(ks & 3) * 32u) >> 4);
-              mma_bf16_ss(sb, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u);
-            }
-            tc_commit(&s_full[gj & 1]);
-            tc_commit(&k_empty[st]);
-          }
-          __syncwarp();
-        } else {
-          if (!wait_all(&v_full[st], uint32_t(gj / C::kStages) & 1u)) {
-            ok = false;
-            break;
-          }
-          const uint64_t vd = vd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
-          for (int h = 0; h < C::kParts; ++h) {
-            if (!wait_all(&p_full[(gj & 1) * C::kParts + h], uint32_t(gj >> 1) & 1u)) {
+        for (int j = 0; j < n; ++j) {
+          const int gj = base + j;
+          const int st = gj % C::kStages;
+          const uint32_t sb = tmem + ((gj & 1) ? C::kS1 : C::kS0);
+          if (is_s) {
+            // P of block j - 2 sits in the buffer that S overwrites.
+            if (!wait_all(&k_full[st], uint32_t(gj / C::kStages) & 1u) ||
+                (gj >= 2 && !wait_all(&o_done[gj & 1], uint32_t((gj - 2) >> 1) & 1u))) {
               ok = false;
               break;
             }
             tc_fence_after();
+            const uint64_t kd = kd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
             if (elect_one()) {
 #pragma unroll
-              for (int ks = 0; ks < C::kPart / 16; ++ks) {
-                const uint64_t off = uint64_t((uint32_t(h * C::kPart) * 128u + uint32_t(ks) * 2048u) >> 4);
-                mma_bf16_ts(tmem + C::kO + uint32_t(h * kD), sb + uint32_t(C::kPart * h + 8 * ks), vd + off, idesc_o,
-                            (j > 0 || ks > 0) ? 1u : 0u);
+              for (int ks = 0; ks < kD / 16; ++ks) {
+                const uint64_t off = uint64_t((uint32_t(ks >> 2) * C::kHalf + uint32_t(ks & 3) * 32u) >> 4);
+                mma_bf16_ss(sb, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u);
               }
-              if (h == C::kParts - 1) {
-                tc_commit(&o_done[gj & 1]);
-                tc_commit(&v_empty[st]);
-              }
+              tc_commit(&s_full[gj & 1]);
+              tc_commit(&k_empty[st]);
             }
             __syncwarp();
+          } else {
+            if (!wait_all(&v_full[st], uint32_t(gj / C::kStages) & 1u)) {
+              ok = false;
+              break;
+            }
+            const uint64_t vd = vd0 + uint64_t((uint32_t(st) * C::kTile) >> 4);
+            for (int h = 0; h < C::kParts; ++h) {
+              if (!wait_all(&p_full[(gj & 1) * C::kParts + h], uint32_t(gj >> 1) & 1u)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int ks = 0; ks < C::kPart / 16; ++ks) {
+                  const uint64_t off = uint64_t((uint32_t(h * C::kPart) * 128u + uint32_t(ks) * 2048u) >> 4);
+                  mma_bf16_ts(tmem + C::kO + uint32_t(h * kD), sb + uint32_t(C::kPart * h + 8 * ks), vd + off, idesc_o,
+                              (j > 0 || ks > 0) ? 1u : 0u);
+                }
+                if (h == C::kParts - 1) {
+                  tc_commit(&o_done[gj & 1]);
+                  tc_commit(&v_empty[st]);
+                }
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
           }
-          if (!ok) break;
         }
+        if (!ok) break;
+        if (!is_s && elect_one()) tc_commit(o_final);
+        __syncwarp();
+        base += n;
+        ++si;
       }
-      if (!ok) break;
-      if (!is_s && elect_one()) tc_commit(o_final);
+      if (elect_one()) tc_commit(&drained[is_s ? 0 : 1]);
       __syncwarp();
-      base += n;
-      ++si;
-    }
-    if (elect_one()) tc_commit(&drained[is_s ? 0 : 1]);
-    __syncwarp();
-    mbar_wait(&drained[is_s ? 0 : 1], 0, drain_limit_ns(lim));
-  } else if (warp == 3) {
-    fewer_registers<C::kPlainRegs>();
-    // ----------------------------------------------------------- segments
-    // Finds the run's segments for the softmax warps, up to two ahead, with the
-    // ancestors of their trees (7000 cycles a segment when every softmax warp walked
-    // the paths of its rows), and brings their Q rows to the L2 cache.
-    Walk walk(run);
-    for (int si = 0;; ++si) {
-      const int sl = si & 1;
-      if (si >= 2 && !__all_sync(0xFFFFFFFFu, wait(&seg_empty[sl], uint32_t((si >> 1) - 1) & 1u))) break;
-      Seg s;
-      const bool more = walk.next(p, run, s);
-      if (lane == 0) {
-        if (more) segs[sl].seg = s;
-        segs[sl].more = more;
-        mbar_arrive(&seg_full[sl]);
-      }
-      if (more) {
-        for (int x = lane; x < 128; x += 32) {
-          const int rr = s.tile * 128 + x;
-          if (rr < s.n * p.G) {
-            const int tok = rr / p.G;
-            const uint16_t* row = p.Q + s.b * p.q_b + tok * p.q_t + (int64_t(s.h) * p.G + rr - tok * p.G) * p.q_h;
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
-            if (kD == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64));
+      mbar_wait(&drained[is_s ? 0 : 1], 0, drain_limit_ns(lim));
+    } else if (warp == 3) {
+      // ----------------------------------------------------------- segments
+      // Finds the run's segments for the softmax warps, up to two ahead, with the
+      // ancestors of their trees (7000 cycles a segment when every softmax warp walked
+      // the paths of its rows), and brings their Q rows to the L2 cache.
+      Walk walk(run);
+      for (int si = 0;; ++si) {
+        const int sl = si & 1;
+        if (si >= 2 && !__all_sync(0xFFFFFFFFu, wait(&seg_empty[sl], uint32_t((si >> 1) - 1) & 1u))) break;
+        Seg s;
+        const bool more = walk.next(p, run, s);
+        if (lane == 0) {
+          if (more) segs[sl].seg = s;
+          segs[sl].more = more;
+          mbar_arrive(&seg_full[sl]);
+        }
+        if (more) {
+          for (int x = lane; x < 128; x += 32) {
+            const int rr = s.tile * 128 + x;
+            if (rr < s.n * p.G) {
+              const int tok = rr / p.G;
+              const uint16_t* row = p.Q + s.b * p.q_b + tok * p.q_t + (int64_t(s.h) * p.G + rr - tok * p.G) * p.q_h;
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+              if (kD == 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64));
+            }
+          }
+          if (p.parents) {
+            ancestors_of(p.parents + int64_t(s.b) * p.T, p.T, ancs + sl * 128, reinterpret_cast<int*>(ancs + 256), p.status);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&anc_full[sl]);
           }
         }
-        if (p.parents) {
-          ancestors_of(p.parents + int64_t(s.b) * p.T, p.T, ancs + sl * 128, reinterpret_cast<int*>(ancs + 256), p.status);
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&anc_full[sl]);
-        }
+        if (si == 0) zero_idle_rows<kD>(p);
+        if (!more) break;
       }
-      if (si == 0) zero_idle_rows<kD>(p);
-      if (!more) break;
     }
   } else if (warp >= C::kRest) {
     fewer_registers<C::kRestRegs>();
@@ -652,7 +653,8 @@ __global__ void __launch_bounds__(TileCfg<kD>::kThreads, 1) kv4_attn_tile_kernel
         }
         // The K warps publish both exponents: the softmax then waits for K alone.
         if (is_k && lane == 0)
-          exps[(gj % C::kExpRing) * 4 + (i >> 5)] = make_float4(p.c * pow2(e - 8), float(f), pow2(-f), key_apart ? 1.f : 0.f);
+          exps[(gj % C::kExpRing) * 4 + (i >> 5)] =
+              make_float4(p.c * pow2(e - 8), float(f), pow2(-f), key_apart ? 1.f : 0.f);
         if (is_k && key_apart) key_exps[(gj % C::kExpRing) * 128 + i] = make_float2(p.c * pow2(e - 8), float(f));
         uint8_t* tile = tiles + st * C::kTile;
 #pragma unroll

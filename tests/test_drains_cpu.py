@@ -1,4 +1,4 @@
-"""Copies into shared memory and the waits for them, where one may expire.
+"""Copies into shared memory and the waits for them, where one may expire; shares of registers.
 
 A thread block may not end while a copy that it has requested can still land in its
 shared memory: the memory may be another block's by then. A wait of another warp can
@@ -60,3 +60,17 @@ def test_log_probabilities_free_no_stage_whose_copy_they_have_not_seen():
     assert arrivals and all("landed" in a for a in arrivals)
     assert re.search(r"mine = go && \w*(::)?mbar_wait\w*\(&s\.full\[st\]", src)
     assert re.search(r"landed = __all_sync\(0xFFFFFFFFu, mine\)", src)
+
+
+def test_a_warpgroup_changes_its_registers_by_one_instruction():
+    """Warps of one group that meet different instructions for it are undefined, and a sum of
+    shares above the launch's registers waits for good."""
+    src = open(os.path.join(B.CSRC, "w12_kv4_tile.cuh")).read()
+    kernel = src[src.index("__global__"):]
+    calls = re.findall(r"if \(([^)]*)\) \{\n(?:\s*//[^\n]*\n)*\s*(?:fewer|more)_registers<C::(\w+)>\(\)", kernel)
+    assert calls == [("warp < 4", "kPlainRegs"), ("warp >= C::kRest", "kRestRegs"), ("warp >= 4", "kSoftRegs")]
+    assert len(re.findall(r"(?:fewer|more)_registers<C::", kernel)) == 3
+    regs = dict(re.findall(r"(k\w+Regs) = (\d+)", src))
+    warps = {"kPlainRegs": 4, "kRestRegs": 8, "kSoftRegs": 8}
+    assert sum(n * int(regs[k]) for k, n in warps.items()) <= 20 * int(regs["kLaunchRegs"])
+    assert all(int(v) % 8 == 0 for v in regs.values())
