@@ -438,10 +438,12 @@ int w12_kv4_commit(const w12_kv4* caches, int n_caches, int B, const int32_t* ta
  * are zero. Positions that no token sees may hold anything, values that are
  * not finite among them. max_kv_len (host) bounds prefix_len[b] + q_len[b] and
  * is at most max_pages * page_size; table [B, max_pages] int32. Products
- * take fp16 operands (a query row over a power of two; a weight to 2^-11 of
- * itself, or, counted with its value row's size, to 2^-30 of the largest; a value of a key or value row to 2^-11 of itself, or to 2^-16 of
- * the row's |z| + 8 s where that is more, whatever other rows hold) and sum in
- * fp32; scores, softmax and sums are fp32. Device-side errors: W12_ERR_ARG (lengths out of
+ * take fp16 operands and sum in fp32; scores, softmax and sums are fp32. The
+ * operands' roundings: a value of a key or value row to 2^-11 of itself, or to
+ * 2^-16 of the row's |z| + 8 s where that is more, whatever other rows hold; a
+ * weight to 2^-11 of itself or, counted with its value row's size, to 2^-30 of
+ * the largest; queries, over a power of two a row, exactly down to 2^-24 of the
+ * row's largest. Device-side errors: W12_ERR_ARG (lengths out of
  * range: taken clamped; a page outside the pool: outputs unspecified),
  * W12_ERR_BAD_TREE (that request's outputs are unspecified), W12_ERR_TIMEOUT. The
  * workspace follows the rules at the top. Returns W12_ERR_ARG,

@@ -9,10 +9,12 @@
 gate_up -> SwiGLU -> down inside the launch).
 --op attn runs the tree-masked verify attention (40 q / 8 kv heads x 128) for
 --B requests x --T-node random trees over a --P-token prefix.
---op kv4 runs attention over the paged 4-bit cache (40 q / 8 kv heads x 128,
-pages of 64) for --B requests x --T drafted tokens (a random tree with --tree)
-over a --P-token prefix; --op kv4_append quantises --B x --P rows into it and
---op logprobs takes --M rows of bf16 logits over 151,936 tokens (top --k).
+--op kv4 runs attention over the paged 4-bit cache (--Hq q heads, 8 kv heads x
+--d, pages of 64) for --B requests x --T drafted tokens (a random tree with
+--tree) over a --P-token prefix; --op kv4_append and kv4_read quantise --B x
+(--P + --T) rows into it and read them back, kv4_commit moves 7 accepted rows a
+request, pages reserves the pages of --B prompts of --P tokens. --op logprobs
+takes --M rows of logits over 151,936 tokens (top --k; --f32: fp32, else bf16).
 Prints the mean CUDA-event time per launch.
 """
 import argparse
@@ -42,7 +44,8 @@ def check_status(st):
 
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("--op", default="w12", choices=["w12", "bf16", "head", "attn", "step", "layer", "kv4", "kv4_append", "logprobs"])
+    ap.add_argument("--op", default="w12", choices=["w12", "bf16", "head", "attn", "step", "layer", "kv4", "kv4_append", "kv4_read",
+                                                        "kv4_commit", "pages", "logprobs"])
     ap.add_argument("--swiglu", action="store_true")
     ap.add_argument("--B", type=int, default=4)
     ap.add_argument("--T", type=int, default=64)
@@ -52,6 +55,9 @@ def main():
     ap.add_argument("--iters", type=int, default=3)
     ap.add_argument("--tree", action="store_true")
     ap.add_argument("--k", type=int, default=8)
+    ap.add_argument("--Hq", type=int, default=40)
+    ap.add_argument("--d", type=int, default=128)
+    ap.add_argument("--f32", action="store_true")
     a = ap.parse_args()
     N, K = SHAPES[a.shape]
     dev = torch.device("cuda")
@@ -61,7 +67,7 @@ def main():
 
     if a.op == "attn":
         return attn(a, dev)
-    if a.op in ("kv4", "kv4_append", "logprobs"):
+    if a.op in ("kv4", "kv4_append", "kv4_read", "kv4_commit", "pages", "logprobs"):
         return serve(a, dev)
     if a.op == "step":
         return step(a, dev, d)
@@ -147,17 +153,17 @@ def step(a, dev, d):
 
 
 def serve(a, dev):
-    """The paged 4-bit cache's attention or append, or token log probabilities."""
+    """The paged 4-bit cache's attention or row kernels, its page tables, or token log probabilities."""
     torch.manual_seed(0)
     st = torch.zeros(1, dtype=torch.int32, device=dev)
     if a.op == "logprobs":
         M, V = a.M, SHAPES["head"][0]
-        logits = torch.randn((M, V), device=dev).to(torch.bfloat16)
+        logits = torch.randn((M, V), device=dev).to(torch.float32 if a.f32 else torch.bfloat16)
         tokens = torch.randint(0, V, (M, 1), dtype=torch.int32, device=dev)
         lp = w12.TokenLogprobs(M, V, a.k, dev)
         what, fn = f"logprobs {M} x {V} top {a.k}", lambda: lp.run(logits, tokens, status=st)  # noqa: E731
     else:
-        Hq, Hkv, d, page = 40, 8, 128, 64
+        Hq, Hkv, d, page = a.Hq, 8, a.d, 64
         L = a.P + a.T
         width = -(-L // page)
         cache = w12.KV4Cache.create(a.B * width, Hkv, d, page, dev)
@@ -168,6 +174,20 @@ def serve(a, dev):
         cache.append(K, V, slots, status=st)
         if a.op == "kv4_append":
             what, fn = f"append {a.B * L} rows", lambda: cache.append(K, V, slots, status=st)  # noqa: E731
+        elif a.op == "kv4_read":
+            what, fn = f"read {a.B * L} rows", lambda: cache.read(slots, out=(K, V), status=st)  # noqa: E731
+        elif a.op == "kv4_commit":
+            path = torch.arange(0, 14, 2, dtype=torch.int32, device=dev).expand(a.B, 7).contiguous()
+            n, new = torch.full_like(prefix, 7), torch.empty_like(prefix)
+            what = f"commit 7 rows of {a.B} requests"
+            fn = lambda: w12.kv4_commit([cache], pages.table, prefix, path, n, new_len=new, status=st)  # noqa: E731
+        elif a.op == "pages":
+            zero, out = torch.zeros_like(prefix), torch.empty((a.B, L), dtype=torch.int32, device=dev)
+            what = f"slots and pages of {a.B} prompts of {L} tokens, and their release"
+
+            def fn():
+                pages.trim(zero, status=st)
+                pages.reserve(zero, prefix + a.T, L, slots=out, status=st)
         else:
             Q = torch.randn((a.B, a.T, Hq, d), device=dev).to(torch.bfloat16)
             par = None

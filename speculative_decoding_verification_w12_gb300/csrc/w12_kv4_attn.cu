@@ -14,10 +14,16 @@ static bool shape_ok(int B, int T, int Hq, int Hkv, int head_dim, int page_size,
 }
 
 // How a call is run: by T G, the rows a kv head has. Up to 8 rows go to the rows kernel
-// in one 8-row tile, up to 16 in two, more to 128-row tiles. 64 requests of up to 8192
-// tokens, us, rows kernel against tiles: 1 row 97 / 181, 5 rows 100 / 182, 8 rows 103 /
-// 180; 10 rows 255 / 278 (no short requests among them), 16 rows 190 / 181. One request
-// of 777 tokens, 10 rows: 13.7 / 20.0, so two 8-row tiles are kept up to 16.
+// in one 8-row tile, up to 16 in two, more to 128-row tiles. 8 kv heads, pages of 64, us,
+// rows kernel / tiles:
+//             1 x 777      1 x 8192     16 x 2048    16 x 8192    64 x 2048-8192
+//   d 128  9  13.5 / 19.2  19.9 / 33.7  33.9 / 41.3  74.5 / 85.7  194 / 197
+//         12  15.1 / 18.2  22.9 / 32.1  35.5 / 40.7  76.4 / 85.4  205 / 198
+//         16  15.8 / 18.4  23.7 / 32.2  36.5 / 40.6  77.5 / 85.3  208 / 198
+//   d  64  9   9.4 / 16.0  13.2 / 26.8  23.7 / 32.9  50.3 / 71.0  132 / 165
+//         16  11.0 / 14.8  16.2 / 26.0  25.1 / 31.9  51.6 / 70.3  141 / 164
+// (one tile, 64 requests: 1 row 97 / 181, 8 rows 103 / 180). The two 8-row tiles lose by 3 to
+// 5 % in one corner, 11 rows or more at d 128 over more than 300 MB, and win elsewhere.
 struct Plan {
   int kind;   // few rows: their 8-row tiles (1 or 2); 0: 128-row tiles
   int ntile, rows;

@@ -2,11 +2,12 @@
 // short blocks): streams the codes and multiplies them in registers.
 //
 // The floor is HBM: d + 8 bytes a (key, kv head) against at most 16 rows of work.
-// 64 requests of 2048 to 8192 tokens (40 q / 8 kv heads x 128, 332 MB): 100 us, 3.3
-// TB/s, 49 % of a copy's rate. What bounds it is the issue of about 380 instructions a
+// 64 requests of 2048 to 8192 tokens (40 q / 8 kv heads x 128, 332 MB): 102 us, 3.3
+// TB/s, 48 % of a copy's rate. What bounds it is the issue of about 380 instructions a
 // 16-key group by seven warps a CTA, two CTAs an SM (59 % of the issue slots, the logic
 // pipe 51 % busy): registers (128 a thread) allow no more warps, and nine a CTA at 96
-// registers spill and take 106 us.
+// registers spill and take 106 us. (Two 8-row tiles at d = 128 run eleven warps at 168
+// registers and spill 100 bytes.)
 // A copy warp brings 128 keys at a time (their pages' blocks, one bulk copy
 // each) into a ring in shared memory; each of the other warps takes groups of
 // 16 keys. With few rows, a tensor-memory tile of 128 rows would be nearly
@@ -21,9 +22,11 @@
 // z + s (q - 8) = (z - 8 s) + s q
 //   score = c 2^a (s (q^.q) + (z - 8 s) sum(q^)),   c = scale log2(e)
 //   o     = sum p~ (q - 8) + sum p~ z/s,            p~ = fp16(p s)
-// with products exact: the one rounding is p~, which stands for the weight p~/s of the
-// whole value (2^-11 relative; with p z in place of p~ z/s the rounding would show where
-// the two cancel). The powers of two of the K nibbles' places are made up for in Q (even
+// with operands exact but for p~, which stands for the weight p~/s of the whole value (2^-11
+// relative; with p z in place of p~ z/s the rounding would show where the two cancel). What is
+// left are the sums: those of p~ (q - 8) and of p~ z/s round apart, in fp32, so next to a key
+// with nearly all of the weight an output is off by up to a few 2^-24 of that key's 8 s; and the
+// tensor cores sum products of subnormals with fewer bits (see key_codes). The powers of two of the K nibbles' places are made up for in Q (even
 // pairs of dims times 16). A row of Q is held as q^ = q / 2^a, a power of two that keeps
 // it in the fp16 range.
 //

@@ -2,11 +2,12 @@
 // trees, prompt chunks): 128-row tiles on the tensor memory.
 //
 // The floor is the tensor pipe (1024 cycles a tile and block at d = 128), or HBM for a
-// single tile of rows. 4 trees of 64 nodes over 32768 tokens: 204 us, 0.84 PFLOP/s of
-// the 320 rows, 43 % of the measured bf16 rate; 16 blocks of 16 over 8192: 82 us, 27 % of
-// either bound; prompt chunk 2 x 2048 (d 64): 140 us. A block takes 2300 cycles of a
-// CTA: the softmax and restore warps (two of each a scheduler) issue 51 % of the slots
-// and wait on one another's and on tensor-memory latencies for the rest.
+// single tile of rows. 4 trees of 64 nodes over 32768 tokens: 211 us, 0.81 PFLOP/s of
+// the 320 rows, 42 % of the measured bf16 rate; 16 blocks of 16 over 8192: 86 us, 26 % of
+// either bound; prompt chunk 2 x 2048 (d 64): 142 us. A block takes 2400 cycles of a
+// CTA: the softmax and restore warps (two of each a scheduler) issue 48 to 50 % of the
+// slots (60 % at d = 64) and wait on one another's and on tensor-memory latencies for the
+// rest.
 //
 // Work unit: 128 query rows of one (request, kv head), token-major, against one
 // block of 128 keys (the split is w12_kv4_sched.cuh's). Per block:
@@ -26,8 +27,9 @@
 // zeros); otherwise each of the 32 keys has its own. So a row keeps its values to 2^-11
 // relative or 2^-16 of its own bound, whatever stands beside it: a key of another
 // size, seen or masked, does not coarsen it. (Exponents a key for all would cost the
-// softmax two loads and three operations more for each pair of scores. As it is, finding
-// out takes trees 210.5 us where one exponent for any 32 rows takes 205, blocks 85 for 82.)
+// softmax two loads and three operations more for each pair of scores. As it is, trees
+// take 211 us where one exponent for any 32 rows took 205, blocks 86 for 82, the prompt
+// chunk 142 for 140.)
 // The tile holds K / 2^e and V / 2^(f + 8), and a row of Q is held over its own power
 // of two 2^a. With
 //   y_ij = c 2^(a_i + e_j) S_ij + f_j,       c = scale log2(e)
@@ -109,8 +111,8 @@ struct TileCfg {
   static constexpr int kThreads = (kRest + 8) * 32;
   // Registers a thread from the role's start on, of the 96 that the launch has for each
   // (checked there): the softmax, with code of its own for keys that have exponents of
-  // their own, spills at 96 (blocks 89 us for 86, prompt chunk 146 for 143.5). A warpgroup
-  // changes its registers by one instruction that all its warps meet.
+  // their own, spills at 96 (blocks 89 us for 85, trees 217 for 210.5). A warpgroup changes
+  // its registers by one instruction that all its warps meet.
   static constexpr int kLaunchRegs = 96, kPlainRegs = 88, kSoftRegs = 112, kRestRegs = 80;
   static_assert(kPlainRegs * 4 + kSoftRegs * kSoft + kRestRegs * 8 <= kLaunchRegs * (kThreads / 32),
                 "the launch's registers");
@@ -304,9 +306,9 @@ __device__ __forceinline__ void ancestors_of(const int32_t* parents, int T, uint
   }
 }
 
-// A softmax warp's share of a segment's Q rows into the swizzled fp16 Q tile: each over a power of two 2^ra[row] that brings it below 2^10, so that
-// c 2^(e - 8) and 2^(ra + 8) have room up to the largest values. A row with NaN or
-// infinities stays one.
+// A softmax warp's share of a segment's Q rows into the swizzled fp16 Q tile: each over a
+// power of two 2^ra[row] that brings it below 2^10, so that c 2^(e - 8) and 2^(ra + 8) have
+// room up to the largest values. A row with NaN or infinities stays one.
 template <int kD>
 __device__ __forceinline__ void load_q(const Params& p, const Seg& s, int share, uint8_t* tile, int* ra) {
   constexpr int kRows = 128 / TileCfg<kD>::kSoft;

@@ -12,8 +12,8 @@
 //   S1 = sum 2^d_i (s1_i + d_i s0_i), lse = M + log S0, entropy = log S0 - ln 2 S1 / S0,
 // and likewise a row's runs by the one that finishes last. Sums are fp32: at most
 // a run's share of a thread, then trees. 256 rows of
-// 151,936 bf16 logits: 21.8 us without a list (3.6 TB/s, half a copy's rate), 33.7 us
-// with the 8 largest (2.3 TB/s); 16 fp32 rows 6.3 us and, with the 20 largest, 12.1.
+// 151,936 bf16 logits: 21.8 us without a list (3.6 TB/s, half a copy's rate), 33.8 us
+// with the 8 largest (2.3 TB/s); 16 fp32 rows 6.4 us and, with the 20 largest, 12.3.
 // Bound by issue (58 % of the slots) and the barriers of the lists for many rows, by
 // launch and join latency for few.
 //
