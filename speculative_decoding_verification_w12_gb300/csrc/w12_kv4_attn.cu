@@ -22,7 +22,7 @@ static bool shape_ok(int B, int T, int Hq, int Hkv, int head_dim, int page_size,
 //         16  15.8 / 18.4  23.7 / 32.2  36.5 / 40.6  77.5 / 85.3  208 / 198
 //   d  64  9   9.4 / 16.0  13.2 / 26.8  23.7 / 32.9  50.3 / 71.0  132 / 165
 //         16  11.0 / 14.8  16.2 / 26.0  25.1 / 31.9  51.6 / 70.3  141 / 164
-// (one tile, 64 requests: 1 row 97 / 181, 8 rows 103 / 180). The two 8-row tiles lose by 3 to
+// (one tile, d 128, 64 requests: 1 row 104 / 203, 8 rows 113 / 200). The two 8-row tiles lose by 3 to
 // 5 % in one corner, 11 rows or more at d 128 over more than 300 MB, and win elsewhere.
 struct Plan {
   int kind;   // few rows: their 8-row tiles (1 or 2); 0: 128-row tiles
