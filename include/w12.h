@@ -476,6 +476,98 @@ int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ro
                  const int32_t* tokens, int n, int k, float* logprob, float* entropy, float* lse,
                  float* top_logprob, int32_t* top_id, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
 
+/* --- Position rotation and norms of query and key heads ------------------- */
+/* A head's row x of head_dim (64 or 128) values, of a token at position pos:
+ *   y = (x r) w, r = 1 / sqrt(mean x^2 + eps), where the norm's weights w are given;
+ *   of the first rot_dim values (a multiple of 16) the pairs (i, i + rot_dim/2),
+ *   or with `interleaved` (2i, 2i + 1), become (y_i c - y_j s, y_j c + y_i s),
+ *   c = table[pos][i], s = table[pos][rot_dim/2 + i]; the rest stays as it is.
+ * All in fp32, each product and sum rounded by itself, r the fp32 value next to
+ * the exact one: a row's result depends on the row alone. table is fp32
+ * [max_pos, rot_dim], the weights fp32 [head_dim] or NULL (no norm), all 16-byte
+ * aligned; 1e-12 <= eps. A row whose position is -1 is no token: its output is
+ * zeros. So is one of another position outside [0, max_pos), which sets
+ * W12_ERR_ARG in dev_status. */
+typedef struct w12_rope {
+  const float* table;
+  int64_t max_pos;
+  int rot_dim, interleaved;
+  const float* q_norm;
+  const float* k_norm;
+  float eps;
+} w12_rope;
+
+/* Q [n, Hq, head_dim] and K [n, Hkv, head_dim] (either may be NULL) of type dtype
+ * with element strides of any sign, into Q_out and K_out, contiguous, of type
+ * out_dtype, 16-byte aligned, not overlapping the inputs. positions int32 [n].
+ * Rows whose base and strides are multiples of 16 bytes are read in wide loads.
+ * Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
+int w12_qk_norm_rope(const w12_rope* rope, int head_dim, const void* Q, int64_t q_token_stride, int64_t q_head_stride, int Hq,
+                     const void* K, int64_t k_token_stride, int64_t k_head_stride, int Hkv, int dtype, int64_t n,
+                     const int32_t* positions, void* Q_out, void* K_out, int out_dtype, int32_t* dev_status, void* stream);
+
+/* w12_kv4_append with the rotation on the way: K's rows are normed and rotated
+ * before they are quantised, bitwise as w12_qk_norm_rope to fp32 and
+ * w12_kv4_append would; V's are quantised as they are. Q (NULL: none) of the same
+ * rows goes normed and rotated to Q_out, bf16 [n, Hq, head_dim]. A row whose
+ * position or slot is -1 is not cached. Errors as there and above. */
+int w12_kv4_append_rope(const w12_kv4* cache, const w12_rope* rope, const void* Q, int64_t q_token_stride, int64_t q_head_stride,
+                        int Hq, const void* K, int64_t k_token_stride, int64_t k_head_stride, const void* V,
+                        int64_t v_token_stride, int64_t v_head_stride, int dtype, int64_t n, const int32_t* positions,
+                        const int32_t* slots, uint16_t* Q_out, int32_t* dev_status, void* stream);
+
+/* Positions of new tokens, int32 [B, T]: prefix_len[b] + t, or with parents [B, T]
+ * (T <= 256; parents[b, 0] = -1, 0 <= parents[b, i] < i) prefix_len[b] + the depth
+ * of node t; -1 from q_len[b] (NULL: T) on. Lengths out of range set W12_ERR_ARG, a
+ * malformed tree W12_ERR_BAD_TREE, and that request's positions are -1. Errors:
+ * W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
+int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const int32_t* q_len, int B, int T, int32_t* positions,
+                       int32_t* dev_status, void* stream);
+
+/* --- Attention over whole prompts ----------------------------------------- */
+/* B sequences packed one behind the other: sequence b is the rows cu_seqlens[b] ..
+ * cu_seqlens[b + 1] - 1 (int32 [B + 1], not decreasing) of Q [total, Hq, head_dim] and of K
+ * and V [total, Hkv, head_dim]:
+ *   O[i, h, :] = sum_{j <= i} softmax_j(scale * Q[i, h, :] . K[j, h / (Hq/Hkv), :]) * V[j, ..]
+ * over the rows j of i's sequence. dtype W12_BF16 or W12_F16, of Q, K, V and O; O
+ * [total, Hq, head_dim] contiguous, its rows outside the sequences left as they are.
+ * Element strides are positive multiples of 8, pointers 16-byte aligned; head_dim 64
+ * or 128, Hq / Hkv <= 128, total < 2^31 - 256. Sequences of no rows are fine. One with offsets
+ * out of [0, total], or decreasing ones, sets W12_ERR_ARG and is taken as empty. Rows
+ * that a row does not see have no part in it, whatever they hold. Scores, softmax and sums are fp32; a weight
+ * meets the values rounded to their type (bf16: 2^-8 of itself, fp16: 2^-11 of itself
+ * or 2^-25 of the row's largest). A score of -inf weighs nothing; a row with no other
+ * is zeros. No workspace. Device-side errors besides: W12_ERR_TIMEOUT. Returns
+ * W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED or W12_ERR_CUDA. */
+int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_stride, const void* K, int64_t k_token_stride,
+                         int64_t k_head_stride, const void* V, int64_t v_token_stride, int64_t v_head_stride, int dtype,
+                         int64_t total, const int32_t* cu_seqlens, int B, int Hq, int Hkv, int head_dim, float scale, void* O,
+                         int32_t* dev_status, void* stream);
+
+/* --- Low-rank adapters beside a shared projection -------------------------- */
+/* n adapters of one projection K -> N: A bf16 [n, rank, K], B bf16 [n, N, rank], scale
+ * fp32 [n], 16-byte aligned (scale: 4). rank a multiple of 8 up to 128, K of 8, N of 16. */
+typedef struct w12_adapters {
+  const uint16_t* A;
+  const uint16_t* B;
+  const float* scale;
+  int64_t N, K;
+  int n, rank;
+} w12_adapters;
+
+/* Y[m, :] += scale[a] * B[a] (A[a] X[m, :]), a = ids[m], for M <= 256 rows of X bf16
+ * [M, K] and Y fp32 [M, N], as the product of that layer left them; rows x_stride (a multiple of 8)
+ * and y_stride (of 4) elements apart, 16-byte aligned. ids int32 [M]: -1 is no
+ * adapter, and the row of Y is not touched; another id outside [0, n) is taken so and
+ * sets W12_ERR_ARG in dev_status. Products of bf16 values are summed in fp32, A X is
+ * kept to 2^-24 of itself. The workspace needs no zero fill, holds nothing between
+ * calls, and follows the other rules at the top. Errors: W12_ERR_ARG,
+ * W12_ERR_SHAPE, W12_ERR_WORKSPACE, W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
+size_t w12_lora_ws_bytes(int64_t M, int n_adapters, int rank);
+
+int w12_lora(const uint16_t* X, int64_t x_stride, int64_t M, const w12_adapters* adapters, const int32_t* ids, float* Y,
+             int64_t y_stride, void* ws, size_t ws_bytes, int32_t* dev_status, void* stream);
+
 /* --- Diagnostics -------------------------------------------------------- */
 
 /* Launch a kernel that waits on a barrier nothing arrives at, with a bound of

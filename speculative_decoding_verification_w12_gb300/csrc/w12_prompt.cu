@@ -1,0 +1,713 @@
+// Causal attention over whole prompts, packed one behind the other:
+//   O[i, h] = sum_{j <= i} softmax_j(scale Q[i, h] . K[j, h / G]) V[j, h / G],
+// i and j tokens of one sequence, G = Hq / Hkv query heads for each kv head.
+//
+// Rows of a tile are (token, head of the group), token-major, 128 / G tokens: a key block is
+// read once for the whole group, and few of a tile's keys are cut by the diagonal. An item is
+// two such tiles, one behind the other, of one (sequence, kv head), with all keys that they
+// see in blocks of 128. The kernel is persistent; items go out longest first, in rounds of
+// the grid that alternate in direction, so every block gets about the same work and nothing
+// is counted in memory. Per key block and tile:
+//   S = Q K^T         tcgen05.mma, both from shared memory, S in TMEM;
+//   P = 2^(c S - m)   a warpgroup for each tile, a row a thread: the running maximum moves only
+//                     when a block's passes it by 2^8, so O is rescaled rarely; P goes over
+//                     the first half of S's columns, in two halves of 64 keys;
+//   O += P V          tcgen05.mma, P from TMEM, V from shared memory (MN-major).
+// While one tile is in the softmax the tensor cores work for the other.
+//
+// P enters O rounded to the type of V (bf16: 2^-8 of itself; fp16: 2^-11, or 2^-25 of the
+// largest weight), its sum is of the unrounded P; scores, maxima, sums and O are fp32.
+//
+// Masked places may hold anything. Masked scores are replaced, not added to. A value that is
+// not finite would turn the zero weights of rows that do not see it into NaN: a warp looks
+// through the V blocks that the diagonal cuts, takes such values out of shared memory and
+// notes their keys, and rows that see one add it at the end.
+//
+// Warps: 0-3 and 4-7 softmax and epilogue of the two tiles, 8 copies (and hands out the items),
+// 9 and 10 issue the products of the two tiles, 11 looks through V.
+#include <atomic>
+
+#include "w12_attn_dev.cuh"
+#include "w12_host.h"
+
+namespace w12 {
+namespace prompt_impl {
+
+using namespace attn_impl;
+
+constexpr int kKeys = 128;
+constexpr int kThreads = 384;
+constexpr float kRescale = 8.0f;   // log2 growth of the maximum that triggers a rescale
+constexpr int kItems = 4;          // items handed out ahead
+constexpr int kItemReaders = 11;   // warps that read an item
+
+template <int kD>
+struct Cfg {
+  static constexpr int kHalves = kD / 64;                      // 128-byte pieces of a row
+  static constexpr uint32_t kHalf = 128u * 128u;               // 128 rows of one piece
+  static constexpr uint32_t kTile = kHalves * kHalf;
+  static constexpr int kStages = kD == 128 ? 5 : 10;           // K and V blocks in turn
+  static constexpr uint32_t kRing = 2 * kTile;                 // behind the two tiles' Q
+  static constexpr uint32_t kBar = kRing + kStages * kTile;
+  static constexpr uint32_t kSmem = kBar + 1024 + 1024;        // barriers, items; alignment
+  static constexpr uint32_t kColS = 0, kColO = 256;            // S of tile i at 128 i, O at 256 + 128 i
+};
+
+struct Item {
+  int first;   // token of the buffer that the first tile begins with
+  int t0;      // its place in the sequence
+  int len;     // tokens of the sequence
+  int head;    // kv head; -1: no more items
+};
+
+struct Params {
+  const void* V;               // for values that are not finite
+  int64_t v_tok, v_head;       // strides in elements
+  void* O;                     // [total, Hq, kD]
+  const int32_t* cu;           // [B + 1]
+  int32_t* status;
+  int64_t total;
+  int B, Hq, Hkv, G, tpt;      // tpt: tokens a tile
+  float c;                     // scale log2(e)
+  uint64_t limit_ns;
+};
+
+// A box of (dims from x on, head y, token z on) rows; the maps' fourth extent is 1.
+__device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(0), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// Key blocks of a tile that begins at token t0 (none past the sequence's end), and the first
+// of them that some row of the tile does not see whole.
+__device__ __forceinline__ int blocks_of(int t0, int tpt, int len) {
+  return t0 >= len ? 0 : (min(t0 + tpt, len) + kKeys - 1) / kKeys;
+}
+__device__ __forceinline__ int first_cut(int t0) { return (t0 + 1) / kKeys; }
+
+// Walks the items in their order, longest first: by place in the sequence (in pairs of
+// tiles) from the last down, then sequence, then kv head. Warp-collective.
+struct Walk {
+  const int32_t* cu;
+  int B, Hkv, step;
+  int64_t total;
+  int level;        // pairs before the current ones in their sequences; -1: past the last
+  int chunk;        // of 32 sequences
+  uint32_t left;    // sequences of the chunk that are still to come at this level
+  int head;         // next kv head of the first of them
+  int n, start, len;  // of this lane's sequence of the chunk: pairs, first token, tokens
+
+  __device__ __forceinline__ void load(int32_t* status) {
+    const int lane = threadIdx.x & 31, b = chunk * 32 + lane;
+    start = len = 0;
+    if (b < B) {
+      const int a = cu[b], e = cu[b + 1];
+      if (a < 0 || e < a || e > total) {
+        if (status) set_status(status, W12_ERR_ARG);
+      } else {
+        start = a;
+        len = e - a;
+      }
+    }
+    n = (len + step - 1) / step;
+  }
+  __device__ __forceinline__ void begin(int32_t* status) {
+    level = -1;
+    const int chunks = (B + 31) / 32;
+    for (chunk = chunks - 1; chunk >= 0; --chunk) {
+      load(status);
+      level = max(level, int(__reduce_max_sync(0xFFFFFFFFu, unsigned(n))) - 1);
+    }
+    chunk = 0;
+    if (chunks > 1) load(nullptr);
+    left = __ballot_sync(0xFFFFFFFFu, n > level);
+    head = 0;
+  }
+  // The item `skip` places on.
+  __device__ __forceinline__ Item next(int64_t skip) {
+    const int chunks = (B + 31) / 32;
+    Item it{0, 0, 0, -1};
+    while (level >= 0) {
+      const int64_t here = int64_t(__popc(left)) * Hkv - head;
+      if (skip < here) {
+        const int64_t at = head + skip;
+        for (int64_t k = at / Hkv; k > 0; --k) left &= left - 1;
+        head = int(at % Hkv);
+        const int src = __ffs(left) - 1;
+        it.t0 = level * step;
+        it.first = __shfl_sync(0xFFFFFFFFu, start, src) + it.t0;
+        it.len = __shfl_sync(0xFFFFFFFFu, len, src);
+        it.head = head;
+        return it;
+      }
+      skip -= here;
+      head = 0;
+      if (++chunk == chunks) {
+        chunk = 0;
+        --level;
+      }
+      if (chunks > 1) load(nullptr);
+      left = __ballot_sync(0xFFFFFFFFu, n > level);
+    }
+    return it;
+  }
+};
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (kBf16) return pack_bf16x2(lo, hi);
+  else return pack_f16x2(lo, hi);
+}
+
+// P_k = 2^(c s_k + negm) of 64 scores, packed as pairs into v[0 .. 31] in place (pair k over
+// v[k], which pair k/2 has read); returns the fp32 sum.
+template <bool kBf16>
+__device__ __forceinline__ float weights64(uint32_t* v, float c, float negm) {
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  const float2 c2 = make_float2(c, c), m2 = make_float2(negm, negm);
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const float2 x = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, m2);
+    const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+    sum[k & 1] = add2(sum[k & 1], p);
+    v[k] = pack2<kBf16>(p.x, p.y);
+  }
+  const float2 s = add2(sum[0], sum[1]);
+  return s.x + s.y;
+}
+
+// A value of V's type is finite: all exponent bits set otherwise.
+template <bool kBf16>
+__device__ __forceinline__ bool finite16(uint32_t h) {
+  constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;
+  return (h & kExp) != kExp;
+}
+
+// x with its elements that are not finite replaced by zeros.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
+  return (finite16<kBf16>(x) ? x & 0xFFFFu : 0u) | (finite16<kBf16>(x >> 16) ? x & 0xFFFF0000u : 0u);
+}
+
+// acc + 0 x, as pairs: NaN in either half once an element of x is not finite.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t spot(uint32_t x, uint32_t acc) {
+  uint32_t r;
+  if constexpr (kBf16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
+  return r;
+}
+
+template <int kD, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params P) {
+  using C = Cfg<kD>;
+  constexpr int kStages = C::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint4* bad = reinterpret_cast<uint4*>(smem + C::kBar);  // [kStages]: keys of a V block with values taken out
+  uint64_t* full = reinterpret_cast<uint64_t*>(bad + kStages);  // [kStages]: block landed
+  uint64_t* empty = full + kStages;       // [kStages]: both tiles' products of the stage's block done
+  uint64_t* clean = empty + kStages;      // [kStages]: block looked through, where it is a V block with a cut
+  uint64_t* q_full = clean + kStages;     // [2]: tile's Q landed
+  uint64_t* q_empty = q_full + 2;         // [2]: the item's last S of the tile done
+  uint64_t* s_full = q_empty + 2;         // [2]: S of the tile's block
+  uint64_t* p_full = s_full + 2;          // [2][2]: P of the tile's block, key half h
+  uint64_t* o_done = p_full + 4;          // [2]: P V of the tile's block done
+  uint64_t* o_free = o_done + 2;          // [2]: the item's O read
+  uint64_t* drained = o_free + 2;         // [2]: all products of a tile's thread done
+  uint64_t* it_full = drained + 2;        // [kItems]
+  uint64_t* it_empty = it_full + kItems;  // [kItems]
+  Item* items = reinterpret_cast<Item*>(it_empty + kItems);       // [kItems]
+  uint32_t* misc = reinterpret_cast<uint32_t*>(items + kItems);
+  volatile uint32_t* tmem_slot = misc;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
+  volatile int* copied = reinterpret_cast<volatile int*>(misc + 2);  // blocks requested
+  volatile int* q_copied = reinterpret_cast<volatile int*>(misc + 3);  // [2]: Q tiles requested
+  static_assert(16 * kStages + (3 * kStages + 16 + 2 * kItems) * 8 + 16 * kItems + 20 <= 1024, "barriers");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 2);   // one commit a tile
+      mbar_init(&clean[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[2 * i], 128);
+      mbar_init(&p_full[2 * i + 1], 128);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&o_free[i], 128);
+      mbar_init(&drained[i], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&it_full[i], 1);
+      mbar_init(&it_empty[i], kItemReaders);
+    }
+    *abort_flag = 0;
+    copied[0] = q_copied[0] = q_copied[1] = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 9) {
+    tmem_alloc(const_cast<uint32_t*>(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  cta_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint64_t lim = P.limit_ns;
+  // Everything below reads what the previous kernel on the stream wrote.
+  grid_dep_wait();
+
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t i = 0; i < 0x80000000u; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if ((i & 63u) == 63u) {
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > lim) break;
+      }
+    }
+    set_status(P.status, W12_ERR_TIMEOUT);
+    *abort_flag = 1;
+    return false;
+  };
+  // One decision for the warp: what follows is warp-collective.
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, wait(bar, parity)); };
+  // The k-th item of this block, for a whole warp.
+  auto get_item = [&](int k, Item& it) -> bool {
+    if (!wait_all(&it_full[k % kItems], uint32_t(k / kItems) & 1u)) return false;
+    it = items[k % kItems];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&it_empty[k % kItems]);
+    return it.head >= 0;
+  };
+
+  if (warp == 8) {
+    // --------------------------------------------------------- items, copies
+    Walk walk{P.cu, P.B, P.Hkv, 2 * P.tpt, P.total};
+    walk.begin(blockIdx.x == 0 ? P.status : nullptr);
+    int issued = 0, q_issued[2] = {0, 0};
+    bool ok = true;
+    const int grid = int(gridDim.x), me = int(blockIdx.x);
+    int64_t skip = me;
+    auto stage = [&](const CUtensorMap* map, int head, int token) -> bool {
+      const int s = issued % kStages;
+      if (issued >= kStages && !wait(&empty[s], uint32_t(issued / kStages - 1) & 1u)) return false;
+      uint8_t* at = smem + C::kRing + uint32_t(s) * C::kTile;
+      mbar_arrive_expect_tx(&full[s], C::kTile);
+      for (int h = 0; h < C::kHalves; ++h) load_box(at + h * C::kHalf, map, 64 * h, head, token, &full[s]);
+      ++issued;
+      return true;
+    };
+    for (int k = 0; ok; ++k) {
+      const Item it = walk.next(skip);
+      // Rounds alternate in direction: place `me` of even rounds, `grid - 1 - me` of odd ones.
+      skip = (k & 1) ? 2 * me : 2 * (grid - 1 - me);
+      // (walk.next leaves the walk on the item: the next one is skip + 1 places on.)
+      ++skip;
+      if (lane == 0) {
+        if (k >= kItems) ok = wait(&it_empty[k % kItems], uint32_t(k / kItems - 1) & 1u);
+        if (ok) {
+          items[k % kItems] = it;
+          mbar_arrive(&it_full[k % kItems]);
+        }
+        if (ok && it.head >= 0) {
+          const int seq = it.first - it.t0;
+          const int n0 = blocks_of(it.t0, P.tpt, it.len), n1 = blocks_of(it.t0 + P.tpt, P.tpt, it.len);
+          const int n = max(n0, n1);
+          for (int j = 0; ok && j < n; ++j) {
+            ok = stage(&tm_k, it.head, seq + j * kKeys);
+            if (j == 0) {
+              for (int i = 0; ok && i < (n1 ? 2 : 1); ++i) {
+                if (q_issued[i] > 0) ok = wait(&q_empty[i], uint32_t(q_issued[i] - 1) & 1u);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&q_full[i], uint32_t(kD * 2 * P.G * P.tpt));
+                for (int h = 0; h < C::kHalves; ++h)
+                  load_box(smem + uint32_t(i) * C::kTile + h * C::kHalf, &tm_q, 64 * h, it.head * P.G, it.first + i * P.tpt,
+                           &q_full[i]);
+                ++q_issued[i];
+              }
+            }
+            if (ok) ok = stage(&tm_v, it.head, seq + j * kKeys);
+          }
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
+      if (it.head < 0) break;
+    }
+    grid_dep_launch();
+    if (lane == 0) {
+      copied[0] = issued;
+      q_copied[0] = q_issued[0];
+      q_copied[1] = q_issued[1];
+    }
+  } else if (warp == 9 || warp == 10) {
+    // ------------------------------------------------------------- products
+    // Block j of the item is K in ring place 2j and V in 2j + 1 from the item's first. The
+    // tile's S of block j + 1 overwrites P of block j: it waits for P V of block j.
+    const int i = warp - 9;
+    const uint32_t sbase = smem_u32(smem);
+    const uint64_t qd = sdesc_k_sw128(sbase + uint32_t(i) * C::kTile);
+    const uint64_t kd0 = sdesc_k_sw128(sbase + C::kRing);
+    const uint64_t vd0 = sdesc_mn_sw128(sbase + C::kRing, C::kHalf);
+    constexpr uint32_t kTypes = kBf16 ? 0u : (1u << 7) | (1u << 10);  // fp16 operands: the formats' bits clear
+    const uint32_t idesc_s = idesc_bf16(128, 128) & ~kTypes;
+    const uint32_t idesc_o = (idesc_bf16(128, kD) & ~kTypes) | (1u << 16);  // V is MN-major
+    const uint32_t s_at = tmem + C::kColS + 128u * i, o_at = tmem + C::kColO + 128u * i;
+    int base = 0;          // ring places before the item
+    int blocks = 0;        // blocks of this tile before the item
+    int mine = 0;          // items of this tile before this one
+    bool ok = true;
+    Item it;
+    for (int k = 0; get_item(k, it); ++k) {
+      const int n0 = blocks_of(it.t0, P.tpt, it.len), n1 = blocks_of(it.t0 + P.tpt, P.tpt, it.len);
+      const int all = max(n0, n1), n = i ? n1 : n0;
+      const int cut = first_cut(it.t0);
+      if (lane == 0) {
+        auto scores = [&](int j) {
+          const int s = (base + 2 * j) % kStages;
+          if (!wait(&full[s], uint32_t((base + 2 * j) / kStages) & 1u)) return false;
+          tc_fence_after();
+          const uint64_t kd = kd0 + uint64_t((uint32_t(s) * C::kTile) >> 4);
+#pragma unroll
+          for (int ks = 0; ks < kD / 16; ++ks) {
+            const uint64_t off = uint64_t((uint32_t(ks >> 2) * C::kHalf + uint32_t(ks & 3) * 32u) >> 4);
+            mma_bf16_ss(s_at, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[i]);
+          tc_commit(&empty[s]);
+          if (j == n - 1) tc_commit(&q_empty[i]);
+          return true;
+        };
+        // (The last item's P V of this tile is done: its o_done was waited for below.)
+        ok = n == 0 || (wait(&q_full[i], uint32_t(mine) & 1u) && scores(0));
+        for (int j = 0; ok && j < n; ++j) {
+          const int place = base + 2 * j + 1, s = place % kStages;
+          ok = wait(j >= cut ? &clean[s] : &full[s], uint32_t(place / kStages) & 1u);
+          if (ok && j == 0 && mine > 0) ok = wait(&o_free[i], uint32_t(mine - 1) & 1u);
+          const uint64_t vd = vd0 + uint64_t((uint32_t(s) * C::kTile) >> 4);
+          for (int h = 0; ok && h < 2; ++h) {
+            ok = wait(&p_full[2 * i + h], uint32_t(blocks + j) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint64_t off = uint64_t((uint32_t(h) * 8192u + uint32_t(ks) * 2048u) >> 4);
+              mma_bf16_ts(o_at, s_at + uint32_t(32 * h + 8 * ks), vd + off, idesc_o, (j > 0 || h > 0 || ks > 0) ? 1u : 0u);
+            }
+          }
+          if (!ok) break;
+          tc_commit(&o_done[i]);
+          tc_commit(&empty[s]);
+          ok = wait(&o_done[i], uint32_t(blocks + j) & 1u);
+          if (ok && j + 1 < n) ok = scores(j + 1);
+        }
+        // Blocks that only the other tile has: an arrival before the block has come would be
+        // counted for the stage's last one.
+        for (int place = base + 2 * n; ok && place < base + 2 * all; ++place) {
+          ok = wait(&full[place % kStages], uint32_t(place / kStages) & 1u);
+          if (ok) mbar_arrive(&empty[place % kStages]);
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
+      if (!ok) break;
+      base += 2 * all;
+      blocks += n;
+      mine += n > 0;
+    }
+    // This thread's products are done before the block leaves: after a failed wait they may not be.
+    if (lane == 0) {
+      tc_commit(&drained[i]);
+      mbar_wait(&drained[i], 0, drain_limit_ns(lim));
+    }
+  } else if (warp == 11) {
+    // ------------------------------------------------- values that are not finite
+    int base = 0;
+    Item it;
+    for (int k = 0; get_item(k, it); ++k) {
+      const int all = max(blocks_of(it.t0, P.tpt, it.len), blocks_of(it.t0 + P.tpt, P.tpt, it.len));
+      const int cut = base + 2 * first_cut(it.t0);
+      bool ok = true;
+      for (int place = base; place < base + 2 * all; ++place) {
+        const int s = place % kStages;
+        // (Every block is waited for: the barrier then runs through the same phases as `full`.)
+        if (!(ok = wait_all(&full[s], uint32_t(place / kStages) & 1u))) break;
+        if (place < cut || !((place - base) & 1)) {
+          if (lane == 0) mbar_arrive(&clean[s]);
+          continue;
+        }
+        uint8_t* v = smem + C::kRing + uint32_t(s) * C::kTile;
+        uint4 keys;
+        uint32_t* word = &keys.x;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int row = 32 * w + lane;
+          uint32_t acc = 0u;
+#pragma unroll
+          for (int h = 0; h < C::kHalves; ++h)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(v + h * C::kHalf + row * 128 + ((c ^ (row & 7)) << 4));
+              acc = spot<kBf16>(x.w, spot<kBf16>(x.z, spot<kBf16>(x.y, spot<kBf16>(x.x, acc))));
+            }
+          const bool odd = !(finite16<kBf16>(acc) && finite16<kBf16>(acc >> 16));
+          if (odd) {
+            for (int c = 0; c < 8 * C::kHalves; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + row * 128 + ((c & 7) << 4));
+              const uint4 x = *at;
+              *at = make_uint4(finite_pair<kBf16>(x.x), finite_pair<kBf16>(x.y), finite_pair<kBf16>(x.z), finite_pair<kBf16>(x.w));
+            }
+          }
+          word[w] = __ballot_sync(0xFFFFFFFFu, odd);
+        }
+        fence_proxy_async_smem();
+        if (lane == 0) bad[s] = keys;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&clean[s]);
+      }
+      if (!ok) break;
+      base += 2 * all;
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int i = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;          // row of the tile = TMEM lane
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lane_off + C::kColS + 128u * i, o_at = tmem + lane_off + C::kColO + 128u * i;
+    const float c = P.c;
+    int base = 0, blocks = 0;
+    Item it;
+    for (int k = 0; get_item(k, it); ++k) {
+      const int t0 = it.t0 + i * P.tpt;
+      const int n0 = blocks_of(it.t0, P.tpt, it.len), n1 = blocks_of(it.t0 + P.tpt, P.tpt, it.len);
+      const int n = i ? n1 : n0;
+      const int t = t0 + r / P.G;                   // the row's token, in its sequence
+      const bool valid = r < P.tpt * P.G && t < it.len;
+      const int cut = first_cut(it.t0);             // (from here on values may have been taken out)
+      float m = -INFINITY, l = 0.f;
+      uint32_t odd = 0;                             // bit j - cut: the row sees a value of block j that is not finite
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = wait_all(&s_full[i], uint32_t(blocks + j) & 1u))) break;
+        tc_fence_after();
+        uint32_t v[128];
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) tmem_ld16(s_at + uint32_t(ch * 16), *reinterpret_cast<uint32_t(*)[16]>(&v[ch * 16]));
+        tmem_ld_wait128(v);
+        if (j >= cut) {
+          const int see = t - j * kKeys + 1;        // keys of the block that the row sees
+#pragma unroll
+          for (int x = 0; x < 128; ++x)
+            if (x >= see) v[x] = __float_as_uint(-INFINITY);
+          const int place = base + 2 * j + 1, s = place % kStages;
+          if (!(ok = wait_all(&clean[s], uint32_t(place / kStages) & 1u))) break;
+          const uint4 keys = bad[s];
+          if (keys.x | keys.y | keys.z | keys.w) {
+            const uint32_t word[4] = {keys.x, keys.y, keys.z, keys.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int lim_w = see - 32 * w;
+              const uint32_t seen = lim_w >= 32 ? ~0u : lim_w <= 0 ? 0u : (1u << lim_w) - 1u;
+              if (word[w] & seen) odd |= 1u << (j - cut);
+            }
+          }
+        }
+        const float mx = block_max<128>(v) * c;
+        float factor = 1.f;
+        if (mx > m + kRescale) {
+          factor = fast_exp2(m - mx);               // 0 while m = -inf
+          m = mx;
+        }
+        const bool resc = j > 0 && factor < 1.f && l > 0.f;
+        if (__any_sync(0xFFFFFFFFu, resc)) {
+          if (!(ok = wait_all(&o_done[i], uint32_t(blocks + j - 1) & 1u))) break;
+          tc_fence_after();
+          rescale_row<kD>(o_at, resc ? factor : 1.f);
+          tmem_st_wait();
+        }
+        const float negm = m == -INFINITY ? 0.f : -m;
+        l *= factor;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          l += weights64<kBf16>(v + 64 * h, c, negm);
+          tmem_st16(s_at + uint32_t(32 * h), *reinterpret_cast<uint32_t(*)[16]>(&v[64 * h]));
+          tmem_st16(s_at + uint32_t(32 * h + 16), *reinterpret_cast<uint32_t(*)[16]>(&v[64 * h + 16]));
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * i + h]);
+        }
+      }
+      if (!ok) break;
+      if (n > 0) {
+        if (!wait_all(&o_done[i], uint32_t(blocks + n - 1) & 1u)) break;
+        tc_fence_after();
+        const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
+        uint16_t* out = static_cast<uint16_t*>(P.O) + (int64_t(it.first - it.t0 + t) * P.Hq + it.head * P.G + r % P.G) * kD;
+#pragma unroll
+        for (int ch = 0; ch < kD / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld16(o_at + uint32_t(32 * ch), *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+          tmem_ld16(o_at + uint32_t(32 * ch + 16), *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[16]>(&o[16]));
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
+          if (odd && valid) {
+            // Values that were taken out, of the keys that the row sees: as they are.
+            for (int b = 0; b < 4; ++b) {
+              if (!((odd >> b) & 1u)) continue;
+              const int key0 = (cut + b) * kKeys;
+              for (int key = key0; key < key0 + kKeys && key <= t; ++key) {
+                const uint16_t* src = static_cast<const uint16_t*>(P.V) + int64_t(it.first - it.t0 + key) * P.v_tok + int64_t(it.head) * P.v_head + 32 * ch;
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                  const uint32_t u = src[x];
+                  if (!finite16<kBf16>(u)) {
+                    const float f = kBf16 ? __uint_as_float(u << 16) : unpack_f16x2(u).x;
+                    o[x] = __float_as_uint(__uint_as_float(o[x]) + f);
+                  }
+                }
+              }
+            }
+          }
+          if (valid) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint4 w;
+              w.x = pack2<kBf16>(__uint_as_float(o[8 * x]), __uint_as_float(o[8 * x + 1]));
+              w.y = pack2<kBf16>(__uint_as_float(o[8 * x + 2]), __uint_as_float(o[8 * x + 3]));
+              w.z = pack2<kBf16>(__uint_as_float(o[8 * x + 4]), __uint_as_float(o[8 * x + 5]));
+              w.w = pack2<kBf16>(__uint_as_float(o[8 * x + 6]), __uint_as_float(o[8 * x + 7]));
+              *reinterpret_cast<uint4*>(out + 32 * ch + 8 * x) = w;
+            }
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&o_free[i]);
+      }
+      base += 2 * max(n0, n1);
+      blocks += n;
+    }
+  }
+
+  tc_fence_before();
+  cta_sync();
+  // Only now is no wait left that could expire: after one, copies may be in flight still.
+  if (*abort_flag && warp == 8 && lane == 0) {
+    for (int k = copied[0] > kStages ? copied[0] - kStages : 0; k < copied[0]; ++k)
+      mbar_wait(&full[k % kStages], uint32_t(k / kStages) & 1u, drain_limit_ns(lim));
+    for (int i = 0; i < 2; ++i)
+      if (q_copied[i] > 0) mbar_wait(&q_full[i], uint32_t(q_copied[i] - 1) & 1u, drain_limit_ns(lim));
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kD, bool kBf16>
+static cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const Params& P, unsigned grid,
+                          cudaStream_t stream) {
+  auto kernel = prompt_kernel<kD, kBf16>;
+  static std::atomic<uint64_t> ready{0};  // devices whose kernel may use the shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!((ready.load() >> dev) & 1)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cfg<kD>::kSmem));
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(uint64_t(1) << dev);
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Cfg<kD>::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, q, k, v, P);
+}
+
+// Rows [total, H, d] with element strides as boxes of `tokens` tokens of `heads` heads, 64 dims each.
+static bool row_map(CUtensorMap* map, const void* x, bool bf16, int d, int H, int64_t total, int64_t tok, int64_t head, int heads,
+                    int tokens) {
+  const uint64_t dims[4] = {uint64_t(d), uint64_t(H), uint64_t(total), 1};
+  const uint64_t strides[3] = {uint64_t(head) * 2, uint64_t(tok) * 2, 16};
+  const uint32_t box[4] = {64, uint32_t(heads), uint32_t(tokens), 1};
+  return encode_tmap_4d(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, const_cast<void*>(x), dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Strides that a tensor map takes: positive multiples of 16 bytes below 2^40.
+static bool stride_ok(int64_t elements) { return elements > 0 && elements % 8 == 0 && elements < (int64_t(1) << 38); }
+
+}  // namespace prompt_impl
+}  // namespace w12
+
+using namespace w12;
+using namespace w12::prompt_impl;
+
+extern "C" {
+
+int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_stride, const void* K, int64_t k_token_stride,
+                         int64_t k_head_stride, const void* V, int64_t v_token_stride, int64_t v_head_stride, int dtype,
+                         int64_t total, const int32_t* cu_seqlens, int B, int Hq, int Hkv, int head_dim, float scale, void* O,
+                         int32_t* dev_status, void* stream) {
+  if (dtype != W12_BF16 && dtype != W12_F16) return W12_ERR_ARG;
+  if (!cu_seqlens || !(scale > 0.f) || scale > 1e30f) return W12_ERR_ARG;
+  if (B < 0 || B > 65535 || total < 0 || total > 0x7FFFFFFF - 256 || Hkv < 1 || Hkv > 1024 || Hq < Hkv || Hq % Hkv ||
+      Hq / Hkv > 128 || (head_dim != 64 && head_dim != 128))
+    return W12_ERR_SHAPE;
+  if (total == 0 || B == 0) return device_supported() ? W12_OK : W12_ERR_UNSUPPORTED;
+  if (!Q || !K || !V || !O || !aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16)) return W12_ERR_ARG;
+  if (!stride_ok(q_token_stride) || !stride_ok(q_head_stride) || !stride_ok(k_token_stride) || !stride_ok(k_head_stride) ||
+      !stride_ok(v_token_stride) || !stride_ok(v_head_stride))
+    return W12_ERR_ARG;
+  if (!device_supported()) return W12_ERR_UNSUPPORTED;
+  Params P{};
+  P.V = V;
+  P.v_tok = v_token_stride;
+  P.v_head = v_head_stride;
+  P.O = O;
+  P.cu = cu_seqlens;
+  P.status = dev_status;
+  P.total = total;
+  P.B = B;
+  P.Hq = Hq;
+  P.Hkv = Hkv;
+  P.G = Hq / Hkv;
+  P.tpt = 128 / P.G;
+  P.c = float(double(scale) * 1.4426950408889634);
+  P.limit_ns = wait_limit_ns();
+  const bool bf16 = dtype == W12_BF16;
+  CUtensorMap q, k, v;
+  if (!row_map(&q, Q, bf16, head_dim, Hq, total, q_token_stride, q_head_stride, P.G, P.tpt) ||
+      !row_map(&k, K, bf16, head_dim, Hkv, total, k_token_stride, k_head_stride, 1, kKeys) ||
+      !row_map(&v, V, bf16, head_dim, Hkv, total, v_token_stride, v_head_stride, 1, kKeys))
+    return W12_ERR_CUDA;
+  const int sms = device_sm_count();
+  const int64_t most = (total / (2 * P.tpt) + B) * Hkv;
+  const unsigned grid = unsigned(most < sms ? most : sms);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return cuda_status(head_dim == 128 ? (bf16 ? launch<128, true>(q, k, v, P, grid, s) : launch<128, false>(q, k, v, P, grid, s))
+                                     : (bf16 ? launch<64, true>(q, k, v, P, grid, s) : launch<64, false>(q, k, v, P, grid, s)));
+}
+
+}  // extern "C"

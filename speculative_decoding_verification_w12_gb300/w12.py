@@ -28,7 +28,8 @@ EXPORTS = [
     "w12_gemm_grouped", "w12_gemm_grouped_bf16_ref", "w12_kv_commit", "w12_state_select",
     "w12_tree_attention_ws_bytes", "w12_tree_attention", "w12_copy", "w12_pages_update", "w12_kv4_page_bytes",
     "w12_kv4_append", "w12_kv4_read", "w12_kv4_commit", "w12_kv4_attention_ws_bytes", "w12_kv4_attention",
-    "w12_logprobs_ws_bytes", "w12_logprobs",
+    "w12_logprobs_ws_bytes", "w12_logprobs", "w12_qk_norm_rope", "w12_kv4_append_rope", "w12_tree_positions",
+    "w12_prompt_attention", "w12_lora_ws_bytes", "w12_lora",
 ]
 
 
@@ -61,6 +62,17 @@ class _Sizes(ctypes.Structure):
 class _KV4(ctypes.Structure):
     _fields_ = [("pool", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("Hkv", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class _Adapters(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("n", ctypes.c_int), ("rank", ctypes.c_int)]
 
 
 _lib = None
@@ -117,6 +129,15 @@ def lib() -> ctypes.CDLL:
             "w12_logprobs_ws_bytes": (sz, [i64, i64, i32]),
             "w12_logprobs": (i32, [vp, i32, i64, i64, i64, ctypes.c_float, vp, i32, i32, vp, vp, vp, vp, vp, vp, sz,
                                    vp, vp]),
+            "w12_qk_norm_rope": (i32, [ctypes.POINTER(_Rope), i32, vp, i64, i64, i32, vp, i64, i64, i32, i32, i64, vp,
+                                       vp, vp, i32, vp, vp]),
+            "w12_kv4_append_rope": (i32, [ctypes.POINTER(_KV4), ctypes.POINTER(_Rope), vp, i64, i64, i32, vp, i64, i64,
+                                          vp, i64, i64, i32, i64, vp, vp, vp, vp, vp]),
+            "w12_tree_positions": (i32, [vp, vp, vp, i32, i32, vp, vp, vp]),
+            "w12_prompt_attention": (i32, [vp, i64, i64, vp, i64, i64, vp, i64, i64, i32, i64, vp, i32, i32, i32, i32,
+                                           ctypes.c_float, vp, vp, vp]),
+            "w12_lora_ws_bytes": (sz, [i64, i32, i32]),
+            "w12_lora": (i32, [vp, i64, i64, ctypes.POINTER(_Adapters), vp, vp, i64, vp, sz, vp, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -640,6 +661,35 @@ class KV4Cache:
             _check(lib().w12_kv4_append(self._ref, K.data_ptr(), V.data_ptr(), dt, n, ks[0], ks[1], vs[0], vs[1],
                                         slots.data_ptr(), _ptr(status), _stream(stream)), "w12_kv4_append")
 
+    def append_rope(self, K: torch.Tensor, V: torch.Tensor, slots: torch.Tensor, rope: "Rope",
+                    positions: torch.Tensor, Q: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    status: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+        """append() with the keys normed and rotated on the way (see Rope). Q [n, Hq,
+        head_dim] of the same rows and type, if given, comes back normed and rotated, bf16."""
+        n = K.shape[0]
+        if K.shape != V.shape or K.shape != (n, self.Hkv, self.head_dim):
+            raise ValueError("K and V must be [n, Hkv, head_dim]")
+        if rope.head_dim != self.head_dim:
+            raise ValueError("the rotation's head dimension must be the cache's")
+        ks, vs = _head_rows(K, "K"), _head_rows(V, "V")
+        qs = (0, 0, 0, 0) if Q is None else _head_rows(Q, "Q")
+        if V.dtype != K.dtype or (Q is not None and (Q.dtype != K.dtype or Q.shape[0] != n or Q.shape[2] != self.head_dim)):
+            raise ValueError("Q, K and V must be rows of the same tokens, head dimension and type")
+        _want(slots, "slots", torch.int32, (n,))
+        _want(positions, "positions", torch.int32, (n,))
+        if Q is None:
+            if out is not None:
+                raise ValueError("out without Q")
+        elif out is None:
+            out = _empty(Q.shape, torch.bfloat16, Q.device, stream)
+        else:
+            _want(out, "out", torch.bfloat16, Q.shape)
+        if n:
+            _check(lib().w12_kv4_append_rope(self._ref, rope._ref, qs[0], qs[1], qs[2], qs[3], ks[0], ks[1], ks[2], vs[0],
+                                             vs[1], vs[2], _DTYPES[K.dtype], n, positions.data_ptr(), slots.data_ptr(),
+                                             _ptr(out), _ptr(status), _stream(stream)), "w12_kv4_append_rope")
+        return out
+
     def read(self, slots: torch.Tensor, out=None, status: torch.Tensor | None = None, stream=None):
         """(K, V) bf16 [n, Hkv, head_dim] of the given slots (int32; -1 reads as zeros)."""
         _want(slots, "slots", torch.int32)
@@ -776,6 +826,173 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 
     """One call of TokenLogprobs on logits [M, V]."""
     with torch.cuda.stream(stream):  # (None: the current one) the workspace belongs to the stream that uses it
         return TokenLogprobs(logits.shape[0], logits.shape[1], k, logits.device).run(logits, tokens, scale, status, stream)
+
+
+# ---------------------------------------------------------------------------
+# Between the products of a layer: rotation, prompt attention, adapters
+# ---------------------------------------------------------------------------
+
+def _head_rows(x: torch.Tensor, what: str, dtypes=_DTYPES) -> tuple[int, int, int, int]:
+    """Address, strides of tokens and heads, and heads of rows [n, H, head_dim]."""
+    if x.dtype not in dtypes:
+        raise TypeError(f"{what} must be one of {', '.join(str(t) for t in dtypes)}")
+    if x.dim() != 3 or not x.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor [n, heads, head_dim]")
+    n, H, d = x.shape
+    st = x.stride()
+    if x.numel() and st[2] != 1:
+        raise ValueError(f"{what} must have a contiguous last dimension")
+    # (An axis of one has no stride of its own.)
+    return x.data_ptr(), st[0] if n > 1 else H * d, st[1] if H > 1 else d, H
+
+
+class Rope:
+    """Rotation of query and key heads by position, with the norms of the heads
+    (w12_rope): table fp32 [max_pos, rot_dim], of each position the cosines of its
+    rot_dim / 2 angles, then their sines; q_norm and k_norm fp32 [head_dim], the
+    weights of x / sqrt(mean x^2 + eps) (None: no norm); interleaved pairs values
+    2i and 2i + 1 instead of i and i + rot_dim / 2. One object serves every layer
+    that shares table and weights. create() works out a table."""
+
+    def __init__(self, table: torch.Tensor, head_dim: int, q_norm: torch.Tensor | None = None,
+                 k_norm: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False):
+        if table.dim() != 2:
+            raise ValueError("table must be [max_pos, rot_dim]")
+        self.head_dim, self.rot_dim = int(head_dim), table.shape[1]
+        if self.rot_dim % 16 or not 16 <= self.rot_dim <= self.head_dim or self.head_dim not in (64, 128):
+            raise ValueError("rot_dim must be a multiple of 16 up to the head dimension, which is 64 or 128")
+        if not 1e-12 <= eps < float("inf"):
+            raise ValueError("eps must be at least 1e-12")
+        self.table = _want(table, "table", torch.float32)
+        self.q_norm, self.k_norm = (None if w is None else _want(w, "norm weights", torch.float32, (self.head_dim,))
+                                    for w in (q_norm, k_norm))
+        self._struct = _Rope(table.data_ptr(), table.shape[0], self.rot_dim, int(interleaved), _ptr(q_norm),
+                             _ptr(k_norm), float(eps))
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def create(cls, head_dim: int, max_pos: int, theta: float = 10000.0, rot_dim: int | None = None, inv_freq=None,
+               device="cuda", **kw) -> "Rope":
+        """Angles pos * theta^(-2i / rot_dim), or pos * inv_freq[i], worked out in 64 bits."""
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        i = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+        f = theta ** (-i / rot_dim) if inv_freq is None else torch.as_tensor(inv_freq, dtype=torch.float64, device=device)
+        a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * f
+        return cls(torch.cat([a.cos(), a.sin()], 1).float(), head_dim, **kw)
+
+    def run(self, Q: torch.Tensor | None, K: torch.Tensor | None, positions: torch.Tensor, out=None,
+            dtype: torch.dtype = torch.bfloat16, status: torch.Tensor | None = None, stream=None):
+        """(Q, K) normed and rotated, of type dtype, for rows Q [n, Hq, head_dim] and K
+        [n, Hkv, head_dim] (fp32, bf16 or fp16; views with a contiguous last dimension;
+        either may be None) at positions int32 [n] (-1: no token, zeros)."""
+        rows = [x for x in (Q, K) if x is not None]
+        if not rows:
+            raise ValueError("Q or K must be given")
+        qs, ks = ((0, 0, 0, 0) if x is None else _head_rows(x, "Q and K") for x in (Q, K))
+        n = rows[0].shape[0]
+        if any(x.shape[0] != n or x.shape[2] != self.head_dim or x.dtype != rows[0].dtype for x in rows):
+            raise ValueError("Q and K must be rows of the same tokens and type, of the rotation's head dimension")
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be float32, bfloat16 or float16")
+        _want(positions, "positions", torch.int32, (n,))
+        if out is None:
+            q, k = (None if x is None else _empty(x.shape, dtype, x.device, stream) for x in (Q, K))
+        else:
+            q, k = (None if x is None else _want(o, "out", dtype, x.shape) for o, x in zip(out, (Q, K)))
+        if n:
+            _check(lib().w12_qk_norm_rope(self._ref, self.head_dim, *qs, *ks, _DTYPES[rows[0].dtype], n,
+                                          positions.data_ptr(), _ptr(q), _ptr(k), _DTYPES[dtype], _ptr(status),
+                                          _stream(stream)), "w12_qk_norm_rope")
+        return q, k
+
+
+def tree_positions(prefix_len: torch.Tensor, parents: torch.Tensor | None = None, T: int | None = None,
+                   q_len: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Positions int32 [B, T] of new tokens: prefix_len[b] + the node's depth in the
+    draft tree parents int32 [B, T], or + t without a tree (T must then be given); -1
+    from q_len[b] on."""
+    B = prefix_len.shape[0]
+    _want(prefix_len, "prefix_len", torch.int32, (B,))
+    if parents is not None:
+        T = parents.shape[-1] if T is None else T
+        _want(parents, "parents", torch.int32, (B, T))
+    elif T is None:
+        raise ValueError("parents or T must be given")
+    if q_len is not None:
+        _want(q_len, "q_len", torch.int32, (B,))
+    if out is None:
+        out = _empty((B, T), torch.int32, prefix_len.device, stream)
+    else:
+        _want(out, "out", torch.int32, (B, T))
+    _check(lib().w12_tree_positions(prefix_len.data_ptr(), _ptr(parents), _ptr(q_len), B, T, out.data_ptr(),
+                                    _ptr(status), _stream(stream)), "w12_tree_positions")
+    return out
+
+
+def prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_seqlens: torch.Tensor,
+                     scale: float | None = None, out: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """Causal attention over whole prompts packed one behind the other: Q [total, Hq,
+    head_dim], K and V [total, Hkv, head_dim], all bf16 or all fp16 (views with a
+    contiguous last dimension and other strides that are multiples of 8), sequence b
+    being rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]). Returns O
+    [total, Hq, head_dim]; rows outside the sequences are left as they are."""
+    half = (torch.bfloat16, torch.float16)
+    (q, qt, qh, Hq), (k, kt, kh, Hkv), (v, vt, vh, _) = _head_rows(Q, "Q", half), _head_rows(K, "K", half), _head_rows(V, "V", half)
+    total, _, d = Q.shape
+    if K.shape != V.shape or K.shape[0] != total or K.shape[2] != d or not Q.dtype == K.dtype == V.dtype:
+        raise ValueError("Q, K and V must be rows of the same tokens, head dimension and type")
+    _want(cu_seqlens, "cu_seqlens", torch.int32)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [B + 1]")
+    if out is None:
+        out = _empty(Q.shape, Q.dtype, Q.device, stream)
+    else:
+        _want(out, "out", Q.dtype, Q.shape)
+    _check(lib().w12_prompt_attention(q, qt, qh, k, kt, kh, v, vt, vh, _DTYPES[Q.dtype], total, cu_seqlens.data_ptr(),
+                                      cu_seqlens.numel() - 1, Hq, Hkv, d, d ** -0.5 if scale is None else float(scale),
+                                      out.data_ptr(), _ptr(status), _stream(stream)), "w12_prompt_attention")
+    return out
+
+
+class LoRA:
+    """Low-rank adapters of one projection K -> N (w12_lora): A bf16 [n, rank, K], B bf16
+    [n, N, rank], scale fp32 [n]; the workspace serves up to max_rows rows a call."""
+
+    def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, max_rows: int = 256):
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError("A must be [n, rank, K] and B [n, N, rank]")
+        self.n, self.rank, self.K = A.shape
+        self.N, self.max_rows = B.shape[1], int(max_rows)
+        self.A = _want(A, "A", torch.bfloat16)
+        self.B = _want(B, "B", torch.bfloat16, (self.n, self.N, self.rank))
+        self.scale = _want(scale, "scale", torch.float32, (self.n,))
+        nbytes = lib().w12_lora_ws_bytes(self.max_rows, self.n, self.rank)
+        if nbytes == 0 or self.K % 8 or self.N % 16:
+            raise W12Error(2, "w12_lora_ws_bytes")
+        self.ws = _kept_workspace(nbytes, A.device)
+        self._struct = _Adapters(A.data_ptr(), B.data_ptr(), scale.data_ptr(), self.N, self.K, self.n, self.rank)
+        self._ref = ctypes.byref(self._struct)
+
+    def run(self, X: torch.Tensor, Y: torch.Tensor, ids: torch.Tensor, status: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+        """Adds scale[a] * B[a] (A[a] X[m]), a = ids[m], to row m of Y fp32 [M, N], in
+        place; X bf16 [M, K], ids int32 [M] (-1: no adapter). Rows of X and Y may be
+        padded. Returns Y."""
+        M = X.shape[0]
+        if X.shape != (M, self.K) or X.dtype is not torch.bfloat16 or not X.is_cuda or X.stride(1) != 1:
+            raise ValueError(f"X must be a bfloat16 CUDA tensor [M, {self.K}] with a contiguous last dimension")
+        if Y.shape != (M, self.N) or Y.dtype is not torch.float32 or not Y.is_cuda or Y.stride(1) != 1:
+            raise ValueError(f"Y must be a float32 CUDA tensor [{M}, {self.N}] with a contiguous last dimension")
+        if M > self.max_rows:
+            raise ValueError(f"at most {self.max_rows} rows")
+        _want(ids, "ids", torch.int32, (M,))
+        if M:
+            _check(lib().w12_lora(X.data_ptr(), X.stride(0) if M > 1 else self.K, M, self._ref, ids.data_ptr(), Y.data_ptr(),
+                                  Y.stride(0) if M > 1 else self.N, self.ws.data_ptr(), self.ws.numel(), _ptr(status),
+                                  _stream(stream)), "w12_lora")
+        return Y
 
 
 def selftest_timeout(limit_us: int, status: torch.Tensor, stream=None):
