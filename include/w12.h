@@ -533,8 +533,8 @@ int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const 
  * [total, Hq, head_dim] contiguous, its rows outside the sequences left as they are.
  * Element strides are positive multiples of 8, pointers 16-byte aligned; head_dim 64
  * or 128, Hq / Hkv <= 128, total < 2^31 - 256. Sequences of no rows are fine. One with offsets
- * out of [0, total], or decreasing ones, sets W12_ERR_ARG and is taken as empty. Rows
- * that a row does not see have no part in it, whatever they hold. Scores, softmax and sums are fp32; a weight
+ * out of [0, total], or decreasing ones, sets W12_ERR_ARG and is taken as empty (sequences
+ * that share rows write either's result). Rows that a row does not see have no part in it, whatever they hold. Scores, softmax and sums are fp32; a weight
  * meets the values rounded to their type (bf16: 2^-8 of itself, fp16: 2^-11 of itself
  * or 2^-25 of the row's largest). A score of -inf weighs nothing; a row with no other
  * is zeros. No workspace. Device-side errors besides: W12_ERR_TIMEOUT. Returns

@@ -5,26 +5,33 @@
 // Rows of a tile are (token, head of the group), token-major, 128 / G tokens: a key block is
 // read once for the whole group, and few of a tile's keys are cut by the diagonal. An item is
 // two such tiles, one behind the other, of one (sequence, kv head), with all keys that they
-// see in blocks of 128. The kernel is persistent; items go out longest first, in rounds of
-// the grid that alternate in direction, so every block gets about the same work and nothing
-// is counted in memory. Per key block and tile:
+// see in blocks. The kernel is persistent; items go out longest first, in rounds of the grid
+// that alternate in direction, so every block gets about the same work and nothing is counted
+// in memory. Per key block and tile:
 //   S = Q K^T         tcgen05.mma, both from shared memory, S in TMEM;
 //   P = 2^(c S - m)   a warpgroup for each tile, a row a thread: the running maximum moves only
-//                     when a block's passes it by 2^8, so O is rescaled rarely; P goes over
-//                     the first half of S's columns, in two halves of 64 keys;
+//                     when a block's passes it by 2^8, so O is rescaled rarely;
 //   O += P V          tcgen05.mma, P from TMEM, V from shared memory (MN-major).
-// While one tile is in the softmax the tensor cores work for the other.
+// P has columns of its own, so the next block's S is under way as soon as the softmax has read
+// this one's: products run about 430 cycles from issue to the waiting thread (measured, eight
+// in a row), which a P over S would add twice a block to the softmax. At d = 128 the columns
+// (512: S, P and O of both tiles) leave room for blocks of 80 keys, at d = 64 for 128.
 //
 // P enters O rounded to the type of V (bf16: 2^-8 of itself; fp16: 2^-11, or 2^-25 of the
 // largest weight), its sum is of the unrounded P; scores, maxima, sums and O are fp32.
 //
 // Masked places may hold anything. Masked scores are replaced, not added to. A value that is
-// not finite would turn the zero weights of rows that do not see it into NaN: a warp looks
-// through the V blocks that the diagonal cuts, takes such values out of shared memory and
-// notes their keys, and rows that see one add it at the end.
+// not finite would turn the zero weights of rows that do not see it into NaN: two warps look
+// through the V blocks that the diagonal cuts, take such values out of shared memory and
+// note their keys, and rows that see one add it at the end.
 //
-// Warps: 0-3 and 4-7 softmax and epilogue of the two tiles, 8 copies (and hands out the items),
-// 9 and 10 issue the products of the two tiles, 11 looks through V.
+// Warps: 0-3 and 4-7 softmax and epilogue of the two tiles; 8 and 9 issue S, 10 and 11 P V of the
+// two tiles; 12 copies (and hands out the items); 13 and 14 look through V. Each of the four
+// series of products has a warp on a scheduler of its own: what a thread waits for comes back
+// behind the products it has issued before (285 idle cycles a wait where one thread issues all,
+// measured), so only other warps' products fill that time. The issuing warps run whole and elect
+// a lane at the instruction: the operands are then known to be the same for the warp (an
+// N = 64 product 32 cycles instead of 46).
 #include <atomic>
 
 #include "w12_attn_dev.cuh"
@@ -35,22 +42,49 @@ namespace prompt_impl {
 
 using namespace attn_impl;
 
-constexpr int kKeys = 128;
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr float kRescale = 8.0f;   // log2 growth of the maximum that triggers a rescale
 constexpr int kItems = 4;          // items handed out ahead
-constexpr int kItemReaders = 11;   // warps that read an item
+constexpr int kItemReaders = 14;   // warps that read an item
+constexpr int kMostCut = 5;        // blocks that the diagonal cuts in an item: 256 tokens of blocks of 80 or more
+
+// Registers: a warpgroup changes its share by one instruction that all its warps meet.
+constexpr int kLaunchRegs = 128, kSoftRegs = 184, kRestRegs = 72;
+static_assert(8 * kSoftRegs + 8 * kRestRegs <= (kThreads / 32) * kLaunchRegs, "the launch's registers");
+
+// Whether this lane is the one that the warp, all of it here, has chosen.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 
 template <int kD>
 struct Cfg {
+  static constexpr int kKeys = kD == 128 ? 80 : 128;           // of a block
   static constexpr int kHalves = kD / 64;                      // 128-byte pieces of a row
-  static constexpr uint32_t kHalf = 128u * 128u;               // 128 rows of one piece
+  static constexpr uint32_t kQHalf = 128u * 128u;              // 128 rows of one piece of Q
+  static constexpr uint32_t kQTile = kHalves * kQHalf;
+  static constexpr uint32_t kHalf = 128u * kKeys;              // a key block's rows of one piece
   static constexpr uint32_t kTile = kHalves * kHalf;
-  static constexpr int kStages = kD == 128 ? 5 : 10;           // K and V blocks in turn
-  static constexpr uint32_t kRing = 2 * kTile;                 // behind the two tiles' Q
+  static constexpr int kStages = kD == 128 ? 8 : 10;           // K and V blocks in turn
+  static constexpr uint32_t kRing = 2 * kQTile;                // behind the two tiles' Q
   static constexpr uint32_t kBar = kRing + kStages * kTile;
   static constexpr uint32_t kSmem = kBar + 1024 + 1024;        // barriers, items; alignment
-  static constexpr uint32_t kColS = 0, kColO = 256;            // S of tile i at 128 i, O at 256 + 128 i
+  // TMEM columns of the first tile, and how far on the second's are.
+  static constexpr uint32_t kColS = 0, kNextS = 128;
+  static constexpr uint32_t kColP = kD == 128 ? kKeys : 256, kNextP = kD == 128 ? 128 : 64;
+  static constexpr uint32_t kColO = kD == 128 ? 256 : 384, kNextO = kD;
+  static_assert(kColP + kKeys / 2 <= (kD == 128 ? kNextS : kColP + kNextP) && kColO + 2 * kNextO <= 512, "columns");
 };
 
 struct Item {
@@ -83,10 +117,14 @@ __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int 
 
 // Key blocks of a tile that begins at token t0 (none past the sequence's end), and the first
 // of them that some row of the tile does not see whole.
+template <int kKeys>
 __device__ __forceinline__ int blocks_of(int t0, int tpt, int len) {
   return t0 >= len ? 0 : (min(t0 + tpt, len) + kKeys - 1) / kKeys;
 }
-__device__ __forceinline__ int first_cut(int t0) { return (t0 + 1) / kKeys; }
+template <int kKeys>
+__device__ __forceinline__ int first_cut(int t0) {
+  return (t0 + 1) / kKeys;
+}
 
 // Walks the items in their order, longest first: by place in the sequence (in pairs of
 // tiles) from the last down, then sequence, then kv head. Warp-collective.
@@ -156,20 +194,61 @@ struct Walk {
   }
 };
 
+#define W12_R8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+#define W12_W8(v, o) \
+  "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
+
+// Each thread reads (valid after the wait for loads) or writes 32 columns of its own lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : W12_W8(v, 0), W12_W8(v, 8), W12_W8(v, 16), W12_W8(v, 24)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::W12_R8(v, 0),
+      W12_R8(v, 8), W12_R8(v, 16), W12_R8(v, 24), "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::W12_R8(v, 0), "r"(taddr) : "memory");
+}
+
+// The largest of N scores, three at a time (the two-operand maximum runs at the same rate).
+__device__ __forceinline__ float max3(float a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+template <int N>
+__device__ __forceinline__ float largest(const uint32_t (&v)[N]) {
+  float m[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) m[a] = __uint_as_float(v[a]);
+#pragma unroll
+  for (int k = 4; k + 1 < N; k += 2) m[(k >> 1) & 3] = max3(m[(k >> 1) & 3], v[k], v[k + 1]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 template <bool kBf16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   if constexpr (kBf16) return pack_bf16x2(lo, hi);
   else return pack_f16x2(lo, hi);
 }
 
-// P_k = 2^(c s_k + negm) of 64 scores, packed as pairs into v[0 .. 31] in place (pair k over
-// v[k], which pair k/2 has read); returns the fp32 sum.
-template <bool kBf16>
-__device__ __forceinline__ float weights64(uint32_t* v, float c, float negm) {
+// P_k = 2^(c s_k + negm) of N scores, packed as pairs into v[0 .. N/2 - 1] in place (pair k
+// over v[k], which pair k/2 has read); returns the fp32 sum.
+template <bool kBf16, int N>
+__device__ __forceinline__ float weights(uint32_t (&v)[N], float c, float negm) {
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 c2 = make_float2(c, c), m2 = make_float2(negm, negm);
 #pragma unroll
-  for (int k = 0; k < 32; ++k) {
+  for (int k = 0; k < N / 2; ++k) {
     const float2 x = fma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2, m2);
     const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
     sum[k & 1] = add2(sum[k & 1], p);
@@ -177,6 +256,29 @@ __device__ __forceinline__ float weights64(uint32_t* v, float c, float negm) {
   }
   const float2 s = add2(sum[0], sum[1]);
   return s.x + s.y;
+}
+
+// A row's scores from TMEM, ready to use.
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&v)[N]) {
+#pragma unroll
+  for (int ch = 0; ch < N / 32; ++ch) tmem_ld32(taddr + uint32_t(32 * ch), &v[32 * ch]);
+  if constexpr (N % 32) tmem_ld16(taddr + uint32_t(N - 16), *reinterpret_cast<uint32_t(*)[16]>(&v[N - 16]));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+r"(v[k]));  // (no use of a value moves before the wait)
+}
+
+// N columns of weights to TMEM, done when it returns.
+template <int N>
+__device__ __forceinline__ void store_weights(uint32_t taddr, uint32_t* v) {
+#pragma unroll
+  for (int ch = 0; ch < N / 32; ++ch) tmem_st32(taddr + uint32_t(32 * ch), v + 32 * ch);
+  if constexpr (N % 32 != 0) {
+    static_assert(N % 32 == 8, "one more piece");
+    tmem_st8(taddr + uint32_t(N - 8), v + N - 8);
+  }
+  tmem_st_wait();
 }
 
 // A value of V's type is finite: all exponent bits set otherwise.
@@ -208,19 +310,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = Cfg<kD>;
   constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (An offset, not a rounded pointer: the compiler then still knows that it is shared memory.)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint4* bad = reinterpret_cast<uint4*>(smem + C::kBar);  // [kStages]: keys of a V block with values taken out
   uint64_t* full = reinterpret_cast<uint64_t*>(bad + kStages);  // [kStages]: block landed
-  uint64_t* empty = full + kStages;       // [kStages]: both tiles' products of the stage's block done
+  uint64_t* empty = full + kStages;       // [kStages]: products of the stage's block done
   uint64_t* clean = empty + kStages;      // [kStages]: block looked through, where it is a V block with a cut
   uint64_t* q_full = clean + kStages;     // [2]: tile's Q landed
   uint64_t* q_empty = q_full + 2;         // [2]: the item's last S of the tile done
   uint64_t* s_full = q_empty + 2;         // [2]: S of the tile's block
-  uint64_t* p_full = s_full + 2;          // [2][2]: P of the tile's block, key half h
-  uint64_t* o_done = p_full + 4;          // [2]: P V of the tile's block done
+  uint64_t* s_read = s_full + 2;          // [2]: and read
+  uint64_t* p_full = s_read + 2;          // [2]: P of the tile's block
+  uint64_t* o_done = p_full + 2;          // [2]: P V of the tile's block done
   uint64_t* o_free = o_done + 2;          // [2]: the item's O read
-  uint64_t* drained = o_free + 2;         // [2]: all products of a tile's thread done
-  uint64_t* it_full = drained + 2;        // [kItems]
+  uint64_t* drained = o_free + 2;         // [4]: all products of an issuing warp done
+  uint64_t* it_full = drained + 4;        // [kItems]
   uint64_t* it_empty = it_full + kItems;  // [kItems]
   Item* items = reinterpret_cast<Item*>(it_empty + kItems);       // [kItems]
   uint32_t* misc = reinterpret_cast<uint32_t*>(items + kItems);
@@ -228,25 +332,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile int* copied = reinterpret_cast<volatile int*>(misc + 2);  // blocks requested
   volatile int* q_copied = reinterpret_cast<volatile int*>(misc + 3);  // [2]: Q tiles requested
-  static_assert(16 * kStages + (3 * kStages + 16 + 2 * kItems) * 8 + 16 * kItems + 20 <= 1024, "barriers");
+  static_assert(16 * kStages + (3 * kStages + 18 + 2 * kItems) * 8 + 16 * kItems + 20 <= 1024, "barriers");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);   // one commit a tile
-      mbar_init(&clean[s], 1);
+      mbar_init(&empty[s], 2);   // one arrival a tile
+      mbar_init(&clean[s], 2);   // two warps, half of the keys each
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[2 * i], 128);
-      mbar_init(&p_full[2 * i + 1], 128);
+      mbar_init(&s_read[i], 4);       // one arrival a warp
+      mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
-      mbar_init(&o_free[i], 128);
-      mbar_init(&drained[i], 1);
+      mbar_init(&o_free[i], 4);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&drained[i], 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&it_full[i], 1);
       mbar_init(&it_empty[i], kItemReaders);
@@ -258,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  if (warp == 9) {
+  if (warp == 8) {
     tmem_alloc(const_cast<uint32_t*>(tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   cta_sync();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const uint64_t lim = P.limit_ns;
   // Everything below reads what the previous kernel on the stream wrote.
   grid_dep_wait();
@@ -295,7 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it.head >= 0;
   };
 
-  if (warp == 8) {
+  if (warp >= 8) {
+    fewer_registers<kRestRegs>();
+  if (warp == 12) {
     // --------------------------------------------------------- items, copies
     Walk walk{P.cu, P.B, P.Hkv, 2 * P.tpt, P.total};
     walk.begin(blockIdx.x == 0 ? P.status : nullptr);
@@ -326,22 +432,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && it.head >= 0) {
           const int seq = it.first - it.t0;
-          const int n0 = blocks_of(it.t0, P.tpt, it.len), n1 = blocks_of(it.t0 + P.tpt, P.tpt, it.len);
+          const int n0 = blocks_of<C::kKeys>(it.t0, P.tpt, it.len), n1 = blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len);
           const int n = max(n0, n1);
           for (int j = 0; ok && j < n; ++j) {
-            ok = stage(&tm_k, it.head, seq + j * kKeys);
+            ok = stage(&tm_k, it.head, seq + j * C::kKeys);
             if (j == 0) {
               for (int i = 0; ok && i < (n1 ? 2 : 1); ++i) {
                 if (q_issued[i] > 0) ok = wait(&q_empty[i], uint32_t(q_issued[i] - 1) & 1u);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&q_full[i], uint32_t(kD * 2 * P.G * P.tpt));
                 for (int h = 0; h < C::kHalves; ++h)
-                  load_box(smem + uint32_t(i) * C::kTile + h * C::kHalf, &tm_q, 64 * h, it.head * P.G, it.first + i * P.tpt,
+                  load_box(smem + uint32_t(i) * C::kQTile + h * C::kQHalf, &tm_q, 64 * h, it.head * P.G, it.first + i * P.tpt,
                            &q_full[i]);
                 ++q_issued[i];
               }
             }
-            if (ok) ok = stage(&tm_v, it.head, seq + j * kKeys);
+            if (ok) ok = stage(&tm_v, it.head, seq + j * C::kKeys);
           }
         }
       }
@@ -354,92 +460,84 @@ __global__ void __launch_bounds__(kThreads, 1)
       q_copied[0] = q_issued[0];
       q_copied[1] = q_issued[1];
     }
-  } else if (warp == 9 || warp == 10) {
+  } else if (warp < 12) {
     // ------------------------------------------------------------- products
-    // Block j of the item is K in ring place 2j and V in 2j + 1 from the item's first. The
-    // tile's S of block j + 1 overwrites P of block j: it waits for P V of block j.
-    const int i = warp - 9;
+    // Block j of the item is K in ring place 2j and V in 2j + 1 from the item's first.
+    const int i = warp & 1;
+    const bool is_s = warp < 10;
     const uint32_t sbase = smem_u32(smem);
-    const uint64_t qd = sdesc_k_sw128(sbase + uint32_t(i) * C::kTile);
+    const uint64_t qd = sdesc_k_sw128(sbase + uint32_t(i) * C::kQTile);
     const uint64_t kd0 = sdesc_k_sw128(sbase + C::kRing);
     const uint64_t vd0 = sdesc_mn_sw128(sbase + C::kRing, C::kHalf);
     constexpr uint32_t kTypes = kBf16 ? 0u : (1u << 7) | (1u << 10);  // fp16 operands: the formats' bits clear
-    const uint32_t idesc_s = idesc_bf16(128, 128) & ~kTypes;
+    const uint32_t idesc_s = idesc_bf16(128, C::kKeys) & ~kTypes;
     const uint32_t idesc_o = (idesc_bf16(128, kD) & ~kTypes) | (1u << 16);  // V is MN-major
-    const uint32_t s_at = tmem + C::kColS + 128u * i, o_at = tmem + C::kColO + 128u * i;
-    int base = 0;          // ring places before the item
-    int blocks = 0;        // blocks of this tile before the item
-    int mine = 0;          // items of this tile before this one
+    const uint32_t s_at = tmem + C::kColS + C::kNextS * i, p_at = tmem + C::kColP + C::kNextP * i, o_at = tmem + C::kColO + C::kNextO * i;
+    int place = is_s ? 0 : 1;   // in the ring, of the next block
+    int blocks = 0;             // blocks of this tile so far
+    int mine = 0;               // items of this tile before this one
     bool ok = true;
     Item it;
-    for (int k = 0; get_item(k, it); ++k) {
-      const int n0 = blocks_of(it.t0, P.tpt, it.len), n1 = blocks_of(it.t0 + P.tpt, P.tpt, it.len);
+    for (int k = 0; ok && get_item(k, it); ++k) {
+      const int n0 = blocks_of<C::kKeys>(it.t0, P.tpt, it.len), n1 = blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len);
       const int all = max(n0, n1), n = i ? n1 : n0;
-      const int cut = first_cut(it.t0);
-      if (lane == 0) {
-        auto scores = [&](int j) {
-          const int s = (base + 2 * j) % kStages;
-          if (!wait(&full[s], uint32_t((base + 2 * j) / kStages) & 1u)) return false;
+      const int cut = first_cut<C::kKeys>(it.t0);
+      if (n > 0 && is_s) ok = wait_all(&q_full[i], uint32_t(mine) & 1u);
+      if (n > 0 && !is_s && mine > 0) ok = wait_all(&o_free[i], uint32_t(mine - 1) & 1u);
+      for (int j = 0; ok && j < all; ++j, place += 2) {
+        const int s = place % kStages;
+        ok = wait_all(!is_s && j >= cut ? &clean[s] : &full[s], uint32_t(place / kStages) & 1u);
+        if (!ok) break;
+        if (j >= n) {  // a block that only the other tile has
+          if (lane == 0) mbar_arrive(&empty[s]);
+          continue;
+        }
+        if (is_s) {
+          // The softmax has read the block before.
+          if (blocks > 0 && !(ok = wait_all(&s_read[i], uint32_t(blocks - 1) & 1u))) break;
           tc_fence_after();
           const uint64_t kd = kd0 + uint64_t((uint32_t(s) * C::kTile) >> 4);
+          if (elected()) {
 #pragma unroll
-          for (int ks = 0; ks < kD / 16; ++ks) {
-            const uint64_t off = uint64_t((uint32_t(ks >> 2) * C::kHalf + uint32_t(ks & 3) * 32u) >> 4);
-            mma_bf16_ss(s_at, qd + off, kd + off, idesc_s, ks > 0 ? 1u : 0u);
-          }
-          tc_commit(&s_full[i]);
-          tc_commit(&empty[s]);
-          if (j == n - 1) tc_commit(&q_empty[i]);
-          return true;
-        };
-        // (The last item's P V of this tile is done: its o_done was waited for below.)
-        ok = n == 0 || (wait(&q_full[i], uint32_t(mine) & 1u) && scores(0));
-        for (int j = 0; ok && j < n; ++j) {
-          const int place = base + 2 * j + 1, s = place % kStages;
-          ok = wait(j >= cut ? &clean[s] : &full[s], uint32_t(place / kStages) & 1u);
-          if (ok && j == 0 && mine > 0) ok = wait(&o_free[i], uint32_t(mine - 1) & 1u);
-          const uint64_t vd = vd0 + uint64_t((uint32_t(s) * C::kTile) >> 4);
-          for (int h = 0; ok && h < 2; ++h) {
-            ok = wait(&p_full[2 * i + h], uint32_t(blocks + j) & 1u);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint64_t off = uint64_t((uint32_t(h) * 8192u + uint32_t(ks) * 2048u) >> 4);
-              mma_bf16_ts(o_at, s_at + uint32_t(32 * h + 8 * ks), vd + off, idesc_o, (j > 0 || h > 0 || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < kD / 16; ++ks) {
+              const uint32_t in = uint32_t(ks & 3) * 32u;
+              mma_bf16_ss(s_at, qd + uint64_t((uint32_t(ks >> 2) * C::kQHalf + in) >> 4),
+                          kd + uint64_t((uint32_t(ks >> 2) * C::kHalf + in) >> 4), idesc_s, ks > 0 ? 1u : 0u);
             }
+            tc_commit(&s_full[i]);
+            tc_commit(&empty[s]);
+            if (j == n - 1) tc_commit(&q_empty[i]);
           }
-          if (!ok) break;
-          tc_commit(&o_done[i]);
-          tc_commit(&empty[s]);
-          ok = wait(&o_done[i], uint32_t(blocks + j) & 1u);
-          if (ok && j + 1 < n) ok = scores(j + 1);
+        } else {
+          if (!(ok = wait_all(&p_full[i], uint32_t(blocks) & 1u))) break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + uint64_t((uint32_t(s) * C::kTile) >> 4);
+          if (elected()) {
+#pragma unroll
+            for (int ks = 0; ks < C::kKeys / 16; ++ks)
+              mma_bf16_ts(o_at, p_at + uint32_t(8 * ks), vd + uint64_t((uint32_t(ks) * 2048u) >> 4), idesc_o, (j > 0 || ks > 0) ? 1u : 0u);
+            tc_commit(&o_done[i]);
+            tc_commit(&empty[s]);
+          }
         }
-        // Blocks that only the other tile has: an arrival before the block has come would be
-        // counted for the stage's last one.
-        for (int place = base + 2 * n; ok && place < base + 2 * all; ++place) {
-          ok = wait(&full[place % kStages], uint32_t(place / kStages) & 1u);
-          if (ok) mbar_arrive(&empty[place % kStages]);
-        }
+        __syncwarp();
+        ++blocks;
       }
-      ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
-      if (!ok) break;
-      base += 2 * all;
-      blocks += n;
       mine += n > 0;
     }
-    // This thread's products are done before the block leaves: after a failed wait they may not be.
-    if (lane == 0) {
-      tc_commit(&drained[i]);
-      mbar_wait(&drained[i], 0, drain_limit_ns(lim));
+    // The products are done before the block leaves: after a failed wait they may not be.
+    if (elected()) {
+      tc_commit(&drained[warp - 8]);
+      mbar_wait(&drained[warp - 8], 0, drain_limit_ns(lim));
     }
-  } else if (warp == 11) {
+    __syncwarp();
+  } else if (warp == 13 || warp == 14) {
     // ------------------------------------------------- values that are not finite
     int base = 0;
     Item it;
     for (int k = 0; get_item(k, it); ++k) {
-      const int all = max(blocks_of(it.t0, P.tpt, it.len), blocks_of(it.t0 + P.tpt, P.tpt, it.len));
-      const int cut = base + 2 * first_cut(it.t0);
+      const int all = max(blocks_of<C::kKeys>(it.t0, P.tpt, it.len), blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len));
+      const int cut = base + 2 * first_cut<C::kKeys>(it.t0);
       bool ok = true;
       for (int place = base; place < base + 2 * all; ++place) {
         const int s = place % kStages;
@@ -450,16 +548,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         uint8_t* v = smem + C::kRing + uint32_t(s) * C::kTile;
-        uint4 keys;
-        uint32_t* word = &keys.x;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int row = 32 * w + lane;
+        for (int w = 0; w < 2; ++w) {
+          const int word = 2 * w + warp - 13, row = 32 * word + lane;   // 32 keys at a time
+          const bool there = row < C::kKeys;
           uint32_t acc = 0u;
 #pragma unroll
           for (int h = 0; h < C::kHalves; ++h)
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; there && c < 8; ++c) {
               const uint4 x = *reinterpret_cast<const uint4*>(v + h * C::kHalf + row * 128 + ((c ^ (row & 7)) << 4));
               acc = spot<kBf16>(x.w, spot<kBf16>(x.z, spot<kBf16>(x.y, spot<kBf16>(x.x, acc))));
             }
@@ -471,46 +568,50 @@ __global__ void __launch_bounds__(kThreads, 1)
               *at = make_uint4(finite_pair<kBf16>(x.x), finite_pair<kBf16>(x.y), finite_pair<kBf16>(x.z), finite_pair<kBf16>(x.w));
             }
           }
-          word[w] = __ballot_sync(0xFFFFFFFFu, odd);
+          const uint32_t keys = __ballot_sync(0xFFFFFFFFu, odd);
+          if (lane == 0) reinterpret_cast<uint32_t*>(&bad[s])[word] = keys;
         }
         fence_proxy_async_smem();
-        if (lane == 0) bad[s] = keys;
         __syncwarp();
         if (lane == 0) mbar_arrive(&clean[s]);
       }
       if (!ok) break;
       base += 2 * all;
     }
+  }
   } else {
+    more_registers<kSoftRegs>();
     // -------------------------------------------------------------- softmax
     const int i = warp >> 2;
     const int r = (warp & 3) * 32 + lane;          // row of the tile = TMEM lane
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t s_at = tmem + lane_off + C::kColS + 128u * i, o_at = tmem + lane_off + C::kColO + 128u * i;
+    const uint32_t s_at = tmem + lane_off + C::kColS + C::kNextS * i, p_at = tmem + lane_off + C::kColP + C::kNextP * i;
+    const uint32_t o_at = tmem + lane_off + C::kColO + C::kNextO * i;
     const float c = P.c;
     int base = 0, blocks = 0;
     Item it;
     for (int k = 0; get_item(k, it); ++k) {
       const int t0 = it.t0 + i * P.tpt;
-      const int n0 = blocks_of(it.t0, P.tpt, it.len), n1 = blocks_of(it.t0 + P.tpt, P.tpt, it.len);
+      const int n0 = blocks_of<C::kKeys>(it.t0, P.tpt, it.len), n1 = blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len);
       const int n = i ? n1 : n0;
       const int t = t0 + r / P.G;                   // the row's token, in its sequence
       const bool valid = r < P.tpt * P.G && t < it.len;
-      const int cut = first_cut(it.t0);             // (from here on values may have been taken out)
+      const int cut = first_cut<C::kKeys>(it.t0);             // (from here on values may have been taken out)
       float m = -INFINITY, l = 0.f;
       uint32_t odd = 0;                             // bit j - cut: the row sees a value of block j that is not finite
       bool ok = true;
       for (int j = 0; j < n; ++j) {
         if (!(ok = wait_all(&s_full[i], uint32_t(blocks + j) & 1u))) break;
         tc_fence_after();
-        uint32_t v[128];
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch) tmem_ld16(s_at + uint32_t(ch * 16), *reinterpret_cast<uint32_t(*)[16]>(&v[ch * 16]));
-        tmem_ld_wait128(v);
+        uint32_t v[C::kKeys];
+        load_scores<C::kKeys>(s_at, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_read[i]);
         if (j >= cut) {
-          const int see = t - j * kKeys + 1;        // keys of the block that the row sees
+          const int see = t - j * C::kKeys + 1;     // keys of the block that the row sees
 #pragma unroll
-          for (int x = 0; x < 128; ++x)
+          for (int x = 0; x < C::kKeys; ++x)
             if (x >= see) v[x] = __float_as_uint(-INFINITY);
           const int place = base + 2 * j + 1, s = place % kStages;
           if (!(ok = wait_all(&clean[s], uint32_t(place / kStages) & 1u))) break;
@@ -518,14 +619,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (keys.x | keys.y | keys.z | keys.w) {
             const uint32_t word[4] = {keys.x, keys.y, keys.z, keys.w};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < (C::kKeys + 31) / 32; ++w) {
               const int lim_w = see - 32 * w;
               const uint32_t seen = lim_w >= 32 ? ~0u : lim_w <= 0 ? 0u : (1u << lim_w) - 1u;
               if (word[w] & seen) odd |= 1u << (j - cut);
             }
           }
         }
-        const float mx = block_max<128>(v) * c;
+        const float mx = largest(v) * c;
         float factor = 1.f;
         if (mx > m + kRescale) {
           factor = fast_exp2(m - mx);               // 0 while m = -inf
@@ -539,16 +640,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
         }
         const float negm = m == -INFINITY ? 0.f : -m;
-        l *= factor;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          l += weights64<kBf16>(v + 64 * h, c, negm);
-          tmem_st16(s_at + uint32_t(32 * h), *reinterpret_cast<uint32_t(*)[16]>(&v[64 * h]));
-          tmem_st16(s_at + uint32_t(32 * h + 16), *reinterpret_cast<uint32_t(*)[16]>(&v[64 * h + 16]));
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&p_full[2 * i + h]);
-        }
+        l = l * factor + weights<kBf16>(v, c, negm);
+        // P of the block before has been used.
+        if (j > 0 && !(ok = wait_all(&o_done[i], uint32_t(blocks + j - 1) & 1u))) break;
+        store_weights<C::kKeys / 2>(p_at, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[i]);
       }
       if (!ok) break;
       if (n > 0) {
@@ -567,10 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
           if (odd && valid) {
             // Values that were taken out, of the keys that the row sees: as they are.
-            for (int b = 0; b < 4; ++b) {
+            for (int b = 0; b < kMostCut; ++b) {
               if (!((odd >> b) & 1u)) continue;
-              const int key0 = (cut + b) * kKeys;
-              for (int key = key0; key < key0 + kKeys && key <= t; ++key) {
+              const int key0 = (cut + b) * C::kKeys;
+              for (int key = key0; key < key0 + C::kKeys && key <= t; ++key) {
                 const uint16_t* src = static_cast<const uint16_t*>(P.V) + int64_t(it.first - it.t0 + key) * P.v_tok + int64_t(it.head) * P.v_head + 32 * ch;
 #pragma unroll
                 for (int x = 0; x < 32; ++x) {
@@ -596,7 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
-        mbar_arrive(&o_free[i]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[i]);
       }
       base += 2 * max(n0, n1);
       blocks += n;
@@ -606,13 +705,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   cta_sync();
   // Only now is no wait left that could expire: after one, copies may be in flight still.
-  if (*abort_flag && warp == 8 && lane == 0) {
+  if (*abort_flag && warp == 12 && lane == 0) {
     for (int k = copied[0] > kStages ? copied[0] - kStages : 0; k < copied[0]; ++k)
       mbar_wait(&full[k % kStages], uint32_t(k / kStages) & 1u, drain_limit_ns(lim));
     for (int i = 0; i < 2; ++i)
       if (q_copied[i] > 0) mbar_wait(&q_full[i], uint32_t(q_copied[i] - 1) & 1u, drain_limit_ns(lim));
   }
-  if (warp == 9) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -698,9 +797,10 @@ int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_s
   P.limit_ns = wait_limit_ns();
   const bool bf16 = dtype == W12_BF16;
   CUtensorMap q, k, v;
+  const int keys = head_dim == 128 ? Cfg<128>::kKeys : Cfg<64>::kKeys;
   if (!row_map(&q, Q, bf16, head_dim, Hq, total, q_token_stride, q_head_stride, P.G, P.tpt) ||
-      !row_map(&k, K, bf16, head_dim, Hkv, total, k_token_stride, k_head_stride, 1, kKeys) ||
-      !row_map(&v, V, bf16, head_dim, Hkv, total, v_token_stride, v_head_stride, 1, kKeys))
+      !row_map(&k, K, bf16, head_dim, Hkv, total, k_token_stride, k_head_stride, 1, keys) ||
+      !row_map(&v, V, bf16, head_dim, Hkv, total, v_token_stride, v_head_stride, 1, keys))
     return W12_ERR_CUDA;
   const int sms = device_sm_count();
   const int64_t most = (total / (2 * P.tpt) + B) * Hkv;
