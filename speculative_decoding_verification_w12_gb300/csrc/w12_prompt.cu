@@ -198,12 +198,21 @@ struct Walk {
 #define W12_W8(v, o) \
   "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
 
-// Each thread reads (valid after the wait for loads) or writes 32 columns of its own lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+// Each thread reads (valid after the wait for loads) columns of its own lane and their largest
+// value (NaN aside), or writes some.
+__device__ __forceinline__ void tmem_ld_max32(uint32_t taddr, uint32_t* v, float& top) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : W12_W8(v, 0), W12_W8(v, 8), W12_W8(v, 16), W12_W8(v, 24)
+      "tcgen05.ld.red.sync.aligned.32x32b.x32.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %32, [%33];"
+      : W12_W8(v, 0), W12_W8(v, 8), W12_W8(v, 16), W12_W8(v, 24), "=f"(top)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_max16(uint32_t taddr, uint32_t* v, float& top) {
+  asm volatile(
+      "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %16, "
+      "[%17];"
+      : W12_W8(v, 0), W12_W8(v, 8), "=f"(top)
       : "r"(taddr)
       : "memory");
 }
@@ -258,15 +267,24 @@ __device__ __forceinline__ float weights(uint32_t (&v)[N], float c, float negm) 
   return s.x + s.y;
 }
 
-// A row's scores from TMEM, ready to use.
+// A row's scores from TMEM, ready to use, and the largest of them (found by the load).
 template <int N>
-__device__ __forceinline__ void load_scores(uint32_t taddr, uint32_t (&v)[N]) {
+__device__ __forceinline__ float load_scores(uint32_t taddr, uint32_t (&v)[N]) {
+  constexpr int kParts = (N + 31) / 32;
+  float top[kParts];
 #pragma unroll
-  for (int ch = 0; ch < N / 32; ++ch) tmem_ld32(taddr + uint32_t(32 * ch), &v[32 * ch]);
-  if constexpr (N % 32) tmem_ld16(taddr + uint32_t(N - 16), *reinterpret_cast<uint32_t(*)[16]>(&v[N - 16]));
+  for (int ch = 0; ch < N / 32; ++ch) tmem_ld_max32(taddr + uint32_t(32 * ch), &v[32 * ch], top[ch]);
+  if constexpr (N % 32) tmem_ld_max16(taddr + uint32_t(N - 16), &v[N - 16], top[kParts - 1]);
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int k = 0; k < N; ++k) asm volatile("" : "+r"(v[k]));  // (no use of a value moves before the wait)
+  float m = -INFINITY;
+#pragma unroll
+  for (int ch = 0; ch < kParts; ++ch) {
+    asm volatile("" : "+f"(top[ch]));
+    m = fmaxf(m, top[ch]);
+  }
+  return m;
 }
 
 // N columns of weights to TMEM, done when it returns.
@@ -599,12 +617,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int cut = first_cut<C::kKeys>(it.t0);             // (from here on values may have been taken out)
       float m = -INFINITY, l = 0.f;
       uint32_t odd = 0;                             // bit j - cut: the row sees a value of block j that is not finite
-      bool ok = true;
+      // A wait is one vote of the warp a block (what follows is warp-collective): barriers are
+      // looked at early, and waited for only where that has not shown them complete.
+      bool ok = true, come = false;                 // come: the block's scores are there
       for (int j = 0; j < n; ++j) {
-        if (!(ok = wait_all(&s_full[i], uint32_t(blocks + j) & 1u))) break;
+        if (!come) ok = wait(&s_full[i], uint32_t(blocks + j) & 1u);
+        __syncwarp();
         tc_fence_after();
+        const bool used = j == 0 || mbar_try_wait(&o_done[i], uint32_t(blocks + j - 1) & 1u);  // P of the block before
         uint32_t v[C::kKeys];
-        load_scores<C::kKeys>(s_at, v);
+        float top = load_scores<C::kKeys>(s_at, v);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_read[i]);
@@ -613,6 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int x = 0; x < C::kKeys; ++x)
             if (x >= see) v[x] = __float_as_uint(-INFINITY);
+          top = largest(v);
           const int place = base + 2 * j + 1, s = place % kStages;
           if (!(ok = wait_all(&clean[s], uint32_t(place / kStages) & 1u))) break;
           const uint4 keys = bad[s];
@@ -626,23 +649,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float mx = largest(v) * c;
+        const float mx = top * c;
         float factor = 1.f;
         if (mx > m + kRescale) {
           factor = fast_exp2(m - mx);               // 0 while m = -inf
           m = mx;
         }
         const bool resc = j > 0 && factor < 1.f && l > 0.f;
-        if (__any_sync(0xFFFFFFFFu, resc)) {
-          if (!(ok = wait_all(&o_done[i], uint32_t(blocks + j - 1) & 1u))) break;
-          tc_fence_after();
-          rescale_row<kD>(o_at, resc ? factor : 1.f);
-          tmem_st_wait();
+        if (__any_sync(0xFFFFFFFFu, resc || !used || !ok)) {
+          if (!used && ok) ok = wait(&o_done[i], uint32_t(blocks + j - 1) & 1u);
+          if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+          if (__any_sync(0xFFFFFFFFu, resc)) {
+            tc_fence_after();
+            rescale_row<kD>(o_at, resc ? factor : 1.f);
+            tmem_st_wait();
+          }
         }
         const float negm = m == -INFINITY ? 0.f : -m;
         l = l * factor + weights<kBf16>(v, c, negm);
-        // P of the block before has been used.
-        if (j > 0 && !(ok = wait_all(&o_done[i], uint32_t(blocks + j - 1) & 1u))) break;
+        come = j + 1 < n && mbar_try_wait(&s_full[i], uint32_t(blocks + j + 1) & 1u);
+        tc_fence_after();
         store_weights<C::kKeys / 2>(p_at, v);
         tc_fence_before();
         __syncwarp();
