@@ -531,7 +531,7 @@ int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const 
  *   O[i, h, :] = sum_{j <= i} softmax_j(scale * Q[i, h, :] . K[j, h / (Hq/Hkv), :]) * V[j, ..]
  * over the rows j of i's sequence. dtype W12_BF16 or W12_F16, of Q, K, V and O; O
  * [total, Hq, head_dim] contiguous, its rows outside the sequences left as they are.
- * Element strides are positive multiples of 8, pointers 16-byte aligned; head_dim 64
+ * Element strides are positive multiples of 8, pointers 16-byte aligned (O: 32); head_dim 64
  * or 128, Hq / Hkv <= 128, total < 2^31 - 256. Sequences of no rows are fine. One with offsets
  * out of [0, total], or decreasing ones, sets W12_ERR_ARG and is taken as empty (sequences
  * that share rows write either's result). Rows that a row does not see have no part in it, whatever they hold. Scores, softmax and sums are fp32; a weight

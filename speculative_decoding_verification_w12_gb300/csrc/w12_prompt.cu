@@ -45,7 +45,7 @@ using namespace attn_impl;
 constexpr int kThreads = 512;
 constexpr float kRescale = 8.0f;   // log2 growth of the maximum that triggers a rescale
 constexpr int kItems = 4;          // items handed out ahead
-constexpr int kItemReaders = 14;   // warps that read an item
+constexpr int kItemReaders = 15;   // warps that read an item
 constexpr int kMostCut = 5;        // blocks that the diagonal cuts in an item: 256 tokens of blocks of 80 or more
 
 // Registers: a warpgroup changes its share by one instruction that all its warps meet.
@@ -165,15 +165,15 @@ struct Walk {
     head = 0;
   }
   // The item `skip` places on.
-  __device__ __forceinline__ Item next(int64_t skip) {
+  __device__ __forceinline__ Item next(int skip) {
     const int chunks = (B + 31) / 32;
     Item it{0, 0, 0, -1};
     while (level >= 0) {
-      const int64_t here = int64_t(__popc(left)) * Hkv - head;
+      const int here = __popc(left) * Hkv - head;
       if (skip < here) {
-        const int64_t at = head + skip;
-        for (int64_t k = at / Hkv; k > 0; --k) left &= left - 1;
-        head = int(at % Hkv);
+        const int at = head + skip;
+        for (int k = at / Hkv; k > 0; --k) left &= left - 1;
+        head = at % Hkv;
         const int src = __ffs(left) - 1;
         it.t0 = level * step;
         it.first = __shfl_sync(0xFFFFFFFFu, start, src) + it.t0;
@@ -208,6 +208,14 @@ __device__ __forceinline__ void tmem_ld_max32(uint32_t taddr, uint32_t* v, float
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : W12_W8(v, 0), W12_W8(v, 8), W12_W8(v, 16), W12_W8(v, 24)
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld_max16(uint32_t taddr, uint32_t* v, float& top) {
   asm volatile(
       "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %16, "
@@ -226,6 +234,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::W12_R8(v, 0), "r"(taddr) : "memory");
+}
+
+// 32 bytes of memory of this thread's: a whole sector.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), W12_R8(w, 0) : "memory");
 }
 
 // The largest of N scores, three at a time (the two-operand maximum runs at the same rate).
@@ -319,6 +332,27 @@ __device__ __forceinline__ uint32_t spot(uint32_t x, uint32_t acc) {
   if constexpr (kBf16) asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
   else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(acc));
   return r;
+}
+
+// Adds to a row's outputs the values that were taken out of V, of the keys that the row sees, as
+// they are: infinities and NaN.
+template <int kKeys, int kD, bool kBf16>
+__device__ __noinline__ void add_taken_out(const Params& P, uint16_t* out, uint32_t odd, int cut, int t, int seq, int head) {
+  for (int b = 0; b < kMostCut; ++b) {
+    if (!((odd >> b) & 1u)) continue;
+    const int key0 = (cut + b) * kKeys;
+    for (int key = key0; key < key0 + kKeys && key <= t; ++key) {
+      const uint16_t* src = static_cast<const uint16_t*>(P.V) + int64_t(seq + key) * P.v_tok + int64_t(head) * P.v_head;
+#pragma unroll 1
+      for (int x = 0; x < kD; ++x) {
+        const uint32_t u = src[x];
+        if (finite16<kBf16>(u)) continue;
+        const uint32_t before = out[x];
+        const float f = kBf16 ? __uint_as_float(before << 16) + __uint_as_float(u << 16) : unpack_f16x2(before).x + unpack_f16x2(u).x;
+        out[x] = uint16_t(pack2<kBf16>(f, f));
+      }
+    }
+  }
 }
 
 template <int kD, bool kBf16>
@@ -421,12 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     fewer_registers<kRestRegs>();
   if (warp == 12) {
     // --------------------------------------------------------- items, copies
-    Walk walk{P.cu, P.B, P.Hkv, 2 * P.tpt, P.total};
-    walk.begin(blockIdx.x == 0 ? P.status : nullptr);
     int issued = 0, q_issued[2] = {0, 0};
     bool ok = true;
-    const int grid = int(gridDim.x), me = int(blockIdx.x);
-    int64_t skip = me;
+    Item it;
     auto stage = [&](const CUtensorMap* map, int head, int token) -> bool {
       const int s = issued % kStages;
       if (issued >= kStages && !wait(&empty[s], uint32_t(issued / kStages - 1) & 1u)) return false;
@@ -436,41 +467,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++issued;
       return true;
     };
-    for (int k = 0; ok; ++k) {
-      const Item it = walk.next(skip);
-      // Rounds alternate in direction: place `me` of even rounds, `grid - 1 - me` of odd ones.
-      skip = (k & 1) ? 2 * me : 2 * (grid - 1 - me);
-      // (walk.next leaves the walk on the item: the next one is skip + 1 places on.)
-      ++skip;
+    for (int k = 0; ok && get_item(k, it); ++k) {
       if (lane == 0) {
-        if (k >= kItems) ok = wait(&it_empty[k % kItems], uint32_t(k / kItems - 1) & 1u);
-        if (ok) {
-          items[k % kItems] = it;
-          mbar_arrive(&it_full[k % kItems]);
-        }
-        if (ok && it.head >= 0) {
-          const int seq = it.first - it.t0;
-          const int n0 = blocks_of<C::kKeys>(it.t0, P.tpt, it.len), n1 = blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len);
-          const int n = max(n0, n1);
-          for (int j = 0; ok && j < n; ++j) {
-            ok = stage(&tm_k, it.head, seq + j * C::kKeys);
-            if (j == 0) {
-              for (int i = 0; ok && i < (n1 ? 2 : 1); ++i) {
-                if (q_issued[i] > 0) ok = wait(&q_empty[i], uint32_t(q_issued[i] - 1) & 1u);
-                if (!ok) break;
-                mbar_arrive_expect_tx(&q_full[i], uint32_t(kD * 2 * P.G * P.tpt));
-                for (int h = 0; h < C::kHalves; ++h)
-                  load_box(smem + uint32_t(i) * C::kQTile + h * C::kQHalf, &tm_q, 64 * h, it.head * P.G, it.first + i * P.tpt,
-                           &q_full[i]);
-                ++q_issued[i];
-              }
+        const int seq = it.first - it.t0;
+        const int n0 = blocks_of<C::kKeys>(it.t0, P.tpt, it.len), n1 = blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len);
+        const int n = max(n0, n1);
+        for (int j = 0; ok && j < n; ++j) {
+          ok = stage(&tm_k, it.head, seq + j * C::kKeys);
+          if (j == 0) {
+            for (int i = 0; ok && i < (n1 ? 2 : 1); ++i) {
+              if (q_issued[i] > 0) ok = wait(&q_empty[i], uint32_t(q_issued[i] - 1) & 1u);
+              if (!ok) break;
+              mbar_arrive_expect_tx(&q_full[i], uint32_t(kD * 2 * P.G * P.tpt));
+              for (int h = 0; h < C::kHalves; ++h)
+                load_box(smem + uint32_t(i) * C::kQTile + h * C::kQHalf, &tm_q, 64 * h, it.head * P.G, it.first + i * P.tpt,
+                         &q_full[i]);
+              ++q_issued[i];
             }
-            if (ok) ok = stage(&tm_v, it.head, seq + j * C::kKeys);
           }
+          if (ok) ok = stage(&tm_v, it.head, seq + j * C::kKeys);
         }
       }
       ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
-      if (it.head < 0) break;
     }
     grid_dep_launch();
     if (lane == 0) {
@@ -549,6 +567,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait(&drained[warp - 8], 0, drain_limit_ns(lim));
     }
     __syncwarp();
+  } else if (warp == 15) {
+    // ---------------------------------------------------------------- items
+    Walk walk{P.cu, P.B, P.Hkv, 2 * P.tpt, P.total};
+    walk.begin(blockIdx.x == 0 ? P.status : nullptr);
+    const int grid = int(gridDim.x), me = int(blockIdx.x);
+    int skip = me;
+    for (int k = 0;; ++k) {
+      const Item it = walk.next(skip);
+      // Rounds alternate in direction: place `me` of even rounds, `grid - 1 - me` of odd ones.
+      // (walk.next leaves the walk on the item: the next one is one place more on.)
+      skip = ((k & 1) ? 2 * me : 2 * (grid - 1 - me)) + 1;
+      if (k >= kItems && !wait_all(&it_empty[k % kItems], uint32_t(k / kItems - 1) & 1u)) break;
+      if (lane == 0) {
+        items[k % kItems] = it;
+        mbar_arrive(&it_full[k % kItems]);
+      }
+      if (it.head < 0) break;
+    }
   } else if (warp == 13 || warp == 14) {
     // ------------------------------------------------- values that are not finite
     int base = 0;
@@ -606,14 +642,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_at = tmem + lane_off + C::kColS + C::kNextS * i, p_at = tmem + lane_off + C::kColP + C::kNextP * i;
     const uint32_t o_at = tmem + lane_off + C::kColO + C::kNextO * i;
     const float c = P.c;
+    const int row_t = r / P.G, row_h = r - row_t * P.G;  // the row's token of the tile and head of the group
     int base = 0, blocks = 0;
     Item it;
     for (int k = 0; get_item(k, it); ++k) {
       const int t0 = it.t0 + i * P.tpt;
       const int n0 = blocks_of<C::kKeys>(it.t0, P.tpt, it.len), n1 = blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len);
       const int n = i ? n1 : n0;
-      const int t = t0 + r / P.G;                   // the row's token, in its sequence
-      const bool valid = r < P.tpt * P.G && t < it.len;
+      const int t = t0 + row_t;                     // the row's token, in its sequence
+      const bool valid = row_t < P.tpt && t < it.len;
       const int cut = first_cut<C::kKeys>(it.t0);             // (from here on values may have been taken out)
       float m = -INFINITY, l = 0.f;
       uint32_t odd = 0;                             // bit j - cut: the row sees a value of block j that is not finite
@@ -636,18 +673,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < C::kKeys; ++x)
             if (x >= see) v[x] = __float_as_uint(-INFINITY);
           top = largest(v);
-          const int place = base + 2 * j + 1, s = place % kStages;
-          if (!(ok = wait_all(&clean[s], uint32_t(place / kStages) & 1u))) break;
-          const uint4 keys = bad[s];
-          if (keys.x | keys.y | keys.z | keys.w) {
-            const uint32_t word[4] = {keys.x, keys.y, keys.z, keys.w};
-#pragma unroll
-            for (int w = 0; w < (C::kKeys + 31) / 32; ++w) {
-              const int lim_w = see - 32 * w;
-              const uint32_t seen = lim_w >= 32 ? ~0u : lim_w <= 0 ? 0u : (1u << lim_w) - 1u;
-              if (word[w] & seen) odd |= 1u << (j - cut);
-            }
-          }
         }
         const float mx = top * c;
         float factor = 1.f;
@@ -667,6 +692,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float negm = m == -INFINITY ? 0.f : -m;
         l = l * factor + weights<kBf16>(v, c, negm);
+        if (j >= cut) {
+          const int see = t - j * C::kKeys + 1;
+          const int place = base + 2 * j + 1, s = place % kStages;
+          if (!(ok = wait_all(&clean[s], uint32_t(place / kStages) & 1u))) break;
+          const uint4 keys = bad[s];
+          if (keys.x | keys.y | keys.z | keys.w) {
+            const uint32_t word[4] = {keys.x, keys.y, keys.z, keys.w};
+#pragma unroll
+            for (int w = 0; w < (C::kKeys + 31) / 32; ++w) {
+              const int lim_w = see - 32 * w;
+              const uint32_t seen = lim_w >= 32 ? ~0u : lim_w <= 0 ? 0u : (1u << lim_w) - 1u;
+              if (word[w] & seen) odd |= 1u << (j - cut);
+            }
+          }
+        }
         come = j + 1 < n && mbar_try_wait(&s_full[i], uint32_t(blocks + j + 1) & 1u);
         tc_fence_after();
         store_weights<C::kKeys / 2>(p_at, v);
@@ -679,49 +719,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_all(&o_done[i], uint32_t(blocks + n - 1) & 1u)) break;
         tc_fence_after();
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
-        uint16_t* out = static_cast<uint16_t*>(P.O) + (int64_t(it.first - it.t0 + t) * P.Hq + it.head * P.G + r % P.G) * kD;
+        uint16_t* out = static_cast<uint16_t*>(P.O) + (int64_t(it.first - it.t0 + t) * P.Hq + it.head * P.G + row_h) * kD;
 #pragma unroll
-        for (int ch = 0; ch < kD / 32; ++ch) {
-          uint32_t o[32];
-          tmem_ld16(o_at + uint32_t(32 * ch), *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-          tmem_ld16(o_at + uint32_t(32 * ch + 16), *reinterpret_cast<uint32_t(*)[16]>(&o[16]));
-          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-          tmem_ld_wait(*reinterpret_cast<uint32_t(*)[16]>(&o[16]));
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * inv);
-          if (odd && valid) {
-            // Values that were taken out, of the keys that the row sees: as they are.
-            for (int b = 0; b < kMostCut; ++b) {
-              if (!((odd >> b) & 1u)) continue;
-              const int key0 = (cut + b) * C::kKeys;
-              for (int key = key0; key < key0 + C::kKeys && key <= t; ++key) {
-                const uint16_t* src = static_cast<const uint16_t*>(P.V) + int64_t(it.first - it.t0 + key) * P.v_tok + int64_t(it.head) * P.v_head + 32 * ch;
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                  const uint32_t u = src[x];
-                  if (!finite16<kBf16>(u)) {
-                    const float f = kBf16 ? __uint_as_float(u << 16) : unpack_f16x2(u).x;
-                    o[x] = __float_as_uint(__uint_as_float(o[x]) + f);
-                  }
-                }
-              }
-            }
+        for (int ch = 0; ch < kD / 64; ++ch) {
+          uint32_t o[64];
+          tmem_ld32(o_at + uint32_t(64 * ch), &o[0]);
+          tmem_ld32(o_at + uint32_t(64 * ch + 32), &o[32]);
+          tmem_ld_wait64(o);
+          if (ch == kD / 64 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_free[i]);
           }
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            o[x] = pack2<kBf16>(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
           if (valid) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              uint4 w;
-              w.x = pack2<kBf16>(__uint_as_float(o[8 * x]), __uint_as_float(o[8 * x + 1]));
-              w.y = pack2<kBf16>(__uint_as_float(o[8 * x + 2]), __uint_as_float(o[8 * x + 3]));
-              w.z = pack2<kBf16>(__uint_as_float(o[8 * x + 4]), __uint_as_float(o[8 * x + 5]));
-              w.w = pack2<kBf16>(__uint_as_float(o[8 * x + 6]), __uint_as_float(o[8 * x + 7]));
-              *reinterpret_cast<uint4*>(out + 32 * ch + 8 * x) = w;
-            }
+            for (int x = 0; x < 4; ++x) st_global32(out + 64 * ch + 16 * x, &o[8 * x]);
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&o_free[i]);
+        if (odd && valid) add_taken_out<C::kKeys, kD, kBf16>(P, out, odd, cut, t, it.first - it.t0, it.head);
       }
       base += 2 * max(n0, n1);
       blocks += n;
