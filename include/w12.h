@@ -482,8 +482,9 @@ int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ro
  *   of the first rot_dim values (a multiple of 16) the pairs (i, i + rot_dim/2),
  *   or with `interleaved` (2i, 2i + 1), become (y_i c - y_j s, y_j c + y_i s),
  *   c = table[pos][i], s = table[pos][rot_dim/2 + i]; the rest stays as it is.
- * All in fp32, each product and sum rounded by itself, r the fp32 value next to
- * the exact one: a row's result depends on the row alone. table is fp32
+ * All in fp32. Of keys each product and sum is rounded by itself, and r is the
+ * fp32 value next to the exact one: a key's result depends on its row alone.
+ * Queries are off by up to 2^-19 of the row's largest value. table is fp32
  * [max_pos, rot_dim], the weights fp32 [head_dim] or NULL (no norm), all 16-byte
  * aligned; 1e-12 <= eps. A row whose position is -1 is no token: its output is
  * zeros. So is one of another position outside [0, max_pos), which sets

@@ -2,18 +2,20 @@
 // way into the paged 4-bit cache; positions of a draft tree's nodes.
 //
 // A head's row x of d values, normed (weights w) and rotated by its token's position:
-//   y_i  = (x_i r) w_i,  r = fp32(1 / sqrt(mean x^2 + eps))
+//   y_i  = (x_i r) w_i,  r = 1 / sqrt(mean x^2 + eps)
 //   y_i' = y_i c - y_j s,  y_j' = y_j c + y_i s   for the pairs (i, j) of the first rot values,
 // c and s from a table of fp32 cosines and sines (a position's angle may be far from zero:
-// whoever makes the table works it out in 64 bits). Every product and sum of these lines is
-// rounded by itself, and r is the fp32 value next to the exact one (the sum of squares is
-// kept as a pair of fp32 numbers): so a row's result depends on nothing but the row, and
-// what the cache gets is bitwise what its append writes for rows rotated to fp32. A code at
-// the border of two would otherwise hang on the order of a sum.
+// whoever makes the table works it out in 64 bits). Keys: every product and sum of these lines
+// is rounded by itself, and r is the fp32 value next to the exact one, so that a row's result
+// depends on nothing but the row, and what the cache gets is bitwise what its append writes for
+// rows rotated to fp32. (A code at the border of two would otherwise hang on the order of a sum.)
+// Queries need no such care: plain fp32 sums and fused products, a third of the instructions.
 //
 // A group of d/16 lanes takes one row, a lane two words of 8 values that hold whole pairs:
 // words l and l + rot/16 where halves are paired (the words past rot two by two), any where
 // neighbours are. The floor is HBM: each row read once and written once.
+#include <type_traits>
+
 #include "w12_kv4_quant.cuh"
 
 namespace w12 {
@@ -39,33 +41,47 @@ struct RopeParams {
   int32_t* status;
 };
 
-// Sum of fp32 numbers as a pair: hi + lo is the sum to about 2^-46 of it.
+// A sum of fp32 numbers as a pair: hi + lo is the sum to about 2^-40 of it.
 struct Sum2 {
   float hi, lo;
-  // (The same for a + b as for b + a: lanes that join their sums get one result.)
-  __device__ __forceinline__ void add(float x, float e) {
+  __device__ __forceinline__ void add(float x) {
     const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
-    const float off = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
     hi = s;
-    lo = __fadd_rn(__fadd_rn(lo, e), off);
   }
 };
 
-// Sum of squares of a row that kLanes lanes hold, 16 values each, times 2^(2 down).
-template <int kLanes>
-__device__ __forceinline__ Sum2 sum_squares(const float (&x)[16], float scale) {
-  Sum2 s{0.f, 0.f};
+// Sum over the lanes of a row.
+template <int kRow>
+__device__ __forceinline__ float over_row(float v) {
+#pragma unroll
+  for (int o = kRow / 2; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
+// The sum of squares of a row that kRow lanes hold, in fp32 (about 2^-21 of it).
+template <int kRow>
+__device__ __forceinline__ float sum_squares(const float (&x)[16]) {
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i & 3] = fmaf(x[i], x[i], s[i & 3]);
+  return over_row<kRow>(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])));
+}
+
+// The same as a pair, from that sum `rough`, which is finite. Each square is cut in two at 2^-16
+// of the whole: by a fused addition of c = 1.5 2^m (whose last place is 2^(m - 23)) the upper
+// parts are whole multiples of it, and their sums exact in any order; the rests are small.
+template <int kRow>
+__device__ __forceinline__ Sum2 sum_squares2(const float (&x)[16], float rough) {
+  const float c = __uint_as_float((__float_as_uint(rough) & 0x7F800000u) + (7u << 23) + 0x400000u);
+  float hi[2] = {0.f, 0.f}, lo[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float v = __fmul_rn(x[i], scale), p = __fmul_rn(v, v);
-    s.add(p, fmaf(v, v, -p));
+    const float h = __fsub_rn(fmaf(x[i], x[i], c), c);
+    hi[i & 1] = __fadd_rn(hi[i & 1], h);
+    lo[i & 1] = __fadd_rn(lo[i & 1], fmaf(x[i], x[i], -h));
   }
-#pragma unroll
-  for (int o = kLanes / 2; o > 0; o >>= 1) {
-    const float h = __shfl_xor_sync(0xFFFFFFFFu, s.hi, o), l = __shfl_xor_sync(0xFFFFFFFFu, s.lo, o);
-    s.add(h, l);
-  }
-  return s;
+  return Sum2{over_row<kRow>(__fadd_rn(hi[0], hi[1])), over_row<kRow>(__fadd_rn(lo[0], lo[1]))};
 }
 
 // fp32(1 / sqrt(m.hi + m.lo)): one step of Newton's iteration from the approximation, its
@@ -80,60 +96,85 @@ __device__ __forceinline__ float rsqrt_of(Sum2 m) {
   return fmaf(r, e * fmaf(0.375f, e, 0.5f), r);
 }
 
-// The factor of a row's norm. Rows whose squares leave the fp32 range (values near 2^64) are
-// summed again 2^70 smaller.
-template <int kD>
-__device__ __forceinline__ float norm_factor(const float (&x)[16], float eps) {
-  constexpr int kLanes = kD / 16;
-  Sum2 s = sum_squares<kLanes>(x, 1.f);
-  float up = 1.f;
-  const bool huge = !(s.hi < 1e37f);
+// The factor of a row's norm; kNearest: the fp32 value next to the exact one. A row whose squares
+// leave the fp32 range (values near 2^60) is made 2^70 smaller first: x then has what the factor
+// is for.
+template <int kD, bool kNearest>
+__device__ __forceinline__ float norm_factor(float (&x)[16], float eps) {
+  constexpr int kRow = kD / 16;
+  float rough = sum_squares<kRow>(x);
+  const bool huge = !(rough < 1e35f);
   if (__any_sync(0xFFFFFFFFu, huge)) {
-    const Sum2 t = sum_squares<kLanes>(x, 0x1p-70f);
-    if (huge) {
-      s = t;
-      up = 0x1p-70f;
-      eps = 0.f;
-    }
+    const float scale = huge ? 0x1p-70f : 1.f;
+    if (huge) eps = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], scale);
+    rough = sum_squares<kRow>(x);
   }
-  s.hi *= 1.f / kD;
-  s.lo *= 1.f / kD;
-  if (!(s.hi < INFINITY)) return s.hi == INFINITY ? 0.f : NAN;
-  s.add(eps, 0.f);
-  return __fmul_rn(rsqrt_of(s), up);
+  Sum2 s;
+  if constexpr (kNearest) {
+    s = sum_squares2<kRow>(x, rough < INFINITY ? rough : 0.f);
+    s.add(0.f);
+    s.hi *= 1.f / kD;
+    s.lo *= 1.f / kD;
+    s.add(eps);
+  } else {
+    s = Sum2{fmaf(rough, 1.f / kD, eps), 0.f};
+  }
+  // (The lanes of a row take one way: their rough sums are the same.)
+  return rough < INFINITY ? rsqrt_of(s) : rough == INFINITY ? 0.f : NAN;
 }
 
-// Rotates the lane's words (see the top). tab: the position's row of the table.
-__device__ __forceinline__ void rotate16(float (&x)[16], const float* tab, int wa, int wb, int rot, bool pairs) {
+// What a lane's 16 values meet at a position: cosines and sines of their 8 pairs.
+struct Turn {
+  float c[8], s[8];
+};
+
+// Pairs of the lane's values and their cosines and sines. Halves paired: value i of word wa with
+// value i of word wb; the table's place is that of wa. Neighbours paired: 2i and 2i + 1 of each
+// word, the places those of both words.
+__device__ __forceinline__ Turn load_turn(const float* tab, int wa, int wb, int rot, bool pairs) {
+  Turn t;
   const int half = rot >> 1;
+  const int at[2] = {pairs ? 4 * wa : 8 * wa, pairs ? 4 * wb : 8 * wa + 4};
+  const bool in[2] = {pairs ? wa * 8 < rot : wb * 8 < rot, wb * 8 < rot};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
+    if (in[k]) {
+      c = *reinterpret_cast<const float4*>(tab + at[k]);
+      s = *reinterpret_cast<const float4*>(tab + half + at[k]);
+    }
+    t.c[4 * k] = c.x, t.c[4 * k + 1] = c.y, t.c[4 * k + 2] = c.z, t.c[4 * k + 3] = c.w;
+    t.s[4 * k] = s.x, t.s[4 * k + 1] = s.y, t.s[4 * k + 2] = s.z, t.s[4 * k + 3] = s.w;
+  }
+  return t;
+}
+
+// A pair turned; kEach: every product and sum rounded by itself.
+template <bool kEach>
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+  const float u = kEach ? __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)) : fmaf(-b, s, a * c);
+  const float v = kEach ? __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)) : fmaf(a, s, b * c);
+  a = u;
+  b = v;
+}
+
+// Rotates the lane's 16 values x[0 .. 7] (word wa), x[8 .. 15] (wb); words past rot stay.
+template <bool kEach>
+__device__ __forceinline__ void rotate16(float (&x)[16], const Turn& t, bool in_a, bool in_b, bool pairs) {
   if (pairs) {
+    if (in_a) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int w = k ? wb : wa;
-      if (w * 8 < rot) {
-        const float4 c4 = *reinterpret_cast<const float4*>(tab + 4 * w), s4 = *reinterpret_cast<const float4*>(tab + half + 4 * w);
-        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = x[8 * k + 2 * i], b = x[8 * k + 2 * i + 1];
-          x[8 * k + 2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-          x[8 * k + 2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-        }
-      }
+      for (int i = 0; i < 4; ++i) turn_pair<kEach>(x[2 * i], x[2 * i + 1], t.c[i], t.s[i]);
     }
-  } else if (wb * 8 < rot) {
+    if (in_b) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float4 c4 = *reinterpret_cast<const float4*>(tab + 8 * wa + 4 * k),
-                   s4 = *reinterpret_cast<const float4*>(tab + half + 8 * wa + 4 * k);
-      const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = x[4 * k + i], b = x[8 + 4 * k + i];
-        x[4 * k + i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-        x[8 + 4 * k + i] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
-      }
+      for (int i = 4; i < 8; ++i) turn_pair<kEach>(x[2 * i], x[2 * i + 1], t.c[i], t.s[i]);
     }
+  } else if (in_b) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn_pair<kEach>(x[i], x[8 + i], t.c[i], t.s[i]);
   }
 }
 
@@ -150,110 +191,138 @@ __device__ __forceinline__ void store8(void* out, int64_t at, int type, const fl
     o[0] = make_float4(x[0], x[1], x[2], x[3]);
     o[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
-    const bool b = type == W12_BF16;
     uint4 v;
-    v.x = b ? pack_bf16x2(x[0], x[1]) : pack_f16x2(x[0], x[1]);
-    v.y = b ? pack_bf16x2(x[2], x[3]) : pack_f16x2(x[2], x[3]);
-    v.z = b ? pack_bf16x2(x[4], x[5]) : pack_f16x2(x[4], x[5]);
-    v.w = b ? pack_bf16x2(x[6], x[7]) : pack_f16x2(x[6], x[7]);
+    if (type == W12_BF16)
+      v = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    else
+      v = make_uint4(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]), pack_f16x2(x[4], x[5]), pack_f16x2(x[6], x[7]));
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = v;
   }
 }
 
-template <int kD, typename E, bool kCache>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+// kHeads: heads of one token that a group of lanes takes one behind the other (weights and
+// table are read once for all of them, and all their loads are in flight together). kPlain:
+// queries go out in bf16, and all of a row is rotated by halves; the other cases are found as it runs.
+template <int kD, typename E, bool kCache, int kHeads, bool kPlain>
+__global__ void __launch_bounds__(kRopeThreads, kHeads == 1 ? 1 : 3) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kRow = kD / 16;  // lanes of a row
   grid_dep_wait();
   grid_dep_launch();
   // A block's rows are all of one kind: 0 queries, 1 keys, 2 values.
   const int kind = blockIdx.x < p.first[0] ? 0 : (!kCache || blockIdx.x < p.first[1]) ? 1 : 2;
   const uint32_t base = blockIdx.x - (kind == 0 ? 0u : p.first[kind - 1]);
-  const uint32_t row = base * uint32_t(kRopeThreads / kRow) + threadIdx.x / kRow;
+  const uint32_t unit = base * uint32_t(kRopeThreads / kRow) + threadIdx.x / kRow;
   const int l = threadIdx.x % kRow;
-  const uint32_t H = uint32_t(p.H[kind]);
-  const uint32_t tok = row / H, h = row - tok * H;
+  const uint32_t H = uint32_t(p.H[kind]), groups = (H + kHeads - 1) / kHeads;
+  const uint32_t tok = unit / groups, h0 = (unit - tok * groups) * kHeads;
   const bool live = tok < uint32_t(p.n);
-  const bool turns = kind != 2;
+  const int rot = kPlain ? kD : p.rot;
+  const bool pairs = !kPlain && p.pairs;
   // The lane's two words.
   int wa = l, wb = l + kRow;
-  const int R = p.rot >> 3;
-  if (turns && !p.pairs && R < 2 * kRow) {
+  const int R = rot >> 3;
+  if (!kPlain && kind != 2 && !pairs && R < 2 * kRow) {
     wa = l < (R >> 1) ? l : R + 2 * (l - (R >> 1));
     wb = l < (R >> 1) ? l + (R >> 1) : wa + 1;
   }
-  E a{}, b{};
-  int pos = -1, slot = -1;
-  if (live) {
-    const uint8_t* x = static_cast<const uint8_t*>(p.x[kind]) + (int64_t(tok) * p.tok[kind] + int64_t(h) * p.head[kind]) * E::kSize;
-    if (p.vec) {
-      a = load8<E, true>(x + wa * 8 * E::kSize);
-      b = load8<E, true>(x + wb * 8 * E::kSize);
-    } else {
-      a = load8<E, false>(x + wa * 8 * E::kSize);
-      b = load8<E, false>(x + wb * 8 * E::kSize);
+  // (Past the last row or head the loads are the last one's again.)
+  const uint32_t from = live ? tok : uint32_t(p.n) - 1;
+  E a[kHeads], b[kHeads];
+  const uint8_t* x0 = static_cast<const uint8_t*>(p.x[kind]) + int64_t(from) * p.tok[kind] * E::kSize;
+  const int64_t step = p.head[kind] * E::kSize;
+  if (p.vec) {
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const uint8_t* x = x0 + (kHeads == 1 ? h0 : min(h0 + k, H - 1)) * step;
+      a[k] = load8<E, true>(x + wa * 8 * E::kSize);
+      b[k] = load8<E, true>(x + wb * 8 * E::kSize);
     }
-    pos = p.positions[tok];
-    if (kCache) slot = p.slots[tok];
+  } else {
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const uint8_t* x = x0 + (kHeads == 1 ? h0 : min(h0 + k, H - 1)) * step;
+      a[k] = load8<E, false>(x + wa * 8 * E::kSize);
+      b[k] = load8<E, false>(x + wb * 8 * E::kSize);
+    }
   }
+  const int pos = p.positions[from], slot = kCache && live ? p.slots[from] : -1;
   const bool there = pos >= 0 && pos < p.max_pos;
   if (!there && pos != -1) set_status(p.status, W12_ERR_ARG);
-  uint3 q{};
+  const int page = slot >> p.p_shift;
+  const bool in = slot >= 0 && page < p.n_pages;
+  if (kCache && !in && slot != -1) set_status(p.status, W12_ERR_ARG);
+  const int r = slot & (p.P - 1), rr = kind == 2 ? p.P + r : r;
+  // Where the row of head h of this token goes in the cache.
+  auto keep = [&](uint32_t h, const uint3& q) {
+    uint8_t* blk = p.pool + (int64_t(page) * p.H[1] + h) * p.block;
+    uint8_t* codes = blk + rr * (kD / 2);
+    *reinterpret_cast<uint32_t*>(codes + word_off(kD, r, wa)) = q.x;
+    *reinterpret_cast<uint32_t*>(codes + word_off(kD, r, wb)) = q.y;
+    if (l == 0) *reinterpret_cast<uint32_t*>(blk + p.P * kD + rr * 4) = q.z;
+  };
   if (kCache && kind == 2) {
-    if constexpr (kCache) q = quantise16<kRow>(a, b);
-  } else {
+    if constexpr (kCache) {
+#pragma unroll
+      for (int k = 0; k < kHeads; ++k) {
+        const uint3 q = quantise16<kRow>(a[k], b[k]);
+        if (in && there && h0 + k < H) keep(h0 + k, q);
+      }
+    }
+    return;
+  }
+  const bool in_a = kPlain || wa * 8 < rot, in_b = kPlain || wb * 8 < rot;
+  const Turn turn = load_turn(p.table + int64_t(there ? pos : 0) * rot, wa, wb, rot, pairs);
+  if (!there) {  // no token: zeros, whatever the rows hold
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) a[k] = b[k] = E{};
+  }
+  const float* w = kind ? p.kw : p.qw;
+  float g[16];
+  if (w) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 f = *reinterpret_cast<const float4*>(w + (k < 2 ? wa * 8 + 4 * k : wb * 8 + 4 * (k - 2)));
+      g[4 * k] = f.x, g[4 * k + 1] = f.y, g[4 * k + 2] = f.z, g[4 * k + 3] = f.w;
+    }
+  }
+  auto row = [&](int k, auto is_key) {
+    constexpr bool kKey = decltype(is_key)::value;
     float x[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      x[i] = a.value(i);
-      x[8 + i] = b.value(i);
+      x[i] = a[k].value(i);
+      x[8 + i] = b[k].value(i);
     }
-    const float* w = kind ? p.kw : p.qw;
     if (w) {
-      const float r = norm_factor<kD>(x, p.eps);
+      const float f = norm_factor<kD, kKey>(x, p.eps);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 g = *reinterpret_cast<const float4*>(w + (k < 2 ? wa * 8 + 4 * k : wb * 8 + 4 * (k - 2)));
-        x[4 * k] = __fmul_rn(__fmul_rn(x[4 * k], r), g.x);
-        x[4 * k + 1] = __fmul_rn(__fmul_rn(x[4 * k + 1], r), g.y);
-        x[4 * k + 2] = __fmul_rn(__fmul_rn(x[4 * k + 2], r), g.z);
-        x[4 * k + 3] = __fmul_rn(__fmul_rn(x[4 * k + 3], r), g.w);
-      }
+      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], f), g[i]);
     }
-    if (there) {
-      rotate16(x, p.table + int64_t(pos) * p.rot, wa, wb, p.rot, p.pairs);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    }
-    if (!kCache || kind == 0) {
-      if (live) {
-        const int64_t at = int64_t(row) * kD;
-        const int type = kCache ? int(W12_BF16) : p.out_type;
-        store8(p.out[kind], at + wa * 8, type, x);
-        store8(p.out[kind], at + wb * 8, type, x + 8);
-      }
-      return;
-    }
-    if constexpr (kCache) {
+    rotate16<kKey>(x, turn, in_a, in_b, pairs);
+    const bool mine = kHeads == 1 || h0 + k < H;
+    if constexpr (kCache && kKey) {
       F32 u, v;
+#pragma unroll
       for (int i = 0; i < 8; ++i) {
         u.w[i] = __float_as_uint(x[i]);
         v.w[i] = __float_as_uint(x[8 + i]);
       }
-      q = quantise16<kRow>(u, v);
+      const uint3 q = quantise16<kRow>(u, v);
+      if (in && there && mine) keep(h0 + k, q);
+    } else if (live && mine) {
+      const int64_t at = (int64_t(tok) * H + h0 + k) * kD;
+      const int type = kCache || kPlain ? int(W12_BF16) : p.out_type;
+      store8(p.out[kKey], at + wa * 8, type, x);
+      store8(p.out[kKey], at + wb * 8, type, x + 8);
     }
+  };
+  if (kind == 0) {
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) row(k, std::false_type());
+  } else {
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) row(k, std::true_type());
   }
-  const int page = slot >> p.p_shift;
-  const bool in = slot >= 0 && page < p.n_pages;
-  if (!in && slot != -1) set_status(p.status, W12_ERR_ARG);
-  if (!in || !there) return;
-  const int r = slot & (p.P - 1);
-  uint8_t* blk = p.pool + (int64_t(page) * p.H[1] + h) * p.block;
-  const int rr = kind == 2 ? p.P + r : r;
-  uint8_t* codes = blk + rr * (kD / 2);
-  *reinterpret_cast<uint32_t*>(codes + word_off(kD, r, wa)) = q.x;
-  *reinterpret_cast<uint32_t*>(codes + word_off(kD, r, wb)) = q.y;
-  if (l == 0) *reinterpret_cast<uint32_t*>(blk + p.P * kD + rr * 4) = q.z;
 }
 
 // ---------------------------------------------------------------- positions
@@ -325,15 +394,36 @@ static cudaLaunchConfig_t config(unsigned grid, int threads, cudaStream_t stream
   return cfg;
 }
 
-template <bool kCache>
+constexpr int kGroup = 4;  // heads of a group of lanes, where there are rows enough
+
+template <bool kCache, int kHeads, bool kPlain>
 static cudaError_t launch_rope(const cudaLaunchConfig_t& cfg, const RopeParams& p, int d, int dtype) {
   if (d == 128)
-    return dtype == W12_F32    ? cudaLaunchKernelEx(&cfg, rope_kernel<128, F32, kCache>, p)
-           : dtype == W12_BF16 ? cudaLaunchKernelEx(&cfg, rope_kernel<128, Half<true>, kCache>, p)
-                               : cudaLaunchKernelEx(&cfg, rope_kernel<128, Half<false>, kCache>, p);
-  return dtype == W12_F32    ? cudaLaunchKernelEx(&cfg, rope_kernel<64, F32, kCache>, p)
-         : dtype == W12_BF16 ? cudaLaunchKernelEx(&cfg, rope_kernel<64, Half<true>, kCache>, p)
-                             : cudaLaunchKernelEx(&cfg, rope_kernel<64, Half<false>, kCache>, p);
+    return dtype == W12_F32    ? cudaLaunchKernelEx(&cfg, rope_kernel<128, F32, kCache, kHeads, kPlain>, p)
+           : dtype == W12_BF16 ? cudaLaunchKernelEx(&cfg, rope_kernel<128, Half<true>, kCache, kHeads, kPlain>, p)
+                               : cudaLaunchKernelEx(&cfg, rope_kernel<128, Half<false>, kCache, kHeads, kPlain>, p);
+  return dtype == W12_F32    ? cudaLaunchKernelEx(&cfg, rope_kernel<64, F32, kCache, kHeads, kPlain>, p)
+         : dtype == W12_BF16 ? cudaLaunchKernelEx(&cfg, rope_kernel<64, Half<true>, kCache, kHeads, kPlain>, p)
+                             : cudaLaunchKernelEx(&cfg, rope_kernel<64, Half<false>, kCache, kHeads, kPlain>, p);
+}
+
+// The launch over the rows that p names, by groups of heads where they fill the GPU.
+template <bool kCache>
+static int launch_rows(RopeParams p, int d, int dtype, void* stream) {
+  const int units = kRopeThreads / (d / 16);  // of a block
+  auto blocks = [&](int kind, int heads) -> int64_t {
+    return p.x[kind] ? (p.n * ((p.H[kind] + heads - 1) / heads) + units - 1) / units : 0;
+  };
+  const int64_t few = 8 * int64_t(device_sm_count());
+  const int heads = blocks(0, kGroup) + blocks(1, kGroup) + blocks(2, kGroup) >= few ? kGroup : 1;
+  int64_t at = 0;
+  for (int k = 0; k < 3; ++k) p.first[k] = unsigned(at += blocks(k, heads));
+  const bool plain = p.rot == d && !p.pairs && (kCache || p.out_type == W12_BF16);
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = config(unsigned(at), kRopeThreads, static_cast<cudaStream_t>(stream), attr);
+  return cuda_status(heads == 1 ? launch_rope<kCache, 1, false>(cfg, p, d, dtype)
+                     : plain    ? launch_rope<kCache, kGroup, true>(cfg, p, d, dtype)
+                                : launch_rope<kCache, kGroup, false>(cfg, p, d, dtype));
 }
 
 // The parts that both entry points check and fill in alike.
@@ -357,10 +447,8 @@ static int rope_params(const w12_rope* r, int d, int dtype, int64_t n, const int
   return W12_OK;
 }
 
-// Rows of one kind: their strides, alignment and blocks.
-static int rope_rows(RopeParams* p, int kind, const void* x, int64_t tok, int64_t head, int H, int d, int esize, int64_t* blocks,
-                     int64_t* strides) {
-  *blocks = 0;
+// Rows of one kind: their strides and alignment.
+static int rope_rows(RopeParams* p, int kind, const void* x, int64_t tok, int64_t head, int H, int esize, int64_t* strides) {
   p->H[kind] = H > 0 ? H : 1;
   if (!x) return W12_OK;
   if (!aligned(x, uintptr_t(esize))) return W12_ERR_ARG;
@@ -369,8 +457,6 @@ static int rope_rows(RopeParams* p, int kind, const void* x, int64_t tok, int64_
   p->tok[kind] = tok;
   p->head[kind] = head;
   *strides |= (tok | head) * esize | int64_t(reinterpret_cast<uintptr_t>(x) & 15);
-  const int rows = kRopeThreads / (d / 16);
-  *blocks = (p->n * H + rows - 1) / rows;
   return W12_OK;
 }
 
@@ -392,9 +478,9 @@ int w12_qk_norm_rope(const w12_rope* rope, int head_dim, const void* Q, int64_t 
       out_dtype > W12_F16)
     return W12_ERR_ARG;
   const int esize = dtype == W12_F32 ? 4 : 2;
-  int64_t nq, nk, strides = 0;
-  if ((st = rope_rows(&p, 0, Q, q_token_stride, q_head_stride, Hq, head_dim, esize, &nq, &strides)) ||
-      (st = rope_rows(&p, 1, K, k_token_stride, k_head_stride, Hkv, head_dim, esize, &nk, &strides)))
+  int64_t strides = 0;
+  if ((st = rope_rows(&p, 0, Q, q_token_stride, q_head_stride, Hq, esize, &strides)) ||
+      (st = rope_rows(&p, 1, K, k_token_stride, k_head_stride, Hkv, esize, &strides)))
     return st;
   if (!device_supported()) return W12_ERR_UNSUPPORTED;
   if (n == 0) return W12_OK;
@@ -402,10 +488,7 @@ int w12_qk_norm_rope(const w12_rope* rope, int head_dim, const void* Q, int64_t 
   p.out[0] = Q_out;
   p.out[1] = K_out;
   p.out_type = out_dtype;
-  p.first[0] = unsigned(nq);
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = config(unsigned(nq + nk), kRopeThreads, static_cast<cudaStream_t>(stream), attr);
-  return cuda_status(launch_rope<false>(cfg, p, head_dim, dtype));
+  return launch_rows<false>(p, head_dim, dtype, stream);
 }
 
 int w12_kv4_append_rope(const w12_kv4* cache, const w12_rope* rope, const void* Q, int64_t q_token_stride, int64_t q_head_stride,
@@ -419,10 +502,10 @@ int w12_kv4_append_rope(const w12_kv4* cache, const w12_rope* rope, const void* 
   if (st) return st;
   if (!K || !V || (Q && (!Q_out || !aligned(Q_out, 16)))) return W12_ERR_ARG;
   const int esize = dtype == W12_F32 ? 4 : 2, d = cache->head_dim;
-  int64_t nq, nk, nv, strides = 0;
-  if ((st = rope_rows(&p, 0, Q, q_token_stride, q_head_stride, Hq, d, esize, &nq, &strides)) ||
-      (st = rope_rows(&p, 1, K, k_token_stride, k_head_stride, cache->Hkv, d, esize, &nk, &strides)) ||
-      (st = rope_rows(&p, 2, V, v_token_stride, v_head_stride, cache->Hkv, d, esize, &nv, &strides)))
+  int64_t strides = 0;
+  if ((st = rope_rows(&p, 0, Q, q_token_stride, q_head_stride, Hq, esize, &strides)) ||
+      (st = rope_rows(&p, 1, K, k_token_stride, k_head_stride, cache->Hkv, esize, &strides)) ||
+      (st = rope_rows(&p, 2, V, v_token_stride, v_head_stride, cache->Hkv, esize, &strides)))
     return st;
   if (!device_supported()) return W12_ERR_UNSUPPORTED;
   if (n == 0) return W12_OK;
@@ -434,11 +517,7 @@ int w12_kv4_append_rope(const w12_kv4* cache, const w12_rope* rope, const void* 
   p.n_pages = int(cache->n_pages);
   p.P = cache->page_size;
   p.p_shift = p.P == 16 ? 4 : p.P == 32 ? 5 : p.P == 64 ? 6 : 7;
-  p.first[0] = unsigned(nq);
-  p.first[1] = unsigned(nq + nk);
-  cudaLaunchAttribute attr[1];
-  const cudaLaunchConfig_t cfg = config(unsigned(nq + nk + nv), kRopeThreads, static_cast<cudaStream_t>(stream), attr);
-  return cuda_status(launch_rope<true>(cfg, p, d, dtype));
+  return launch_rows<true>(p, d, dtype, stream);
 }
 
 int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const int32_t* q_len, int B, int T, int32_t* positions,

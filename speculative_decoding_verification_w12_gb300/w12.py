@@ -666,14 +666,14 @@ class KV4Cache:
                     status: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
         """append() with the keys normed and rotated on the way (see Rope). Q [n, Hq,
         head_dim] of the same rows and type, if given, comes back normed and rotated, bf16."""
-        n = K.shape[0]
-        if K.shape != V.shape or K.shape != (n, self.Hkv, self.head_dim):
+        (kp, kt, kh, _, ks), (vp, vt, vh, _, vs) = _head_rows(K, "K"), _head_rows(V, "V")
+        n, d, dtype = ks[0], self.head_dim, K.dtype
+        if ks != vs or ks != (n, self.Hkv, d):
             raise ValueError("K and V must be [n, Hkv, head_dim]")
-        if rope.head_dim != self.head_dim:
+        if rope.head_dim != d:
             raise ValueError("the rotation's head dimension must be the cache's")
-        ks, vs = _head_rows(K, "K"), _head_rows(V, "V")
-        qs = (0, 0, 0, 0) if Q is None else _head_rows(Q, "Q")
-        if V.dtype != K.dtype or (Q is not None and (Q.dtype != K.dtype or Q.shape[0] != n or Q.shape[2] != self.head_dim)):
+        qp, qt, qh, Hq, qs = _NO_ROWS if Q is None else _head_rows(Q, "Q")
+        if V.dtype is not dtype or (Q is not None and (Q.dtype is not dtype or qs != (n, Hq, d))):
             raise ValueError("Q, K and V must be rows of the same tokens, head dimension and type")
         _want(slots, "slots", torch.int32, (n,))
         _want(positions, "positions", torch.int32, (n,))
@@ -681,13 +681,13 @@ class KV4Cache:
             if out is not None:
                 raise ValueError("out without Q")
         elif out is None:
-            out = _empty(Q.shape, torch.bfloat16, Q.device, stream)
+            out = _empty(qs, torch.bfloat16, Q.device, stream)
         else:
-            _want(out, "out", torch.bfloat16, Q.shape)
+            _want(out, "out", torch.bfloat16, qs)
         if n:
-            _check(lib().w12_kv4_append_rope(self._ref, rope._ref, qs[0], qs[1], qs[2], qs[3], ks[0], ks[1], ks[2], vs[0],
-                                             vs[1], vs[2], _DTYPES[K.dtype], n, positions.data_ptr(), slots.data_ptr(),
-                                             _ptr(out), _ptr(status), _stream(stream)), "w12_kv4_append_rope")
+            _check(lib().w12_kv4_append_rope(self._ref, rope._ref, qp, qt, qh, Hq, kp, kt, kh, vp, vt, vh,
+                                             _DTYPES[dtype], n, positions.data_ptr(), slots.data_ptr(), _ptr(out),
+                                             _ptr(status), _stream(stream)), "w12_kv4_append_rope")
         return out
 
     def read(self, slots: torch.Tensor, out=None, status: torch.Tensor | None = None, stream=None):
@@ -832,18 +832,21 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 
 # Between the products of a layer: rotation, prompt attention, adapters
 # ---------------------------------------------------------------------------
 
-def _head_rows(x: torch.Tensor, what: str, dtypes=_DTYPES) -> tuple[int, int, int, int]:
-    """Address, strides of tokens and heads, and heads of rows [n, H, head_dim]."""
+def _head_rows(x: torch.Tensor, what: str, dtypes=_DTYPES):
+    """Address, strides of tokens and heads, heads, and (n, H, head_dim) of rows."""
     if x.dtype not in dtypes:
         raise TypeError(f"{what} must be one of {', '.join(str(t) for t in dtypes)}")
-    if x.dim() != 3 or not x.is_cuda:
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or not x.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor [n, heads, head_dim]")
-    n, H, d = x.shape
-    st = x.stride()
-    if x.numel() and st[2] != 1:
+    n, H, d = shape
+    if st[2] != 1 and n and H:
         raise ValueError(f"{what} must have a contiguous last dimension")
     # (An axis of one has no stride of its own.)
-    return x.data_ptr(), st[0] if n > 1 else H * d, st[1] if H > 1 else d, H
+    return x.data_ptr(), st[0] if n > 1 else H * d, st[1] if H > 1 else d, H, shape
+
+
+_NO_ROWS = (None, 0, 0, 0, None)
 
 
 class Rope:
@@ -885,24 +888,27 @@ class Rope:
         """(Q, K) normed and rotated, of type dtype, for rows Q [n, Hq, head_dim] and K
         [n, Hkv, head_dim] (fp32, bf16 or fp16; views with a contiguous last dimension;
         either may be None) at positions int32 [n] (-1: no token, zeros)."""
-        rows = [x for x in (Q, K) if x is not None]
-        if not rows:
+        some = Q if Q is not None else K
+        if some is None:
             raise ValueError("Q or K must be given")
-        qs, ks = ((0, 0, 0, 0) if x is None else _head_rows(x, "Q and K") for x in (Q, K))
-        n = rows[0].shape[0]
-        if any(x.shape[0] != n or x.shape[2] != self.head_dim or x.dtype != rows[0].dtype for x in rows):
+        qp, qt, qh, Hq, qs = _NO_ROWS if Q is None else _head_rows(Q, "Q")
+        kp, kt, kh, Hkv, ks = _NO_ROWS if K is None else _head_rows(K, "K")
+        n, d = some.shape[0], self.head_dim
+        if (Q is not None and qs != (n, Hq, d)) or (K is not None and (ks != (n, Hkv, d) or K.dtype is not some.dtype)):
             raise ValueError("Q and K must be rows of the same tokens and type, of the rotation's head dimension")
-        if dtype not in _DTYPES:
+        to = _DTYPES.get(dtype)
+        if to is None:
             raise TypeError("dtype must be float32, bfloat16 or float16")
         _want(positions, "positions", torch.int32, (n,))
         if out is None:
-            q, k = (None if x is None else _empty(x.shape, dtype, x.device, stream) for x in (Q, K))
+            q = None if Q is None else _empty(qs, dtype, some.device, stream)
+            k = None if K is None else _empty(ks, dtype, some.device, stream)
         else:
             q, k = (None if x is None else _want(o, "out", dtype, x.shape) for o, x in zip(out, (Q, K)))
         if n:
-            _check(lib().w12_qk_norm_rope(self._ref, self.head_dim, *qs, *ks, _DTYPES[rows[0].dtype], n,
-                                          positions.data_ptr(), _ptr(q), _ptr(k), _DTYPES[dtype], _ptr(status),
-                                          _stream(stream)), "w12_qk_norm_rope")
+            _check(lib().w12_qk_norm_rope(self._ref, d, qp, qt, qh, Hq, kp, kt, kh, Hkv, _DTYPES[some.dtype], n,
+                                          positions.data_ptr(), _ptr(q), _ptr(k), to, _ptr(status), _stream(stream)),
+                   "w12_qk_norm_rope")
         return q, k
 
 
@@ -939,9 +945,9 @@ def prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_seqle
     being rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]). Returns O
     [total, Hq, head_dim]; rows outside the sequences are left as they are."""
     half = (torch.bfloat16, torch.float16)
-    (q, qt, qh, Hq), (k, kt, kh, Hkv), (v, vt, vh, _) = _head_rows(Q, "Q", half), _head_rows(K, "K", half), _head_rows(V, "V", half)
-    total, _, d = Q.shape
-    if K.shape != V.shape or K.shape[0] != total or K.shape[2] != d or not Q.dtype == K.dtype == V.dtype:
+    q, qt, qh, Hq, (total, _, d) = _head_rows(Q, "Q", half)
+    (k, kt, kh, Hkv, ks), (v, vt, vh, _, vs) = _head_rows(K, "K", half), _head_rows(V, "V", half)
+    if ks != vs or ks != (total, Hkv, d) or not Q.dtype == K.dtype == V.dtype:
         raise ValueError("Q, K and V must be rows of the same tokens, head dimension and type")
     _want(cu_seqlens, "cu_seqlens", torch.int32)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
