@@ -1,20 +1,25 @@
 // Low-rank adapters of many requests beside a shared projection:
 //   Y[m, :] += scale_a B_a (A_a x_m),  a = ids[m],  m < M <= 256.
 //
-// Two launches. The first groups the rows by adapter into tiles of up to 16 (every block
-// does that for itself from the ids: 256 numbers), multiplies a tile's rows by A_a and
-// leaves T = scale (A x) for the second, which adds B_a T to the tile's rows of Y. So an
-// adapter that several requests share is read once for each 16 of their rows, and a row
-// without an adapter costs nothing.
+// Two launches. The first groups the rows by adapter into tiles of up to 16 (every block does
+// that for itself from the ids: 256 numbers), multiplies a tile's rows by A_a and leaves
+// T = scale (A x) for the second, which adds B_a T to the tile's rows of Y. So an adapter that
+// several requests share is read once for each 16 of their rows, and a row without an adapter
+// costs nothing. Up to 32 rows are grouped by one warp in a few instructions: then the second
+// launch does so too, and starts beside the first; for more it takes the tiles that the first
+// has written down (grouped by every block of it, 256 rows cost 13 of 47 us).
 //
 // Both are products of mma.sync m16n8k16 with 16 rows at a time: what is read decides, and a
 // tensor-memory tile of 128 rows would be nearly empty. T is fp32; the second product takes
 // it as the sum of three bf16 numbers (8 + 8 + 8 bits), since Y is fp32 and a T rounded to
 // bf16 would leave 2^-9 of the adapter's part. The order of K within a product is free, so a
-// lane's operands are 16 (A, X) or 8 bytes (B) in a row of memory.
+// lane's operands are 16 bytes of a row of memory (8 of B at rank 16 and below). The loads of a
+// step are in flight before the step before it computes.
 //
 // The first launch splits K over a cluster of eight blocks (and their eight warps); the
 // blocks' sums meet in distributed shared memory, in a fixed order.
+#include <algorithm>
+
 #include "w12_dev.cuh"
 #include "w12_host.h"
 
@@ -25,15 +30,19 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSplit = 8;        // blocks of a cluster, along K
 constexpr int kMaxRank = 128;
-constexpr int kCols = 512;       // columns of Y a block of the second launch
+// Columns of Y that a block of the second launch has at least: few rows want many blocks (256:
+// 5.7 us where 512 take 6.5, 16 rows of one adapter, N 5120), many rows longer ones (38 us where 256
+// take 40, 16 adapters, N 34,816).
+constexpr int kColsFew = 256, kCols = 512;
+constexpr int kFill = 4;         // blocks an SM of the second launch, which take the tiles in turn
 
 struct Params {
   const uint16_t *X, *A, *B;
   const float* scale;
   const int32_t* ids;
   float* Y;
-  int32_t* head;     // [0]: tiles; from 64 on 32 words a tile: its 16 rows (-1: none), its adapter
   uint32_t* frag;    // [tile][16 of the rank][term][lane][4]: T as operands
+  int32_t* head;     // [0]: tiles; from 64 on 32 words a tile: its 16 rows (-1: none), its adapter
   int64_t N, K, x_stride, y_stride;
   int M, n, rank;
   int32_t* status;
@@ -67,199 +76,328 @@ __device__ __forceinline__ float2 peer_load2(const float* p, uint32_t rank) {
 // What of x is left beside its bf16 part; nothing beside infinities and NaN.
 __device__ __forceinline__ float rest_of(float x, float part) { return fabsf(part) < INFINITY ? x - part : 0.f; }
 
-struct alignas(16) Tile {
-  int id[kMaxM];
-  int row[16];
-  int count[kWarps];
-  int key, rank;
+// Rows by adapter: a tile begins at the first row of an adapter and at every 16th after it.
+struct Tiles {
+  int run_key[kMaxM], run_at[kMaxM + 1], run_before[kMaxM];  // neighbours of one adapter: which, from where, rows of it before
+  int count[2][kWarps];
+  int row[16];        // of the tile in hand; -1: none
+  int key;            // its adapter
+  int nth;            // its place among the adapter's tiles
 };
 
-// Block-wide: the rows of tile `t` into s.row, its adapter into s.key (-1: no such tile); the
-// number of tiles. A tile begins at the first row of an adapter and at every 16th after it.
-__device__ __forceinline__ int find_tile(const Params& p, Tile& s, int t) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int key = -1;
-  if (tid < p.M) {
-    key = p.ids[tid];
-    if (key < -1 || key >= p.n) {
-      set_status(p.status, W12_ERR_ARG);
-      key = -1;
-    }
-  }
-  s.id[tid] = key;
-  if (tid < 16) s.row[tid] = -1;
-  if (tid == 0) s.key = -1;
+// A thread's row: its adapter, the rows of the same before it, and the tile that begins with it (-1).
+struct Mine {
+  int key, before, begins;
+};
+
+// Threads of the block before this one for which `yes` holds; in `all`, how many do.
+__device__ __forceinline__ int before_me(bool yes, int (&count)[kWarps], int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, yes);
+  if (lane == 0) count[warp] = __popc(mask);
   __syncthreads();
-  int before = 0;
-  const int4* all = reinterpret_cast<const int4*>(s.id);
-  for (int i = 0; key >= 0 && i < (tid + 3) / 4; ++i) {
-    const int4 v = all[i];
-    before += (v.x == key) + (v.y == key && 4 * i + 1 < tid) + (v.z == key && 4 * i + 2 < tid) + (v.w == key && 4 * i + 3 < tid);
-  }
-  const bool first = key >= 0 && before % 16 == 0;
-  const uint32_t firsts = __ballot_sync(0xFFFFFFFFu, first);
-  if (lane == 0) s.count[warp] = __popc(firsts);
-  __syncthreads();
-  int at = __popc(firsts & ((1u << lane) - 1u)), total = 0;
+  int at = __popc(mask & ((1u << lane) - 1u));
+  all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
-    at += w < warp ? s.count[w] : 0;
-    total += s.count[w];
+    at += w < warp ? count[w] : 0;
+    all += count[w];
   }
-  if (first && at == t) {
-    s.key = key;
-    s.rank = before / 16;
+  return at;
+}
+
+// Block-wide: every thread's row (the row of its index); the number of tiles. Neighbours of one
+// adapter (a request's rows) are taken together: runs are compared, not rows.
+__device__ __forceinline__ int sort_rows(const Params& p, Tiles& s, Mine& m) {
+  const int tid = threadIdx.x;
+  auto id_of = [&](int row) {
+    const int id = p.ids[row];
+    return id >= -1 && id < p.n ? id : -2;
+  };
+  m.key = tid < p.M ? id_of(tid) : -1;
+  if (m.key == -2) {
+    set_status(p.status, W12_ERR_ARG);
+    m.key = -1;
+  }
+  const int last = tid > 0 && tid < p.M ? max(id_of(tid - 1), -1) : -1;
+  const bool begins = tid == 0 || m.key != last;
+  int runs, total;
+  const int run = before_me(begins, s.count[0], runs) + begins - 1;
+  if (begins) {
+    s.run_key[run] = m.key;
+    s.run_at[run] = tid;
+  }
+  if (tid == 0) s.run_at[runs] = kThreads;
+  __syncthreads();
+  if (begins) {
+    int n = 0;
+    for (int j = 0; m.key >= 0 && j < run; ++j)
+      if (s.run_key[j] == m.key) n += s.run_at[j + 1] - s.run_at[j];
+    s.run_before[run] = n;
   }
   __syncthreads();
-  if (key >= 0 && key == s.key && before / 16 == s.rank) s.row[before % 16] = tid;
-  __syncthreads();
+  m.before = s.run_before[run] + tid - s.run_at[run];
+  const bool first = m.key >= 0 && m.before % 16 == 0;
+  const int at = before_me(first, s.count[1], total);
+  m.begins = first ? at : -1;
   return total;
 }
 
+constexpr int kFew = 32;   // rows that one warp groups
+
+// Of up to 32 rows, by every warp for itself: the rows g and g + 8 and the adapter of tile t; the
+// number of tiles.
+struct Few {
+  uint32_t same, firsts;
+  int key, before;
+};
+__device__ __forceinline__ int sort_few(const Params& p, Few& f) {
+  const int lane = threadIdx.x & 31;
+  f.key = lane < p.M ? p.ids[lane] : -1;
+  if (f.key < -1 || f.key >= p.n) {
+    set_status(p.status, W12_ERR_ARG);
+    f.key = -1;
+  }
+  f.same = __match_any_sync(0xFFFFFFFFu, f.key);
+  f.before = __popc(f.same & ((1u << lane) - 1u));
+  f.firsts = __ballot_sync(0xFFFFFFFFu, f.key >= 0 && f.before % 16 == 0);
+  return __popc(f.firsts);
+}
+__device__ __forceinline__ int nth_bit(uint32_t mask, int n) {  // n + 1 bits are set
+  for (; n > 0; --n) mask &= mask - 1;
+  return __ffs(mask) - 1;
+}
+__device__ __forceinline__ int few_tile(const Few& f, int t, int& r0, int& r1) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, from = nth_bit(f.firsts, t);
+  const int key = __shfl_sync(0xFFFFFFFFu, f.key, from), at = __shfl_sync(0xFFFFFFFFu, f.before, from);
+  const uint32_t same = __shfl_sync(0xFFFFFFFFu, f.same, from);
+  const int n = __popc(same) - at;   // rows from the tile's first on
+  r0 = g < n ? nth_bit(same, at + g) : -1;
+  r1 = g + 8 < n ? nth_bit(same, at + g + 8) : -1;
+  return key;
+}
+
+// Block-wide: the rows and the adapter of tile t (there is one) into s. Behind a barrier after
+// the last use of the tile before.
+__device__ __forceinline__ void take_tile(Tiles& s, const Mine& m, int t) {
+  if (threadIdx.x < 16) s.row[threadIdx.x] = -1;
+  if (m.begins == t) {
+    s.key = m.key;
+    s.nth = m.before / 16;
+  }
+  __syncthreads();
+  if (m.key >= 0 && m.key == s.key && m.before / 16 == s.nth) s.row[m.before % 16] = threadIdx.x;
+  __syncthreads();
+}
+
 // kR: rank rounded up to the next of 16, 32, 64, 128.
-template <int kR>
-__global__ void __launch_bounds__(kThreads) shrink_kernel(const __grid_constant__ Params p) {
+template <int kR, bool kSmall>
+__global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shrink_kernel(const __grid_constant__ Params p) {
   constexpr int kN = kR / 8;   // tiles of 8 of the rank
   constexpr int kParts = 4;
-  __shared__ Tile s;
+  __shared__ Tiles s;
   __shared__ __align__(16) float part[kParts][16][kR];
   grid_dep_wait();
   grid_dep_launch();
-  const int split = int(blockIdx.x), t = int(blockIdx.y);  // (the cluster is the grid's x)
-  const int total = find_tile(p, s, t);
-  if (split == 0 && t == 0 && threadIdx.x == 0) p.head[0] = total;
-  if (t >= total) return;  // the same in all of the cluster
+  const int split = int(blockIdx.x);  // (the cluster is the grid's x)
+  Mine m;
+  Few f;
+  const int total = kSmall ? sort_few(p, f) : sort_rows(p, s, m);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int a = s.key;
-  if (split == 0 && threadIdx.x < 17) p.head[64 + 32 * t + threadIdx.x] = threadIdx.x < 16 ? s.row[threadIdx.x] : a;
-  const int r0 = s.row[g], r1 = s.row[g + 8];
-  const uint16_t *x0 = p.X + int64_t(max(r0, 0)) * p.x_stride, *x1 = p.X + int64_t(max(r1, 0)) * p.x_stride;
-  const uint16_t* Aa = p.A + int64_t(a) * p.rank * p.K;
-  float acc[kN][4];
-#pragma unroll
-  for (int i = 0; i < kN; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  for (int64_t k = 32 * (split + kSplit * warp); k < p.K; k += 32 * kSplit * kWarps) {
-    const int64_t at = k + 8 * q;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    const bool in = at < p.K;  // K is a multiple of 8
-    const uint4 u0 = in && r0 >= 0 ? *reinterpret_cast<const uint4*>(x0 + at) : zero;
-    const uint4 u1 = in && r1 >= 0 ? *reinterpret_cast<const uint4*>(x1 + at) : zero;
-    uint4 w[kN];
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      w[i] = in && 8 * i + g < p.rank ? __ldg(reinterpret_cast<const uint4*>(Aa + int64_t(8 * i + g) * p.K + at)) : zero;
-    const uint32_t m0[4] = {u0.x, u1.x, u0.y, u1.y}, m1[4] = {u0.z, u1.z, u0.w, u1.w};
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      mma16816(acc[i], m0, w[i].x, w[i].y);
-      mma16816(acc[i], m1, w[i].z, w[i].w);
+  if (!kSmall && split == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.head[0] = total;
+  for (int t = int(blockIdx.y); t < total; t += int(gridDim.y)) {  // (the same in all of the cluster)
+    int a, r0, r1;
+    if constexpr (kSmall) {
+      a = few_tile(f, t, r0, r1);
+    } else {
+      take_tile(s, m, t);
+      a = s.key;
+      r0 = s.row[g];
+      r1 = s.row[g + 8];
+      if (split == 0 && threadIdx.x < 17) p.head[64 + 32 * t + threadIdx.x] = threadIdx.x < 16 ? s.row[threadIdx.x] : a;
     }
-  }
-  // The warps' sums: those of the later four onto those of the first four, then these.
+    const uint16_t *x0 = p.X + int64_t(max(r0, 0)) * p.x_stride, *x1 = p.X + int64_t(max(r1, 0)) * p.x_stride;
+    const uint16_t* Aa = p.A + int64_t(a) * p.rank * p.K;
+    float acc[kN][4];
 #pragma unroll
-  for (int step = 1; step >= 0; --step) {
-    if (warp / kParts == step) {
+    for (int i = 0; i < kN; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    // Steps ahead that loads are in flight: as the registers allow.
+    constexpr int kAhead = kR <= 16 ? 2 : 1;
+    constexpr int kStep = 32 * kSplit * kWarps;
+    uint4 u0[kAhead], u1[kAhead], w[kAhead][kN];
+    auto load = [&](int i, int64_t k) {
+      const int64_t at = k + 8 * q;
+      const bool in = at < p.K;  // K is a multiple of 8
+      u0[i] = in && r0 >= 0 ? *reinterpret_cast<const uint4*>(x0 + at) : zero;
+      u1[i] = in && r1 >= 0 ? *reinterpret_cast<const uint4*>(x1 + at) : zero;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        float2* lo = reinterpret_cast<float2*>(&part[warp % kParts][g][8 * i + 2 * q]);
-        float2* hi = reinterpret_cast<float2*>(&part[warp % kParts][g + 8][8 * i + 2 * q]);
-        if (step == 1) {
-          *lo = make_float2(acc[i][0], acc[i][1]);
-          *hi = make_float2(acc[i][2], acc[i][3]);
-        } else {
-          *lo = make_float2(lo->x + acc[i][0], lo->y + acc[i][1]);
-          *hi = make_float2(hi->x + acc[i][2], hi->y + acc[i][3]);
+      for (int j = 0; j < kN; ++j)
+        w[i][j] = in && 8 * j + g < p.rank ? __ldg(reinterpret_cast<const uint4*>(Aa + int64_t(8 * j + g) * p.K + at)) : zero;
+    };
+    int64_t k = 32 * (split + kSplit * warp);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i, k + i * kStep);
+    while (k < p.K) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {  // (past K all operands are zero)
+        const uint32_t m0[4] = {u0[i].x, u1[i].x, u0[i].y, u1[i].y}, m1[4] = {u0[i].z, u1[i].z, u0[i].w, u1[i].w};
+        uint4 v[kN];
+#pragma unroll
+        for (int j = 0; j < kN; ++j) v[j] = w[i][j];
+        load(i, k + kAhead * kStep);
+        k += kStep;
+#pragma unroll
+        for (int j = 0; j < kN; ++j) {
+          mma16816(acc[j], m0, v[j].x, v[j].y);
+          mma16816(acc[j], m1, v[j].z, v[j].w);
         }
       }
     }
-    __syncthreads();
-  }
-  for (int e = threadIdx.x; e < 16 * kR; e += kThreads) {
-    float v = 0.f;
+    // The warps' sums: those of the later four onto those of the first four, then these.
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) v += part[i][e / kR][e % kR];
-    part[0][e / kR][e % kR] = v;
-  }
-  __syncwarp();
-  cluster_sync();
-  // The blocks' sums, a share of the pairs each: T, three bf16 parts, in the operands' order.
-  const float scale = p.scale[a];
-  for (int e = split * kThreads + threadIdx.x; e < 8 * kR; e += kSplit * kThreads) {
-    const int row = e / (kR / 2), j = 2 * (e % (kR / 2));
-    float2 v = make_float2(0.f, 0.f);
+    for (int step = 1; step >= 0; --step) {
+      if (warp / kParts == step) {
 #pragma unroll
-    for (uint32_t c = 0; c < kSplit; ++c) {
-      const float2 o = peer_load2(&part[0][row][j], c);
-      v.x += o.x;
-      v.y += o.y;
+        for (int i = 0; i < kN; ++i) {
+          float2* lo = reinterpret_cast<float2*>(&part[warp % kParts][g][8 * i + 2 * q]);
+          float2* hi = reinterpret_cast<float2*>(&part[warp % kParts][g + 8][8 * i + 2 * q]);
+          if (step == 1) {
+            *lo = make_float2(acc[i][0], acc[i][1]);
+            *hi = make_float2(acc[i][2], acc[i][3]);
+          } else {
+            *lo = make_float2(lo->x + acc[i][0], lo->y + acc[i][1]);
+            *hi = make_float2(hi->x + acc[i][2], hi->y + acc[i][3]);
+          }
+        }
+      }
+      __syncthreads();
     }
-    v.x *= scale;
-    v.y *= scale;
-    uint32_t* out = p.frag + (int64_t(t) * (kR / 16) + j / 16) * 384 + ((row & 7) * 4 + (j % 16) / 4) * 4 + ((j & 2) ? 2 : 0) + (row >> 3);
+    for (int e = threadIdx.x; e < 16 * kR; e += kThreads) {
+      float v = 0.f;
 #pragma unroll
-    for (int term = 0; term < 3; ++term) {
-      const uint32_t b = pack_bf16x2(v.x, v.y);
-      out[term * 128] = b;
-      v.x = rest_of(v.x, __uint_as_float(b << 16));
-      v.y = rest_of(v.y, __uint_as_float(b & 0xFFFF0000u));
+      for (int i = 0; i < kParts; ++i) v += part[i][e / kR][e % kR];
+      part[0][e / kR][e % kR] = v;
     }
+    __syncwarp();
+    cluster_sync();
+    // The blocks' sums, a share of the pairs each: T, three bf16 parts, in the operands' order.
+    const float scale = p.scale[a];
+    for (int e = split * kThreads + threadIdx.x; e < 8 * kR; e += kSplit * kThreads) {
+      const int row = e / (kR / 2), j = 2 * (e % (kR / 2));
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+      for (uint32_t c = 0; c < kSplit; ++c) {
+        const float2 o = peer_load2(&part[0][row][j], c);
+        v.x += o.x;
+        v.y += o.y;
+      }
+      v.x *= scale;
+      v.y *= scale;
+      // At 32 and above a lane has 8 neighbours of 32, the first four of them in the first of two steps.
+      const int step = kR >= 32 ? 2 * (j / 32) + ((j & 4) ? 1 : 0) : 0, lane_q = kR >= 32 ? (j % 32) / 8 : j / 4;
+      uint32_t* out = p.frag + (int64_t(t) * (kR / 16) + step) * 384 + ((row & 7) * 4 + lane_q) * 4 + ((j & 2) ? 2 : 0) + (row >> 3);
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+        const uint32_t b = pack_bf16x2(v.x, v.y);
+        out[term * 128] = b;
+        v.x = rest_of(v.x, __uint_as_float(b << 16));
+        v.y = rest_of(v.y, __uint_as_float(b & 0xFFFF0000u));
+      }
+    }
+    __syncwarp();
+    cluster_sync();  // no block goes on while another reads its sums
   }
-  __syncwarp();
-  cluster_sync();  // no block leaves while another reads its sums
 }
 
-template <int kR>
-__global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ Params p) {
+template <int kR, bool kSmall>
+__global__ void __launch_bounds__(kThreads, kR > 64 ? 1 : kR > 32 ? 2 : 3) expand_kernel(const __grid_constant__ Params p) {
   constexpr int kC = kR / 16;
-  grid_dep_wait();
-  grid_dep_launch();
-  const int t = int(blockIdx.y);
-  if (t >= p.head[0]) return;
+  constexpr bool kWide = kR >= 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int32_t* tile = p.head + 64 + 32 * t;
-  const int r0 = tile[g], r1 = tile[g + 8], a = tile[16];
-  uint32_t T[kC][3][4];
-#pragma unroll
-  for (int c = 0; c < kC; ++c)
-#pragma unroll
-    for (int term = 0; term < 3; ++term) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p.frag + ((int64_t(t) * kC + c) * 3 + term) * 128 + lane * 4);
-      T[c][term][0] = v.x;
-      T[c][term][1] = v.y;
-      T[c][term][2] = v.z;
-      T[c][term][3] = v.w;
-    }
-  const uint16_t* Ba = p.B + int64_t(a) * p.N * p.rank;
-  float *y0 = p.Y + int64_t(max(r0, 0)) * p.y_stride, *y1 = p.Y + int64_t(max(r1, 0)) * p.y_stride;
-  // 16 columns a step: column 4q + {0, 1} of them from the first product, 4q + {2, 3} from
-  // the second, so that a lane holds four neighbours of a row.
-  const int64_t end = min(int64_t(blockIdx.x + 1) * kCols, p.N);
-  for (int64_t n = int64_t(blockIdx.x) * kCols + 16 * warp; n < end; n += 16 * kWarps) {
-    const int64_t b0 = n + 4 * (g >> 1) + (g & 1);
-    float4 u0 = make_float4(0.f, 0.f, 0.f, 0.f), u1 = u0;
-    if (r0 >= 0) u0 = *reinterpret_cast<const float4*>(y0 + n + 4 * q);
-    if (r1 >= 0) u1 = *reinterpret_cast<const float4*>(y1 + n + 4 * q);
-    float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
-    uint2 w0[kC], w1[kC];
-#pragma unroll
-    for (int c = 0; c < kC; ++c) {
-      const int k = 16 * c + 4 * q;
-      w0[c] = w1[c] = make_uint2(0, 0);
-      if (k < p.rank) {  // (the rank is a multiple of 8)
-        w0[c] = __ldg(reinterpret_cast<const uint2*>(Ba + b0 * p.rank + k));
-        w1[c] = __ldg(reinterpret_cast<const uint2*>(Ba + (b0 + 2) * p.rank + k));
-      }
-    }
-#pragma unroll
-    for (int term = 2; term >= 0; --term)
-#pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        mma16816(c0, T[c][term], w0[c].x, w0[c].y);
-        mma16816(c1, T[c][term], w1[c].x, w1[c].y);
-      }
-    if (r0 >= 0) *reinterpret_cast<float4*>(y0 + n + 4 * q) = make_float4(u0.x + c0[0], u0.y + c0[1], u0.z + c1[0], u0.w + c1[1]);
-    if (r1 >= 0) *reinterpret_cast<float4*>(y1 + n + 4 * q) = make_float4(u1.x + c0[2], u1.y + c0[3], u1.z + c1[2], u1.w + c1[3]);
+  // What the launch before writes of this is T alone where rows are few: their rows, Y and B are
+  // there before it ends.
+  Few f;
+  int total;
+  if constexpr (kSmall) {
+    total = sort_few(p, f);
+  } else {
+    grid_dep_wait();
+    total = p.head[0];
   }
+  bool waited = !kSmall;
+  for (int t = int(blockIdx.y); t < total; t += int(gridDim.y)) {
+    int r0, r1, a;
+    if constexpr (kSmall) {
+      a = few_tile(f, t, r0, r1);
+    } else {
+      const int32_t* tile = p.head + 64 + 32 * t;
+      r0 = tile[g], r1 = tile[g + 8], a = tile[16];
+    }
+    const uint16_t* Ba = p.B + int64_t(a) * p.N * p.rank;
+    float *y0 = p.Y + int64_t(max(r0, 0)) * p.y_stride + 4 * q, *y1 = p.Y + int64_t(max(r1, 0)) * p.y_stride + 4 * q;
+    // 16 columns a step: column 4q + {0, 1} of them from the first product, 4q + {2, 3} from
+    // the second, so that a lane holds four neighbours of a row.
+    struct Cols {
+      float4 u0, u1;
+      uint32_t w0[2 * kC], w1[2 * kC];
+    };
+    auto load = [&](Cols& c, int64_t n) {
+      const uint16_t* b0 = Ba + (n + 4 * (g >> 1) + (g & 1)) * p.rank;
+      const uint16_t* b1 = b0 + 2 * p.rank;
+      if constexpr (kWide) {
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kC / 2; ++i) {
+          const int k = 32 * i + 8 * q;
+          const bool in = k < p.rank;  // the rank is a multiple of 8
+          const uint4 f = in ? __ldg(reinterpret_cast<const uint4*>(b0 + k)) : zero, h = in ? __ldg(reinterpret_cast<const uint4*>(b1 + k)) : zero;
+          c.w0[4 * i] = f.x, c.w0[4 * i + 1] = f.y, c.w0[4 * i + 2] = f.z, c.w0[4 * i + 3] = f.w;
+          c.w1[4 * i] = h.x, c.w1[4 * i + 1] = h.y, c.w1[4 * i + 2] = h.z, c.w1[4 * i + 3] = h.w;
+        }
+      } else {
+        const bool in = 4 * q < p.rank;
+        const uint2 f = in ? __ldg(reinterpret_cast<const uint2*>(b0 + 4 * q)) : make_uint2(0, 0);
+        const uint2 h = in ? __ldg(reinterpret_cast<const uint2*>(b1 + 4 * q)) : make_uint2(0, 0);
+        c.w0[0] = f.x, c.w0[1] = f.y, c.w1[0] = h.x, c.w1[1] = h.y;
+      }
+      c.u0 = c.u1 = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r0 >= 0) c.u0 = *reinterpret_cast<const float4*>(y0 + n);
+      if (r1 >= 0) c.u1 = *reinterpret_cast<const float4*>(y1 + n);
+    };
+    const int64_t stride = 16 * int64_t(kWarps) * gridDim.x;
+    int64_t n = 16 * (int64_t(blockIdx.x) * kWarps + warp);
+    Cols next;
+    if (n < p.N) load(next, n);
+    if (!waited) grid_dep_wait();
+    waited = true;
+    uint32_t T[kC][3][4];
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+#pragma unroll
+      for (int term = 0; term < 3; ++term) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p.frag + ((int64_t(t) * kC + c) * 3 + term) * 128 + lane * 4);
+        T[c][term][0] = v.x, T[c][term][1] = v.y, T[c][term][2] = v.z, T[c][term][3] = v.w;
+      }
+    while (n < p.N) {
+      const Cols c = next;
+      const int64_t at = n;
+      n += stride;
+      if (n < p.N) load(next, n);
+      float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int term = 2; term >= 0; --term)
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+          mma16816(c0, T[i][term], c.w0[2 * i], c.w0[2 * i + 1]);
+          mma16816(c1, T[i][term], c.w1[2 * i], c.w1[2 * i + 1]);
+        }
+      if (r0 >= 0) *reinterpret_cast<float4*>(y0 + at) = make_float4(c.u0.x + c0[0], c.u0.y + c0[1], c.u0.z + c1[0], c.u0.w + c1[1]);
+      if (r1 >= 0) *reinterpret_cast<float4*>(y1 + at) = make_float4(c.u1.x + c0[2], c.u1.y + c0[3], c.u1.z + c1[2], c.u1.w + c1[3]);
+    }
+  }
+  if (!waited) grid_dep_wait();
+  grid_dep_launch();
 }
 
 static bool shape_ok(int64_t M, int n, int rank) {
@@ -273,11 +411,11 @@ static int64_t max_tiles(int64_t M, int n) {
   return t < M ? t : M;
 }
 
-static int padded_rank(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
-
 static size_t head_bytes(int64_t tiles) { return size_t(256 + 128 * tiles); }
 
-template <int kR>
+static int padded_rank(int rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : rank <= 64 ? 64 : 128; }
+
+template <int kR, bool kSmall>
 static cudaError_t launch(const Params& p, int64_t tiles, cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -286,17 +424,20 @@ static cudaError_t launch(const Params& p, int64_t tiles, cudaStream_t stream) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kSplit, unsigned(tiles));
+  // Clusters that the GPU holds at a time take the tiles in turn.
+  cfg.gridDim = dim3(kSplit, unsigned(std::min<int64_t>(tiles, (kR > 64 ? 1 : kR > 32 ? 2 : 3) * device_sm_count() / kSplit)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = overlap_enabled() ? 2 : 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, shrink_kernel<kR>, p);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, shrink_kernel<kR, kSmall>, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(unsigned((p.N + kCols - 1) / kCols), unsigned(tiles));
+  const int64_t cols = kSmall ? kColsFew : kCols, most = kFill * int64_t(device_sm_count());
+  const int64_t x = std::min((p.N + cols - 1) / cols, most);
+  cfg.gridDim = dim3(unsigned(x), unsigned(std::min(tiles, std::max<int64_t>(1, most / x))));
   cfg.attrs = attr + 1;
   cfg.numAttrs = overlap_enabled() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, expand_kernel<kR>, p);
+  return cudaLaunchKernelEx(&cfg, expand_kernel<kR, kSmall>, p);
 }
 
 }  // namespace lora
@@ -342,11 +483,12 @@ int w12_lora(const uint16_t* X, int64_t x_stride, int64_t M, const w12_adapters*
   p.rank = a.rank;
   p.status = dev_status;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool few = M <= kFew;
   switch (padded_rank(a.rank)) {
-    case 16: return cuda_status(launch<16>(p, tiles, s));
-    case 32: return cuda_status(launch<32>(p, tiles, s));
-    case 64: return cuda_status(launch<64>(p, tiles, s));
-    default: return cuda_status(launch<128>(p, tiles, s));
+    case 16: return cuda_status(few ? launch<16, true>(p, tiles, s) : launch<16, false>(p, tiles, s));
+    case 32: return cuda_status(few ? launch<32, true>(p, tiles, s) : launch<32, false>(p, tiles, s));
+    case 64: return cuda_status(few ? launch<64, true>(p, tiles, s) : launch<64, false>(p, tiles, s));
+    default: return cuda_status(few ? launch<128, true>(p, tiles, s) : launch<128, false>(p, tiles, s));
   }
 }
 
