@@ -819,7 +819,7 @@ int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_s
       Hq / Hkv > 128 || (head_dim != 64 && head_dim != 128))
     return W12_ERR_SHAPE;
   if (total == 0 || B == 0) return device_supported() ? W12_OK : W12_ERR_UNSUPPORTED;
-  if (!Q || !K || !V || !O || !aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16)) return W12_ERR_ARG;
+  if (!Q || !K || !V || !O || !aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 32)) return W12_ERR_ARG;
   if (!stride_ok(q_token_stride) || !stride_ok(q_head_stride) || !stride_ok(k_token_stride) || !stride_ok(k_head_stride) ||
       !stride_ok(v_token_stride) || !stride_ok(v_head_stride))
     return W12_ERR_ARG;

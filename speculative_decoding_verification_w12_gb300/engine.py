@@ -20,7 +20,8 @@ addresses page-locked memory in place).
 
 PagedVerifyStep is one layer's step over a paged 4-bit key/value cache: pages for
 the draft tree, the layer's products and attention, acceptance, log probabilities
-of what is answered, commit of the accepted path and the pages given back.
+of what is answered, commit of the accepted path and the pages given back; with
+the norms and the rotation of its heads and adapters of its products, if given.
 """
 from __future__ import annotations
 
@@ -162,9 +163,14 @@ class PagedVerifyStep:
 
     B requests of T draft nodes (B * T <= 256 rows). qkv, out and head are packed
     weights: hidden -> (Hq + 2 Hkv) * head_dim, Hq * head_dim -> hidden, hidden ->
-    vocabulary. Position encodings, norms and the MLP are the caller's: the step
-    takes the rows that enter the layer. length int32 [B] holds each request's
+    vocabulary. The MLP and the norms before it and before the layer are the caller's:
+    the step takes the rows that enter the layer. length int32 [B] holds each request's
     committed tokens and is advanced by every step.
+
+    rope (w12.Rope) norms and rotates queries and keys by position, a draft node's being
+    its depth behind the committed tokens; without it they are taken as they come.
+    adapters ({"qkv": w12.LoRA, "out": ..., "head": ...}, any of them) are added to
+    those products' rows, for the adapter of each request that run() is given.
 
     A request that there are no pages for, or whose tokens would pass max_len, is
     not served by a step: its length, pages and cached rows stay as they are, and
@@ -174,10 +180,17 @@ class PagedVerifyStep:
 
     def __init__(self, qkv: w12.W12Weights, out: w12.W12Weights, head: w12.W12Weights, B: int, T: int, Hq: int,
                  Hkv: int, head_dim: int, n_pages: int, page_size: int = 64, max_len: int = 8192, top_k: int = 8,
-                 device=None):
+                 device=None, rope: w12.Rope | None = None, adapters: dict[str, w12.LoRA] | None = None):
         dev = torch.device(device or "cuda")
         if qkv.N != (Hq + 2 * Hkv) * head_dim or out.K != Hq * head_dim or head.K != out.N:
             raise ValueError("qkv, out and head do not fit the heads")
+        if rope is not None and (rope.head_dim != head_dim or rope.table.shape[0] < max_len):
+            raise ValueError("the rotation must be of the heads' dimension and reach max_len positions")
+        self.rope, self.adapters = rope, dict(adapters or {})
+        for name, lora in self.adapters.items():
+            w = {"qkv": qkv, "out": out, "head": head}.get(name)
+            if w is None or (lora.K, lora.N) != (w.K, w.N):
+                raise ValueError("adapters must be of qkv, out or head, and of their sizes")
         self.B, self.T, self.M, self.Hq, self.Hkv, self.head_dim = B, T, B * T, Hq, Hkv, head_dim
         self.max_len = max_len
         self.qkv, self.out, self.head, self.top_k = qkv, out, head, top_k
@@ -208,8 +221,47 @@ class PagedVerifyStep:
         given = (new == 0) | (slots[:, :1] >= 0).any(1)
         self.length.copy_(torch.where(given & ~keep, length, self.length))
 
-    def run(self, X: torch.Tensor, parents: torch.Tensor, draft: torch.Tensor) -> dict:
+    def prompt(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_seqlens: torch.Tensor,
+               longest: int | None = None) -> torch.Tensor:
+        """Admit whole prompts, packed one behind the other, and attend over them.
+
+        Rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]) of Q [n, Hq, head_dim]
+        and K, V [n, Hkv, head_dim] (of one type: fp32, bf16 or fp16) are request b's
+        prompt, at positions 0, 1, ...; a request without rows stays as it is. longest
+        bounds the prompts' lengths (default: the rows, or max_len). Queries and keys are
+        normed and rotated where the step does that, keys and values are cached, and the
+        causal attention over them, before they are quantised, comes back as bf16 [n, Hq,
+        head_dim]. A prompt that there are no pages for, or that is too long, is attended
+        over but not cached: its request stays as it was, and the status word says so.
+        """
+        n, st = K.shape[0], self.status
+        T = max(1, min(n, self.max_len) if longest is None else min(longest, self.max_len))
+        length = cu_seqlens[1:] - cu_seqlens[:-1]
+        keep = length <= 0
+        start = torch.where(keep, self.length, 0)
+        new = torch.where(keep, 0, torch.where(length <= T, length, -1)).to(torch.int32)
+        slots = self.pages.reserve(start, new, T, status=st)
+        # The request and the place of each row; rows outside the prompts have none.
+        row = torch.arange(n, dtype=torch.int32, device=K.device)
+        b = (torch.searchsorted(cu_seqlens, row, right=True) - 1).clamp(0, self.B - 1)
+        at = row - cu_seqlens[b]
+        inside = (at >= 0) & (at < length[b])
+        slots = torch.where(inside & (at < T), slots[b, at.clamp(0, T - 1).long()], -1)
+        given = (slots.new_zeros(self.B).index_add_(0, b, (slots >= 0).to(torch.int32)) > 0) & ~keep
+        positions = torch.where(inside & (at < self.max_len), at, -1)
+        if self.rope is not None:
+            self.cache.append_rope(K, V, slots, self.rope, positions, status=st)
+            Q, K = self.rope.run(Q, K, positions, status=st)
+        else:
+            self.cache.append(K, V, slots, status=st)
+        half = [x.to(torch.bfloat16) for x in (Q, K, V)]
+        self.length.copy_(torch.where(given, length, self.length))
+        return w12.prompt_attention(*half, cu_seqlens, status=st)
+
+    def run(self, X: torch.Tensor, parents: torch.Tensor, draft: torch.Tensor,
+            adapter: torch.Tensor | None = None) -> dict:
         """One step on X bf16 [B * T, hidden], the draft trees parents, draft int32 [B, T].
+        adapter int32 [B]: the adapter of each request (-1, or without it: none).
 
         Returns path [B, T], path_len, accept_len, bonus (as verify_tree); tokens
         [B, T], the answered tokens in order (the accepted drafts, then the bonus
@@ -223,14 +275,27 @@ class PagedVerifyStep:
         nodes = torch.where(self.length <= self.max_len - T, self.nodes, -1)
         slots = self.pages.reserve(self.length, nodes, T, status=st)
         served = slots[:, 0] >= 0
-        Y = w12.gemm(X, self.qkv, ws=self._ws[0], status=st)
-        q, k, v = Y.split([self.Hq * d, self.Hkv * d, self.Hkv * d], 1)
+        q_len = torch.where(served, nodes, 0)
+        ids = None if adapter is None or not self.adapters else adapter[:, None].expand(B, T).reshape(M)
+
+        def product(name, x, w, ws):
+            y = w12.gemm(x, w, ws=ws, status=st)
+            if ids is not None and name in self.adapters:
+                self.adapters[name].run(x, y, ids, status=st)
+            return y
+        Y = product("qkv", X, self.qkv, self._ws[0])
+        q, k, v = (x.unflatten(1, (-1, d)) for x in Y.split([self.Hq * d, self.Hkv * d, self.Hkv * d], 1))
         # Keys and values are quantised straight from the fp32 product (views of it).
-        self.cache.append(k.unflatten(1, (self.Hkv, d)), v.unflatten(1, (self.Hkv, d)), slots, status=st)
-        O = self.attention.run(q.to(torch.bfloat16).view(B, T, self.Hq, d), self.cache, self.pages.table, self.length,
-                               parents=parents, q_len=torch.where(served, nodes, 0), status=st)
-        H = w12.gemm(O.view(M, self.Hq * d), self.out, ws=self._ws[1], status=st).to(torch.bfloat16)
-        logits = w12.gemm(H, self.head, ws=self._ws[2], status=st)
+        if self.rope is not None:
+            at = w12.tree_positions(self.length, parents, q_len=q_len, status=st)
+            q = self.cache.append_rope(k, v, slots.view(M), self.rope, at.view(M), Q=q, status=st)
+        else:
+            self.cache.append(k, v, slots, status=st)
+            q = q.to(torch.bfloat16)
+        O = self.attention.run(q.view(B, T, self.Hq, d), self.cache, self.pages.table, self.length, parents=parents,
+                               q_len=q_len, status=st)
+        H = product("out", O.view(M, self.Hq * d), self.out, self._ws[1]).to(torch.bfloat16)
+        logits = product("head", H, self.head, self._ws[2])
         path, path_len, accept_len, bonus, _ = w12.verify_tree(logits, parents, draft, ws=self._vws, status=st)
         path, bonus = torch.where(served[:, None], path, -1), torch.where(served, bonus, -1)
         path_len, accept_len = path_len * served, accept_len * served

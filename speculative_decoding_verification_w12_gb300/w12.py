@@ -971,13 +971,14 @@ class LoRA:
             raise ValueError("A must be [n, rank, K] and B [n, N, rank]")
         self.n, self.rank, self.K = A.shape
         self.N, self.max_rows = B.shape[1], int(max_rows)
+        if self.n < 1 or self.rank % 8 or not 8 <= self.rank <= 128 or self.K % 8 or self.N % 16 or not self.K or not self.N:
+            raise ValueError("the rank must be a multiple of 8 up to 128, K a multiple of 8, N of 16")
+        if not 1 <= self.max_rows <= 256:
+            raise ValueError("max_rows must be at most 256")
         self.A = _want(A, "A", torch.bfloat16)
         self.B = _want(B, "B", torch.bfloat16, (self.n, self.N, self.rank))
         self.scale = _want(scale, "scale", torch.float32, (self.n,))
-        nbytes = lib().w12_lora_ws_bytes(self.max_rows, self.n, self.rank)
-        if nbytes == 0 or self.K % 8 or self.N % 16:
-            raise W12Error(2, "w12_lora_ws_bytes")
-        self.ws = _kept_workspace(nbytes, A.device)
+        self.ws = _kept_workspace(lib().w12_lora_ws_bytes(self.max_rows, self.n, self.rank), A.device)
         self._struct = _Adapters(A.data_ptr(), B.data_ptr(), scale.data_ptr(), self.N, self.K, self.n, self.rank)
         self._ref = ctypes.byref(self._struct)
 
