@@ -292,8 +292,9 @@ __global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shr
         v.x += o.x;
         v.y += o.y;
       }
-      v.x *= scale;
-      v.y *= scale;
+      // (Columns past the rank: an infinity of X has met zeros there.)
+      v.x = j < p.rank ? v.x * scale : 0.f;
+      v.y = j + 1 < p.rank ? v.y * scale : 0.f;
       // At 32 and above a lane has 8 neighbours of 32, the first four of them in the first of two steps.
       const int step = kR >= 32 ? 2 * (j / 32) + ((j & 4) ? 1 : 0) : 0, lane_q = kR >= 32 ? (j % 32) / 8 : j / 4;
       uint32_t* out = p.frag + (int64_t(t) * (kR / 16) + step) * 384 + ((row & 7) * 4 + lane_q) * 4 + ((j & 2) ? 2 : 0) + (row >> 3);

@@ -140,3 +140,59 @@ def test_beside_the_packed_projection():
     w12.LoRA(A, B, scale).run(X, Y, to_dev_i32(ids))
     _check(X, base, Y, A, B, scale, ids)
     assert np.linalg.norm(base.cpu().numpy() - WO.gemm(Xb, WO.pack(Wb))) <= 1e-3 * np.linalg.norm(base.cpu().numpy())
+
+
+@pytest.mark.parametrize("r", [8, 16, 24, 40, 104])
+def test_an_infinity_of_a_row_meets_the_rank_alone(r):
+    """Weights above zero: the row's outputs are infinite, not NaN (2 and 40 rows: both groupings)."""
+    A, B, scale, g = _make(2, 48, 64, r)
+    A, B = A.abs() + 0.01, B.abs() + 0.01
+    for M in (2, 40):
+        X, Y0 = torch.rand((M, 64), generator=g, device="cuda").bfloat16(), torch.zeros((M, 48), device="cuda")
+        X[M // 2, 5] = float("inf")
+        Y, ids = Y0.clone(), [m % 2 for m in range(M)]
+        w12.LoRA(A, B, scale).run(X, Y, to_dev_i32(ids))
+        assert (Y[M // 2] == float("inf")).all()
+        Y[M // 2] = 0
+        ids[M // 2] = -1
+        _check(X, Y0, Y, A, B, scale, ids)
+
+
+def test_sizes_past_32_bits():
+    """Rows and adapters behind more than 2^31 values: bitwise what they give by themselves."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    scale = torch.ones(3, device="cuda")
+    for K, N in ((2 ** 23, 32), (64, 2 ** 23)):
+        A, B = (torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16) for s in ((3, 128, K), (3, N, 128)))
+        X, Y = torch.randn((5, K), generator=g, device="cuda").bfloat16(), torch.zeros((5, N), device="cuda")
+        alone = Y.clone()
+        w12.LoRA(A, B, scale).run(X, Y, to_dev_i32([2] * 5))
+        w12.LoRA(A[2:], B[2:], scale[2:]).run(X, alone, to_dev_i32([0] * 5))
+        assert Y.abs().min() > 0 and torch.equal(Y, alone)
+        del A, B, X, Y, alone
+    M, apart = 200, 2 ** 24
+    A, B, scale, g = _make(2, 64, 72, 16)
+    X = torch.empty(M * apart, dtype=torch.bfloat16, device="cuda").as_strided((M, 72), (apart, 1))
+    Y = torch.empty(M * apart, device="cuda").as_strided((M, 64), (apart, 1))
+    X.copy_(torch.randn((M, 72), generator=g, device="cuda"))
+    Y.zero_()
+    ids = [m % 3 - 1 for m in range(M)]
+    w12.LoRA(A, B, scale).run(X, Y, to_dev_i32(ids))
+    _check(X, torch.zeros((M, 64), device="cuda"), Y, A, B, scale, ids)
+
+
+def test_two_adapters_at_the_same_time():
+    """Objects of their own (each has a workspace) on two streams."""
+    sets = [_make(5, 512, 1024, r, seed=r) for r in (16, 64)]
+    work = []
+    for A, B, scale, g in sets:
+        X, ids = torch.randn((64, 1024), generator=g, device="cuda").bfloat16(), to_dev_i32(np.arange(64) % 5)
+        work.append((w12.LoRA(A, B, scale), X, ids, torch.cuda.Stream()))
+    want = [lora.run(X, torch.zeros((64, 512), device="cuda"), ids) for lora, X, ids, _ in work]
+    ys = [[torch.zeros((64, 512), device="cuda") for _ in range(20)] for _ in work]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for (lora, X, ids, s), y in zip(work, ys):
+            lora.run(X, y[i], ids, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for some, w in zip(ys, want) for y in some)
