@@ -483,7 +483,8 @@ int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ro
  *   or with `interleaved` (2i, 2i + 1), become (y_i c - y_j s, y_j c + y_i s),
  *   c = table[pos][i], s = table[pos][rot_dim/2 + i]; the rest stays as it is.
  * All in fp32. Of keys each product and sum is rounded by itself, and r is the
- * fp32 value next to the exact one: a key's result depends on its row alone.
+ * fp32 value next to the exact one (of the row times 2^-76, where values pass
+ * 2^50): a key's result depends on its row alone.
  * Queries are off by up to 2^-19 of the row's largest value. table is fp32
  * [max_pos, rot_dim], the weights fp32 [head_dim] or NULL (no norm), all 16-byte
  * aligned; 1e-12 <= eps. A row whose position is -1 is no token: its output is
@@ -518,7 +519,7 @@ int w12_kv4_append_rope(const w12_kv4* cache, const w12_rope* rope, const void* 
                         const int32_t* slots, uint16_t* Q_out, int32_t* dev_status, void* stream);
 
 /* Positions of new tokens, int32 [B, T]: prefix_len[b] + t, or with parents [B, T]
- * (T <= 256; parents[b, 0] = -1, 0 <= parents[b, i] < i) prefix_len[b] + the depth
+ * (T <= 256, without a tree 2^23; parents[b, 0] = -1, 0 <= parents[b, i] < i) prefix_len[b] + the depth
  * of node t; -1 from q_len[b] (NULL: T) on. Lengths out of range set W12_ERR_ARG, a
  * malformed tree W12_ERR_BAD_TREE, and that request's positions are -1. Errors:
  * W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
@@ -535,9 +536,9 @@ int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const 
  * Element strides are positive multiples of 8, pointers 16-byte aligned (O: 32); head_dim 64
  * or 128, Hq / Hkv <= 128, total < 2^31 - 256. Sequences of no rows are fine. One with offsets
  * out of [0, total], or decreasing ones, sets W12_ERR_ARG and is taken as empty (sequences
- * that share rows write either's result). Rows that a row does not see have no part in it, whatever they hold. Scores, softmax and sums are fp32; a weight
- * meets the values rounded to their type (bf16: 2^-8 of itself, fp16: 2^-11 of itself
- * or 2^-25 of the row's largest). A score of -inf weighs nothing; a row with no other
+ * that share rows write either's result). Rows that a row does not see have no part in it,
+ * whatever they hold. Scores, softmax and sums are fp32; a weight meets the values rounded to
+ * their type (bf16: 2^-8 of itself, fp16: 2^-11 of itself or 2^-25 of the row's largest). A score of -inf weighs nothing; a row with no other
  * is zeros. No workspace. Device-side errors besides: W12_ERR_TIMEOUT. Returns
  * W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED or W12_ERR_CUDA. */
 int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_stride, const void* K, int64_t k_token_stride,
@@ -561,7 +562,7 @@ typedef struct w12_adapters {
  * and y_stride (of 4) elements apart, 16-byte aligned. ids int32 [M]: -1 is no
  * adapter, and the row of Y is not touched; another id outside [0, n) is taken so and
  * sets W12_ERR_ARG in dev_status. Products of bf16 values are summed in fp32, A X is
- * kept to 2^-24 of itself. The workspace needs no zero fill, holds nothing between
+ * kept to 2^-24 of itself. B is finite (an infinity may come out as NaN). The workspace needs no zero fill, holds nothing between
  * calls, and follows the other rules at the top. Errors: W12_ERR_ARG,
  * W12_ERR_SHAPE, W12_ERR_WORKSPACE, W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
 size_t w12_lora_ws_bytes(int64_t M, int n_adapters, int rank);

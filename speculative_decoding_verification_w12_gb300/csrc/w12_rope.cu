@@ -97,15 +97,15 @@ __device__ __forceinline__ float rsqrt_of(Sum2 m) {
 }
 
 // The factor of a row's norm; kNearest: the fp32 value next to the exact one. A row whose squares
-// leave the fp32 range (values near 2^60) is made 2^70 smaller first: x then has what the factor
-// is for.
+// leave the fp32 range (values past 2^51) is made 2^76 smaller first: x then has what the factor
+// is for, and the squares' sum is at most 2^111, below the 2^121 where c has no exponent left.
 template <int kD, bool kNearest>
 __device__ __forceinline__ float norm_factor(float (&x)[16], float eps) {
   constexpr int kRow = kD / 16;
   float rough = sum_squares<kRow>(x);
   const bool huge = !(rough < 1e35f);
   if (__any_sync(0xFFFFFFFFu, huge)) {
-    const float scale = huge ? 0x1p-70f : 1.f;
+    const float scale = huge ? 0x1p-76f : 1.f;
     if (huge) eps = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], scale);
@@ -523,9 +523,8 @@ int w12_kv4_append_rope(const w12_kv4* cache, const w12_rope* rope, const void* 
 int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const int32_t* q_len, int B, int T, int32_t* positions,
                        int32_t* dev_status, void* stream) {
   if (!prefix_len || !positions) return W12_ERR_ARG;
-  if (B < 1 || T < 1 || (parents && T > kTreeMax) || B > 65535) return W12_ERR_SHAPE;
+  if (B < 1 || T < 1 || (parents && T > kTreeMax) || B > 65535 || T > (1 << 23)) return W12_ERR_SHAPE;
   PositionParams p{prefix_len, parents, q_len, positions, dev_status, T, (T + kTreeThreads - 1) / kTreeThreads};
-  if (int64_t(B) * p.blocks > 0x7FFFFFFF) return W12_ERR_SHAPE;
   if (!device_supported()) return W12_ERR_UNSUPPORTED;
   static_assert(kTreeMax == kTreeThreads, "one block a tree");
   cudaLaunchAttribute attr[1];

@@ -189,8 +189,8 @@ class PagedVerifyStep:
         self.rope, self.adapters = rope, dict(adapters or {})
         for name, lora in self.adapters.items():
             w = {"qkv": qkv, "out": out, "head": head}.get(name)
-            if w is None or (lora.K, lora.N) != (w.K, w.N):
-                raise ValueError("adapters must be of qkv, out or head, and of their sizes")
+            if w is None or (lora.K, lora.N) != (w.K, w.N) or lora.max_rows < B * T:
+                raise ValueError("adapters must be of qkv, out or head, of their sizes, and for B * T rows")
         self.B, self.T, self.M, self.Hq, self.Hkv, self.head_dim = B, T, B * T, Hq, Hkv, head_dim
         self.max_len = max_len
         self.qkv, self.out, self.head, self.top_k = qkv, out, head, top_k
@@ -232,9 +232,14 @@ class PagedVerifyStep:
         normed and rotated where the step does that, keys and values are cached, and the
         causal attention over them, before they are quantised, comes back as bf16 [n, Hq,
         head_dim]. A prompt that there are no pages for, or that is too long, is attended
-        over but not cached: its request stays as it was, and the status word says so.
+        over but not cached: its request stays as it was, and the status word says so. (Rows
+        past max_len have no position: with a rotation their queries and keys are zeros.)
         """
         n, st = K.shape[0], self.status
+        w12._want(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,))
+        if not Q.dtype == K.dtype == V.dtype or Q.shape != (n, self.Hq, self.head_dim) or \
+                not K.shape == V.shape == (n, self.Hkv, self.head_dim):
+            raise ValueError("Q, K and V must be rows of the same tokens and type, of the step's heads")
         T = max(1, min(n, self.max_len) if longest is None else min(longest, self.max_len))
         length = cu_seqlens[1:] - cu_seqlens[:-1]
         keep = length <= 0
@@ -272,11 +277,13 @@ class PagedVerifyStep:
         B, T, M, d = self.B, self.T, self.M, self.head_dim
         st = self.status
         # (A negative count is refused: the request keeps its pages and gets slots of -1.)
+        if adapter is not None and not self.adapters:
+            raise ValueError("the step has no adapters")
         nodes = torch.where(self.length <= self.max_len - T, self.nodes, -1)
         slots = self.pages.reserve(self.length, nodes, T, status=st)
         served = slots[:, 0] >= 0
         q_len = torch.where(served, nodes, 0)
-        ids = None if adapter is None or not self.adapters else adapter[:, None].expand(B, T).reshape(M)
+        ids = None if adapter is None else adapter[:, None].expand(B, T).reshape(M)
 
         def product(name, x, w, ws):
             y = w12.gemm(x, w, ws=ws, status=st)

@@ -832,6 +832,14 @@ def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 
 # Between the products of a layer: rotation, prompt attention, adapters
 # ---------------------------------------------------------------------------
 
+def _here(x: torch.Tensor, what: str) -> torch.Tensor:
+    """x, checked: on the device that the call will launch on."""
+    dev = x.get_device()
+    if dev >= 0 and _device_index is not None and dev != _device_index():
+        raise ValueError(f"{what} must be on the current device")
+    return x
+
+
 def _head_rows(x: torch.Tensor, what: str, dtypes=_DTYPES):
     """Address, strides of tokens and heads, heads, and (n, H, head_dim) of rows."""
     if x.dtype not in dtypes:
@@ -839,6 +847,7 @@ def _head_rows(x: torch.Tensor, what: str, dtypes=_DTYPES):
     shape, st = x.shape, x.stride()
     if len(shape) != 3 or not x.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor [n, heads, head_dim]")
+    _here(x, what)
     n, H, d = shape
     if st[2] != 1 and n and H:
         raise ValueError(f"{what} must have a contiguous last dimension")
@@ -919,7 +928,7 @@ def tree_positions(prefix_len: torch.Tensor, parents: torch.Tensor | None = None
     draft tree parents int32 [B, T], or + t without a tree (T must then be given); -1
     from q_len[b] on."""
     B = prefix_len.shape[0]
-    _want(prefix_len, "prefix_len", torch.int32, (B,))
+    _here(_want(prefix_len, "prefix_len", torch.int32, (B,)), "prefix_len")
     if parents is not None:
         T = parents.shape[-1] if T is None else T
         _want(parents, "parents", torch.int32, (B, T))
@@ -964,7 +973,8 @@ def prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_seqle
 
 class LoRA:
     """Low-rank adapters of one projection K -> N (w12_lora): A bf16 [n, rank, K], B bf16
-    [n, N, rank], scale fp32 [n]; the workspace serves up to max_rows rows a call."""
+    [n, N, rank], scale fp32 [n]; the workspace serves up to max_rows rows a call, one
+    call (or replay of a graph that holds one) at a time."""
 
     def __init__(self, A: torch.Tensor, B: torch.Tensor, scale: torch.Tensor, max_rows: int = 256):
         if A.dim() != 3 or B.dim() != 3:
@@ -990,6 +1000,7 @@ class LoRA:
         M = X.shape[0]
         if X.shape != (M, self.K) or X.dtype is not torch.bfloat16 or not X.is_cuda or X.stride(1) != 1:
             raise ValueError(f"X must be a bfloat16 CUDA tensor [M, {self.K}] with a contiguous last dimension")
+        _here(X, "X")
         if Y.shape != (M, self.N) or Y.dtype is not torch.float32 or not Y.is_cuda or Y.stride(1) != 1:
             raise ValueError(f"Y must be a float32 CUDA tensor [{M}, {self.N}] with a contiguous last dimension")
         if M > self.max_rows:

@@ -185,3 +185,28 @@ def test_parts_that_do_not_fit_are_refused():
                 dict(adapters={"qkv": _adapters(128, 256, 1)})):
         with pytest.raises(ValueError):
             PagedVerifyStep(*args, n_pages=4, max_len=64, **bad)
+
+
+def test_prompts_and_adapters_that_the_step_refuses():
+    step = _step(adapters=False)[0]
+    Q, K, V = (torch.randn((30, h, D), device="cuda") for h in (HQ, HKV, HKV))
+    cu = to_dev_i32([0, 30, 30, 30])
+    for bad in ((Q, K, V, cu.long()), (Q, K, V, cu[:3]), (Q[:29], K, V, cu), (Q, K, V[:29], cu), (K, K, V, cu), (Q, K, V.bfloat16(), cu)):
+        with pytest.raises(ValueError):
+            step.prompt(*bad)
+    assert step.length.tolist() == [0, 0, 0] and status_value(step.status) == 0
+    X, tree = torch.zeros((B * T, HIDDEN), dtype=torch.bfloat16, device="cuda"), to_dev_i32(np.tile(np.arange(-1, T - 1), (B, 1)))
+    with pytest.raises(ValueError):
+        step.run(X, tree, torch.zeros_like(tree), adapter=to_dev_i32([0, 0, 0]))
+    W = [w12.pack(to_dev_bf16(S.weights_bf16(*s, seed=1))) for s in ((512, 128), (128, 256), (1024, 128))]
+    few = w12.LoRA(*(torch.zeros(s, dtype=torch.bfloat16, device="cuda") for s in ((1, 8, 128), (1, 512, 8))), torch.ones(1, device="cuda"), max_rows=7)
+    with pytest.raises(ValueError):
+        PagedVerifyStep(*W, 2, 4, 4, 2, 64, n_pages=4, max_len=64, adapters={"qkv": few})
+
+
+def test_no_prompts_at_all():
+    step = _step()[0]
+    none = [torch.empty((0, h, D), device="cuda") for h in (HQ, HKV, HKV)]
+    assert step.prompt(*none, to_dev_i32([0, 0, 0, 0])).shape == (0, HQ, D)
+    torch.cuda.synchronize()
+    assert step.length.tolist() == [0, 0, 0] and status_value(step.status) == 0 and not step.pages.used.any()

@@ -234,3 +234,44 @@ def test_an_expired_wait_is_reported_and_the_next_call_is_whole():
         w12.set_wait_limit_us(2000000)
     assert status_value(st) in (0, 6)
     assert torch.equal(w12.prompt_attention(q, k, v, to_dev_i32(cu)), want)
+
+
+def test_rows_past_32_bits():
+    """Rows 2^23 values apart, 600 of them (an infinity among the values); more than 2^31 outputs."""
+    n, apart = 600, 2 ** 23
+    base = torch.empty(n * apart, dtype=BF16, device="cuda")
+    q, k, v = (base.as_strided((n, h, 128), (apart, 128, 1), at) for h, at in ((4, 0), (2, 512), (2, 768)))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for x in (q, k, v):
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+    v[599, 1, 7] = float("inf")
+    cu, st = to_dev_i32([0, 90, n]), new_status()
+    got = w12.prompt_attention(q, k, v, cu, status=st)
+    want = w12.prompt_attention(q.contiguous(), k.contiguous(), v.contiguous(), cu)
+    assert torch.equal(got, want) and torch.isinf(got[599, 2:, 7]).all() and torch.isfinite(got[:599]).all()
+    del base, q, k, v
+    L, B, H = 300, 900, 64
+    q, k, v = (torch.randn((L * B, h, 128), generator=g, device="cuda", dtype=BF16) for h in (H, 8, 8))
+    assert q.numel() > 2 ** 31
+    out = w12.prompt_attention(q, k, v, to_dev_i32(np.arange(B + 1) * L), status=st)
+    for b in (0, B // 2, B - 1):
+        one = slice(b * L, b * L + L)
+        assert torch.equal(out[one], w12.prompt_attention(q[one], k[one], v[one], to_dev_i32([0, L])))
+    assert status_value(st) == 0
+
+
+def test_calls_at_the_same_time():
+    """Two streams at once, each with calls of its own sizes: what each gives alone."""
+    cases = []
+    for lens, Hq, Hkv, d, dtype in (([700, 33], 8, 2, 128, BF16), ([130, 1, 500], 4, 4, 64, F16)):
+        q, k, v = _rows(sum(lens), Hq, Hkv, d, dtype, len(lens))
+        cases.append((q, k, v, to_dev_i32(_offsets(lens))))
+    alone = [w12.prompt_attention(*c) for c in cases]
+    streams, got, st = [torch.cuda.Stream() for _ in cases], [[] for _ in cases], new_status()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, s, g in zip(cases, streams, got):
+            g.append(w12.prompt_attention(*c, status=st, stream=s))
+    torch.cuda.synchronize()
+    assert status_value(st) == 0
+    assert all(torch.equal(x, want) for g, want in zip(got, alone) for x in g)

@@ -315,3 +315,43 @@ def test_captured_and_replayed_on_another_stream():
     q, _ = rope.run(Q, K, to_dev_i32(pos), stream=side)
     side.synchronize()
     assert torch.equal(q, out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_factor_of_the_largest_rows(d):
+    """Values of [2^127, 2^128): the row times 2^-76 (exact), and the fp32 value next to its factor.
+    (One row of these may be a tie of two, as above.)"""
+    rope, tab, qw, kw = _make(d, d, False, True, 4)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    K = (torch.rand((200, 3, d), generator=g, device="cuda") * 0.99 + 1.0) * 2.0 ** 127
+    K = torch.where(torch.rand(K.shape, generator=g, device="cuda") < 0.5, -K, K)
+    assert torch.isfinite(K).all()
+    k = rope.run(None, K, to_dev_i32(np.zeros(200)), dtype=F32)[1].cpu().numpy()   # (a turn by nothing)
+    x = K.cpu().numpy() * np.float32(2.0 ** -76)
+    f = (1 / np.sqrt(np.square(x.astype(np.float64)).mean(-1, keepdims=True))).astype(np.float32)
+    want = (x * f) * kw
+    assert (k != want).any(-1).sum() <= 1
+    assert np.abs(k - want).max() <= 2.0 ** -22 * np.abs(want).max()
+
+
+def test_rows_and_slots_past_32_bits():
+    """Rows 2^23 values apart, 600 of them, and a pool of more than 2^32 bytes."""
+    n, apart = 600, 2 ** 23
+    rope = _make(128, 128, False, True, n)[0]
+    base = torch.empty(n * apart, dtype=BF16, device="cuda")
+    Q, K, V = (base.as_strided((n, h, 128), (apart, 128, 1), at) for h, at in ((3, 0), (2, 384), (2, 640)))
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for x in (Q, K, V):
+        x.copy_(torch.randn(x.shape, generator=g, device="cuda"))
+    pos, st = to_dev_i32(np.arange(n)), new_status()
+    for got, want in zip(rope.run(Q, K, pos, status=st), rope.run(Q.contiguous(), K.contiguous(), pos)):
+        assert torch.equal(got, want)
+    P, pages = 64, 260_000
+    big, small = _pool(pages, 2, 128, P), _pool(n // P + 1, 2, 128, P)
+    assert big.pool.numel() > 2 ** 32
+    slots = to_dev_i32(np.arange(n) + (pages - n // P - 1) * P)
+    q = big.append_rope(K, V, slots, rope, pos, Q=Q, status=st)
+    assert torch.equal(q, small.append_rope(K.contiguous(), V.contiguous(), pos, rope, pos, Q=Q.contiguous()))
+    for got, want in zip(big.read(slots), small.read(pos)):
+        assert torch.equal(got, want)
+    assert status_value(st) == 0

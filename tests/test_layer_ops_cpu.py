@@ -11,7 +11,7 @@ import torch
 from speculative_decoding_verification_w12_gb300 import build as B
 from speculative_decoding_verification_w12_gb300 import w12
 from test_refusals_cpu import calls, i32  # noqa: F401
-from test_streams_cpu import Stream, cuda, record  # noqa: F401
+from test_streams_cpu import Cuda, Stream, cuda, record  # noqa: F401
 
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 
@@ -217,3 +217,35 @@ def test_prompt_kernel_waits_for_its_copies_and_shares_its_registers():
     assert int(regs["kLaunchRegs"]) * threads <= 65536 and all(int(v) % 8 == 0 for v in regs.values())
     calls_ = re.findall(r"(?:fewer|more)_registers<(\w+)>\(\)", kernel)
     assert sorted(calls_) == ["kRestRegs", "kSoftRegs"]                   # one instruction a warpgroup
+
+
+class Elsewhere(Cuda):
+    """Passes for a tensor of device 1."""
+    def get_device(self):
+        return 1
+
+
+def test_tensors_of_another_device_are_refused(calls, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    monkeypatch.setattr(w12, "_device_index", lambda: 0)
+    other = lambda *s, dtype=F32: cuda(*s, dtype=dtype).as_subclass(Elsewhere)  # noqa: E731
+    r, c, lora = _rope(), _cache(), _lora()
+    n = len(calls)
+    for call in (lambda f: r.run(f(5, 3, 64), cuda(5, 2, 64), i32(5)), lambda f: r.run(cuda(5, 3, 64), f(5, 2, 64), i32(5)),
+                 lambda f: c.append_rope(f(5, 2, 64), cuda(5, 2, 64), i32(5), r, i32(5)),
+                 lambda f: w12.tree_positions(f(3, dtype=torch.int32), T=4),
+                 lambda f: w12.prompt_attention(f(6, 4, 64, dtype=BF16), cuda(6, 2, 64, dtype=BF16), cuda(6, 2, 64, dtype=BF16), i32(2)),
+                 lambda f: lora.run(f(5, 64, dtype=BF16), cuda(5, 32), i32(5))):
+        with refused(ValueError):
+            call(other)
+        assert len(calls) == n
+        call(cuda)
+        n += 1
+        assert len(calls) == n
+    monkeypatch.setattr(w12, "_device_index", lambda: 1)
+    r.run(other(5, 3, 64), None, i32(5))                                  # the current one
+
+
+def test_c_longest_chunk(L, at):
+    f = L.w12_tree_positions
+    assert f(at, None, None, 1, 2 ** 23 + 1, at, None, None) == 2 and f(at, None, None, 1, 2 ** 31 - 1, at, None, None) == 2
