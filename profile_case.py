@@ -15,6 +15,9 @@ gate_up -> SwiGLU -> down inside the launch).
 (--P + --T) rows into it and read them back, kv4_commit moves 7 accepted rows a
 request, pages reserves the pages of --B prompts of --P tokens. --op logprobs
 takes --M rows of logits over 151,936 tokens (top --k; --f32: fp32, else bf16).
+--op prompt attends over --B prompts of --P tokens (--Hq q heads, 8 kv heads x --d; --f32:
+fp16, else bf16), rope norms and rotates their heads, append_rope theirs into the cache,
+lora adds rank --k adapters of --B requests of --T rows to the product --shape.
 Prints the mean CUDA-event time per launch.
 """
 import argparse
@@ -45,7 +48,7 @@ def check_status(st):
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--op", default="w12", choices=["w12", "bf16", "head", "attn", "step", "layer", "kv4", "kv4_append", "kv4_read",
-                                                        "kv4_commit", "pages", "logprobs"])
+                                                        "kv4_commit", "pages", "logprobs", "prompt", "rope", "append_rope", "lora"])
     ap.add_argument("--swiglu", action="store_true")
     ap.add_argument("--B", type=int, default=4)
     ap.add_argument("--T", type=int, default=64)
@@ -69,6 +72,8 @@ def main():
         return attn(a, dev)
     if a.op in ("kv4", "kv4_append", "kv4_read", "kv4_commit", "pages", "logprobs"):
         return serve(a, dev)
+    if a.op in ("prompt", "rope", "append_rope", "lora"):
+        return between(a, dev)
     if a.op == "step":
         return step(a, dev, d)
     if a.op == "layer":
@@ -198,6 +203,10 @@ def serve(a, dev):
             att = w12.KV4Attention(a.B, a.T, Hq, Hkv, d, page, L, dev)
             what = f"kv4 attention {a.B} x {a.T} over {a.P}"
             fn = lambda: att.run(Q, cache, pages.table, prefix, parents=par, status=st)  # noqa: E731
+    timed(a, what, fn, st)
+
+
+def timed(a, what, fn, st):
     fn()
     torch.cuda.synchronize()
     e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
@@ -208,6 +217,34 @@ def serve(a, dev):
     torch.cuda.synchronize()
     check_status(st)
     print(f"{what}: {e0.elapsed_time(e1) / a.iters * 1e3:.1f} us/launch")
+
+
+def between(a, dev):
+    """What a layer does between its products: prompt attention, rotation, adapters."""
+    torch.manual_seed(0)
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    if a.op == "lora":
+        (N, K), M = SHAPES[a.shape], a.B * a.T
+        A, Bm = (torch.randn(s, device=dev, dtype=torch.bfloat16) for s in ((a.B, a.k, K), (a.B, N, a.k)))
+        lora = w12.LoRA(A, Bm, torch.ones(a.B, device=dev))
+        X, Y = torch.randn((M, K), device=dev, dtype=torch.bfloat16), torch.zeros((M, N), device=dev)
+        ids = torch.arange(a.B, dtype=torch.int32, device=dev).repeat_interleave(a.T)
+        return timed(a, f"{a.B} x {a.T} rows, rank {a.k}, {K} -> {N}", lambda: lora.run(X, Y, ids, status=st), st)
+    n, Hq, Hkv, d, page = a.B * a.P, a.Hq, 8, a.d, 64
+    Q, K, V = (torch.randn((n, h, d), device=dev).to(torch.float16 if a.f32 else torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    out = torch.empty_like(Q)
+    if a.op == "prompt":
+        cu = torch.arange(0, n + 1, a.P, dtype=torch.int32, device=dev)
+        return timed(a, f"prompts {a.B} x {a.P}, {Hq}/{Hkv} x {d}", lambda: w12.prompt_attention(Q, K, V, cu, out=out, status=st), st)
+    ones = torch.ones(d, device=dev)
+    rope = w12.Rope.create(d, a.P, q_norm=ones, k_norm=ones, device=dev)
+    pos = torch.arange(a.P, dtype=torch.int32, device=dev).repeat(a.B)
+    if a.op == "rope":
+        k_out = torch.empty_like(K)
+        return timed(a, f"rotation of {n} rows", lambda: rope.run(Q, K, pos, out=(out, k_out), dtype=Q.dtype, status=st), st)
+    cache = w12.KV4Cache.create(-(-n // page), Hkv, d, page, dev)
+    slots = torch.arange(n, dtype=torch.int32, device=dev)
+    timed(a, f"rotated append of {n} rows", lambda: cache.append_rope(K, V, slots, rope, pos, status=st), st)
 
 
 def attn(a, dev):

@@ -5,9 +5,9 @@
 // Rows of a tile are (token, head of the group), token-major, 128 / G tokens: a key block is
 // read once for the whole group, and few of a tile's keys are cut by the diagonal. An item is
 // two such tiles, one behind the other, of one (sequence, kv head), with all keys that they
-// see in blocks. The kernel is persistent; items go out longest first, in rounds of the grid
-// that alternate in direction, so every block gets about the same work and nothing is counted
-// in memory. Per key block and tile:
+// see in blocks. The kernel is persistent; the items of some sequences go out longest first
+// (Walk), in rounds of the grid that alternate in direction, so every block gets about the same
+// work and nothing is counted in memory. Per key block and tile:
 //   S = Q K^T         tcgen05.mma, both from shared memory, S in TMEM;
 //   P = 2^(c S - m)   a warpgroup for each tile, a row a thread: the running maximum moves only
 //                     when a block's passes it by 2^8, so O is rescaled rarely;
@@ -44,6 +44,11 @@ using namespace attn_impl;
 
 constexpr int kThreads = 512;
 constexpr float kRescale = 8.0f;   // log2 growth of the maximum that triggers a rescale
+// Keys and values of a group of sequences whose items are under way together: a third of the L2
+// cache, which Q and O pass through too. All sequences at once read them again for every place:
+// 64 prompts of up to 1000 (40 / 8 heads of 128) took 324 us instead of 284, 8 of 8192 3350
+// instead of 3150 (16 to 64 MB: alike).
+constexpr int kGroupBytes = 43 << 20;
 constexpr int kItems = 4;          // items handed out ahead
 constexpr int kItemReaders = 15;   // warps that read an item
 constexpr int kMostCut = 5;        // blocks that the diagonal cuts in an item: 256 tokens of blocks of 80 or more
@@ -102,6 +107,7 @@ struct Params {
   int32_t* status;
   int64_t total;
   int B, Hq, Hkv, G, tpt;      // tpt: tokens a tile
+  int room;                    // tokens of a group of sequences
   float c;                     // scale log2(e)
   uint64_t limit_ns;
 };
@@ -126,18 +132,24 @@ __device__ __forceinline__ int first_cut(int t0) {
   return (t0 + 1) / kKeys;
 }
 
-// Walks the items in their order, longest first: by place in the sequence (in pairs of
-// tiles) from the last down, then sequence, then kv head. Warp-collective.
+// Walks the items in their order: groups of sequences, whose keys and values stay in the L2 cache
+// while their items are under way; in a group by place in the sequence (in pairs of tiles), then
+// sequence, then kv head. Groups run alternately up and down the places, the last one down, so that
+// neighbours in the order are alike in size and the smallest come last. Warp-collective.
 struct Walk {
   const int32_t* cu;
-  int B, Hkv, step;
+  int B, Hkv, step, room;   // room: tokens of a group
   int64_t total;
-  int level;        // pairs before the current ones in their sequences; -1: past the last
-  int chunk;        // of 32 sequences
-  uint32_t left;    // sequences of the chunk that are still to come at this level
+  int chunk;        // of 32 sequences; past the last one: no more items
+  uint32_t firsts;  // sequences of the chunk that a group begins with, those to come
+  bool member;      // this lane's sequence is of the current group
+  bool down;
+  int level, top;   // pairs before the current ones in their sequences, and the most of the group
+  uint32_t left;    // sequences of the group that are still to come at this level
   int head;         // next kv head of the first of them
-  int n, start, len;  // of this lane's sequence of the chunk: pairs, first token, tokens
+  int n, start, len, group;  // of this lane's sequence of the chunk: pairs, first token, tokens, group
 
+  __device__ __forceinline__ int chunks() const { return (B + 31) / 32; }
   __device__ __forceinline__ void load(int32_t* status) {
     const int lane = threadIdx.x & 31, b = chunk * 32 + lane;
     start = len = 0;
@@ -151,24 +163,60 @@ struct Walk {
       }
     }
     n = (len + step - 1) / step;
+    // A group for every `room` tokens, by where a sequence begins among the chunk's.
+    const int mine = min(len, room);
+    const uint32_t some = __ballot_sync(0xFFFFFFFFu, n > 0);
+    group = n > 0 ? 0 : -1;
+    firsts = some & (0u - some);
+    if (int(__reduce_add_sync(0xFFFFFFFFu, unsigned(mine))) > room) {
+      int before = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, before, o);
+        if (lane >= o) before += v;
+      }
+      if (n > 0) group = (before - mine) / room;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, group);
+      firsts = __ballot_sync(0xFFFFFFFFu, n > 0 && !(same & ((1u << lane) - 1u)));
+    }
   }
   __device__ __forceinline__ void begin(int32_t* status) {
-    level = -1;
-    const int chunks = (B + 31) / 32;
-    for (chunk = chunks - 1; chunk >= 0; --chunk) {
+    int groups = 0;
+    for (chunk = chunks() - 1; chunk >= 0; --chunk) {
       load(status);
-      level = max(level, int(__reduce_max_sync(0xFFFFFFFFu, unsigned(n))) - 1);
+      groups += __popc(firsts);
     }
     chunk = 0;
-    if (chunks > 1) load(nullptr);
-    left = __ballot_sync(0xFFFFFFFFu, n > level);
+    if (chunks() > 1) load(nullptr);
+    down = !(groups & 1);
+    member = false;
+    level = top = -1;
+    left = 0;
     head = 0;
+  }
+  // To the next level that has items; false: there is none.
+  __device__ __forceinline__ bool advance() {
+    head = 0;
+    level += down ? -1 : 1;
+    if (level < 0 || level > top) {
+      while (!firsts) {
+        if (++chunk >= chunks()) return false;
+        load(nullptr);
+      }
+      const int first = __ffs(firsts) - 1;
+      firsts &= firsts - 1;
+      down = !down;
+      member = group == __shfl_sync(0xFFFFFFFFu, group, first);
+      top = int(__reduce_max_sync(0xFFFFFFFFu, member ? unsigned(n) : 0u)) - 1;
+      level = down ? top : 0;
+    }
+    left = __ballot_sync(0xFFFFFFFFu, member && n > level);
+    return true;
   }
   // The item `skip` places on.
   __device__ __forceinline__ Item next(int skip) {
-    const int chunks = (B + 31) / 32;
     Item it{0, 0, 0, -1};
-    while (level >= 0) {
+    while (chunk < chunks()) {
       const int here = __popc(left) * Hkv - head;
       if (skip < here) {
         const int at = head + skip;
@@ -182,13 +230,7 @@ struct Walk {
         return it;
       }
       skip -= here;
-      head = 0;
-      if (++chunk == chunks) {
-        chunk = 0;
-        --level;
-      }
-      if (chunks > 1) load(nullptr);
-      left = __ballot_sync(0xFFFFFFFFu, n > level);
+      if (!advance()) break;
     }
     return it;
   }
@@ -569,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 15) {
     // ---------------------------------------------------------------- items
-    Walk walk{P.cu, P.B, P.Hkv, 2 * P.tpt, P.total};
+    Walk walk{P.cu, P.B, P.Hkv, 2 * P.tpt, P.room, P.total};
     walk.begin(blockIdx.x == 0 ? P.status : nullptr);
     const int grid = int(gridDim.x), me = int(blockIdx.x);
     int skip = me;
@@ -837,6 +879,7 @@ int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_s
   P.Hkv = Hkv;
   P.G = Hq / Hkv;
   P.tpt = 128 / P.G;
+  P.room = kGroupBytes / (4 * Hkv * head_dim) + 1;
   P.c = float(double(scale) * 1.4426950408889634);
   P.limit_ns = wait_limit_ns();
   const bool bf16 = dtype == W12_BF16;

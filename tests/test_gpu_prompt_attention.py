@@ -275,3 +275,22 @@ def test_calls_at_the_same_time():
     torch.cuda.synchronize()
     assert status_value(st) == 0
     assert all(torch.equal(x, want) for g, want in zip(got, alone) for x in g)
+
+
+@pytest.mark.parametrize("lens", ["ragged", "long and short"])
+def test_groups_of_sequences(lens):
+    """More keys and values than one group of sequences has, over several of the walk's chunks: each
+    sequence bitwise as it comes by itself."""
+    rng = np.random.default_rng(5)
+    lens = [int(v) for v in (rng.integers(0, 500, 70) if lens == "ragged" else rng.permutation([2200, 1900, 1500] + [3] * 60 + [0] * 5))]
+    H, d = 64, 128
+    cu, total = _offsets(lens), sum(lens)
+    assert 4 * total * H * d > 4 * 43 * 2 ** 20
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn((total, H, d), generator=g, device="cuda", dtype=BF16) for _ in range(3))
+    st = new_status()
+    out = w12.prompt_attention(q, k, v, to_dev_i32(cu), out=torch.full_like(q, float("nan")), status=st)
+    assert status_value(st) == 0
+    for a, e in zip(cu[:-1], cu[1:]):
+        if e > a:
+            assert torch.equal(out[a:e], w12.prompt_attention(q[a:e], k[a:e], v[a:e], to_dev_i32([0, e - a]))), (a, e)
