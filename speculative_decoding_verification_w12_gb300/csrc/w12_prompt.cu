@@ -108,6 +108,7 @@ struct Params {
   int64_t total;
   int B, Hq, Hkv, G, tpt;      // tpt: tokens a tile
   int room;                    // tokens of a group of sequences
+  uint32_t inv_g;              // a row's token is row inv_g / 2^16
   float c;                     // scale log2(e)
   uint64_t limit_ns;
 };
@@ -276,6 +277,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::W12_R8(v, 0), "r"(taddr) : "memory");
+}
+
+// 16 rows of 32 columns: a lane gets column 4 k + lane % 4 of row lane / 4 as v[k], of row lane / 4 + 8
+// as v[8 + k].
+__device__ __forceinline__ void tmem_ld_quads(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x128b.x8.b32 {%0, %8, %1, %9, %2, %10, %3, %11, %4, %12, %5, %13, %6, %14, %7, %15}, [%16];"
+      : W12_W8(v, 0), W12_W8(v, 8)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(v[k]));  // (no use of a value moves before the wait)
 }
 
 // 32 bytes of memory of this thread's: a whole sector.
@@ -761,10 +777,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_all(&o_done[i], uint32_t(blocks + n - 1) & 1u)) break;
         tc_fence_after();
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
-        uint16_t* out = static_cast<uint16_t*>(P.O) + (int64_t(it.first - it.t0 + t) * P.Hq + it.head * P.G + row_h) * kD;
+        // Of its own row a lane would store 32 bytes at a time, a line each; the lines are what the
+        // stores take. So half rows change lanes on the way, through P's columns: four lanes have a
+        // line of a row then, an instruction eight lines (2,400 -> VEPI cycles for both tiles).
+        uint16_t* tile = static_cast<uint16_t*>(P.O) + (int64_t(it.first - it.t0 + t0) * P.Hq + it.head * P.G) * kD;
+        const int end = min(P.tpt, it.len - t0);      // tokens
 #pragma unroll
         for (int ch = 0; ch < kD / 64; ++ch) {
-          uint32_t o[64];
+          uint32_t o[64], w[32];
           tmem_ld32(o_at + uint32_t(64 * ch), &o[0]);
           tmem_ld32(o_at + uint32_t(64 * ch + 32), &o[32]);
           tmem_ld_wait64(o);
@@ -773,15 +793,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_free[i]);
           }
+          // Column 4 k + q has word 8 q + k: lane q of four gets eight neighbours.
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            o[x] = pack2<kBf16>(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
-          if (valid) {
+          for (int x = 0; x < 32; ++x) {
+            const int y = 8 * (x & 3) + (x >> 2);
+            w[x] = pack2<kBf16>(__uint_as_float(o[2 * y]) * inv, __uint_as_float(o[2 * y + 1]) * inv);
+          }
+          tmem_st32(p_at, w);
+          tmem_st_wait();
+          tmem_ld_quads(p_at, &w[0]);
+          tmem_ld_quads(p_at + (16u << 16), &w[16]);
+          tmem_ld_wait32(w);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) st_global32(out + 64 * ch + 16 * x, &o[8 * x]);
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t row = (warp & 3) * 32 + 8 * x + (lane >> 2), tok = (row * P.inv_g) >> 16;
+            if (int(tok) < end)
+              st_global32(tile + int64_t(tok * P.Hq + row - tok * P.G) * kD + 64 * ch + 16 * (lane & 3), &w[8 * x]);
           }
         }
-        if (odd && valid) add_taken_out<C::kKeys, kD, kBf16>(P, out, odd, cut, t, it.first - it.t0, it.head);
+        if (__any_sync(0xFFFFFFFFu, odd && valid)) {
+          __syncwarp();
+          uint16_t* out = tile + int64_t(row_t * P.Hq + row_h) * kD;
+          if (odd && valid) add_taken_out<C::kKeys, kD, kBf16>(P, out, odd, cut, t, it.first - it.t0, it.head);
+        }
       }
       base += 2 * max(n0, n1);
       blocks += n;
@@ -879,6 +913,7 @@ int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_s
   P.Hkv = Hkv;
   P.G = Hq / Hkv;
   P.tpt = 128 / P.G;
+  P.inv_g = 65536u / P.G + 1;  // (exact for 128 rows)
   P.room = kGroupBytes / (4 * Hkv * head_dim) + 1;
   P.c = float(double(scale) * 1.4426950408889634);
   P.limit_ns = wait_limit_ns();
