@@ -26,7 +26,7 @@
 // note their keys, and rows that see one add it at the end.
 //
 // Warps: 0-3 and 4-7 softmax and epilogue of the two tiles; 8 and 9 issue S, 10 and 11 P V of the
-// two tiles; 12 copies (and hands out the items); 13 and 14 look through V. Each of the four
+// two tiles; 12 copies; 13 and 14 look through V; 15 finds the items. Each of the four
 // series of products has a warp on a scheduler of its own: what a thread waits for comes back
 // behind the products it has issued before (285 idle cycles a wait where one thread issues all,
 // measured), so only other warps' products fill that time. The issuing warps run whole and elect
@@ -51,6 +51,8 @@ constexpr float kRescale = 8.0f;   // log2 growth of the maximum that triggers a
 constexpr int kGroupBytes = 43 << 20;
 constexpr int kItems = 4;          // items handed out ahead
 constexpr int kItemReaders = 15;   // warps that read an item
+constexpr int kBadItems = 8;       // items whose cut blocks are noted (no warp is more than kItems ahead of another)
+static_assert(kBadItems > kItems, "notes");
 constexpr int kMostCut = 5;        // blocks that the diagonal cuts in an item: 256 tokens of blocks of 80 or more
 
 // Registers: a warpgroup changes its share by one instruction that all its warps meet.
@@ -84,7 +86,7 @@ struct Cfg {
   static constexpr int kStages = kD == 128 ? 8 : 10;           // K and V blocks in turn
   static constexpr uint32_t kRing = 2 * kQTile;                // behind the two tiles' Q
   static constexpr uint32_t kBar = kRing + kStages * kTile;
-  static constexpr uint32_t kSmem = kBar + 1024 + 1024;        // barriers, items; alignment
+  static constexpr uint32_t kSmem = kBar + 1280 + 1024;        // barriers, items; alignment
   // TMEM columns of the first tile, and how far on the second's are.
   static constexpr uint32_t kColS = 0, kNextS = 128;
   static constexpr uint32_t kColP = kD == 128 ? kKeys : 256, kNextP = kD == 128 ? 128 : 64;
@@ -422,8 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // (An offset, not a rounded pointer: the compiler then still knows that it is shared memory.)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint4* bad = reinterpret_cast<uint4*>(smem + C::kBar);  // [kStages]: keys of a V block with values taken out
-  uint64_t* full = reinterpret_cast<uint64_t*>(bad + kStages);  // [kStages]: block landed
+  // [kBadItems][kMostCut]: keys of an item's cut blocks with values taken out of V
+  uint4* bad = reinterpret_cast<uint4*>(smem + C::kBar);
+  uint64_t* full = reinterpret_cast<uint64_t*>(bad + kBadItems * kMostCut);  // [kStages]: block landed
   uint64_t* empty = full + kStages;       // [kStages]: products of the stage's block done
   uint64_t* clean = empty + kStages;      // [kStages]: block looked through, where it is a V block with a cut
   uint64_t* q_full = clean + kStages;     // [2]: tile's Q landed
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   volatile int* copied = reinterpret_cast<volatile int*>(misc + 2);  // blocks requested
   volatile int* q_copied = reinterpret_cast<volatile int*>(misc + 3);  // [2]: Q tiles requested
-  static_assert(16 * kStages + (3 * kStages + 18 + 2 * kItems) * 8 + 16 * kItems + 20 <= 1024, "barriers");
+  static_assert(16 * kBadItems * kMostCut + (3 * kStages + 18 + 2 * kItems) * 8 + 16 * kItems + 20 <= 1280, "barriers");
 
   const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -650,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; get_item(k, it); ++k) {
       const int all = max(blocks_of<C::kKeys>(it.t0, P.tpt, it.len), blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len));
       const int cut = base + 2 * first_cut<C::kKeys>(it.t0);
+      uint4* notes = bad + (k % kBadItems) * kMostCut;
       bool ok = true;
       for (int place = base; place < base + 2 * all; ++place) {
         const int s = place % kStages;
@@ -681,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const uint32_t keys = __ballot_sync(0xFFFFFFFFu, odd);
-          if (lane == 0) reinterpret_cast<uint32_t*>(&bad[s])[word] = keys;
+          if (lane == 0) reinterpret_cast<uint32_t*>(&notes[(place - cut) >> 1])[word] = keys;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -701,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t o_at = tmem + lane_off + C::kColO + C::kNextO * i;
     const float c = P.c;
     const int row_t = r / P.G, row_h = r - row_t * P.G;  // the row's token of the tile and head of the group
-    int base = 0, blocks = 0;
+    int blocks = 0;
     Item it;
     for (int k = 0; get_item(k, it); ++k) {
       const int t0 = it.t0 + i * P.tpt;
@@ -709,9 +713,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = i ? n1 : n0;
       const int t = t0 + row_t;                     // the row's token, in its sequence
       const bool valid = row_t < P.tpt && t < it.len;
-      const int cut = first_cut<C::kKeys>(it.t0);             // (from here on values may have been taken out)
+      const int cut = first_cut<C::kKeys>(it.t0);   // (from here on values may have been taken out)
       float m = -INFINITY, l = 0.f;
-      uint32_t odd = 0;                             // bit j - cut: the row sees a value of block j that is not finite
       // A wait is one vote of the warp a block (what follows is warp-collective): barriers are
       // looked at early, and waited for only where that has not shown them complete.
       bool ok = true, come = false;                 // come: the block's scores are there
@@ -750,21 +753,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float negm = m == -INFINITY ? 0.f : -m;
         l = l * factor + weights<kBf16>(v, c, negm);
-        if (j >= cut) {
-          const int see = t - j * C::kKeys + 1;
-          const int place = base + 2 * j + 1, s = place % kStages;
-          if (!(ok = wait_all(&clean[s], uint32_t(place / kStages) & 1u))) break;
-          const uint4 keys = bad[s];
-          if (keys.x | keys.y | keys.z | keys.w) {
-            const uint32_t word[4] = {keys.x, keys.y, keys.z, keys.w};
-#pragma unroll
-            for (int w = 0; w < (C::kKeys + 31) / 32; ++w) {
-              const int lim_w = see - 32 * w;
-              const uint32_t seen = lim_w >= 32 ? ~0u : lim_w <= 0 ? 0u : (1u << lim_w) - 1u;
-              if (word[w] & seen) odd |= 1u << (j - cut);
-            }
-          }
-        }
         come = j + 1 < n && mbar_try_wait(&s_full[i], uint32_t(blocks + j + 1) & 1u);
         tc_fence_after();
         store_weights<C::kKeys / 2>(p_at, v);
@@ -776,10 +764,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0) {
         if (!wait_all(&o_done[i], uint32_t(blocks + n - 1) & 1u)) break;
         tc_fence_after();
+        // Bit b: the row sees a value of block cut + b that is not finite. (The products waited for the notes.)
+        uint32_t odd = 0;
+        const uint4* notes = bad + (k % kBadItems) * kMostCut;
+#pragma unroll
+        for (int b = 0; b < kMostCut; ++b) {
+          const uint4 keys = b < n - cut ? notes[b] : make_uint4(0, 0, 0, 0);
+          if (keys.x | keys.y | keys.z | keys.w) {
+            const uint32_t word[4] = {keys.x, keys.y, keys.z, keys.w};
+            const int see = t - (cut + b) * C::kKeys + 1;
+#pragma unroll
+            for (int w = 0; w < (C::kKeys + 31) / 32; ++w) {
+              const int lim_w = see - 32 * w;
+              const uint32_t seen = lim_w >= 32 ? ~0u : lim_w <= 0 ? 0u : (1u << lim_w) - 1u;
+              if (word[w] & seen) odd |= 1u << b;
+            }
+          }
+        }
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // (NaN stays)
         // Of its own row a lane would store 32 bytes at a time, a line each; the lines are what the
         // stores take. So half rows change lanes on the way, through P's columns: four lanes have a
-        // line of a row then, an instruction eight lines (2,400 -> VEPI cycles for both tiles).
+        // line of a row then, an instruction eight lines (2,400 -> 1,700 cycles an item of short prompts).
         uint16_t* tile = static_cast<uint16_t*>(P.O) + (int64_t(it.first - it.t0 + t0) * P.Hq + it.head * P.G) * kD;
         const int end = min(P.tpt, it.len - t0);      // tokens
 #pragma unroll
@@ -817,7 +822,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (odd && valid) add_taken_out<C::kKeys, kD, kBf16>(P, out, odd, cut, t, it.first - it.t0, it.head);
         }
       }
-      base += 2 * max(n0, n1);
       blocks += n;
     }
   }
