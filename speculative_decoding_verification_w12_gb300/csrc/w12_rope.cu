@@ -13,7 +13,10 @@
 //
 // A group of d/16 lanes takes one row, a lane two words of 8 values that hold whole pairs:
 // words l and l + rot/16 where halves are paired (the words past rot two by two), any where
-// neighbours are. The floor is HBM: each row read once and written once.
+// neighbours are. The floor is HBM: each row read once and written once. 16,384 tokens of 40 + 8
+// heads of 128 in bf16 take 78 us, 5.3 TB/s, where a copy of as much takes 61: a group of lanes
+// has four heads of a token in flight (one or two: 92 to 99 us), half of the issue slots are full
+// and three quarters with the quantiser of the cache's append behind it (32,768 rows: 56 us).
 #include <type_traits>
 
 #include "w12_kv4_quant.cuh"
