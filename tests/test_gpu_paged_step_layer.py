@@ -210,3 +210,54 @@ def test_no_prompts_at_all():
     assert step.prompt(*none, to_dev_i32([0, 0, 0, 0])).shape == (0, HQ, D)
     torch.cuda.synchronize()
     assert step.length.tolist() == [0, 0, 0] and status_value(step.status) == 0 and not step.pages.used.any()
+
+
+def test_a_graph_of_prompts_takes_other_offsets():
+    """Captured with one set of prompts, replayed with others of as many rows; eager beside it."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    rows = [torch.randn((90, h, D), generator=g, device="cuda") for h in (HQ, HKV, HKV)]
+    eager, graphed = (_step()[0] for _ in range(2))
+    cu = to_dev_i32([0, 30, 60, 90])
+    graphed.prompt(*rows, cu)          # (makes what is made once)
+    graphed.pages.trim(torch.zeros_like(graphed.length))
+    graphed.length.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = graphed.prompt(*rows, cu)
+    for offsets in ([0, 90, 90, 90], [0, 1, 2, 77], [0, 0, 45, 90]):
+        for step in (eager, graphed):
+            step.pages.trim(torch.zeros_like(step.length))
+            step.length.zero_()
+        cu.copy_(to_dev_i32(offsets))
+        graph.replay()
+        want = eager.prompt(*rows, to_dev_i32(offsets))
+        n = offsets[-1]
+        assert torch.equal(out[:n], want[:n]) and torch.equal(graphed.length, eager.length)
+        assert graphed.length.tolist() == np.diff(offsets).tolist()
+        for b, k in enumerate(np.diff(offsets)):
+            for x, y in zip(_rows(graphed, b, int(k)), _rows(eager, b, int(k))):
+                np.testing.assert_array_equal(x, y)
+    assert status_value(graphed.status) == 0 and status_value(eager.status) == 0
+
+
+def test_without_launch_overlap():
+    """Launches that wait for one another give the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rows = [torch.randn((60, h, D), generator=g, device="cuda") for h in (HQ, HKV, HKV)]
+    X = torch.randn((B * T, HIDDEN), generator=g, device="cuda").bfloat16()
+    tree = to_dev_i32(np.tile(np.arange(-1, T - 1), (B, 1)))
+    draft, which = torch.zeros_like(tree), to_dev_i32([0, -1, 2])
+    got = []
+    for overlap in (True, False):
+        step = _step()[0]
+        w12.set_overlap(overlap)
+        try:
+            O = step.prompt(*rows, to_dev_i32([0, 20, 40, 60]))
+            r = step.run(X, tree, draft, adapter=which)
+            torch.cuda.synchronize()
+        finally:
+            w12.set_overlap(True)
+        assert status_value(step.status) == 0
+        got.append([O, step.length] + [r[k] for k in sorted(r)])
+    assert all(torch.equal(x, y) for x, y in zip(*got))
