@@ -73,13 +73,16 @@ struct Half {
   }
 };
 
-template <typename E, bool kVec>
+// kOnce: memory that nothing reads again.
+template <typename E, bool kVec, bool kOnce = false>
 __device__ __forceinline__ E load8(const uint8_t* p) {
   E e;
   if constexpr (kVec) {
 #pragma unroll
-    for (int i = 0; i < int(sizeof(E) / 16); ++i)
-      reinterpret_cast<uint4*>(e.w)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < int(sizeof(E) / 16); ++i) {
+      const uint4* at = reinterpret_cast<const uint4*>(p) + i;
+      reinterpret_cast<uint4*>(e.w)[i] = kOnce ? __ldcs(at) : __ldg(at);
+    }
   } else if constexpr (E::kSize == 4) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) e.w[i] = reinterpret_cast<const uint32_t*>(p)[i];

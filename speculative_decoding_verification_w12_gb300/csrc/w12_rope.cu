@@ -14,9 +14,9 @@
 // A group of d/16 lanes takes one row, a lane two words of 8 values that hold whole pairs:
 // words l and l + rot/16 where halves are paired (the words past rot two by two), any where
 // neighbours are. The floor is HBM: each row read once and written once. 16,384 tokens of 40 + 8
-// heads of 128 in bf16 take 78 us, 5.3 TB/s, where a copy of as much takes 61: a group of lanes
-// has four heads of a token in flight (one or two: 92 to 99 us), half of the issue slots are full
-// and three quarters with the quantiser of the cache's append behind it (32,768 rows: 56 us).
+// heads of 128 in bf16 take 68 us, 6.1 TB/s, where a copy of as much takes 61: a group of lanes
+// has four heads of a token in flight (two: 75 us). With the quantiser of the cache's append behind
+// it issue decides (72 % of the slots; 32,768 rows: 54 us).
 #include <type_traits>
 
 #include "w12_kv4_quant.cuh"
@@ -24,7 +24,10 @@
 namespace w12 {
 namespace kv4 {
 
-constexpr int kRopeThreads = 256;
+// Small blocks, 100 registers a thread: 20 warps an SM with 128 bytes a thread in flight. Blocks of 256
+// at 80 registers take 78 us where these take 68 (16,384 tokens, 40 + 8 heads of 128, bf16), 128
+// registers 76, 72 86; without the loads' and stores' mark that memory is passed through once 74.
+constexpr int kRopeThreads = 128, kRopeBlocks = 5;
 
 struct RopeParams {
   const float* table;
@@ -191,15 +194,15 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ void store8(void* out, int64_t at, int type, const float* x) {
   if (type == W12_F32) {
     float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-    o[0] = make_float4(x[0], x[1], x[2], x[3]);
-    o[1] = make_float4(x[4], x[5], x[6], x[7]);
+    __stcs(o, make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(o + 1, make_float4(x[4], x[5], x[6], x[7]));
   } else {
     uint4 v;
     if (type == W12_BF16)
       v = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     else
       v = make_uint4(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]), pack_f16x2(x[4], x[5]), pack_f16x2(x[6], x[7]));
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at) = v;
+    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at), v);
   }
 }
 
@@ -207,7 +210,7 @@ __device__ __forceinline__ void store8(void* out, int64_t at, int type, const fl
 // table are read once for all of them, and all their loads are in flight together). kPlain:
 // queries go out in bf16, and all of a row is rotated by halves; the other cases are found as it runs.
 template <int kD, typename E, bool kCache, int kHeads, bool kPlain>
-__global__ void __launch_bounds__(kRopeThreads, kHeads == 1 ? 1 : 3) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kHeads == 1 ? 1 : kRopeBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kRow = kD / 16;  // lanes of a row
   grid_dep_wait();
   grid_dep_launch();
@@ -237,8 +240,8 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 1 ? 1 : 3) rope_kernel
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
       const uint8_t* x = x0 + (kHeads == 1 ? h0 : min(h0 + k, H - 1)) * step;
-      a[k] = load8<E, true>(x + wa * 8 * E::kSize);
-      b[k] = load8<E, true>(x + wb * 8 * E::kSize);
+      a[k] = load8<E, true, true>(x + wa * 8 * E::kSize);
+      b[k] = load8<E, true, true>(x + wb * 8 * E::kSize);
     }
   } else {
 #pragma unroll
@@ -417,7 +420,7 @@ static int launch_rows(RopeParams p, int d, int dtype, void* stream) {
   auto blocks = [&](int kind, int heads) -> int64_t {
     return p.x[kind] ? (p.n * ((p.H[kind] + heads - 1) / heads) + units - 1) / units : 0;
   };
-  const int64_t few = 8 * int64_t(device_sm_count());
+  const int64_t few = 16 * int64_t(device_sm_count());
   const int heads = blocks(0, kGroup) + blocks(1, kGroup) + blocks(2, kGroup) >= few ? kGroup : 1;
   int64_t at = 0;
   for (int k = 0; k < 3; ++k) p.first[k] = unsigned(at += blocks(k, heads));
