@@ -17,13 +17,20 @@
 // step are in flight before the step before it computes.
 //
 // The first launch splits K over a cluster of eight blocks (and their eight warps); the
-// blocks' sums meet in distributed shared memory, in a fixed order.
+// blocks' sums meet in distributed shared memory, in a fixed order. With more tiles than clusters a
+// cluster takes 2, 4 or 8 of them at a time and splits K that much less: 256 rows of an adapter
+// each had 47 us there when every tile went through a whole cluster, 21 so.
 //
-// Bound by HBM where many adapters are read: 16 x 16 rows, rank 64, 5120 -> 34,816 take 38 us for
-// 156 MB, 10 of them the first launch's loads and joins and 28 the second's 142 MB at 5 TB/s. Few
-// rows are two launches' latency: 16 rows of one adapter of rank 16, 5120 -> 5120, 5.8 us.
+// The second gives every warp as many neighbouring units of 16 columns, over the tiles: warps that
+// went over the tiles one behind the other waited for each one's rows, T and first columns (256
+// rows of an adapter each, rank 16, 5120 -> 7168: both launches 84 us, now 42). B is marked as read once,
+// which leaves the L2 cache to Y (64 rows of an adapter each, rank 16, 5120 -> 34,816: 36 us, without 39).
+//
+// 16 x 16 rows, rank 64, 5120 -> 34,816 take 37 us for 156 MB: 11 for the first launch's chain of
+// loads and sums, 26 for the second's 142 MB at 5.5 TB/s. Few rows are two launches' latency: 16
+// rows of one adapter of rank 16, 5120 -> 5120, 5.7 us. Many single rows of a small rank are bound
+// by issue: those 64 rows' 100 MB at 2.8 TB/s. (All from HBM; 27, 5.5 and 33 us from L2.)
 #include <algorithm>
-
 #include "w12_dev.cuh"
 #include "w12_host.h"
 
@@ -34,12 +41,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSplit = 8;        // blocks of a cluster, along K
 constexpr int kMaxRank = 128;
-// Columns of Y that a block of the second launch has at least: few rows want many blocks (256:
-// 5.7 us where 512 take 6.5, 16 rows of one adapter, N 5120), many rows longer ones (38 us where 256
-// take 40, 16 adapters, N 34,816).
-constexpr int kColsFew = 256, kCols = 512;
-constexpr int kFill = 4;         // blocks an SM of the second launch, which take the tiles in turn
-
 struct Params {
   const uint16_t *X, *A, *B;
   const float* scale;
@@ -82,7 +83,9 @@ __device__ __forceinline__ float rest_of(float x, float part) { return fabsf(par
 
 // Rows by adapter: a tile begins at the first row of an adapter and at every 16th after it.
 struct Tiles {
-  int run_key[kMaxM], run_at[kMaxM + 1], run_before[kMaxM];  // neighbours of one adapter: which, from where, rows of it before
+  // Neighbours of one adapter: which, from where, how many; rows of it before.
+  __align__(16) int run_key[kMaxM], run_len[kMaxM];
+  int run_at[kMaxM + 1], run_before[kMaxM];
   int count[2][kWarps];
   int row[16];        // of the tile in hand; -1: none
   int key;            // its adapter
@@ -133,10 +136,17 @@ __device__ __forceinline__ int sort_rows(const Params& p, Tiles& s, Mine& m) {
   }
   if (tid == 0) s.run_at[runs] = kThreads;
   __syncthreads();
+  if (begins) s.run_len[run] = s.run_at[run + 1] - s.run_at[run];
+  __syncthreads();
   if (begins) {
     int n = 0;
-    for (int j = 0; m.key >= 0 && j < run; ++j)
-      if (s.run_key[j] == m.key) n += s.run_at[j + 1] - s.run_at[j];
+    for (int j = 0; m.key >= 0 && j < run; j += 4) {  // (runs from this one on are looked at and not counted)
+      const int4 k = *reinterpret_cast<const int4*>(&s.run_key[j]), l = *reinterpret_cast<const int4*>(&s.run_len[j]);
+      n += k.x == m.key ? l.x : 0;
+      n += k.y == m.key && j + 1 < run ? l.y : 0;
+      n += k.z == m.key && j + 2 < run ? l.z : 0;
+      n += k.w == m.key && j + 3 < run ? l.w : 0;
+    }
     s.run_before[run] = n;
   }
   __syncthreads();
@@ -194,22 +204,34 @@ __device__ __forceinline__ void take_tile(Tiles& s, const Mine& m, int t) {
   __syncthreads();
 }
 
+// Blocks an SM of the two launches that a rank has registers for. (Rank 64 with one block of the first and
+// three steps of loads ahead: 16 x 16 rows 31 us where two and one ahead take 27.)
+constexpr int shrink_blocks(int rank) { return rank <= 64 ? 2 : 1; }
+constexpr int expand_blocks(int rank) { return rank <= 16 ? 3 : rank <= 64 ? 2 : 1; }
+
 // kR: rank rounded up to the next of 16, 32, 64, 128.
 template <int kR, bool kSmall>
-__global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shrink_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, shrink_blocks(kR)) shrink_kernel(const __grid_constant__ Params p) {
   constexpr int kN = kR / 8;   // tiles of 8 of the rank
   constexpr int kParts = 4;
   __shared__ Tiles s;
   __shared__ __align__(16) float part[kParts][16][kR];
   grid_dep_wait();
   grid_dep_launch();
-  const int split = int(blockIdx.x);  // (the cluster is the grid's x)
+  const int rank = int(blockIdx.x);  // (the cluster is the grid's x)
   Mine m;
   Few f;
   const int total = kSmall ? sort_few(p, f) : sort_rows(p, s, m);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  if (!kSmall && split == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.head[0] = total;
-  for (int t = int(blockIdx.y); t < total; t += int(gridDim.y)) {  // (the same in all of the cluster)
+  if (!kSmall && rank == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.head[0] = total;
+  // A cluster takes as many tiles at a time (1, 2, 4, 8) as leaves few rounds; K is split over a
+  // tile's blocks.
+  int split = kSplit;
+  while (split > 1 && total * split > int(gridDim.y) * kSplit) split >>= 1;
+  const int group = rank / split, part_k = rank % split, groups = kSplit / split;
+  for (int t0 = int(blockIdx.y) * groups; t0 < total; t0 += int(gridDim.y) * groups) {  // (the same in all of the cluster)
+    const bool there = t0 + group < total;
+    const int t = there ? t0 + group : t0;
     int a, r0, r1;
     if constexpr (kSmall) {
       a = few_tile(f, t, r0, r1);
@@ -218,8 +240,9 @@ __global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shr
       a = s.key;
       r0 = s.row[g];
       r1 = s.row[g + 8];
-      if (split == 0 && threadIdx.x < 17) p.head[64 + 32 * t + threadIdx.x] = threadIdx.x < 16 ? s.row[threadIdx.x] : a;
+      if (part_k == 0 && there && threadIdx.x < 17) p.head[64 + 32 * t + threadIdx.x] = threadIdx.x < 16 ? s.row[threadIdx.x] : a;
     }
+    const float scale = p.scale[a];
     const uint16_t *x0 = p.X + int64_t(max(r0, 0)) * p.x_stride, *x1 = p.X + int64_t(max(r1, 0)) * p.x_stride;
     const uint16_t* Aa = p.A + int64_t(a) * p.rank * p.K;
     float acc[kN][4];
@@ -227,8 +250,8 @@ __global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shr
     for (int i = 0; i < kN; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     // Steps ahead that loads are in flight: as the registers allow.
-    constexpr int kAhead = kR <= 16 ? 2 : 1;
-    constexpr int kStep = 32 * kSplit * kWarps;
+    constexpr int kAhead = kR <= 16 ? 3 : kR <= 32 ? 2 : 1;
+    const int step_k = 32 * split * kWarps;
     uint4 u0[kAhead], u1[kAhead], w[kAhead][kN];
     auto load = [&](int i, int64_t k) {
       const int64_t at = k + 8 * q;
@@ -239,9 +262,9 @@ __global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shr
       for (int j = 0; j < kN; ++j)
         w[i][j] = in && 8 * j + g < p.rank ? __ldg(reinterpret_cast<const uint4*>(Aa + int64_t(8 * j + g) * p.K + at)) : zero;
     };
-    int64_t k = 32 * (split + kSplit * warp);
+    int64_t k = there ? 32 * (part_k + split * warp) : p.K;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load(i, k + i * kStep);
+    for (int i = 0; i < kAhead; ++i) load(i, k + i * step_k);
     while (k < p.K) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {  // (past K all operands are zero)
@@ -249,8 +272,8 @@ __global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shr
         uint4 v[kN];
 #pragma unroll
         for (int j = 0; j < kN; ++j) v[j] = w[i][j];
-        load(i, k + kAhead * kStep);
-        k += kStep;
+        load(i, k + kAhead * step_k);
+        k += step_k;
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
           mma16816(acc[j], m0, v[j].x, v[j].y);
@@ -286,13 +309,11 @@ __global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shr
     __syncwarp();
     cluster_sync();
     // The blocks' sums, a share of the pairs each: T, three bf16 parts, in the operands' order.
-    const float scale = p.scale[a];
-    for (int e = split * kThreads + threadIdx.x; e < 8 * kR; e += kSplit * kThreads) {
+    for (int e = there ? part_k * kThreads + threadIdx.x : 8 * kR; e < 8 * kR; e += split * kThreads) {
       const int row = e / (kR / 2), j = 2 * (e % (kR / 2));
       float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-      for (uint32_t c = 0; c < kSplit; ++c) {
-        const float2 o = peer_load2(&part[0][row][j], c);
+      for (int c = 0; c < split; ++c) {
+        const float2 o = peer_load2(&part[0][row][j], uint32_t(group * split + c));
         v.x += o.x;
         v.y += o.y;
       }
@@ -316,9 +337,10 @@ __global__ void __launch_bounds__(kThreads, kR <= 32 ? 3 : kR <= 64 ? 2 : 1) shr
 }
 
 template <int kR, bool kSmall>
-__global__ void __launch_bounds__(kThreads, kR > 64 ? 1 : kR > 32 ? 2 : 3) expand_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, expand_blocks(kR)) expand_kernel(const __grid_constant__ Params p) {
   constexpr int kC = kR / 16;
   constexpr bool kWide = kR >= 32;
+  constexpr int kAhead = kR <= 32 ? 2 : 1;   // units that loads are ahead: as the registers allow
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
   // What the launch before writes of this is T alone where rows are few: their rows, Y and B are
   // there before it ends.
@@ -330,8 +352,18 @@ __global__ void __launch_bounds__(kThreads, kR > 64 ? 1 : kR > 32 ? 2 : 3) expan
     grid_dep_wait();
     total = p.head[0];
   }
-  bool waited = !kSmall;
-  for (int t = int(blockIdx.y); t < total; t += int(gridDim.y)) {
+  // Units of 16 columns of a tile, in order; every warp takes as many neighbours.
+  const int64_t per = p.N / 16, units = total * per, warps = int64_t(gridDim.x) * kWarps, me = int64_t(blockIdx.x) * kWarps + warp;
+  const int64_t from = units * me / warps;
+  int left = int(units * (me + 1) / warps - from), to_load = left;
+  // Where a warp is: its tile, the lane's places in the tile's rows (null: no row) and in B, and the
+  // columns that are left of the tile.
+  struct At {
+    int t, cols;
+    float *y0, *y1;
+    const uint16_t* b;
+  };
+  auto enter = [&](At& at, int t, int col) {
     int r0, r1, a;
     if constexpr (kSmall) {
       a = few_tile(f, t, r0, r1);
@@ -339,69 +371,92 @@ __global__ void __launch_bounds__(kThreads, kR > 64 ? 1 : kR > 32 ? 2 : 3) expan
       const int32_t* tile = p.head + 64 + 32 * t;
       r0 = tile[g], r1 = tile[g + 8], a = tile[16];
     }
-    const uint16_t* Ba = p.B + int64_t(a) * p.N * p.rank;
-    float *y0 = p.Y + int64_t(max(r0, 0)) * p.y_stride + 4 * q, *y1 = p.Y + int64_t(max(r1, 0)) * p.y_stride + 4 * q;
-    // 16 columns a step: column 4q + {0, 1} of them from the first product, 4q + {2, 3} from
-    // the second, so that a lane holds four neighbours of a row.
-    struct Cols {
-      float4 u0, u1;
-      uint32_t w0[2 * kC], w1[2 * kC];
-    };
-    auto load = [&](Cols& c, int64_t n) {
-      const uint16_t* b0 = Ba + (n + 4 * (g >> 1) + (g & 1)) * p.rank;
-      const uint16_t* b1 = b0 + 2 * p.rank;
-      if constexpr (kWide) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+    at.t = t;
+    at.cols = int(p.N) - col;
+    at.y0 = r0 >= 0 ? p.Y + int64_t(r0) * p.y_stride + col + 4 * q : nullptr;
+    at.y1 = r1 >= 0 ? p.Y + int64_t(r1) * p.y_stride + col + 4 * q : nullptr;
+    at.b = p.B + (int64_t(a) * p.N + col + 4 * (g >> 1) + (g & 1)) * p.rank + (kWide ? 8 : 4) * q;
+  };
+  // To the next unit; more: there is one.
+  auto advance = [&](At& at, bool more) -> bool {
+    at.cols -= 16;
+    if (more && at.cols == 0) {
+      enter(at, at.t + 1, 0);
+      return true;
+    }
+    at.b += 16 * p.rank;
+    if (at.y0) at.y0 += 16;
+    if (at.y1) at.y1 += 16;
+    return false;
+  };
+  // 16 columns a step: column 4q + {0, 1} of them from the first product, 4q + {2, 3} from
+  // the second, so that a lane holds four neighbours of a row.
+  struct Cols {
+    float4 u0, u1;
+    uint32_t w0[2 * kC], w1[2 * kC];
+  };
+  At in{};
+  auto load = [&](Cols& c) {   // the unit at `in`, which moves on
+    const uint16_t *b0 = in.b, *b1 = in.b + 2 * p.rank;
+    if constexpr (kWide) {
+      const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < kC / 2; ++i) {
-          const int k = 32 * i + 8 * q;
-          const bool in = k < p.rank;  // the rank is a multiple of 8
-          const uint4 f = in ? __ldg(reinterpret_cast<const uint4*>(b0 + k)) : zero, h = in ? __ldg(reinterpret_cast<const uint4*>(b1 + k)) : zero;
-          c.w0[4 * i] = f.x, c.w0[4 * i + 1] = f.y, c.w0[4 * i + 2] = f.z, c.w0[4 * i + 3] = f.w;
-          c.w1[4 * i] = h.x, c.w1[4 * i + 1] = h.y, c.w1[4 * i + 2] = h.z, c.w1[4 * i + 3] = h.w;
-        }
-      } else {
-        const bool in = 4 * q < p.rank;
-        const uint2 f = in ? __ldg(reinterpret_cast<const uint2*>(b0 + 4 * q)) : make_uint2(0, 0);
-        const uint2 h = in ? __ldg(reinterpret_cast<const uint2*>(b1 + 4 * q)) : make_uint2(0, 0);
-        c.w0[0] = f.x, c.w0[1] = f.y, c.w1[0] = h.x, c.w1[1] = h.y;
+      for (int i = 0; i < kC / 2; ++i) {
+        const bool is = 32 * i + 8 * q < p.rank;  // the rank is a multiple of 8
+        const uint4 f = is ? __ldcs(reinterpret_cast<const uint4*>(b0 + 32 * i)) : zero, h = is ? __ldcs(reinterpret_cast<const uint4*>(b1 + 32 * i)) : zero;
+        c.w0[4 * i] = f.x, c.w0[4 * i + 1] = f.y, c.w0[4 * i + 2] = f.z, c.w0[4 * i + 3] = f.w;
+        c.w1[4 * i] = h.x, c.w1[4 * i + 1] = h.y, c.w1[4 * i + 2] = h.z, c.w1[4 * i + 3] = h.w;
       }
-      c.u0 = c.u1 = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (r0 >= 0) c.u0 = *reinterpret_cast<const float4*>(y0 + n);
-      if (r1 >= 0) c.u1 = *reinterpret_cast<const float4*>(y1 + n);
-    };
-    const int64_t stride = 16 * int64_t(kWarps) * gridDim.x;
-    int64_t n = 16 * (int64_t(blockIdx.x) * kWarps + warp);
-    Cols next;
-    if (n < p.N) load(next, n);
-    if (!waited) grid_dep_wait();
-    waited = true;
-    uint32_t T[kC][3][4];
+    } else {
+      const bool is = 4 * q < p.rank;
+      const uint2 f = is ? __ldcs(reinterpret_cast<const uint2*>(b0)) : make_uint2(0, 0);
+      const uint2 h = is ? __ldcs(reinterpret_cast<const uint2*>(b1)) : make_uint2(0, 0);
+      c.w0[0] = f.x, c.w0[1] = f.y, c.w1[0] = h.x, c.w1[1] = h.y;
+    }
+    c.u0 = c.u1 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in.y0) c.u0 = *reinterpret_cast<const float4*>(in.y0);
+    if (in.y1) c.u1 = *reinterpret_cast<const float4*>(in.y1);
+    advance(in, --to_load > 0);
+  };
+  Cols next[kAhead];
+  if (left > 0) enter(in, int(from / per), 16 * int(from % per));
+  At at = in;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (to_load > 0) load(next[i]);
+  if (kSmall) grid_dep_wait();
+  uint32_t T[kC][3][4];
+  auto load_t = [&]() {
 #pragma unroll
     for (int c = 0; c < kC; ++c)
 #pragma unroll
       for (int term = 0; term < 3; ++term) {
-        const uint4 v = *reinterpret_cast<const uint4*>(p.frag + ((int64_t(t) * kC + c) * 3 + term) * 128 + lane * 4);
+        const uint4 v = *reinterpret_cast<const uint4*>(p.frag + ((int64_t(at.t) * kC + c) * 3 + term) * 128 + lane * 4);
         T[c][term][0] = v.x, T[c][term][1] = v.y, T[c][term][2] = v.z, T[c][term][3] = v.w;
       }
-    while (n < p.N) {
-      const Cols c = next;
-      const int64_t at = n;
-      n += stride;
-      if (n < p.N) load(next, n);
+  };
+  if (left > 0) load_t();
+  while (left > 0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (left == 0) break;
+      const Cols c = next[i];
+      if (to_load > 0) load(next[i]);
       float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int term = 2; term >= 0; --term)
 #pragma unroll
-        for (int i = 0; i < kC; ++i) {
-          mma16816(c0, T[i][term], c.w0[2 * i], c.w0[2 * i + 1]);
-          mma16816(c1, T[i][term], c.w1[2 * i], c.w1[2 * i + 1]);
+        for (int j = 0; j < kC; ++j) {
+          mma16816(c0, T[j][term], c.w0[2 * j], c.w0[2 * j + 1]);
+          mma16816(c1, T[j][term], c.w1[2 * j], c.w1[2 * j + 1]);
         }
-      if (r0 >= 0) *reinterpret_cast<float4*>(y0 + at) = make_float4(c.u0.x + c0[0], c.u0.y + c0[1], c.u0.z + c1[0], c.u0.w + c1[1]);
-      if (r1 >= 0) *reinterpret_cast<float4*>(y1 + at) = make_float4(c.u1.x + c0[2], c.u1.y + c0[3], c.u1.z + c1[2], c.u1.w + c1[3]);
+      if (at.y0)
+        *reinterpret_cast<float4*>(at.y0) = make_float4(c.u0.x + c0[0], c.u0.y + c0[1], c.u0.z + c1[0], c.u0.w + c1[1]);
+      if (at.y1)
+        *reinterpret_cast<float4*>(at.y1) = make_float4(c.u1.x + c0[2], c.u1.y + c0[3], c.u1.z + c1[2], c.u1.w + c1[3]);
+      if (advance(at, --left > 0)) load_t();
     }
   }
-  if (!waited) grid_dep_wait();
   grid_dep_launch();
 }
 
@@ -430,16 +485,14 @@ static cudaError_t launch(const Params& p, int64_t tiles, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   // Clusters that the GPU holds at a time take the tiles in turn.
-  cfg.gridDim = dim3(kSplit, unsigned(std::min<int64_t>(tiles, (kR > 64 ? 1 : kR > 32 ? 2 : 3) * device_sm_count() / kSplit)));
+  cfg.gridDim = dim3(kSplit, unsigned(std::min<int64_t>(tiles, shrink_blocks(kR) * device_sm_count() / kSplit)));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = overlap_enabled() ? 2 : 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, shrink_kernel<kR, kSmall>, p);
   if (e != cudaSuccess) return e;
-  const int64_t cols = kSmall ? kColsFew : kCols, most = kFill * int64_t(device_sm_count());
-  const int64_t x = std::min((p.N + cols - 1) / cols, most);
-  cfg.gridDim = dim3(unsigned(x), unsigned(std::min(tiles, std::max<int64_t>(1, most / x))));
+  cfg.gridDim = dim3(unsigned(std::min<int64_t>((tiles * (p.N / 16) + 2 * kWarps - 1) / (2 * kWarps), expand_blocks(kR) * int64_t(device_sm_count()))));
   cfg.attrs = attr + 1;
   cfg.numAttrs = overlap_enabled() ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, expand_kernel<kR, kSmall>, p);

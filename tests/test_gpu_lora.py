@@ -196,3 +196,18 @@ def test_two_adapters_at_the_same_time():
             lora.run(X, y[i], ids, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(y, w) for some, w in zip(ys, want) for y in some)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(256, 80, 2072, 16), (200, 64, 520, 8), (129, 208, 1000, 64), (60, 16, 4104, 128), (31, 112, 5000, 32)])
+def test_a_request_a_row_each_with_an_adapter_of_its_own(M, N, K, r):
+    """More tiles than the clusters that the GPU holds, warps that go over several tiles; a row gets the
+    same whatever the order of the rows."""
+    A, B, scale, g = _make(M, N, K, r, seed=M)
+    X, Y0 = torch.randn((M, K), generator=g, device="cuda").bfloat16(), torch.randn((M, N), generator=g, device="cuda")
+    lora = w12.LoRA(A, B, scale)
+    order = torch.randperm(M, generator=g, device="cuda")
+    Y, Z = Y0.clone(), Y0[order].contiguous()
+    lora.run(X, Y, torch.arange(M, dtype=torch.int32, device="cuda"))
+    _check(X, Y0, Y, A, B, scale, list(range(M)))
+    lora.run(X[order].contiguous(), Z, order.to(torch.int32))
+    assert torch.equal(Z, Y[order])
