@@ -4,8 +4,8 @@
 //
 // Rows of a tile are (token, head of the group), token-major, 128 / G tokens: a key block is
 // read once for the whole group, and few of a tile's keys are cut by the diagonal. An item is
-// two such tiles, one behind the other, of one (sequence, kv head), with all keys that they
-// see in blocks. The kernel is persistent; the items of some sequences go out longest first
+// two such tiles (few rows: one), one behind the other, of one (sequence, kv head), with all keys
+// that they see in blocks. The kernel is persistent; the items of some sequences go out longest first
 // (Walk), in rounds of the grid that alternate in direction, so every block gets about the same
 // work and nothing is counted in memory. Per key block and tile:
 //   S = Q K^T         tcgen05.mma, both from shared memory, S in TMEM;
@@ -116,6 +116,7 @@ struct Params {
   int64_t total;
   int B, Hq, Hkv, G, tpt;      // tpt: tokens a tile
   int room;                    // tokens of a group of sequences
+  int step;                    // tokens of an item: two tiles or one
   uint32_t inv_g;              // a row's token is row inv_g / 2^16
   float c;                     // scale log2(e)
   uint64_t limit_ns;
@@ -142,7 +143,7 @@ __device__ __forceinline__ int first_cut(int t0) {
 }
 
 // Walks the items in their order: groups of sequences, whose keys and values stay in the L2 cache
-// while their items are under way; in a group by place in the sequence (in pairs of tiles), then
+// while their items are under way; in a group by place in the sequence (in items), then
 // sequence, then kv head. Groups run alternately up and down the places, the last one down, so that
 // neighbours in the order are alike in size and the smallest come last. Warp-collective.
 struct Walk {
@@ -153,10 +154,10 @@ struct Walk {
   uint32_t firsts;  // sequences of the chunk that a group begins with, those to come
   bool member;      // this lane's sequence is of the current group
   bool down;
-  int level, top;   // pairs before the current ones in their sequences, and the most of the group
+  int level, top;   // items before the current ones in their sequences, and the most of the group
   uint32_t left;    // sequences of the group that are still to come at this level
   int head;         // next kv head of the first of them
-  int n, start, len, group;  // of this lane's sequence of the chunk: pairs, first token, tokens, group
+  int n, start, len, group;  // of this lane's sequence of the chunk: items, first token, tokens, group
 
   __device__ __forceinline__ int chunks() const { return (B + 31) / 32; }
   __device__ __forceinline__ void load(int32_t* status) {
@@ -234,7 +235,7 @@ struct Walk {
         const int src = __ffs(left) - 1;
         it.t0 = level * step;
         it.first = __shfl_sync(0xFFFFFFFFu, start, src) + it.t0;
-        it.len = __shfl_sync(0xFFFFFFFFu, len, src);
+        it.len = min(__shfl_sync(0xFFFFFFFFu, len, src), it.t0 + step);
         it.head = head;
         return it;
       }
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 15) {
     // ---------------------------------------------------------------- items
-    Walk walk{P.cu, P.B, P.Hkv, 2 * P.tpt, P.room, P.total};
+    Walk walk{P.cu, P.B, P.Hkv, P.step, P.room, P.total};
     walk.begin(blockIdx.x == 0 ? P.status : nullptr);
     const int grid = int(gridDim.x), me = int(blockIdx.x);
     int skip = me;
@@ -935,7 +936,11 @@ int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_s
       !row_map(&v, V, bf16, head_dim, Hkv, total, v_token_stride, v_head_stride, 1, keys))
     return W12_ERR_CUDA;
   const int sms = device_sm_count();
-  const int64_t most = (total / (2 * P.tpt) + B) * Hkv;
+  const int64_t pairs = (total / (2 * P.tpt) + B) * Hkv;
+  // One tile an item where that leaves no block with two: tiles then do not share a block's schedulers
+  // (400 tokens, 40 / 8 heads of 128: 8.8 us, pairs 10.4; 777, where blocks would have two: 15.2, pairs 14.3).
+  P.step = pairs <= sms / 2 ? P.tpt : 2 * P.tpt;
+  const int64_t most = (total / P.step + B) * Hkv;
   const unsigned grid = unsigned(most < sms ? most : sms);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return cuda_status(head_dim == 128 ? (bf16 ? launch<128, true>(q, k, v, P, grid, s) : launch<128, false>(q, k, v, P, grid, s))
