@@ -94,6 +94,25 @@ __device__ __forceinline__ E load8(const uint8_t* p) {
   return e;
 }
 
+// Two fp32 operations by one instruction, each rounded by itself. A product alone is fma2 with a
+// -0 that the compiler does not know (it would join a product and a sum of pairs into one rounding).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 r, x, y, z;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 r, x, y;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // Scale, centre and 1 / s of a row.
 struct RowScale {
   uint32_t par;
@@ -143,19 +162,36 @@ __device__ __forceinline__ uint32_t code_word(const E& e, const RowScale& r) {
   return word - base;
 }
 
+// The same two elements at a time; nz: -0.
+template <bool kClamp, typename E>
+__device__ __forceinline__ uint32_t code_word2(const E& e, const RowScale& r, float nz) {
+  constexpr float kMagic = 12582920.f;
+  constexpr uint32_t kBits = 0x4B400000u;
+  uint32_t word = 0, base = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 t = fma2(add2(make_float2(e.value(2 * i), e.value(2 * i + 1)), both(-r.z)), both(r.inv), both(nz));
+    if constexpr (kClamp) t = make_float2(fminf(fmaxf(t.x, -8.f), 7.f), fminf(fmaxf(t.y, -8.f), 7.f));
+    t = add2(t, both(kMagic));
+    word += (__float_as_uint(t.x) << 4 * i) + (__float_as_uint(t.y) << (4 * i + 16));
+    base += (kBits << 4 * i) + (kBits << (4 * i + 16));
+  }
+  return word - base;
+}
+
 // The lane's two code words and its row's parameter word (z). Most rows have no code
 // outside -8 .. 7 (their centre's rounding is far below a step), and a warp of such
 // rows saves the clamps, a third of its work an element.
-template <int kLanes, typename E>
-__device__ __forceinline__ uint3 quantise16(const E& a, const E& b) {
+template <int kLanes, bool kPairs = false, typename E>
+__device__ __forceinline__ uint3 quantise16(const E& a, const E& b, float nz = 0.f) {
   const RowScale r = row_scale<kLanes>(a, b);
   uint3 q;
   if (__all_sync(0xFFFFFFFFu, r.inside)) {
-    q.x = code_word<false>(a, r);
-    q.y = code_word<false>(b, r);
+    q.x = kPairs ? code_word2<false>(a, r, nz) : code_word<false>(a, r);
+    q.y = kPairs ? code_word2<false>(b, r, nz) : code_word<false>(b, r);
   } else {
-    q.x = code_word<true>(a, r);
-    q.y = code_word<true>(b, r);
+    q.x = kPairs ? code_word2<true>(a, r, nz) : code_word<true>(a, r);
+    q.y = kPairs ? code_word2<true>(b, r, nz) : code_word<true>(b, r);
   }
   q.z = r.par;
   return r.finite ? q : make_uint3(0x88888888u, 0x88888888u, 0x7FC07FC0u);

@@ -43,7 +43,7 @@ struct RopeParams {
   int64_t block;
   int n_pages, P, p_shift;
   int rot, pairs, out_type, vec;
-  float eps;
+  float eps, nz;               // nz: -0, see fma2
   int32_t* status;
 };
 
@@ -68,10 +68,13 @@ __device__ __forceinline__ float over_row(float v) {
 // The sum of squares of a row that kRow lanes hold, in fp32 (about 2^-21 of it).
 template <int kRow>
 __device__ __forceinline__ float sum_squares(const float (&x)[16]) {
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  float2 s[2] = {both(0.f), both(0.f)};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i & 3] = fmaf(x[i], x[i], s[i & 3]);
-  return over_row<kRow>(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])));
+  for (int i = 0; i < 8; ++i) {
+    const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
+    s[i & 1] = fma2(v, v, s[i & 1]);
+  }
+  return over_row<kRow>(__fadd_rn(__fadd_rn(s[0].x, s[0].y), __fadd_rn(s[1].x, s[1].y)));
 }
 
 // The same as a pair, from that sum `rough`, which is finite. Each square is cut in two at 2^-16
@@ -80,14 +83,15 @@ __device__ __forceinline__ float sum_squares(const float (&x)[16]) {
 template <int kRow>
 __device__ __forceinline__ Sum2 sum_squares2(const float (&x)[16], float rough) {
   const float c = __uint_as_float((__float_as_uint(rough) & 0x7F800000u) + (7u << 23) + 0x400000u);
-  float hi[2] = {0.f, 0.f}, lo[2] = {0.f, 0.f};
+  float2 hi = both(0.f), lo = both(0.f);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float h = __fsub_rn(fmaf(x[i], x[i], c), c);
-    hi[i & 1] = __fadd_rn(hi[i & 1], h);
-    lo[i & 1] = __fadd_rn(lo[i & 1], fmaf(x[i], x[i], -h));
+  for (int i = 0; i < 8; ++i) {
+    const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
+    const float2 less = fma2(fma2(v, v, both(c)), both(-1.f), both(c));  // minus the upper parts
+    hi = fma2(less, both(-1.f), hi);
+    lo = add2(lo, fma2(v, v, less));
   }
-  return Sum2{over_row<kRow>(__fadd_rn(hi[0], hi[1])), over_row<kRow>(__fadd_rn(lo[0], lo[1]))};
+  return Sum2{over_row<kRow>(__fadd_rn(hi.x, hi.y)), over_row<kRow>(__fadd_rn(lo.x, lo.y))};
 }
 
 // fp32(1 / sqrt(m.hi + m.lo)): one step of Newton's iteration from the approximation, its
@@ -168,7 +172,7 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) 
 
 // Rotates the lane's 16 values x[0 .. 7] (word wa), x[8 .. 15] (wb); words past rot stay.
 template <bool kEach>
-__device__ __forceinline__ void rotate16(float (&x)[16], const Turn& t, bool in_a, bool in_b, bool pairs) {
+__device__ __forceinline__ void rotate16(float (&x)[16], const Turn& t, bool in_a, bool in_b, bool pairs, float nz) {
   if (pairs) {
     if (in_a) {
 #pragma unroll
@@ -180,7 +184,15 @@ __device__ __forceinline__ void rotate16(float (&x)[16], const Turn& t, bool in_
     }
   } else if (in_b) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) turn_pair<kEach>(x[i], x[8 + i], t.c[i], t.s[i]);
+    for (int i = 0; i < 8; i += 2) {
+      const float2 a = make_float2(x[i], x[i + 1]), b = make_float2(x[8 + i], x[9 + i]);
+      const float2 c = make_float2(t.c[i], t.c[i + 1]), s = make_float2(t.s[i], t.s[i + 1]), less = make_float2(-s.x, -s.y);
+      const float2 ac = fma2(a, c, both(nz)), bc = fma2(b, c, both(nz));
+      const float2 u = kEach ? add2(ac, fma2(b, less, both(nz))) : fma2(b, less, ac);
+      const float2 v = kEach ? add2(bc, fma2(a, s, both(nz))) : fma2(a, s, bc);
+      x[i] = u.x, x[i + 1] = u.y;
+      x[8 + i] = v.x, x[9 + i] = v.y;
+    }
   }
 }
 
@@ -270,7 +282,7 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 1 ? 1 : kRopeBlocks) r
     if constexpr (kCache) {
 #pragma unroll
       for (int k = 0; k < kHeads; ++k) {
-        const uint3 q = quantise16<kRow>(a[k], b[k]);
+        const uint3 q = quantise16<kRow, true>(a[k], b[k], p.nz);
         if (in && there && h0 + k < H) keep(h0 + k, q);
       }
     }
@@ -302,9 +314,12 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 1 ? 1 : kRopeBlocks) r
     if (w) {
       const float f = norm_factor<kD, kKey>(x, p.eps);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], f), g[i]);
+      for (int i = 0; i < 16; i += 2) {
+        const float2 y = fma2(fma2(make_float2(x[i], x[i + 1]), both(f), both(p.nz)), make_float2(g[i], g[i + 1]), both(p.nz));
+        x[i] = y.x, x[i + 1] = y.y;
+      }
     }
-    rotate16<kKey>(x, turn, in_a, in_b, pairs);
+    rotate16<kKey>(x, turn, in_a, in_b, pairs, p.nz);
     const bool mine = kHeads == 1 || h0 + k < H;
     if constexpr (kCache && kKey) {
       F32 u, v;
@@ -313,7 +328,7 @@ __global__ void __launch_bounds__(kRopeThreads, kHeads == 1 ? 1 : kRopeBlocks) r
         u.w[i] = __float_as_uint(x[i]);
         v.w[i] = __float_as_uint(x[8 + i]);
       }
-      const uint3 q = quantise16<kRow>(u, v);
+      const uint3 q = quantise16<kRow, true>(u, v, p.nz);
       if (in && there && mine) keep(h0 + k, q);
     } else if (live && mine) {
       const int64_t at = (int64_t(tok) * H + h0 + k) * kD;
@@ -447,6 +462,7 @@ static int rope_params(const w12_rope* r, int d, int dtype, int64_t n, const int
   p->qw = r->q_norm;
   p->kw = r->k_norm;
   p->eps = r->eps;
+  p->nz = -0.f;
   p->positions = positions;
   p->n = n;
   p->status = status;
