@@ -9,14 +9,15 @@
 // is rounded by itself, and r is the fp32 value next to the exact one, so that a row's result
 // depends on nothing but the row, and what the cache gets is bitwise what its append writes for
 // rows rotated to fp32. (A code at the border of two would otherwise hang on the order of a sum.)
-// Queries need no such care: plain fp32 sums and fused products, a third of the instructions.
+// Queries need no such care: plain fp32 sums and fused products, half of the instructions. All of it
+// runs two values an instruction (fma2): append of 32,768 rows 46 us, one value 52.
 //
 // A group of d/16 lanes takes one row, a lane two words of 8 values that hold whole pairs:
 // words l and l + rot/16 where halves are paired (the words past rot two by two), any where
 // neighbours are. The floor is HBM: each row read once and written once. 16,384 tokens of 40 + 8
-// heads of 128 in bf16 take 68 us, 6.1 TB/s, where a copy of as much takes 61: a group of lanes
-// has four heads of a token in flight (two: 75 us). With the quantiser of the cache's append behind
-// it issue decides (72 % of the slots; 32,768 rows: 54 us).
+// heads of 128 in bf16 take 66 us, 6.2 TB/s, where a copy of as much takes 61: a group of lanes
+// has four heads of a token in flight (two: 75 us; of fp32 rows two: 92 us, 6.7 TB/s, four 102). With
+// the quantiser of the cache's append behind it issue decides: those 46 us are 3.7 TB/s.
 #include <type_traits>
 
 #include "w12_kv4_quant.cuh"
@@ -417,15 +418,17 @@ static cudaLaunchConfig_t config(unsigned grid, int threads, cudaStream_t stream
 
 constexpr int kGroup = 4;  // heads of a group of lanes, where there are rows enough
 
-template <bool kCache, int kHeads, bool kPlain>
+// Of fp32 rows half as many: as many bytes in flight.
+template <bool kCache, bool kGrouped, bool kPlain>
 static cudaError_t launch_rope(const cudaLaunchConfig_t& cfg, const RopeParams& p, int d, int dtype) {
+  constexpr int kWide = kGrouped ? kGroup : 1, kF32 = kGrouped ? kGroup / 2 : 1;
   if (d == 128)
-    return dtype == W12_F32    ? cudaLaunchKernelEx(&cfg, rope_kernel<128, F32, kCache, kHeads, kPlain>, p)
-           : dtype == W12_BF16 ? cudaLaunchKernelEx(&cfg, rope_kernel<128, Half<true>, kCache, kHeads, kPlain>, p)
-                               : cudaLaunchKernelEx(&cfg, rope_kernel<128, Half<false>, kCache, kHeads, kPlain>, p);
-  return dtype == W12_F32    ? cudaLaunchKernelEx(&cfg, rope_kernel<64, F32, kCache, kHeads, kPlain>, p)
-         : dtype == W12_BF16 ? cudaLaunchKernelEx(&cfg, rope_kernel<64, Half<true>, kCache, kHeads, kPlain>, p)
-                             : cudaLaunchKernelEx(&cfg, rope_kernel<64, Half<false>, kCache, kHeads, kPlain>, p);
+    return dtype == W12_F32    ? cudaLaunchKernelEx(&cfg, rope_kernel<128, F32, kCache, kF32, kPlain>, p)
+           : dtype == W12_BF16 ? cudaLaunchKernelEx(&cfg, rope_kernel<128, Half<true>, kCache, kWide, kPlain>, p)
+                               : cudaLaunchKernelEx(&cfg, rope_kernel<128, Half<false>, kCache, kWide, kPlain>, p);
+  return dtype == W12_F32    ? cudaLaunchKernelEx(&cfg, rope_kernel<64, F32, kCache, kF32, kPlain>, p)
+         : dtype == W12_BF16 ? cudaLaunchKernelEx(&cfg, rope_kernel<64, Half<true>, kCache, kWide, kPlain>, p)
+                             : cudaLaunchKernelEx(&cfg, rope_kernel<64, Half<false>, kCache, kWide, kPlain>, p);
 }
 
 // The launch over the rows that p names, by groups of heads where they fill the GPU.
@@ -436,15 +439,16 @@ static int launch_rows(RopeParams p, int d, int dtype, void* stream) {
     return p.x[kind] ? (p.n * ((p.H[kind] + heads - 1) / heads) + units - 1) / units : 0;
   };
   const int64_t few = 16 * int64_t(device_sm_count());
-  const int heads = blocks(0, kGroup) + blocks(1, kGroup) + blocks(2, kGroup) >= few ? kGroup : 1;
+  const int group = dtype == W12_F32 ? kGroup / 2 : kGroup;
+  const int heads = blocks(0, group) + blocks(1, group) + blocks(2, group) >= few ? group : 1;
   int64_t at = 0;
   for (int k = 0; k < 3; ++k) p.first[k] = unsigned(at += blocks(k, heads));
   const bool plain = p.rot == d && !p.pairs && (kCache || p.out_type == W12_BF16);
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = config(unsigned(at), kRopeThreads, static_cast<cudaStream_t>(stream), attr);
-  return cuda_status(heads == 1 ? launch_rope<kCache, 1, false>(cfg, p, d, dtype)
-                     : plain    ? launch_rope<kCache, kGroup, true>(cfg, p, d, dtype)
-                                : launch_rope<kCache, kGroup, false>(cfg, p, d, dtype));
+  return cuda_status(heads == 1 ? launch_rope<kCache, false, false>(cfg, p, d, dtype)
+                     : plain    ? launch_rope<kCache, true, true>(cfg, p, d, dtype)
+                                : launch_rope<kCache, true, false>(cfg, p, d, dtype));
 }
 
 // The parts that both entry points check and fill in alike.
