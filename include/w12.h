@@ -484,7 +484,8 @@ int w12_logprobs(const void* logits, int dtype, int64_t M, int64_t V, int64_t ro
  *   c = table[pos][i], s = table[pos][rot_dim/2 + i]; the rest stays as it is.
  * All in fp32. Of keys each product and sum is rounded by itself, and r is the
  * fp32 value next to the exact one (of the row times 2^-76, where values pass
- * 2^50): a key's result depends on its row alone.
+ * 2^50; either of two that the exact one lies in the middle of, to 2^-7 of their
+ * distance): a key's result depends on its row alone.
  * Queries are off by up to 2^-19 of the row's largest value. table is fp32
  * [max_pos, rot_dim], the weights fp32 [head_dim] or NULL (no norm), all 16-byte
  * aligned; 1e-12 <= eps. A row whose position is -1 is no token: its output is

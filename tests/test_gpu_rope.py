@@ -355,3 +355,65 @@ def test_rows_and_slots_past_32_bits():
     for got, want in zip(big.read(slots), small.read(pos)):
         assert torch.equal(got, want)
     assert status_value(st) == 0
+
+
+# Rows enough for groups of heads: at least 608 blocks of 128 / (d / 16) of them.
+MANY = [(3400, 5, 1, 128, 128, False, True), (5000, 10, 2, 64, 64, False, True), (3400, 6, 3, 128, 64, False, False), (2500, 7, 4, 128, 128, True, True),
+        (5000, 9, 2, 64, 32, True, "q")]
+
+
+def _same_or_tie(got, x, w, pos, tab, pairs):
+    """As _same, among so many rows that a factor may lie in the middle of two fp32 numbers: 128 rests of
+    squares of up to 2^-17 of the whole are summed in 12 fp32 additions, off by up to 12 2^-24 2^-10 of
+    it, the factor by half of that, which is less than 2^-7 of the distance of two. There it is either."""
+    dtype = got.dtype
+    want = torch.from_numpy(O.rope(x, w, 1e-6, pos, tab, pairs)).to(dtype).float().numpy()
+    got = got.float().cpu().numpy()
+    n, h = np.nonzero((got != want).any(-1))
+    if len(n):
+        assert w is not None and len(n) <= 3
+        row = x[n, h][:, None]
+        r = 1 / np.sqrt(np.square(row.astype(np.float64)).mean(-1, keepdims=True) + np.float64(np.float32(1e-6)))
+        near = r.astype(np.float32)
+        other = np.nextafter(near, np.where(r > near, np.float32(np.inf), np.float32(0)))
+        assert (np.abs(r - (near.astype(np.float64) + other) / 2) <= 2.0 ** -7 * np.abs(other - near)).all()
+        want = torch.from_numpy(O.rope((row * other) * w, None, 0, pos[n], tab, pairs)).to(dtype).float().numpy()
+        np.testing.assert_array_equal(got[n, h][:, None], want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n,Hq,Hkv,d,rot,pairs,norm", MANY)
+def test_many_rows_give_what_few_give(n, Hq, Hkv, d, rot, pairs, norm, dtype):
+    rope, tab, qw, kw = _make(d, rot, pairs, norm, 97)
+    g = np.random.default_rng(n)
+    pos = g.integers(-1, 97, n)
+    dev = to_dev_i32(pos)
+    for offset, out in ((0, BF16), (0, F32), (3, F16)):    # (an odd offset: rows read one value at a time)
+        Q, K = _rows(n, (Hq, Hkv), d, dtype, n + d, offset=offset)
+        st = new_status()
+        got = rope.run(Q, K, dev, dtype=out, status=st)
+        few = [rope.run(Q[i:i + 90], K[i:i + 90], dev[i:i + 90], dtype=out) for i in range(0, n, 90)]
+        for a, b in zip(got, zip(*few)):
+            assert torch.equal(a, torch.cat(b))
+        assert status_value(st) == 0
+        _near(got[0], O.rope(Q.float().cpu().numpy(), qw, 1e-6, pos, tab, pairs))
+        _same_or_tie(got[1], K.float().cpu().numpy(), kw, pos, tab, pairs)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n,Hq,Hkv,d,rot,pairs,norm", MANY)
+def test_many_appended_rows_give_what_few_give(n, Hq, Hkv, d, rot, pairs, norm, dtype):
+    rope = _make(d, rot, pairs, norm, 97)[0]
+    g = np.random.default_rng(n)
+    Q, K, V = _rows(n, (Hq, Hkv, Hkv), d, dtype, n + d)
+    K = torch.where(torch.rand((n, 1, 1), device="cuda") < 0.1, K * 1000, K)     # (codes that need their clamp, some rows)
+    slots, pos = g.permutation(n + 100)[:n], g.integers(-1, 97, n)
+    slots[g.random(n) < 0.05] = -1
+    slots, pos, st = to_dev_i32(slots), to_dev_i32(pos), new_status()
+    whole, parts, two = (_pool((n + 100) // 64 + 1, Hkv, d, 64) for _ in range(3))
+    q = whole.append_rope(K, V, slots, rope, pos, Q=Q, status=st)
+    few = [parts.append_rope(K[i:i + 90], V[i:i + 90], slots[i:i + 90], rope, pos[i:i + 90], Q=Q[i:i + 90]) for i in range(0, n, 90)]
+    assert status_value(st) == 0
+    assert torch.equal(q, torch.cat(few)) and torch.equal(whole.pool, parts.pool)
+    two.append(rope.run(None, K, pos, dtype=F32)[1], V.float(), torch.where(pos < 0, -1, slots))
+    assert torch.equal(two.pool, whole.pool)
