@@ -294,3 +294,28 @@ def test_groups_of_sequences(lens):
     for a, e in zip(cu[:-1], cu[1:]):
         if e > a:
             assert torch.equal(out[a:e], w12.prompt_attention(q[a:e], k[a:e], v[a:e], to_dev_i32([0, e - a]))), (a, e)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 5, 16])
+def test_two_tiles_an_item_give_what_one_gives(G, d, dtype):
+    """Sixteen kv heads fill the GPU with items of two tiles; each by itself leaves it to single ones. With
+    values and keys that are not finite here and there."""
+    lens = [300, 0, 1, 257, 40, 513, 79, 80, 81, 128, 16]
+    cu, Hkv = _offsets(lens), 16
+    q, k, v = _rows(sum(lens), Hkv * G, Hkv, d, dtype, G + d)
+    for i, bad in enumerate((float("inf"), float("nan"), float("-inf"))):
+        v[37 + 211 * i, i, 5] = bad
+        v[301 + 17 * i, 4 + i, d - 1] = bad
+        k[640 + 30 * i, 8 + i, 3] = bad
+    dev, st = to_dev_i32(cu), new_status()
+    out = w12.prompt_attention(q, k, v, dev, status=st)
+    assert status_value(st) == 0
+    for h in range(Hkv):
+        heads = slice(h * G, h * G + G)
+        one = w12.prompt_attention(q[:, heads], k[:, h:h + 1], v[:, h:h + 1], dev)
+        assert torch.equal(torch.nan_to_num(out[:, heads], 77.0), torch.nan_to_num(one, 77.0)), h
+        assert torch.equal(torch.isnan(out[:, heads]), torch.isnan(one)), h
+    clean = slice(11 * G, 16 * G)                          # heads without such values
+    _close(out[:, clean], q[:, clean], k[:, 11:], v[:, 11:], cu, d ** -0.5)
