@@ -539,8 +539,9 @@ int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const 
  * out of [0, total], or decreasing ones, sets W12_ERR_ARG and is taken as empty (sequences
  * that share rows write either's result). Rows that a row does not see have no part in it,
  * whatever they hold. Scores, softmax and sums are fp32; a weight meets the values rounded to
- * their type (bf16: 2^-8 of itself, fp16: 2^-11 of itself or 2^-25 of the row's largest). A score of -inf weighs nothing; a row with no other
- * is zeros. No workspace. Device-side errors besides: W12_ERR_TIMEOUT. Returns
+ * their type (bf16: 2^-8 of itself, fp16: 2^-11 of itself or 2^-25 of the row's largest). A
+ * score of -inf weighs nothing; a row with no other is zeros. A sequence's bits do not depend
+ * on the call's others. No workspace. Device-side errors besides: W12_ERR_TIMEOUT. Returns
  * W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED or W12_ERR_CUDA. */
 int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_stride, const void* K, int64_t k_token_stride,
                          int64_t k_head_stride, const void* V, int64_t v_token_stride, int64_t v_head_stride, int dtype,
@@ -563,9 +564,11 @@ typedef struct w12_adapters {
  * and y_stride (of 4) elements apart, 16-byte aligned. ids int32 [M]: -1 is no
  * adapter, and the row of Y is not touched; another id outside [0, n) is taken so and
  * sets W12_ERR_ARG in dev_status. Products of bf16 values are summed in fp32, A X is
- * kept to 2^-24 of itself. B is finite (an infinity may come out as NaN). The workspace needs no zero fill, holds nothing between
- * calls, and follows the other rules at the top. Errors: W12_ERR_ARG,
- * W12_ERR_SHAPE, W12_ERR_WORKSPACE, W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
+ * kept to 2^-24 of itself. The same call gives the same bits; how many adapters it
+ * uses decides the order of the sums over K. B is finite (an infinity may come out as
+ * NaN). The workspace needs no zero fill, holds nothing between calls, and follows the
+ * other rules at the top. Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_WORKSPACE,
+ * W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
 size_t w12_lora_ws_bytes(int64_t M, int n_adapters, int rank);
 
 int w12_lora(const uint16_t* X, int64_t x_stride, int64_t M, const w12_adapters* adapters, const int32_t* ids, float* Y,
