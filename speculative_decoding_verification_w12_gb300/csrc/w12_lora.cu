@@ -26,7 +26,7 @@
 // rows of an adapter each, rank 16, 5120 -> 7168: both launches 84 us, now 42). B is marked as read once,
 // which leaves the L2 cache to Y (64 rows of an adapter each, rank 16, 5120 -> 34,816: 36 us, without 39).
 //
-// 16 x 16 rows, rank 64, 5120 -> 34,816 take 37 us for 156 MB: 11 for the first launch's chain of
+// 16 x 16 rows, rank 64, 5120 -> 34,816 take 36 us for 156 MB: 10 for the first launch's chain of
 // loads and sums, 26 for the second's 142 MB at 5.5 TB/s. Few rows are two launches' latency: 16
 // rows of one adapter of rank 16, 5120 -> 5120, 5.7 us. Many single rows of a small rank are bound
 // by issue: those 64 rows' 100 MB at 2.8 TB/s. (All from HBM; 27, 5.5 and 33 us from L2.)
@@ -253,19 +253,20 @@ __global__ void __launch_bounds__(kThreads, shrink_blocks(kR)) shrink_kernel(con
     constexpr int kAhead = kR <= 16 ? 3 : kR <= 32 ? 2 : 1;
     const int step_k = 32 * split * kWarps;
     uint4 u0[kAhead], u1[kAhead], w[kAhead][kN];
-    auto load = [&](int i, int64_t k) {
-      const int64_t at = k + 8 * q;
-      const bool in = at < p.K;  // K is a multiple of 8
+    const int K = int(p.K);  // below 2^30
+    auto load = [&](int i, int k) {
+      const int at = k + 8 * q;
+      const bool in = at < K;  // K is a multiple of 8
       u0[i] = in && r0 >= 0 ? *reinterpret_cast<const uint4*>(x0 + at) : zero;
       u1[i] = in && r1 >= 0 ? *reinterpret_cast<const uint4*>(x1 + at) : zero;
 #pragma unroll
       for (int j = 0; j < kN; ++j)
         w[i][j] = in && 8 * j + g < p.rank ? __ldg(reinterpret_cast<const uint4*>(Aa + int64_t(8 * j + g) * p.K + at)) : zero;
     };
-    int64_t k = there ? 32 * (part_k + split * warp) : p.K;
+    int k = there ? 32 * (part_k + split * warp) : K;
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load(i, k + i * step_k);
-    while (k < p.K) {
+    while (k < K) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {  // (past K all operands are zero)
         const uint32_t m0[4] = {u0[i].x, u1[i].x, u0[i].y, u1[i].y}, m1[4] = {u0[i].z, u1[i].z, u0[i].w, u1[i].w};
