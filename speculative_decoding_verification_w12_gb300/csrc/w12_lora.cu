@@ -31,6 +31,7 @@
 // rows of one adapter of rank 16, 5120 -> 5120, 5.7 us. Many single rows of a small rank are bound
 // by issue: those 64 rows' 100 MB at 2.8 TB/s. (All from HBM; 27, 5.5 and 33 us from L2.)
 #include <algorithm>
+
 #include "w12_dev.cuh"
 #include "w12_host.h"
 
@@ -41,6 +42,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSplit = 8;        // blocks of a cluster, along K
 constexpr int kMaxRank = 128;
+
 struct Params {
   const uint16_t *X, *A, *B;
   const float* scale;
