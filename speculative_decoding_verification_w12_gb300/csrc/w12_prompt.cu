@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint4* bad = reinterpret_cast<uint4*>(smem + C::kBar);
   uint64_t* full = reinterpret_cast<uint64_t*>(bad + kBadItems * kMostCut);  // [kStages]: block landed
   uint64_t* empty = full + kStages;       // [kStages]: products of the stage's block done
-  uint64_t* clean = empty + kStages;      // [kStages]: block looked through, where it is a V block with a cut
+  uint64_t* clean = empty + kStages;      // [kStages]: V block passed on, looked through where the diagonal cuts it
   uint64_t* q_full = clean + kStages;     // [2]: tile's Q landed
   uint64_t* q_empty = q_full + 2;         // [2]: the item's last S of the tile done
   uint64_t* s_full = q_empty + 2;         // [2]: S of the tile's block
@@ -585,12 +585,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok && get_item(k, it); ++k) {
       const int n0 = blocks_of<C::kKeys>(it.t0, P.tpt, it.len), n1 = blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len);
       const int all = max(n0, n1), n = i ? n1 : n0;
-      const int cut = first_cut<C::kKeys>(it.t0);
       if (n > 0 && is_s) ok = wait_all(&q_full[i], uint32_t(mine) & 1u);
       if (n > 0 && !is_s && mine > 0) ok = wait_all(&o_free[i], uint32_t(mine - 1) & 1u);
       for (int j = 0; ok && j < all; ++j, place += 2) {
         const int s = place % kStages;
-        ok = wait_all(!is_s && j >= cut ? &clean[s] : &full[s], uint32_t(place / kStages) & 1u);
+        // V is waited for as looked through in every block, cut or not: a wait names a parity alone, and
+        // were some turns of `clean` not waited for, the ring could pass the two warps that look.
+        const uint32_t turn = uint32_t(place / kStages) & 1u;
+        ok = wait_all(&full[s], turn) && (is_s || wait_all(&clean[s], turn));
         if (!ok) break;
         if (j >= n) {  // a block that only the other tile has
           if (lane == 0) mbar_arrive(&empty[s]);
@@ -655,18 +657,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 13 || warp == 14) {
     // ------------------------------------------------- values that are not finite
-    int base = 0;
+    int place = 1;   // in the ring, of the next V block
+    bool ok = true;
     Item it;
-    for (int k = 0; get_item(k, it); ++k) {
+    for (int k = 0; ok && get_item(k, it); ++k) {
       const int all = max(blocks_of<C::kKeys>(it.t0, P.tpt, it.len), blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len));
-      const int cut = base + 2 * first_cut<C::kKeys>(it.t0);
+      const int cut = first_cut<C::kKeys>(it.t0);
       uint4* notes = bad + (k % kBadItems) * kMostCut;
-      bool ok = true;
-      for (int place = base; place < base + 2 * all; ++place) {
+      // (V blocks that the diagonal does not cut are waited for and passed on too: the ring cannot pass these warps.)
+      for (int j = 0; ok && j < all; ++j, place += 2) {
         const int s = place % kStages;
-        // (Every block is waited for: the barrier then runs through the same phases as `full`.)
         if (!(ok = wait_all(&full[s], uint32_t(place / kStages) & 1u))) break;
-        if (place < cut || !((place - base) & 1)) {
+        if (j < cut) {
           if (lane == 0) mbar_arrive(&clean[s]);
           continue;
         }
@@ -692,14 +694,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const uint32_t keys = __ballot_sync(0xFFFFFFFFu, odd);
-          if (lane == 0) reinterpret_cast<uint32_t*>(&notes[(place - cut) >> 1])[word] = keys;
+          if (lane == 0) reinterpret_cast<uint32_t*>(&notes[j - cut])[word] = keys;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&clean[s]);
       }
-      if (!ok) break;
-      base += 2 * all;
     }
   }
   } else {
