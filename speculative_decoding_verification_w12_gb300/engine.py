@@ -234,6 +234,8 @@ class PagedVerifyStep:
         head_dim]. A prompt that there are no pages for, or that is too long, is attended
         over but not cached: its request stays as it was, and the status word says so. (Rows
         past max_len have no position: with a rotation their queries and keys are zeros.)
+        A prompt whose offsets decrease, leave the rows or share rows with another's is not
+        cached either (W12_ERR_ARG), and its rows of the answer mean nothing.
         """
         n, st = K.shape[0], self.status
         w12._want(cu_seqlens, "cu_seqlens", torch.int32, (self.B + 1,))
@@ -241,18 +243,24 @@ class PagedVerifyStep:
                 not K.shape == V.shape == (n, self.Hkv, self.head_dim):
             raise ValueError("Q, K and V must be rows of the same tokens and type, of the step's heads")
         T = max(1, min(n, self.max_len) if longest is None else min(longest, self.max_len))
-        length = cu_seqlens[1:] - cu_seqlens[:-1]
-        keep = length <= 0
+        # A prompt's rows lie between all offsets before and all behind it, within the given rows: so every
+        # place of it is there, and no other's. (Any other is refused by its count of -1.)
+        first, end = cu_seqlens[:-1], cu_seqlens[1:]
+        before, behind = cu_seqlens.cummax(0).values, cu_seqlens.flip(0).cummin(0).values.flip(0)
+        fits = (first >= 0) & (first <= end) & (end <= n) & (first == before[:-1]) & (end == behind[1:])
+        length = torch.where(fits, end - first, -1)
+        keep = length == 0
         start = torch.where(keep, self.length, 0)
-        new = torch.where(keep, 0, torch.where(length <= T, length, -1)).to(torch.int32)
+        new = torch.where(length <= T, length, -1)
         slots = self.pages.reserve(start, new, T, status=st)
         # The request and the place of each row; rows outside the prompts have none.
         row = torch.arange(n, dtype=torch.int32, device=K.device)
-        b = (torch.searchsorted(cu_seqlens, row, right=True) - 1).clamp(0, self.B - 1)
-        at = row - cu_seqlens[b]
+        b = (torch.searchsorted(before, row, right=True) - 1).clamp(0, self.B - 1)
+        at = row - first[b]
         inside = (at >= 0) & (at < length[b])
         slots = torch.where(inside & (at < T), slots[b, at.clamp(0, T - 1).long()], -1)
-        given = (slots.new_zeros(self.B).index_add_(0, b, (slots >= 0).to(torch.int32)) > 0) & ~keep
+        # Only a prompt that all rows of are cached is its request's.
+        given = (slots.new_zeros(self.B).index_add_(0, b, (slots >= 0).to(torch.int32)) == length) & ~keep
         positions = torch.where(inside & (at < self.max_len), at, -1)
         if self.rope is not None:
             self.cache.append_rope(K, V, slots, self.rope, positions, status=st)

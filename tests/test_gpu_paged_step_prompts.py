@@ -1,0 +1,84 @@
+"""PagedVerifyStep's ways in, where a call is not what it should be: prompts whose offsets do not fit their
+rows, rows in any layout and type, prompts beside a rotation, adapters of another number of requests. A
+request that is refused keeps its state to the byte."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import status_value, to_dev_bf16, to_dev_i32
+from oracle import kv4_oracle as KO
+from oracle import layer_oracle as LO
+from speculative_decoding_verification_w12_gb300 import synthetic as S
+from speculative_decoding_verification_w12_gb300 import w12
+from speculative_decoding_verification_w12_gb300.engine import PagedVerifyStep
+from test_gpu_paged_step_layer import B, D, HIDDEN, HKV, HQ, MAX, P, T, VOCAB, _f, _rows, _step
+
+pytestmark = pytest.mark.gpu
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+
+
+def _plain(n_pages=60):
+    """A step that takes queries and keys as they come."""
+    W = [S.weights_bf16((HQ + 2 * HKV) * D, HIDDEN, seed=5), S.weights_bf16(HIDDEN, HQ * D, seed=6), S.weights_bf16(VOCAB, HIDDEN, seed=7)]
+    return PagedVerifyStep(*(w12.pack(to_dev_bf16(w)) for w in W), B, T, HQ, HKV, D, n_pages=n_pages, page_size=P, max_len=MAX, top_k=2)
+
+
+def _made(rotated):
+    """(step, what its keys become by position)."""
+    if rotated:
+        step, _, turn_k = _step()
+        return step, turn_k
+    return _plain(), lambda x, pos: x
+
+
+def _qkv(n, dtype=F32, seed=1, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return [(torch.randn((n, h, D), generator=g, device="cuda") * scale).to(dtype) for h in (HQ, HKV, HKV)]
+
+
+def _state(step):
+    p = step.pages
+    return [t.clone() for t in (step.length, p.table, p.used, p.n_free, p.free, step.cache.pool)]
+
+
+def _holds(step, b, k, v):
+    """Request b's cached rows are those of the keys k and values v, fp32."""
+    for got, want in zip(_rows(step, b, len(k)), (k, v)):
+        np.testing.assert_array_equal(got, KO.values(*KO.quantise(want)))
+
+
+# Offsets, rows, the requests whose prompts are taken.
+OFFSETS = [([100, 200, 200, 200], 150, []), ([0, 50, 120, 120], 100, [0]), ([-5, 4, 10, 30], 30, [1, 2]), ([0, -3, 10, 30], 30, [2]),
+           ([0, 20, 10, 30], 30, []), ([0, 31, 10, 30], 30, []), ([0, 10, 31, 31], 30, [0]), ([10, 0, 20, 30], 30, [2]), ([-20, -10, 5, 30], 30, [2]),
+           ([5, 5, 9, 2 ** 31 - 1], 30, [1]), ([-2 ** 31, 2 ** 31 - 1, 7, 9], 30, []), ([40, 45, 50, 60], 30, []), ([3, 10, 10, 30], 30, [0, 2])]
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("cu,n,taken", OFFSETS, ids=str)
+def test_offsets_that_do_not_fit_the_rows(cu, n, taken, rotated):
+    """A prompt with a place outside the rows, or that shares rows with another, is not cached; its request
+    keeps its length, its pages and what they hold. The others are taken as ever."""
+    step, turn = _made(rotated)
+    first = [20, 7, 33]
+    q, k, v = _qkv(60, seed=2)
+    step.prompt(q, k, v, to_dev_i32(np.concatenate([[0], np.cumsum(first)])))
+    assert status_value(step.status) == 0
+    before, rows = _state(step), [_rows(step, b, x) for b, x in enumerate(first)]
+    q, k, v = _qkv(n)
+    step.prompt(q, k, v, to_dev_i32(cu))
+    good = all(a <= e for a, e in zip(cu, cu[1:])) and cu[0] >= 0 and cu[-1] <= n
+    assert status_value(step.status) == (0 if good else 1)
+    want = [cu[b + 1] - cu[b] if b in taken else first[b] for b in range(B)]
+    assert step.length.tolist() == want
+    assert step.pages.used.tolist() == [-(-x // P) for x in want]
+    assert int(step.pages.n_free[0]) == 60 - sum(-(-x // P) for x in want)
+    for b in range(B):
+        if b in taken:
+            a, e = cu[b], cu[b + 1]
+            _holds(step, b, turn(_f(k[a:e]), np.arange(e - a)), _f(v[a:e]))
+        else:
+            assert torch.equal(step.pages.table[b], before[1][b])
+            for got, old in zip(_rows(step, b, first[b]), rows[b]):
+                np.testing.assert_array_equal(got, old)
+    if not taken:
+        assert all(torch.equal(x, y) for x, y in zip(_state(step), before))
