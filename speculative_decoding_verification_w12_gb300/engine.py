@@ -242,6 +242,8 @@ class PagedVerifyStep:
         if not Q.dtype == K.dtype == V.dtype or Q.shape != (n, self.Hq, self.head_dim) or \
                 not K.shape == V.shape == (n, self.Hkv, self.head_dim):
             raise ValueError("Q, K and V must be rows of the same tokens and type, of the step's heads")
+        for x, what in ((Q, "Q"), (K, "K"), (V, "V")):
+            w12._head_rows(x, what)   # (refused before the requests' pages change)
         T = max(1, min(n, self.max_len) if longest is None else min(longest, self.max_len))
         # A prompt's rows lie between all offsets before and all behind it, within the given rows: so every
         # place of it is there, and no other's. (Any other is refused by its count of -1.)

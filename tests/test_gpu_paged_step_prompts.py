@@ -82,3 +82,29 @@ def test_offsets_that_do_not_fit_the_rows(cu, n, taken, rotated):
                 np.testing.assert_array_equal(got, old)
     if not taken:
         assert all(torch.equal(x, y) for x, y in zip(_state(step), before))
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("what", ["type", "type of one", "layout", "host", "offsets"])
+def test_rows_that_are_refused_change_nothing(what, rotated):
+    step, _ = _made(rotated)
+    q, k, v = _qkv(60, seed=2)
+    cu = to_dev_i32([0, 20, 27, 60])
+    step.prompt(q, k, v, cu)
+    torch.cuda.synchronize()
+    before = _state(step)
+    q, k, v = _qkv(30)
+    cu = to_dev_i32([0, 10, 10, 30])                       # fewer pages than the requests have
+    if what == "type":
+        q, k, v = (x.double() for x in (q, k, v))
+    elif what == "type of one":
+        v = v.bfloat16()
+    elif what == "layout":
+        k = k.transpose(1, 2).contiguous().transpose(1, 2)
+    elif what == "host":
+        v = v.cpu()
+    else:
+        cu = cu[:3]
+    with pytest.raises((ValueError, TypeError)):
+        step.prompt(q, k, v, cu)
+    assert all(torch.equal(x, y) for x, y in zip(_state(step), before)) and status_value(step.status) == 0
