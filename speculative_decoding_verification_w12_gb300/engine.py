@@ -158,6 +158,14 @@ class VerifyStep:
         return self._out_host.numel() * 4
 
 
+def _attendable(x: torch.Tensor) -> torch.Tensor:
+    """Rows [n, H, d] of a 16-bit type where prompt attention takes them: at 16-byte boundaries,
+    strides above zero; as they are or copied."""
+    token, head, _ = x.stride()
+    fits = x.data_ptr() % 16 == 0 and token > 0 and head > 0 and token % 8 == 0 and head % 8 == 0
+    return x if fits else x.clone(memory_format=torch.contiguous_format)
+
+
 class PagedVerifyStep:
     """A tree-verify step of one target layer over a paged 4-bit cache.
 
@@ -269,7 +277,7 @@ class PagedVerifyStep:
             Q, K = self.rope.run(Q, K, positions, status=st)
         else:
             self.cache.append(K, V, slots, status=st)
-        half = [x.to(torch.bfloat16) for x in (Q, K, V)]
+        half = [_attendable(x.to(torch.bfloat16)) for x in (Q, K, V)]
         self.length.copy_(torch.where(given, length, self.length))
         return w12.prompt_attention(*half, cu_seqlens, status=st)
 

@@ -108,3 +108,28 @@ def test_rows_that_are_refused_change_nothing(what, rotated):
     with pytest.raises((ValueError, TypeError)):
         step.prompt(q, k, v, cu)
     assert all(torch.equal(x, y) for x, y in zip(_state(step), before)) and status_value(step.status) == 0
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("how", ["base", "token stride", "head stride"])
+def test_rows_at_any_address(how, dtype, rotated):
+    """Views that start between 16-byte boundaries, or whose strides are no whole number of them."""
+    q, k, v = _qkv(50, dtype)
+
+    def view(x):
+        n, h, d = x.shape
+        token, head, first = {"base": (h * d, d, 3), "token stride": (h * d + 5, d, 0), "head stride": (h * (d + 1), d + 1, 0)}[how]
+        wide = torch.zeros(n * token + 8, dtype=dtype, device="cuda")
+        y = wide.as_strided((n, h, d), (token, head, 1), first)
+        y.copy_(x)
+        return y
+    cu, out = to_dev_i32([0, 20, 20, 50]), []
+    for rows in ((q, k, v), [view(x) for x in (q, k, v)]):
+        step, _ = _made(rotated)
+        O = step.prompt(*rows, cu)
+        assert status_value(step.status) == 0 and step.length.tolist() == [20, 0, 30]
+        out.append((O, _rows(step, 0, 20), _rows(step, 2, 30)))
+    assert torch.equal(out[0][0], out[1][0])
+    for x, y in zip(out[0][1] + out[0][2], out[1][1] + out[1][2]):
+        np.testing.assert_array_equal(x, y)
