@@ -238,8 +238,8 @@ class PagedVerifyStep:
         prompt, at positions 0, 1, ...; a request without rows stays as it is. longest
         bounds the prompts' lengths (default: the rows, or max_len). Queries and keys are
         normed and rotated where the step does that, keys and values are cached, and the
-        causal attention over them, before they are quantised, comes back as bf16 [n, Hq,
-        head_dim]. A prompt that there are no pages for, or that is too long, is attended
+        causal attention over them, before they are quantised (in bf16, fp16 rows without a
+        rotation in fp16), comes back as bf16 [n, Hq, head_dim]. A prompt that there are no pages for, or that is too long, is attended
         over but not cached: its request stays as it was, and the status word says so. (Rows
         past max_len have no position: with a rotation their queries and keys are zeros.)
         A prompt whose offsets decrease, leave the rows or share rows with another's is not
@@ -277,9 +277,12 @@ class PagedVerifyStep:
             Q, K = self.rope.run(Q, K, positions, status=st)
         else:
             self.cache.append(K, V, slots, status=st)
-        half = [_attendable(x.to(torch.bfloat16)) for x in (Q, K, V)]
+        # fp16 rows go in as they are. (Rotated they are bf16, like all rotated rows of the step: a pair's
+        # larger value may grow by sqrt 2, which fp16 has no room for at the end of its range.)
+        to = Q.dtype if Q.dtype is torch.float16 and self.rope is None else torch.bfloat16
+        half = [_attendable(x.to(to)) for x in (Q, K, V)]
         self.length.copy_(torch.where(given, length, self.length))
-        return w12.prompt_attention(*half, cu_seqlens, status=st)
+        return w12.prompt_attention(*half, cu_seqlens, status=st).to(torch.bfloat16)
 
     def run(self, X: torch.Tensor, parents: torch.Tensor, draft: torch.Tensor,
             adapter: torch.Tensor | None = None) -> dict:

@@ -133,3 +133,13 @@ def test_rows_at_any_address(how, dtype, rotated):
     assert torch.equal(out[0][0], out[1][0])
     for x, y in zip(out[0][1] + out[0][2], out[1][1] + out[1][2]):
         np.testing.assert_array_equal(x, y)
+
+
+def test_fp16_prompts_are_attended_over_as_they_are():
+    """Without a rotation nothing is rounded on the way to the scores."""
+    step = _plain()
+    q, k, v = _qkv(120, F16, scale=2.0)
+    cu = to_dev_i32([0, 50, 50, 120])
+    O = step.prompt(q, k, v, cu)
+    assert O.dtype is BF16
+    assert torch.equal(O, w12.prompt_attention(q, k, v, cu).to(BF16))
