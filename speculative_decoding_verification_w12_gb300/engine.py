@@ -216,7 +216,7 @@ class PagedVerifyStep:
         """Cache the first length[b] rows of K, V [B, n, Hkv, head_dim] (one prompt a request).
 
         length int32 [B]: a request with -1 stays as it is, 0 ends one and frees its
-        pages. A prompt that there are no pages for, or that is longer than n or
+        pages. Keys are normed and rotated by their place where the step does that. A prompt that there are no pages for, or that is longer than n or
         max_len, leaves its request as it was and sets the status word.
         """
         n = K.shape[1]
@@ -225,7 +225,12 @@ class PagedVerifyStep:
         start = torch.where(keep, self.length, 0)
         new = torch.where(keep, 0, torch.where(length <= self.max_len, length, -1))
         slots = self.pages.reserve(start, new, n, status=self.status)
-        self.cache.append(K.flatten(0, 1), V.flatten(0, 1), slots, status=self.status)
+        rows = K.flatten(0, 1), V.flatten(0, 1), slots.view(-1)
+        if self.rope is not None:
+            place = torch.arange(n, dtype=torch.int32, device=K.device).expand(self.B, n)
+            self.cache.append_rope(*rows, self.rope, torch.where(slots >= 0, place, -1).view(-1), status=self.status)
+        else:
+            self.cache.append(*rows, status=self.status)
         given = (new == 0) | (slots[:, :1] >= 0).any(1)
         self.length.copy_(torch.where(given & ~keep, length, self.length))
 

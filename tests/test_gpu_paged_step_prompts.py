@@ -143,3 +143,27 @@ def test_fp16_prompts_are_attended_over_as_they_are():
     O = step.prompt(q, k, v, cu)
     assert O.dtype is BF16
     assert torch.equal(O, w12.prompt_attention(q, k, v, cu).to(BF16))
+
+
+def test_prefill_of_a_step_with_a_rotation():
+    """Keys are normed and rotated as those of run() and prompt(); running requests beside them stay."""
+    step, _, turn = _step()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    K, V = (torch.randn((B, 40, HKV, D), generator=g, device="cuda") for _ in range(2))
+    step.prefill(K, V, to_dev_i32([40, 0, 13]))
+    assert status_value(step.status) == 0 and step.length.tolist() == [40, 0, 13]
+    for b, n in ((0, 40), (2, 13)):
+        _holds(step, b, turn(_f(K[b, :n]), np.arange(n)), _f(V[b, :n]))
+    other = _step()[0]
+    rows = [torch.cat([x[0, :40], x[2, :13]]) for x in (K, V)]
+    other.prompt(torch.zeros((53, HQ, D), device="cuda"), *rows, to_dev_i32([0, 40, 40, 53]))
+    for b, n in ((0, 40), (2, 13)):
+        for x, y in zip(_rows(step, b, n), _rows(other, b, n)):
+            np.testing.assert_array_equal(x, y)
+    step.prefill(K.flip(0), V.flip(0), to_dev_i32([-1, 30, -1]))
+    assert status_value(step.status) == 0 and step.length.tolist() == [40, 30, 13]
+    _holds(step, 1, turn(_f(K[1, :30]), np.arange(30)), _f(V[1, :30]))
+    _holds(step, 0, turn(_f(K[0]), np.arange(40)), _f(V[0]))
+    step.status.zero_()
+    step.prefill(K, V, to_dev_i32([41, -1, -1]))           # more than the rows
+    assert status_value(step.status) == 1 and step.length.tolist() == [40, 30, 13]
