@@ -302,9 +302,11 @@ class PagedVerifyStep:
         """
         B, T, M, d = self.B, self.T, self.M, self.head_dim
         st = self.status
-        # (A negative count is refused: the request keeps its pages and gets slots of -1.)
         if adapter is not None and not self.adapters:
             raise ValueError("the step has no adapters")
+        if adapter is not None and (adapter.dtype is not torch.int32 or adapter.shape != (B,) or not adapter.is_cuda):
+            raise ValueError(f"adapter must be an int32 CUDA tensor of the {B} requests")
+        # (A negative count is refused: the request keeps its pages and gets slots of -1.)
         nodes = torch.where(self.length <= self.max_len - T, self.nodes, -1)
         slots = self.pages.reserve(self.length, nodes, T, status=st)
         served = slots[:, 0] >= 0

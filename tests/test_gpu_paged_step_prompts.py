@@ -167,3 +167,20 @@ def test_prefill_of_a_step_with_a_rotation():
     step.status.zero_()
     step.prefill(K, V, to_dev_i32([41, -1, -1]))           # more than the rows
     assert status_value(step.status) == 1 and step.length.tolist() == [40, 30, 13]
+
+
+def test_adapters_of_another_number_of_requests_are_refused():
+    step = _step()[0]
+    step.prompt(*_qkv(60, seed=2), to_dev_i32([0, 20, 27, 60]))
+    torch.cuda.synchronize()
+    before = _state(step)
+    X, tree = torch.zeros((B * T, HIDDEN), dtype=BF16, device="cuda"), to_dev_i32(np.tile(np.arange(-1, T - 1), (B, 1)))
+    for bad in (to_dev_i32([1]), to_dev_i32([[1], [0], [2]]), to_dev_i32([0, 1]), to_dev_i32([0, 1, 2, 0]), to_dev_i32([0, 1, 2]).long(),
+                torch.zeros(B, dtype=torch.int32), torch.zeros((), dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError):
+            step.run(X, tree, torch.zeros_like(tree), adapter=bad)
+        assert all(torch.equal(x, y) for x, y in zip(_state(step), before)) and status_value(step.status) == 0
+    # A strided one of the right number is as good as any.
+    wide = to_dev_i32([[2, 9], [-1, 9], [0, 9]])
+    a, b = (_step()[0].run(X + 1, tree, torch.zeros_like(tree), adapter=x) for x in (wide[:, 0], wide[:, 0].contiguous()))
+    assert all(torch.equal(a[k], b[k]) for k in a)
