@@ -48,9 +48,15 @@ struct RopeParams {
   int32_t* status;
 };
 
-// A sum of fp32 numbers as a pair: hi + lo is the sum to about 2^-40 of it.
+// A sum of fp32 numbers as a pair, hi + lo. add() is off by 2^-48 of it where lo is small beside hi;
+// join() makes that so, exactly: lo is then at most half a last place of hi.
 struct Sum2 {
   float hi, lo;
+  __device__ __forceinline__ void join() {
+    const float s = __fadd_rn(hi, lo);
+    lo = __fsub_rn(lo, __fsub_rn(s, hi));
+    hi = s;
+  }
   __device__ __forceinline__ void add(float x) {
     const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
@@ -79,8 +85,11 @@ __device__ __forceinline__ float sum_squares(const float (&x)[16]) {
 }
 
 // The same as a pair, from that sum `rough`, which is finite. Each square is cut in two at 2^-16
-// of the whole: by a fused addition of c = 1.5 2^m (whose last place is 2^(m - 23)) the upper
-// parts are whole multiples of it, and their sums exact in any order; the rests are small.
+// of the whole (of 2^e, the power of two below it): by a fused addition of c = 1.5 2^m (whose last
+// place is 2^(m - 23)) the upper parts are whole multiples of it, and their sums exact in any order.
+// The rests are at most 2^(e - 17) each, 2^(e - 10) together, so lo may be 2^-10 of hi. Their roundings: 128
+// of a rest, in units of 2^(e - 41), and in the sums 35 for each lane's two runs of eight and 16 to join
+// them (8 lanes), 3 times 128 over the lanes: 1200 in all, 2^-30.7 of the whole, half of that of the factor.
 template <int kRow>
 __device__ __forceinline__ Sum2 sum_squares2(const float (&x)[16], float rough) {
   const float c = __uint_as_float((__float_as_uint(rough) & 0x7F800000u) + (7u << 23) + 0x400000u);
@@ -95,8 +104,8 @@ __device__ __forceinline__ Sum2 sum_squares2(const float (&x)[16], float rough) 
   return Sum2{over_row<kRow>(__fadd_rn(hi.x, hi.y)), over_row<kRow>(__fadd_rn(lo.x, lo.y))};
 }
 
-// fp32(1 / sqrt(m.hi + m.lo)): one step of Newton's iteration from the approximation, its
-// residual 1 - m r^2 exact to about 2^-46.
+// fp32(1 / sqrt(m.hi + m.lo)), m joined: one step of Newton's iteration from the approximation, which
+// is off by 2^-22 or so: the step leaves 2^-60 of r. Its residual 1 - m r^2 (2^-21 at most) is exact to 2^-43.
 __device__ __forceinline__ float rsqrt_of(Sum2 m) {
   const float r = rsqrtf(m.hi);
   const float p = __fmul_rn(r, r), pe = fmaf(r, r, -p);
@@ -107,7 +116,9 @@ __device__ __forceinline__ float rsqrt_of(Sum2 m) {
   return fmaf(r, e * fmaf(0.375f, e, 0.5f), r);
 }
 
-// The factor of a row's norm; kNearest: the fp32 value next to the exact one. A row whose squares
+// The factor of a row's norm; kNearest: the fp32 value next to the exact one (before its rounding it is
+// off by 2^-31.7 of itself, less than 2^-7 of the distance of two fp32 values, which is 2^-24 or more of
+// them: so near the middle of two it is either). A row whose squares
 // leave the fp32 range (values past 2^51) is made 2^76 smaller first: x then has what the factor
 // is for, and the squares' sum is at most 2^111, below the 2^121 where c has no exponent left.
 template <int kD, bool kNearest>
@@ -125,7 +136,7 @@ __device__ __forceinline__ float norm_factor(float (&x)[16], float eps) {
   Sum2 s;
   if constexpr (kNearest) {
     s = sum_squares2<kRow>(x, rough < INFINITY ? rough : 0.f);
-    s.add(0.f);
+    s.join();
     s.hi *= 1.f / kD;
     s.lo *= 1.f / kD;
     s.add(eps);
