@@ -538,10 +538,11 @@ int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const 
  * or 128, Hq / Hkv <= 128, total < 2^31 - 256. Sequences of no rows are fine. One with offsets
  * out of [0, total], or decreasing ones, sets W12_ERR_ARG and is taken as empty (sequences
  * that share rows write either's result). Rows that a row does not see have no part in it,
- * whatever they hold. Scores, softmax and sums are fp32; a weight meets the values rounded to
+ * whatever they hold; a value that is not finite makes the outputs that see it so, whatever its
+ * weight. Scores, softmax and sums are fp32; a weight meets the values rounded to
  * their type (bf16: 2^-8 of itself, fp16: 2^-11 of itself or 2^-25 of the row's largest). A
- * score of -inf weighs nothing; a row with no other is zeros. A sequence's bits do not depend
- * on the call's others. No workspace. Device-side errors besides: W12_ERR_TIMEOUT. Returns
+ * score of -inf weighs nothing; a row with no other is zeros (of finite values). A sequence's bits
+ * do not depend on the call's others. No workspace. Device-side errors besides: W12_ERR_TIMEOUT. Returns
  * W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_UNSUPPORTED or W12_ERR_CUDA. */
 int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_stride, const void* K, int64_t k_token_stride,
                          int64_t k_head_stride, const void* V, int64_t v_token_stride, int64_t v_head_stride, int dtype,

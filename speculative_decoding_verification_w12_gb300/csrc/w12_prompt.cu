@@ -104,7 +104,9 @@ struct Item {
   int first;   // token of the buffer that the first tile begins with
   int t0;      // its place in the sequence
   int len;     // tokens of the sequence
-  int head;    // kv head; -1: no more items
+  int head;    // kv head; kSecond in it: the one tile is the second of a pair; -1: no more items
+  static constexpr int kSecond = 1 << 16;
+  __device__ __forceinline__ int kv() const { return head & (kSecond - 1); }
 };
 
 struct Params {
@@ -132,14 +134,15 @@ __device__ __forceinline__ void load_box(void* dst, const CUtensorMap* map, int 
 }
 
 // Key blocks of a tile that begins at token t0 (none past the sequence's end), and the first
-// of them that some row of the tile does not see whole.
+// of them that some row of the item or, of an item of one tile, of its pair of tiles does not see whole: what
+// is taken out of V then hangs on the sequence alone.
 template <int kKeys>
 __device__ __forceinline__ int blocks_of(int t0, int tpt, int len) {
   return t0 >= len ? 0 : (min(t0 + tpt, len) + kKeys - 1) / kKeys;
 }
 template <int kKeys>
-__device__ __forceinline__ int first_cut(int t0) {
-  return (t0 + 1) / kKeys;
+__device__ __forceinline__ int first_cut(const Item& it, int tpt) {
+  return (it.t0 + 1 - ((it.head & Item::kSecond) ? tpt : 0)) / kKeys;
 }
 
 // Walks the items in their order: groups of sequences, whose keys and values stay in the L2 cache
@@ -541,19 +544,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n0 = blocks_of<C::kKeys>(it.t0, P.tpt, it.len), n1 = blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len);
         const int n = max(n0, n1);
         for (int j = 0; ok && j < n; ++j) {
-          ok = stage(&tm_k, it.head, seq + j * C::kKeys);
+          ok = stage(&tm_k, it.kv(), seq + j * C::kKeys);
           if (j == 0) {
             for (int i = 0; ok && i < (n1 ? 2 : 1); ++i) {
               if (q_issued[i] > 0) ok = wait(&q_empty[i], uint32_t(q_issued[i] - 1) & 1u);
               if (!ok) break;
               mbar_arrive_expect_tx(&q_full[i], uint32_t(kD * 2 * P.G * P.tpt));
               for (int h = 0; h < C::kHalves; ++h)
-                load_box(smem + uint32_t(i) * C::kQTile + h * C::kQHalf, &tm_q, 64 * h, it.head * P.G, it.first + i * P.tpt,
+                load_box(smem + uint32_t(i) * C::kQTile + h * C::kQHalf, &tm_q, 64 * h, it.kv() * P.G, it.first + i * P.tpt,
                          &q_full[i]);
               ++q_issued[i];
             }
           }
-          if (ok) ok = stage(&tm_v, it.head, seq + j * C::kKeys);
+          if (ok) ok = stage(&tm_v, it.kv(), seq + j * C::kKeys);
         }
       }
       ok = __shfl_sync(0xFFFFFFFFu, int(ok), 0);
@@ -644,7 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int grid = int(gridDim.x), me = int(blockIdx.x);
     int skip = me;
     for (int k = 0;; ++k) {
-      const Item it = walk.next(skip);
+      Item it = walk.next(skip);
+      if (P.step == P.tpt && it.head >= 0 && (walk.level & 1)) it.head |= Item::kSecond;
       // Rounds alternate in direction: place `me` of even rounds, `grid - 1 - me` of odd ones.
       // (walk.next leaves the walk on the item: the next one is one place more on.)
       skip = ((k & 1) ? 2 * me : 2 * (grid - 1 - me)) + 1;
@@ -662,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it;
     for (int k = 0; ok && get_item(k, it); ++k) {
       const int all = max(blocks_of<C::kKeys>(it.t0, P.tpt, it.len), blocks_of<C::kKeys>(it.t0 + P.tpt, P.tpt, it.len));
-      const int cut = first_cut<C::kKeys>(it.t0);
+      const int cut = first_cut<C::kKeys>(it, P.tpt);
       uint4* notes = bad + (k % kBadItems) * kMostCut;
       // (V blocks that the diagonal does not cut are waited for and passed on too: the ring cannot pass these warps.)
       for (int j = 0; ok && j < all; ++j, place += 2) {
@@ -720,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = i ? n1 : n0;
       const int t = t0 + row_t;                     // the row's token, in its sequence
       const bool valid = row_t < P.tpt && t < it.len;
-      const int cut = first_cut<C::kKeys>(it.t0);   // (from here on values may have been taken out)
+      const int cut = first_cut<C::kKeys>(it, P.tpt);   // (from here on values may have been taken out)
+      const int masked = (it.t0 + 1) / C::kKeys;    // (and from here on the item's first rows do not see all keys)
       float m = -INFINITY, l = 0.f;
       // A wait is one vote of the warp a block (what follows is warp-collective): barriers are
       // looked at early, and waited for only where that has not shown them complete.
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_read[i]);
-        if (j >= cut) {
+        if (j >= masked) {
           const int see = t - j * C::kKeys + 1;     // keys of the block that the row sees
 #pragma unroll
           for (int x = 0; x < C::kKeys; ++x)
@@ -792,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Of its own row a lane would store 32 bytes at a time, a line each; the lines are what the
         // stores take. So half rows change lanes on the way, through P's columns: four lanes have a
         // line of a row then, an instruction eight lines (2,400 -> 1,700 cycles an item of short prompts).
-        uint16_t* tile = static_cast<uint16_t*>(P.O) + (int64_t(it.first - it.t0 + t0) * P.Hq + it.head * P.G) * kD;
+        uint16_t* tile = static_cast<uint16_t*>(P.O) + (int64_t(it.first - it.t0 + t0) * P.Hq + it.kv() * P.G) * kD;
         const int end = min(P.tpt, it.len - t0);      // tokens
 #pragma unroll
         for (int ch = 0; ch < kD / 64; ++ch) {
@@ -826,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xFFFFFFFFu, odd && valid)) {
           __syncwarp();
           uint16_t* out = tile + int64_t(row_t * P.Hq + row_h) * kD;
-          if (odd && valid) add_taken_out<C::kKeys, kD, kBf16>(P, out, odd, cut, t, it.first - it.t0, it.head);
+          if (odd && valid) add_taken_out<C::kKeys, kD, kBf16>(P, out, odd, cut, t, it.first - it.t0, it.kv());
         }
       }
       blocks += n;
