@@ -122,6 +122,7 @@ struct Params {
   uint32_t inv_g;              // a row's token is row inv_g / 2^16
   float c;                     // scale log2(e)
   uint64_t limit_ns;
+  uint32_t sleep_ns;           // longest sleep of a wait between looks at its bound
 };
 
 // A box of (dims from x on, head y, token z on) rows; the maps' fourth extent is 1.
@@ -497,15 +498,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Everything below reads what the previous kernel on the stream wrote.
   grid_dep_wait();
 
+  // (Asleep for no longer than its bound at a time, as in mbar_wait_asleep: 64 x 300 57.3 us, with that one 57.9.)
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_hint(bar, parity, P.sleep_ns)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t i = 0; i < 0x80000000u; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if ((i & 63u) == 63u) {
-        if (*abort_flag) return false;
-        if (globaltimer_ns() - t0 > lim) break;
-      }
+      if (mbar_try_wait_hint(bar, parity, P.sleep_ns)) return true;
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > lim) break;
     }
     set_status(P.status, W12_ERR_TIMEOUT);
     *abort_flag = 1;
@@ -933,6 +933,7 @@ int w12_prompt_attention(const void* Q, int64_t q_token_stride, int64_t q_head_s
   P.room = kGroupBytes / (4 * Hkv * head_dim) + 1;
   P.c = float(double(scale) * 1.4426950408889634);
   P.limit_ns = wait_limit_ns();
+  P.sleep_ns = sleep_ns(P.limit_ns);
   const bool bf16 = dtype == W12_BF16;
   CUtensorMap q, k, v;
   const int keys = head_dim == 128 ? Cfg<128>::kKeys : Cfg<64>::kKeys;

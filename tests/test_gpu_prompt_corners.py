@@ -1,10 +1,11 @@
 """Prompt attention where a call's form must not show: values that are not finite beside weights that
-vanish."""
+vanish, and waits that expire."""
 import pytest
 import torch
 
 from gpu_util import new_status, status_value, to_dev_i32
 from speculative_decoding_verification_w12_gb300 import w12
+from test_gpu_expired_waits import short_waits, until_expired  # noqa: F401
 from test_gpu_prompt_attention import BF16, F16, _offsets, _rows
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +41,16 @@ def test_values_beside_weights_that_vanish(G, d, dtype):
         sees = ((at[None] >= start[:, None]) & (at[None] <= rows[:, None])).any(1)
         assert torch.equal(torch.isfinite(out[..., 5 + i]).all(1), ~sees) and torch.equal(torch.isfinite(out[..., 5 + i]).any(1), ~sees)
     assert torch.isfinite(out[..., 8:]).all()
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,d,dtype", [([1900, 2000], 40, 8, 128, BF16), ([6000], 32, 8, 64, F16), ([500] * 40, 16, 8, 64, BF16)])
+def test_a_bound_of_a_microsecond_expires(short_waits, lens, Hq, Hkv, d, dtype):  # noqa: F811
+    q, k, v = _rows(sum(lens), Hq, Hkv, d, dtype, 6)
+    cu = to_dev_i32(_offsets(lens))
+    w12.set_wait_limit_us(2000000)
+    want = w12.prompt_attention(q, k, v, cu)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        until_expired(lambda st: w12.prompt_attention(q, k, v, cu, status=st), lambda: None)
+        st = new_status()
+        assert torch.equal(w12.prompt_attention(q, k, v, cu, status=st), want) and status_value(st) == 0
