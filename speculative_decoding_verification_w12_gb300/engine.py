@@ -219,18 +219,22 @@ class PagedVerifyStep:
         pages. Keys are normed and rotated by their place where the step does that. A prompt that there are no pages for, or that is longer than n or
         max_len, leaves its request as it was and sets the status word.
         """
-        n = K.shape[1]
+        n, d = K.shape[1], self.head_dim
+        if not K.shape == V.shape == (self.B, n, self.Hkv, d) or K.dtype is not V.dtype:
+            raise ValueError("K and V must be rows of the same type, of every request and the step's heads")
+        rows = K.flatten(0, 1), V.flatten(0, 1)
+        for x, what in zip(rows, "KV"):
+            w12._head_rows(x, what)   # (refused before the requests' pages change)
         keep = length < 0
         # (A kept request asks for no more than it has; a count of -1 is refused.)
         start = torch.where(keep, self.length, 0)
         new = torch.where(keep, 0, torch.where(length <= self.max_len, length, -1))
         slots = self.pages.reserve(start, new, n, status=self.status)
-        rows = K.flatten(0, 1), V.flatten(0, 1), slots.view(-1)
         if self.rope is not None:
             place = torch.arange(n, dtype=torch.int32, device=K.device).expand(self.B, n)
-            self.cache.append_rope(*rows, self.rope, torch.where(slots >= 0, place, -1).view(-1), status=self.status)
+            self.cache.append_rope(*rows, slots.view(-1), self.rope, torch.where(slots >= 0, place, -1).view(-1), status=self.status)
         else:
-            self.cache.append(*rows, status=self.status)
+            self.cache.append(*rows, slots.view(-1), status=self.status)
         given = (new == 0) | (slots[:, :1] >= 0).any(1)
         self.length.copy_(torch.where(given & ~keep, length, self.length))
 

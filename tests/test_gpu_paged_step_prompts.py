@@ -169,6 +169,33 @@ def test_prefill_of_a_step_with_a_rotation():
     assert status_value(step.status) == 1 and step.length.tolist() == [40, 30, 13]
 
 
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("what", ["type", "type of one", "layout", "host", "heads", "requests", "rows"])
+def test_prefilled_rows_that_are_refused_change_nothing(what, rotated):
+    step, _ = _made(rotated)
+    step.prompt(*_qkv(60, seed=2), to_dev_i32([0, 20, 27, 60]))
+    torch.cuda.synchronize()
+    before = _state(step)
+    K, V = (torch.randn((B, 10, HKV, D), device="cuda") for _ in range(2))
+    if what == "type":
+        K, V = K.double(), V.double()
+    elif what == "type of one":
+        V = V.bfloat16()
+    elif what == "layout":
+        K = K.transpose(2, 3).contiguous().transpose(2, 3)
+    elif what == "host":
+        V = V.cpu()
+    elif what == "heads":
+        K, V = K[:, :, :1], V[:, :, :1]
+    elif what == "requests":
+        K, V = K[:2], V[:2]
+    else:
+        V = V[:, :9]
+    with pytest.raises((ValueError, TypeError)):
+        step.prefill(K, V, to_dev_i32([10, 0, 3]))
+    assert all(torch.equal(x, y) for x, y in zip(_state(step), before)) and status_value(step.status) == 0
+
+
 def test_adapters_of_another_number_of_requests_are_refused():
     step = _step()[0]
     step.prompt(*_qkv(60, seed=2), to_dev_i32([0, 20, 27, 60]))
