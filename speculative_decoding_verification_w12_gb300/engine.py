@@ -264,24 +264,22 @@ class PagedVerifyStep:
         T = max(1, min(n, self.max_len) if longest is None else min(longest, self.max_len))
         # A prompt's rows lie between all offsets before and all behind it, within the given rows: so every
         # place of it is there, and no other's. (Any other is refused by its count of -1.)
-        first, end = cu_seqlens[:-1], cu_seqlens[1:]
+        first, inside = cu_seqlens[:-1], cu_seqlens.clamp(0, n)
         before, behind = cu_seqlens.cummax(0).values, cu_seqlens.flip(0).cummin(0).values.flip(0)
-        fits = (first >= 0) & (first <= end) & (end <= n) & (first == before[:-1]) & (end == behind[1:])
-        length = torch.where(fits, end - first, -1)
-        keep = length == 0
-        start = torch.where(keep, self.length, 0)
-        new = torch.where(length <= T, length, -1)
-        slots = self.pages.reserve(start, new, T, status=st)
-        # The request and the place of each row; rows outside the prompts have none.
+        fits = (inside == before) & (inside == behind)
+        length = torch.where(fits[:-1] & fits[1:], cu_seqlens[1:] - first, -1)
+        start = torch.where(length == 0, self.length, 0)
+        places = self.pages.reserve(start, torch.where(length <= T, length, -1), T, status=st)
+        # The request and the place of each row. (Those of rows outside the prompts are below 0 or past a prompt's end,
+        # where there are no slots; a prompt has slots for all of its rows or for none.)
         row = torch.arange(n, dtype=torch.int32, device=K.device)
-        b = (torch.searchsorted(before, row, right=True) - 1).clamp(0, self.B - 1)
+        b = torch.searchsorted(before[1:-1], row, right=True, out_int32=True)
         at = row - first[b]
-        inside = (at >= 0) & (at < length[b])
-        slots = torch.where(inside & (at < T), slots[b, at.clamp(0, T - 1).long()], -1)
-        # Only a prompt that all rows of are cached is its request's.
-        given = (slots.new_zeros(self.B).index_add_(0, b, (slots >= 0).to(torch.int32)) == length) & ~keep
-        positions = torch.where(inside & (at < self.max_len), at, -1)
+        some = at >= 0
+        slots = torch.where(some & (at < T), places[b, at.clamp(0, T - 1)], -1)
+        given = places[:, 0] >= 0
         if self.rope is not None:
+            positions = torch.where(some & (at < self.max_len), at, -1)
             self.cache.append_rope(K, V, slots, self.rope, positions, status=st)
             Q, K = self.rope.run(Q, K, positions, status=st)
         else:
