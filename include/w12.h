@@ -534,8 +534,8 @@ int w12_tree_positions(const int32_t* prefix_len, const int32_t* parents, const 
  *   O[i, h, :] = sum_{j <= i} softmax_j(scale * Q[i, h, :] . K[j, h / (Hq/Hkv), :]) * V[j, ..]
  * over the rows j of i's sequence. dtype W12_BF16 or W12_F16, of Q, K, V and O; O
  * [total, Hq, head_dim] contiguous, its rows outside the sequences left as they are.
- * Element strides are positive multiples of 8, pointers 16-byte aligned (O: 32); head_dim 64
- * or 128, Hq / Hkv <= 128, total < 2^31 - 256. Sequences of no rows are fine. One with offsets
+ * Element strides are positive multiples of 8, pointers 16-byte aligned (O: 32), O apart from the
+ * inputs; head_dim 64 or 128, Hq / Hkv <= 128, total < 2^31 - 256, 0 < scale <= 1e30. Sequences of no rows are fine. One with offsets
  * out of [0, total], or decreasing ones, sets W12_ERR_ARG and is taken as empty (sequences
  * that share rows write either's result). Rows that a row does not see have no part in it,
  * whatever they hold; a value that is not finite makes the outputs that see it so, whatever its
@@ -569,7 +569,7 @@ typedef struct w12_adapters {
  * uses decides the order of the sums over K. B is finite (an infinity may come out as
  * NaN). The workspace needs no zero fill, holds nothing between calls, and follows the
  * other rules at the top. Errors: W12_ERR_ARG, W12_ERR_SHAPE, W12_ERR_WORKSPACE,
- * W12_ERR_UNSUPPORTED, W12_ERR_CUDA. */
+ * W12_ERR_UNSUPPORTED, W12_ERR_CUDA. (Prompts: a call for each 256 of their rows.) */
 size_t w12_lora_ws_bytes(int64_t M, int n_adapters, int rank);
 
 int w12_lora(const uint16_t* X, int64_t x_stride, int64_t M, const w12_adapters* adapters, const int32_t* ids, float* Y,

@@ -20,7 +20,7 @@
 // Long prompts are bound by the products: 8192 tokens of 40 / 8 heads of 128 take 381 us, 1800
 // TFLOP/s. At d = 64 a block of both tiles has 1024 cycles of products, 1024 of exponentials (4 a
 // warp's instruction) and about as many issue slots a scheduler, and takes 1950: 8192 tokens of 32 / 8
-// heads 226 us (1210 TFLOP/s). Short prompts are bound by the steps of an item (first scores,
+// heads 226 us (1210 TFLOP/s; all of these from L2). Short prompts are bound by the steps of an item (first scores,
 // masks, last products, outputs), 7,000 to 9,000 cycles for 2 to 4 blocks: 64 of up to 300 57 us.
 //
 // P enters O rounded to the type of V (bf16: 2^-8 of itself; fp16: 2^-11, or 2^-25 of the
@@ -29,7 +29,8 @@
 // Masked places may hold anything. Masked scores are replaced, not added to. A value that is
 // not finite would turn the zero weights of rows that do not see it into NaN: two warps look
 // through the V blocks that the diagonal cuts, take such values out of shared memory and
-// note their keys, and rows that see one add it at the end.
+// note their keys, and rows that see one add it at the end. (They pass on every V block, which P V waits
+// for, so that no warp can fall a turn of the ring behind.)
 //
 // Warps: 0-3 and 4-7 softmax and epilogue of the two tiles; 8 and 9 issue S, 10 and 11 P V of the
 // two tiles; 12 copies; 13 and 14 look through V; 15 finds the items. Each of the four

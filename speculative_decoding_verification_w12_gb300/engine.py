@@ -178,7 +178,9 @@ class PagedVerifyStep:
     rope (w12.Rope) norms and rotates queries and keys by position, a draft node's being
     its depth behind the committed tokens; without it they are taken as they come.
     adapters ({"qkv": w12.LoRA, "out": ..., "head": ...}, any of them) are added to
-    those products' rows, for the adapter of each request that run() is given.
+    those products' rows, for the adapter of each request that run() is given. (The rows
+    that prefill() and prompt() take are the caller's, adapters and all: w12.LoRA.run takes
+    256 of them a call.)
 
     A request that there are no pages for, or whose tokens would pass max_len, is
     not served by a step: its length, pages and cached rows stay as they are, and

@@ -952,7 +952,8 @@ def prompt_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_seqle
     head_dim], K and V [total, Hkv, head_dim], all bf16 or all fp16 (views with a
     contiguous last dimension and other strides that are multiples of 8), sequence b
     being rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (int32 [B + 1]). Returns O
-    [total, Hq, head_dim]; rows outside the sequences are left as they are."""
+    [total, Hq, head_dim]; rows outside the sequences are left as they are. The default
+    scale is head_dim ** -0.5; a given one must be above 0, out apart from Q, K and V."""
     half = (torch.bfloat16, torch.float16)
     q, qt, qh, Hq, (total, _, d) = _head_rows(Q, "Q", half)
     (k, kt, kh, Hkv, ks), (v, vt, vh, _, vs) = _head_rows(K, "K", half), _head_rows(V, "V", half)
@@ -996,7 +997,7 @@ class LoRA:
             stream=None) -> torch.Tensor:
         """Adds scale[a] * B[a] (A[a] X[m]), a = ids[m], to row m of Y fp32 [M, N], in
         place; X bf16 [M, K], ids int32 [M] (-1: no adapter). Rows of X and Y may be
-        padded. Returns Y."""
+        padded. Returns Y. Rows of a prompt go in calls of up to max_rows (256) each."""
         M = X.shape[0]
         if X.shape != (M, self.K) or X.dtype is not torch.bfloat16 or not X.is_cuda or X.stride(1) != 1:
             raise ValueError(f"X must be a bfloat16 CUDA tensor [M, {self.K}] with a contiguous last dimension")
