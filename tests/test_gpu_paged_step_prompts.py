@@ -84,6 +84,46 @@ def test_offsets_that_do_not_fit_the_rows(cu, n, taken, rotated):
         assert all(torch.equal(x, y) for x, y in zip(_state(step), before))
 
 
+def test_a_step_of_one_request():
+    W = [w12.pack(to_dev_bf16(S.weights_bf16(*x, seed=1))) for x in ((512, 128), (128, 256), (1024, 128))]
+    step = PagedVerifyStep(*W, 1, 4, 4, 2, D, n_pages=8, page_size=P, max_len=100)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn((60, h, D), generator=g, device="cuda") for h in (4, 2, 2))
+    for cu, length, code in (([3, 50], 47, 0), ([0, 61], 47, 1), ([-1, 5], 47, 1), ([50, 3], 47, 1), ([7, 7], 47, 0), ([59, 60], 1, 0), ([0, 60], 60, 0)):
+        step.status.zero_()
+        O = step.prompt(q, k, v, to_dev_i32(cu))
+        assert status_value(step.status) == code and step.length.tolist() == [length]
+        if code == 0 and cu[1] > cu[0]:
+            _holds(step, 0, _f(k[cu[0]:cu[1]]), _f(v[cu[0]:cu[1]]))
+            part = [x[cu[0]:cu[1]].bfloat16() for x in (q, k, v)]
+            assert torch.equal(O[cu[0]:cu[1]], w12.prompt_attention(*part, to_dev_i32([0, cu[1] - cu[0]])))
+
+
+def test_a_graph_of_prompts_meets_offsets_that_do_not_fit():
+    """Captured with good offsets: replays refuse what an eager call refuses, and serve again."""
+    q, k, v = _qkv(90)
+    eager, graphed = _plain(), _plain()
+    cu = to_dev_i32([0, 30, 60, 90])
+    graphed.prompt(q, k, v, cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        graphed.prompt(q, k, v, cu)
+    eager.prompt(q, k, v, cu)
+    for offsets in ([0, 50, 20, 90], [0, 10, 40, 91], [-1, 10, 40, 90], [0, 10, 40, 90], [5, 5, 2, 90], [0, 20, 20, 50]):
+        for step in (eager, graphed):
+            step.status.zero_()
+        cu.copy_(to_dev_i32(offsets))
+        graph.replay()
+        eager.prompt(q, k, v, to_dev_i32(offsets))
+        assert status_value(eager.status) == status_value(graphed.status)
+        assert torch.equal(eager.length, graphed.length)
+        for b, n in enumerate(eager.length.tolist()):
+            for x, y in zip(_rows(eager, b, n), _rows(graphed, b, n)):
+                np.testing.assert_array_equal(x, y)
+    assert graphed.length.tolist() == [20, 30, 30]
+
+
 @pytest.mark.parametrize("rotated", [False, True])
 @pytest.mark.parametrize("what", ["type", "type of one", "layout", "host", "offsets"])
 def test_rows_that_are_refused_change_nothing(what, rotated):
